@@ -1,0 +1,385 @@
+// block_norm.hip -- the norms around a block with its gate and residual sum,
+// and their gradients.
+//
+//   residual_out = residual + scale sigmoid(gate) post y / rms(y)
+//   out          = pre residual_out / rms(residual_out)
+//
+// Bound by memory: 16 (forward) or 45 (backward) operations for every channel
+// of a token against 5 or 8 activations moved.  A workgroup holds a row in
+// registers, so the row is read once for both norms; the sums over the row
+// are wave sums joined in shared memory.
+#include <hip/hip_runtime.h>
+
+#include "block_device.hpp"
+
+namespace dwps {
+namespace {
+
+struct NormArgs {
+    const void *y, *gate, *residual;
+    int64_t y_stride, gate_stride, residual_stride;
+    const float *scale, *post, *pre;
+    uint32_t tokens, channels;
+    float eps, inv;  // 1 / channels
+};
+
+__device__ __forceinline__ float wave_total(float v) {
+    v = row_total(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// The workgroup's sums of n values, in every thread.
+template <int NT, int n>
+__device__ __forceinline__ void group_totals(float (&v)[n], float *shared) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = wave_total(v[i]);
+    if (NT == 64) return;
+    const uint32_t wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63u) == 0u)
+#pragma unroll
+        for (int i = 0; i < n; ++i) shared[wave * n + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        v[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NT / 64; ++k) v[i] += shared[k * n + i];
+    }
+}
+
+// n neighbouring values from p, or `none` without p; `have` of them exist.
+template <class T, int n>
+__device__ __forceinline__ void load_n(float (&v)[n], const T *p, uint32_t have, float none) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = (uint32_t)i < have ? none : 0.0f;
+    } else if (have >= (uint32_t)n) {
+        const Pack<T, n> r = *reinterpret_cast<const Pack<T, n> *>(p);
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = (float)r.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = (uint32_t)i < have ? (float)p[i] : 0.0f;
+    }
+}
+template <class T, int n>
+__device__ __forceinline__ void store_n(T *p, const float (&v)[n], uint32_t have) {
+    if (have >= (uint32_t)n) {
+        Pack<T, n> r;
+#pragma unroll
+        for (int i = 0; i < n; ++i) r.v[i] = (T)v[i];
+        *reinterpret_cast<Pack<T, n> *>(p) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if ((uint32_t)i < have) p[i] = (T)v[i];
+    }
+}
+template <class T>
+__device__ __forceinline__ const T *at_row(const void *p, int64_t t, int64_t stride, uint32_t c) {
+    return p ? static_cast<const T *>(p) + t * stride + c : nullptr;
+}
+__device__ __forceinline__ const float *at_col(const float *p, uint32_t c) { return p ? p + c : nullptr; }
+
+// One row: NT threads, K times V neighbouring channels each.
+template <class T, class R, int NT, int V, int K>
+__global__ __launch_bounds__(NT) void norm_kernel(NormArgs a, R *__restrict__ res_out, T *__restrict__ out) {
+    __shared__ float sh[2][NT / 64];
+    const int64_t t = blockIdx.x, C = a.channels;
+    float q[K][V], r[K][V], sum[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        float y[V], z[V], s[V], w[V];
+        load_n<T, V>(y, at_row<T>(a.y, t, a.y_stride, c), have, 0.0f);
+        load_n<T, V>(z, at_row<T>(a.gate, t, a.gate_stride, c), have, 0.0f);
+        load_n<R, V>(r[k], at_row<R>(a.residual, t, a.residual_stride, c), have, 0.0f);
+        load_n<float, V>(s, at_col(a.scale, c), have, 1.0f);
+        load_n<float, V>(w, at_col(a.post, c), have, 1.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sum[0] = __builtin_fmaf(y[i], y[i], sum[0]);
+            q[k][i] = (a.gate ? s[i] * sigmoid(z[i]) : s[i]) * (y[i] * w[i]);
+        }
+    }
+    group_totals<NT, 1>(sum, sh[0]);
+    const float ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            r[k][i] = __builtin_fmaf(q[k][i], ry, r[k][i]);
+            sum[0] = __builtin_fmaf(r[k][i], r[k][i], sum[0]);
+        }
+        store_n<R, V>(res_out + t * C + c, r[k], have);
+    }
+    group_totals<NT, 1>(sum, sh[1]);
+    const float rr = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        float w[V];
+        load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] *= r[k][i] * rr;
+        store_n<T, V>(out + t * C + c, w, have);
+    }
+}
+
+// Gradients.  With r = residual_out, ry and rr the two reciprocal norms,
+// s = sigmoid(gate), w = pre dout:
+//   dr = dresidual_out + rr (w - r rr^2 mean(w r))
+//   u = scale s post dr,  dy = ry (u - y ry^2 mean(u y))
+//   dgate = scale dr y ry post s (1 - s)
+//   dscale = sum dr s y ry post,  dpost = sum scale dr s y ry,  dpre = sum dout r rr
+// A workgroup takes every gridDim.x-th row and keeps its sums over rows in
+// registers; part[workgroup][dscale, dpost, dpre][channel].
+template <class T, class R, int NT, int V, int K>
+__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__restrict__ dout, const R *__restrict__ dres,
+                                                      T *__restrict__ dy, T *__restrict__ dgate, R *__restrict__ dr_out,
+                                                      float *__restrict__ part, uint32_t *hdr, uint32_t words) {
+    __shared__ float sh[2][NT / 64 * 3];
+    if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
+    const int64_t C = a.channels;
+    float acc[3][K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[0][k][i] = acc[1][k][i] = acc[2][k][i] = 0.0f;
+    for (int64_t t = blockIdx.x; t < (int64_t)a.tokens; t += gridDim.x) {
+        float y[K][V], z[K][V], r[K][V], g[K][V], sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+            float w[V];
+            load_n<T, V>(y[k], at_row<T>(a.y, t, a.y_stride, c), have, 0.0f);
+            load_n<T, V>(z[k], at_row<T>(a.gate, t, a.gate_stride, c), have, 0.0f);
+            load_n<R, V>(r[k], at_row<R>(a.residual, t, a.residual_stride, c), have, 0.0f);
+            load_n<T, V>(g[k], dout + t * C + c, have, 0.0f);
+            load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sum[0] = __builtin_fmaf(y[k][i], y[k][i], sum[0]);
+                sum[1] = __builtin_fmaf(r[k][i], r[k][i], sum[1]);
+                sum[2] = __builtin_fmaf(w[i] * g[k][i], r[k][i], sum[2]);
+            }
+        }
+        group_totals<NT, 3>(sum, sh[0]);
+        const float ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
+        const float rr = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[1], a.inv, a.eps));
+        const float lean = rr * rr * (sum[2] * a.inv);
+        float tilt[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+            float w[V], d[V], s[V], po[V];
+            load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
+            load_n<float, V>(s, at_col(a.scale, c), have, 1.0f);
+            load_n<float, V>(po, at_col(a.post, c), have, 1.0f);
+            load_n<R, V>(d, dres ? dres + t * C + c : nullptr, have, 0.0f);
+            float dg[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float dr = __builtin_fmaf(rr, __builtin_fmaf(-r[k][i], lean, w[i] * g[k][i]), d[i]);
+                acc[2][k][i] = __builtin_fmaf(g[k][i], r[k][i] * rr, acc[2][k][i]);
+                const float sg = a.gate ? sigmoid(z[k][i]) : 1.0f, unit = y[k][i] * ry;
+                const float along = dr * sg * unit;
+                acc[0][k][i] = __builtin_fmaf(along, po[i], acc[0][k][i]);
+                acc[1][k][i] = __builtin_fmaf(along, s[i], acc[1][k][i]);
+                dg[i] = along * s[i] * po[i] * (1.0f - sg);
+                const float u = s[i] * dr * sg * po[i];
+                tilt[0] = __builtin_fmaf(u, y[k][i], tilt[0]);
+                d[i] = dr;
+                z[k][i] = u;
+            }
+            store_n<R, V>(dr_out + t * C + c, d, have);
+            if (dgate) store_n<T, V>(dgate + t * C + c, dg, have);
+        }
+        group_totals<NT, 1>(tilt, sh[1]);
+        const float turn = ry * ry * (tilt[0] * a.inv);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[k][i] = ry * __builtin_fmaf(-y[k][i], turn, z[k][i]);
+            store_n<T, V>(dy + t * C + c, y[k], have);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+#pragma unroll
+        for (int w = 0; w < 3; ++w) store_n<float, V>(part + ((int64_t)blockIdx.x * 3 + w) * C + c, acc[w][k], have);
+    }
+}
+
+__global__ __launch_bounds__(256) void norm_params_kernel(const float *__restrict__ part, uint32_t rows,
+                                                          uint32_t channels, float *__restrict__ dscale,
+                                                          float *__restrict__ dpost, float *__restrict__ dpre) {
+    __shared__ float s[4][64];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint32_t cols = 3u * channels, col = blockIdx.x * 64u + lane;
+    float v = 0.0f;
+    if (col < cols)
+        for (uint32_t r = wave; r < rows; r += 4u) v += part[(uint64_t)r * cols + col];
+    s[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0u && col < cols) {
+        v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+        const uint32_t which = col / channels, c = col % channels;
+        float *to = which == 0u ? dscale : which == 1u ? dpost : dpre;
+        if (to) to[c] = v;
+    }
+}
+
+constexpr uint32_t kNormBwdGroups = 512;  // workgroups that share the rows
+
+ps_status norm_sizes(const ps_norm_input *in) {
+    if (!in) return PS_ERR_NULL;
+    if (!dtype_bytes(in->dtype) || (in->residual_dtype != in->dtype && in->residual_dtype != PS_F32))
+        return PS_ERR_UNSUPPORTED;
+    const int64_t c = in->channels;
+    if (in->tokens > kBlockMaxTokens || c == 0 || c > PS_NORM_MAX_CHANNELS || in->y_stride < c ||
+        (in->gate && in->gate_stride < c) || in->residual_stride < c)
+        return PS_ERR_SIZE;
+    return PS_OK;
+}
+
+ps_status norm_pointers(const ps_norm_input *in) {
+    const size_t e = dtype_bytes(in->dtype);
+    if (in->tokens && (!in->y || !in->residual)) return PS_ERR_NULL;
+    if (!aligned(in->y, e) || !aligned(in->gate, e) || !aligned(in->residual, dtype_bytes(in->residual_dtype)) ||
+        !aligned(in->scale, 4) || !aligned(in->post_weight, 4) || !aligned(in->pre_weight, 4))
+        return PS_ERR_ALIGNMENT;
+    return PS_OK;
+}
+
+bool norm_overlaps(const ps_norm_input *in, const void *p, size_t bytes) {
+    const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype);
+    return p && (ranges_overlap(p, bytes, in->y, rows_bytes(in->tokens, in->y_stride, in->channels, e)) ||
+                 (in->gate && ranges_overlap(p, bytes, in->gate, rows_bytes(in->tokens, in->gate_stride, in->channels, e))) ||
+                 ranges_overlap(p, bytes, in->residual, rows_bytes(in->tokens, in->residual_stride, in->channels, re)));
+}
+
+NormArgs norm_args(const ps_norm_input *in) {
+    NormArgs a{};
+    a.y = in->y, a.gate = in->gate, a.residual = in->residual;
+    a.y_stride = in->y_stride, a.gate_stride = in->gate_stride, a.residual_stride = in->residual_stride;
+    a.scale = in->scale, a.post = in->post_weight, a.pre = in->pre_weight;
+    a.tokens = (uint32_t)in->tokens, a.channels = in->channels;
+    a.eps = in->eps;
+    a.inv = 1.0f / (float)in->channels;
+    return a;
+}
+
+// Calls f(threads, vectors per thread) as constants: the fewest threads that
+// hold a row of `channels` in `most` vectors of V each.
+template <int V, class F>
+ps_status with_shape(uint32_t channels, F f) {
+    auto fit = [&](auto nt, auto k) { return channels <= (uint32_t)(decltype(nt)::value * decltype(k)::value * V); };
+#define DWPS_NORM_SHAPE(NT, K)                                                                      \
+    if (fit(std::integral_constant<int, NT>(), std::integral_constant<int, K>()))                   \
+        return f(std::integral_constant<int, NT>(), std::integral_constant<int, K>())
+    DWPS_NORM_SHAPE(64, 1);
+    if constexpr (V == 4) DWPS_NORM_SHAPE(64, 2);
+    DWPS_NORM_SHAPE(256, 1);
+    DWPS_NORM_SHAPE(256, 2);
+    DWPS_NORM_SHAPE(256, 3);
+    DWPS_NORM_SHAPE(256, 4);
+    if constexpr (V == 4) DWPS_NORM_SHAPE(256, 5);
+    DWPS_NORM_SHAPE(512, 3);
+    DWPS_NORM_SHAPE(512, 4);
+    if constexpr (V == 4) DWPS_NORM_SHAPE(1024, 3);
+    if constexpr (V == 4) DWPS_NORM_SHAPE(1024, 4);
+#undef DWPS_NORM_SHAPE
+    return PS_ERR_SIZE;
+}
+
+template <class F>
+ps_status with_norm_types(const ps_norm_input *in, F f) {
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        if (in->residual_dtype == PS_F32) return f(T(), float());
+        return f(T(), T());
+    });
+}
+
+}  // namespace
+}  // namespace dwps
+
+using namespace dwps;
+
+extern "C" ps_status ps_block_norm(const ps_norm_input *in, void *residual_out, void *out, void *stream) {
+    ps_status st = norm_sizes(in);
+    if (st != PS_OK) return st;
+    if ((st = norm_pointers(in)) != PS_OK) return st;
+    if (!in->tokens) return PS_OK;
+    const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype);
+    if (!residual_out || !out) return PS_ERR_NULL;
+    if (!aligned(residual_out, re) || !aligned(out, e)) return PS_ERR_ALIGNMENT;
+    const size_t cells = in->tokens * in->channels;
+    if (norm_overlaps(in, residual_out, cells * re) || norm_overlaps(in, out, cells * e) ||
+        ranges_overlap(out, cells * e, residual_out, cells * re))
+        return PS_ERR_ALIAS;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const NormArgs a = norm_args(in);
+    return with_norm_types(in, [&](auto zt, auto zr) {
+        using T = decltype(zt);
+        using R = decltype(zr);
+        return with_shape<8>(in->channels, [&](auto nt, auto k) {
+            constexpr int NT = decltype(nt)::value, K = decltype(k)::value;
+            timing_begin(s);
+            hipLaunchKernelGGL((norm_kernel<T, R, NT, 8, K>), dim3(a.tokens), dim3(NT), 0, s, a,
+                               static_cast<R *>(residual_out), static_cast<T *>(out));
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm_input *in, const void *dout,
+                                       const void *dresidual_out, const ps_norm_grads *grads, void *stream) {
+    ps_status st = norm_sizes(in);
+    if (st != PS_OK) return st;
+    const uint32_t groups = in->tokens < kNormBwdGroups ? (uint32_t)in->tokens : kNormBwdGroups;
+    PlainWs plan;
+    const size_t part_at = plan.take((size_t)groups * 3u * in->channels * 4u);
+    bool query = false;
+    st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+    if (st != PS_OK || query) return st;
+    if ((st = norm_pointers(in)) != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype);
+    if (!grads || (in->tokens && (!dout || !grads->dy || !grads->dresidual))) return PS_ERR_NULL;
+    if (!aligned(ws, 16) || !aligned(dout, e) || !aligned(dresidual_out, re) || !aligned(grads->dy, e) ||
+        !aligned(grads->dgate, e) || !aligned(grads->dresidual, re) || !aligned(grads->dscale, 4) ||
+        !aligned(grads->dpost_weight, 4) || !aligned(grads->dpre_weight, 4))
+        return PS_ERR_ALIGNMENT;
+    const size_t cells = in->tokens * in->channels;
+    if (norm_overlaps(in, grads->dy, cells * e) || norm_overlaps(in, grads->dgate, cells * e) ||
+        norm_overlaps(in, grads->dresidual, cells * re))
+        return PS_ERR_ALIAS;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const NormArgs a = norm_args(in);
+    return with_norm_types(in, [&](auto zt, auto zr) {
+        using T = decltype(zt);
+        using R = decltype(zr);
+        return with_shape<4>(in->channels, [&](auto nt, auto k) {
+            constexpr int NT = decltype(nt)::value, K = decltype(k)::value;
+            float *part = ws_at<float>(ws, part_at);
+            timing_begin(s);
+            if (groups)
+                hipLaunchKernelGGL((norm_bwd_kernel<T, R, NT, 4, K>), dim3(groups), dim3(NT), 0, s, a,
+                                   static_cast<const T *>(dout), static_cast<const R *>(dresidual_out),
+                                   static_cast<T *>(grads->dy), in->gate ? static_cast<T *>(grads->dgate) : nullptr,
+                                   static_cast<R *>(grads->dresidual), part, ws_counter(ws), plan.words());
+            if (grads->dscale || grads->dpost_weight || grads->dpre_weight)
+                hipLaunchKernelGGL(norm_params_kernel, dim3((uint32_t)ceil_div(3u * in->channels, 64)), dim3(256), 0, s,
+                                   part, groups, in->channels, grads->dscale, grads->dpost_weight, grads->dpre_weight);
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}

@@ -1,0 +1,447 @@
+// causal_conv.hip -- the short causal convolution of a state space block:
+// forward, backward and the form for single tokens.
+//
+//   pre[t, d] = bias[d] + sum_k weight[d, k] x[t - (W - 1) + k, d]
+//   out[t, d] = silu(pre[t, d])
+//
+// Bound by memory: 2 W + 5 operations for two activations moved.  A thread
+// owns up to 16 bytes of neighbouring channels and walks down a piece of one
+// sequence, the last W rows in registers, so every row is read once but for
+// the W - 1 rows before each piece.
+#include <hip/hip_runtime.h>
+
+#include "block_device.hpp"
+
+namespace dwps {
+namespace {
+
+struct ConvArgs {
+    const void *x, *initial;
+    const float *weight, *bias;
+    const uint32_t *offsets;
+    int64_t x_stride;
+    uint32_t tokens, channels, num_seqs;
+    uint32_t shift;      // log2 of the rows of a piece
+    uint32_t col_blocks; // workgroups side by side
+    uint32_t group;      // of xcd_neighbours
+};
+
+constexpr int kConvThreads = 64;
+
+// Loads / stores up to n channels; `have` of them exist (n but for the last
+// thread of a row).
+template <class T, int n>
+__device__ __forceinline__ void load_row(float (&v)[n], const T *p, uint32_t have) {
+    if (have >= (uint32_t)n) {
+        const Pack<T, n> r = *reinterpret_cast<const Pack<T, n> *>(p);
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = (float)r.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = (uint32_t)i < have ? (float)p[i] : 0.0f;
+    }
+}
+template <class T, int n>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[n], uint32_t have) {
+    if (have >= (uint32_t)n) {
+        Pack<T, n> r;
+#pragma unroll
+        for (int i = 0; i < n; ++i) r.v[i] = (T)v[i];
+        *reinterpret_cast<Pack<T, n> *>(p) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if ((uint32_t)i < have) p[i] = (T)v[i];
+    }
+}
+
+// Row r (any row from seq_lo - (W - 1) on) of the sequence: an input row, an
+// initial row, or zeros.
+template <class T, int V, int W>
+__device__ __forceinline__ void past_row(float (&v)[V], const ConvArgs &a, const Piece &q, int64_t r, uint32_t c,
+                                         uint32_t have) {
+    if (r >= (int64_t)q.seq_lo) {
+        load_row<T, V>(v, static_cast<const T *>(a.x) + r * a.x_stride + c, have);
+    } else if (a.initial) {
+        const int64_t j = (int64_t)(W - 1) + r - (int64_t)q.seq_lo;
+        load_row<T, V>(v, static_cast<const T *>(a.initial) + ((int64_t)q.seq * (W - 1) + j) * a.channels + c, have);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    }
+}
+
+template <class T, int V, int W>
+__device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const ConvArgs &a, uint32_t c,
+                                             uint32_t have) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = (uint32_t)i < have;
+        b[i] = in && a.bias ? a.bias[c + i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][i] = in ? a.weight[(int64_t)(c + i) * W + k] : 0.0f;
+    }
+}
+
+template <class T, int V, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__restrict__ out, T *__restrict__ fin) {
+    const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
+    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, b / a.col_blocks);
+    if (!q.any) return;
+    const uint32_t c = (b % a.col_blocks * kConvThreads + threadIdx.x) * V;
+    if (c >= a.channels) return;
+    const uint32_t have = a.channels - c;
+    const int64_t C = a.channels;
+    const T *x = static_cast<const T *>(a.x);
+    float w[W][V], bias[V], win[W][V];  // win[k]: the row W - 1 - k before the present one
+    load_weights<T, V, W>(w, bias, a, c, have);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c, have);
+    for (uint32_t t = q.lo; t < q.hi; ++t) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
+        load_row<T, V>(win[W - 1], x + (int64_t)t * a.x_stride + c, have);
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float pre = bias[i];
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
+            o[i] = silu(pre);
+        }
+        store_row<T, V>(out + (int64_t)t * C + c, o, have);
+    }
+    if (fin && q.hi == q.seq_hi) {
+#pragma unroll
+        for (int k = 1; k < W; ++k)
+            store_row<T, V>(fin + ((int64_t)q.seq * (W - 1) + k - 1) * C + c, win[k], have);
+    }
+}
+
+// Backward.  With g[t] = dout[t] silu'(pre[t]):
+//   dx[t] = sum_k weight[k] g[t + W - 1 - k]   (rows past the sequence: 0)
+//   dweight[k] = sum_t g[t] x[t - (W - 1) + k],  dbias = sum_t g[t]
+// and the rows before the sequence's first (dinitial) as dx.  A piece walks
+// W - 1 rows past its end for the g its last rows need, and sums dweight and
+// dbias over its own rows into part[piece][k][channel] (k = W: dbias).
+template <class T, int V, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, const T *__restrict__ dout,
+                                                                T *__restrict__ dx, T *__restrict__ dinit,
+                                                                float *__restrict__ part, uint32_t *hdr,
+                                                                uint32_t words) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
+    const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
+    const uint32_t p = b / a.col_blocks;
+    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
+    const uint32_t c = (b % a.col_blocks * kConvThreads + threadIdx.x) * V;
+    if (c >= a.channels) return;
+    const uint32_t have = a.channels - c;
+    const int64_t C = a.channels;
+    const T *x = static_cast<const T *>(a.x);
+    float w[W][V], bias[V], win[W][V], gw[W][V], sum[W + 1][V];
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[k][i] = 0.0f;
+    if (q.any) {
+        load_weights<T, V, W>(w, bias, a, c, have);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c, have);
+        // an empty sequence: its dinitial rows are zero
+        const uint32_t end = q.hi + (W - 1);
+        for (uint32_t t = q.lo; t < end; ++t) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    win[k][i] = win[k + 1][i];
+                    gw[k][i] = gw[k + 1][i];
+                }
+            if (t < q.seq_hi) {
+                float o[V];
+                load_row<T, V>(win[W - 1], x + (int64_t)t * a.x_stride + c, have);
+                load_row<T, V>(o, dout + (int64_t)t * C + c, have);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float pre = bias[i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
+                    gw[W - 1][i] = o[i] * dsilu(pre, sigmoid(pre));
+                }
+                if (t < q.hi) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+#pragma unroll
+                        for (int k = 0; k < W; ++k) sum[k][i] = __builtin_fmaf(gw[W - 1][i], win[k][i], sum[k][i]);
+                        sum[W][i] += gw[W - 1][i];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) gw[W - 1][i] = 0.0f;
+            }
+            // the row that now has all its g: gw[j] is g of row r + j
+            const int64_t r = (int64_t)t - (W - 1);
+            if (r >= (int64_t)q.lo || (dinit && q.lo == q.seq_lo)) {
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    o[i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) o[i] = __builtin_fmaf(w[k][i], gw[W - 1 - k][i], o[i]);
+                }
+                if (r >= (int64_t)q.lo)
+                    store_row<T, V>(dx + r * C + c, o, have);
+                else
+                    store_row<T, V>(dinit + ((int64_t)q.seq * (W - 1) + (r - (int64_t)q.lo + (W - 1))) * C + c, o,
+                                    have);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((uint32_t)i < have) part[((int64_t)p * (W + 1) + k) * C + c + i] = sum[k][i];
+}
+
+// Sums part over the pieces: columns are the (k, channel) pairs.  Each of
+// four waves sums every fourth piece of 64 columns, then the four are added
+// in order.
+__global__ __launch_bounds__(256) void conv_params_kernel(const float *__restrict__ part, uint32_t pieces, uint32_t width,
+                                                          uint32_t channels, float *__restrict__ dweight,
+                                                          float *__restrict__ dbias) {
+    __shared__ float s[4][64];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint64_t cols = (uint64_t)(width + 1u) * channels, col = (uint64_t)blockIdx.x * 64u + lane;
+    float v = 0.0f;
+    if (col < cols)
+        for (uint32_t p = wave; p < pieces; p += 4u) v += part[p * cols + col];
+    s[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0u && col < cols) {
+        v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+        const uint32_t k = (uint32_t)(col / channels), c = (uint32_t)(col % channels);
+        if (k < width) dweight[(uint64_t)c * width + k] = v;
+        else if (dbias) dbias[c] = v;
+    }
+}
+
+// One token for each row: W - 1 rows of state in, W - 1 out.
+template <class T, int V, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, const T *state, T *new_state,
+                                                                 const int32_t *__restrict__ slots, uint32_t pool,
+                                                                 T *__restrict__ out) {
+    const uint32_t i0 = blockIdx.x / a.col_blocks;
+    const uint32_t c = (blockIdx.x % a.col_blocks * kConvThreads + threadIdx.x) * V;
+    if (c >= a.channels) return;
+    const uint32_t have = a.channels - c;
+    const int64_t C = a.channels;
+    const int64_t slot = slots ? (int64_t)slots[i0] : (int64_t)i0;
+    const bool held = slot >= 0 && slot < (int64_t)pool;
+    float w[W][V], bias[V], win[W][V], o[V];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        if (held) {
+            load_row<T, V>(win[k], state + (slot * (W - 1) + k) * C + c, have);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) win[k][i] = 0.0f;
+        }
+    }
+    load_row<T, V>(win[W - 1], static_cast<const T *>(a.x) + (int64_t)i0 * a.x_stride + c, have);
+    load_weights<T, V, W>(w, bias, a, c, have);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float pre = bias[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
+        o[i] = silu(pre);
+    }
+    store_row<T, V>(out + (int64_t)i0 * C + c, o, have);
+    if (held) {
+#pragma unroll
+        for (int k = 1; k < W; ++k) store_row<T, V>(new_state + (slot * (W - 1) + k - 1) * C + c, win[k], have);
+    }
+}
+
+// Calls f with the width as a constant.
+template <class F>
+ps_status with_width(uint32_t width, F f) {
+    switch (width) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    case 8: return f(std::integral_constant<int, 8>());
+    default: return PS_ERR_SIZE;
+    }
+}
+
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// Sizes and types alone.
+ps_status conv_sizes(const ps_conv_input *in, bool packed) {
+    if (!in) return PS_ERR_NULL;
+    if (!dtype_bytes(in->dtype)) return PS_ERR_UNSUPPORTED;
+    if (in->tokens > kBlockMaxTokens || in->channels == 0u || in->channels > kBlockMaxChannels || in->width == 0u ||
+        in->width > PS_CONV_MAX_WIDTH || in->num_seqs > kBlockMaxSeqs || in->x_stride < (int64_t)in->channels)
+        return PS_ERR_SIZE;
+    if (packed && !in->offsets && in->num_seqs > 1u) return PS_ERR_SIZE;
+    return PS_OK;
+}
+
+ps_status conv_pointers(const ps_conv_input *in) {
+    const size_t e = dtype_bytes(in->dtype);
+    if (!in->weight || (in->tokens && !in->x)) return PS_ERR_NULL;
+    if (!aligned(in->x, e) || !aligned(in->weight, 4) || !aligned(in->bias, 4) || !aligned(in->offsets, 4) ||
+        !aligned(in->initial, e))
+        return PS_ERR_ALIGNMENT;
+    return PS_OK;
+}
+
+ConvArgs conv_args(const ps_conv_input *in, uint32_t vec, uint32_t shift) {
+    ConvArgs a{};
+    a.x = in->x;
+    a.initial = in->width > 1u ? in->initial : nullptr;
+    a.weight = in->weight;
+    a.bias = in->bias;
+    a.offsets = in->offsets;
+    a.x_stride = in->x_stride;
+    a.tokens = (uint32_t)in->tokens;
+    a.channels = in->channels;
+    a.num_seqs = in->offsets ? in->num_seqs : 1u;
+    a.shift = shift;
+    a.col_blocks = (uint32_t)ceil_div(in->channels, (uint64_t)vec * kConvThreads);
+    a.group = 1u;
+    return a;
+}
+
+uint32_t conv_shift(const ps_conv_input *, uint32_t) { return 5u; }
+
+constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
+
+uint32_t seqs_of(const ps_conv_input *in) { return in->offsets ? in->num_seqs : 1u; }
+
+}  // namespace
+}  // namespace dwps
+
+using namespace dwps;
+
+extern "C" ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *final, void *stream) {
+    ps_status st = conv_sizes(in, true);
+    if (st != PS_OK) return st;
+    if ((st = conv_pointers(in)) != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype);
+    if (in->tokens && !out) return PS_ERR_NULL;
+    if (!aligned(out, e) || !aligned(final, e)) return PS_ERR_ALIGNMENT;
+    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
+    const size_t out_bytes = in->tokens * in->channels * e;
+    const size_t state_bytes = (size_t)seqs_of(in) * (in->width - 1u) * in->channels * e;
+    if (ranges_overlap(out, out_bytes, in->x, in_bytes) ||
+        (final && (ranges_overlap(final, state_bytes, in->x, in_bytes) || ranges_overlap(final, state_bytes, out, out_bytes) ||
+                   (in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)))) ||
+        (in->initial && ranges_overlap(out, out_bytes, in->initial, state_bytes)))
+        return PS_ERR_ALIAS;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_width(in->width, [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            const ConvArgs a = conv_args(in, kVec<T>, conv_shift(in, kVec<T>));
+            const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
+            if (grid > kMaxGrid) return PS_ERR_SIZE;
+            if (!grid) return PS_OK;
+            timing_begin(s);
+            hipLaunchKernelGGL((conv_kernel<T, kVec<T>, W>), dim3((uint32_t)grid), dim3(kConvThreads), 0, s, a,
+                               static_cast<T *>(out), W > 1 ? static_cast<T *>(final) : nullptr);
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_conv_input *in, const void *dout, void *dx,
+                                        float *dweight, float *dbias, void *dinitial, void *stream) {
+    ps_status st = conv_sizes(in, true);
+    if (st != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype);
+    const ConvArgs a = conv_args(in, 16u / (uint32_t)e, conv_shift(in, 16u / (uint32_t)e));
+    const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
+    if (pieces * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
+    PlainWs plan;
+    const size_t part_at = plan.take(pieces * (in->width + 1u) * in->channels * 4u);
+    bool query = false;
+    st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+    if (st != PS_OK || query) return st;
+    if ((st = conv_pointers(in)) != PS_OK) return st;
+    if (!dweight || (in->tokens && (!dout || !dx))) return PS_ERR_NULL;
+    if (!aligned(ws, 16) || !aligned(dout, e) || !aligned(dx, e) || !aligned(dweight, 4) || !aligned(dbias, 4) ||
+        !aligned(dinitial, e))
+        return PS_ERR_ALIGNMENT;
+    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
+    const size_t out_bytes = in->tokens * in->channels * e;
+    if (ranges_overlap(dx, out_bytes, in->x, in_bytes) || ranges_overlap(dx, out_bytes, dout, out_bytes)) return PS_ERR_ALIAS;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_width(in->width, [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            float *part = ws_at<float>(ws, part_at);
+            timing_begin(s);
+            if (pieces)
+                hipLaunchKernelGGL((conv_bwd_kernel<T, kVec<T>, W>), dim3((uint32_t)(pieces * a.col_blocks)),
+                                   dim3(kConvThreads), 0, s, a, static_cast<const T *>(dout), static_cast<T *>(dx),
+                                   W > 1 ? static_cast<T *>(dinitial) : nullptr, part, ws_counter(ws), plan.words());
+            hipLaunchKernelGGL(conv_params_kernel,
+                               dim3((uint32_t)ceil_div((uint64_t)(in->width + 1u) * in->channels, 64)), dim3(256), 0, s,
+                               part, (uint32_t)pieces, in->width, in->channels, dweight, dbias);
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" ps_status ps_causal_conv_step(const ps_conv_input *in, const void *state, void *new_state,
+                                         const int32_t *slots, uint32_t pool, void *out, void *stream) {
+    ps_status st = conv_sizes(in, false);
+    if (st != PS_OK) return st;
+    if ((st = conv_pointers(in)) != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype);
+    if (in->tokens && (!out || (in->width > 1u && pool && (!state || !new_state)))) return PS_ERR_NULL;
+    if (!aligned(out, e) || !aligned(state, e) || !aligned(new_state, e) || !aligned(slots, 4)) return PS_ERR_ALIGNMENT;
+    if (!slots && in->tokens > pool) return PS_ERR_SIZE;
+    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
+    const size_t out_bytes = in->tokens * in->channels * e;
+    const size_t state_bytes = (size_t)pool * (in->width - 1u) * in->channels * e;
+    if (ranges_overlap(out, out_bytes, in->x, in_bytes) || ranges_overlap(out, out_bytes, state, state_bytes) ||
+        ranges_overlap(out, out_bytes, new_state, state_bytes) || ranges_overlap(new_state, state_bytes, in->x, in_bytes) ||
+        (state != new_state && ranges_overlap(new_state, state_bytes, state, state_bytes)))
+        return PS_ERR_ALIAS;
+    if (!in->tokens) return PS_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_width(in->width, [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            const ConvArgs a = conv_args(in, kVec<T>, 0u);
+            if (in->tokens * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
+            timing_begin(s);
+            hipLaunchKernelGGL((conv_step_kernel<T, kVec<T>, W>), dim3((uint32_t)in->tokens * a.col_blocks),
+                               dim3(kConvThreads), 0, s, a, static_cast<const T *>(state), static_cast<T *>(new_state),
+                               slots, pool, static_cast<T *>(out));
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}

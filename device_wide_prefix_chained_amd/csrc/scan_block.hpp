@@ -1,0 +1,93 @@
+// scan_block.hpp -- parts shared by the selective scan's kernels
+// (selective_scan.hip, selective_scan_bwd.hip).
+//
+// Layout of the walking kernels: a row of 16 lanes owns one channel, lane n
+// its states n, n + 16, ...; a workgroup of 4 waves owns 16 channels of one
+// group, so that a token row's 16 channels are one 32-byte (16-bit types) or
+// 64-byte load and B and C are staged once for all of them.  Tokens are
+// staged 32 at a time, aligned to 32 packed rows; rows of the block outside
+// the piece have step = 0 and zero inputs, which leaves the states as they
+// are.
+#pragma once
+
+#include "block_device.hpp"
+
+namespace dwps {
+
+constexpr uint32_t kScanCellShift = 5;            // rows between checkpoints
+constexpr uint32_t kScanCell = 1u << kScanCellShift;
+constexpr int kScanTile = 32;                     // tokens staged at a time
+constexpr int kScanChannels = 16;                 // channels of a workgroup
+constexpr int kScanThreads = 256;
+// Floats from one staged channel (or state) to the next: a multiple of 4 for
+// 16-byte reads, and 36 mod 64 = 36 spreads pairs of channels over the banks.
+constexpr int kScanPad = kScanTile + 4;
+
+struct ScanArgs {
+    const void *x, *dt, *z, *B, *C;
+    const float *A, *D, *bias, *initial;
+    const uint32_t *offsets;
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+    uint32_t tokens, channels, groups, states, num_seqs;
+    uint32_t shift;            // log2 of the rows of a piece; 32: whole sequences
+    uint32_t group_channels;   // channels / groups
+    uint32_t group_blocks;     // workgroups of 16 channels in a group
+    uint32_t col_blocks;       // groups * group_blocks
+};
+
+// What a workgroup works on.
+struct ScanPlace {
+    Piece q;
+    uint32_t p;         // piece number
+    uint32_t group;
+    uint32_t ch0;       // first channel
+    uint32_t have;      // channels, up to 16
+};
+
+__device__ __forceinline__ ScanPlace scan_place(const ScanArgs &a, uint32_t b) {
+    ScanPlace w;
+    w.p = b / a.col_blocks;
+    const uint32_t cb = b % a.col_blocks;
+    w.group = cb / a.group_blocks;
+    const uint32_t in_group = cb % a.group_blocks * kScanChannels;
+    w.ch0 = w.group * a.group_channels + in_group;
+    w.have = a.group_channels - in_group < (uint32_t)kScanChannels ? a.group_channels - in_group : kScanChannels;
+    w.q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, w.p);
+    return w;
+}
+
+// Two neighbouring elements, or zeros where they are not `in`.
+template <class T>
+__device__ __forceinline__ void load_pair(float (&v)[2], const T *p, bool in0, bool in1) {
+    v[0] = in0 ? (float)p[0] : 0.0f;
+    v[1] = in1 ? (float)p[1] : 0.0f;
+}
+
+// How far each carry reaches: row 0 unused.
+enum ScanLink : uint32_t { kLinkNone = 0, kLinkStart = 1, kLinkChain = 2 };
+
+ScanArgs scan_args(const ps_scan_input *in, uint32_t shift);
+ps_status scan_sizes(const ps_scan_input *in, bool packed);
+ps_status scan_pointers(const ps_scan_input *in);
+// Whether bytes at p overlap one of the call's token arrays (p may be NULL).
+bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes);
+
+// Carries from cell to cell (forward: entering each cell from the left, in
+// increasing order; backward: from the right): carry[c] = part[c] +
+// exp(A steps[c]) carry[c -+ 1], or part[c] alone where the chain starts.
+void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
+                      bool backward, hipStream_t s);
+
+// Calls f with the states of a lane (a power of two >= states / 16).
+template <class F>
+inline ps_status with_states(uint32_t states, F f) {
+    if (states <= 16u) return f(std::integral_constant<int, 1>());
+    if (states <= 32u) return f(std::integral_constant<int, 2>());
+    if (states <= 64u) return f(std::integral_constant<int, 4>());
+    if (states <= 128u) return f(std::integral_constant<int, 8>());
+    return f(std::integral_constant<int, 16>());
+}
+
+constexpr uint64_t kScanMaxGrid = 0x7FFFFFFFull;
+
+}  // namespace dwps

@@ -1,0 +1,367 @@
+// selective_scan.hip -- the selective scan of a state space block: forward
+// over packed sequences and the form for single tokens.
+//
+//   step = softplus(dt + bias),  a = exp(step A),  h <- a h + step B x
+//   out = (C . h + D x) * silu(z)
+#include <hip/hip_runtime.h>
+
+#include "scan_block.hpp"
+
+namespace dwps {
+namespace {
+
+// One walk over a piece.  OUT: outputs, final states and checkpoints, from
+// the initial states or from carry[cell].  Otherwise: only what the piece
+// adds to the states that enter the next cell (carry[cell + 1]) and the sum
+// of its steps, for pieces that go on there.
+template <class T, int S, bool OUT>
+__global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *__restrict__ out,
+                                                                 float *__restrict__ fin, float *__restrict__ marks,
+                                                                 float *__restrict__ carry, float *__restrict__ steps,
+                                                                 uint32_t *__restrict__ links, uint32_t *hdr,
+                                                                 uint32_t words) {
+    __shared__ __attribute__((aligned(16))) float sStep[kScanChannels * kScanPad], sDrive[kScanChannels * kScanPad],
+        sY[OUT ? kScanChannels * kScanPad : 1], sB[16 * S * kScanPad], sC[OUT ? 16 * S * kScanPad : 1];
+    if (!OUT && blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
+    const ScanPlace w = scan_place(a, xcd_neighbours(blockIdx.x, gridDim.x, sizeof(T) == 2 ? 4u : 2u));
+    const Piece &q = w.q;
+    if (!q.any) return;
+    const uint32_t N = a.states;
+    const int64_t DN = (int64_t)a.channels * N;
+    if (!OUT) {
+        const uint64_t cell_end = (uint64_t)(q.cell + 1u) << a.shift;
+        if (q.hi != cell_end) return;  // reaches no further cell
+        const bool on = q.seq_hi > q.hi;
+        if (w.ch0 == 0u && threadIdx.x == 0)
+            links[q.cell + 1u] = !on ? kLinkNone : q.lo == q.seq_lo ? kLinkStart : kLinkChain;
+        if (!on) return;
+    }
+    // staging: two channels of one token
+    const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
+    const bool in0 = c2 < w.have, in1 = c2 + 1u < w.have;
+    const uint32_t cs = w.ch0 + c2;
+    const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
+    const float skip0 = a.D && in0 ? a.D[cs] : 0.0f, skip1 = a.D && in1 ? a.D[cs + 1] : 0.0f;
+    // walking: one channel of a row of lanes
+    const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
+    const uint32_t cw = (threadIdx.x >> 6) * 4u + (lane >> 4);
+    const uint32_t d = w.ch0 + cw;
+    float A2[S], h[S], total = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const uint32_t n = s * 16 + l;
+        const bool in = cw < w.have && n < N;
+        A2[s] = in ? a.A[(int64_t)d * N + n] * kLog2e : 0.0f;
+        h[s] = 0.0f;
+        if (in) {
+            if (q.lo == q.seq_lo) h[s] = a.initial ? a.initial[(int64_t)q.seq * DN + (int64_t)d * N + n] : 0.0f;
+            else if (OUT) h[s] = carry[(int64_t)q.cell * DN + (int64_t)d * N + n];
+        }
+    }
+    for (uint32_t blk = q.lo & ~(uint32_t)(kScanTile - 1); blk < q.hi; blk += kScanTile) {
+        const uint32_t t = blk + row;
+        const bool live = t >= q.lo && t < q.hi;
+        float x[2], dt[2], z[2] = {0.0f, 0.0f};
+        load_pair<T>(x, static_cast<const T *>(a.x) + (int64_t)t * a.x_stride + cs, live && in0, live && in1);
+        load_pair<T>(dt, static_cast<const T *>(a.dt) + (int64_t)t * a.dt_stride + cs, live && in0, live && in1);
+        if (OUT && a.z)
+            load_pair<T>(z, static_cast<const T *>(a.z) + (int64_t)t * a.z_stride + cs, live && in0, live && in1);
+        const float st0 = live ? softplus(dt[0] + bias0) : 0.0f, st1 = live ? softplus(dt[1] + bias1) : 0.0f;
+        sStep[c2 * kScanPad + row] = st0;
+        sStep[(c2 + 1) * kScanPad + row] = st1;
+        sDrive[c2 * kScanPad + row] = st0 * x[0];
+        sDrive[(c2 + 1) * kScanPad + row] = st1 * x[1];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t n = s * 16 + c2;
+            float v[2];
+            load_pair<T>(v, static_cast<const T *>(a.B) + (int64_t)t * a.b_stride + w.group * N + n, live && n < N,
+                         live && n + 1 < N);
+            sB[n * kScanPad + row] = v[0];
+            sB[(n + 1) * kScanPad + row] = v[1];
+            if (OUT) {
+                load_pair<T>(v, static_cast<const T *>(a.C) + (int64_t)t * a.c_stride + w.group * N + n, live && n < N,
+                             live && n + 1 < N);
+                sC[n * kScanPad + row] = v[0];
+                sC[(n + 1) * kScanPad + row] = v[1];
+            }
+        }
+        if (OUT && marks && blk > q.lo && (blk & (kScanCell - 1u)) == 0u && cw < w.have) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (s * 16 + l < N) marks[(int64_t)(blk >> kScanCellShift) * DN + (int64_t)d * N + s * 16 + l] = h[s];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int sub = 0; sub < kScanTile / 16; ++sub) {
+            const float st = sStep[cw * kScanPad + sub * 16 + l], dr = sDrive[cw * kScanPad + sub * 16 + l];
+            if (!OUT) total += st;
+            float y[16];
+            auto token = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                const float stj = row_lane<j>(st), drj = row_lane<j>(dr);
+                y[j] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float e = exp2_hw(stj * A2[s]);
+                    h[s] = __builtin_fmaf(e, h[s], drj * sB[(s * 16 + l) * kScanPad + sub * 16 + j]);
+                    if (OUT) y[j] = __builtin_fmaf(h[s], sC[(s * 16 + l) * kScanPad + sub * 16 + j], y[j]);
+                }
+            };
+            for_each_index(token, std::make_integer_sequence<int, 16>());
+            if (OUT) sY[cw * kScanPad + sub * 16 + l] = row_sums(y, lane);
+        }
+        __syncthreads();
+        if (OUT && live) {
+            T *o = out + (int64_t)t * a.channels + cs;
+            const float y0 = __builtin_fmaf(skip0, x[0], sY[c2 * kScanPad + row]);
+            const float y1 = __builtin_fmaf(skip1, x[1], sY[(c2 + 1) * kScanPad + row]);
+            if (in0) o[0] = (T)(a.z ? y0 * silu(z[0]) : y0);
+            if (in1) o[1] = (T)(a.z ? y1 * silu(z[1]) : y1);
+        }
+    }
+    if (OUT) {
+        if (fin && q.hi == q.seq_hi && cw < w.have) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (s * 16 + l < N) fin[(int64_t)q.seq * DN + (int64_t)d * N + s * 16 + l] = h[s];
+        }
+    } else if (cw < w.have) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (s * 16 + l < N) carry[(int64_t)(q.cell + 1u) * DN + (int64_t)d * N + s * 16 + l] = h[s];
+        total = row_total(total);
+        if (l == 0u) steps[(int64_t)(q.cell + 1u) * a.channels + d] = total;
+    }
+}
+
+__global__ __launch_bounds__(256) void scan_link_kernel(ScanArgs a, float *__restrict__ carry,
+                                                        const float *__restrict__ steps,
+                                                        const uint32_t *__restrict__ links, uint32_t cells,
+                                                        int backward) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t DN = (int64_t)a.channels * a.states;
+    if (i >= DN) return;
+    const uint32_t d = (uint32_t)(i / a.states);
+    const float A2 = a.A[i] * kLog2e;
+    float h = 0.0f;
+    constexpr int U = 8;
+    for (uint32_t k0 = 1; k0 < cells; k0 += U) {
+        float v[U], s[U];
+        uint32_t f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t k = k0 + u < cells ? k0 + u : cells - 1u, c = backward ? cells - k : k;
+            v[u] = carry[c * DN + i];
+            s[u] = steps[(int64_t)c * a.channels + d];
+            f[u] = links[c];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= cells) break;
+            const uint32_t c = backward ? cells - (k0 + u) : k0 + u;
+            h = f[u] == kLinkChain ? __builtin_fmaf(exp2_hw(A2 * s[u]), h, v[u]) : v[u];
+            carry[c * DN + i] = h;
+        }
+    }
+}
+
+// One token for each row.  A lane holds 4 states of one channel (16 bytes of
+// the state), `lanes` = a power of two lanes share a channel.
+template <class T>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float *state, float *new_state,
+                                                        const int32_t *__restrict__ slots, uint32_t pool,
+                                                        T *__restrict__ out, uint32_t lanes, uint32_t blocks) {
+    const uint32_t i = blockIdx.x / blocks;
+    const uint32_t at = blockIdx.x % blocks * 256u + threadIdx.x;
+    const uint32_t d = at / lanes, part = at % lanes, N = a.states;
+    const bool in = d < a.channels;
+    const int64_t slot = slots ? (int64_t)slots[i] : (int64_t)i;
+    const bool held = slot >= 0 && slot < (int64_t)pool;
+    float sum = 0.0f, x = 0.0f;
+    if (in) {
+        x = (float)static_cast<const T *>(a.x)[(int64_t)i * a.x_stride + d];
+        const float dt = (float)static_cast<const T *>(a.dt)[(int64_t)i * a.dt_stride + d];
+        const float step = softplus(dt + (a.bias ? a.bias[d] : 0.0f));
+        const float drive = step * x;
+        const uint32_t g = d / a.group_channels;
+        for (uint32_t n = part * 4u; n < N; n += lanes * 4u) {
+            const int64_t sat = (slot * a.channels + d) * (int64_t)N + n;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (n + k >= N) break;
+                const float e = exp2_hw(step * (a.A[(int64_t)d * N + n + k] * kLog2e));
+                const float b = (float)static_cast<const T *>(a.B)[(int64_t)i * a.b_stride + g * N + n + k];
+                const float c = (float)static_cast<const T *>(a.C)[(int64_t)i * a.c_stride + g * N + n + k];
+                const float h = __builtin_fmaf(e, held ? state[sat + k] : 0.0f, drive * b);
+                if (held) new_state[sat + k] = h;
+                sum = __builtin_fmaf(h, c, sum);
+            }
+        }
+    }
+    for (uint32_t m = lanes / 2u; m; m /= 2u) sum += __shfl_xor(sum, (int)m);
+    if (in && part == 0u) {
+        float y = a.D ? __builtin_fmaf(a.D[d], x, sum) : sum;
+        if (a.z) y *= silu((float)static_cast<const T *>(a.z)[(int64_t)i * a.z_stride + d]);
+        out[(int64_t)i * a.channels + d] = (T)y;
+    }
+}
+
+// Whether a forward call over whole sequences would leave most of the GPU
+// idle, so that cells side by side are faster although every decay is then
+// computed twice.
+bool scan_split(const ps_scan_input *) { return false; }
+
+}  // namespace
+
+ScanArgs scan_args(const ps_scan_input *in, uint32_t shift) {
+    ScanArgs a{};
+    a.x = in->x, a.dt = in->dt, a.z = in->z, a.B = in->B, a.C = in->C;
+    a.A = in->A, a.D = in->D, a.bias = in->dt_bias, a.initial = in->initial;
+    a.offsets = in->offsets;
+    a.x_stride = in->x_stride, a.dt_stride = in->dt_stride, a.z_stride = in->z_stride;
+    a.b_stride = in->b_stride, a.c_stride = in->c_stride;
+    a.tokens = (uint32_t)in->tokens, a.channels = in->channels, a.groups = in->groups, a.states = in->states;
+    a.num_seqs = in->offsets ? in->num_seqs : 1u;
+    a.shift = shift;
+    a.group_channels = in->channels / in->groups;
+    a.group_blocks = (uint32_t)ceil_div(a.group_channels, kScanChannels);
+    a.col_blocks = in->groups * a.group_blocks;
+    return a;
+}
+
+ps_status scan_sizes(const ps_scan_input *in, bool packed) {
+    if (!in) return PS_ERR_NULL;
+    if (!dtype_bytes(in->dtype)) return PS_ERR_UNSUPPORTED;
+    const int64_t c = in->channels, gn = (int64_t)in->groups * in->states;
+    if (in->tokens > kBlockMaxTokens || in->channels == 0u || in->channels > kBlockMaxChannels || in->groups == 0u ||
+        in->groups > in->channels || in->channels % in->groups || in->states == 0u || in->states > PS_SCAN_MAX_STATES ||
+        in->num_seqs > kBlockMaxSeqs || in->x_stride < c || in->dt_stride < c || (in->z && in->z_stride < c) ||
+        in->b_stride < gn || in->c_stride < gn)
+        return PS_ERR_SIZE;
+    if (packed && !in->offsets && in->num_seqs > 1u) return PS_ERR_SIZE;
+    return PS_OK;
+}
+
+ps_status scan_pointers(const ps_scan_input *in) {
+    const size_t e = dtype_bytes(in->dtype);
+    if (!in->A || (in->tokens && (!in->x || !in->dt || !in->B || !in->C))) return PS_ERR_NULL;
+    if (!aligned(in->x, e) || !aligned(in->dt, e) || !aligned(in->z, e) || !aligned(in->B, e) || !aligned(in->C, e) ||
+        !aligned(in->A, 4) || !aligned(in->D, 4) || !aligned(in->dt_bias, 4) || !aligned(in->offsets, 4) ||
+        !aligned(in->initial, 4))
+        return PS_ERR_ALIGNMENT;
+    return PS_OK;
+}
+
+bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes) {
+    const size_t e = dtype_bytes(in->dtype);
+    const uint64_t gn = (uint64_t)in->groups * in->states;
+    return p && (ranges_overlap(p, bytes, in->x, rows_bytes(in->tokens, in->x_stride, in->channels, e)) ||
+                 ranges_overlap(p, bytes, in->dt, rows_bytes(in->tokens, in->dt_stride, in->channels, e)) ||
+                 (in->z && ranges_overlap(p, bytes, in->z, rows_bytes(in->tokens, in->z_stride, in->channels, e))) ||
+                 ranges_overlap(p, bytes, in->B, rows_bytes(in->tokens, in->b_stride, gn, e)) ||
+                 ranges_overlap(p, bytes, in->C, rows_bytes(in->tokens, in->c_stride, gn, e)));
+}
+
+void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
+                      bool backward, hipStream_t s) {
+    const uint64_t grid = ceil_div((uint64_t)a.channels * a.states, 256);
+    hipLaunchKernelGGL(scan_link_kernel, dim3((uint32_t)grid), dim3(256), 0, s, a, carry, steps, links, cells,
+                       backward ? 1 : 0);
+}
+
+}  // namespace dwps
+
+using namespace dwps;
+
+extern "C" uint64_t ps_selective_scan_checkpoint_rows(uint64_t tokens, uint32_t states) {
+    (void)states;  // the same spacing for every number of states
+    return ceil_div(tokens, kScanCell);
+}
+
+extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan_input *in, void *out, float *final,
+                                       float *checkpoints, void *stream) {
+    ps_status st = scan_sizes(in, true);
+    if (st != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype);
+    const uint64_t DN = (uint64_t)in->channels * in->states;
+    const bool split = scan_split(in);
+    const ScanArgs a = scan_args(in, split ? kScanCellShift : 32u);
+    const uint64_t cells = ceil_div(in->tokens, kScanCell);
+    PlainWs plan;
+    size_t carry_at = 0, steps_at = 0, links_at = 0;
+    if (split) {
+        carry_at = plan.take((cells + 1u) * DN * 4u);
+        steps_at = plan.take((cells + 1u) * in->channels * 4u);
+        links_at = plan.take((cells + 1u) * 4u);
+    }
+    bool query = false;
+    st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+    if (st != PS_OK || query) return st;
+    if ((st = scan_pointers(in)) != PS_OK) return st;
+    if (in->tokens && !out) return PS_ERR_NULL;
+    if (!aligned(ws, 16) || !aligned(out, e) || !aligned(final, 4) || !aligned(checkpoints, 4)) return PS_ERR_ALIGNMENT;
+    const size_t out_bytes = in->tokens * in->channels * e, state_bytes = (size_t)a.num_seqs * DN * 4u;
+    const size_t mark_bytes = cells * DN * 4u;
+    if (scan_overlaps(in, out, out_bytes) || scan_overlaps(in, final, state_bytes) ||
+        scan_overlaps(in, checkpoints, mark_bytes) || (final && ranges_overlap(final, state_bytes, out, out_bytes)) ||
+        (final && in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)) ||
+        (checkpoints && ranges_overlap(checkpoints, mark_bytes, out, out_bytes)))
+        return PS_ERR_ALIAS;
+    const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
+    if (grid > kScanMaxGrid) return PS_ERR_SIZE;
+    if (!grid) return PS_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_states(in->states, [&](auto sc) {
+            constexpr int S = decltype(sc)::value;
+            float *carry = split ? ws_at<float>(ws, carry_at) : nullptr;
+            float *steps = split ? ws_at<float>(ws, steps_at) : nullptr;
+            uint32_t *links = split ? ws_at<uint32_t>(ws, links_at) : nullptr;
+            timing_begin(s);
+            if (split) {
+                hipLaunchKernelGGL((scan_walk_kernel<T, S, false>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+                                   (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
+                                   plan.words());
+                launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
+            }
+            hipLaunchKernelGGL((scan_walk_kernel<T, S, true>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+                               static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, float *new_state,
+                                            const int32_t *slots, uint32_t pool, void *out, void *stream) {
+    ps_status st = scan_sizes(in, false);
+    if (st != PS_OK) return st;
+    if ((st = scan_pointers(in)) != PS_OK) return st;
+    const size_t e = dtype_bytes(in->dtype);
+    if (in->tokens && (!out || (pool && (!state || !new_state)))) return PS_ERR_NULL;
+    if (!aligned(out, e) || !aligned(state, 4) || !aligned(new_state, 4) || !aligned(slots, 4)) return PS_ERR_ALIGNMENT;
+    if (!slots && in->tokens > pool) return PS_ERR_SIZE;
+    const size_t out_bytes = in->tokens * in->channels * e;
+    const size_t state_bytes = (size_t)pool * in->channels * in->states * 4u;
+    if (scan_overlaps(in, out, out_bytes) || scan_overlaps(in, new_state, state_bytes) ||
+        ranges_overlap(out, out_bytes, state, state_bytes) || ranges_overlap(out, out_bytes, new_state, state_bytes) ||
+        (state != new_state && ranges_overlap(new_state, state_bytes, state, state_bytes)))
+        return PS_ERR_ALIAS;
+    if (!in->tokens) return PS_OK;
+    uint32_t lanes = 1u;
+    while (lanes < 64u && lanes * 4u < in->states) lanes *= 2u;
+    const uint64_t blocks = ceil_div((uint64_t)in->channels * lanes, 256);
+    if (in->tokens * blocks > kScanMaxGrid) return PS_ERR_SIZE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const ScanArgs a = scan_args(in, 32u);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        timing_begin(s);
+        hipLaunchKernelGGL(scan_step_kernel<T>, dim3((uint32_t)(in->tokens * blocks)), dim3(256), 0, s, a, state,
+                           new_state, slots, pool, static_cast<T *>(out), lanes, (uint32_t)blocks);
+        timing_end(s);
+        return launch_status();
+    });
+}

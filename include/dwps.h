@@ -111,8 +111,10 @@ typedef enum ps_status {
 } ps_status;
 
 /* Element types.  PS_U64 names the widening sum: uint32 inputs, uint64
- * outputs and total (ps_scan with PS_OP_SUM only). */
-typedef enum ps_dtype { PS_U32 = 0, PS_F32 = 1, PS_U64 = 2 } ps_dtype;
+ * outputs and total (ps_scan with PS_OP_SUM only).  PS_BF16 and PS_F16 are
+ * types of the state space block's activations (with PS_F32); the scans do
+ * not take them. */
+typedef enum ps_dtype { PS_U32 = 0, PS_F32 = 1, PS_U64 = 2, PS_BF16 = 3, PS_F16 = 4 } ps_dtype;
 
 /* Associative operators ([P2] "Inclusive, exclusive and associative": any
  * associative operator, commutativity not required).  Operands are always
@@ -568,6 +570,153 @@ uint32_t ps_lookback_debug_get(void);
  * timing a sample of the calls spreads thin. */
 ps_status ps_kernel_timing(int every);
 ps_status ps_kernel_timing_read(double *total_ms, uint64_t *launches);
+
+/* ---------------------------------------------------------------------
+ * The operators of a state space block: a short causal convolution, the
+ * selective scan (the linear recurrence of [P2] "What scan builds" with
+ * decays and inputs computed from the tokens), and the norms around the
+ * block.  Shared rules:
+ *  - Activations are PS_BF16, PS_F16 or PS_F32, one type per call, rows of
+ *    tokens: row t starts at element t * stride, its channels follow one
+ *    another; strides are in elements, at least the row's length, and
+ *    outputs of the call are packed (stride = row length).  Parameters
+ *    (weight, bias, A, D, dt_bias, norm weights), scan states and the
+ *    gradients of all of these are fp32.  All arithmetic is fp32; a value is
+ *    rounded once, when it is stored.
+ *  - Tokens of several sequences are packed one after another: rows
+ *    offsets[s] .. offsets[s + 1] are sequence s (num_seqs + 1 entries, not
+ *    decreasing, as in the segmented scan).  Sequences may be empty.
+ *    offsets == NULL with num_seqs <= 1 means one sequence of all rows.
+ *    Rows outside [offsets[0], offsets[num_seqs]) belong to no sequence:
+ *    their outputs are not written, and they count in no sum.  Offsets that
+ *    break the contract give wrong values, never an access out of bounds.
+ *  - Nothing crosses from one sequence to another, NaN and infinities
+ *    included.
+ *  - Sums over tokens or channels are formed in a fixed order: the same call
+ *    gives the same bits.
+ *  - No output may overlap an input or another output, but for the step
+ *    calls' new_state, which may be the state itself (else PS_ERR_ALIAS for
+ *    the main arrays).
+ *  - Calls with a workspace use it as plain memory (it need not be prepared,
+ *    and a prepared one stays ready for the scans).  They follow the same
+ *    two-call pattern; pointers of the structs are not looked at in the size
+ *    query, sizes and types are.
+ *  - PS_ERR_SIZE: 0 channels, width outside 1..PS_CONV_MAX_WIDTH, states
+ *    outside 1..PS_SCAN_MAX_STATES, channels not a multiple of groups,
+ *    2^31 tokens or more, more than 2^24 channels (norms:
+ *    PS_NORM_MAX_CHANNELS), 2^24 sequences or more, a stride below the row's
+ *    length.
+ * ------------------------------------------------------------------ */
+#define PS_CONV_MAX_WIDTH 8
+#define PS_SCAN_MAX_STATES 256
+#define PS_NORM_MAX_CHANNELS 16384
+
+/* Causal convolution over each channel's own past, with silu:
+ *   pre[t, d] = bias[d] + sum_k weight[d, k] * x[t - (width - 1) + k, d]
+ *   out[t, d] = pre * sigmoid(pre)
+ * where rows before a sequence's first are initial[s] (width - 1 rows of
+ * activations, oldest first), or zero without it. */
+typedef struct ps_conv_input {
+    const void *x;           /* [tokens, channels] */
+    int64_t x_stride;
+    const float *weight;     /* [channels, width] */
+    const float *bias;       /* [channels] or NULL */
+    const uint32_t *offsets; /* [num_seqs + 1] or NULL */
+    const void *initial;     /* [num_seqs, width - 1, channels] or NULL */
+    uint64_t tokens;
+    uint32_t channels, width, num_seqs;
+    ps_dtype dtype;
+} ps_conv_input;
+/* final (optional): [num_seqs, width - 1, channels], the last width - 1 rows
+ * of each sequence and its initial rows, the initial of what follows. */
+ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *final, void *stream);
+/* Gradients of out given dout (packed): dx [tokens, channels] and dinitial
+ * [num_seqs, width - 1, channels] in the activations' type, dweight
+ * [channels, width] and dbias [channels] in fp32.  dinitial and dbias may be
+ * NULL. */
+ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_conv_input *in, const void *dout,
+                             void *dx, float *dweight, float *dbias, void *dinitial, void *stream);
+/* One token for each of in->tokens rows: row i continues the sequence whose
+ * last width - 1 rows are state[slots[i]] ([pool, width - 1, channels];
+ * slots == NULL: slot i), and new_state[slots[i]] becomes the rows after it.
+ * Slots must differ from one another.  A slot outside [0, pool) (padding of a
+ * batch) reads zeros and writes no state.  in->offsets and in->initial are
+ * not used. */
+ps_status ps_causal_conv_step(const ps_conv_input *in, const void *state, void *new_state,
+                              const int32_t *slots, uint32_t pool, void *out, void *stream);
+
+/* Selective scan.  With step = softplus(dt + dt_bias), for every channel d
+ * and state n (B and C are shared by the channels / groups channels of a
+ * group):
+ *   h[t, d, n] = exp(step[t, d] A[d, n]) h[t - 1, d, n] + step[t, d] B[t, n] x[t, d]
+ *   out[t, d]  = (sum_n C[t, n] h[t, d, n] + D[d] x[t, d]) * z sigmoid(z)
+ * h before a sequence's first row is initial[s], or zero without it; D, z
+ * and dt_bias are optional (no term, no gate, no bias). */
+typedef struct ps_scan_input {
+    const void *x, *dt, *z;  /* [tokens, channels]; z may be NULL */
+    const void *B, *C;       /* [tokens, groups, states] */
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+    const float *A;          /* [channels, states] */
+    const float *D;          /* [channels] or NULL */
+    const float *dt_bias;    /* [channels] or NULL */
+    const uint32_t *offsets; /* [num_seqs + 1] or NULL */
+    const float *initial;    /* [num_seqs, channels, states] or NULL */
+    uint64_t tokens;
+    uint32_t channels, groups, states, num_seqs;
+    ps_dtype dtype;
+} ps_scan_input;
+/* Rows of a call's checkpoints: the states that enter every
+ * 32nd packed row, which the backward pass starts from. */
+uint64_t ps_selective_scan_checkpoint_rows(uint64_t tokens, uint32_t states);
+/* final (optional): [num_seqs, channels, states], the states after each
+ * sequence.  checkpoints (optional): [checkpoint rows, channels, states]. */
+ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan_input *in, void *out, float *final,
+                            float *checkpoints, void *stream);
+/* Gradients of out given dout (packed), from the checkpoints that
+ * ps_selective_scan wrote for the same input: dx, ddt, dz [tokens,
+ * channels], dB, dC [tokens, groups, states] in the activations' type; dA
+ * [channels, states], dD, ddt_bias [channels], dinitial [num_seqs, channels,
+ * states] in fp32.  dz, dD, ddt_bias and dinitial may be NULL. */
+typedef struct ps_scan_grads {
+    void *dx, *ddt, *dz, *dB, *dC;
+    float *dA, *dD, *ddt_bias, *dinitial;
+} ps_scan_grads;
+ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_scan_input *in, const void *dout,
+                                const float *checkpoints, const ps_scan_grads *grads, void *stream);
+/* One token for each of in->tokens rows, with state and new_state [pool,
+ * channels, states] in fp32; slots as in ps_causal_conv_step.  in->offsets
+ * and in->initial are not used. */
+ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, float *new_state,
+                                 const int32_t *slots, uint32_t pool, void *out, void *stream);
+
+/* The norms around a block, with its gate and residual sum.  With
+ * norm(v) = v / sqrt(mean(v^2) + eps) over a row:
+ *   residual_out = residual + scale * sigmoid(gate) * norm(y) * post_weight
+ *   out          = norm(residual_out) * pre_weight
+ * (out from residual_out before it is rounded).  gate, scale, post_weight
+ * and pre_weight are optional (factors of 1).  residual and residual_out
+ * have the type residual_dtype, which is dtype or PS_F32. */
+typedef struct ps_norm_input {
+    const void *y, *gate;    /* [tokens, channels] */
+    const void *residual;    /* [tokens, channels]; the backward pass: residual_out */
+    int64_t y_stride, gate_stride, residual_stride;
+    const float *scale, *post_weight, *pre_weight; /* [channels] */
+    uint64_t tokens;
+    uint32_t channels;
+    ps_dtype dtype, residual_dtype;
+    float eps;
+} ps_norm_input;
+ps_status ps_block_norm(const ps_norm_input *in, void *residual_out, void *out, void *stream);
+/* Gradients given dout and dresidual_out (both packed, the latter of the
+ * residual's type, NULL = zero): dy, dgate (of dtype), dresidual (of
+ * residual_dtype), dscale, dpost_weight, dpre_weight (fp32).  dgate and the
+ * last three may be NULL. */
+typedef struct ps_norm_grads {
+    void *dy, *dgate, *dresidual;
+    float *dscale, *dpost_weight, *dpre_weight;
+} ps_norm_grads;
+ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm_input *in, const void *dout,
+                            const void *dresidual_out, const ps_norm_grads *grads, void *stream);
 
 /* Elements per tile of the flat scan kernel for `dtype` (PS_U64: the
  * widening scan), of the segmented
