@@ -56,12 +56,23 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs &a, uint32_t b) {
     return w;
 }
 
-// Two neighbouring elements, or zeros where they are not `in`.
-template <class T>
-__device__ __forceinline__ void load_pair(float (&v)[2], const T *p, bool in0, bool in1) {
-    v[0] = in0 ? (float)p[0] : 0.0f;
-    v[1] = in1 ? (float)p[1] : 0.0f;
+// Two neighbouring elements of a token's row as they lie in memory.  FULL:
+// both exist, one load.  Otherwise each has an offset of its own that stays
+// inside the row (the second of a pair that ends the row, or both of a pair
+// past it, repeat an element), and pair_values drops what is not `in`.  No
+// load is under a branch, so all of a block's are on their way at once.
+template <bool FULL, class T>
+__device__ __forceinline__ Pack<T, 2> load_pair(const T *row, uint32_t off0, uint32_t off1) {
+    if (FULL) return *reinterpret_cast<const Pack<T, 2> *>(row + off0);
+    return Pack<T, 2>{{row[off0], row[off1]}};
 }
+template <class T>
+__device__ __forceinline__ void pair_values(float (&v)[2], const Pack<T, 2> &r, bool in0, bool in1) {
+    v[0] = in0 ? (float)r.v[0] : 0.0f;
+    v[1] = in1 ? (float)r.v[1] : 0.0f;
+}
+// Offset of element c of `have`, kept inside.
+__device__ __forceinline__ uint32_t inside(uint32_t c, uint32_t have) { return c < have ? c : have - 1u; }
 
 // How far each carry reaches: row 0 unused.
 enum ScanLink : uint32_t { kLinkNone = 0, kLinkStart = 1, kLinkChain = 2 };
@@ -77,6 +88,14 @@ bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes);
 // exp(A steps[c]) carry[c -+ 1], or part[c] alone where the chain starts.
 void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
                       bool backward, hipStream_t s);
+
+// Calls f(true) if every group is made of whole blocks of 16 channels and 16
+// states (pairs are then loaded whole).
+template <class F>
+inline ps_status with_full(const ps_scan_input *in, F f) {
+    if (in->channels / in->groups % kScanChannels == 0u && in->states % 16u == 0u) return f(std::true_type());
+    return f(std::false_type());
+}
 
 // Calls f with the states of a lane (a power of two >= states / 16).
 template <class F>

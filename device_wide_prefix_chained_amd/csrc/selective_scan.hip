@@ -14,14 +14,25 @@ namespace {
 // the initial states or from carry[cell].  Otherwise: only what the piece
 // adds to the states that enter the next cell (carry[cell + 1]) and the sum
 // of its steps, for pieces that go on there.
-template <class T, int S, bool OUT>
+//
+// A block of 32 tokens is loaded kAhead blocks before its turn, staged in one
+// half of shared memory (step, step x, B, C as fp32, tokens next to one
+// another), and walked by all lanes; its outputs are gated and stored while
+// the next block is staged, so there is one barrier a block.  The walk is
+// bound by arithmetic: for every state exp2 and 4 more operations (the
+// broadcasts of step and step x are part of the products), 45 for 16 sums
+// over states.
+constexpr int kAhead = 2;
+
+template <class T, int S, bool OUT, bool FULL>
 __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *__restrict__ out,
                                                                  float *__restrict__ fin, float *__restrict__ marks,
                                                                  float *__restrict__ carry, float *__restrict__ steps,
                                                                  uint32_t *__restrict__ links, uint32_t *hdr,
                                                                  uint32_t words) {
-    __shared__ __attribute__((aligned(16))) float sStep[kScanChannels * kScanPad], sDrive[kScanChannels * kScanPad],
-        sY[OUT ? kScanChannels * kScanPad : 1], sB[16 * S * kScanPad], sC[OUT ? 16 * S * kScanPad : 1];
+    constexpr int kPlane = kScanChannels * kScanPad;
+    __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sDrive[2][kPlane], sY[2][OUT ? kPlane : 1],
+        sB[2][16 * S * kScanPad], sC[2][OUT ? 16 * S * kScanPad : 1];
     if (!OUT && blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
     const ScanPlace w = scan_place(a, xcd_neighbours(blockIdx.x, gridDim.x, sizeof(T) == 2 ? 4u : 2u));
     const Piece &q = w.q;
@@ -36,12 +47,35 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             links[q.cell + 1u] = !on ? kLinkNone : q.lo == q.seq_lo ? kLinkStart : kLinkChain;
         if (!on) return;
     }
-    // staging: two channels of one token
+    // staging: two channels (and two states of each 16) of one token
     const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
-    const bool in0 = c2 < w.have, in1 = c2 + 1u < w.have;
+    const bool in0 = FULL || c2 < w.have, in1 = FULL || c2 + 1u < w.have;
+    const uint32_t o0 = FULL ? c2 : inside(c2, w.have), o1 = FULL ? c2 + 1u : inside(c2 + 1u, w.have);
     const uint32_t cs = w.ch0 + c2;
     const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
-    const float skip0 = a.D && in0 ? a.D[cs] : 0.0f, skip1 = a.D && in1 ? a.D[cs + 1] : 0.0f;
+    const float skip0 = OUT && a.D && in0 ? a.D[cs] : 0.0f, skip1 = OUT && a.D && in1 ? a.D[cs + 1] : 0.0f;
+    const bool gated = OUT && a.z;
+    const T *px = static_cast<const T *>(a.x) + w.ch0, *pdt = static_cast<const T *>(a.dt) + w.ch0;
+    const T *pz = static_cast<const T *>(gated ? a.z : a.x) + w.ch0;  // without a gate: any row, not used
+    const int64_t z_stride = gated ? a.z_stride : a.x_stride;
+    const T *pB = static_cast<const T *>(a.B) + (int64_t)w.group * N, *pC = static_cast<const T *>(a.C) + (int64_t)w.group * N;
+    struct Raw {
+        Pack<T, 2> x, dt, z, B[S], C[OUT ? S : 1];
+    };
+    auto load = [&](Raw &r, uint32_t blk) {
+        // rows outside the piece repeat one inside it; staging drops them
+        uint32_t t = blk + row;
+        t = t < q.lo ? q.lo : t >= q.hi ? q.hi - 1u : t;
+        r.x = load_pair<FULL, T>(px + (int64_t)t * a.x_stride, o0, o1);
+        r.dt = load_pair<FULL, T>(pdt + (int64_t)t * a.dt_stride, o0, o1);
+        if (OUT) r.z = load_pair<FULL, T>(pz + (int64_t)t * z_stride, o0, o1);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t n = s * 16 + c2, n0 = FULL ? n : inside(n, N), n1 = FULL ? n + 1u : inside(n + 1u, N);
+            r.B[s] = load_pair<FULL, T>(pB + (int64_t)t * a.b_stride, n0, n1);
+            if (OUT) r.C[s] = load_pair<FULL, T>(pC + (int64_t)t * a.c_stride, n0, n1);
+        }
+    };
     // walking: one channel of a row of lanes
     const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
     const uint32_t cw = (threadIdx.x >> 6) * 4u + (lane >> 4);
@@ -58,69 +92,99 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             else if (OUT) h[s] = carry[(int64_t)q.cell * DN + (int64_t)d * N + n];
         }
     }
-    for (uint32_t blk = q.lo & ~(uint32_t)(kScanTile - 1); blk < q.hi; blk += kScanTile) {
+    Raw raw[kAhead];
+    const uint32_t first = q.lo & ~(uint32_t)(kScanTile - 1);
+    if (q.lo < q.hi) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) load(raw[k], first + k * kScanTile);
+    }
+    float px2[2] = {0.0f, 0.0f}, pz2[2] = {0.0f, 0.0f};  // x, z of the block before
+    auto store = [&](uint32_t blk, const float *y) {
+        const uint32_t t = blk + row;
+        if (t < q.lo || t >= q.hi) return;
+        float y0 = __builtin_fmaf(skip0, px2[0], y[c2 * kScanPad + row]);
+        float y1 = __builtin_fmaf(skip1, px2[1], y[(c2 + 1) * kScanPad + row]);
+        if (gated) {
+            y0 *= silu(pz2[0]);
+            y1 *= silu(pz2[1]);
+        }
+        T *o = out + (int64_t)t * a.channels + cs;
+        if (FULL) {
+            *reinterpret_cast<Pack<T, 2> *>(o) = Pack<T, 2>{{(T)y0, (T)y1}};
+        } else {
+            if (in0) o[0] = (T)y0;
+            if (in1) o[1] = (T)y1;
+        }
+    };
+    auto block = [&](Raw &r, uint32_t blk, int half) {
         const uint32_t t = blk + row;
         const bool live = t >= q.lo && t < q.hi;
-        float x[2], dt[2], z[2] = {0.0f, 0.0f};
-        load_pair<T>(x, static_cast<const T *>(a.x) + (int64_t)t * a.x_stride + cs, live && in0, live && in1);
-        load_pair<T>(dt, static_cast<const T *>(a.dt) + (int64_t)t * a.dt_stride + cs, live && in0, live && in1);
-        if (OUT && a.z)
-            load_pair<T>(z, static_cast<const T *>(a.z) + (int64_t)t * a.z_stride + cs, live && in0, live && in1);
-        const float st0 = live ? softplus(dt[0] + bias0) : 0.0f, st1 = live ? softplus(dt[1] + bias1) : 0.0f;
-        sStep[c2 * kScanPad + row] = st0;
-        sStep[(c2 + 1) * kScanPad + row] = st1;
-        sDrive[c2 * kScanPad + row] = st0 * x[0];
-        sDrive[(c2 + 1) * kScanPad + row] = st1 * x[1];
+        float x[2], z[2], v[2];
+        pair_values<T>(x, r.x, live && in0, live && in1);
+        pair_values<T>(v, r.dt, true, true);
+        if (OUT) pair_values<T>(z, r.z, true, true);
+        const float st0 = live && in0 ? softplus(v[0] + bias0) : 0.0f, st1 = live && in1 ? softplus(v[1] + bias1) : 0.0f;
+        sStep[half][c2 * kScanPad + row] = st0;
+        sStep[half][(c2 + 1) * kScanPad + row] = st1;
+        sDrive[half][c2 * kScanPad + row] = st0 * x[0];
+        sDrive[half][(c2 + 1) * kScanPad + row] = st1 * x[1];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const uint32_t n = s * 16 + c2;
-            float v[2];
-            load_pair<T>(v, static_cast<const T *>(a.B) + (int64_t)t * a.b_stride + w.group * N + n, live && n < N,
-                         live && n + 1 < N);
-            sB[n * kScanPad + row] = v[0];
-            sB[(n + 1) * kScanPad + row] = v[1];
+            pair_values<T>(v, r.B[s], live && (FULL || n < N), live && (FULL || n + 1u < N));
+            sB[half][n * kScanPad + row] = v[0];
+            sB[half][(n + 1) * kScanPad + row] = v[1];
             if (OUT) {
-                load_pair<T>(v, static_cast<const T *>(a.C) + (int64_t)t * a.c_stride + w.group * N + n, live && n < N,
-                             live && n + 1 < N);
-                sC[n * kScanPad + row] = v[0];
-                sC[(n + 1) * kScanPad + row] = v[1];
+                pair_values<T>(v, r.C[s], live && (FULL || n < N), live && (FULL || n + 1u < N));
+                sC[half][n * kScanPad + row] = v[0];
+                sC[half][(n + 1) * kScanPad + row] = v[1];
             }
         }
+        load(r, blk + kAhead * kScanTile);
         if (OUT && marks && blk > q.lo && (blk & (kScanCell - 1u)) == 0u && cw < w.have) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (s * 16 + l < N) marks[(int64_t)(blk >> kScanCellShift) * DN + (int64_t)d * N + s * 16 + l] = h[s];
         }
         __syncthreads();
+        if (OUT) {
+            if (blk > first) store(blk - kScanTile, sY[half ^ 1]);
+            px2[0] = x[0], px2[1] = x[1], pz2[0] = z[0], pz2[1] = z[1];
+        }
 #pragma unroll
         for (int sub = 0; sub < kScanTile / 16; ++sub) {
-            const float st = sStep[cw * kScanPad + sub * 16 + l], dr = sDrive[cw * kScanPad + sub * 16 + l];
+            const float st = sStep[half][cw * kScanPad + sub * 16 + l], dr = sDrive[half][cw * kScanPad + sub * 16 + l];
             if (!OUT) total += st;
             float y[16];
             auto token = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
                 const float stj = row_lane<j>(st), drj = row_lane<j>(dr);
-                y[j] = 0.0f;
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const float e = exp2_hw(stj * A2[s]);
-                    h[s] = __builtin_fmaf(e, h[s], drj * sB[(s * 16 + l) * kScanPad + sub * 16 + j]);
-                    if (OUT) y[j] = __builtin_fmaf(h[s], sC[(s * 16 + l) * kScanPad + sub * 16 + j], y[j]);
+                    h[s] = __builtin_fmaf(e, h[s], drj * sB[half][(s * 16 + l) * kScanPad + sub * 16 + j]);
+                    if (OUT) {
+                        const float c = sC[half][(s * 16 + l) * kScanPad + sub * 16 + j];
+                        y[j] = s ? __builtin_fmaf(h[s], c, y[j]) : h[s] * c;
+                    }
                 }
             };
             for_each_index(token, std::make_integer_sequence<int, 16>());
-            if (OUT) sY[cw * kScanPad + sub * 16 + l] = row_sums(y, lane);
+            if (OUT) sY[half][cw * kScanPad + sub * 16 + l] = row_sums(y, lane);
         }
-        __syncthreads();
-        if (OUT && live) {
-            T *o = out + (int64_t)t * a.channels + cs;
-            const float y0 = __builtin_fmaf(skip0, x[0], sY[c2 * kScanPad + row]);
-            const float y1 = __builtin_fmaf(skip1, x[1], sY[(c2 + 1) * kScanPad + row]);
-            if (in0) o[0] = (T)(a.z ? y0 * silu(z[0]) : y0);
-            if (in1) o[1] = (T)(a.z ? y1 * silu(z[1]) : y1);
-        }
+    };
+    static_assert(kAhead == 2, "the two halves of shared memory go round with the loads in flight");
+    uint32_t blk = first;
+    for (; blk < q.hi; blk += 2 * kScanTile) {
+        block(raw[0], blk, 0);
+        if (blk + kScanTile < q.hi) block(raw[1], blk + kScanTile, 1);
     }
     if (OUT) {
+        if (q.lo < q.hi) {  // the last block's outputs
+            const uint32_t last = (q.hi - 1u) & ~(uint32_t)(kScanTile - 1);
+            __syncthreads();
+            store(last, sY[((last - first) / kScanTile) & 1u]);
+        }
         if (fin && q.hi == q.seq_hi && cw < w.have) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
@@ -319,17 +383,20 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
             float *carry = split ? ws_at<float>(ws, carry_at) : nullptr;
             float *steps = split ? ws_at<float>(ws, steps_at) : nullptr;
             uint32_t *links = split ? ws_at<uint32_t>(ws, links_at) : nullptr;
+            return with_full(in, [&](auto full) {
+            constexpr bool FULL = decltype(full)::value;
             timing_begin(s);
             if (split) {
-                hipLaunchKernelGGL((scan_walk_kernel<T, S, false>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+                hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
                                    (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
                                    plan.words());
                 launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
             }
-            hipLaunchKernelGGL((scan_walk_kernel<T, S, true>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+            hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
                                static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
             timing_end(s);
             return launch_status();
+            });
         });
     });
 }

@@ -22,6 +22,13 @@
 namespace dwps {
 namespace {
 
+// Two neighbouring elements, or zeros where they are not `in`.
+template <class T>
+__device__ __forceinline__ void load_pair(float (&v)[2], const T *p, bool in0, bool in1) {
+    v[0] = in0 ? (float)p[0] : 0.0f;
+    v[1] = in1 ? (float)p[1] : 0.0f;
+}
+
 // Walks backwards over a piece (a whole sequence, or its rows in one cell).
 // WHOLE: stores the carry at every cell it crosses.  Otherwise stores what
 // the piece adds to the carry out of its cell, and the sum of its steps.
