@@ -75,21 +75,40 @@ __device__ __forceinline__ float row_lane(float v) {
 constexpr int kRowMirror = 0x140, kRowHalfMirror = 0x141, kQuadSwap2 = 0x4E, kQuadSwap1 = 0xB1;
 
 // Sixteen sums across each row of 16 lanes at once: lane l gets the sum over
-// its row of v[l].  Every level adds a lane's half of the values it keeps to
-// its partner's (mirrored row, mirrored half, two lanes on, one lane on:
-// together the partners are the 16 lanes), so the values halve from level to
-// level: 15 additions and 30 selections in place of 64 additions.
+// its row of v[l].  Every level adds to a lane's half of the values their
+// mirror images (mirrored row, mirrored half) or neighbours (two lanes on,
+// one lane on; together the partners are the 16 lanes), so the values halve
+// from level to level.  The first two levels take whole banks of four lanes:
+// the lower half's sum is formed in every lane, then the upper half's in its
+// banks alone (a DPP bank mask, in assembly: the compiler has no way to say
+// it), 24 additions for 12 values; then 9 operations in the quads.
+#define DPP_ADD4(what, mask)                                                                                  \
+    "v_add_f32_dpp %0, %4, %4 " what " row_mask:0xf bank_mask:" mask "\n\t"                                   \
+    "v_add_f32_dpp %1, %5, %5 " what " row_mask:0xf bank_mask:" mask "\n\t"                                   \
+    "v_add_f32_dpp %2, %6, %6 " what " row_mask:0xf bank_mask:" mask "\n\t"                                   \
+    "v_add_f32_dpp %3, %7, %7 " what " row_mask:0xf bank_mask:" mask
 __device__ __forceinline__ float row_sums(const float (&v)[16], uint32_t lane) {
-    const bool b8 = lane & 8u, b4 = lane & 4u, b2 = lane & 2u, b1 = lane & 1u;
+#pragma clang fp contract(off)  // a product fused into the first addition would cost a move for its partner
+    const bool b2 = lane & 2u, b1 = lane & 1u;
     float a[8], b[4], c[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = (b8 ? v[j + 8] : v[j]) + dpp<kRowMirror>(b8 ? v[j] : v[j + 8]);
+    for (int j = 0; j < 8; ++j) a[j] = v[j] + dpp<kRowMirror>(v[j]);
+    // s_nop: two wait states between a VALU write and a DPP read of it
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = (b4 ? a[j + 4] : a[j]) + dpp<kRowHalfMirror>(b4 ? a[j] : a[j + 4]);
+    for (int j = 0; j < 8; j += 4)
+        asm("s_nop 1\n\t" DPP_ADD4("row_mirror", "0xc")
+            : "+v"(a[j]), "+v"(a[j + 1]), "+v"(a[j + 2]), "+v"(a[j + 3])
+            : "v"(v[j + 8]), "v"(v[j + 9]), "v"(v[j + 10]), "v"(v[j + 11]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = a[j] + dpp<kRowHalfMirror>(a[j]);
+    asm("s_nop 1\n\t" DPP_ADD4("row_half_mirror", "0xa")
+        : "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3])
+        : "v"(a[4]), "v"(a[5]), "v"(a[6]), "v"(a[7]));
 #pragma unroll
     for (int j = 0; j < 2; ++j) c[j] = (b2 ? b[j + 2] : b[j]) + dpp<kQuadSwap2>(b2 ? b[j] : b[j + 2]);
     return (b1 ? c[1] : c[0]) + dpp<kQuadSwap1>(b1 ? c[0] : c[1]);
 }
+#undef DPP_ADD4
 
 // The sum over each row of 16 lanes, in every lane.
 __device__ __forceinline__ float row_total(float v) {
@@ -144,6 +163,8 @@ inline size_t dtype_bytes(ps_dtype t) { return t == PS_F32 ? 4u : t == PS_BF16 |
 constexpr uint64_t kBlockMaxTokens = (1ull << 31) - 1u;
 constexpr uint32_t kBlockMaxChannels = 1u << 24;
 constexpr uint32_t kBlockMaxSeqs = (1u << 24) - 1u;
+// Offsets within 32 rows of a token array are 32-bit byte counts.
+constexpr int64_t kBlockMaxStride = 1 << 24;
 
 // Bytes from the first to past the last element of `rows` rows.
 inline size_t rows_bytes(uint64_t rows, int64_t stride, uint64_t row, size_t elem) {

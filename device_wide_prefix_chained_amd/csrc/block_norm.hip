@@ -243,7 +243,8 @@ ps_status norm_sizes(const ps_norm_input *in) {
         return PS_ERR_UNSUPPORTED;
     const int64_t c = in->channels;
     if (in->tokens > kBlockMaxTokens || c == 0 || c > PS_NORM_MAX_CHANNELS || in->y_stride < c ||
-        (in->gate && in->gate_stride < c) || in->residual_stride < c)
+        (in->gate && (in->gate_stride < c || in->gate_stride > kBlockMaxStride)) || in->residual_stride < c ||
+        in->y_stride > kBlockMaxStride || in->residual_stride > kBlockMaxStride)
         return PS_ERR_SIZE;
     return PS_OK;
 }

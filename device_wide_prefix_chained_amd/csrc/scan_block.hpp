@@ -62,10 +62,27 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs &a, uint32_t b) {
 // past it, repeat an element), and pair_values drops what is not `in`.  No
 // load is under a branch, so all of a block's are on their way at once.
 template <bool FULL, class T>
-__device__ __forceinline__ Pack<T, 2> load_pair(const T *row, uint32_t off0, uint32_t off1) {
-    if (FULL) return *reinterpret_cast<const Pack<T, 2> *>(row + off0);
-    return Pack<T, 2>{{row[off0], row[off1]}};
+__device__ __forceinline__ Pack<T, 2> load_pair(const T *base, uint32_t byte0, uint32_t byte1) {
+    const char *p = reinterpret_cast<const char *>(base);
+    if (FULL) return *reinterpret_cast<const Pack<T, 2> *>(p + byte0);
+    return Pack<T, 2>{{*reinterpret_cast<const T *>(p + byte0), *reinterpret_cast<const T *>(p + byte1)}};
 }
+// One token array as a thread of the staging sees it: its pair's place in 32
+// rows (32 bits, so that a load is one instruction on the block's address in
+// scalar registers).
+template <class T, bool FULL>
+struct PairRows {
+    const T *base;
+    int64_t stride;
+    uint32_t byte0, byte1;
+    __device__ __forceinline__ void place(uint32_t row, uint32_t e0, uint32_t e1) {
+        byte0 = (row * (uint32_t)stride + e0) * (uint32_t)sizeof(T);
+        byte1 = FULL ? 0u : (row * (uint32_t)stride + e1) * (uint32_t)sizeof(T);
+    }
+    __device__ __forceinline__ Pack<T, 2> load(uint32_t first_row) const {
+        return load_pair<FULL, T>(base + (int64_t)first_row * stride, byte0, byte1);
+    }
+};
 template <class T>
 __device__ __forceinline__ void pair_values(float (&v)[2], const Pack<T, 2> &r, bool in0, bool in1) {
     v[0] = in0 ? (float)r.v[0] : 0.0f;

@@ -55,25 +55,41 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
     const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
     const float skip0 = OUT && a.D && in0 ? a.D[cs] : 0.0f, skip1 = OUT && a.D && in1 ? a.D[cs + 1] : 0.0f;
     const bool gated = OUT && a.z;
-    const T *px = static_cast<const T *>(a.x) + w.ch0, *pdt = static_cast<const T *>(a.dt) + w.ch0;
-    const T *pz = static_cast<const T *>(gated ? a.z : a.x) + w.ch0;  // without a gate: any row, not used
-    const int64_t z_stride = gated ? a.z_stride : a.x_stride;
-    const T *pB = static_cast<const T *>(a.B) + (int64_t)w.group * N, *pC = static_cast<const T *>(a.C) + (int64_t)w.group * N;
     struct Raw {
         Pack<T, 2> x, dt, z, B[S], C[OUT ? S : 1];
     };
-    auto load = [&](Raw &r, uint32_t blk) {
-        // rows outside the piece repeat one inside it; staging drops them
-        uint32_t t = blk + row;
-        t = t < q.lo ? q.lo : t >= q.hi ? q.hi - 1u : t;
-        r.x = load_pair<FULL, T>(px + (int64_t)t * a.x_stride, o0, o1);
-        r.dt = load_pair<FULL, T>(pdt + (int64_t)t * a.dt_stride, o0, o1);
-        if (OUT) r.z = load_pair<FULL, T>(pz + (int64_t)t * z_stride, o0, o1);
+    PairRows<T, FULL> rx{static_cast<const T *>(a.x) + w.ch0, a.x_stride}, rdt{static_cast<const T *>(a.dt) + w.ch0, a.dt_stride};
+    // without a gate: any row, not used
+    PairRows<T, FULL> rz{static_cast<const T *>(gated ? a.z : a.x) + w.ch0, gated ? a.z_stride : a.x_stride};
+    PairRows<T, FULL> rB[S], rC[OUT ? S : 1];
+    auto place = [&](uint32_t r) {
+        rx.place(r, o0, o1);
+        rdt.place(r, o0, o1);
+        if (OUT) rz.place(r, o0, o1);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const uint32_t n = s * 16 + c2, n0 = FULL ? n : inside(n, N), n1 = FULL ? n + 1u : inside(n + 1u, N);
-            r.B[s] = load_pair<FULL, T>(pB + (int64_t)t * a.b_stride, n0, n1);
-            if (OUT) r.C[s] = load_pair<FULL, T>(pC + (int64_t)t * a.c_stride, n0, n1);
+            rB[s] = {static_cast<const T *>(a.B) + (int64_t)w.group * N, a.b_stride};
+            rB[s].place(r, n0, n1);
+            if (OUT) {
+                rC[s] = {static_cast<const T *>(a.C) + (int64_t)w.group * N, a.c_stride};
+                rC[s].place(r, n0, n1);
+            }
+        }
+    };
+    place(row);
+    auto load = [&](Raw &r, uint32_t blk) {
+        if (blk + kScanTile > a.tokens) {  // rows past the last repeat it; staging drops them
+            if (blk >= a.tokens) blk = a.tokens - 1u;
+            place(row < a.tokens - 1u - blk ? row : a.tokens - 1u - blk);
+        }
+        r.x = rx.load(blk);
+        r.dt = rdt.load(blk);
+        if (OUT) r.z = rz.load(blk);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            r.B[s] = rB[s].load(blk);
+            if (OUT) r.C[s] = rC[s].load(blk);
         }
     };
     // walking: one channel of a row of lanes
@@ -99,6 +115,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
         for (int k = 0; k < kAhead; ++k) load(raw[k], first + k * kScanTile);
     }
     float px2[2] = {0.0f, 0.0f}, pz2[2] = {0.0f, 0.0f};  // x, z of the block before
+    const uint32_t out_byte = (row * a.channels + c2) * (uint32_t)sizeof(T);
     auto store = [&](uint32_t blk, const float *y) {
         const uint32_t t = blk + row;
         if (t < q.lo || t >= q.hi) return;
@@ -108,7 +125,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             y0 *= silu(pz2[0]);
             y1 *= silu(pz2[1]);
         }
-        T *o = out + (int64_t)t * a.channels + cs;
+        T *o = reinterpret_cast<T *>(reinterpret_cast<char *>(out + (int64_t)blk * a.channels + w.ch0) + out_byte);
         if (FULL) {
             *reinterpret_cast<Pack<T, 2> *>(o) = Pack<T, 2>{{(T)y0, (T)y1}};
         } else {
@@ -301,7 +318,8 @@ ps_status scan_sizes(const ps_scan_input *in, bool packed) {
     if (in->tokens > kBlockMaxTokens || in->channels == 0u || in->channels > kBlockMaxChannels || in->groups == 0u ||
         in->groups > in->channels || in->channels % in->groups || in->states == 0u || in->states > PS_SCAN_MAX_STATES ||
         in->num_seqs > kBlockMaxSeqs || in->x_stride < c || in->dt_stride < c || (in->z && in->z_stride < c) ||
-        in->b_stride < gn || in->c_stride < gn)
+        in->b_stride < gn || in->c_stride < gn || in->x_stride > kBlockMaxStride || in->dt_stride > kBlockMaxStride ||
+        (in->z && in->z_stride > kBlockMaxStride) || in->b_stride > kBlockMaxStride || in->c_stride > kBlockMaxStride)
         return PS_ERR_SIZE;
     if (packed && !in->offsets && in->num_seqs > 1u) return PS_ERR_SIZE;
     return PS_OK;

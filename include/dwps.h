@@ -605,7 +605,7 @@ ps_status ps_kernel_timing_read(double *total_ms, uint64_t *launches);
  *    outside 1..PS_SCAN_MAX_STATES, channels not a multiple of groups,
  *    2^31 tokens or more, more than 2^24 channels (norms:
  *    PS_NORM_MAX_CHANNELS), 2^24 sequences or more, a stride below the row's
- *    length.
+ *    length or above 2^24.
  * ------------------------------------------------------------------ */
 #define PS_CONV_MAX_WIDTH 8
 #define PS_SCAN_MAX_STATES 256
