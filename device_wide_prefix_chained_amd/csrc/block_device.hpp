@@ -47,6 +47,9 @@ __device__ __forceinline__ float softplus(float v) {
     return base + 2.0f * (q + tail);
 }
 
+// An argument whose softplus is exactly 0.
+constexpr float kNoStep = -256.0f;
+
 // d silu(v) / dv from s = sigmoid(v).
 __device__ __forceinline__ float dsilu(float v, float s) { return s * __builtin_fmaf(v, 1.0f - s, 1.0f); }
 __device__ __forceinline__ float silu(float v) {

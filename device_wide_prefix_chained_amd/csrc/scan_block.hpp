@@ -56,17 +56,48 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs &a, uint32_t b) {
     return w;
 }
 
-// Two neighbouring elements of a token's row as they lie in memory.  FULL:
-// both exist, one load.  Otherwise each has an offset of its own that stays
-// inside the row (the second of a pair that ends the row, or both of a pair
-// past it, repeat an element), and pair_values drops what is not `in`.  No
-// load is under a branch, so all of a block's are on their way at once.
-template <bool FULL, class T>
-__device__ __forceinline__ Pack<T, 2> load_pair(const T *base, uint32_t byte0, uint32_t byte1) {
-    const char *p = reinterpret_cast<const char *>(base);
-    if (FULL) return *reinterpret_cast<const Pack<T, 2> *>(p + byte0);
-    return Pack<T, 2>{{*reinterpret_cast<const T *>(p + byte0), *reinterpret_cast<const T *>(p + byte1)}};
-}
+// Two neighbouring elements of a token's row as they were loaded.  FULL: both
+// exist, one load (kept as the 32 bits it is: split into elements, the
+// compiler would wait for it long before its use).  Otherwise each has an
+// offset of its own that stays inside the row (the second of a pair that ends
+// the row, or both of a pair past it, repeat an element), and values() drops
+// what is not `in`.  No load is under a branch, so all of a block's are on
+// their way at once.
+template <class T, bool FULL>
+struct RawPair {
+    T e0, e1;
+    __device__ __forceinline__ void load(const char *base, uint32_t byte0, uint32_t byte1) {
+        e0 = *reinterpret_cast<const T *>(base + byte0);
+        e1 = *reinterpret_cast<const T *>(base + (FULL ? byte0 + (uint32_t)sizeof(T) : byte1));
+    }
+    __device__ __forceinline__ void values(float (&v)[2], bool in0, bool in1) const {
+        v[0] = in0 ? (float)e0 : 0.0f;
+        v[1] = in1 ? (float)e1 : 0.0f;
+    }
+};
+typedef uint32_t __attribute__((aligned(2), may_alias)) word_at_2;
+template <>
+struct RawPair<bf16_t, true> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const char *base, uint32_t byte0, uint32_t) {
+        w = *reinterpret_cast<const word_at_2 *>(base + byte0);
+    }
+    __device__ __forceinline__ void values(float (&v)[2], bool in0, bool in1) const {
+        v[0] = in0 ? __builtin_bit_cast(float, w << 16) : 0.0f;
+        v[1] = in1 ? __builtin_bit_cast(float, w & 0xFFFF0000u) : 0.0f;
+    }
+};
+template <>
+struct RawPair<f16_t, true> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const char *base, uint32_t byte0, uint32_t) {
+        w = *reinterpret_cast<const word_at_2 *>(base + byte0);
+    }
+    __device__ __forceinline__ void values(float (&v)[2], bool in0, bool in1) const {
+        v[0] = in0 ? (float)__builtin_bit_cast(f16_t, (uint16_t)w) : 0.0f;
+        v[1] = in1 ? (float)__builtin_bit_cast(f16_t, (uint16_t)(w >> 16)) : 0.0f;
+    }
+};
 // One token array as a thread of the staging sees it: its pair's place in 32
 // rows (32 bits, so that a load is one instruction on the block's address in
 // scalar registers).
@@ -79,15 +110,10 @@ struct PairRows {
         byte0 = (row * (uint32_t)stride + e0) * (uint32_t)sizeof(T);
         byte1 = FULL ? 0u : (row * (uint32_t)stride + e1) * (uint32_t)sizeof(T);
     }
-    __device__ __forceinline__ Pack<T, 2> load(uint32_t first_row) const {
-        return load_pair<FULL, T>(base + (int64_t)first_row * stride, byte0, byte1);
+    __device__ __forceinline__ void load(RawPair<T, FULL> &r, uint32_t first_row) const {
+        r.load(reinterpret_cast<const char *>(base + (int64_t)first_row * stride), byte0, byte1);
     }
 };
-template <class T>
-__device__ __forceinline__ void pair_values(float (&v)[2], const Pack<T, 2> &r, bool in0, bool in1) {
-    v[0] = in0 ? (float)r.v[0] : 0.0f;
-    v[1] = in1 ? (float)r.v[1] : 0.0f;
-}
 // Offset of element c of `have`, kept inside.
 __device__ __forceinline__ uint32_t inside(uint32_t c, uint32_t have) { return c < have ? c : have - 1u; }
 

@@ -15,22 +15,21 @@ namespace {
 // adds to the states that enter the next cell (carry[cell + 1]) and the sum
 // of its steps, for pieces that go on there.
 //
-// A block of 32 tokens is loaded kAhead blocks before its turn, staged in one
-// half of shared memory (step, step x, B, C as fp32, tokens next to one
-// another), and walked by all lanes; its outputs are gated and stored while
-// the next block is staged, so there is one barrier a block.  The walk is
-// bound by arithmetic: for every state exp2 and 4 more operations (the
-// broadcasts of step and step x are part of the products), 45 for 16 sums
-// over states.
-constexpr int kAhead = 2;
-
+// Four waves walk and four feed them.  A feeding thread loads its pair of a
+// block of 32 tokens kAhead blocks before its turn, writes step, step x, B
+// and C as fp32 into one half of shared memory while the walking waves work
+// on the other, and gates and stores the outputs of the block before; one
+// barrier a block.  The walk is bound by arithmetic: for every state exp2
+// (two issue slots) and 4 more operations (the broadcasts of step and step x
+// are part of the products), and 33 for 16 sums over states.
 template <class T, int S, bool OUT, bool FULL>
-__global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *__restrict__ out,
-                                                                 float *__restrict__ fin, float *__restrict__ marks,
-                                                                 float *__restrict__ carry, float *__restrict__ steps,
-                                                                 uint32_t *__restrict__ links, uint32_t *hdr,
-                                                                 uint32_t words) {
+__global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a, T *__restrict__ out,
+                                                                     float *__restrict__ fin, float *__restrict__ marks,
+                                                                     float *__restrict__ carry, float *__restrict__ steps,
+                                                                     uint32_t *__restrict__ links, uint32_t *hdr,
+                                                                     uint32_t words) {
     constexpr int kPlane = kScanChannels * kScanPad;
+    constexpr int kAhead = S <= 4 ? 4 : 2;  // even: the halves of shared memory go round with it
     __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sDrive[2][kPlane], sY[2][OUT ? kPlane : 1],
         sB[2][16 * S * kScanPad], sC[2][OUT ? 16 * S * kScanPad : 1];
     if (!OUT && blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
@@ -47,54 +46,135 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             links[q.cell + 1u] = !on ? kLinkNone : q.lo == q.seq_lo ? kLinkStart : kLinkChain;
         if (!on) return;
     }
-    // staging: two channels (and two states of each 16) of one token
-    const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
-    const bool in0 = FULL || c2 < w.have, in1 = FULL || c2 + 1u < w.have;
-    const uint32_t o0 = FULL ? c2 : inside(c2, w.have), o1 = FULL ? c2 + 1u : inside(c2 + 1u, w.have);
-    const uint32_t cs = w.ch0 + c2;
-    const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
-    const float skip0 = OUT && a.D && in0 ? a.D[cs] : 0.0f, skip1 = OUT && a.D && in1 ? a.D[cs + 1] : 0.0f;
-    const bool gated = OUT && a.z;
-    struct Raw {
-        Pack<T, 2> x, dt, z, B[S], C[OUT ? S : 1];
-    };
-    PairRows<T, FULL> rx{static_cast<const T *>(a.x) + w.ch0, a.x_stride}, rdt{static_cast<const T *>(a.dt) + w.ch0, a.dt_stride};
-    // without a gate: any row, not used
-    PairRows<T, FULL> rz{static_cast<const T *>(gated ? a.z : a.x) + w.ch0, gated ? a.z_stride : a.x_stride};
-    PairRows<T, FULL> rB[S], rC[OUT ? S : 1];
-    auto place = [&](uint32_t r) {
-        rx.place(r, o0, o1);
-        rdt.place(r, o0, o1);
-        if (OUT) rz.place(r, o0, o1);
+    const uint32_t first = q.lo & ~(uint32_t)(kScanTile - 1);
+    const uint32_t blocks = q.lo < q.hi ? (q.hi - first + kScanTile - 1u) / kScanTile : 0u;
+    const bool feeds = __builtin_amdgcn_readfirstlane(threadIdx.x) < (uint32_t)kScanThreads;
+    if (feeds) {
+        if (blocks == 0u) return;
+        // two channels (and two states of each 16) of one token
+        const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
+        const bool in0 = FULL || c2 < w.have, in1 = FULL || c2 + 1u < w.have;
+        const uint32_t o0 = FULL ? c2 : inside(c2, w.have), o1 = FULL ? c2 + 1u : inside(c2 + 1u, w.have);
+        const uint32_t cs = w.ch0 + c2;
+        const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
+        const float skip0 = OUT && a.D && in0 ? a.D[cs] : 0.0f, skip1 = OUT && a.D && in1 ? a.D[cs + 1] : 0.0f;
+        const bool gated = OUT && a.z;
+        struct Raw {
+            RawPair<T, FULL> x, dt, z, B[S], C[OUT ? S : 1];
+        };
+        PairRows<T, FULL> rx{static_cast<const T *>(a.x) + w.ch0, a.x_stride};
+        PairRows<T, FULL> rdt{static_cast<const T *>(a.dt) + w.ch0, a.dt_stride};
+        // without a gate: any row, not used
+        PairRows<T, FULL> rz{static_cast<const T *>(gated ? a.z : a.x) + w.ch0, gated ? a.z_stride : a.x_stride};
+        PairRows<T, FULL> rB[S], rC[OUT ? S : 1];
+        auto place = [&](uint32_t r) {
+            rx.place(r, o0, o1);
+            rdt.place(r, o0, o1);
+            if (OUT) rz.place(r, o0, o1);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint32_t n = s * 16 + c2, n0 = FULL ? n : inside(n, N), n1 = FULL ? n + 1u : inside(n + 1u, N);
-            rB[s] = {static_cast<const T *>(a.B) + (int64_t)w.group * N, a.b_stride};
-            rB[s].place(r, n0, n1);
-            if (OUT) {
-                rC[s] = {static_cast<const T *>(a.C) + (int64_t)w.group * N, a.c_stride};
-                rC[s].place(r, n0, n1);
+            for (int s = 0; s < S; ++s) {
+                const uint32_t n = s * 16 + c2, n0 = FULL ? n : inside(n, N), n1 = FULL ? n + 1u : inside(n + 1u, N);
+                rB[s] = {static_cast<const T *>(a.B) + (int64_t)w.group * N, a.b_stride};
+                rB[s].place(r, n0, n1);
+                if (OUT) {
+                    rC[s] = {static_cast<const T *>(a.C) + (int64_t)w.group * N, a.c_stride};
+                    rC[s].place(r, n0, n1);
+                }
             }
-        }
-    };
-    place(row);
-    auto load = [&](Raw &r, uint32_t blk) {
-        if (blk + kScanTile > a.tokens) {  // rows past the last repeat it; staging drops them
-            if (blk >= a.tokens) blk = a.tokens - 1u;
-            place(row < a.tokens - 1u - blk ? row : a.tokens - 1u - blk);
-        }
-        r.x = rx.load(blk);
-        r.dt = rdt.load(blk);
-        if (OUT) r.z = rz.load(blk);
+        };
+        place(row);
+        auto load = [&](Raw &r, uint32_t k) {
+            uint32_t blk = first + k * kScanTile;
+            if (blk + kScanTile > a.tokens) {  // rows past the last repeat it; staging drops them
+                if (blk >= a.tokens) blk = a.tokens - 1u;
+                place(row < a.tokens - 1u - blk ? row : a.tokens - 1u - blk);
+            }
+            rx.load(r.x, blk);
+            rdt.load(r.dt, blk);
+            if (OUT) rz.load(r.z, blk);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            r.B[s] = rB[s].load(blk);
-            if (OUT) r.C[s] = rC[s].load(blk);
+            for (int s = 0; s < S; ++s) {
+                rB[s].load(r.B[s], blk);
+                if (OUT) rC[s].load(r.C[s], blk);
+            }
+        };
+        RawPair<T, FULL> kept_x[2], kept_z[2];
+        const uint32_t out_byte = (row * a.channels + c2) * (uint32_t)sizeof(T);
+        auto stage = [&](Raw &r, uint32_t k, int half) {
+            const uint32_t t = first + k * kScanTile + row;
+            const bool live = t >= q.lo && t < q.hi;
+            float x[2], v[2];
+            r.x.values(x, live && in0, live && in1);
+            r.dt.values(v, true, true);
+            const float st0 = softplus(live && in0 ? v[0] + bias0 : kNoStep);
+            const float st1 = softplus(live && in1 ? v[1] + bias1 : kNoStep);
+            sStep[half][c2 * kScanPad + row] = st0;
+            sStep[half][(c2 + 1) * kScanPad + row] = st1;
+            sDrive[half][c2 * kScanPad + row] = st0 * x[0];
+            sDrive[half][(c2 + 1) * kScanPad + row] = st1 * x[1];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t n = s * 16 + c2;
+                r.B[s].values(v, live && (FULL || n < N), live && (FULL || n + 1u < N));
+                sB[half][n * kScanPad + row] = v[0];
+                sB[half][(n + 1) * kScanPad + row] = v[1];
+                if (OUT) {
+                    r.C[s].values(v, live && (FULL || n < N), live && (FULL || n + 1u < N));
+                    sC[half][n * kScanPad + row] = v[0];
+                    sC[half][(n + 1) * kScanPad + row] = v[1];
+                }
+            }
+            if (OUT) kept_x[half] = r.x, kept_z[half] = r.z;
+            load(r, k + kAhead);
+        };
+        auto store = [&](uint32_t k, int half) {
+            const uint32_t blk = first + k * kScanTile, t = blk + row;
+            if (t < q.lo || t >= q.hi) return;
+            float x[2], z[2];
+            kept_x[half].values(x, true, true);
+            float y0 = __builtin_fmaf(skip0, x[0], sY[half][c2 * kScanPad + row]);
+            float y1 = __builtin_fmaf(skip1, x[1], sY[half][(c2 + 1) * kScanPad + row]);
+            if (gated) {
+                kept_z[half].values(z, true, true);
+                y0 *= silu(z[0]);
+                y1 *= silu(z[1]);
+            }
+            T *o = reinterpret_cast<T *>(reinterpret_cast<char *>(out + (int64_t)blk * a.channels + w.ch0) + out_byte);
+            if (FULL) {
+                *reinterpret_cast<Pack<T, 2> *>(o) = Pack<T, 2>{{(T)y0, (T)y1}};
+            } else {
+                if (in0) o[0] = (T)y0;
+                if (in1) o[1] = (T)y1;
+            }
+        };
+        Raw raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(raw[i], i);
+        stage(raw[0], 0u, 0);
+        __syncthreads();
+        auto turn = [&](uint32_t k, int i) {
+            if (OUT && k > 0u) store(k - 1u, (i + 1) & 1);
+            stage(raw[(i + 1) % kAhead], k + 1u, (i + 1) & 1);
+            __syncthreads();
+        };
+        // Whole rounds of the ring without a branch around any load: only
+        // then does the compiler wait for the oldest loads alone.  Past the
+        // last block there are only dropped rows to stage.
+        uint32_t k = 0;
+        for (; k + kAhead <= blocks; k += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) turn(k + i, i);
         }
-    };
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i)
+            if (k + i < blocks) turn(k + i, i);
+        if (OUT && (blocks & 1u)) store(blocks - 1u, 0);
+        if (OUT && !(blocks & 1u)) store(blocks - 1u, 1);
+        return;
+    }
     // walking: one channel of a row of lanes
     const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
-    const uint32_t cw = (threadIdx.x >> 6) * 4u + (lane >> 4);
+    const uint32_t cw = ((threadIdx.x - kScanThreads) >> 6) * 4u + (lane >> 4);
     const uint32_t d = w.ch0 + cw;
     float A2[S], h[S], total = 0.0f;
 #pragma unroll
@@ -108,65 +188,12 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             else if (OUT) h[s] = carry[(int64_t)q.cell * DN + (int64_t)d * N + n];
         }
     }
-    Raw raw[kAhead];
-    const uint32_t first = q.lo & ~(uint32_t)(kScanTile - 1);
-    if (q.lo < q.hi) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) load(raw[k], first + k * kScanTile);
-    }
-    float px2[2] = {0.0f, 0.0f}, pz2[2] = {0.0f, 0.0f};  // x, z of the block before
-    const uint32_t out_byte = (row * a.channels + c2) * (uint32_t)sizeof(T);
-    auto store = [&](uint32_t blk, const float *y) {
-        const uint32_t t = blk + row;
-        if (t < q.lo || t >= q.hi) return;
-        float y0 = __builtin_fmaf(skip0, px2[0], y[c2 * kScanPad + row]);
-        float y1 = __builtin_fmaf(skip1, px2[1], y[(c2 + 1) * kScanPad + row]);
-        if (gated) {
-            y0 *= silu(pz2[0]);
-            y1 *= silu(pz2[1]);
-        }
-        T *o = reinterpret_cast<T *>(reinterpret_cast<char *>(out + (int64_t)blk * a.channels + w.ch0) + out_byte);
-        if (FULL) {
-            *reinterpret_cast<Pack<T, 2> *>(o) = Pack<T, 2>{{(T)y0, (T)y1}};
-        } else {
-            if (in0) o[0] = (T)y0;
-            if (in1) o[1] = (T)y1;
-        }
-    };
-    auto block = [&](Raw &r, uint32_t blk, int half) {
-        const uint32_t t = blk + row;
-        const bool live = t >= q.lo && t < q.hi;
-        float x[2], z[2], v[2];
-        pair_values<T>(x, r.x, live && in0, live && in1);
-        pair_values<T>(v, r.dt, true, true);
-        if (OUT) pair_values<T>(z, r.z, true, true);
-        const float st0 = live && in0 ? softplus(v[0] + bias0) : 0.0f, st1 = live && in1 ? softplus(v[1] + bias1) : 0.0f;
-        sStep[half][c2 * kScanPad + row] = st0;
-        sStep[half][(c2 + 1) * kScanPad + row] = st1;
-        sDrive[half][c2 * kScanPad + row] = st0 * x[0];
-        sDrive[half][(c2 + 1) * kScanPad + row] = st1 * x[1];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint32_t n = s * 16 + c2;
-            pair_values<T>(v, r.B[s], live && (FULL || n < N), live && (FULL || n + 1u < N));
-            sB[half][n * kScanPad + row] = v[0];
-            sB[half][(n + 1) * kScanPad + row] = v[1];
-            if (OUT) {
-                pair_values<T>(v, r.C[s], live && (FULL || n < N), live && (FULL || n + 1u < N));
-                sC[half][n * kScanPad + row] = v[0];
-                sC[half][(n + 1) * kScanPad + row] = v[1];
-            }
-        }
-        load(r, blk + kAhead * kScanTile);
+    auto walk = [&](uint32_t k, int half) {
+        const uint32_t blk = first + k * kScanTile;
         if (OUT && marks && blk > q.lo && (blk & (kScanCell - 1u)) == 0u && cw < w.have) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (s * 16 + l < N) marks[(int64_t)(blk >> kScanCellShift) * DN + (int64_t)d * N + s * 16 + l] = h[s];
-        }
-        __syncthreads();
-        if (OUT) {
-            if (blk > first) store(blk - kScanTile, sY[half ^ 1]);
-            px2[0] = x[0], px2[1] = x[1], pz2[0] = z[0], pz2[1] = z[1];
         }
 #pragma unroll
         for (int sub = 0; sub < kScanTile / 16; ++sub) {
@@ -190,18 +217,16 @@ __global__ __launch_bounds__(kScanThreads) void scan_walk_kernel(ScanArgs a, T *
             if (OUT) sY[half][cw * kScanPad + sub * 16 + l] = row_sums(y, lane);
         }
     };
-    static_assert(kAhead == 2, "the two halves of shared memory go round with the loads in flight");
-    uint32_t blk = first;
-    for (; blk < q.hi; blk += 2 * kScanTile) {
-        block(raw[0], blk, 0);
-        if (blk + kScanTile < q.hi) block(raw[1], blk + kScanTile, 1);
+    if (blocks) __syncthreads();
+    for (uint32_t k = 0; k < blocks; k += 2u) {
+        walk(k, 0);
+        __syncthreads();
+        if (k + 1u < blocks) {
+            walk(k + 1u, 1);
+            __syncthreads();
+        }
     }
     if (OUT) {
-        if (q.lo < q.hi) {  // the last block's outputs
-            const uint32_t last = (q.hi - 1u) & ~(uint32_t)(kScanTile - 1);
-            __syncthreads();
-            store(last, sY[((last - first) / kScanTile) & 1u]);
-        }
         if (fin && q.hi == q.seq_hi && cw < w.have) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
@@ -405,12 +430,12 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
             constexpr bool FULL = decltype(full)::value;
             timing_begin(s);
             if (split) {
-                hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+                hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
                                    (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
                                    plan.words());
                 launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
             }
-            hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(kScanThreads), 0, s, a,
+            hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
                                static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
             timing_end(s);
             return launch_status();
