@@ -217,6 +217,7 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a,
             if (OUT) sY[half][cw * kScanPad + sub * 16 + l] = row_sums(y, lane);
         }
     };
+    __builtin_amdgcn_s_setprio(2);  // the feeding waves fill the gaps
     if (blocks) __syncthreads();
     for (uint32_t k = 0; k < blocks; k += 2u) {
         walk(k, 0);
