@@ -75,7 +75,7 @@ template <int j>
 __device__ __forceinline__ float row_lane(float v) {
     return dpp<0x150 + j>(v);
 }
-constexpr int kRowMirror = 0x140, kRowHalfMirror = 0x141, kQuadSwap2 = 0x4E, kQuadSwap1 = 0xB1;
+constexpr int kRowRotate8 = 0x128, kRowMirror = 0x140, kRowHalfMirror = 0x141, kQuadSwap2 = 0x4E, kQuadSwap1 = 0xB1;
 
 // Sixteen sums across each row of 16 lanes at once: lane l gets the sum over
 // its row of v[l].  Every level adds to a lane's half of the values their

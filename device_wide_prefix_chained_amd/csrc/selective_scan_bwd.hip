@@ -153,22 +153,36 @@ __device__ __forceinline__ void fold_rows(float (&o)[8], float (&v)[32]) {
     }
 }
 
+// Nothing read from shared memory moves across this, so that values are read
+// where they are used and do not push others out of the registers.
+__device__ __forceinline__ void read_later() { asm volatile("" ::: "memory"); }
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f4 four(const float *p) { return *reinterpret_cast<const f4 *>(p); }
+
 // One piece of a cell, a range of channel blocks.  States 16 at a time
 // (outer loop), channels 16 at a time (inner loop): a lane sums dB and dC of
 // its state over the inner loop in registers, token by token, and keeps a
 // and h of the piece's 32 rows in registers between the walk forward and the
 // walk back.  With more than 16 states the three sums over states wait in
 // shared memory for the last 16.
-template <class T>
-__global__ __launch_bounds__(kScanThreads) void scan_grad_kernel(ScanArgs a, const T *__restrict__ dout,
-                                                                 const float *__restrict__ marks,
-                                                                 const float *__restrict__ carry, BackOut o,
-                                                                 uint32_t *hdr, uint32_t words) {
+//
+// As in the forward walk, four waves feed (they load, stage and, a block
+// later, form the block's outputs) and four walk.  Bound by arithmetic: for
+// every state 5 operations and exp2 forwards, 8 backwards and 99 / 16 for the
+// three sums over states.  The 128 sums and factors of a walking lane take
+// half of the 256 registers that two waves per SIMD leave it.
+template <class T, bool FULL, bool MANY>
+__global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs a, const T *__restrict__ dout,
+                                                                        const float *__restrict__ marks,
+                                                                        const float *__restrict__ carry, BackOut o,
+                                                                        uint32_t *hdr, uint32_t words) {
     constexpr int kPlane = kScanChannels * kScanPad;
-    __shared__ __attribute__((aligned(16))) float sStep[kPlane], sDrive[kPlane], sGrad[kPlane], sB[kPlane], sC[kPlane];
-    __shared__ float sFold[4][8][64];
-    __shared__ float sSum[4][2][kScanChannels];
-    extern __shared__ float sCell[];  // [channel blocks of the range or 1][3][kPlane]
+    __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sDrive[2][kPlane], sGrad[2][kPlane], sB[kPlane],
+        sC[kPlane];
+    __shared__ float sFold[2][4][8][64];
+    __shared__ float sSum[2][4][4][8];  // [half][wave][dD of two channels, ddt_bias of two][pair]
+    extern __shared__ float sCell[];    // [channel blocks of the range, or 2][3][kPlane]
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
     const uint32_t p = blockIdx.x / o.blocks, rg = blockIdx.x % o.blocks;
     const uint32_t group = rg / o.ranges, range = rg % o.ranges;
@@ -177,193 +191,310 @@ __global__ __launch_bounds__(kScanThreads) void scan_grad_kernel(ScanArgs a, con
     const uint32_t cb1 = cb0 + o.per_range < a.group_blocks ? cb0 + o.per_range : a.group_blocks;
     const uint32_t N = a.states;
     const int64_t DN = (int64_t)a.channels * N;
-    const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
-    const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, wave = threadIdx.x >> 6;
-    const uint32_t cw = wave * 4u + (lane >> 4);
     if (!q.any || q.lo == q.hi) {  // no rows: sums of nothing, an empty sequence's dinitial
         const uint32_t c_lo = group * a.group_channels + cb0 * kScanChannels;
         uint32_t c_hi = group * a.group_channels + cb1 * kScanChannels;
         if (c_hi > (group + 1u) * a.group_channels) c_hi = (group + 1u) * a.group_channels;
-        for (int64_t i = (int64_t)c_lo * N + threadIdx.x; i < (int64_t)c_hi * N; i += kScanThreads) {
+        for (int64_t i = (int64_t)c_lo * N + threadIdx.x; i < (int64_t)c_hi * N; i += 2 * kScanThreads) {
             o.part_A[p * DN + i] = 0.0f;
             if (q.any && o.dinitial) o.dinitial[q.seq * DN + i] = 0.0f;
         }
-        for (uint32_t c = c_lo + threadIdx.x; c < c_hi; c += kScanThreads) {
+        for (uint32_t c = c_lo + threadIdx.x; c < c_hi; c += 2 * kScanThreads) {
             o.part_D[(int64_t)p * a.channels + c] = 0.0f;
             o.part_bias[(int64_t)p * a.channels + c] = 0.0f;
         }
         return;
     }
-    const uint32_t blk = q.cell << kScanCellShift, t = blk + row;
-    const bool live = t >= q.lo && t < q.hi;
-    const bool on = (uint64_t)q.seq_hi > (uint64_t)blk + kScanCell;
-    const uint32_t state_blocks = (N + 15u) / 16u;
-    for (uint32_t sb = 0; sb < state_blocks; ++sb) {
-        const bool last = sb + 1u == state_blocks;
-        {
-            const uint32_t n = sb * 16u + c2;
-            float v[2];
-            load_pair<T>(v, static_cast<const T *>(a.B) + (int64_t)t * a.b_stride + group * N + n, live && n < N,
-                         live && n + 1 < N);
-            sB[c2 * kScanPad + row] = v[0];
-            sB[(c2 + 1) * kScanPad + row] = v[1];
-            load_pair<T>(v, static_cast<const T *>(a.C) + (int64_t)t * a.c_stride + group * N + n, live && n < N,
-                         live && n + 1 < N);
-            sC[c2 * kScanPad + row] = v[0];
-            sC[(c2 + 1) * kScanPad + row] = v[1];
+    const uint32_t blk = q.cell << kScanCellShift;
+    const uint32_t state_blocks = MANY ? (N + 15u) / 16u : 1u;
+    const bool feeds = __builtin_amdgcn_readfirstlane(threadIdx.x) < (uint32_t)kScanThreads;
+    const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, wave = (threadIdx.x >> 6) & 3u;
+    auto have_of = [&](uint32_t cb) {
+        const uint32_t left = a.group_channels - cb * kScanChannels;
+        return FULL || left >= (uint32_t)kScanChannels ? (uint32_t)kScanChannels : left;
+    };
+    // the sums over states of block cb
+    auto cell_of = [&](uint32_t cb) {
+        return sCell + (MANY ? cb - cb0 : (cb - cb0) & 1u) * 3u * kPlane;
+    };
+    // dB, dC over the range's channels: the last sums over the waves
+    auto write_parts = [&](uint32_t sb) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t j = threadIdx.x >> 6, ln = threadIdx.x & 63u;
+            const float v = ((sFold[r][0][j][ln] + sFold[r][1][j][ln]) + sFold[r][2][j][ln]) + sFold[r][3][j][ln];
+            const uint32_t tk = blk + (ln >> 4) * 8u + j, nn = sb * 16u + (ln & 15u);
+            if (tk >= q.lo && tk < q.hi && nn < N)
+                (r ? o.part_C : o.part_B)[(((int64_t)range * a.tokens + tk) * a.groups + group) * N + nn] = v;
         }
+    };
+    if (feeds) {
+        const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3, t = blk + row;
+        const bool live = t >= q.lo && t < q.hi;
+        // rows past the last repeat it; staging drops them
+        const uint32_t rt = row < a.tokens - 1u - blk ? row : a.tokens - 1u - blk;
+        struct Raw {
+            RawPair<T, FULL> x, dt, dy, z;
+            float bias[2], skip[2];
+        } raw;
+        // what the outputs of a block need of its inputs, one block long
+        struct Kept {
+            RawPair<T, FULL> x, dy, z;
+            float raw[2], st[2], skip[2];
+        } kept, next;
+        PairRows<T, FULL> rx{static_cast<const T *>(a.x), a.x_stride}, rdt{static_cast<const T *>(a.dt), a.dt_stride};
+        PairRows<T, FULL> rdy{dout, a.channels}, rz{static_cast<const T *>(a.z ? a.z : a.x), a.z ? a.z_stride : a.x_stride};
+        auto place = [&](uint32_t e0, uint32_t e1) {
+            rx.place(rt, e0, e1);
+            rdt.place(rt, e0, e1);
+            rdy.place(rt, e0, e1);
+            rz.place(rt, e0, e1);
+        };
+        place(c2, c2 + 1u);
+        auto fetch = [&](uint32_t cb) {
+            if (cb >= cb1) cb = cb1 - 1u;
+            const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
+            const uint32_t e0 = FULL ? c2 : inside(c2, have), e1 = FULL ? c2 + 1u : inside(c2 + 1u, have);
+            if (!FULL) place(e0, e1);
+            auto pair = [&](RawPair<T, FULL> &to, PairRows<T, FULL> rows) {
+                rows.base += ch0;
+                rows.load(to, blk);
+            };
+            pair(raw.x, rx);
+            pair(raw.dt, rdt);
+            pair(raw.dy, rdy);
+            pair(raw.z, rz);
+            raw.bias[0] = a.bias ? a.bias[ch0 + e0] : 0.0f, raw.bias[1] = a.bias ? a.bias[ch0 + e1] : 0.0f;
+            raw.skip[0] = a.D ? a.D[ch0 + e0] : 0.0f, raw.skip[1] = a.D ? a.D[ch0 + e1] : 0.0f;
+        };
+        auto stage = [&](uint32_t cb) {
+            const uint32_t half = (cb - cb0) & 1u, have = cb < cb1 ? have_of(cb) : 0u;
+            const bool in0 = live && c2 < have, in1 = live && c2 + 1u < have;
+            float x[2], v[2], z[2];
+            raw.x.values(x, in0, in1);
+            raw.dy.values(v, in0, in1);
+            raw.z.values(z, true, true);
+            if (a.z) v[0] *= silu(z[0]), v[1] *= silu(z[1]);
+            sGrad[half][c2 * kScanPad + row] = in0 ? v[0] : 0.0f;
+            sGrad[half][(c2 + 1) * kScanPad + row] = in1 ? v[1] : 0.0f;
+            raw.dt.values(v, true, true);
+            next.x = raw.x, next.dy = raw.dy, next.z = raw.z;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                next.raw[i] = v[i] + raw.bias[i];
+                next.skip[i] = raw.skip[i];
+                next.st[i] = softplus((i ? in1 : in0) ? next.raw[i] : kNoStep);
+                sStep[half][(c2 + i) * kScanPad + row] = next.st[i];
+                sDrive[half][(c2 + i) * kScanPad + row] = next.st[i] * x[i];
+            }
+            fetch(cb + 1u);
+        };
+        auto outputs = [&](uint32_t cb) {
+            const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
+            float x[2], dy[2], z[2], sx[2], sd[2];
+            const bool in0 = c2 < have, in1 = c2 + 1u < have;
+            kept.x.values(x, true, true);
+            kept.dy.values(dy, true, true);
+            kept.z.values(z, true, true);
+            const float *c = cell_of(cb) + c2 * kScanPad + row;
+            T vx[2], vd[2], vz[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float inner = c[i * kScanPad], along = c[kPlane + i * kScanPad], flow = c[2 * kPlane + i * kScanPad];
+                const float sz = a.z ? sigmoid(z[i]) : 1.0f;
+                const float g = a.z ? dy[i] * (z[i] * sz) : dy[i];
+                const float ddt = __builtin_fmaf(x[i], along, flow) * sigmoid(kept.raw[i]);
+                vx[i] = (T)__builtin_fmaf(kept.skip[i], g, kept.st[i] * along);
+                vd[i] = (T)ddt;
+                vz[i] = (T)(dy[i] * __builtin_fmaf(kept.skip[i], x[i], inner) * dsilu(z[i], sz));
+                sx[i] = live ? g * x[i] : 0.0f;
+                sd[i] = live ? ddt : 0.0f;
+            }
+            if (live) {
+                const int64_t to = (int64_t)t * a.channels + ch0 + c2;
+                T *dx = static_cast<T *>(o.dx) + to, *dd = static_cast<T *>(o.ddt) + to;
+                T *dz = o.dz ? static_cast<T *>(o.dz) + to : nullptr;
+                if (FULL) {
+                    *reinterpret_cast<Pack<T, 2> *>(dx) = Pack<T, 2>{{vx[0], vx[1]}};
+                    *reinterpret_cast<Pack<T, 2> *>(dd) = Pack<T, 2>{{vd[0], vd[1]}};
+                    if (dz) *reinterpret_cast<Pack<T, 2> *>(dz) = Pack<T, 2>{{vz[0], vz[1]}};
+                } else {
+                    if (in0) dx[0] = vx[0], dd[0] = vd[0];
+                    if (in1) dx[1] = vx[1], dd[1] = vd[1];
+                    if (in0 && dz) dz[0] = vz[0];
+                    if (in1 && dz) dz[1] = vz[1];
+                }
+            }
+            // over the wave's 8 tokens: rows of lanes end up with one sum each
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sx[i] += dpp<kRowRotate8>(sx[i]);
+                sd[i] += dpp<kRowRotate8>(sd[i]);
+            }
+            swap_rows(sx[0], sx[1]);
+            swap_rows(sd[0], sd[1]);
+            float ux = sx[0] + sx[1], ud = sd[0] + sd[1];
+            swap_halves(ux, ud);
+            if (l < 8u) sSum[(cb - cb0) & 1u][wave][lane >> 4][l] = ux + ud;
+        };
+        // and, a barrier later, over the 4 waves
+        auto totals = [&](uint32_t cb) {
+            if (threadIdx.x >= 32u) return;
+            const uint32_t which = threadIdx.x >> 3, pair = threadIdx.x & 7u, c = pair * 2u + (which & 1u);
+            const float(*v)[4][8] = sSum[(cb - cb0) & 1u];
+            if (c < have_of(cb))
+                (which >= 2u ? o.part_bias : o.part_D)[(int64_t)p * a.channels + group * a.group_channels + cb * kScanChannels + c] =
+                    ((v[0][which][pair] + v[1][which][pair]) + v[2][which][pair]) + v[3][which][pair];
+        };
+        for (uint32_t sb = 0; sb < state_blocks; ++sb) {
+            const bool last = sb + 1u == state_blocks;
+            fetch(cb0);
+            {
+                const uint32_t m = sb * 16u + c2, n0 = FULL ? m : inside(m, N), n1 = FULL ? m + 1u : inside(m + 1u, N);
+                PairRows<T, FULL> rB{static_cast<const T *>(a.B) + (int64_t)group * N, a.b_stride};
+                PairRows<T, FULL> rC{static_cast<const T *>(a.C) + (int64_t)group * N, a.c_stride};
+                RawPair<T, FULL> vB, vC;
+                rB.place(rt, n0, n1);
+                rC.place(rt, n0, n1);
+                rB.load(vB, blk);
+                rC.load(vC, blk);
+                float v[2];
+                vB.values(v, live && (FULL || m < N), live && (FULL || m + 1u < N));
+                sB[c2 * kScanPad + row] = v[0];
+                sB[(c2 + 1) * kScanPad + row] = v[1];
+                vC.values(v, live && (FULL || m < N), live && (FULL || m + 1u < N));
+                sC[c2 * kScanPad + row] = v[0];
+                sC[(c2 + 1) * kScanPad + row] = v[1];
+            }
+            stage(cb0);
+            __syncthreads();
+            for (uint32_t cb = cb0; cb < cb1; ++cb) {
+                if (last && cb > cb0 + 1u) totals(cb - 2u);
+                if (last && cb > cb0) outputs(cb - 1u);
+                kept = next;
+                stage(cb + 1u);  // past the range: dropped
+                __syncthreads();
+            }
+            if (last && cb1 > cb0 + 1u) totals(cb1 - 2u);
+            if (last) outputs(cb1 - 1u);
+            __syncthreads();
+            if (last) totals(cb1 - 1u);
+            write_parts(sb);
+            __syncthreads();
+        }
+        return;
+    }
+    const uint32_t cw = wave * 4u + (lane >> 4);
+    const bool on = (uint64_t)q.seq_hi > (uint64_t)blk + kScanCell, starts = q.lo == q.seq_lo;
+    __builtin_amdgcn_s_setprio(2);  // the feeding waves fill the gaps
+    for (uint32_t sb = 0; sb < state_blocks; ++sb) {
         const uint32_t n = sb * 16u + l;
+        float nextA, next_h0, next_back;
+        auto fetch = [&](uint32_t cb) {
+            if (cb >= cb1) cb = cb1 - 1u;
+            // lanes without a channel or state read one that exists and drop it
+            const uint32_t dc = group * a.group_channels + cb * kScanChannels + (FULL ? cw : inside(cw, have_of(cb)));
+            const int64_t at = (int64_t)dc * N + (FULL || n < N ? n : N - 1u);
+            nextA = a.A[at];
+            next_h0 = next_back = 0.0f;
+            if (!starts) next_h0 = marks[(int64_t)q.cell * DN + at];
+            else if (a.initial) next_h0 = a.initial[(int64_t)q.seq * DN + at];
+            if (on) next_back = carry[(int64_t)(q.cell + 1u) * DN + at];
+        };
+        fetch(cb0);
         float accB[32], accC[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) accB[j] = accC[j] = 0.0f;
+        const float *pB = sB + l * kScanPad, *pC = sC + l * kScanPad;
+        const float keep = sb ? 1.0f : 0.0f;
+        auto add_to = [&](float *to, float v) {  // without a branch: the walk is one block of code
+            if (MANY) v += keep != 0.0f ? *to : 0.0f;
+            *to = v;
+        };
+        __syncthreads();
         for (uint32_t cb = cb0; cb < cb1; ++cb) {
-            float *cell = sCell + (state_blocks > 1u ? (cb - cb0) * 3u * kPlane : 0u);
-            const uint32_t ch0 = group * a.group_channels + cb * kScanChannels;
-            const uint32_t left = a.group_channels - cb * kScanChannels;
-            const uint32_t have = left < (uint32_t)kScanChannels ? left : kScanChannels;
-            const bool in0 = c2 < have, in1 = c2 + 1u < have;
-            const uint32_t cs = ch0 + c2;
-            float x[2], raw[2], dy[2], z[2] = {0.0f, 0.0f}, g[2], st[2];
-            load_pair<T>(x, static_cast<const T *>(a.x) + (int64_t)t * a.x_stride + cs, live && in0, live && in1);
-            load_pair<T>(raw, static_cast<const T *>(a.dt) + (int64_t)t * a.dt_stride + cs, live && in0, live && in1);
-            load_pair<T>(dy, dout + (int64_t)t * a.channels + cs, live && in0, live && in1);
-            if (a.z)
-                load_pair<T>(z, static_cast<const T *>(a.z) + (int64_t)t * a.z_stride + cs, live && in0, live && in1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool in = i ? in1 : in0;
-                raw[i] += a.bias && in ? a.bias[cs + i] : 0.0f;
-                st[i] = live ? softplus(raw[i]) : 0.0f;
-                g[i] = a.z ? dy[i] * silu(z[i]) : dy[i];
-                sStep[(c2 + i) * kScanPad + row] = st[i];
-                sDrive[(c2 + i) * kScanPad + row] = st[i] * x[i];
-                sGrad[(c2 + i) * kScanPad + row] = g[i];
-            }
-            const uint32_t d = ch0 + cw;
-            const bool in = cw < have && n < N;
-            const int64_t at = (int64_t)d * N + n;
-            const float A = in ? a.A[at] : 0.0f, A2 = A * kLog2e;
-            float h0 = 0.0f, back = 0.0f;
-            if (in) {
-                if (q.lo > q.seq_lo) h0 = marks[(int64_t)q.cell * DN + at];
-                else if (a.initial) h0 = a.initial[(int64_t)q.seq * DN + at];
-                if (on) back = carry[(int64_t)(q.cell + 1u) * DN + at];
-            }
-            __syncthreads();
-            float e[32], h[32], y[16];
-            float stv[2], drv[2], grv[2];
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                stv[sub] = sStep[cw * kScanPad + sub * 16 + l];
-                drv[sub] = sDrive[cw * kScanPad + sub * 16 + l];
-                grv[sub] = sGrad[cw * kScanPad + sub * 16 + l];
-            }
+            const uint32_t half = (cb - cb0) & 1u;
+            const bool in = FULL || (cw < have_of(cb) && n < N);
+            const float A = in ? nextA : 0.0f, A2 = A * kLog2e, h0 = in ? next_h0 : 0.0f;
+            float back = in ? next_back : 0.0f;
+            fetch(cb + 1u);
+            float *cell = cell_of(cb) + cw * kScanPad + l;
+            const float *pS = sStep[half] + cw * kScanPad, *pD = sDrive[half] + cw * kScanPad, *pG = sGrad[half] + cw * kScanPad;
+            float e[32], h[32];
             float run = h0;
+            f4 vB = four(pB), vC = four(pC);
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
+                const float st = pS[sub * 16 + l], dr = pD[sub * 16 + l];
+                float y[16];
                 auto token = [&](auto jc) {
                     constexpr int j = decltype(jc)::value;
                     const int k = sub * 16 + j;
-                    e[k] = exp2_hw(row_lane<j>(stv[sub]) * A2);
-                    run = __builtin_fmaf(e[k], run, row_lane<j>(drv[sub]) * sB[l * kScanPad + k]);
+                    e[k] = exp2_hw(row_lane<j>(st) * A2);
+                    run = __builtin_fmaf(e[k], run, row_lane<j>(dr) * vB[j & 3]);
                     h[k] = run;
-                    y[j] = run * sC[l * kScanPad + k];
+                    y[j] = run * vC[j & 3];
+                    if constexpr ((j & 3) == 3) {  // the next four's
+                        if (k < 31) vB = four(pB + k + 1), vC = four(pC + k + 1);
+                    }
                 };
                 for_each_index(token, std::make_integer_sequence<int, 16>());
                 const float v = row_sums(y, lane);
-                float *to = cell + cw * kScanPad + sub * 16 + l;
-                *to = sb ? *to + v : v;
+                float *to = cell + sub * 16;
+                add_to(to, v);
             }
+            read_later();
             float sumA = 0.0f;
+            f4 uB = four(pB + 28), uC = four(pC + 28), uS = four(pS + 28), uD = four(pD + 28), uG = four(pG + 28);
 #pragma unroll
             for (int sub = 1; sub >= 0; --sub) {
                 float along[16], flowA[16];
-                auto token = [&](auto jc) {
-                    constexpr int j = 15 - decltype(jc)::value;
-                    const int k = sub * 16 + j;
-                    const float gj = row_lane<j>(grv[sub]);
-                    const float dh = __builtin_fmaf(gj, sC[l * kScanPad + k], back);
-                    accC[k] = __builtin_fmaf(gj, h[k], accC[k]);
-                    accB[k] = __builtin_fmaf(row_lane<j>(drv[sub]), dh, accB[k]);
-                    back = e[k] * dh;
-                    const float flow = back * (k ? h[k ? k - 1 : 0] : h0);
-                    sumA = __builtin_fmaf(flow, row_lane<j>(stv[sub]), sumA);
-                    along[j] = dh * sB[l * kScanPad + k];
-                    flowA[j] = flow * A;
+                auto quad = [&](auto jc) {
+                    constexpr int j0 = 12 - 4 * decltype(jc)::value;
+                    const int k0 = sub * 16 + j0;
+                    const f4 B4 = uB, C4 = uC, S4 = uS, D4 = uD, G4 = uG;
+                    if (k0) {
+                        uB = four(pB + k0 - 4), uC = four(pC + k0 - 4), uS = four(pS + k0 - 4);
+                        uD = four(pD + k0 - 4), uG = four(pG + k0 - 4);
+                    }
+                    read_later();
+#pragma unroll
+                    for (int i = 3; i >= 0; --i) {
+                        const int k = k0 + i;
+                        const float dh = __builtin_fmaf(G4[i], C4[i], back);
+                        accC[k] = __builtin_fmaf(G4[i], h[k], accC[k]);
+                        accB[k] = __builtin_fmaf(D4[i], dh, accB[k]);
+                        back = e[k] * dh;
+                        const float flow = back * (k ? h[k ? k - 1 : 0] : h0);
+                        sumA = __builtin_fmaf(S4[i], flow, sumA);
+                        along[j0 + i] = dh * B4[i];
+                        flowA[j0 + i] = flow * A;
+                    }
                 };
-                for_each_index(token, std::make_integer_sequence<int, 16>());
+                for_each_index(quad, std::make_integer_sequence<int, 4>());
                 const float va = row_sums(along, lane), vf = row_sums(flowA, lane);
-                float *to = cell + kPlane + cw * kScanPad + sub * 16 + l;
-                to[0] = sb ? to[0] + va : va;
-                to[kPlane] = sb ? to[kPlane] + vf : vf;
+                float *to = cell + kPlane + sub * 16;
+                add_to(to, va);
+                add_to(to + kPlane, vf);
             }
             if (in) {
+                const int64_t at = (int64_t)(group * a.group_channels + cb * kScanChannels + cw) * N + n;
                 o.part_A[p * DN + at] = sumA;
-                if (o.dinitial && q.lo == q.seq_lo) o.dinitial[(int64_t)q.seq * DN + at] = back;
+                if (o.dinitial && starts) o.dinitial[(int64_t)q.seq * DN + at] = back;
             }
             __syncthreads();
-            if (last) {
-                float sx[2], sd[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool have_c = i ? in1 : in0;
-                    const float skip = a.D && have_c ? a.D[cs + i] : 0.0f;
-                    const float *c = cell + (c2 + i) * kScanPad + row;
-                    const float ddt = __builtin_fmaf(x[i], c[kPlane], c[2 * kPlane]) * sigmoid(raw[i]);
-                    sx[i] = live ? g[i] * x[i] : 0.0f;
-                    sd[i] = live ? ddt : 0.0f;
-                    if (live && have_c) {
-                        const int64_t to = (int64_t)t * a.channels + cs + i;
-                        static_cast<T *>(o.dx)[to] = (T)__builtin_fmaf(skip, g[i], st[i] * c[kPlane]);
-                        static_cast<T *>(o.ddt)[to] = (T)ddt;
-                        if (o.dz)
-                            static_cast<T *>(o.dz)[to] =
-                                (T)(dy[i] * __builtin_fmaf(skip, x[i], c[0]) * dsilu(z[i], sigmoid(z[i])));
-                    }
-                }
-                // over the wave's 8 tokens, then the 4 waves
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                    for (int m = 8; m < 64; m *= 2) {
-                        sx[i] += __shfl_xor(sx[i], m);
-                        sd[i] += __shfl_xor(sd[i], m);
-                    }
-                    if (lane < 8u) {
-                        sSum[wave][0][c2 + i] = sx[i];
-                        sSum[wave][1][c2 + i] = sd[i];
-                    }
-                }
-                __syncthreads();
-                if (threadIdx.x < 32u) {
-                    const uint32_t which = threadIdx.x >> 4, c = threadIdx.x & 15u;
-                    if (c < have) {
-                        const float v = ((sSum[0][which][c] + sSum[1][which][c]) + sSum[2][which][c]) + sSum[3][which][c];
-                        (which ? o.part_bias : o.part_D)[(int64_t)p * a.channels + ch0 + c] = v;
-                    }
-                }
-            }
         }
         // dB, dC over the range's channels: rows of a wave, then the waves
+        float f[8];
+        fold_rows(f, accB);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            float f[8];
-            if (which) fold_rows(f, accC);
-            else fold_rows(f, accB);
+        for (int j = 0; j < 8; ++j) sFold[0][wave][j][lane] = f[j];
+        fold_rows(f, accC);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sFold[wave][j][lane] = f[j];
-            __syncthreads();
-            float *part = which ? o.part_C : o.part_B;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t i = r * 256u + threadIdx.x, j = i >> 6, ln = i & 63u;
-                const float v = ((sFold[0][j][ln] + sFold[1][j][ln]) + sFold[2][j][ln]) + sFold[3][j][ln];
-                const uint32_t tk = blk + (ln >> 4) * 8u + j, nn = sb * 16u + (ln & 15u);
-                if (tk >= q.lo && tk < q.hi && nn < N)
-                    part[(((int64_t)range * a.tokens + tk) * a.groups + group) * N + nn] = v;
-            }
-            __syncthreads();
-        }
+        for (int j = 0; j < 8; ++j) sFold[1][wave][j][lane] = f[j];
+        __syncthreads();
+        write_parts(sb);
+        __syncthreads();
     }
 }
 
@@ -407,6 +538,17 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a
 
 bool back_split(const ps_scan_input *) { return false; }
 
+// Channel blocks that one workgroup goes through: as many as leave about 4
+// rounds of the 256 workgroups that the GPU holds, 16 at most (the sums of dB
+// and dC then leave a workgroup once in 256 channels), 4 where the sums over
+// states wait in shared memory.
+uint32_t grad_range(const ScanArgs &a, uint64_t pieces) {
+    const uint64_t fit = pieces * a.groups * a.group_blocks / 1024u;
+    const uint64_t most = a.states > 16u ? 4u : 16u;
+    const uint64_t per = fit < 1u ? 1u : fit > most ? most : fit;
+    return (uint32_t)(per < a.group_blocks ? per : a.group_blocks);
+}
+
 }  // namespace
 }  // namespace dwps
 
@@ -422,7 +564,7 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
     const ScanArgs a = scan_args(in, kScanCellShift);
     const uint64_t cells = ceil_div(in->tokens, kScanCell);
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
-    const uint32_t per_range = a.group_blocks < 4u ? a.group_blocks : 4u;
+    const uint32_t per_range = grad_range(a, pieces);
     BackOut o{};
     o.per_range = per_range;
     o.ranges = (uint32_t)ceil_div(a.group_blocks, per_range);
@@ -490,10 +632,18 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
             });
         }
         if (grid) {
-            const uint32_t held = in->states > 16u ? per_range : 1u;
-            hipLaunchKernelGGL(scan_grad_kernel<T>, dim3((uint32_t)grid), dim3(kScanThreads),
-                               held * 3u * kScanChannels * kScanPad * 4u, s, a, static_cast<const T *>(dout), checkpoints,
-                               carry, o, ws_counter(ws), plan.words());
+            const uint32_t held = in->states > 16u ? per_range : 2u;
+            with_full(in, [&](auto full) {
+                auto launch = [&](auto many) {
+                    hipLaunchKernelGGL((scan_grad_kernel<T, decltype(full)::value, decltype(many)::value>),
+                                       dim3((uint32_t)grid), dim3(2 * kScanThreads),
+                                       held * 3u * kScanChannels * kScanPad * 4u, s, a, static_cast<const T *>(dout),
+                                       checkpoints, carry, o, ws_counter(ws), plan.words());
+                };
+                if (in->states > 16u) launch(std::true_type());
+                else launch(std::false_type());
+                return PS_OK;
+            });
         }
         hipLaunchKernelGGL(scan_sums_kernel<T>, dim3((uint32_t)at), dim3(256), 0, s, jobs, a);
         timing_end(s);
