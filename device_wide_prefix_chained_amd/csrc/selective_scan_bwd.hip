@@ -9,10 +9,11 @@
 //   dB     = sum_d dh step x,   dC = sum_d g h,   dA = sum_t flow step
 //   dz     = dout (C . h + D x) silu'(z),   dD = sum_t g x,   dinitial = a dh
 //            of a sequence's first row.
-// Two passes: the first walks backwards and stores a dh where it crosses from
-// one cell of 32 rows to the one before (carry); then every piece of a
-// sequence in a cell is worked on by itself, from the checkpoint that the
-// forward pass left at the cell's first row and from the carry at its last.
+// Every piece of a sequence in a cell of 32 rows is worked on by itself.  A
+// first pass walks back over each to find what it adds to a dh where it
+// crosses to the cell before, these are linked from cell to cell (carry), and
+// the main pass starts from the checkpoint that the forward pass left at the
+// cell's first row and from the carry at its last.
 // Sums over channels and over pieces go to partial sums that a last launch
 // adds up in a fixed order.
 #include <hip/hip_runtime.h>
@@ -22,106 +23,151 @@
 namespace dwps {
 namespace {
 
-// Two neighbouring elements, or zeros where they are not `in`.
-template <class T>
-__device__ __forceinline__ void load_pair(float (&v)[2], const T *p, bool in0, bool in1) {
-    v[0] = in0 ? (float)p[0] : 0.0f;
-    v[1] = in1 ? (float)p[1] : 0.0f;
-}
+// Nothing read from shared memory moves across this, so that values are read
+// where they are used and do not push others out of the registers.
+__device__ __forceinline__ void read_later() { asm volatile("" ::: "memory"); }
 
-// Walks backwards over a piece (a whole sequence, or its rows in one cell).
-// WHOLE: stores the carry at every cell it crosses.  Otherwise stores what
-// the piece adds to the carry out of its cell, and the sum of its steps.
-template <class T, int S, bool WHOLE>
-__global__ __launch_bounds__(kScanThreads) void scan_back_kernel(ScanArgs a, const T *__restrict__ dout,
-                                                                 float *__restrict__ carry, float *__restrict__ steps,
-                                                                 uint32_t *__restrict__ links) {
-    __shared__ __attribute__((aligned(16))) float sStep[kScanChannels * kScanPad], sGrad[kScanChannels * kScanPad],
-        sC[16 * S * kScanPad];
-    const ScanPlace w = scan_place(a, xcd_neighbours(blockIdx.x, gridDim.x, sizeof(T) == 2 ? 4u : 2u));
-    const Piece &q = w.q;
-    if (!q.any) return;
-    const uint32_t N = a.states;
+typedef float f4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f4 four(const float *p) { return *reinterpret_cast<const f4 *>(p); }
+
+// What each piece that starts its cell inside a sequence adds to the carry
+// out of the cell (carry[cell], from no carry in), the sum of its steps, and
+// how its cell's carry follows from the next cell's (links).  One piece and a
+// range of channel blocks; four waves feed the four that walk.  A walk needs
+// exp2 and 3 operations for every state, about as much as the steps and gated
+// gradients that feed it, so the feeding waves are the other half of the work.
+template <class T, int S, bool FULL>
+__global__ __launch_bounds__(2 * kScanThreads) void scan_back_kernel(ScanArgs a, const T *__restrict__ dout,
+                                                                     float *__restrict__ carry, float *__restrict__ steps,
+                                                                     uint32_t *__restrict__ links, uint32_t ranges,
+                                                                     uint32_t per_range) {
+    constexpr int kPlane = kScanChannels * kScanPad;
+    __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sGrad[2][kPlane], sC[16 * S * kScanPad];
+    const uint32_t p = blockIdx.x / (a.groups * ranges), rg = blockIdx.x % (a.groups * ranges);
+    const uint32_t group = rg / ranges, range = rg % ranges;
+    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
+    if (!q.any || q.lo != (uint64_t)q.cell << a.shift) return;  // starts inside its cell: nothing enters another
+    const bool on = q.lo > q.seq_lo;
+    if (rg == 0u && threadIdx.x == 0)
+        links[q.cell] = !on ? kLinkNone
+                        : (uint64_t)q.seq_hi > ((uint64_t)(q.cell + 1u) << a.shift) ? kLinkChain : kLinkStart;
+    if (!on) return;
+    const uint32_t cb0 = range * per_range;
+    const uint32_t cb1 = cb0 + per_range < a.group_blocks ? cb0 + per_range : a.group_blocks;
+    const uint32_t N = a.states, blk = q.lo;
     const int64_t DN = (int64_t)a.channels * N;
-    if (!WHOLE) {
-        if (q.lo != (uint64_t)q.cell << a.shift) return;  // starts inside its cell: nothing enters another
-        const bool on = q.lo > q.seq_lo;
-        if (w.ch0 == 0u && threadIdx.x == 0)
-            links[q.cell] = !on ? kLinkNone
-                            : (uint64_t)q.seq_hi > ((uint64_t)(q.cell + 1u) << a.shift) ? kLinkChain : kLinkStart;
-        if (!on) return;
-    }
-    const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
-    const bool in0 = c2 < w.have, in1 = c2 + 1u < w.have;
-    const uint32_t cs = w.ch0 + c2;
-    const float bias0 = a.bias && in0 ? a.bias[cs] : 0.0f, bias1 = a.bias && in1 ? a.bias[cs + 1] : 0.0f;
-    const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
-    const uint32_t cw = (threadIdx.x >> 6) * 4u + (lane >> 4);
-    const uint32_t d = w.ch0 + cw;
-    float A2[S], back[S], total = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const uint32_t n = s * 16 + l;
-        A2[s] = cw < w.have && n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.0f;
-        back[s] = 0.0f;
-    }
-    const uint32_t first = q.lo & ~(uint32_t)(kScanTile - 1);
-    // a sequence's first cell sends nothing on
-    const uint32_t stop = WHOLE ? (q.lo | (kScanCell - 1u)) + 1u : first;
-    for (uint32_t end = (q.hi + kScanTile - 1u) & ~(uint32_t)(kScanTile - 1); end > stop; end -= kScanTile) {
-        const uint32_t blk = end - kScanTile, t = blk + row;
-        const bool live = t >= q.lo && t < q.hi;
-        float dt[2], g[2], z[2];
-        load_pair<T>(dt, static_cast<const T *>(a.dt) + (int64_t)t * a.dt_stride + cs, live && in0, live && in1);
-        load_pair<T>(g, dout + (int64_t)t * a.channels + cs, live && in0, live && in1);
-        if (a.z) {
-            load_pair<T>(z, static_cast<const T *>(a.z) + (int64_t)t * a.z_stride + cs, live && in0, live && in1);
-            g[0] *= silu(z[0]);
-            g[1] *= silu(z[1]);
-        }
-        sStep[c2 * kScanPad + row] = live ? softplus(dt[0] + bias0) : 0.0f;
-        sStep[(c2 + 1) * kScanPad + row] = live ? softplus(dt[1] + bias1) : 0.0f;
-        sGrad[c2 * kScanPad + row] = g[0];
-        sGrad[(c2 + 1) * kScanPad + row] = g[1];
+    auto have_of = [&](uint32_t cb) {
+        const uint32_t left = a.group_channels - cb * kScanChannels;
+        return FULL || left >= (uint32_t)kScanChannels ? (uint32_t)kScanChannels : left;
+    };
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) < (uint32_t)kScanThreads) {
+        const uint32_t c2 = (threadIdx.x & 7u) * 2u, row = threadIdx.x >> 3;
+        const bool live = blk + row < q.hi;
+        // rows past the last repeat it; staging drops them
+        const uint32_t rt = row < a.tokens - 1u - blk ? row : a.tokens - 1u - blk;
+        struct Raw {
+            RawPair<T, FULL> dt, dy, z;
+            float bias[2];
+        } raw[2];
+        PairRows<T, FULL> rdt{static_cast<const T *>(a.dt), a.dt_stride}, rdy{dout, a.channels};
+        PairRows<T, FULL> rz{static_cast<const T *>(a.z ? a.z : a.dt), a.z ? a.z_stride : a.dt_stride};
+        auto fetch = [&](Raw &r, uint32_t cb) {
+            if (cb >= cb1) cb = cb1 - 1u;
+            const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
+            const uint32_t e0 = FULL ? c2 : inside(c2, have), e1 = FULL ? c2 + 1u : inside(c2 + 1u, have);
+            auto pair = [&](RawPair<T, FULL> &to, PairRows<T, FULL> rows) {
+                rows.place(rt, e0, e1);
+                rows.base += ch0;
+                rows.load(to, blk);
+            };
+            pair(r.dt, rdt);
+            pair(r.dy, rdy);
+            pair(r.z, rz);
+            r.bias[0] = a.bias ? a.bias[ch0 + e0] : 0.0f, r.bias[1] = a.bias ? a.bias[ch0 + e1] : 0.0f;
+        };
+        auto stage = [&](Raw &r, uint32_t cb, int half) {
+            const uint32_t have = cb < cb1 ? have_of(cb) : 0u;
+            const bool in0 = live && c2 < have, in1 = live && c2 + 1u < have;
+            float v[2], z[2];
+            r.dy.values(v, true, true);
+            r.z.values(z, true, true);
+            if (a.z) v[0] *= silu(z[0]), v[1] *= silu(z[1]);
+            sGrad[half][c2 * kScanPad + row] = in0 ? v[0] : 0.0f;
+            sGrad[half][(c2 + 1) * kScanPad + row] = in1 ? v[1] : 0.0f;
+            r.dt.values(v, true, true);
+            sStep[half][c2 * kScanPad + row] = softplus(in0 ? v[0] + r.bias[0] : kNoStep);
+            sStep[half][(c2 + 1) * kScanPad + row] = softplus(in1 ? v[1] + r.bias[1] : kNoStep);
+            fetch(r, cb + 2u);
+        };
+        fetch(raw[0], cb0);
+        fetch(raw[1], cb0 + 1u);
+        PairRows<T, FULL> rC{static_cast<const T *>(a.C) + (int64_t)group * N, a.c_stride};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const uint32_t n = s * 16 + c2;
+            const uint32_t m = s * 16 + c2, n0 = FULL ? m : inside(m, N), n1 = FULL ? m + 1u : inside(m + 1u, N);
+            RawPair<T, FULL> vC;
             float v[2];
-            load_pair<T>(v, static_cast<const T *>(a.C) + (int64_t)t * a.c_stride + w.group * N + n, live && n < N,
-                         live && n + 1 < N);
-            sC[n * kScanPad + row] = v[0];
-            sC[(n + 1) * kScanPad + row] = v[1];
+            rC.place(rt, n0, n1);
+            rC.load(vC, blk);
+            vC.values(v, live && (FULL || m < N), live && (FULL || m + 1u < N));
+            sC[m * kScanPad + row] = v[0];
+            sC[(m + 1) * kScanPad + row] = v[1];
         }
+        stage(raw[0], cb0, 0);
         __syncthreads();
-#pragma unroll
-        for (int sub = kScanTile / 16 - 1; sub >= 0; --sub) {
-            const float st = sStep[cw * kScanPad + sub * 16 + l], gr = sGrad[cw * kScanPad + sub * 16 + l];
-            if (!WHOLE) total += st;
-            auto token = [&](auto jc) {
-                constexpr int j = 15 - decltype(jc)::value;
-                const float stj = row_lane<j>(st), gj = row_lane<j>(gr);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const float e = exp2_hw(stj * A2[s]);
-                    back[s] = e * __builtin_fmaf(gj, sC[(s * 16 + l) * kScanPad + sub * 16 + j], back[s]);
-                }
-            };
-            for_each_index(token, std::make_integer_sequence<int, 16>());
+        for (uint32_t cb = cb0; cb < cb1; cb += 2u) {
+            stage(raw[1], cb + 1u, 1);  // past the range: dropped
+            __syncthreads();
+            if (cb + 1u < cb1) {
+                stage(raw[0], cb + 2u, 0);
+                __syncthreads();
+            }
         }
-        if (WHOLE && cw < w.have) {
+        return;
+    }
+    const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
+    const uint32_t cw = ((threadIdx.x - kScanThreads) >> 6) * 4u + (lane >> 4);
+    __builtin_amdgcn_s_setprio(2);
+    float next[S];
+    auto fetch = [&](uint32_t cb) {
+        if (cb >= cb1) cb = cb1 - 1u;
+        const uint32_t d = group * a.group_channels + cb * kScanChannels + (FULL ? cw : inside(cw, have_of(cb)));
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t n = s * 16 + l;
+            next[s] = a.A[(int64_t)d * N + (FULL || n < N ? n : N - 1u)];
+        }
+    };
+    fetch(cb0);
+    __syncthreads();
+    for (uint32_t cb = cb0; cb < cb1; ++cb) {
+        const uint32_t half = (cb - cb0) & 1u, d = group * a.group_channels + cb * kScanChannels + cw;
+        const float *pS = sStep[half] + cw * kScanPad, *pG = sGrad[half] + cw * kScanPad;
+        float A2[S], back[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            A2[s] = FULL || (cw < have_of(cb) && s * 16 + l < N) ? next[s] * kLog2e : 0.0f;
+            back[s] = 0.0f;
+        }
+        fetch(cb + 1u);
+        const float total = row_total(pS[l] + pS[16 + l]);
+#pragma unroll
+        for (int k0 = kScanTile - 4; k0 >= 0; k0 -= 4) {
+            const f4 S4 = four(pS + k0), G4 = four(pG + k0);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const f4 C4 = four(sC + (s * 16 + l) * kScanPad + k0);
+#pragma unroll
+                for (int i = 3; i >= 0; --i) back[s] = exp2_hw(S4[i] * A2[s]) * __builtin_fmaf(G4[i], C4[i], back[s]);
+            }
+        }
+        if (FULL || cw < have_of(cb)) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
-                if (s * 16 + l < N)
-                    carry[(int64_t)(blk >> kScanCellShift) * DN + (int64_t)d * N + s * 16 + l] = back[s];
+                if (FULL || s * 16 + l < N) carry[(int64_t)q.cell * DN + (int64_t)d * N + s * 16 + l] = back[s];
+            if (l == 0u) steps[(int64_t)q.cell * a.channels + d] = total;
         }
         __syncthreads();
-    }
-    if (!WHOLE && cw < w.have) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (s * 16 + l < N) carry[(int64_t)q.cell * DN + (int64_t)d * N + s * 16 + l] = back[s];
-        total = row_total(total);
-        if (l == 0u) steps[(int64_t)q.cell * a.channels + d] = total;
     }
 }
 
@@ -152,13 +198,6 @@ __device__ __forceinline__ void fold_rows(float (&o)[8], float (&v)[32]) {
         o[j] = v[j] + v[j + 8];
     }
 }
-
-// Nothing read from shared memory moves across this, so that values are read
-// where they are used and do not push others out of the registers.
-__device__ __forceinline__ void read_later() { asm volatile("" ::: "memory"); }
-
-typedef float f4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ f4 four(const float *p) { return *reinterpret_cast<const f4 *>(p); }
 
 // One piece of a cell, a range of channel blocks.  States 16 at a time
 // (outer loop), channels 16 at a time (inner loop): a lane sums dB and dC of
@@ -251,6 +290,9 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
             rz.place(rt, e0, e1);
         };
         place(c2, c2 + 1u);
+        if (MANY) {  // the sums over states start from zero: the walk adds to them without a branch
+            for (uint32_t i = threadIdx.x; i < (cb1 - cb0) * 3u * kPlane; i += kScanThreads) sCell[i] = 0.0f;
+        }
         auto fetch = [&](uint32_t cb) {
             if (cb >= cb1) cb = cb1 - 1u;
             const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
@@ -406,11 +448,7 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
 #pragma unroll
         for (int j = 0; j < 32; ++j) accB[j] = accC[j] = 0.0f;
         const float *pB = sB + l * kScanPad, *pC = sC + l * kScanPad;
-        const float keep = sb ? 1.0f : 0.0f;
-        auto add_to = [&](float *to, float v) {  // without a branch: the walk is one block of code
-            if (MANY) v += keep != 0.0f ? *to : 0.0f;
-            *to = v;
-        };
+        auto add_to = [&](float *to, float v) { *to = MANY ? *to + v : v; };
         __syncthreads();
         for (uint32_t cb = cb0; cb < cb1; ++cb) {
             const uint32_t half = (cb - cb0) & 1u;
@@ -536,8 +574,6 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a
     else static_cast<float *>(j.out)[col] = v;
 }
 
-bool back_split(const ps_scan_input *) { return false; }
-
 // Channel blocks that one workgroup goes through: as many as leave about 4
 // rounds of the 256 workgroups that the GPU holds, 16 at most (the sums of dB
 // and dC then leave a workgroup once in 256 channels), 4 where the sums over
@@ -560,7 +596,6 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
     const uint64_t DN = (uint64_t)in->channels * in->states, GN = (uint64_t)in->groups * in->states;
-    const bool split = back_split(in);
     const ScanArgs a = scan_args(in, kScanCellShift);
     const uint64_t cells = ceil_div(in->tokens, kScanCell);
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
@@ -575,9 +610,7 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
                  pD_at = plan.take(pieces * in->channels * 4u), pb_at = plan.take(pieces * in->channels * 4u),
                  pB_at = plan.take(o.ranges * in->tokens * GN * 4u), pC_at = plan.take(o.ranges * in->tokens * GN * 4u);
     const uint64_t grid = pieces * o.blocks;
-    const ScanArgs wa = scan_args(in, split ? kScanCellShift : 32u);
-    const uint64_t back_grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, wa.shift) * wa.col_blocks;
-    if (grid > kScanMaxGrid || back_grid > kScanMaxGrid) return PS_ERR_SIZE;
+    if (grid > kScanMaxGrid) return PS_ERR_SIZE;
     bool query = false;
     st = workspace_protocol(ws, ws_bytes, plan.at, &query);
     if (st != PS_OK || query) return st;
@@ -617,19 +650,16 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
         float *carry = ws_at<float>(ws, carry_at), *steps = ws_at<float>(ws, steps_at);
         uint32_t *links = ws_at<uint32_t>(ws, links_at);
         timing_begin(s);
-        if (back_grid && in->tokens) {
+        if (grid && cells > 1u) {
             with_states(in->states, [&](auto sc) {
-                constexpr int S = decltype(sc)::value;
-                if (split) {
-                    hipLaunchKernelGGL((scan_back_kernel<T, S, false>), dim3((uint32_t)back_grid), dim3(kScanThreads), 0,
-                                       s, wa, static_cast<const T *>(dout), carry, steps, links);
-                    launch_scan_link(wa, carry, steps, links, (uint32_t)cells, true, s);
-                } else {
-                    hipLaunchKernelGGL((scan_back_kernel<T, S, true>), dim3((uint32_t)back_grid), dim3(kScanThreads), 0,
-                                       s, wa, static_cast<const T *>(dout), carry, steps, links);
-                }
-                return PS_OK;
+                return with_full(in, [&](auto full) {
+                    hipLaunchKernelGGL((scan_back_kernel<T, decltype(sc)::value, decltype(full)::value>),
+                                       dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a, static_cast<const T *>(dout),
+                                       carry, steps, links, o.ranges, o.per_range);
+                    return PS_OK;
+                });
             });
+            launch_scan_link(a, carry, steps, links, (uint32_t)cells, true, s);
         }
         if (grid) {
             const uint32_t held = in->states > 16u ? per_range : 2u;
