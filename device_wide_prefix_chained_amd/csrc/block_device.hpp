@@ -138,6 +138,20 @@ __device__ __forceinline__ void for_each_index(F f, std::integer_sequence<int, i
     (f(std::integral_constant<int, i>()), ...);
 }
 
+// p[first * stride] + p[(first + step) * stride] + ... up to `rows`, eight
+// loads at a time on their way, in a fixed order.
+__device__ __forceinline__ float column_sum(const float *p, uint32_t first, uint32_t step, uint32_t rows, uint64_t stride) {
+    float v[8] = {};
+    uint32_t r = first;
+    for (; r + 7u * step < rows; r += 8u * step) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] += p[(r + u * step) * stride];
+    }
+    float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    for (; r < rows; r += step) s += p[r * stride];
+    return s;
+}
+
 // Workgroups go round the 8 XCDs in turn.  Neighbouring channel blocks share
 // cache lines of the token rows, so of every 8 * group workgroups each XCD
 // gets `group` neighbours.

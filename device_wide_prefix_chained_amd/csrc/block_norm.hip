@@ -222,9 +222,7 @@ __global__ __launch_bounds__(256) void norm_params_kernel(const float *__restric
     __shared__ float s[4][64];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint32_t cols = 3u * channels, col = blockIdx.x * 64u + lane;
-    float v = 0.0f;
-    if (col < cols)
-        for (uint32_t r = wave; r < rows; r += 4u) v += part[(uint64_t)r * cols + col];
+    float v = col < cols ? column_sum(part + col, wave, 4u, rows, cols) : 0.0f;
     s[wave][lane] = v;
     __syncthreads();
     if (wave == 0u && col < cols) {

@@ -220,9 +220,7 @@ __global__ __launch_bounds__(256) void conv_params_kernel(const float *__restric
     __shared__ float s[4][64];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint64_t cols = (uint64_t)(width + 1u) * channels, col = (uint64_t)blockIdx.x * 64u + lane;
-    float v = 0.0f;
-    if (col < cols)
-        for (uint32_t p = wave; p < pieces; p += 4u) v += part[p * cols + col];
+    float v = col < cols ? column_sum(part + col, wave, 4u, pieces, cols) : 0.0f;
     s[wave][lane] = v;
     __syncthreads();
     if (wave == 0u && col < cols) {

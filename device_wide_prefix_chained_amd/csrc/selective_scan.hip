@@ -242,35 +242,40 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a,
     }
 }
 
-__global__ __launch_bounds__(256) void scan_link_kernel(ScanArgs a, float *__restrict__ carry,
+// One (channel, state) per lane, from cell to cell; the loads of 32 cells are
+// on their way at once.
+__global__ __launch_bounds__(64) void scan_link_kernel(ScanArgs a, float *__restrict__ carry,
                                                         const float *__restrict__ steps,
                                                         const uint32_t *__restrict__ links, uint32_t cells,
                                                         int backward) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
     const int64_t DN = (int64_t)a.channels * a.states;
     if (i >= DN) return;
     const uint32_t d = (uint32_t)(i / a.states);
     const float A2 = a.A[i] * kLog2e;
     float h = 0.0f;
-    constexpr int U = 8;
-    for (uint32_t k0 = 1; k0 < cells; k0 += U) {
-        float v[U], s[U];
-        uint32_t f[U];
+    auto batch = [&](uint32_t k0, auto count) {
+        constexpr int U = decltype(count)::value;
+        float v[U], keep[U];
+        uint32_t link[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t k = k0 + u < cells ? k0 + u : cells - 1u, c = backward ? cells - k : k;
+            const uint32_t c = backward ? cells - (k0 + u) : k0 + u;
             v[u] = carry[c * DN + i];
-            s[u] = steps[(int64_t)c * a.channels + d];
-            f[u] = links[c];
+            keep[u] = steps[(int64_t)c * a.channels + d];
+            link[u] = links[c];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (k0 + u >= cells) break;
             const uint32_t c = backward ? cells - (k0 + u) : k0 + u;
-            h = f[u] == kLinkChain ? __builtin_fmaf(exp2_hw(A2 * s[u]), h, v[u]) : v[u];
+            // a chain starts anew where nothing enters (steps are not written there)
+            h = link[u] == kLinkChain ? __builtin_fmaf(exp2_hw(A2 * keep[u]), h, v[u]) : v[u];
             carry[c * DN + i] = h;
         }
-    }
+    };
+    uint32_t k = 1;
+    for (; k + 32u <= cells; k += 32u) batch(k, std::integral_constant<int, 32>());
+    for (; k < cells; ++k) batch(k, std::integral_constant<int, 1>());
 }
 
 // One token for each row.  A lane holds 4 states of one channel (16 bytes of
@@ -373,8 +378,8 @@ bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes) {
 
 void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
                       bool backward, hipStream_t s) {
-    const uint64_t grid = ceil_div((uint64_t)a.channels * a.states, 256);
-    hipLaunchKernelGGL(scan_link_kernel, dim3((uint32_t)grid), dim3(256), 0, s, a, carry, steps, links, cells,
+    const uint64_t grid = ceil_div((uint64_t)a.channels * a.states, 64);
+    hipLaunchKernelGGL(scan_link_kernel, dim3((uint32_t)grid), dim3(64), 0, s, a, carry, steps, links, cells,
                        backward ? 1 : 0);
 }
 

@@ -160,6 +160,7 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_back_kernel(ScanArgs a,
 #pragma unroll
                 for (int i = 3; i >= 0; --i) back[s] = exp2_hw(S4[i] * A2[s]) * __builtin_fmaf(G4[i], C4[i], back[s]);
             }
+            if (S > 1 && k0 % 8 == 0) read_later();
         }
         if (FULL || cw < have_of(cb)) {
 #pragma unroll
@@ -559,9 +560,7 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a
     const SumJob j = jobs.job[k];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint64_t col = (uint64_t)(blockIdx.x - j.first) * 64u + lane;
-    float v = 0.0f;
-    if (col < j.cols)
-        for (uint32_t r = wave; r < j.rows; r += 4u) v += j.part[r * j.cols + col];
+    float v = col < j.cols ? column_sum(j.part + col, wave, 4u, j.rows, j.cols) : 0.0f;
     s[wave][lane] = v;
     __syncthreads();
     if (wave != 0u || col >= j.cols) return;
