@@ -90,26 +90,38 @@ constexpr int kRowRotate8 = 0x128, kRowMirror = 0x140, kRowHalfMirror = 0x141, k
     "v_add_f32_dpp %1, %5, %5 " what " row_mask:0xf bank_mask:" mask "\n\t"                                   \
     "v_add_f32_dpp %2, %6, %6 " what " row_mask:0xf bank_mask:" mask "\n\t"                                   \
     "v_add_f32_dpp %3, %7, %7 " what " row_mask:0xf bank_mask:" mask
-__device__ __forceinline__ float row_sums(const float (&v)[16], uint32_t lane) {
+struct Four {
+    float v[4];
+};
+// The first level for four pairs (lower half: lo, upper half: hi).
+__device__ __forceinline__ Four row_fold8(const Four &lo, const Four &hi) {
 #pragma clang fp contract(off)  // a product fused into the first addition would cost a move for its partner
-    const bool b2 = lane & 2u, b1 = lane & 1u;
-    float a[8], b[4], c[2];
+    Four a;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = v[j] + dpp<kRowMirror>(v[j]);
+    for (int j = 0; j < 4; ++j) a.v[j] = lo.v[j] + dpp<kRowMirror>(lo.v[j]);
     // s_nop: two wait states between a VALU write and a DPP read of it
+    asm("s_nop 1\n\t" DPP_ADD4("row_mirror", "0xc")
+        : "+v"(a.v[0]), "+v"(a.v[1]), "+v"(a.v[2]), "+v"(a.v[3])
+        : "v"(hi.v[0]), "v"(hi.v[1]), "v"(hi.v[2]), "v"(hi.v[3]));
+    return a;
+}
+// The other levels: a holds values 0-3 and 8-11, b values 4-7 and 12-15.
+__device__ __forceinline__ float row_fold(const Four &a, const Four &b, uint32_t lane) {
+    const bool b2 = lane & 2u, b1 = lane & 1u;
+    float q[4], c[2];
 #pragma unroll
-    for (int j = 0; j < 8; j += 4)
-        asm("s_nop 1\n\t" DPP_ADD4("row_mirror", "0xc")
-            : "+v"(a[j]), "+v"(a[j + 1]), "+v"(a[j + 2]), "+v"(a[j + 3])
-            : "v"(v[j + 8]), "v"(v[j + 9]), "v"(v[j + 10]), "v"(v[j + 11]));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = a[j] + dpp<kRowHalfMirror>(a[j]);
+    for (int j = 0; j < 4; ++j) q[j] = a.v[j] + dpp<kRowHalfMirror>(a.v[j]);
     asm("s_nop 1\n\t" DPP_ADD4("row_half_mirror", "0xa")
-        : "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3])
-        : "v"(a[4]), "v"(a[5]), "v"(a[6]), "v"(a[7]));
+        : "+v"(q[0]), "+v"(q[1]), "+v"(q[2]), "+v"(q[3])
+        : "v"(b.v[0]), "v"(b.v[1]), "v"(b.v[2]), "v"(b.v[3]));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) c[j] = (b2 ? b[j + 2] : b[j]) + dpp<kQuadSwap2>(b2 ? b[j] : b[j + 2]);
+    for (int j = 0; j < 2; ++j) c[j] = (b2 ? q[j + 2] : q[j]) + dpp<kQuadSwap2>(b2 ? q[j] : q[j + 2]);
     return (b1 ? c[1] : c[0]) + dpp<kQuadSwap1>(b1 ? c[0] : c[1]);
+}
+__device__ __forceinline__ float row_sums(const float (&v)[16], uint32_t lane) {
+    const Four a = row_fold8({{v[0], v[1], v[2], v[3]}}, {{v[8], v[9], v[10], v[11]}});
+    const Four b = row_fold8({{v[4], v[5], v[6], v[7]}}, {{v[12], v[13], v[14], v[15]}});
+    return row_fold(a, b, lane);
 }
 #undef DPP_ADD4
 

@@ -190,7 +190,7 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a,
     }
     auto walk = [&](uint32_t k, int half) {
         const uint32_t blk = first + k * kScanTile;
-        if (OUT && marks && blk > q.lo && (blk & (kScanCell - 1u)) == 0u && cw < w.have) {
+        if (OUT && marks && blk > q.seq_lo && (blk & (kScanCell - 1u)) == 0u && cw < w.have) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (s * 16 + l < N) marks[(int64_t)(blk >> kScanCellShift) * DN + (int64_t)d * N + s * 16 + l] = h[s];
@@ -319,10 +319,27 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float 
     }
 }
 
-// Whether a forward call over whole sequences would leave most of the GPU
-// idle, so that cells side by side are faster although every decay is then
-// computed twice.
-bool scan_split(const ps_scan_input *) { return false; }
+// Rows of a piece, as a power of two: 32 for whole sequences, or less where
+// those leave too much of the GPU idle.  Then cells of sequences are walked
+// side by side, after a first walk for the states that enter them, which
+// computes every decay twice.  Counted in turns (32 tokens of 16 channels on
+// one of 256 CUs, 0.75 us): whole sequences take the longer of the longest
+// sequence (random cuts: (1 + ln seqs) / seqs of the rows) and an even share;
+// cells 1.75 shares and about 30 turns for two more launches, and the link of
+// 32 cells about 4.  Cells are as long as leaves four workgroups for a CU.
+// Both sides, bf16 and 16 states, one sequence of 16384 rows, whole / cells:
+// SPLIT_MEASURED
+uint32_t scan_shift(const ps_scan_input *in) {
+    const ScanArgs a = scan_args(in, 32u);
+    const double blocks = (double)ceil_div(in->tokens, kScanTile), share = blocks * a.col_blocks / 256.0;
+    const uint32_t seqs = a.num_seqs ? a.num_seqs : 1u;
+    const double longest = blocks * (1.0 + 0.6931 * (31 - __builtin_clz(seqs))) / seqs;
+    const double whole = longest > share ? longest : share;
+    uint32_t shift = kScanCellShift;
+    while (shift < 9u && ceil_div(in->tokens, 2ull << shift) * a.col_blocks >= 1024u) ++shift;
+    const double cells = (double)ceil_div(in->tokens, 1ull << shift);
+    return 1.75 * share + 30.0 + cells / 8.0 < whole ? shift : 32u;
+}
 
 }  // namespace
 
@@ -398,9 +415,9 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
     const uint64_t DN = (uint64_t)in->channels * in->states;
-    const bool split = scan_split(in);
-    const ScanArgs a = scan_args(in, split ? kScanCellShift : 32u);
-    const uint64_t cells = ceil_div(in->tokens, kScanCell);
+    const ScanArgs a = scan_args(in, scan_shift(in));
+    const bool split = a.shift < 32u;
+    const uint64_t cells = split ? ceil_div(in->tokens, 1ull << a.shift) : 0u;
     PlainWs plan;
     size_t carry_at = 0, steps_at = 0, links_at = 0;
     if (split) {
@@ -415,7 +432,7 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
     if (in->tokens && !out) return PS_ERR_NULL;
     if (!aligned(ws, 16) || !aligned(out, e) || !aligned(final, 4) || !aligned(checkpoints, 4)) return PS_ERR_ALIGNMENT;
     const size_t out_bytes = in->tokens * in->channels * e, state_bytes = (size_t)a.num_seqs * DN * 4u;
-    const size_t mark_bytes = cells * DN * 4u;
+    const size_t mark_bytes = ceil_div(in->tokens, kScanCell) * DN * 4u;
     if (scan_overlaps(in, out, out_bytes) || scan_overlaps(in, final, state_bytes) ||
         scan_overlaps(in, checkpoints, mark_bytes) || (final && ranges_overlap(final, state_bytes, out, out_bytes)) ||
         (final && in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)) ||

@@ -27,6 +27,10 @@ namespace {
 // where they are used and do not push others out of the registers.
 __device__ __forceinline__ void read_later() { asm volatile("" ::: "memory"); }
 
+// No instruction moves across this: the reads before it are on their way
+// while the arithmetic after it runs.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 typedef float f4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ f4 four(const float *p) { return *reinterpret_cast<const f4 *>(p); }
 
@@ -203,15 +207,15 @@ __device__ __forceinline__ void fold_rows(float (&o)[8], float (&v)[32]) {
 // One piece of a cell, a range of channel blocks.  States 16 at a time
 // (outer loop), channels 16 at a time (inner loop): a lane sums dB and dC of
 // its state over the inner loop in registers, token by token, and keeps a
-// and h of the piece's 32 rows in registers between the walk forward and the
-// walk back.  With more than 16 states the three sums over states wait in
+// and h of the piece's 32 rows between the walk forward and the walk back.  With more than 16 states the three sums over states wait in
 // shared memory for the last 16.
 //
 // As in the forward walk, four waves feed (they load, stage and, a block
 // later, form the block's outputs) and four walk.  Bound by arithmetic: for
 // every state 5 operations and exp2 forwards, 8 backwards and 99 / 16 for the
-// three sums over states.  The 128 sums and factors of a walking lane take
-// half of the 256 registers that two waves per SIMD leave it.
+// three sums over states.  The 64 sums and 32 states of a walking lane and
+// what is on its way from shared memory fill the 256 registers that two waves
+// per SIMD leave it, so a waits in shared memory.
 template <class T, bool FULL, bool MANY>
 __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs a, const T *__restrict__ dout,
                                                                         const float *__restrict__ marks,
@@ -221,6 +225,8 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
     __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sDrive[2][kPlane], sGrad[2][kPlane], sB[kPlane],
         sC[kPlane];
     __shared__ float sFold[2][4][8][64];
+    // for each walking lane A, the states and the carry that enter its piece; its dA and the carry that leaves
+    __shared__ float sEnter[2][3][kScanThreads], sLeave[2][2][kScanThreads];
     __shared__ float sSum[2][4][4][8];  // [half][wave][dD of two channels, ddt_bias of two][pair]
     extern __shared__ float sCell[];    // [channel blocks of the range, or 2][3][kPlane]
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
@@ -276,11 +282,26 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
         struct Raw {
             RawPair<T, FULL> x, dt, dy, z;
             float bias[2], skip[2];
+            float A, h, back;  // of the walking lane with this thread's place
         } raw;
+        const uint32_t cw = wave * 4u + (lane >> 4);
+        const bool on = (uint64_t)q.seq_hi > (uint64_t)blk + kScanCell, starts = q.lo == q.seq_lo;
+        // the states that enter the piece: a checkpoint, initial ones or zeros (then any address does)
+        const float *enter = !starts ? marks + (int64_t)q.cell * DN : a.initial ? a.initial + (int64_t)q.seq * DN : a.A;
+        const float *enter_back = on ? carry + (int64_t)(q.cell + 1u) * DN : a.A;
+        // this lane's place among 16 channels' states, in bytes from the block's first
+        auto lane_byte = [&](uint32_t have, uint32_t sb) {
+            const uint32_t n = sb * 16u + l;
+            return ((FULL ? cw : inside(cw, have)) * N + (FULL || n < N ? n : N - 1u)) * 4u;
+        };
+        auto of_lane = [](auto *base, int64_t first, uint32_t byte) {
+            return reinterpret_cast<decltype(base)>((uintptr_t)(base + first) + byte);
+        };
+        const bool has_enter = !starts || a.initial;
         // what the outputs of a block need of its inputs, one block long
         struct Kept {
             RawPair<T, FULL> x, dy, z;
-            float raw[2], st[2], skip[2];
+            float raw[2], st[2], skip[2], sz[2];
         } kept, next;
         PairRows<T, FULL> rx{static_cast<const T *>(a.x), a.x_stride}, rdt{static_cast<const T *>(a.dt), a.dt_stride};
         PairRows<T, FULL> rdy{dout, a.channels}, rz{static_cast<const T *>(a.z ? a.z : a.x), a.z ? a.z_stride : a.x_stride};
@@ -294,11 +315,18 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
         if (MANY) {  // the sums over states start from zero: the walk adds to them without a branch
             for (uint32_t i = threadIdx.x; i < (cb1 - cb0) * 3u * kPlane; i += kScanThreads) sCell[i] = 0.0f;
         }
-        auto fetch = [&](uint32_t cb) {
+        auto fetch = [&](uint32_t cb, uint32_t sb) {
             if (cb >= cb1) cb = cb1 - 1u;
             const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
             const uint32_t e0 = FULL ? c2 : inside(c2, have), e1 = FULL ? c2 + 1u : inside(c2 + 1u, have);
             if (!FULL) place(e0, e1);
+            {   // lanes without a channel or state read one that exists; staging drops it
+                const uint32_t byte = lane_byte(have, sb);
+                const int64_t first = (int64_t)ch0 * N;
+                raw.A = *of_lane(a.A, first, byte);
+                raw.h = *of_lane(enter, first, byte);
+                raw.back = *of_lane(enter_back, first, byte);
+            }
             auto pair = [&](RawPair<T, FULL> &to, PairRows<T, FULL> rows) {
                 rows.base += ch0;
                 rows.load(to, blk);
@@ -310,14 +338,22 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
             raw.bias[0] = a.bias ? a.bias[ch0 + e0] : 0.0f, raw.bias[1] = a.bias ? a.bias[ch0 + e1] : 0.0f;
             raw.skip[0] = a.D ? a.D[ch0 + e0] : 0.0f, raw.skip[1] = a.D ? a.D[ch0 + e1] : 0.0f;
         };
-        auto stage = [&](uint32_t cb) {
+        auto stage = [&](uint32_t cb, uint32_t sb) {
             const uint32_t half = (cb - cb0) & 1u, have = cb < cb1 ? have_of(cb) : 0u;
             const bool in0 = live && c2 < have, in1 = live && c2 + 1u < have;
+            const bool walks = FULL || (cw < have && sb * 16u + l < N);
+            sEnter[half][0][threadIdx.x] = walks ? raw.A : 0.0f;
+            sEnter[half][1][threadIdx.x] = walks && has_enter ? raw.h : 0.0f;
+            sEnter[half][2][threadIdx.x] = walks && on ? raw.back : 0.0f;
             float x[2], v[2], z[2];
             raw.x.values(x, in0, in1);
             raw.dy.values(v, in0, in1);
             raw.z.values(z, true, true);
-            if (a.z) v[0] *= silu(z[0]), v[1] *= silu(z[1]);
+            next.sz[0] = next.sz[1] = 1.0f;
+            if (a.z) {
+                next.sz[0] = sigmoid(z[0]), next.sz[1] = sigmoid(z[1]);
+                v[0] *= z[0] * next.sz[0], v[1] *= z[1] * next.sz[1];
+            }
             sGrad[half][c2 * kScanPad + row] = in0 ? v[0] : 0.0f;
             sGrad[half][(c2 + 1) * kScanPad + row] = in1 ? v[1] : 0.0f;
             raw.dt.values(v, true, true);
@@ -330,8 +366,18 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
                 sStep[half][(c2 + i) * kScanPad + row] = next.st[i];
                 sDrive[half][(c2 + i) * kScanPad + row] = next.st[i] * x[i];
             }
-            fetch(cb + 1u);
+            fetch(cb + 1u, sb);
         };
+        // a walking lane's dA and dinitial
+        auto leave = [&](uint32_t cb, uint32_t sb) {
+            const uint32_t half = (cb - cb0) & 1u, have = have_of(cb), byte = lane_byte(have, sb);
+            const int64_t first = (int64_t)(group * a.group_channels + cb * kScanChannels) * N;
+            if (FULL || (cw < have && sb * 16u + l < N)) {
+                *of_lane(o.part_A, p * DN + first, byte) = sLeave[half][0][threadIdx.x];
+                if (o.dinitial && starts) *of_lane(o.dinitial, (int64_t)q.seq * DN + first, byte) = sLeave[half][1][threadIdx.x];
+            }
+        };
+        const uint32_t out_byte = (row * a.channels + c2) * (uint32_t)sizeof(T);
         auto outputs = [&](uint32_t cb) {
             const uint32_t have = have_of(cb), ch0 = group * a.group_channels + cb * kScanChannels;
             float x[2], dy[2], z[2], sx[2], sd[2];
@@ -344,7 +390,7 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float inner = c[i * kScanPad], along = c[kPlane + i * kScanPad], flow = c[2 * kPlane + i * kScanPad];
-                const float sz = a.z ? sigmoid(z[i]) : 1.0f;
+                const float sz = kept.sz[i];
                 const float g = a.z ? dy[i] * (z[i] * sz) : dy[i];
                 const float ddt = __builtin_fmaf(x[i], along, flow) * sigmoid(kept.raw[i]);
                 vx[i] = (T)__builtin_fmaf(kept.skip[i], g, kept.st[i] * along);
@@ -354,9 +400,9 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
                 sd[i] = live ? ddt : 0.0f;
             }
             if (live) {
-                const int64_t to = (int64_t)t * a.channels + ch0 + c2;
-                T *dx = static_cast<T *>(o.dx) + to, *dd = static_cast<T *>(o.ddt) + to;
-                T *dz = o.dz ? static_cast<T *>(o.dz) + to : nullptr;
+                const int64_t first = (int64_t)blk * a.channels + ch0;
+                T *dx = of_lane(static_cast<T *>(o.dx), first, out_byte), *dd = of_lane(static_cast<T *>(o.ddt), first, out_byte);
+                T *dz = o.dz ? of_lane(static_cast<T *>(o.dz), first, out_byte) : nullptr;
                 if (FULL) {
                     *reinterpret_cast<Pack<T, 2> *>(dx) = Pack<T, 2>{{vx[0], vx[1]}};
                     *reinterpret_cast<Pack<T, 2> *>(dd) = Pack<T, 2>{{vd[0], vd[1]}};
@@ -391,7 +437,7 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
         };
         for (uint32_t sb = 0; sb < state_blocks; ++sb) {
             const bool last = sb + 1u == state_blocks;
-            fetch(cb0);
+            fetch(cb0, sb);
             {
                 const uint32_t m = sb * 16u + c2, n0 = FULL ? m : inside(m, N), n1 = FULL ? m + 1u : inside(m + 1u, N);
                 PairRows<T, FULL> rB{static_cast<const T *>(a.B) + (int64_t)group * N, a.b_stride};
@@ -409,15 +455,17 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
                 sC[c2 * kScanPad + row] = v[0];
                 sC[(c2 + 1) * kScanPad + row] = v[1];
             }
-            stage(cb0);
+            stage(cb0, sb);
             __syncthreads();
             for (uint32_t cb = cb0; cb < cb1; ++cb) {
                 if (last && cb > cb0 + 1u) totals(cb - 2u);
+                if (cb > cb0) leave(cb - 1u, sb);
                 if (last && cb > cb0) outputs(cb - 1u);
                 kept = next;
-                stage(cb + 1u);  // past the range: dropped
+                stage(cb + 1u, sb);  // past the range: dropped
                 __syncthreads();
             }
+            leave(cb1 - 1u, sb);
             if (last && cb1 > cb0 + 1u) totals(cb1 - 2u);
             if (last) outputs(cb1 - 1u);
             __syncthreads();
@@ -427,24 +475,9 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
         }
         return;
     }
-    const uint32_t cw = wave * 4u + (lane >> 4);
-    const bool on = (uint64_t)q.seq_hi > (uint64_t)blk + kScanCell, starts = q.lo == q.seq_lo;
+    const uint32_t cw = wave * 4u + (lane >> 4), place = threadIdx.x - kScanThreads;
     __builtin_amdgcn_s_setprio(2);  // the feeding waves fill the gaps
     for (uint32_t sb = 0; sb < state_blocks; ++sb) {
-        const uint32_t n = sb * 16u + l;
-        float nextA, next_h0, next_back;
-        auto fetch = [&](uint32_t cb) {
-            if (cb >= cb1) cb = cb1 - 1u;
-            // lanes without a channel or state read one that exists and drop it
-            const uint32_t dc = group * a.group_channels + cb * kScanChannels + (FULL ? cw : inside(cw, have_of(cb)));
-            const int64_t at = (int64_t)dc * N + (FULL || n < N ? n : N - 1u);
-            nextA = a.A[at];
-            next_h0 = next_back = 0.0f;
-            if (!starts) next_h0 = marks[(int64_t)q.cell * DN + at];
-            else if (a.initial) next_h0 = a.initial[(int64_t)q.seq * DN + at];
-            if (on) next_back = carry[(int64_t)(q.cell + 1u) * DN + at];
-        };
-        fetch(cb0);
         float accB[32], accC[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) accB[j] = accC[j] = 0.0f;
@@ -453,74 +486,79 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
         __syncthreads();
         for (uint32_t cb = cb0; cb < cb1; ++cb) {
             const uint32_t half = (cb - cb0) & 1u;
-            const bool in = FULL || (cw < have_of(cb) && n < N);
-            const float A = in ? nextA : 0.0f, A2 = A * kLog2e, h0 = in ? next_h0 : 0.0f;
-            float back = in ? next_back : 0.0f;
-            fetch(cb + 1u);
+            const float A = sEnter[half][0][place], A2 = A * kLog2e, h0 = sEnter[half][1][place];
+            float back = sEnter[half][2][place];
             float *cell = cell_of(cb) + cw * kScanPad + l;
             const float *pS = sStep[half] + cw * kScanPad, *pD = sDrive[half] + cw * kScanPad, *pG = sGrad[half] + cw * kScanPad;
-            float e[32], h[32];
+            float h[32];
+            f4 er[8];
             float run = h0;
-            f4 vB = four(pB), vC = four(pC);
+
+            const float stv[2] = {pS[l], pS[16 + l]}, drv[2] = {pD[l], pD[16 + l]};
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                const float st = pS[sub * 16 + l], dr = pD[sub * 16 + l];
-                float y[16];
-                auto token = [&](auto jc) {
-                    constexpr int j = decltype(jc)::value;
-                    const int k = sub * 16 + j;
-                    e[k] = exp2_hw(row_lane<j>(st) * A2);
-                    run = __builtin_fmaf(e[k], run, row_lane<j>(dr) * vB[j & 3]);
-                    h[k] = run;
-                    y[j] = run * vC[j & 3];
-                    if constexpr ((j & 3) == 3) {  // the next four's
-                        if (k < 31) vB = four(pB + k + 1), vC = four(pC + k + 1);
-                    }
+                Four y[4];
+                auto quad = [&](auto jc) {
+                    constexpr int q0 = decltype(jc)::value;
+                    const f4 B4 = four(pB + sub * 16 + q0 * 4), C4 = four(pC + sub * 16 + q0 * 4);
+                    f4 e;
+                    auto token = [&](auto ic) {
+                        constexpr int i = decltype(ic)::value;
+                        const int k = sub * 16 + q0 * 4 + i;
+                        e[i] = exp2_hw(row_lane<q0 * 4 + i>(stv[sub]) * A2);
+                        run = __builtin_fmaf(e[i], run, row_lane<q0 * 4 + i>(drv[sub]) * B4[i]);
+                        h[k] = run;
+                        y[q0].v[i] = run * C4[i];
+                    };
+                    for_each_index(token, std::make_integer_sequence<int, 4>());
+                    er[sub * 4 + q0] = e;
+                    if constexpr (q0 >= 2) y[q0 - 2] = row_fold8(y[q0 - 2], y[q0]);
                 };
-                for_each_index(token, std::make_integer_sequence<int, 16>());
-                const float v = row_sums(y, lane);
-                float *to = cell + sub * 16;
-                add_to(to, v);
+                for_each_index(quad, std::make_integer_sequence<int, 4>());
+                add_to(cell + sub * 16, row_fold(y[0], y[1], lane));
             }
             read_later();
             float sumA = 0.0f;
             f4 uB = four(pB + 28), uC = four(pC + 28), uS = four(pS + 28), uD = four(pD + 28), uG = four(pG + 28);
+            
 #pragma unroll
             for (int sub = 1; sub >= 0; --sub) {
-                float along[16], flowA[16];
+                Four along[4], flowA[4];
                 auto quad = [&](auto jc) {
-                    constexpr int j0 = 12 - 4 * decltype(jc)::value;
-                    const int k0 = sub * 16 + j0;
-                    const f4 B4 = uB, C4 = uC, S4 = uS, D4 = uD, G4 = uG;
+                    constexpr int q0 = 3 - decltype(jc)::value;
+                    const int k0 = sub * 16 + q0 * 4;
+                    const f4 B4 = uB, C4 = uC, S4 = uS, D4 = uD, G4 = uG, E4 = er[k0 / 4];
                     if (k0) {
                         uB = four(pB + k0 - 4), uC = four(pC + k0 - 4), uS = four(pS + k0 - 4);
                         uD = four(pD + k0 - 4), uG = four(pG + k0 - 4);
+                        
                     }
-                    read_later();
+                    in_order();
 #pragma unroll
                     for (int i = 3; i >= 0; --i) {
                         const int k = k0 + i;
                         const float dh = __builtin_fmaf(G4[i], C4[i], back);
                         accC[k] = __builtin_fmaf(G4[i], h[k], accC[k]);
                         accB[k] = __builtin_fmaf(D4[i], dh, accB[k]);
-                        back = e[k] * dh;
+                        back = E4[i] * dh;
                         const float flow = back * (k ? h[k ? k - 1 : 0] : h0);
                         sumA = __builtin_fmaf(S4[i], flow, sumA);
-                        along[j0 + i] = dh * B4[i];
-                        flowA[j0 + i] = flow * A;
+                        along[q0].v[i] = dh * B4[i];
+                        flowA[q0].v[i] = flow * A;
+                    }
+                    // the upper half's values wait for the lower half's
+                    if constexpr (q0 < 2) {
+                        along[q0] = row_fold8(along[q0], along[q0 + 2]);
+                        flowA[q0] = row_fold8(flowA[q0], flowA[q0 + 2]);
                     }
                 };
                 for_each_index(quad, std::make_integer_sequence<int, 4>());
-                const float va = row_sums(along, lane), vf = row_sums(flowA, lane);
                 float *to = cell + kPlane + sub * 16;
-                add_to(to, va);
-                add_to(to + kPlane, vf);
+                add_to(to, row_fold(along[0], along[1], lane));
+                add_to(to + kPlane, row_fold(flowA[0], flowA[1], lane));
             }
-            if (in) {
-                const int64_t at = (int64_t)(group * a.group_channels + cb * kScanChannels + cw) * N + n;
-                o.part_A[p * DN + at] = sumA;
-                if (o.dinitial && starts) o.dinitial[(int64_t)q.seq * DN + at] = back;
-            }
+            sLeave[half][0][place] = sumA;
+            sLeave[half][1][place] = back;
             __syncthreads();
         }
         // dB, dC over the range's channels: rows of a wave, then the waves

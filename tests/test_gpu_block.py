@@ -141,6 +141,10 @@ SCAN = [  # tokens, cuts, channels, groups, states, type, initial, optional inpu
     (50, list(range(51)), 24, 2, 8, F32, True, "Dzb", False),
     (700, [0, 650, 700], 64, 1, 16, BF16, True, "Dzb", False),
     (900, None, 80, 1, 16, F32, False, "Dzb", False),
+    # few channels and long sequences: cells of sequences side by side
+    (2500, None, 16, 1, 16, F32, True, "Dzb", False),
+    (3001, [0, 2, 1500, 1500, 1531, 3001], 20, 1, 24, BF16, True, "Dzb", True),
+    (4096, [0, 4096], 24, 2, 4, F16, False, "z", False),
 ]
 
 
