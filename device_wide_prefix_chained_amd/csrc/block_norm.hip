@@ -23,29 +23,35 @@ struct NormArgs {
     float eps, inv;  // 1 / channels
 };
 
+constexpr int kVec = 8;  // neighbouring channels of a thread
+constexpr int kMostWaves = 16;
+
 __device__ __forceinline__ float wave_total(float v) {
     v = row_total(v);
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    float w = v;
+    swap_rows(v, w);
+    v += w;
+    w = v;
+    swap_halves(v, w);
+    return v + w;
 }
 
-// The workgroup's sums of n values, in every thread.
-template <int NT, int n>
-__device__ __forceinline__ void group_totals(float (&v)[n], float *shared) {
+// The workgroup's sums of n values, in every thread: wave sums meet in
+// shared memory, and every row of lanes adds the up to 16 of them.
+template <int n>
+__device__ __forceinline__ void group_totals(float (&v)[n], float (*shared)[kMostWaves]) {
 #pragma unroll
     for (int i = 0; i < n; ++i) v[i] = wave_total(v[i]);
-    if (NT == 64) return;
-    const uint32_t wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63u) == 0u)
+    const uint32_t waves = blockDim.x >> 6;
+    if (waves == 1u) return;
+    if ((threadIdx.x & 63u) == 0u) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) shared[wave * n + i] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-        v[i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NT / 64; ++k) v[i] += shared[k * n + i];
+        for (int i = 0; i < n; ++i) shared[i][threadIdx.x >> 6] = v[i];
     }
+    __syncthreads();
+    const uint32_t l = threadIdx.x & 15u;
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = row_total(l < waves ? shared[i][l] : 0.0f);
 }
 
 // n neighbouring values from p, or `none` without p; `have` of them exist.
@@ -82,15 +88,16 @@ __device__ __forceinline__ const T *at_row(const void *p, int64_t t, int64_t str
 }
 __device__ __forceinline__ const float *at_col(const float *p, uint32_t c) { return p ? p + c : nullptr; }
 
-// One row: NT threads, K times V neighbouring channels each.
-template <class T, class R, int NT, int V, int K>
-__global__ __launch_bounds__(NT) void norm_kernel(NormArgs a, R *__restrict__ res_out, T *__restrict__ out) {
-    __shared__ float sh[2][NT / 64];
+// One row: blockDim.x threads with K times 8 neighbouring channels each.
+template <class T, class R, int K>
+__global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a, R *__restrict__ res_out, T *__restrict__ out) {
+    constexpr int V = kVec;
+    __shared__ float sh[2][1][kMostWaves];
     const int64_t t = blockIdx.x, C = a.channels;
     float q[K][V], r[K][V], sum[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
         float y[V], z[V], s[V], w[V];
         load_n<T, V>(y, at_row<T>(a.y, t, a.y_stride, c), have, 0.0f);
         load_n<T, V>(z, at_row<T>(a.gate, t, a.gate_stride, c), have, 0.0f);
@@ -103,12 +110,12 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a, R *__restrict__ re
             q[k][i] = (a.gate ? s[i] * sigmoid(z[i]) : s[i]) * (y[i] * w[i]);
         }
     }
-    group_totals<NT, 1>(sum, sh[0]);
+    group_totals<1>(sum, sh[0]);
     const float ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
     sum[0] = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             r[k][i] = __builtin_fmaf(q[k][i], ry, r[k][i]);
@@ -116,11 +123,11 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a, R *__restrict__ re
         }
         store_n<R, V>(res_out + t * C + c, r[k], have);
     }
-    group_totals<NT, 1>(sum, sh[1]);
+    group_totals<1>(sum, sh[1]);
     const float rr = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
         float w[V];
         load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
 #pragma unroll
@@ -136,12 +143,52 @@ __global__ __launch_bounds__(NT) void norm_kernel(NormArgs a, R *__restrict__ re
 //   dgate = scale dr y ry post s (1 - s)
 //   dscale = sum dr s y ry post,  dpost = sum scale dr s y ry,  dpre = sum dout r rr
 // A workgroup takes every gridDim.x-th row and keeps its sums over rows in
-// registers; part[workgroup][dscale, dpost, dpre][channel].
-template <class T, class R, int NT, int V, int K>
-__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__restrict__ dout, const R *__restrict__ dres,
-                                                      T *__restrict__ dy, T *__restrict__ dgate, R *__restrict__ dr_out,
-                                                      float *__restrict__ part, uint32_t *hdr, uint32_t words) {
-    __shared__ float sh[2][NT / 64 * 3];
+// registers; part[workgroup][dscale, dpost, dpre][channel].  The next row's
+// loads are on their way while one is worked on (rows of whole vectors;
+// others load their own).
+
+// Eight activations as they were loaded: 16-bit types stay packed until they
+// are used, so that nothing waits for them before.
+template <class T>
+struct Raw8 {
+    float v[8];
+    __device__ __forceinline__ void load(const T *p) {
+        const Pack<T, 8> r = *reinterpret_cast<const Pack<T, 8> *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)r.v[i];
+    }
+    __device__ __forceinline__ void values(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = v[i];
+    }
+};
+template <class T>
+struct Raw8Packed {
+    typedef uint32_t words __attribute__((ext_vector_type(4)));
+    typedef words words_at_2 __attribute__((aligned(2), may_alias));
+    words w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const words_at_2 *>(p); }
+    __device__ __forceinline__ void values(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t b = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            o[i] = (float)__builtin_bit_cast(T, b);
+        }
+    }
+};
+template <>
+struct Raw8<bf16_t> : Raw8Packed<bf16_t> {};
+template <>
+struct Raw8<f16_t> : Raw8Packed<f16_t> {};
+
+template <class T, class R, int K, bool WHOLE>
+__global__ __launch_bounds__(64 * kMostWaves) void norm_bwd_kernel(NormArgs a, const T *__restrict__ dout,
+                                                                   const R *__restrict__ dres, T *__restrict__ dy,
+                                                                   T *__restrict__ dgate, R *__restrict__ dr_out,
+                                                                   float *__restrict__ part, uint32_t *hdr,
+                                                                   uint32_t words) {
+    constexpr int V = kVec;
+    __shared__ float sh[2][3][kMostWaves];
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
     const int64_t C = a.channels;
     float acc[3][K][V];
@@ -149,16 +196,48 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__res
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[0][k][i] = acc[1][k][i] = acc[2][k][i] = 0.0f;
-    for (int64_t t = blockIdx.x; t < (int64_t)a.tokens; t += gridDim.x) {
-        float y[K][V], z[K][V], r[K][V], g[K][V], sum[3] = {0.0f, 0.0f, 0.0f};
+    struct Row {
+        Raw8<T> y[K], z[K], g[K];
+        Raw8<R> r[K], d[K];
+    } next;
+    auto fetch = [&](int64_t t) {
+        if (t >= (int64_t)a.tokens) t = blockIdx.x;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+            uint32_t c = (k * blockDim.x + threadIdx.x) * V;
+            if (c >= a.channels) c = 0u;  // dropped
+            next.y[k].load(static_cast<const T *>(a.y) + t * a.y_stride + c);
+            next.z[k].load(a.gate ? static_cast<const T *>(a.gate) + t * a.gate_stride + c : dout + t * C + c);
+            next.r[k].load(static_cast<const R *>(a.residual) + t * a.residual_stride + c);
+            next.g[k].load(dout + t * C + c);
+            next.d[k].load(dres ? dres + t * C + c : static_cast<const R *>(a.residual) + t * a.residual_stride + c);
+        }
+    };
+    if (WHOLE) fetch(blockIdx.x);
+    for (int64_t t = blockIdx.x; t < (int64_t)a.tokens; t += gridDim.x) {
+        float y[K][V], z[K][V], r[K][V], g[K][V], d[K][V], sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
             float w[V];
-            load_n<T, V>(y[k], at_row<T>(a.y, t, a.y_stride, c), have, 0.0f);
-            load_n<T, V>(z[k], at_row<T>(a.gate, t, a.gate_stride, c), have, 0.0f);
-            load_n<R, V>(r[k], at_row<R>(a.residual, t, a.residual_stride, c), have, 0.0f);
-            load_n<T, V>(g[k], dout + t * C + c, have, 0.0f);
+            if (WHOLE) {
+                next.y[k].values(y[k]);
+                next.z[k].values(z[k]);
+                next.r[k].values(r[k]);
+                next.g[k].values(g[k]);
+                next.d[k].values(d[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (!have) y[k][i] = z[k][i] = r[k][i] = g[k][i] = 0.0f;
+                    if (!have || !dres) d[k][i] = 0.0f;
+                }
+            } else {
+                load_n<T, V>(y[k], at_row<T>(a.y, t, a.y_stride, c), have, 0.0f);
+                load_n<T, V>(z[k], at_row<T>(a.gate, t, a.gate_stride, c), have, 0.0f);
+                load_n<R, V>(r[k], at_row<R>(a.residual, t, a.residual_stride, c), have, 0.0f);
+                load_n<T, V>(g[k], dout + t * C + c, have, 0.0f);
+                load_n<R, V>(d[k], dres ? dres + t * C + c : nullptr, have, 0.0f);
+            }
             load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -167,23 +246,22 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__res
                 sum[2] = __builtin_fmaf(w[i] * g[k][i], r[k][i], sum[2]);
             }
         }
-        group_totals<NT, 3>(sum, sh[0]);
+        if (WHOLE) fetch(t + gridDim.x);
+        group_totals<3>(sum, sh[0]);
         const float ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
         const float rr = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[1], a.inv, a.eps));
         const float lean = rr * rr * (sum[2] * a.inv);
         float tilt[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
-            float w[V], d[V], s[V], po[V];
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+            float w[V], s[V], po[V], dg[V];
             load_n<float, V>(w, at_col(a.pre, c), have, 1.0f);
             load_n<float, V>(s, at_col(a.scale, c), have, 1.0f);
             load_n<float, V>(po, at_col(a.post, c), have, 1.0f);
-            load_n<R, V>(d, dres ? dres + t * C + c : nullptr, have, 0.0f);
-            float dg[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float dr = __builtin_fmaf(rr, __builtin_fmaf(-r[k][i], lean, w[i] * g[k][i]), d[i]);
+                const float dr = __builtin_fmaf(rr, __builtin_fmaf(-r[k][i], lean, w[i] * g[k][i]), d[k][i]);
                 acc[2][k][i] = __builtin_fmaf(g[k][i], r[k][i] * rr, acc[2][k][i]);
                 const float sg = a.gate ? sigmoid(z[k][i]) : 1.0f, unit = y[k][i] * ry;
                 const float along = dr * sg * unit;
@@ -192,17 +270,17 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__res
                 dg[i] = along * s[i] * po[i] * (1.0f - sg);
                 const float u = s[i] * dr * sg * po[i];
                 tilt[0] = __builtin_fmaf(u, y[k][i], tilt[0]);
-                d[i] = dr;
+                d[k][i] = dr;
                 z[k][i] = u;
             }
-            store_n<R, V>(dr_out + t * C + c, d, have);
+            store_n<R, V>(dr_out + t * C + c, d[k], have);
             if (dgate) store_n<T, V>(dgate + t * C + c, dg, have);
         }
-        group_totals<NT, 1>(tilt, sh[1]);
+        group_totals<1>(tilt, sh[1]);
         const float turn = ry * ry * (tilt[0] * a.inv);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
 #pragma unroll
             for (int i = 0; i < V; ++i) y[k][i] = ry * __builtin_fmaf(-y[k][i], turn, z[k][i]);
             store_n<T, V>(dy + t * C + c, y[k], have);
@@ -210,7 +288,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, const T *__res
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const uint32_t c = (k * NT + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * V, have = c < a.channels ? a.channels - c : 0u;
 #pragma unroll
         for (int w = 0; w < 3; ++w) store_n<float, V>(part + ((int64_t)blockIdx.x * 3 + w) * C + c, acc[w][k], have);
     }
@@ -274,27 +352,14 @@ NormArgs norm_args(const ps_norm_input *in) {
     return a;
 }
 
-// Calls f(threads, vectors per thread) as constants: the fewest threads that
-// hold a row of `channels` in `most` vectors of V each.
-template <int V, class F>
+// Calls f(vectors per thread as a constant, threads): one vector a thread up
+// to 8192 channels, two above.
+template <class F>
 ps_status with_shape(uint32_t channels, F f) {
-    auto fit = [&](auto nt, auto k) { return channels <= (uint32_t)(decltype(nt)::value * decltype(k)::value * V); };
-#define DWPS_NORM_SHAPE(NT, K)                                                                      \
-    if (fit(std::integral_constant<int, NT>(), std::integral_constant<int, K>()))                   \
-        return f(std::integral_constant<int, NT>(), std::integral_constant<int, K>())
-    DWPS_NORM_SHAPE(64, 1);
-    if constexpr (V == 4) DWPS_NORM_SHAPE(64, 2);
-    DWPS_NORM_SHAPE(256, 1);
-    DWPS_NORM_SHAPE(256, 2);
-    DWPS_NORM_SHAPE(256, 3);
-    DWPS_NORM_SHAPE(256, 4);
-    if constexpr (V == 4) DWPS_NORM_SHAPE(256, 5);
-    DWPS_NORM_SHAPE(512, 3);
-    DWPS_NORM_SHAPE(512, 4);
-    if constexpr (V == 4) DWPS_NORM_SHAPE(1024, 3);
-    if constexpr (V == 4) DWPS_NORM_SHAPE(1024, 4);
-#undef DWPS_NORM_SHAPE
-    return PS_ERR_SIZE;
+    const uint32_t wave = 64u * kVec;
+    if (channels <= wave * kMostWaves)
+        return f(std::integral_constant<int, 1>(), (uint32_t)ceil_div(channels, wave) * 64u);
+    return f(std::integral_constant<int, 2>(), (uint32_t)ceil_div(channels, 2u * wave) * 64u);
 }
 
 template <class F>
@@ -328,10 +393,9 @@ extern "C" ps_status ps_block_norm(const ps_norm_input *in, void *residual_out, 
     return with_norm_types(in, [&](auto zt, auto zr) {
         using T = decltype(zt);
         using R = decltype(zr);
-        return with_shape<8>(in->channels, [&](auto nt, auto k) {
-            constexpr int NT = decltype(nt)::value, K = decltype(k)::value;
+        return with_shape(in->channels, [&](auto k, uint32_t threads) {
             timing_begin(s);
-            hipLaunchKernelGGL((norm_kernel<T, R, NT, 8, K>), dim3(a.tokens), dim3(NT), 0, s, a,
+            hipLaunchKernelGGL((norm_kernel<T, R, decltype(k)::value>), dim3(a.tokens), dim3(threads), 0, s, a,
                                static_cast<R *>(residual_out), static_cast<T *>(out));
             timing_end(s);
             return launch_status();
@@ -365,15 +429,18 @@ extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm
     return with_norm_types(in, [&](auto zt, auto zr) {
         using T = decltype(zt);
         using R = decltype(zr);
-        return with_shape<4>(in->channels, [&](auto nt, auto k) {
-            constexpr int NT = decltype(nt)::value, K = decltype(k)::value;
+        return with_shape(in->channels, [&](auto k, uint32_t threads) {
+            constexpr int K = decltype(k)::value;
             float *part = ws_at<float>(ws, part_at);
             timing_begin(s);
-            if (groups)
-                hipLaunchKernelGGL((norm_bwd_kernel<T, R, NT, 4, K>), dim3(groups), dim3(NT), 0, s, a,
+            auto launch = [&](auto whole) {
+                hipLaunchKernelGGL((norm_bwd_kernel<T, R, K, decltype(whole)::value>), dim3(groups), dim3(threads), 0, s, a,
                                    static_cast<const T *>(dout), static_cast<const R *>(dresidual_out),
                                    static_cast<T *>(grads->dy), in->gate ? static_cast<T *>(grads->dgate) : nullptr,
                                    static_cast<R *>(grads->dresidual), part, ws_counter(ws), plan.words());
+            };
+            if (groups && in->channels % kVec == 0u) launch(std::true_type());
+            else if (groups) launch(std::false_type());
             if (grads->dscale || grads->dpost_weight || grads->dpre_weight)
                 hipLaunchKernelGGL(norm_params_kernel, dim3((uint32_t)ceil_div(3u * in->channels, 64)), dim3(256), 0, s,
                                    part, groups, in->channels, grads->dscale, grads->dpost_weight, grads->dpre_weight);
