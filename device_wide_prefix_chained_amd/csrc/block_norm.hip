@@ -144,8 +144,8 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a, R *__
 //   dscale = sum dr s y ry post,  dpost = sum scale dr s y ry,  dpre = sum dout r rr
 // A workgroup takes every gridDim.x-th row and keeps its sums over rows in
 // registers; part[workgroup][dscale, dpost, dpre][channel].  The next row's
-// loads are on their way while one is worked on (rows of whole vectors;
-// others load their own).
+// loads are on their way while one is worked on (WHOLE: rows of whole
+// vectors, one a thread; others load their own).
 
 // Eight activations as they were loaded: 16-bit types stay packed until they
 // are used, so that nothing waits for them before.
@@ -181,8 +181,8 @@ struct Raw8<bf16_t> : Raw8Packed<bf16_t> {};
 template <>
 struct Raw8<f16_t> : Raw8Packed<f16_t> {};
 
-template <class T, class R, int K, bool WHOLE>
-__global__ __launch_bounds__(64 * kMostWaves) void norm_bwd_kernel(NormArgs a, const T *__restrict__ dout,
+template <class T, class R, int MOST, int K, bool WHOLE>
+__global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormArgs a, const T *__restrict__ dout,
                                                                    const R *__restrict__ dres, T *__restrict__ dy,
                                                                    T *__restrict__ dgate, R *__restrict__ dr_out,
                                                                    float *__restrict__ part, uint32_t *hdr,
@@ -311,7 +311,13 @@ __global__ __launch_bounds__(256) void norm_params_kernel(const float *__restric
     }
 }
 
-constexpr uint32_t kNormBwdGroups = 512;  // workgroups that share the rows
+// Workgroups that share the rows: as many as the GPU holds at once (12 waves
+// on a CU), up to 4 on a CU.
+uint32_t bwd_groups(const ps_norm_input *in) {
+    const uint32_t waves = (uint32_t)ceil_div(in->channels, 64u * kVec), each = 12u / (waves < 12u ? waves : 12u);
+    const uint32_t groups = 256u * (each < 4u ? each : 4u);
+    return in->tokens < groups ? (uint32_t)in->tokens : groups;
+}
 
 ps_status norm_sizes(const ps_norm_input *in) {
     if (!in) return PS_ERR_NULL;
@@ -362,6 +368,21 @@ ps_status with_shape(uint32_t channels, F f) {
     return f(std::integral_constant<int, 2>(), (uint32_t)ceil_div(channels, 2u * wave) * 64u);
 }
 
+// The same for the backward pass, whose rows and sums over rows take about
+// 150 registers for each vector: f(most threads, vectors per thread,
+// threads), with more than 640 threads (3 waves per SIMD) only where 512 with
+// two vectors do not hold the row.
+template <class F>
+ps_status with_bwd_shape(uint32_t channels, F f) {
+    auto threads = [&](uint32_t k) { return (uint32_t)ceil_div(channels, k * 64u * kVec) * 64u; };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
+    if (channels <= 256u * kVec) return f(std::integral_constant<int, 256>(), One(), threads(1));
+    if (channels <= 640u * kVec) return f(std::integral_constant<int, 640>(), One(), threads(1));
+    if (channels <= 1024u * kVec) return f(std::integral_constant<int, 512>(), Two(), threads(2));
+    return f(std::integral_constant<int, 1024>(), Two(), threads(2));
+}
+
 template <class F>
 ps_status with_norm_types(const ps_norm_input *in, F f) {
     return with_type(in->dtype, [&](auto zero) {
@@ -407,7 +428,7 @@ extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm
                                        const void *dresidual_out, const ps_norm_grads *grads, void *stream) {
     ps_status st = norm_sizes(in);
     if (st != PS_OK) return st;
-    const uint32_t groups = in->tokens < kNormBwdGroups ? (uint32_t)in->tokens : kNormBwdGroups;
+    const uint32_t groups = bwd_groups(in);
     PlainWs plan;
     const size_t part_at = plan.take((size_t)groups * 3u * in->channels * 4u);
     bool query = false;
@@ -429,17 +450,18 @@ extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm
     return with_norm_types(in, [&](auto zt, auto zr) {
         using T = decltype(zt);
         using R = decltype(zr);
-        return with_shape(in->channels, [&](auto k, uint32_t threads) {
+        return with_bwd_shape(in->channels, [&](auto most, auto k, uint32_t threads) {
             constexpr int K = decltype(k)::value;
             float *part = ws_at<float>(ws, part_at);
             timing_begin(s);
             auto launch = [&](auto whole) {
-                hipLaunchKernelGGL((norm_bwd_kernel<T, R, K, decltype(whole)::value>), dim3(groups), dim3(threads), 0, s, a,
+                hipLaunchKernelGGL((norm_bwd_kernel<T, R, decltype(most)::value, K, decltype(whole)::value>), dim3(groups), dim3(threads), 0, s, a,
                                    static_cast<const T *>(dout), static_cast<const R *>(dresidual_out),
                                    static_cast<T *>(grads->dy), in->gate ? static_cast<T *>(grads->dgate) : nullptr,
                                    static_cast<R *>(grads->dresidual), part, ws_counter(ws), plan.words());
             };
-            if (groups && in->channels % kVec == 0u) launch(std::true_type());
+            // a second vector leaves no registers for the next row
+            if (groups && K == 1 && in->channels % kVec == 0u) launch(std::integral_constant<bool, K == 1>());
             else if (groups) launch(std::false_type());
             if (grads->dscale || grads->dpost_weight || grads->dpre_weight)
                 hipLaunchKernelGGL(norm_params_kernel, dim3((uint32_t)ceil_div(3u * in->channels, 64)), dim3(256), 0, s,
