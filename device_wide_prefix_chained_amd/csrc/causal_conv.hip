@@ -28,81 +28,131 @@ struct ConvArgs {
 
 constexpr int kConvThreads = 64;
 
-// Loads / stores up to n channels; `have` of them exist (n but for the last
-// thread of a row).
-template <class T, int n>
-__device__ __forceinline__ void load_row(float (&v)[n], const T *p, uint32_t have) {
-    if (have >= (uint32_t)n) {
-        const Pack<T, n> r = *reinterpret_cast<const Pack<T, n> *>(p);
+// V neighbouring channels as they were loaded: 16-bit types stay packed until
+// they are used, so that nothing waits for them before.
+template <class T, int V>
+struct RawRow {
+    Pack<T, V> r;
+    __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Pack<T, V> *>(p); }
+    __device__ __forceinline__ void values(float (&o)[V]) const {
 #pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = (float)r.v[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = (uint32_t)i < have ? (float)p[i] : 0.0f;
+        for (int i = 0; i < V; ++i) o[i] = (float)r.v[i];
     }
+};
+template <class T>
+struct RawRowPacked {
+    typedef uint32_t words __attribute__((ext_vector_type(4)));
+    typedef words words_at_2 __attribute__((aligned(2), may_alias));
+    words w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const words_at_2 *>(p); }
+    __device__ __forceinline__ void values(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t b = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            o[i] = (float)__builtin_bit_cast(T, b);
+        }
+    }
+};
+template <>
+struct RawRow<bf16_t, 8> : RawRowPacked<bf16_t> {};
+template <>
+struct RawRow<f16_t, 8> : RawRowPacked<f16_t> {};
+
+template <class T, int V>
+__device__ __forceinline__ void load_row(float (&v)[V], const T *p) {
+    RawRow<T, V> r;
+    r.load(p);
+    r.values(v);
 }
-template <class T, int n>
-__device__ __forceinline__ void store_row(T *p, const float (&v)[n], uint32_t have) {
-    if (have >= (uint32_t)n) {
-        Pack<T, n> r;
+template <class T, int V>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
+    Pack<T, V> r;
 #pragma unroll
-        for (int i = 0; i < n; ++i) r.v[i] = (T)v[i];
-        *reinterpret_cast<Pack<T, n> *>(p) = r;
-    } else {
-#pragma unroll
-        for (int i = 0; i < n; ++i)
-            if ((uint32_t)i < have) p[i] = (T)v[i];
+    for (int i = 0; i < V; ++i) r.v[i] = (T)v[i];
+    *reinterpret_cast<Pack<T, V> *>(p) = r;
+}
+
+// The thread's first channel.  The last thread of a row steps back to end
+// with the row: it and its neighbour compute the same values of the channels
+// they share (the first `shared` ones), and no thread has a part of a vector.
+template <int V>
+__device__ __forceinline__ bool own_channels(const ConvArgs &a, uint32_t block, uint32_t &c, uint32_t *shared = nullptr) {
+    const uint32_t own = (block * kConvThreads + threadIdx.x) * V;
+    if (own >= a.channels) return false;
+    c = own + V > a.channels ? a.channels - V : own;
+    if (shared) *shared = own - c;
+    return true;
+}
+// The same, of the channels that the thread shares with no other.
+template <class T, int V>
+__device__ __forceinline__ void store_own(T *p, const float (&v)[V], uint32_t shared) {
+    if (shared == 0u) {
+        store_row<T, V>(p, v);
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if ((uint32_t)i >= shared) p[i] = (T)v[i];
 }
 
 // Row r (any row from seq_lo - (W - 1) on) of the sequence: an input row, an
 // initial row, or zeros.
 template <class T, int V, int W>
-__device__ __forceinline__ void past_row(float (&v)[V], const ConvArgs &a, const Piece &q, int64_t r, uint32_t c,
-                                         uint32_t have) {
+__device__ __forceinline__ void past_row(float (&v)[V], const ConvArgs &a, const Piece &q, int64_t r, uint32_t c) {
     if (r >= (int64_t)q.seq_lo) {
-        load_row<T, V>(v, static_cast<const T *>(a.x) + r * a.x_stride + c, have);
+        load_row<T, V>(v, static_cast<const T *>(a.x) + r * a.x_stride + c);
     } else if (a.initial) {
         const int64_t j = (int64_t)(W - 1) + r - (int64_t)q.seq_lo;
-        load_row<T, V>(v, static_cast<const T *>(a.initial) + ((int64_t)q.seq * (W - 1) + j) * a.channels + c, have);
+        load_row<T, V>(v, static_cast<const T *>(a.initial) + ((int64_t)q.seq * (W - 1) + j) * a.channels + c);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = 0.0f;
     }
 }
 
-template <class T, int V, int W>
-__device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const ConvArgs &a, uint32_t c,
-                                             uint32_t have) {
+template <int V, int W>
+__device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const ConvArgs &a, uint32_t c) {
+    const Pack<float, V * W> all = *reinterpret_cast<const Pack<float, V * W> *>(a.weight + (int64_t)c * W);
+    if (a.bias) {
+        const Pack<float, V> r = *reinterpret_cast<const Pack<float, V> *>(a.bias + c);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool in = (uint32_t)i < have;
-        b[i] = in && a.bias ? a.bias[c + i] : 0.0f;
+        for (int i = 0; i < V; ++i) b[i] = r.v[i];
+    } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = in ? a.weight[(int64_t)(c + i) * W + k] : 0.0f;
+        for (int i = 0; i < V; ++i) b[i] = 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][i] = all.v[i * W + k];
 }
+
+constexpr int kRows = 4;  // rows loaded ahead
 
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__restrict__ out, T *__restrict__ fin) {
     const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, b / a.col_blocks);
-    if (!q.any) return;
-    const uint32_t c = (b % a.col_blocks * kConvThreads + threadIdx.x) * V;
-    if (c >= a.channels) return;
-    const uint32_t have = a.channels - c;
+    uint32_t c;
+    if (!q.any || !own_channels<V>(a, b % a.col_blocks, c)) return;
     const int64_t C = a.channels;
-    const T *x = static_cast<const T *>(a.x);
-    float w[W][V], bias[V], win[W][V];  // win[k]: the row W - 1 - k before the present one
-    load_weights<T, V, W>(w, bias, a, c, have);
+    const T *x = static_cast<const T *>(a.x) + c;
+    RawRow<T, V> next[kRows];
+    auto fetch = [&](uint32_t t) {  // rows past the last repeat it
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c, have);
-    for (uint32_t t = q.lo; t < q.hi; ++t) {
+        for (int i = 0; i < kRows; ++i) next[i].load(x + (int64_t)(t + i < q.hi ? t + i : q.hi - 1u) * a.x_stride);
+    };
+    if (q.lo < q.hi) fetch(q.lo);
+    float w[W][V], bias[V], win[W][V];  // win[k]: the row W - 1 - k before the present one
+    load_weights<V, W>(w, bias, a, c);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c);
+    auto step = [&](const RawRow<T, V> &r, uint32_t t) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
-        load_row<T, V>(win[W - 1], x + (int64_t)t * a.x_stride + c, have);
+        r.values(win[W - 1]);
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -111,12 +161,23 @@ __global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__res
             for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
             o[i] = silu(pre);
         }
-        store_row<T, V>(out + (int64_t)t * C + c, o, have);
+        store_row<T, V>(out + (int64_t)t * C + c, o);
+    };
+    uint32_t t = q.lo;
+    for (; t + kRows <= q.hi; t += kRows) {
+        RawRow<T, V> now[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) now[i] = next[i];
+        fetch(t + kRows);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) step(now[i], t + i);
     }
+#pragma unroll
+    for (int i = 0; i < kRows - 1; ++i)
+        if (t + i < q.hi) step(next[i], t + i);
     if (fin && q.hi == q.seq_hi) {
 #pragma unroll
-        for (int k = 1; k < W; ++k)
-            store_row<T, V>(fin + ((int64_t)q.seq * (W - 1) + k - 1) * C + c, win[k], have);
+        for (int k = 1; k < W; ++k) store_row<T, V>(fin + ((int64_t)q.seq * (W - 1) + k - 1) * C + c, win[k]);
     }
 }
 
@@ -135,27 +196,38 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, cons
     const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
     const uint32_t p = b / a.col_blocks;
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
-    const uint32_t c = (b % a.col_blocks * kConvThreads + threadIdx.x) * V;
-    if (c >= a.channels) return;
-    const uint32_t have = a.channels - c;
+    uint32_t c;
+    if (!own_channels<V>(a, b % a.col_blocks, c)) return;
     const int64_t C = a.channels;
-    const T *x = static_cast<const T *>(a.x);
+    const T *x = static_cast<const T *>(a.x) + c, *gy = dout + c;
     float w[W][V], bias[V], win[W][V], gw[W][V], sum[W + 1][V];
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[k][i] = 0.0f;
     if (q.any) {
-        load_weights<T, V, W>(w, bias, a, c, have);
+        struct Rows {
+            RawRow<T, V> x[kRows], g[kRows];
+        } next;
+        auto fetch = [&](uint32_t t) {  // rows past the sequence's last repeat it
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int64_t r = t + i < q.seq_hi ? t + i : q.seq_hi - 1u;
+                next.x[i].load(x + r * a.x_stride);
+                next.g[i].load(gy + r * C);
+            }
+        };
+        if (q.lo < q.seq_hi) fetch(q.lo);
+        load_weights<V, W>(w, bias, a, c);
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c, have);
-        // an empty sequence: its dinitial rows are zero
-        const uint32_t end = q.hi + (W - 1);
-        for (uint32_t t = q.lo; t < end; ++t) {
+        for (int k = 0; k < W - 1; ++k) past_row<T, V, W>(win[k + 1], a, q, (int64_t)q.lo - (W - 1) + k, c);
+        auto step = [&](const RawRow<T, V> &rx, const RawRow<T, V> &rg, uint32_t t) {
+            // the row's own g, 0 past the sequence
+            float g[V];
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
@@ -163,28 +235,22 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, cons
                     win[k][i] = win[k + 1][i];
                     gw[k][i] = gw[k + 1][i];
                 }
-            if (t < q.seq_hi) {
-                float o[V];
-                load_row<T, V>(win[W - 1], x + (int64_t)t * a.x_stride + c, have);
-                load_row<T, V>(o, dout + (int64_t)t * C + c, have);
+            rx.values(win[W - 1]);
+            rg.values(g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float pre = bias[i];
+#pragma unroll
+                for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
+                gw[W - 1][i] = t < q.seq_hi ? g[i] * dsilu(pre, sigmoid(pre)) : 0.0f;
+            }
+            if (t < q.hi) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float pre = bias[i];
 #pragma unroll
-                    for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
-                    gw[W - 1][i] = o[i] * dsilu(pre, sigmoid(pre));
+                    for (int k = 0; k < W; ++k) sum[k][i] = __builtin_fmaf(gw[W - 1][i], win[k][i], sum[k][i]);
+                    sum[W][i] += gw[W - 1][i];
                 }
-                if (t < q.hi) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-#pragma unroll
-                        for (int k = 0; k < W; ++k) sum[k][i] = __builtin_fmaf(gw[W - 1][i], win[k][i], sum[k][i]);
-                        sum[W][i] += gw[W - 1][i];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) gw[W - 1][i] = 0.0f;
             }
             // the row that now has all its g: gw[j] is g of row r + j
             const int64_t r = (int64_t)t - (W - 1);
@@ -196,19 +262,30 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, cons
 #pragma unroll
                     for (int k = 0; k < W; ++k) o[i] = __builtin_fmaf(w[k][i], gw[W - 1 - k][i], o[i]);
                 }
-                if (r >= (int64_t)q.lo)
-                    store_row<T, V>(dx + r * C + c, o, have);
-                else
-                    store_row<T, V>(dinit + ((int64_t)q.seq * (W - 1) + (r - (int64_t)q.lo + (W - 1))) * C + c, o,
-                                    have);
+                T *to = r >= (int64_t)q.lo ? dx + r * C
+                                           : dinit + ((int64_t)q.seq * (W - 1) + (r - (int64_t)q.lo + (W - 1))) * C;
+                store_row<T, V>(to + c, o);
             }
+        };
+        const uint32_t end = q.hi + (W - 1);
+        if (q.lo < q.seq_hi) {
+            uint32_t t = q.lo;
+            for (; t + kRows <= end; t += kRows) {
+                const Rows now = next;
+                fetch(t + kRows);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) step(now.x[i], now.g[i], t + i);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows - 1; ++i)
+                if (t + i < end) step(next.x[i], next.g[i], t + i);
+        } else if (dinit) {  // an empty sequence gives its initial rows nothing
+            const float none[V] = {};
+            for (int k = 0; k < W - 1; ++k) store_row<T, V>(dinit + ((int64_t)q.seq * (W - 1) + k) * C + c, none);
         }
     }
 #pragma unroll
-    for (int k = 0; k <= W; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if ((uint32_t)i < have) part[((int64_t)p * (W + 1) + k) * C + c + i] = sum[k][i];
+    for (int k = 0; k <= W; ++k) store_row<float, V>(part + ((int64_t)p * (W + 1) + k) * C + c, sum[k]);
 }
 
 // Sums part over the pieces: columns are the (k, channel) pairs.  Each of
@@ -231,41 +308,61 @@ __global__ __launch_bounds__(256) void conv_params_kernel(const float *__restric
     }
 }
 
-// One token for each row: W - 1 rows of state in, W - 1 out.
+// One token for each row: W - 1 rows of state in, W - 1 out.  A workgroup
+// takes `each` rows, so that the weights, which are as large as the states of
+// a row in fp32, are read once for them.  The state may be updated in place,
+// so every channel has one thread that stores it, and what a thread reads of
+// the others' does not matter.
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, const T *state, T *new_state,
                                                                  const int32_t *__restrict__ slots, uint32_t pool,
-                                                                 T *__restrict__ out) {
-    const uint32_t i0 = blockIdx.x / a.col_blocks;
-    const uint32_t c = (blockIdx.x % a.col_blocks * kConvThreads + threadIdx.x) * V;
-    if (c >= a.channels) return;
-    const uint32_t have = a.channels - c;
+                                                                 T *__restrict__ out, uint32_t each) {
+    uint32_t c, shared;
+    if (!own_channels<V>(a, blockIdx.x % a.col_blocks, c, &shared)) return;
     const int64_t C = a.channels;
-    const int64_t slot = slots ? (int64_t)slots[i0] : (int64_t)i0;
-    const bool held = slot >= 0 && slot < (int64_t)pool;
-    float w[W][V], bias[V], win[W][V], o[V];
+    const uint32_t i0 = blockIdx.x / a.col_blocks * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
+    struct Rows {
+        RawRow<T, V> x, s[W];
+        int64_t slot;
+    };
+    auto fetch = [&](Rows &r, uint32_t i) {
+        if (i >= i1) i = i1 - 1u;
+        const int64_t slot = slots ? (int64_t)slots[i] : (int64_t)i;
+        r.slot = slot >= 0 && slot < (int64_t)pool ? slot : -1;
+        r.x.load(static_cast<const T *>(a.x) + (int64_t)i * a.x_stride + c);
+        if (W > 1 && pool) {  // padding reads a slot that exists and drops it
+            const int64_t from = r.slot < 0 ? 0 : r.slot;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        if (held) {
-            load_row<T, V>(win[k], state + (slot * (W - 1) + k) * C + c, have);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) win[k][i] = 0.0f;
+            for (int k = 0; k < W - 1; ++k) r.s[k].load(state + (from * (W - 1) + k) * C + c);
         }
-    }
-    load_row<T, V>(win[W - 1], static_cast<const T *>(a.x) + (int64_t)i0 * a.x_stride + c, have);
-    load_weights<T, V, W>(w, bias, a, c, have);
+    };
+    Rows next;
+    fetch(next, i0);
+    float w[W][V], bias[V];
+    load_weights<V, W>(w, bias, a, c);
+    for (uint32_t i = i0; i < i1; ++i) {
+        const Rows now = next;
+        fetch(next, i + 1u);
+        float win[W][V], o[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float pre = bias[i];
+        for (int k = 0; k < W - 1; ++k) {
+            now.s[k].values(win[k]);
 #pragma unroll
-        for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][i], win[k][i], pre);
-        o[i] = silu(pre);
-    }
-    store_row<T, V>(out + (int64_t)i0 * C + c, o, have);
-    if (held) {
+            for (int j = 0; j < V; ++j) win[k][j] = now.slot < 0 ? 0.0f : win[k][j];
+        }
+        now.x.values(win[W - 1]);
 #pragma unroll
-        for (int k = 1; k < W; ++k) store_row<T, V>(new_state + (slot * (W - 1) + k - 1) * C + c, win[k], have);
+        for (int j = 0; j < V; ++j) {
+            float pre = bias[j];
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][j], win[k][j], pre);
+            o[j] = silu(pre);
+        }
+        store_own<T, V>(out + (int64_t)i * C + c, o, shared);
+        if (now.slot >= 0) {
+#pragma unroll
+            for (int k = 1; k < W; ++k) store_own<T, V>(new_state + (now.slot * (W - 1) + k - 1) * C + c, win[k], shared);
+        }
     }
 }
 
@@ -285,8 +382,24 @@ ps_status with_width(uint32_t width, F f) {
     }
 }
 
+// Calls f with a value of the activations' type, the width and the channels
+// of a thread (16 bytes, or one where a row is shorter) as constants.
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
+uint32_t vec_of(const ps_conv_input *in) {
+    const uint32_t v = 16u / (uint32_t)dtype_bytes(in->dtype);
+    return in->channels < v ? 1u : v;
+}
+template <class F>
+ps_status with_conv(const ps_conv_input *in, F f) {
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_width(in->width, [&](auto w) {
+            if (vec_of(in) == 1u) return f(zero, w, std::integral_constant<int, 1>());
+            return f(zero, w, std::integral_constant<int, kVec<T>>());
+        });
+    });
+}
 
 // Sizes and types alone.
 ps_status conv_sizes(const ps_conv_input *in, bool packed) {
@@ -308,7 +421,8 @@ ps_status conv_pointers(const ps_conv_input *in) {
     return PS_OK;
 }
 
-ConvArgs conv_args(const ps_conv_input *in, uint32_t vec, uint32_t shift) {
+ConvArgs conv_args(const ps_conv_input *in, uint32_t shift) {
+    const uint32_t vec = vec_of(in);
     ConvArgs a{};
     a.x = in->x;
     a.initial = in->width > 1u ? in->initial : nullptr;
@@ -325,7 +439,20 @@ ConvArgs conv_args(const ps_conv_input *in, uint32_t vec, uint32_t shift) {
     return a;
 }
 
-uint32_t conv_shift(const ps_conv_input *, uint32_t) { return 5u; }
+// Rows of a piece, as a power of two.  Forward: as many (8 to 64) as leave
+// 4096 waves, 4 on each SIMD.  Backward: 32, more where there would be above
+// 512 pieces, each of which leaves width + 1 rows of partial sums.
+uint32_t conv_shift(const ps_conv_input *in) {
+    const uint64_t cols = ceil_div(in->channels, (uint64_t)vec_of(in) * kConvThreads);
+    uint32_t shift = 3u;
+    while (shift < 6u && (in->tokens >> (shift + 1u)) * cols >= 4096u) ++shift;
+    return shift;
+}
+uint32_t conv_bwd_shift(const ps_conv_input *in) {
+    uint32_t shift = 5u;
+    while ((in->tokens >> shift) > 512u) ++shift;
+    return shift;
+}
 
 constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
 
@@ -352,20 +479,18 @@ extern "C" ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *fi
         (in->initial && ranges_overlap(out, out_bytes, in->initial, state_bytes)))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return with_type(in->dtype, [&](auto zero) {
+    const ConvArgs a = conv_args(in, conv_shift(in));
+    const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
+    if (grid > kMaxGrid) return PS_ERR_SIZE;
+    if (!grid) return PS_OK;
+    return with_conv(in, [&](auto zero, auto w, auto v) {
         using T = decltype(zero);
-        return with_width(in->width, [&](auto w) {
-            constexpr int W = decltype(w)::value;
-            const ConvArgs a = conv_args(in, kVec<T>, conv_shift(in, kVec<T>));
-            const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
-            if (grid > kMaxGrid) return PS_ERR_SIZE;
-            if (!grid) return PS_OK;
-            timing_begin(s);
-            hipLaunchKernelGGL((conv_kernel<T, kVec<T>, W>), dim3((uint32_t)grid), dim3(kConvThreads), 0, s, a,
-                               static_cast<T *>(out), W > 1 ? static_cast<T *>(final) : nullptr);
-            timing_end(s);
-            return launch_status();
-        });
+        constexpr int W = decltype(w)::value, V = decltype(v)::value;
+        timing_begin(s);
+        hipLaunchKernelGGL((conv_kernel<T, V, W>), dim3((uint32_t)grid), dim3(kConvThreads), 0, s, a,
+                           static_cast<T *>(out), W > 1 ? static_cast<T *>(final) : nullptr);
+        timing_end(s);
+        return launch_status();
     });
 }
 
@@ -374,7 +499,7 @@ extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_con
     ps_status st = conv_sizes(in, true);
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
-    const ConvArgs a = conv_args(in, 16u / (uint32_t)e, conv_shift(in, 16u / (uint32_t)e));
+    const ConvArgs a = conv_args(in, conv_bwd_shift(in));
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
     if (pieces * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
     PlainWs plan;
@@ -391,22 +516,19 @@ extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_con
     const size_t out_bytes = in->tokens * in->channels * e;
     if (ranges_overlap(dx, out_bytes, in->x, in_bytes) || ranges_overlap(dx, out_bytes, dout, out_bytes)) return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return with_type(in->dtype, [&](auto zero) {
+    return with_conv(in, [&](auto zero, auto w, auto v) {
         using T = decltype(zero);
-        return with_width(in->width, [&](auto w) {
-            constexpr int W = decltype(w)::value;
-            float *part = ws_at<float>(ws, part_at);
-            timing_begin(s);
-            if (pieces)
-                hipLaunchKernelGGL((conv_bwd_kernel<T, kVec<T>, W>), dim3((uint32_t)(pieces * a.col_blocks)),
-                                   dim3(kConvThreads), 0, s, a, static_cast<const T *>(dout), static_cast<T *>(dx),
-                                   W > 1 ? static_cast<T *>(dinitial) : nullptr, part, ws_counter(ws), plan.words());
-            hipLaunchKernelGGL(conv_params_kernel,
-                               dim3((uint32_t)ceil_div((uint64_t)(in->width + 1u) * in->channels, 64)), dim3(256), 0, s,
-                               part, (uint32_t)pieces, in->width, in->channels, dweight, dbias);
-            timing_end(s);
-            return launch_status();
-        });
+        constexpr int W = decltype(w)::value, V = decltype(v)::value;
+        float *part = ws_at<float>(ws, part_at);
+        timing_begin(s);
+        if (pieces)
+            hipLaunchKernelGGL((conv_bwd_kernel<T, V, W>), dim3((uint32_t)(pieces * a.col_blocks)), dim3(kConvThreads), 0,
+                               s, a, static_cast<const T *>(dout), static_cast<T *>(dx),
+                               W > 1 ? static_cast<T *>(dinitial) : nullptr, part, ws_counter(ws), plan.words());
+        hipLaunchKernelGGL(conv_params_kernel, dim3((uint32_t)ceil_div((uint64_t)(in->width + 1u) * in->channels, 64)),
+                           dim3(256), 0, s, part, (uint32_t)pieces, in->width, in->channels, dweight, dbias);
+        timing_end(s);
+        return launch_status();
     });
 }
 
@@ -428,18 +550,19 @@ extern "C" ps_status ps_causal_conv_step(const ps_conv_input *in, const void *st
         return PS_ERR_ALIAS;
     if (!in->tokens) return PS_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return with_type(in->dtype, [&](auto zero) {
+    const ConvArgs a = conv_args(in, 0u);
+    if (in->tokens * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
+    // up to 4 rows a workgroup, while 2 waves are left for each SIMD
+    const uint64_t share = in->tokens * a.col_blocks / 2048u;
+    const uint32_t each = share < 1u ? 1u : share > 4u ? 4u : (uint32_t)share;
+    return with_conv(in, [&](auto zero, auto w, auto v) {
         using T = decltype(zero);
-        return with_width(in->width, [&](auto w) {
-            constexpr int W = decltype(w)::value;
-            const ConvArgs a = conv_args(in, kVec<T>, 0u);
-            if (in->tokens * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
-            timing_begin(s);
-            hipLaunchKernelGGL((conv_step_kernel<T, kVec<T>, W>), dim3((uint32_t)in->tokens * a.col_blocks),
-                               dim3(kConvThreads), 0, s, a, static_cast<const T *>(state), static_cast<T *>(new_state),
-                               slots, pool, static_cast<T *>(out));
-            timing_end(s);
-            return launch_status();
-        });
+        constexpr int W = decltype(w)::value, V = decltype(v)::value;
+        timing_begin(s);
+        hipLaunchKernelGGL((conv_step_kernel<T, V, W>), dim3((uint32_t)ceil_div(in->tokens, each) * a.col_blocks),
+                           dim3(kConvThreads), 0, s, a, static_cast<const T *>(state), static_cast<T *>(new_state), slots,
+                           pool, static_cast<T *>(out), each);
+        timing_end(s);
+        return launch_status();
     });
 }

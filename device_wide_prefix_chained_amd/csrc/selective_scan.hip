@@ -279,43 +279,83 @@ __global__ __launch_bounds__(64) void scan_link_kernel(ScanArgs a, float *__rest
 }
 
 // One token for each row.  A lane holds 4 states of one channel (16 bytes of
-// the state), `lanes` = a power of two lanes share a channel.
-template <class T>
+// the state, where VEC: the states are a multiple of 4), a power of two
+// `lanes` of them a channel, and a workgroup takes `each` rows: A, as large as
+// a row's states, is read once for them.  Bound by memory, the states once in
+// and once out; the next row's are on their way while one is worked on.
+template <class T, bool VEC>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float *state, float *new_state,
                                                         const int32_t *__restrict__ slots, uint32_t pool,
-                                                        T *__restrict__ out, uint32_t lanes, uint32_t blocks) {
-    const uint32_t i = blockIdx.x / blocks;
+                                                        T *__restrict__ out, uint32_t lanes, uint32_t blocks,
+                                                        uint32_t each) {
     const uint32_t at = blockIdx.x % blocks * 256u + threadIdx.x;
-    const uint32_t d = at / lanes, part = at % lanes, N = a.states;
-    const bool in = d < a.channels;
-    const int64_t slot = slots ? (int64_t)slots[i] : (int64_t)i;
-    const bool held = slot >= 0 && slot < (int64_t)pool;
-    float sum = 0.0f, x = 0.0f;
-    if (in) {
-        x = (float)static_cast<const T *>(a.x)[(int64_t)i * a.x_stride + d];
-        const float dt = (float)static_cast<const T *>(a.dt)[(int64_t)i * a.dt_stride + d];
-        const float step = softplus(dt + (a.bias ? a.bias[d] : 0.0f));
-        const float drive = step * x;
-        const uint32_t g = d / a.group_channels;
-        for (uint32_t n = part * 4u; n < N; n += lanes * 4u) {
-            const int64_t sat = (slot * a.channels + d) * (int64_t)N + n;
+    const uint32_t i0 = blockIdx.x / blocks * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
+    const uint32_t N = a.states, own = at / lanes, n = at % lanes * 4u;
+    // lanes past the last channel or state work on one that exists and store nothing
+    const uint32_t d = own < a.channels ? own : a.channels - 1u;
+    const bool in = own < a.channels && n < N;
+    const uint32_t n0 = n < N ? n : VEC ? N - 4u : N - 1u;
+    const uint32_t g = d / a.group_channels;
+    uint32_t off[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (n + k >= N) break;
-                const float e = exp2_hw(step * (a.A[(int64_t)d * N + n + k] * kLog2e));
-                const float b = (float)static_cast<const T *>(a.B)[(int64_t)i * a.b_stride + g * N + n + k];
-                const float c = (float)static_cast<const T *>(a.C)[(int64_t)i * a.c_stride + g * N + n + k];
-                const float h = __builtin_fmaf(e, held ? state[sat + k] : 0.0f, drive * b);
-                if (held) new_state[sat + k] = h;
-                sum = __builtin_fmaf(h, c, sum);
+    for (int k = 0; k < 4; ++k) off[k] = VEC || n0 + k < N ? k : 0u;
+    struct Row {
+        float h[4], x, dt, z;
+        T b[4], c[4];
+        int64_t slot;
+    };
+    auto fetch = [&](Row &r, uint32_t i) {
+        if (i >= i1) i = i1 - 1u;
+        const int64_t slot = slots ? (int64_t)slots[i] : (int64_t)i;
+        r.slot = slot >= 0 && slot < (int64_t)pool ? slot : -1;
+        const T *b = static_cast<const T *>(a.B) + (int64_t)i * a.b_stride + g * N + n0;
+        const T *c = static_cast<const T *>(a.C) + (int64_t)i * a.c_stride + g * N + n0;
+        // padding reads a slot that exists and drops it (any floats where there is none)
+        const float *h = (pool ? state + ((r.slot < 0 ? 0 : r.slot) * a.channels + d) * (int64_t)N : a.A + (int64_t)d * N) + n0;
+        if (VEC) {
+            const Pack<float, 4> hv = *reinterpret_cast<const Pack<float, 4> *>(h);
+            const Pack<T, 4> bv = *reinterpret_cast<const Pack<T, 4> *>(b), cv = *reinterpret_cast<const Pack<T, 4> *>(c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.h[k] = hv.v[k], r.b[k] = bv.v[k], r.c[k] = cv.v[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.h[k] = h[off[k]], r.b[k] = b[off[k]], r.c[k] = c[off[k]];
+        }
+        r.x = (float)static_cast<const T *>(a.x)[(int64_t)i * a.x_stride + d];
+        r.dt = (float)static_cast<const T *>(a.dt)[(int64_t)i * a.dt_stride + d];
+        r.z = a.z ? (float)static_cast<const T *>(a.z)[(int64_t)i * a.z_stride + d] : 0.0f;
+    };
+    Row next;
+    fetch(next, i0);
+    float A2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] = a.A[(int64_t)d * N + n0 + off[k]] * kLog2e;
+    const float bias = a.bias ? a.bias[d] : 0.0f, skip = a.D ? a.D[d] : 0.0f;
+    for (uint32_t i = i0; i < i1; ++i) {
+        const Row r = next;
+        if (i + 1u < i1) fetch(next, i + 1u);
+        const float step = softplus(r.dt + bias), drive = step * r.x;
+        float h[4], sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = __builtin_fmaf(exp2_hw(step * A2[k]), r.slot < 0 ? 0.0f : r.h[k], drive * (float)r.b[k]);
+            if (n < N && (VEC || n + k < N)) sum = __builtin_fmaf(h[k], (float)r.c[k], sum);
+        }
+        if (in && r.slot >= 0) {
+            float *to = new_state + (r.slot * a.channels + d) * (int64_t)N + n;
+            if (VEC) {
+                *reinterpret_cast<Pack<float, 4> *>(to) = Pack<float, 4>{{h[0], h[1], h[2], h[3]}};
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (n + k < N) to[k] = h[k];
             }
         }
-    }
-    for (uint32_t m = lanes / 2u; m; m /= 2u) sum += __shfl_xor(sum, (int)m);
-    if (in && part == 0u) {
-        float y = a.D ? __builtin_fmaf(a.D[d], x, sum) : sum;
-        if (a.z) y *= silu((float)static_cast<const T *>(a.z)[(int64_t)i * a.z_stride + d]);
-        out[(int64_t)i * a.channels + d] = (T)y;
+        for (uint32_t m = lanes / 2u; m; m /= 2u) sum += __shfl_xor(sum, (int)m);
+        if (in && n == 0u) {
+            const float y = __builtin_fmaf(skip, r.x, sum);
+            out[(int64_t)i * a.channels + d] = (T)(a.z ? y * silu(r.z) : y);
+        }
     }
 }
 
@@ -487,13 +527,21 @@ extern "C" ps_status ps_selective_scan_step(const ps_scan_input *in, const float
     while (lanes < 64u && lanes * 4u < in->states) lanes *= 2u;
     const uint64_t blocks = ceil_div((uint64_t)in->channels * lanes, 256);
     if (in->tokens * blocks > kScanMaxGrid) return PS_ERR_SIZE;
+    // up to 8 rows a workgroup, while 4 workgroups are left for each CU
+    const uint64_t share = in->tokens * blocks / 1024u;
+    const uint32_t each = share < 1u ? 1u : share > 8u ? 8u : (uint32_t)share;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const ScanArgs a = scan_args(in, 32u);
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
         timing_begin(s);
-        hipLaunchKernelGGL(scan_step_kernel<T>, dim3((uint32_t)(in->tokens * blocks)), dim3(256), 0, s, a, state,
-                           new_state, slots, pool, static_cast<T *>(out), lanes, (uint32_t)blocks);
+        auto launch = [&](auto vec) {
+            hipLaunchKernelGGL((scan_step_kernel<T, decltype(vec)::value>),
+                               dim3((uint32_t)(ceil_div(in->tokens, each) * blocks)), dim3(256), 0, s, a, state, new_state,
+                               slots, pool, static_cast<T *>(out), lanes, (uint32_t)blocks, each);
+        };
+        if (in->states % 4u == 0u) launch(std::true_type());
+        else launch(std::false_type());
         timing_end(s);
         return launch_status();
     });
