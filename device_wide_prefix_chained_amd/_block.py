@@ -108,53 +108,73 @@ def _lib():
     return _lib_ready
 
 
-def _tokens(name, t, dims):
-    """An activation tensor with `dims` dimensions: its row stride."""
+# A call checks ten tensors or more; each check is one expression where
+# nothing is wrong, and only then does _refuse look for what is.
+def _refuse(name, t, like, shape, dtype):
+    """Raises for a tensor that is not of like's device, `shape` and `dtype`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions" % (name, dims))
-    stride = t.stride()
-    step = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(stride[1:])):
-        if s != step and n > 1:
-            raise ValueError("%s must be packed within its rows" % name)
-        step *= n
-    # the stride of a single row (or none) says nothing
-    if t.shape[0] <= 1:
-        return step
-    if stride[0] < step:
-        raise ValueError("%s has rows that overlap" % name)
-    return stride[0]
-
-
-def _same(name, t, like, shape, dtype=None):
-    """An activation shaped `shape` of like's type and device: its row stride."""
-    stride = _tokens(name, t, len(shape))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    _typed(name, t, like, like.dtype if dtype is None else dtype)
-    return stride
-
-
-def _typed(name, t, like, dtype):
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.get_device() != like.get_device():
         raise ValueError("%s must be on the device of the other tensors" % name)
 
 
+def _row_stride(name, t):
+    """Elements from row to row of an activation, packed within its rows."""
+    if t.is_contiguous() and t.shape[0]:
+        return t.numel() // t.shape[0]
+    step = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if s != step and n > 1:
+            raise ValueError("%s must be packed within its rows" % name)
+        step *= n
+    # the stride of a single row (or none) says nothing
+    if t.shape[0] <= 1:
+        return step
+    if t.stride(0) < step:
+        raise ValueError("%s has rows that overlap" % name)
+    return t.stride(0)
+
+
+def _first(name, t):
+    """The activation the others are compared with ([tokens, channels])."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be [tokens, channels]" % name)
+    return _row_stride(name, t)
+
+
+def _same(name, t, like, shape, dtype=None):
+    """An activation shaped `shape` of like's type and device: its row stride."""
+    if dtype is None:
+        dtype = like.dtype
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == like.get_device():
+            return _row_stride(name, t)
+    except AttributeError:
+        pass
+    _refuse(name, t, like, shape, dtype)
+
+
 def _packed(name, t, like, shape, dtype):
     """A packed tensor (parameter, state, result) or None: its address."""
     if t is None:
         return None
-    _dev_tensor(name, t)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    _typed(name, t, like, dtype)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, like, shape, dtype)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _type_of(name, t):
@@ -197,6 +217,8 @@ class _Results:
 
     def __call__(self, shape, dtype):
         if self.stream is None:
+            if dtype is self.like.dtype and shape == self.like.shape and self.like.is_contiguous():
+                return torch.empty_like(self.like)
             return torch.empty(shape, dtype=dtype, device=self.like.device)
         with torch.cuda.stream(_torch_stream(self.like.device, self.stream)):
             return torch.empty(shape, dtype=dtype, device=self.like.device)
@@ -216,7 +238,7 @@ def _with_workspace(fn, call, like, workspace, stream):
 # ---------------------------------------------------------------------------
 def _conv_input(x, weight, bias, offsets, initial):
     f32 = torch.float32
-    stride = _tokens("x", x, 2)
+    stride = _first("x", x)
     code = _type_of("x", x)
     tokens, channels = x.shape
     if weight.dim() != 2:
@@ -278,7 +300,7 @@ def ps_causal_conv_step(x, state, weight, bias=None, *, slots=None, new_state=No
 # ---------------------------------------------------------------------------
 def _scan_input(x, dt, A, B, C, D, z, dt_bias, offsets, initial):
     f32 = torch.float32
-    xs = _tokens("x", x, 2)
+    xs = _first("x", x)
     code = _type_of("x", x)
     tokens, channels = x.shape
     if B.dim() != 3 or A.dim() != 2:
@@ -365,7 +387,7 @@ def ps_selective_scan_step(x, state, dt, A, B, C, *, D=None, z=None, dt_bias=Non
 # ---------------------------------------------------------------------------
 def _norm_input(y, residual, gate, scale, post_weight, pre_weight, eps):
     f32 = torch.float32
-    ys = _tokens("y", y, 2)
+    ys = _first("y", y)
     code = _type_of("y", y)
     tokens, channels = y.shape
     rt = residual.dtype

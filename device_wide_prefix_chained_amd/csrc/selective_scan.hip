@@ -367,8 +367,10 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float 
 // sequence (random cuts: (1 + ln seqs) / seqs of the rows) and an even share;
 // cells 1.75 shares and about 30 turns for two more launches, and the link of
 // 32 cells about 4.  Cells are as long as leaves four workgroups for a CU.
-// Both sides, bf16 and 16 states, one sequence of 16384 rows, whole / cells:
-// SPLIT_MEASURED
+// Both sides in us, bf16, 16 states, one sequence, whole / cells: 16384 rows
+// of 64 channels 358 / 46, 512: 359 / 88, 1024: 361 / 151, 2048: 364 / 273
+// (4096: 387 whole); 256 channels of 4096 rows 91 / 33, 2048: 48 / 29 (1024:
+// 26 whole).
 uint32_t scan_shift(const ps_scan_input *in) {
     const ScanArgs a = scan_args(in, 32u);
     const double blocks = (double)ceil_div(in->tokens, kScanTile), share = blocks * a.col_blocks / 256.0;
