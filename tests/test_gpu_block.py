@@ -495,3 +495,29 @@ def test_binding_refuses(dw):
         dw.ps_causal_conv(x, m.par(ch, 9))
     with pytest.raises(dw.DwpsError):
         dw.ps_causal_conv(x, w, out=x)
+
+
+def test_a_sequence_alone_and_among_others(dw):
+    """Many states, few channels and long sequences: the gradients' largest
+    workgroups (four channel blocks, their sums over states in shared memory).
+    A sequence gives what it gives by itself; only where its states come from
+    (cells or the walk itself) may round differently."""
+    m = Maker(14, F32)
+    T, cut, ch, N = 16448, 320, 64, 64
+    a, more = _scan_inputs(m, T, ch, 1, N, 2, False, "Dzb")
+    dout = m.act(T, ch)
+
+    def run(rows, off):
+        at = {k: v[rows] if v.shape[0] == T else v for k, v in a.items()}
+        opt = dict(more, z=more["z"][rows])
+        kept = torch.empty(dw.ps_selective_scan_checkpoint_rows(at["x"].shape[0], N), ch, N, device="cuda")
+        out = dw.ps_selective_scan(**at, **opt, offsets=off, checkpoints=kept)
+        g = dw.ps_selective_scan_bwd(*at.values(), dout[rows], kept, **opt, offsets=off)
+        return at, opt, [out, g.dx, g.ddt, g.dz, g.dB, g.dC]
+    say("alone and among others")
+    _, _, among = run(slice(0, T), _offsets([0, cut, T]))
+    at, opt, alone = run(slice(0, cut), None)
+    mag = ref.scan(**at, **opt, dout=dout[:cut], bound=True)
+    K = 2 * ref.scan_roundings(at["dt"], at["A"], opt["dt_bias"], cut, ch, N)
+    for name, x, y in zip(("out", "dx", "ddt", "dz", "dB", "dC"), among, alone):
+        ref.close(name, x[:cut], ref.f64(y), mag[name], K)
