@@ -212,16 +212,22 @@ def _slots(slots, like, batch, pool):
 class _Results:
     """Allocates results on the call's stream."""
 
-    def __init__(self, like, stream):
-        self.like, self.stream = like, stream
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
 
     def __call__(self, shape, dtype):
         if self.stream is None:
-            if dtype is self.like.dtype and shape == self.like.shape and self.like.is_contiguous():
-                return torch.empty_like(self.like)
-            return torch.empty(shape, dtype=dtype, device=self.like.device)
-        with torch.cuda.stream(_torch_stream(self.like.device, self.stream)):
-            return torch.empty(shape, dtype=dtype, device=self.like.device)
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(_torch_stream(self.device, self.stream)):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def like(self, t):
+        """A packed tensor of t's shape and type, or None for None."""
+        if t is None:
+            return None
+        if self.stream is None and t.is_contiguous():
+            return torch.empty_like(t)
+        return self(t.shape, t.dtype)
 
 
 def _addr(t):
@@ -256,7 +262,7 @@ def ps_causal_conv(x, weight, bias=None, *, offsets=None, initial=None, out=None
     width] over each channel's past); ``initial`` and ``final`` are the width
     - 1 rows before and at the end of each sequence."""
     a = _conv_input(x, weight, bias, offsets, initial)
-    o = _Results(x, stream)(x.shape, x.dtype) if out is None else out
+    o = _Results(x.device, stream).like(x) if out is None else out
     _check("ps_causal_conv", _lib().ps_causal_conv(
         a, _packed("out", o, x, x.shape, x.dtype),
         _packed("final", final, x, (a.num_seqs, a.width - 1, a.channels), x.dtype), _stream(x, stream)))
@@ -268,10 +274,8 @@ def ps_causal_conv_bwd(x, weight, dout, bias=None, *, offsets=None, initial=None
     the last two where there is a bias and an initial."""
     a = _conv_input(x, weight, bias, offsets, initial)
     g = _packed("dout", dout, x, x.shape, x.dtype)
-    new = _Results(x, stream)
-    f32 = torch.float32
-    r = ConvGrads(new(x.shape, x.dtype), new(weight.shape, f32), None if bias is None else new(bias.shape, f32),
-                  None if initial is None else new(initial.shape, x.dtype))
+    new = _Results(x.device, stream)
+    r = ConvGrads(*(new.like(t) for t in (x, weight, bias, initial)))
     s, f = _stream(x, stream), _lib().ps_causal_conv_bwd
     call = lambda ws, wsb: f(ws, wsb, a, g, _addr(r.dx), _addr(r.dweight), _addr(r.dbias),  # noqa: E731
                              _addr(r.dinitial), s)
@@ -288,7 +292,7 @@ def ps_causal_conv_step(x, state, weight, bias=None, *, slots=None, new_state=No
     shape = (pool, a.width - 1, a.channels)
     old = _packed("state", state, x, shape, x.dtype)
     new = old if new_state is None else _packed("new_state", new_state, x, shape, x.dtype)
-    o = _Results(x, stream)(x.shape, x.dtype) if out is None else out
+    o = _Results(x.device, stream).like(x) if out is None else out
     _check("ps_causal_conv_step", _lib().ps_causal_conv_step(
         a, old, new, _slots(slots, x, a.tokens, pool), pool, _packed("out", o, x, x.shape, x.dtype),
         _stream(x, stream)))
@@ -332,7 +336,7 @@ def ps_selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, offsets=N
     ``checkpoints``, what ps_selective_scan_bwd starts from)."""
     a = _scan_input(x, dt, A, B, C, D, z, dt_bias, offsets, initial)
     f32 = torch.float32
-    o = _Results(x, stream)(x.shape, x.dtype) if out is None else out
+    o = _Results(x.device, stream).like(x) if out is None else out
     to = _packed("out", o, x, x.shape, x.dtype)
     fin = _packed("final", final, x, (a.num_seqs, a.channels, a.states), f32)
     kept = None
@@ -353,11 +357,8 @@ def ps_selective_scan_bwd(x, dt, A, B, C, dout, checkpoints, *, D=None, z=None, 
     g = _packed("dout", dout, x, x.shape, x.dtype)
     rows = ps_selective_scan_checkpoint_rows(a.tokens, a.states)
     kept = _packed("checkpoints", checkpoints, x, (rows, a.channels, a.states), f32)
-    new = _Results(x, stream)
-    r = ScanGrads(new(x.shape, x.dtype), new(x.shape, x.dtype), new(A.shape, f32), new(B.shape, x.dtype),
-                  new(B.shape, x.dtype), None if D is None else new(D.shape, f32),
-                  None if z is None else new(x.shape, x.dtype), None if dt_bias is None else new(dt_bias.shape, f32),
-                  None if initial is None else new(initial.shape, f32))
+    new = _Results(x.device, stream)
+    r = ScanGrads(*(new.like(t) for t in (x, dt, A, B, C, D, z, dt_bias, initial)))
     grads = _ScanGrads(_addr(r.dx), _addr(r.ddt), _addr(r.dz), _addr(r.dB), _addr(r.dC), _addr(r.dA), _addr(r.dD),
                        _addr(r.ddt_bias), _addr(r.dinitial))
     s, f = _stream(x, stream), _lib().ps_selective_scan_bwd
@@ -376,7 +377,7 @@ def ps_selective_scan_step(x, state, dt, A, B, C, *, D=None, z=None, dt_bias=Non
     shape = (pool, a.channels, a.states)
     old = _packed("state", state, x, shape, f32)
     new = old if new_state is None else _packed("new_state", new_state, x, shape, f32)
-    o = _Results(x, stream)(x.shape, x.dtype) if out is None else out
+    o = _Results(x.device, stream).like(x) if out is None else out
     _check("ps_selective_scan_step", _lib().ps_selective_scan_step(
         a, old, new, _slots(slots, x, a.tokens, pool), pool, _packed("out", o, x, x.shape, x.dtype), _stream(x, stream)))
     return o
@@ -406,9 +407,9 @@ def ps_block_norm(y, residual, *, gate=None, scale=None, post_weight=None, pre_w
     """(residual + scale * sigmoid(gate) * norm(y) * post_weight, its norm *
     pre_weight): the residual stream after a block and the input of the next."""
     a = _norm_input(y, residual, gate, scale, post_weight, pre_weight, eps)
-    new = _Results(y, stream)
-    r = new(y.shape, residual.dtype) if residual_out is None else residual_out
-    o = new(y.shape, y.dtype) if out is None else out
+    new = _Results(y.device, stream)
+    r = new.like(residual) if residual_out is None else residual_out
+    o = new.like(y) if out is None else out
     _check("ps_block_norm", _lib().ps_block_norm(
         a, _packed("residual_out", r, y, y.shape, residual.dtype), _packed("out", o, y, y.shape, y.dtype),
         _stream(y, stream)))
@@ -422,10 +423,8 @@ def ps_block_norm_bwd(y, residual_out, dout, dresidual_out=None, *, gate=None, s
     a = _norm_input(y, residual_out, gate, scale, post_weight, pre_weight, eps)
     g = _packed("dout", dout, y, y.shape, y.dtype)
     dr = _packed("dresidual_out", dresidual_out, y, y.shape, residual_out.dtype)
-    new = _Results(y, stream)
-    w, f32 = (y.shape[1],), torch.float32
-    r = NormGrads(new(y.shape, y.dtype), new(y.shape, residual_out.dtype), None if gate is None else new(y.shape, y.dtype),
-                  *(None if p is None else new(w, f32) for p in (scale, post_weight, pre_weight)))
+    new = _Results(y.device, stream)
+    r = NormGrads(*(new.like(t) for t in (y, residual_out, gate, scale, post_weight, pre_weight)))
     grads = _NormGrads(_addr(r.dy), _addr(r.dgate), _addr(r.dresidual), _addr(r.dscale), _addr(r.dpost_weight),
                        _addr(r.dpre_weight))
     s, f = _stream(y, stream), _lib().ps_block_norm_bwd
