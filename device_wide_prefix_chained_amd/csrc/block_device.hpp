@@ -43,8 +43,7 @@ __device__ __forceinline__ float softplus(float v) {
     p = __builtin_fmaf(s, p, 1.0f / 5.0f);
     p = __builtin_fmaf(s, p, 1.0f / 3.0f);
     const float tail = q * s * p;
-    const float base = v > 0.0f ? v : v != v ? v : 0.0f;
-    return base + 2.0f * (q + tail);
+    return __builtin_fmaxf(v, 0.0f) + 2.0f * (q + tail);  // NaN through q
 }
 
 // An argument whose softplus is exactly 0.
