@@ -458,7 +458,8 @@ extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm
             float *part = ws_at<float>(ws, part_at);
             timing_begin(s);
             auto launch = [&](auto whole) {
-                hipLaunchKernelGGL((norm_bwd_kernel<T, R, decltype(most)::value, K, decltype(whole)::value>), dim3(groups), dim3(threads), 0, s, a,
+                hipLaunchKernelGGL((norm_bwd_kernel<T, R, decltype(most)::value, K, decltype(whole)::value>),
+                                   dim3(groups), dim3(threads), 0, s, a,
                                    static_cast<const T *>(dout), static_cast<const R *>(dresidual_out),
                                    static_cast<T *>(grads->dy), in->gate ? static_cast<T *>(grads->dgate) : nullptr,
                                    static_cast<R *>(grads->dresidual), part, ws_counter(ws), plan.words());

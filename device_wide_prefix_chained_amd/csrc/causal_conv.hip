@@ -409,7 +409,8 @@ ps_status conv_sizes(const ps_conv_input *in, bool packed) {
     if (!in) return PS_ERR_NULL;
     if (!dtype_bytes(in->dtype)) return PS_ERR_UNSUPPORTED;
     if (in->tokens > kBlockMaxTokens || in->channels == 0u || in->channels > kBlockMaxChannels || in->width == 0u ||
-        in->width > PS_CONV_MAX_WIDTH || in->num_seqs > kBlockMaxSeqs || in->x_stride < (int64_t)in->channels || in->x_stride > kBlockMaxStride)
+        in->width > PS_CONV_MAX_WIDTH || in->num_seqs > kBlockMaxSeqs || in->x_stride < (int64_t)in->channels ||
+        in->x_stride > kBlockMaxStride)
         return PS_ERR_SIZE;
     if (packed && !in->offsets && in->num_seqs > 1u) return PS_ERR_SIZE;
     return PS_OK;

@@ -22,7 +22,7 @@ namespace {
 // barrier a block.  The walk is bound by arithmetic: for every state exp2
 // (two issue slots) and 4 more operations (the broadcasts of step and step x
 // are part of the products), and 33 for 16 sums over states.  8191 x 4096 x 16
-// states, bf16, one sequence (a walking wave for each SIMD): 193 us, 77% of the
+// states, bf16, one sequence (a walking wave for each SIMD): 191 us, 77% of the
 // vector issue slots taken; without waves that feed 289 us, without the
 // walking waves' priority 215 us.
 template <class T, int S, bool OUT, bool FULL>
@@ -498,18 +498,18 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
             float *steps = split ? ws_at<float>(ws, steps_at) : nullptr;
             uint32_t *links = split ? ws_at<uint32_t>(ws, links_at) : nullptr;
             return with_full(in, [&](auto full) {
-            constexpr bool FULL = decltype(full)::value;
-            timing_begin(s);
-            if (split) {
-                hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
-                                   (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
-                                   plan.words());
-                launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
-            }
-            hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
-                               static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
-            timing_end(s);
-            return launch_status();
+                constexpr bool FULL = decltype(full)::value;
+                timing_begin(s);
+                if (split) {
+                    hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
+                                       (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
+                                       plan.words());
+                    launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
+                }
+                hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
+                                   static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
+                timing_end(s);
+                return launch_status();
             });
         });
     });

@@ -208,8 +208,9 @@ __device__ __forceinline__ void fold_rows(float (&o)[8], float (&v)[32]) {
 // One piece of a cell, a range of channel blocks.  States 16 at a time
 // (outer loop), channels 16 at a time (inner loop): a lane sums dB and dC of
 // its state over the inner loop in registers, token by token, and keeps a
-// and h of the piece's 32 rows between the walk forward and the walk back.  With more than 16 states the three sums over states wait in
-// shared memory for the last 16.
+// and h of the piece's 32 rows between the walk forward and the walk back.
+// With more than 16 states the three sums over states wait in shared memory
+// for the last 16.
 //
 // As in the forward walk, four waves feed (they load, stage and, a block
 // later, form the block's outputs) and four walk.  Bound by arithmetic: for
@@ -503,9 +504,8 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
             float *cell = cell_of(cb) + cw * kScanPad + l;
             const float *pS = sStep[half] + cw * kScanPad, *pD = sDrive[half] + cw * kScanPad, *pG = sGrad[half] + cw * kScanPad;
             float h[32];
-            f4 er[8];
+            f4 decay[8];
             float run = h0;
-
             const float stv[2] = {pS[l], pS[16 + l]}, drv[2] = {pD[l], pD[16 + l]};
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
                         y[q0].v[i] = run * C4[i];
                     };
                     for_each_index(token, std::make_integer_sequence<int, 4>());
-                    er[sub * 4 + q0] = e;
+                    decay[sub * 4 + q0] = e;
                     if constexpr (q0 >= 2) y[q0 - 2] = row_fold8(y[q0 - 2], y[q0]);
                 };
                 for_each_index(quad, std::make_integer_sequence<int, 4>());
@@ -532,18 +532,16 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
             read_later();
             float sumA = 0.0f;
             f4 uB = four(pB + 28), uC = four(pC + 28), uS = four(pS + 28), uD = four(pD + 28), uG = four(pG + 28);
-            
 #pragma unroll
             for (int sub = 1; sub >= 0; --sub) {
                 Four along[4], flowA[4];
                 auto quad = [&](auto jc) {
                     constexpr int q0 = 3 - decltype(jc)::value;
                     const int k0 = sub * 16 + q0 * 4;
-                    const f4 B4 = uB, C4 = uC, S4 = uS, D4 = uD, G4 = uG, E4 = er[k0 / 4];
+                    const f4 B4 = uB, C4 = uC, S4 = uS, D4 = uD, G4 = uG, E4 = decay[k0 / 4];
                     if (k0) {
                         uB = four(pB + k0 - 4), uC = four(pC + k0 - 4), uS = four(pS + k0 - 4);
                         uD = four(pD + k0 - 4), uG = four(pG + k0 - 4);
-                        
                     }
                     in_order();
 #pragma unroll
