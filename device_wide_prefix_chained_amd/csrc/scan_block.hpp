@@ -11,13 +11,13 @@
 #pragma once
 
 #include "block_device.hpp"
+#include "scan_shape.hpp"
 
 namespace dwps {
 
 constexpr uint32_t kScanCellShift = 5;            // rows between checkpoints
 constexpr uint32_t kScanCell = 1u << kScanCellShift;
 constexpr int kScanTile = 32;                     // tokens staged at a time
-constexpr int kScanChannels = 16;                 // channels of a workgroup
 constexpr int kScanThreads = 256;
 // Floats from one staged channel (or state) to the next: a multiple of 4 for
 // 16-byte reads, and 36 mod 64 = 36 spreads pairs of channels over the banks.
@@ -132,22 +132,24 @@ bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes);
 void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
                       bool backward, hipStream_t s);
 
-// Calls f(true) if every group is made of whole blocks of 16 channels and 16
-// states (pairs are then loaded whole).
+// Calls f(true) if a kernel with per_lane states in a lane has no place without
+// a state or a channel (pairs are then loaded whole).
 template <class F>
-inline ps_status with_full(const ps_scan_input *in, F f) {
-    if (in->channels / in->groups % kScanChannels == 0u && in->states % 16u == 0u) return f(std::true_type());
+inline ps_status with_full(const ps_scan_input *in, uint32_t per_lane, F f) {
+    if (scan_whole(in->channels / in->groups, in->states, per_lane)) return f(std::true_type());
     return f(std::false_type());
 }
 
-// Calls f with the states of a lane (a power of two >= states / 16).
+// Calls f with the states of a lane.
 template <class F>
 inline ps_status with_states(uint32_t states, F f) {
-    if (states <= 16u) return f(std::integral_constant<int, 1>());
-    if (states <= 32u) return f(std::integral_constant<int, 2>());
-    if (states <= 64u) return f(std::integral_constant<int, 4>());
-    if (states <= 128u) return f(std::integral_constant<int, 8>());
-    return f(std::integral_constant<int, 16>());
+    switch (scan_states_per_lane(states)) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    default: return f(std::integral_constant<int, 16>());
+    }
 }
 
 constexpr uint64_t kScanMaxGrid = 0x7FFFFFFFull;

@@ -497,7 +497,7 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
             float *carry = split ? ws_at<float>(ws, carry_at) : nullptr;
             float *steps = split ? ws_at<float>(ws, steps_at) : nullptr;
             uint32_t *links = split ? ws_at<uint32_t>(ws, links_at) : nullptr;
-            return with_full(in, [&](auto full) {
+            return with_full(in, S, [&](auto full) {
                 constexpr bool FULL = decltype(full)::value;
                 timing_begin(s);
                 if (split) {

@@ -703,7 +703,7 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
         timing_begin(s);
         if (grid && cells > 1u) {
             with_states(in->states, [&](auto sc) {
-                return with_full(in, [&](auto full) {
+                return with_full(in, decltype(sc)::value, [&](auto full) {
                     hipLaunchKernelGGL((scan_back_kernel<T, decltype(sc)::value, decltype(full)::value>),
                                        dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a, static_cast<const T *>(dout),
                                        carry, steps, links, o.ranges, o.per_range);
@@ -714,7 +714,8 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
         }
         if (grid) {
             const uint32_t held = in->states > 16u ? per_range : 2u;
-            with_full(in, [&](auto full) {
+            // this kernel takes the states 16 at a time
+            with_full(in, (uint32_t)ceil_div(in->states, kScanLanes), [&](auto full) {
                 auto launch = [&](auto many) {
                     hipLaunchKernelGGL((scan_grad_kernel<T, decltype(full)::value, decltype(many)::value>),
                                        dim3((uint32_t)grid), dim3(2 * kScanThreads),

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import block_ref as ref
+import scan_bound
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000000  # a 256-byte aligned "device" address, never dereferenced
@@ -81,6 +82,38 @@ def test_pieces(tmp_path):
                     os.path.join(ROOT, "tests", "c", "pieces_model.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0 and " 0 violations" in r.stdout, r.stdout + r.stderr
+
+
+def _run_model(tmp_path, name):
+    exe = str(tmp_path / name)
+    subprocess.run(["g++", "-O1", "-g", "-fsanitize=undefined,address", "-std=c++17", "-Wall", "-Wextra", "-Werror",
+                    "-I" + os.path.join(ROOT, "device_wide_prefix_chained_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "c", name + ".cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0 and " 0 violations" in r.stdout, r.stdout + r.stderr
+
+
+def test_scan_shape(tmp_path):
+    """A kernel without bounds has a state and a channel in every place, for
+    all numbers of states that the scan takes."""
+    _run_model(tmp_path, "scan_shape_model")
+
+
+def test_bounded_scan_is_the_oracle():
+    """scan_bound's values are block_ref's, and its bounds are those of an
+    arithmetic with 24 bits: small next to the values, and zero nowhere that
+    something is computed."""
+    off = torch.tensor([0, 3, 3, 40])
+    a, r = _scan_inputs(40, 6, 2, 5, 4)
+    a["initial"] = r(3, 6, 5)
+    dout = r(40, 6)
+    want = ref.scan(**a, offsets=off, dout=dout)
+    got, bound = scan_bound.scan(**a, offsets=off, dout=dout)
+    assert set(got) == set(want) == set(bound)
+    for name in want:
+        size = want[name].abs().mean()
+        assert torch.allclose(got[name], want[name], rtol=1e-12, atol=1e-12 * float(size)), name
+        assert 0 < float(bound[name].mean()) < 2.0 ** -10 * float(size), name
 
 
 # ---------------------------------------------------------------------------

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import block_ref as ref
+import scan_bound
 from gpu_util import require_gpu, say
 
 pytestmark = pytest.mark.gpu
@@ -189,6 +190,69 @@ def test_scan(dw, case):
         assert (getattr(g, name) is not None) == there
         if there and name != "dz":
             ref.close(name, getattr(g, name), want[name], mag[name], K)
+
+
+# Groups of whole blocks of 16 channels.  Numbers of states that are a multiple
+# of 16 and no power of two leave places of a lane without a state; those that
+# are 16 times a power of two run the kernels without bounds.  The strided
+# cases' rows lie between NaN, so a state past the last shows.
+SCAN_WHOLE = [  # as SCAN
+    (100, [0, 1, 1, 40, 100], 32, 1, 48, BF16, True, "Dzb", True),
+    (100, None, 64, 2, 80, F32, True, "Dzb", True),
+    (97, [0, 31, 32, 97], 64, 2, 96, F16, False, "Dz", False),
+    (100, [0, 65, 100], 16, 1, 112, F32, True, "b", True),
+    (70, [0, 33, 33, 70], 32, 2, 144, F32, False, "Dzb", False),
+    (70, [0, 33, 70], 32, 2, 240, BF16, True, "Dzb", True),
+    (70, [5, 33, 66], 16, 1, 240, F32, True, "zb", True),
+    (100, [0, 1, 1, 40, 100], 64, 2, 16, F32, True, "Dzb", True),
+    (100, [0, 1, 1, 40, 100], 64, 4, 32, F32, True, "Dzb", True),
+    (130, [0, 31, 32, 96, 96, 130], 128, 2, 64, BF16, True, "Dzb", True),
+    (70, [0, 33, 70], 64, 4, 128, F32, True, "Dzb", False),
+    (70, None, 32, 2, 256, F16, True, "Dzb", True),
+    # cells of sequences side by side
+    (2500, [0, 2, 1500, 1500, 2500], 16, 1, 48, F32, True, "Dzb", True),
+    (2500, None, 32, 2, 80, BF16, False, "Dzb", True),
+    (2500, [0, 2, 1500, 1500, 2500], 32, 2, 16, F32, True, "Dzb", True),
+    (2500, None, 32, 2, 32, BF16, True, "zb", True),
+    (2500, [0, 700, 2500], 16, 1, 64, F32, True, "Dzb", True),
+    (2500, [0, 700, 2500], 16, 1, 128, F16, True, "Dzb", False),
+]
+
+
+@pytest.mark.parametrize("case", SCAN_WHOLE, ids=str)
+def test_scan_whole_channel_blocks(dw, case):
+    """Every result against 64 bits, within a bound carried along with the
+    values (scan_bound)."""
+    T, cuts, ch, G, N, dtype, initial, extra, wide = case
+    say("scan, whole channel blocks", case)
+    m = Maker(T + ch + N, dtype, wide)
+    off = _offsets(cuts)
+    seqs = 1 if cuts is None else len(cuts) - 1
+    a, more = _scan_inputs(m, T, ch, G, N, seqs, initial, extra)
+    dout = m.act(T, ch, packed=True)
+    out = torch.full((T, ch), 7.0, dtype=dtype, device="cuda")
+    final = torch.full((seqs, ch, N), 7.0, device="cuda")
+    kept = torch.full((dw.ps_selective_scan_checkpoint_rows(T, N), ch, N), float("nan"), device="cuda")
+    dw.ps_selective_scan(**a, **more, offsets=off, out=out, final=final, checkpoints=kept)
+    g = dw.ps_selective_scan_bwd(*a.values(), dout, kept, **more, offsets=off)
+    torch.cuda.synchronize()
+    want, bound = scan_bound.scan(**a, **more, offsets=off, dout=dout)
+    rows = _finite_rows(cuts, T)
+    outside = torch.ones(T, dtype=torch.bool)
+    outside[rows] = False
+    assert (out.cpu()[outside] == 7.0).all()
+    scan_bound.close("out", out[rows], want["out"][rows], bound["out"][rows])
+    scan_bound.close("final", final, want["final"], bound["final"])
+    for name in g._fields:
+        got, by_row = getattr(g, name), name in ("dx", "ddt", "dz", "dB", "dC")
+        given = {"dD": "D" in extra, "dz": "z" in extra, "ddt_bias": "b" in extra, "dinitial": initial}
+        assert (got is not None) == given.get(name, True)
+        if got is None:
+            continue
+        if by_row:
+            scan_bound.close(name, got[rows], want[name][rows], bound[name][rows])
+        else:
+            scan_bound.close(name, got, want[name], bound[name])
 
 
 @pytest.mark.parametrize("case", [(1, 1, 16, 1, 16, BF16, False, False), (7, 9, 40, 2, 24, F32, True, True),
