@@ -11,6 +11,7 @@
 
 #include "dwps.h"
 #include "host_common.hpp"
+#include "launch_parts.hpp"
 #include "pieces.hpp"
 
 namespace dwps {

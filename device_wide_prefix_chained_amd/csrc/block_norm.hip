@@ -20,6 +20,7 @@ struct NormArgs {
     int64_t y_stride, gate_stride, residual_stride;
     const float *scale, *post, *pre;
     uint32_t tokens, channels;
+    uint32_t first;  // row of the launch's first workgroup
     float eps, inv;  // 1 / channels
 };
 
@@ -94,7 +95,7 @@ template <class T, class R, int K>
 __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a, R *__restrict__ res_out, T *__restrict__ out) {
     constexpr int V = kVec;
     __shared__ float sh[2][1][kMostWaves];
-    const int64_t t = blockIdx.x, C = a.channels;
+    const int64_t t = a.first + blockIdx.x, C = a.channels;
     float q[K][V], r[K][V], sum[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -413,14 +414,17 @@ extern "C" ps_status ps_block_norm(const ps_norm_input *in, void *residual_out, 
         ranges_overlap(out, cells * e, residual_out, cells * re))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const NormArgs a = norm_args(in);
+    NormArgs a = norm_args(in);
     return with_norm_types(in, [&](auto zt, auto zr) {
         using T = decltype(zt);
         using R = decltype(zr);
         return with_shape(in->channels, [&](auto k, uint32_t threads) {
             timing_begin(s);
-            hipLaunchKernelGGL((norm_kernel<T, R, decltype(k)::value>), dim3(a.tokens), dim3(threads), 0, s, a,
-                               static_cast<R *>(residual_out), static_cast<T *>(out));
+            launch_in_parts(a.tokens, 1u, threads, [&](uint32_t first, uint32_t grid) {
+                a.first = first;
+                hipLaunchKernelGGL((norm_kernel<T, R, decltype(k)::value>), dim3(grid), dim3(threads), 0, s, a,
+                                   static_cast<R *>(residual_out), static_cast<T *>(out));
+            });
             timing_end(s);
             return launch_status();
         });

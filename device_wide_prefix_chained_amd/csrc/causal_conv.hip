@@ -23,6 +23,7 @@ struct ConvArgs {
     const uint32_t *offsets;
     int64_t x_stride;
     uint32_t tokens, channels, num_seqs;
+    uint32_t first;      // piece (rows' share, for single tokens) of the launch's first workgroup
     uint32_t shift;      // log2 of the rows of a piece
     uint32_t col_blocks; // workgroups side by side
     uint32_t group;      // of xcd_neighbours
@@ -134,7 +135,7 @@ constexpr int kRows = 4;  // rows loaded ahead
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__restrict__ out, T *__restrict__ fin) {
     const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
-    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, b / a.col_blocks);
+    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, a.first + b / a.col_blocks);
     uint32_t c;
     if (!q.any || !own_channels<V>(a, b % a.col_blocks, c)) return;
     const int64_t C = a.channels;
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, cons
                                                                 uint32_t words) {
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
     const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
-    const uint32_t p = b / a.col_blocks;
+    const uint32_t p = a.first + b / a.col_blocks;
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
     uint32_t c;
     if (!own_channels<V>(a, b % a.col_blocks, c)) return;
@@ -323,7 +324,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, con
     uint32_t c, shared;
     if (!own_channels<V>(a, blockIdx.x % a.col_blocks, c, &shared)) return;
     const int64_t C = a.channels;
-    const uint32_t i0 = blockIdx.x / a.col_blocks * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
+    const uint32_t i0 = (a.first + blockIdx.x / a.col_blocks) * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
     struct Rows {
         RawRow<T, V> x, s[W];
         int64_t slot;
@@ -458,8 +459,6 @@ uint32_t conv_bwd_shift(const ps_conv_input *in) {
     return shift;
 }
 
-constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
-
 uint32_t seqs_of(const ps_conv_input *in) { return in->offsets ? in->num_seqs : 1u; }
 
 }  // namespace
@@ -483,16 +482,18 @@ extern "C" ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *fi
         (in->initial && ranges_overlap(out, out_bytes, in->initial, state_bytes)))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const ConvArgs a = conv_args(in, conv_shift(in));
-    const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
-    if (grid > kMaxGrid) return PS_ERR_SIZE;
-    if (!grid) return PS_OK;
+    ConvArgs a = conv_args(in, conv_shift(in));
+    const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
+    if (!pieces) return PS_OK;
     return with_conv(in, [&](auto zero, auto w, auto v) {
         using T = decltype(zero);
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         timing_begin(s);
-        hipLaunchKernelGGL((conv_kernel<T, V, W>), dim3((uint32_t)grid), dim3(kConvThreads), 0, s, a,
-                           static_cast<T *>(out), W > 1 ? static_cast<T *>(final) : nullptr);
+        launch_in_parts(pieces, a.col_blocks, kConvThreads, [&](uint32_t first, uint32_t grid) {
+            a.first = first;
+            hipLaunchKernelGGL((conv_kernel<T, V, W>), dim3(grid), dim3(kConvThreads), 0, s, a, static_cast<T *>(out),
+                               W > 1 ? static_cast<T *>(final) : nullptr);
+        });
         timing_end(s);
         return launch_status();
     });
@@ -503,9 +504,8 @@ extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_con
     ps_status st = conv_sizes(in, true);
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
-    const ConvArgs a = conv_args(in, conv_bwd_shift(in));
+    ConvArgs a = conv_args(in, conv_bwd_shift(in));
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
-    if (pieces * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
     PlainWs plan;
     const size_t part_at = plan.take(pieces * (in->width + 1u) * in->channels * 4u);
     bool query = false;
@@ -525,10 +525,12 @@ extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_con
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         float *part = ws_at<float>(ws, part_at);
         timing_begin(s);
-        if (pieces)
-            hipLaunchKernelGGL((conv_bwd_kernel<T, V, W>), dim3((uint32_t)(pieces * a.col_blocks)), dim3(kConvThreads), 0,
-                               s, a, static_cast<const T *>(dout), static_cast<T *>(dx),
+        launch_in_parts(pieces, a.col_blocks, kConvThreads, [&](uint32_t first, uint32_t grid) {
+            a.first = first;
+            hipLaunchKernelGGL((conv_bwd_kernel<T, V, W>), dim3(grid), dim3(kConvThreads), 0, s, a,
+                               static_cast<const T *>(dout), static_cast<T *>(dx),
                                W > 1 ? static_cast<T *>(dinitial) : nullptr, part, ws_counter(ws), plan.words());
+        });
         hipLaunchKernelGGL(conv_params_kernel, dim3((uint32_t)ceil_div((uint64_t)(in->width + 1u) * in->channels, 64)),
                            dim3(256), 0, s, part, (uint32_t)pieces, in->width, in->channels, dweight, dbias);
         timing_end(s);
@@ -554,8 +556,7 @@ extern "C" ps_status ps_causal_conv_step(const ps_conv_input *in, const void *st
         return PS_ERR_ALIAS;
     if (!in->tokens) return PS_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const ConvArgs a = conv_args(in, 0u);
-    if (in->tokens * a.col_blocks > kMaxGrid) return PS_ERR_SIZE;
+    ConvArgs a = conv_args(in, 0u);
     // up to 4 rows a workgroup, while 2 waves are left for each SIMD
     const uint64_t share = in->tokens * a.col_blocks / 2048u;
     const uint32_t each = share < 1u ? 1u : share > 4u ? 4u : (uint32_t)share;
@@ -563,9 +564,12 @@ extern "C" ps_status ps_causal_conv_step(const ps_conv_input *in, const void *st
         using T = decltype(zero);
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         timing_begin(s);
-        hipLaunchKernelGGL((conv_step_kernel<T, V, W>), dim3((uint32_t)ceil_div(in->tokens, each) * a.col_blocks),
-                           dim3(kConvThreads), 0, s, a, static_cast<const T *>(state), static_cast<T *>(new_state), slots,
-                           pool, static_cast<T *>(out), each);
+        launch_in_parts(ceil_div(in->tokens, each), a.col_blocks, kConvThreads, [&](uint32_t first, uint32_t grid) {
+            a.first = first;
+            hipLaunchKernelGGL((conv_step_kernel<T, V, W>), dim3(grid), dim3(kConvThreads), 0, s, a,
+                               static_cast<const T *>(state), static_cast<T *>(new_state), slots, pool,
+                               static_cast<T *>(out), each);
+        });
         timing_end(s);
         return launch_status();
     });

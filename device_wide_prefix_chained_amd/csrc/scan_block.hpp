@@ -29,6 +29,7 @@ struct ScanArgs {
     const uint32_t *offsets;
     int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
     uint32_t tokens, channels, groups, states, num_seqs;
+    uint32_t first;            // piece (rows' share, for single tokens) of the launch's first workgroup
     uint32_t shift;            // log2 of the rows of a piece; 32: whole sequences
     uint32_t group_channels;   // channels / groups
     uint32_t group_blocks;     // workgroups of 16 channels in a group
@@ -46,7 +47,7 @@ struct ScanPlace {
 
 __device__ __forceinline__ ScanPlace scan_place(const ScanArgs &a, uint32_t b) {
     ScanPlace w;
-    w.p = b / a.col_blocks;
+    w.p = a.first + b / a.col_blocks;
     const uint32_t cb = b % a.col_blocks;
     w.group = cb / a.group_blocks;
     const uint32_t in_group = cb % a.group_blocks * kScanChannels;
@@ -120,6 +121,10 @@ __device__ __forceinline__ uint32_t inside(uint32_t c, uint32_t have) { return c
 // How far each carry reaches: row 0 unused.
 enum ScanLink : uint32_t { kLinkNone = 0, kLinkStart = 1, kLinkChain = 2 };
 
+// Workgroups side by side for one piece, so that a piece fits a launch.
+constexpr uint64_t kScanMaxBlocks = (1u << 23) - 1u;
+static_assert(kScanMaxBlocks <= kLaunchMostItems / (2 * kScanThreads), "a piece fits a launch");
+
 ScanArgs scan_args(const ps_scan_input *in, uint32_t shift);
 ps_status scan_sizes(const ps_scan_input *in, bool packed);
 ps_status scan_pointers(const ps_scan_input *in);
@@ -151,7 +156,5 @@ inline ps_status with_states(uint32_t states, F f) {
     default: return f(std::integral_constant<int, 16>());
     }
 }
-
-constexpr uint64_t kScanMaxGrid = 0x7FFFFFFFull;
 
 }  // namespace dwps

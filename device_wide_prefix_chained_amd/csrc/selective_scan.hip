@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64) void scan_link_kernel(ScanArgs a, float *__rest
                                                         const float *__restrict__ steps,
                                                         const uint32_t *__restrict__ links, uint32_t cells,
                                                         int backward) {
-    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const int64_t i = (int64_t)(a.first + blockIdx.x) * 64 + threadIdx.x;
     const int64_t DN = (int64_t)a.channels * a.states;
     if (i >= DN) return;
     const uint32_t d = (uint32_t)(i / a.states);
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float 
                                                         T *__restrict__ out, uint32_t lanes, uint32_t blocks,
                                                         uint32_t each) {
     const uint32_t at = blockIdx.x % blocks * 256u + threadIdx.x;
-    const uint32_t i0 = blockIdx.x / blocks * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
+    const uint32_t i0 = (a.first + blockIdx.x / blocks) * each, i1 = i0 + each < a.tokens ? i0 + each : a.tokens;
     const uint32_t N = a.states, own = at / lanes, n = at % lanes * 4u;
     // lanes past the last channel or state work on one that exists and store nothing
     const uint32_t d = own < a.channels ? own : a.channels - 1u;
@@ -417,6 +417,7 @@ ps_status scan_sizes(const ps_scan_input *in, bool packed) {
         in->b_stride < gn || in->c_stride < gn || in->x_stride > kBlockMaxStride || in->dt_stride > kBlockMaxStride ||
         (in->z && in->z_stride > kBlockMaxStride) || in->b_stride > kBlockMaxStride || in->c_stride > kBlockMaxStride)
         return PS_ERR_SIZE;
+    if ((uint64_t)in->groups * ceil_div(in->channels / in->groups, kScanChannels) > kScanMaxBlocks) return PS_ERR_SIZE;
     if (packed && !in->offsets && in->num_seqs > 1u) return PS_ERR_SIZE;
     return PS_OK;
 }
@@ -443,9 +444,11 @@ bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes) {
 
 void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
                       bool backward, hipStream_t s) {
-    const uint64_t grid = ceil_div((uint64_t)a.channels * a.states, 64);
-    hipLaunchKernelGGL(scan_link_kernel, dim3((uint32_t)grid), dim3(64), 0, s, a, carry, steps, links, cells,
-                       backward ? 1 : 0);
+    launch_in_parts(ceil_div((uint64_t)a.channels * a.states, 64), 1u, 64u, [&](uint32_t first, uint32_t grid) {
+        ScanArgs part = a;
+        part.first = first;
+        hipLaunchKernelGGL(scan_link_kernel, dim3(grid), dim3(64), 0, s, part, carry, steps, links, cells, backward ? 1 : 0);
+    });
 }
 
 }  // namespace dwps
@@ -463,7 +466,7 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
     const uint64_t DN = (uint64_t)in->channels * in->states;
-    const ScanArgs a = scan_args(in, scan_shift(in));
+    ScanArgs a = scan_args(in, scan_shift(in));
     const bool split = a.shift < 32u;
     const uint64_t cells = split ? ceil_div(in->tokens, 1ull << a.shift) : 0u;
     PlainWs plan;
@@ -486,9 +489,8 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
         (final && in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)) ||
         (checkpoints && ranges_overlap(checkpoints, mark_bytes, out, out_bytes)))
         return PS_ERR_ALIAS;
-    const uint64_t grid = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift) * a.col_blocks;
-    if (grid > kScanMaxGrid) return PS_ERR_SIZE;
-    if (!grid) return PS_OK;
+    const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
+    if (!pieces) return PS_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
@@ -501,13 +503,19 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
                 constexpr bool FULL = decltype(full)::value;
                 timing_begin(s);
                 if (split) {
-                    hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
-                                       (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links, ws_counter(ws),
-                                       plan.words());
+                    launch_in_parts(pieces, a.col_blocks, 2 * kScanThreads, [&](uint32_t first, uint32_t grid) {
+                        a.first = first;
+                        hipLaunchKernelGGL((scan_walk_kernel<T, S, false, FULL>), dim3(grid), dim3(2 * kScanThreads), 0, s, a,
+                                           (T *)nullptr, (float *)nullptr, (float *)nullptr, carry, steps, links,
+                                           ws_counter(ws), plan.words());
+                    });
                     launch_scan_link(a, carry, steps, links, (uint32_t)cells, false, s);
                 }
-                hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a,
-                                   static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
+                launch_in_parts(pieces, a.col_blocks, 2 * kScanThreads, [&](uint32_t first, uint32_t grid) {
+                    a.first = first;
+                    hipLaunchKernelGGL((scan_walk_kernel<T, S, true, FULL>), dim3(grid), dim3(2 * kScanThreads), 0, s, a,
+                                       static_cast<T *>(out), final, checkpoints, carry, steps, links, (uint32_t *)nullptr, 0u);
+                });
                 timing_end(s);
                 return launch_status();
             });
@@ -534,19 +542,20 @@ extern "C" ps_status ps_selective_scan_step(const ps_scan_input *in, const float
     uint32_t lanes = 1u;
     while (lanes < 64u && lanes * 4u < in->states) lanes *= 2u;
     const uint64_t blocks = ceil_div((uint64_t)in->channels * lanes, 256);
-    if (in->tokens * blocks > kScanMaxGrid) return PS_ERR_SIZE;
     // up to 8 rows a workgroup, while 4 workgroups are left for each CU
     const uint64_t share = in->tokens * blocks / 1024u;
     const uint32_t each = share < 1u ? 1u : share > 8u ? 8u : (uint32_t)share;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const ScanArgs a = scan_args(in, 32u);
+    ScanArgs a = scan_args(in, 32u);
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
         timing_begin(s);
         auto launch = [&](auto vec) {
-            hipLaunchKernelGGL((scan_step_kernel<T, decltype(vec)::value>),
-                               dim3((uint32_t)(ceil_div(in->tokens, each) * blocks)), dim3(256), 0, s, a, state, new_state,
-                               slots, pool, static_cast<T *>(out), lanes, (uint32_t)blocks, each);
+            launch_in_parts(ceil_div(in->tokens, each), blocks, 256u, [&](uint32_t first, uint32_t grid) {
+                a.first = first;
+                hipLaunchKernelGGL((scan_step_kernel<T, decltype(vec)::value>), dim3(grid), dim3(256), 0, s, a, state,
+                                   new_state, slots, pool, static_cast<T *>(out), lanes, (uint32_t)blocks, each);
+            });
         };
         if (in->states % 4u == 0u) launch(std::true_type());
         else launch(std::false_type());

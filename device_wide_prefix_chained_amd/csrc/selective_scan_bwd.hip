@@ -48,7 +48,7 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_back_kernel(ScanArgs a,
                                                                      uint32_t per_range) {
     constexpr int kPlane = kScanChannels * kScanPad;
     __shared__ __attribute__((aligned(16))) float sStep[2][kPlane], sGrad[2][kPlane], sC[16 * S * kScanPad];
-    const uint32_t p = blockIdx.x / (a.groups * ranges), rg = blockIdx.x % (a.groups * ranges);
+    const uint32_t p = a.first + blockIdx.x / (a.groups * ranges), rg = blockIdx.x % (a.groups * ranges);
     const uint32_t group = rg / ranges, range = rg % ranges;
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
     if (!q.any || q.lo != (uint64_t)q.cell << a.shift) return;  // starts inside its cell: nothing enters another
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs
     extern __shared__ float sCell[];    // [channel blocks of the range, or 2][3][kPlane]
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
     // piece by piece of one range, the shorter last ranges at the end
-    const uint32_t pieces = gridDim.x / o.blocks, p = blockIdx.x % pieces, rg = blockIdx.x / pieces;
+    const uint32_t pieces = gridDim.x / o.blocks, p = a.first + blockIdx.x % pieces, rg = blockIdx.x / pieces;
     const uint32_t group = rg % a.groups, range = rg / a.groups;
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
     const uint32_t cb0 = range * o.per_range;
@@ -591,7 +591,7 @@ struct SumJob {
     void *out;
     uint64_t cols;
     uint32_t rows;
-    uint32_t first;   // workgroup
+    uint64_t first;   // workgroup
     uint32_t typed;   // the activations' type, not fp32
     uint32_t guard;   // rows of tokens outside every sequence stay unwritten
 };
@@ -601,13 +601,14 @@ struct SumJobs {
 };
 
 template <class T>
-__global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a) {
+__global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a) {  // a.first: workgroups before these
     __shared__ float s[4][64];
     uint32_t k = 0;
-    while (k + 1u < jobs.count && blockIdx.x >= jobs.job[k + 1u].first) ++k;
+    const uint64_t b = (uint64_t)a.first + blockIdx.x;
+    while (k + 1u < jobs.count && b >= jobs.job[k + 1u].first) ++k;
     const SumJob j = jobs.job[k];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint64_t col = (uint64_t)(blockIdx.x - j.first) * 64u + lane;
+    const uint64_t col = (b - j.first) * 64u + lane;
     float v = col < j.cols ? column_sum(j.part + col, wave, 4u, j.rows, j.cols) : 0.0f;
     s[wave][lane] = v;
     __syncthreads();
@@ -647,7 +648,7 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
     if (st != PS_OK) return st;
     const size_t e = dtype_bytes(in->dtype);
     const uint64_t DN = (uint64_t)in->channels * in->states, GN = (uint64_t)in->groups * in->states;
-    const ScanArgs a = scan_args(in, kScanCellShift);
+    ScanArgs a = scan_args(in, kScanCellShift);
     const uint64_t cells = ceil_div(in->tokens, kScanCell);
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
     const uint32_t per_range = grad_range(a, pieces);
@@ -660,8 +661,6 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
                  links_at = plan.take((cells + 1u) * 4u), pA_at = plan.take(pieces * DN * 4u),
                  pD_at = plan.take(pieces * in->channels * 4u), pb_at = plan.take(pieces * in->channels * 4u),
                  pB_at = plan.take(o.ranges * in->tokens * GN * 4u), pC_at = plan.take(o.ranges * in->tokens * GN * 4u);
-    const uint64_t grid = pieces * o.blocks;
-    if (grid > kScanMaxGrid) return PS_ERR_SIZE;
     bool query = false;
     st = workspace_protocol(ws, ws_bytes, plan.at, &query);
     if (st != PS_OK || query) return st;
@@ -685,7 +684,7 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
     uint64_t at = 0;
     auto add = [&](const float *part, void *out, uint64_t cols, uint64_t rows, bool typed, bool guard) {
         if (!out || !cols) return;
-        jobs.job[jobs.count++] = SumJob{part, out, cols, (uint32_t)rows, (uint32_t)at, typed ? 1u : 0u, guard ? 1u : 0u};
+        jobs.job[jobs.count++] = SumJob{part, out, cols, (uint32_t)rows, at, typed ? 1u : 0u, guard ? 1u : 0u};
         at += ceil_div(cols, 64);
     };
     add(o.part_A, grads->dA, DN, pieces, false, false);
@@ -695,39 +694,44 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
         add(o.part_B, grads->dB, in->tokens * GN, o.ranges, true, true);
         add(o.part_C, grads->dC, in->tokens * GN, o.ranges, true, true);
     }
-    if (at > kScanMaxGrid) return PS_ERR_SIZE;
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
         float *carry = ws_at<float>(ws, carry_at), *steps = ws_at<float>(ws, steps_at);
         uint32_t *links = ws_at<uint32_t>(ws, links_at);
         timing_begin(s);
-        if (grid && cells > 1u) {
+        if (pieces && cells > 1u) {
             with_states(in->states, [&](auto sc) {
                 return with_full(in, decltype(sc)::value, [&](auto full) {
-                    hipLaunchKernelGGL((scan_back_kernel<T, decltype(sc)::value, decltype(full)::value>),
-                                       dim3((uint32_t)grid), dim3(2 * kScanThreads), 0, s, a, static_cast<const T *>(dout),
-                                       carry, steps, links, o.ranges, o.per_range);
+                    launch_in_parts(pieces, o.blocks, 2 * kScanThreads, [&](uint32_t first, uint32_t grid) {
+                        a.first = first;
+                        hipLaunchKernelGGL((scan_back_kernel<T, decltype(sc)::value, decltype(full)::value>), dim3(grid),
+                                           dim3(2 * kScanThreads), 0, s, a, static_cast<const T *>(dout), carry, steps,
+                                           links, o.ranges, o.per_range);
+                    });
                     return PS_OK;
                 });
             });
             launch_scan_link(a, carry, steps, links, (uint32_t)cells, true, s);
         }
-        if (grid) {
-            const uint32_t held = in->states > 16u ? per_range : 2u;
-            // this kernel takes the states 16 at a time
-            with_full(in, (uint32_t)ceil_div(in->states, kScanLanes), [&](auto full) {
-                auto launch = [&](auto many) {
-                    hipLaunchKernelGGL((scan_grad_kernel<T, decltype(full)::value, decltype(many)::value>),
-                                       dim3((uint32_t)grid), dim3(2 * kScanThreads),
-                                       held * 3u * kScanChannels * kScanPad * 4u, s, a, static_cast<const T *>(dout),
-                                       checkpoints, carry, o, ws_counter(ws), plan.words());
-                };
-                if (in->states > 16u) launch(std::true_type());
-                else launch(std::false_type());
-                return PS_OK;
-            });
-        }
-        hipLaunchKernelGGL(scan_sums_kernel<T>, dim3((uint32_t)at), dim3(256), 0, s, jobs, a);
+        const uint32_t held = in->states > 16u ? per_range : 2u;
+        // this kernel takes the states 16 at a time
+        with_full(in, (uint32_t)ceil_div(in->states, kScanLanes), [&](auto full) {
+            auto launch = [&](auto many) {
+                launch_in_parts(pieces, o.blocks, 2 * kScanThreads, [&](uint32_t first, uint32_t grid) {
+                    a.first = first;
+                    hipLaunchKernelGGL((scan_grad_kernel<T, decltype(full)::value, decltype(many)::value>), dim3(grid),
+                                       dim3(2 * kScanThreads), held * 3u * kScanChannels * kScanPad * 4u, s, a,
+                                       static_cast<const T *>(dout), checkpoints, carry, o, ws_counter(ws), plan.words());
+                });
+            };
+            if (in->states > 16u) launch(std::true_type());
+            else launch(std::false_type());
+            return PS_OK;
+        });
+        launch_in_parts(at, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+            a.first = first;
+            hipLaunchKernelGGL(scan_sums_kernel<T>, dim3(grid), dim3(256), 0, s, jobs, a);
+        });
         timing_end(s);
         return launch_status();
     });

@@ -604,8 +604,9 @@ ps_status ps_kernel_timing_read(double *total_ms, uint64_t *launches);
  *  - PS_ERR_SIZE: 0 channels, width outside 1..PS_CONV_MAX_WIDTH, states
  *    outside 1..PS_SCAN_MAX_STATES, channels not a multiple of groups,
  *    2^31 tokens or more, more than 2^24 channels (norms:
- *    PS_NORM_MAX_CHANNELS), 2^24 sequences or more, a stride below the row's
- *    length or above 2^24.
+ *    PS_NORM_MAX_CHANNELS), 2^24 sequences or more, 2^23 blocks or more of up
+ *    to 16 channels of one group (the scan), a stride below the row's length
+ *    or above 2^24.  Work that one launch cannot hold is launched in parts.
  * ------------------------------------------------------------------ */
 #define PS_CONV_MAX_WIDTH 8
 #define PS_SCAN_MAX_STATES 256

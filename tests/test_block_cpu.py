@@ -99,6 +99,11 @@ def test_scan_shape(tmp_path):
     _run_model(tmp_path, "scan_shape_model")
 
 
+def test_launches_in_parts(tmp_path):
+    """More work than one launch can count is launched in parts."""
+    _run_model(tmp_path, "launch_parts_model")
+
+
 def test_bounded_scan_is_the_oracle():
     """scan_bound's values are block_ref's, and its bounds are those of an
     arithmetic with 24 bits: small next to the values, and zero nowhere that
@@ -252,6 +257,33 @@ def test_scan_refuses_more():
     need = ctypes.c_size_t(0)
     assert s(None, ctypes.byref(need), _scan(b, x=None, A=None), None, None, None, None) == 0 and need.value >= 256
     assert w(None, ctypes.byref(need), _scan(b, x=None, A=None), None, None, None, None) == 0 and need.value > 256
+
+
+def test_scan_refuses_more_blocks_than_a_launch_holds():
+    b, L = _mod()
+    big = ctypes.c_size_t(1 << 60)
+    wide = dict(x_stride=1 << 24, dt_stride=1 << 24, z=None, states=1, b_stride=1 << 24, c_stride=1 << 24, tokens=1)
+    for channels, groups, code in ((1 << 23, 1 << 23, SIZE), (1 << 24, 1 << 23, SIZE), ((1 << 23) - 1, (1 << 23) - 1, 0)):
+        a, need = _scan(b, channels=channels, groups=groups, **wide), ctypes.c_size_t(0)
+        assert L.ps_selective_scan(None, ctypes.byref(need), a, None, None, None, None) == code
+        assert L.ps_selective_scan_bwd(None, ctypes.byref(need), a, None, None, None, None) == code
+        if code:
+            assert L.ps_selective_scan(FAKE, ctypes.byref(big), a, _at(10), None, None, None) == code
+            assert L.ps_selective_scan_step(a, _at(10), _at(10), None, 100, _at(11), None) == code
+
+
+def test_size_queries_take_more_than_one_launch_holds():
+    """Sizes inside the documented limits whose work items pass 32 bits."""
+    b, L = _mod()
+    need = ctypes.c_size_t(0)
+    ref_need = ctypes.byref(need)
+    many = dict(offsets=FAKE, num_seqs=(1 << 24) - 1, tokens=(1 << 24) - 1)
+    for channels in (2048, 1 << 14):
+        a = _scan(b, channels=channels, groups=1, x_stride=channels, dt_stride=channels, z_stride=channels, **many)
+        assert L.ps_selective_scan(None, ref_need, a, None, None, None, None) == 0
+        assert L.ps_selective_scan_bwd(None, ref_need, a, None, None, None, None) == 0
+        a = _conv(b, channels=channels, x_stride=channels, **many)
+        assert L.ps_causal_conv_bwd(None, ref_need, a, None, None, None, None, None, None) == 0
 
 
 def _norm(b, **kw):
