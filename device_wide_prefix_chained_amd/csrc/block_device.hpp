@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <type_traits>
 #include <utility>
 
@@ -198,6 +199,23 @@ constexpr int64_t kBlockMaxStride = 1 << 24;
 // Bytes from the first to past the last element of `rows` rows.
 inline size_t rows_bytes(uint64_t rows, int64_t stride, uint64_t row, size_t elem) {
     return rows ? ((rows - 1u) * (uint64_t)stride + row) * elem : 0u;
+}
+
+// An array of a call; NULL or 0 bytes: not there.
+struct Bytes {
+    const void *at;
+    size_t n;
+};
+// Whether an output overlaps an input or another output.
+inline bool outputs_overlap(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+    auto meet = [](const Bytes &a, const Bytes &b) { return a.at && b.at && ranges_overlap(a.at, a.n, b.at, b.n); };
+    for (const Bytes *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Bytes &i : ins)
+            if (meet(*o, i)) return true;
+        for (const Bytes *p = outs.begin(); p != o; ++p)
+            if (meet(*o, *p)) return true;
+    }
+    return false;
 }
 
 // Plain memory of a workspace, handed out in pieces of whole 256 bytes after

@@ -344,12 +344,19 @@ ps_status norm_pointers(const ps_norm_input *in) {
     return PS_OK;
 }
 
-bool norm_overlaps(const ps_norm_input *in, const void *p, size_t bytes) {
-    const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype);
-    return p && (ranges_overlap(p, bytes, in->y, rows_bytes(in->tokens, in->y_stride, in->channels, e)) ||
-                 (in->gate && ranges_overlap(p, bytes, in->gate, rows_bytes(in->tokens, in->gate_stride, in->channels, e))) ||
-                 ranges_overlap(p, bytes, in->residual, rows_bytes(in->tokens, in->residual_stride, in->channels, re)));
-}
+// Bytes of a call's arrays; cells and res: packed rows of the two types.
+struct NormBytes {
+    size_t y, gate, residual, cells, res, weight;
+    explicit NormBytes(const ps_norm_input *in) {
+        const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype), c = in->channels;
+        y = rows_bytes(in->tokens, in->y_stride, c, e);
+        gate = rows_bytes(in->tokens, in->gate_stride, c, e);
+        residual = rows_bytes(in->tokens, in->residual_stride, c, re);
+        cells = in->tokens * c * e;
+        res = in->tokens * c * re;
+        weight = c * 4u;
+    }
+};
 
 NormArgs norm_args(const ps_norm_input *in) {
     NormArgs a{};
@@ -409,9 +416,10 @@ extern "C" ps_status ps_block_norm(const ps_norm_input *in, void *residual_out, 
     const size_t e = dtype_bytes(in->dtype), re = dtype_bytes(in->residual_dtype);
     if (!residual_out || !out) return PS_ERR_NULL;
     if (!aligned(residual_out, re) || !aligned(out, e)) return PS_ERR_ALIGNMENT;
-    const size_t cells = in->tokens * in->channels;
-    if (norm_overlaps(in, residual_out, cells * re) || norm_overlaps(in, out, cells * e) ||
-        ranges_overlap(out, cells * e, residual_out, cells * re))
+    const NormBytes n(in);
+    if (outputs_overlap({{residual_out, n.res}, {out, n.cells}},
+                        {{in->y, n.y}, {in->gate, n.gate}, {in->residual, n.residual}, {in->scale, n.weight},
+                         {in->post_weight, n.weight}, {in->pre_weight, n.weight}}))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
     NormArgs a = norm_args(in);
@@ -448,9 +456,11 @@ extern "C" ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm
         !aligned(grads->dgate, e) || !aligned(grads->dresidual, re) || !aligned(grads->dscale, 4) ||
         !aligned(grads->dpost_weight, 4) || !aligned(grads->dpre_weight, 4))
         return PS_ERR_ALIGNMENT;
-    const size_t cells = in->tokens * in->channels;
-    if (norm_overlaps(in, grads->dy, cells * e) || norm_overlaps(in, grads->dgate, cells * e) ||
-        norm_overlaps(in, grads->dresidual, cells * re))
+    const NormBytes n(in);
+    if (outputs_overlap({{grads->dy, n.cells}, {in->gate ? grads->dgate : nullptr, n.cells}, {grads->dresidual, n.res},
+                         {grads->dscale, n.weight}, {grads->dpost_weight, n.weight}, {grads->dpre_weight, n.weight}},
+                        {{in->y, n.y}, {in->gate, n.gate}, {in->residual, n.residual}, {in->scale, n.weight},
+                         {in->post_weight, n.weight}, {in->pre_weight, n.weight}, {dout, n.cells}, {dresidual_out, n.res}}))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const NormArgs a = norm_args(in);

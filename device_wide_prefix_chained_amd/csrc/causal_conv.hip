@@ -459,7 +459,19 @@ uint32_t conv_bwd_shift(const ps_conv_input *in) {
     return shift;
 }
 
-uint32_t seqs_of(const ps_conv_input *in) { return in->offsets ? in->num_seqs : 1u; }
+// Bytes of a call's arrays; edge: initial, final and dinitial.
+struct ConvBytes {
+    size_t x, out, weight, bias, offsets, edge;
+    explicit ConvBytes(const ps_conv_input *in) {
+        const size_t e = dtype_bytes(in->dtype), c = in->channels;
+        x = rows_bytes(in->tokens, in->x_stride, c, e);
+        out = in->tokens * c * e;
+        weight = c * in->width * 4u;
+        bias = c * 4u;
+        offsets = ((size_t)in->num_seqs + 1u) * 4u;
+        edge = (in->offsets ? in->num_seqs : 1u) * (in->width - 1u) * c * e;
+    }
+};
 
 }  // namespace
 }  // namespace dwps
@@ -473,13 +485,9 @@ extern "C" ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *fi
     const size_t e = dtype_bytes(in->dtype);
     if (in->tokens && !out) return PS_ERR_NULL;
     if (!aligned(out, e) || !aligned(final, e)) return PS_ERR_ALIGNMENT;
-    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
-    const size_t out_bytes = in->tokens * in->channels * e;
-    const size_t state_bytes = (size_t)seqs_of(in) * (in->width - 1u) * in->channels * e;
-    if (ranges_overlap(out, out_bytes, in->x, in_bytes) ||
-        (final && (ranges_overlap(final, state_bytes, in->x, in_bytes) || ranges_overlap(final, state_bytes, out, out_bytes) ||
-                   (in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)))) ||
-        (in->initial && ranges_overlap(out, out_bytes, in->initial, state_bytes)))
+    const ConvBytes n(in);
+    if (outputs_overlap({{out, n.out}, {final, n.edge}},
+                        {{in->x, n.x}, {in->weight, n.weight}, {in->bias, n.bias}, {in->offsets, n.offsets}, {in->initial, n.edge}}))
         return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ConvArgs a = conv_args(in, conv_shift(in));
@@ -516,9 +524,11 @@ extern "C" ps_status ps_causal_conv_bwd(void *ws, size_t *ws_bytes, const ps_con
     if (!aligned(ws, 16) || !aligned(dout, e) || !aligned(dx, e) || !aligned(dweight, 4) || !aligned(dbias, 4) ||
         !aligned(dinitial, e))
         return PS_ERR_ALIGNMENT;
-    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
-    const size_t out_bytes = in->tokens * in->channels * e;
-    if (ranges_overlap(dx, out_bytes, in->x, in_bytes) || ranges_overlap(dx, out_bytes, dout, out_bytes)) return PS_ERR_ALIAS;
+    const ConvBytes n(in);
+    if (outputs_overlap({{dx, n.out}, {dweight, n.weight}, {dbias, n.bias}, {dinitial, n.edge}},
+                        {{in->x, n.x}, {in->weight, n.weight}, {in->bias, n.bias}, {in->offsets, n.offsets},
+                         {in->initial, n.edge}, {dout, n.out}}))
+        return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return with_conv(in, [&](auto zero, auto w, auto v) {
         using T = decltype(zero);
@@ -547,12 +557,11 @@ extern "C" ps_status ps_causal_conv_step(const ps_conv_input *in, const void *st
     if (in->tokens && (!out || (in->width > 1u && pool && (!state || !new_state)))) return PS_ERR_NULL;
     if (!aligned(out, e) || !aligned(state, e) || !aligned(new_state, e) || !aligned(slots, 4)) return PS_ERR_ALIGNMENT;
     if (!slots && in->tokens > pool) return PS_ERR_SIZE;
-    const size_t in_bytes = rows_bytes(in->tokens, in->x_stride, in->channels, e);
-    const size_t out_bytes = in->tokens * in->channels * e;
+    const ConvBytes n(in);
     const size_t state_bytes = (size_t)pool * (in->width - 1u) * in->channels * e;
-    if (ranges_overlap(out, out_bytes, in->x, in_bytes) || ranges_overlap(out, out_bytes, state, state_bytes) ||
-        ranges_overlap(out, out_bytes, new_state, state_bytes) || ranges_overlap(new_state, state_bytes, in->x, in_bytes) ||
-        (state != new_state && ranges_overlap(new_state, state_bytes, state, state_bytes)))
+    if (outputs_overlap({{out, n.out}, {new_state, state_bytes}},
+                        {{in->x, n.x}, {in->weight, n.weight}, {in->bias, n.bias}, {slots, in->tokens * 4u},
+                         {state != new_state ? state : nullptr, state_bytes}}))
         return PS_ERR_ALIAS;
     if (!in->tokens) return PS_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -128,8 +128,26 @@ static_assert(kScanMaxBlocks <= kLaunchMostItems / (2 * kScanThreads), "a piece 
 ScanArgs scan_args(const ps_scan_input *in, uint32_t shift);
 ps_status scan_sizes(const ps_scan_input *in, bool packed);
 ps_status scan_pointers(const ps_scan_input *in);
-// Whether bytes at p overlap one of the call's token arrays (p may be NULL).
-bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes);
+// Bytes of a call's arrays; cells and bc: packed rows of x's and B's shape,
+// edge: initial, final and dinitial.
+struct ScanBytes {
+    size_t x, dt, z, B, C, cells, bc, A, channel, offsets, edge, marks;
+    explicit ScanBytes(const ps_scan_input *in) {
+        const size_t e = dtype_bytes(in->dtype), c = in->channels, gn = (size_t)in->groups * in->states;
+        x = rows_bytes(in->tokens, in->x_stride, c, e);
+        dt = rows_bytes(in->tokens, in->dt_stride, c, e);
+        z = rows_bytes(in->tokens, in->z_stride, c, e);
+        B = rows_bytes(in->tokens, in->b_stride, gn, e);
+        C = rows_bytes(in->tokens, in->c_stride, gn, e);
+        cells = in->tokens * c * e;
+        bc = in->tokens * gn * e;
+        A = c * in->states * 4u;
+        channel = c * 4u;
+        offsets = ((size_t)in->num_seqs + 1u) * 4u;
+        edge = (in->offsets ? in->num_seqs : 1u) * A;
+        marks = ceil_div(in->tokens, kScanCell) * A;
+    }
+};
 
 // Carries from cell to cell (forward: entering each cell from the left, in
 // increasing order; backward: from the right): carry[c] = part[c] +

@@ -432,16 +432,6 @@ ps_status scan_pointers(const ps_scan_input *in) {
     return PS_OK;
 }
 
-bool scan_overlaps(const ps_scan_input *in, const void *p, size_t bytes) {
-    const size_t e = dtype_bytes(in->dtype);
-    const uint64_t gn = (uint64_t)in->groups * in->states;
-    return p && (ranges_overlap(p, bytes, in->x, rows_bytes(in->tokens, in->x_stride, in->channels, e)) ||
-                 ranges_overlap(p, bytes, in->dt, rows_bytes(in->tokens, in->dt_stride, in->channels, e)) ||
-                 (in->z && ranges_overlap(p, bytes, in->z, rows_bytes(in->tokens, in->z_stride, in->channels, e))) ||
-                 ranges_overlap(p, bytes, in->B, rows_bytes(in->tokens, in->b_stride, gn, e)) ||
-                 ranges_overlap(p, bytes, in->C, rows_bytes(in->tokens, in->c_stride, gn, e)));
-}
-
 void launch_scan_link(const ScanArgs &a, float *carry, const float *steps, const uint32_t *links, uint32_t cells,
                       bool backward, hipStream_t s) {
     launch_in_parts(ceil_div((uint64_t)a.channels * a.states, 64), 1u, 64u, [&](uint32_t first, uint32_t grid) {
@@ -482,12 +472,10 @@ extern "C" ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan
     if ((st = scan_pointers(in)) != PS_OK) return st;
     if (in->tokens && !out) return PS_ERR_NULL;
     if (!aligned(ws, 16) || !aligned(out, e) || !aligned(final, 4) || !aligned(checkpoints, 4)) return PS_ERR_ALIGNMENT;
-    const size_t out_bytes = in->tokens * in->channels * e, state_bytes = (size_t)a.num_seqs * DN * 4u;
-    const size_t mark_bytes = ceil_div(in->tokens, kScanCell) * DN * 4u;
-    if (scan_overlaps(in, out, out_bytes) || scan_overlaps(in, final, state_bytes) ||
-        scan_overlaps(in, checkpoints, mark_bytes) || (final && ranges_overlap(final, state_bytes, out, out_bytes)) ||
-        (final && in->initial && ranges_overlap(final, state_bytes, in->initial, state_bytes)) ||
-        (checkpoints && ranges_overlap(checkpoints, mark_bytes, out, out_bytes)))
+    const ScanBytes n(in);
+    if (outputs_overlap({{out, n.cells}, {final, n.edge}, {checkpoints, n.marks}},
+                        {{in->x, n.x}, {in->dt, n.dt}, {in->z, n.z}, {in->B, n.B}, {in->C, n.C}, {in->A, n.A},
+                         {in->D, n.channel}, {in->dt_bias, n.channel}, {in->offsets, n.offsets}, {in->initial, n.edge}}))
         return PS_ERR_ALIAS;
     const uint64_t pieces = piece_count(in->tokens, a.num_seqs, in->offsets != nullptr, a.shift);
     if (!pieces) return PS_OK;
@@ -532,11 +520,12 @@ extern "C" ps_status ps_selective_scan_step(const ps_scan_input *in, const float
     if (in->tokens && (!out || (pool && (!state || !new_state)))) return PS_ERR_NULL;
     if (!aligned(out, e) || !aligned(state, 4) || !aligned(new_state, 4) || !aligned(slots, 4)) return PS_ERR_ALIGNMENT;
     if (!slots && in->tokens > pool) return PS_ERR_SIZE;
-    const size_t out_bytes = in->tokens * in->channels * e;
-    const size_t state_bytes = (size_t)pool * in->channels * in->states * 4u;
-    if (scan_overlaps(in, out, out_bytes) || scan_overlaps(in, new_state, state_bytes) ||
-        ranges_overlap(out, out_bytes, state, state_bytes) || ranges_overlap(out, out_bytes, new_state, state_bytes) ||
-        (state != new_state && ranges_overlap(new_state, state_bytes, state, state_bytes)))
+    const ScanBytes n(in);
+    const size_t state_bytes = pool * n.A;
+    if (outputs_overlap({{out, n.cells}, {new_state, state_bytes}},
+                        {{in->x, n.x}, {in->dt, n.dt}, {in->z, n.z}, {in->B, n.B}, {in->C, n.C}, {in->A, n.A},
+                         {in->D, n.channel}, {in->dt_bias, n.channel}, {slots, in->tokens * 4u},
+                         {state != new_state ? state : nullptr, state_bytes}}))
         return PS_ERR_ALIAS;
     if (!in->tokens) return PS_OK;
     uint32_t lanes = 1u;

@@ -671,11 +671,14 @@ extern "C" ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_
         !aligned(grads->ddt, e) || !aligned(grads->dz, e) || !aligned(grads->dB, e) || !aligned(grads->dC, e) ||
         !aligned(grads->dA, 4) || !aligned(grads->dD, 4) || !aligned(grads->ddt_bias, 4) || !aligned(grads->dinitial, 4))
         return PS_ERR_ALIGNMENT;
-    const size_t cell_bytes = in->tokens * in->channels * e, bc_bytes = in->tokens * GN * e;
-    for (const void *p : {grads->dx, grads->ddt, grads->dz})
-        if (scan_overlaps(in, p, cell_bytes) || (p && ranges_overlap(p, cell_bytes, dout, cell_bytes))) return PS_ERR_ALIAS;
-    for (const void *p : {grads->dB, grads->dC})
-        if (scan_overlaps(in, p, bc_bytes) || (p && ranges_overlap(p, bc_bytes, dout, cell_bytes))) return PS_ERR_ALIAS;
+    const ScanBytes n(in);
+    if (outputs_overlap({{grads->dx, n.cells}, {grads->ddt, n.cells}, {in->z ? grads->dz : nullptr, n.cells},
+                         {grads->dB, n.bc}, {grads->dC, n.bc}, {grads->dA, n.A}, {grads->dD, n.channel},
+                         {grads->ddt_bias, n.channel}, {grads->dinitial, n.edge}},
+                        {{in->x, n.x}, {in->dt, n.dt}, {in->z, n.z}, {in->B, n.B}, {in->C, n.C}, {in->A, n.A},
+                         {in->D, n.channel}, {in->dt_bias, n.channel}, {in->offsets, n.offsets}, {in->initial, n.edge},
+                         {dout, n.cells}, {checkpoints, n.marks}}))
+        return PS_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
     o.dx = grads->dx, o.ddt = grads->ddt, o.dz = in->z ? grads->dz : nullptr, o.dinitial = grads->dinitial;
     o.part_A = ws_at<float>(ws, pA_at), o.part_D = ws_at<float>(ws, pD_at), o.part_bias = ws_at<float>(ws, pb_at);

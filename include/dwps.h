@@ -594,9 +594,9 @@ ps_status ps_kernel_timing_read(double *total_ms, uint64_t *launches);
  *    included.
  *  - Sums over tokens or channels are formed in a fixed order: the same call
  *    gives the same bits.
- *  - No output may overlap an input or another output, but for the step
- *    calls' new_state, which may be the state itself (else PS_ERR_ALIAS for
- *    the main arrays).
+ *  - No output may overlap an input or another output (PS_ERR_ALIAS), but
+ *    for the step calls' new_state, which may be the state itself.  A strided
+ *    array counts from its first row to its last.
  *  - Calls with a workspace use it as plain memory (it need not be prepared,
  *    and a prepared one stays ready for the scans).  They follow the same
  *    two-call pattern; pointers of the structs are not looked at in the size

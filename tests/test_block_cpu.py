@@ -329,6 +329,63 @@ def test_norm_refuses_more():
     assert w(FAKE, ctypes.byref(big), a, _at(12), _at(13), b._NormGrads(_at(1), _at(21), _at(22)), None) == ALIAS
 
 
+# Every output of an entry point laid over every input and every other output.
+# The arrays of a call stand at places of their own (_at); a case moves one.
+def _alias_calls():
+    b, L = _mod()
+    big = ctypes.byref(ctypes.c_size_t(GB))
+
+    def conv(at):
+        return _conv(b, x=at["x"], weight=at["weight"], bias=at["bias"], offsets=at["offsets"], initial=at["initial"],
+                     num_seqs=3)
+
+    def scan(at):
+        return _scan(b, **{k: at[k] for k in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "offsets", "initial")}, num_seqs=3)
+
+    def norm(at):
+        return _norm(b, **{k: at[k] for k in ("y", "gate", "residual", "scale", "post_weight", "pre_weight")})
+    conv_in = ("x", "weight", "bias", "offsets", "initial")
+    step_in = ("x", "weight", "bias", "state", "slots")
+    scan_in = ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "offsets", "initial")
+    scan_grads = ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dinitial")
+    norm_in = ("y", "gate", "residual", "scale", "post_weight", "pre_weight")
+    norm_grads = ("dy", "dgate", "dresidual", "dscale", "dpost_weight", "dpre_weight")
+    off = dict(offsets=None, initial=None)
+    return {
+        "conv": (conv_in, ("out", "final"), lambda at: L.ps_causal_conv(conv(at), at["out"], at["final"], None)),
+        "conv_bwd": (conv_in + ("dout",), ("dx", "dweight", "dbias", "dinitial"),
+                     lambda at: L.ps_causal_conv_bwd(FAKE, big, conv(at), at["dout"], at["dx"], at["dweight"], at["dbias"],
+                                                     at["dinitial"], None)),
+        "conv_step": (step_in, ("out", "new_state"),
+                      lambda at: L.ps_causal_conv_step(conv(dict(at, **off)), at["state"], at["new_state"], at["slots"], 100,
+                                                       at["out"], None)),
+        "scan": (scan_in, ("out", "final", "checkpoints"),
+                 lambda at: L.ps_selective_scan(FAKE, big, scan(at), at["out"], at["final"], at["checkpoints"], None)),
+        "scan_bwd": (scan_in + ("dout", "checkpoints"), scan_grads,
+                     lambda at: L.ps_selective_scan_bwd(FAKE, big, scan(at), at["dout"], at["checkpoints"],
+                                                        b._ScanGrads(**{k: at[k] for k in scan_grads}), None)),
+        "scan_step": (scan_in[:8] + ("state", "slots"), ("out", "new_state"),
+                      lambda at: L.ps_selective_scan_step(scan(dict(at, **off)), at["state"], at["new_state"], at["slots"], 100,
+                                                          at["out"], None)),
+        "norm": (norm_in, ("residual_out", "out"), lambda at: L.ps_block_norm(norm(at), at["residual_out"], at["out"], None)),
+        "norm_bwd": (norm_in + ("dout", "dresidual_out"), norm_grads,
+                     lambda at: L.ps_block_norm_bwd(FAKE, big, norm(at), at["dout"], at["dresidual_out"],
+                                                    b._NormGrads(**{k: at[k] for k in norm_grads}), None)),
+    }
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_bwd", "conv_step", "scan", "scan_bwd", "scan_step", "norm", "norm_bwd"])
+def test_overlaps_are_refused(name):
+    ins, outs, call = _alias_calls()[name]
+    place = {n: _at(1 + i) for i, n in enumerate(ins + outs)}
+    for o in outs:
+        for other in ins + outs:
+            if other != o:
+                # 8 bytes into the other array: never the state itself
+                assert call(dict(place, **{o: place[other] + 8})) == ALIAS, (o, other)
+                assert call(dict(place, **{other: place[o] + 8})) == ALIAS, (o, other)
+
+
 def test_structs_have_the_headers_layout(tmp_path):
     """sizeof and the last member's offset of every struct, C against ctypes."""
     b, _ = _mod()
