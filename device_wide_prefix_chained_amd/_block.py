@@ -141,6 +141,15 @@ def _row_stride(name, t):
     return t.stride(0)
 
 
+def _shape(name, t, dims, of):
+    """The shape of a tensor that gives the call sizes: `dims` dimensions, `of`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != dims:
+        raise ValueError("%s must be %s" % (name, of))
+    return t.shape
+
+
 def _first(name, t):
     """The activation the others are compared with ([tokens, channels])."""
     if not isinstance(t, torch.Tensor):
@@ -247,9 +256,7 @@ def _conv_input(x, weight, bias, offsets, initial):
     stride = _first("x", x)
     code = _type_of("x", x)
     tokens, channels = x.shape
-    if weight.dim() != 2:
-        raise ValueError("weight must be [channels, width]")
-    width = weight.shape[1]
+    width = _shape("weight", weight, 2, "[channels, width]")[1]
     w = _packed("weight", weight, x, (channels, width), f32)
     b = _packed("bias", bias, x, (channels,), f32)
     off, seqs = _sequences(offsets, x)
@@ -288,7 +295,7 @@ def ps_causal_conv_step(x, state, weight, bias=None, *, slots=None, new_state=No
     - 1, channels] holds each sequence's last rows, row i's in slot slots[i].
     The rows after the token go to ``new_state`` (default: state itself)."""
     a = _conv_input(x, weight, bias, None, None)
-    pool = state.shape[0]
+    pool = _shape("state", state, 3, "[pool, width - 1, channels]")[0]
     shape = (pool, a.width - 1, a.channels)
     old = _packed("state", state, x, shape, x.dtype)
     new = old if new_state is None else _packed("new_state", new_state, x, shape, x.dtype)
@@ -307,13 +314,12 @@ def _scan_input(x, dt, A, B, C, D, z, dt_bias, offsets, initial):
     xs = _first("x", x)
     code = _type_of("x", x)
     tokens, channels = x.shape
-    if B.dim() != 3 or A.dim() != 2:
-        raise ValueError("A must be [channels, states], B and C [tokens, groups, states]")
-    groups, states = B.shape[1], B.shape[2]
+    _, groups, states = _shape("B", B, 3, "[tokens, groups, states]")
     bc = (tokens, groups, states)
     dts = _same("dt", dt, x, x.shape)
     zs = 0 if z is None else _same("z", z, x, x.shape)
     bs, cs = _same("B", B, x, bc), _same("C", C, x, bc)
+    _shape("A", A, 2, "[channels, states]")
     a = _packed("A", A, x, (channels, states), f32)
     d = _packed("D", D, x, (channels,), f32)
     db = _packed("dt_bias", dt_bias, x, (channels,), f32)
@@ -373,7 +379,7 @@ def ps_selective_scan_step(x, state, dt, A, B, C, *, D=None, z=None, dt_bias=Non
     the token go to ``new_state`` (default: state itself)."""
     a = _scan_input(x, dt, A, B, C, D, z, dt_bias, None, None)
     f32 = torch.float32
-    pool = state.shape[0]
+    pool = _shape("state", state, 3, "[pool, channels, states]")[0]
     shape = (pool, a.channels, a.states)
     old = _packed("state", state, x, shape, f32)
     new = old if new_state is None else _packed("new_state", new_state, x, shape, f32)
@@ -391,6 +397,7 @@ def _norm_input(y, residual, gate, scale, post_weight, pre_weight, eps):
     ys = _first("y", y)
     code = _type_of("y", y)
     tokens, channels = y.shape
+    _shape("residual", residual, 2, "[tokens, channels]")
     rt = residual.dtype
     if rt != y.dtype and rt != f32:
         raise TypeError("residual has dtype %s, expected %s or %s" % (rt, y.dtype, f32))

@@ -411,3 +411,39 @@ def test_binding_refuses_cpu_tensors():
                  lambda: dw.ps_selective_scan_step(x, torch.zeros(4, 8, 2), x, a, bc, bc), lambda: dw.ps_block_norm(x, x)):
         with pytest.raises(ValueError):
             call()
+
+
+class _AsIfOnGpu(torch.Tensor):
+    """A CPU tensor that the binding takes for one of the GPU's."""
+    is_cuda = True
+
+
+@pytest.mark.parametrize("wrong", [None, 3.0, [1.0, 2.0]], ids=str)
+def test_binding_refuses_what_is_no_tensor(wrong):
+    """In every place that the binding looks into before it checks it."""
+    import device_wide_prefix_chained_amd as dw
+    g = lambda *s: torch.zeros(*s).as_subclass(_AsIfOnGpu)  # noqa: E731
+    x, w, a, bc, s = g(4, 8), g(8, 4), g(8, 2), g(4, 1, 2), g(4, 8, 2)
+    for call in (lambda: dw.ps_causal_conv(x, wrong), lambda: dw.ps_causal_conv_bwd(x, wrong, x),
+                 lambda: dw.ps_causal_conv_step(x, s, wrong), lambda: dw.ps_causal_conv_step(x, wrong, w),
+                 lambda: dw.ps_selective_scan(x, x, wrong, bc, bc), lambda: dw.ps_selective_scan(x, x, a, wrong, bc),
+                 lambda: dw.ps_selective_scan(x, x, a, bc, wrong), lambda: dw.ps_selective_scan(x, wrong, a, bc, bc),
+                 lambda: dw.ps_selective_scan_bwd(x, x, wrong, bc, bc, x, s),
+                 lambda: dw.ps_selective_scan_step(x, wrong, x, a, bc, bc),
+                 lambda: dw.ps_selective_scan_step(x, s, x, a, wrong, bc),
+                 lambda: dw.ps_block_norm(x, wrong), lambda: dw.ps_block_norm_bwd(x, wrong, x)):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            call()
+
+
+def test_binding_refuses_wrong_dimensions():
+    import device_wide_prefix_chained_amd as dw
+    g = lambda *s: torch.zeros(*s).as_subclass(_AsIfOnGpu)  # noqa: E731
+    x, w, a, bc, s = g(4, 8), g(8, 4), g(8, 2), g(4, 1, 2), g(4, 8, 2)
+    for call in (lambda: dw.ps_causal_conv(x, g(8)), lambda: dw.ps_causal_conv_step(x, g(()), w),
+                 lambda: dw.ps_causal_conv_step(x, g(4), w), lambda: dw.ps_selective_scan(x, x, g(8), bc, bc),
+                 lambda: dw.ps_selective_scan(x, x, a, g(4, 2), bc), lambda: dw.ps_selective_scan(x, x, a, bc, g(4, 2)),
+                 lambda: dw.ps_selective_scan_step(x, g(()), x, a, bc, bc),
+                 lambda: dw.ps_selective_scan_step(x, s[0], x, a, bc, bc), lambda: dw.ps_block_norm(x, g(()))):
+        with pytest.raises(ValueError):
+            call()
