@@ -6,6 +6,8 @@ PyTorch supplies device memory and streams.  A call that is given no
 workspace uses one kept per (device, stream), allocated on that stream and
 prepared once with ``ps_workspace_init``, so it is one kernel launch like
 any other and its workspace is never handed to another stream while in use.
+While a graph is captured, such a call gets a workspace from the graph's own
+memory, prepared in the graph; pass one (``new_workspace``) to save that launch.
 Every step of the computation runs in the library's HIP kernels; there is
 no fallback: if the library is missing or a call fails, an exception is
 raised.
@@ -223,15 +225,18 @@ def new_workspace(nbytes, device="cuda", stream=None):
 _WS_CACHE = {}
 
 
-def _cached_workspace(fn, need, t, stream):
+def _cached_workspace(need, t, stream):
+    if torch.cuda.is_current_stream_capturing():
+        # a graph gets one of its own, from its own memory pool: the stream's
+        # may be in use by eager calls while the graph is replayed on another
+        # stream, and goes back to the allocator when a larger call comes
+        return new_workspace(need, t.device, _torch_stream(t.device, stream))
     key = (t.get_device(), _raw_stream(t, stream))
     ws = _WS_CACHE.get(key)
     if ws is not None and ws.numel() >= need:
         return ws
     device = t.device
     ts = _torch_stream(device, stream)
-    if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("%s: pass a workspace (new_workspace) when capturing a graph" % fn)
     # grow geometrically; the old buffer was only ever used on this stream,
     # so the allocator may hand it out again in this stream's order
     size = max(int(need), 1 << 16)
@@ -250,7 +255,7 @@ def _workspace(fn: str, call, t, workspace, stream=None):
     if workspace is None:
         need = ctypes.c_size_t(0)
         _check(fn, call(None, ctypes.byref(need)))
-        workspace = _cached_workspace(fn, int(need.value), t, stream)
+        workspace = _cached_workspace(int(need.value), t, stream)
     else:
         _dev_tensor("workspace", workspace)
     have = ctypes.c_size_t(workspace.numel() * workspace.element_size())

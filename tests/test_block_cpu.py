@@ -447,3 +447,34 @@ def test_binding_refuses_wrong_dimensions():
                  lambda: dw.ps_selective_scan_step(x, s[0], x, a, bc, bc), lambda: dw.ps_block_norm(x, g(()))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_captured_call_does_not_use_the_streams_workspace(monkeypatch):
+    """The workspace kept for a stream is replaced when a larger call comes, so
+    a graph must not hold it."""
+    from device_wide_prefix_chained_amd import _binding as bind
+    made = []
+
+    def new(nbytes, device="cuda", stream=None):
+        made.append(torch.zeros(int(nbytes), dtype=torch.uint8))
+        return made[-1]
+    monkeypatch.setattr(bind, "new_workspace", new)
+    monkeypatch.setattr(bind, "_raw_stream", lambda t, stream: 7)
+    monkeypatch.setattr(bind, "_torch_stream", lambda device, stream: None)
+    monkeypatch.setattr(bind, "_WS_CACHE", {})
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def call(need):
+        def size(ws, have):
+            have._obj.value = need
+            return 0
+        return bind._workspace("ps_scan", size, torch.zeros(1), None)[0]
+    kept = call(1000)
+    assert call(900) is kept
+    capturing[0] = True
+    first, second = call(1000), call(500)
+    assert first is not kept and second is not kept and second is not first
+    assert first.numel() >= 1000 and second.numel() >= 500
+    capturing[0] = False
+    assert call(1000) is kept

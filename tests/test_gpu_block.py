@@ -523,6 +523,49 @@ def test_graph(dw):
             assert torch.equal(x, y)
 
 
+def test_graph_without_a_workspace(dw, orc):
+    """Calls captured without a workspace have one of the graph's own: larger
+    eager calls on the capture's stream, which replace the stream's workspace,
+    and tensors that take its memory change no replay."""
+    import numpy as np
+    import workloads as wl
+    from gpu_util import dev, host
+    args = _train_inputs(15)
+    n = 3 * dw.ps_tile_elements(0) + 7
+    x = wl.full_range_u32(n, seed=78)
+    total = orc.scan_u32(x, "sum", True)[0]
+    d_in, d_out = dev(x), torch.empty(n, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    say("graph without a workspace")
+    want = _train_step(dw, *args)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the stream has a workspace that would do
+        _train_step(dw, *args)
+        dw.ps_scan_single_pass("sum", True, d_in, d_out)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = _train_step(dw, *args)
+        dw.ps_scan_single_pass("sum", True, d_in, d_out)
+    large = [torch.ones(k << 16, dtype=torch.int32, device="cuda") for k in (64, 256, 1024)]
+    torch.cuda.synchronize()
+    for k, big in enumerate(large):
+        say("graph without a workspace, replay", k)
+        with torch.cuda.stream(side):
+            dw.ps_scan_single_pass("sum", True, big, torch.empty_like(big))
+            junk = [torch.full((1 << 16,), -1, dtype=torch.int32, device="cuda") for _ in range(16)]
+        d_out.fill_(0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(d_out), total)
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+        for g, w in zip(_train_step(dw, *args), want):
+            assert torch.equal(g, w)
+        del junk
+
+
 # ---------------------------------------------------------------------------
 # what the binding refuses
 # ---------------------------------------------------------------------------
