@@ -315,10 +315,13 @@ __global__ __launch_bounds__(256) void norm_params_kernel(const float *__restric
     }
 }
 
-// Workgroups that share the rows: as many as the GPU holds at once (12 waves
-// on a CU), up to 4 on a CU.
+constexpr int kBwdWaves = 12;  // of the backward pass on a CU, 3 on each SIMD
+
+// Workgroups that share the rows: as many as the GPU holds at once, up to 4
+// on a CU.
 uint32_t bwd_groups(const ps_norm_input *in) {
-    const uint32_t waves = (uint32_t)ceil_div(in->channels, 64u * kVec), each = 12u / (waves < 12u ? waves : 12u);
+    const uint32_t most = kBwdWaves, waves = (uint32_t)ceil_div(in->channels, 64u * kVec);
+    const uint32_t each = most / (waves < most ? waves : most);
     const uint32_t groups = 256u * (each < 4u ? each : 4u);
     return in->tokens < groups ? (uint32_t)in->tokens : groups;
 }
@@ -379,17 +382,21 @@ ps_status with_shape(uint32_t channels, F f) {
     return f(std::integral_constant<int, 2>(), (uint32_t)ceil_div(channels, 2u * wave) * 64u);
 }
 
-// The same for the backward pass, whose rows and sums over rows take about
-// 150 registers for each vector: f(most threads, vectors per thread,
-// threads), with more than 640 threads (3 waves per SIMD) only where 512 with
-// two vectors do not hold the row.
+// The same for the backward pass: f(most threads, vectors per thread,
+// threads).  A row of one vector a thread and its sums take up to 168
+// registers, of which a SIMD holds 3 waves: one vector up to kBwdWaves, then
+// 512 threads with two (231 registers, no room for the next row), and 1024 with
+// two above 8192 channels, whose 128 registers spill 400 bytes a lane in the
+// row loop.  8192 rows, bf16 with an fp32 residual, us: 5632 channels 208 (two
+// vectors 311), 6144 224 (310), 8192 348, 16384 1685.
 template <class F>
 ps_status with_bwd_shape(uint32_t channels, F f) {
     auto threads = [&](uint32_t k) { return (uint32_t)ceil_div(channels, k * 64u * kVec) * 64u; };
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 2> Two;
     if (channels <= 256u * kVec) return f(std::integral_constant<int, 256>(), One(), threads(1));
-    if (channels <= 640u * kVec) return f(std::integral_constant<int, 640>(), One(), threads(1));
+    constexpr int kMost = 64 * kBwdWaves;
+    if (channels <= (uint32_t)kMost * kVec) return f(std::integral_constant<int, kMost>(), One(), threads(1));
     if (channels <= 1024u * kVec) return f(std::integral_constant<int, 512>(), Two(), threads(2));
     return f(std::integral_constant<int, 1024>(), Two(), threads(2));
 }

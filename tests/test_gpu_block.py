@@ -404,6 +404,21 @@ def test_norm(dw, case):
                 ref.close(name, getattr(g, name), want[key], mag[key], 200 + T)
 
 
+NORM_WIDE = [  # as NORM: rows next to where the gradients change from one vector a thread to two
+    (400, 5128, BF16, F32, "gsop", False),
+    (5, 5127, BF16, BF16, "gsop", True),
+    (600, 6144, F16, F32, "gsop", True),
+    (300, 6144, F32, F32, "so", False),
+    (4, 6143, F32, F32, "gsop", False),
+    (3, 6152, BF16, F32, "gsop", False),
+]
+
+
+@pytest.mark.parametrize("case", NORM_WIDE, ids=str)
+def test_norm_wide_rows(dw, case):
+    test_norm(dw, case)
+
+
 # ---------------------------------------------------------------------------
 # streams, workspaces, graphs
 # ---------------------------------------------------------------------------
