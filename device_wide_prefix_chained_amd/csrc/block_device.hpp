@@ -32,9 +32,9 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw
 
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p by the
 // series of the inverse hyperbolic tangent: with q = e / (2 + e) <= 1/3,
-// log(1 + e) = 2 (q + q^3/3 + q^5/5 + ...); the first term left out, q^15/15,
-// is below 2^-27 of the sum, so small steps (v << 0) keep full precision,
-// which log(1 + e) itself would lose.
+// log(1 + e) = 2 (q + q^3/3 + q^5/5 + ...); the terms left out, from q^15/15
+// on, are below 2^-26 of the sum (at v = 0; a quarter of a rounding), so
+// small steps (v << 0) keep full precision, which log(1 + e) itself would lose.
 __device__ __forceinline__ float softplus(float v) {
     const float e = exp2_hw(__builtin_fabsf(v) * -kLog2e);
     const float q = e * rcp_hw(2.0f + e);

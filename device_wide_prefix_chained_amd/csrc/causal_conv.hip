@@ -26,7 +26,6 @@ struct ConvArgs {
     uint32_t first;      // piece (rows' share, for single tokens) of the launch's first workgroup
     uint32_t shift;      // log2 of the rows of a piece
     uint32_t col_blocks; // workgroups side by side
-    uint32_t group;      // of xcd_neighbours
 };
 
 constexpr int kConvThreads = 64;
@@ -134,10 +133,9 @@ constexpr int kRows = 4;  // rows loaded ahead
 
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__restrict__ out, T *__restrict__ fin) {
-    const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
-    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, a.first + b / a.col_blocks);
+    const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, a.first + blockIdx.x / a.col_blocks);
     uint32_t c;
-    if (!q.any || !own_channels<V>(a, b % a.col_blocks, c)) return;
+    if (!q.any || !own_channels<V>(a, blockIdx.x % a.col_blocks, c)) return;
     const int64_t C = a.channels;
     const T *x = static_cast<const T *>(a.x) + c;
     RawRow<T, V> next[kRows];
@@ -197,11 +195,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, cons
                                                                 float *__restrict__ part, uint32_t *hdr,
                                                                 uint32_t words) {
     if (blockIdx.x == 0 && threadIdx.x == 0) mark_plain(hdr, words);
-    const uint32_t b = xcd_neighbours(blockIdx.x, gridDim.x, a.group);
-    const uint32_t p = a.first + b / a.col_blocks;
+    const uint32_t p = a.first + blockIdx.x / a.col_blocks;
     const Piece q = find_piece(a.offsets, a.num_seqs, a.tokens, a.shift, p);
     uint32_t c;
-    if (!own_channels<V>(a, b % a.col_blocks, c)) return;
+    if (!own_channels<V>(a, blockIdx.x % a.col_blocks, c)) return;
     const int64_t C = a.channels;
     const T *x = static_cast<const T *>(a.x) + c, *gy = dout + c;
     float w[W][V], bias[V], win[W][V], gw[W][V], sum[W + 1][V];
@@ -440,13 +437,13 @@ ConvArgs conv_args(const ps_conv_input *in, uint32_t shift) {
     a.num_seqs = in->offsets ? in->num_seqs : 1u;
     a.shift = shift;
     a.col_blocks = (uint32_t)ceil_div(in->channels, (uint64_t)vec * kConvThreads);
-    a.group = 1u;
     return a;
 }
 
 // Rows of a piece, as a power of two.  Forward: as many (8 to 64) as leave
 // 4096 waves, 4 on each SIMD.  Backward: 32, more where there would be above
-// 512 pieces, each of which leaves width + 1 rows of partial sums.
+// 512 cells.  A piece leaves width + 1 rows of partial sums, and each sequence
+// beyond the cells adds a piece, so many short sequences cost that much more.
 uint32_t conv_shift(const ps_conv_input *in) {
     const uint64_t cols = ceil_div(in->channels, (uint64_t)vec_of(in) * kConvThreads);
     uint32_t shift = 3u;
