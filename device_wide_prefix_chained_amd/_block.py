@@ -277,8 +277,8 @@ def ps_causal_conv(x, weight, bias=None, *, offsets=None, initial=None, out=None
 
 
 def ps_causal_conv_bwd(x, weight, dout, bias=None, *, offsets=None, initial=None, workspace=None, stream=None):
-    """Gradients of ps_causal_conv: ConvGrads(dx, dweight, dbias, dinitial),
-    the last two where there is a bias and an initial."""
+    """Gradients of ps_causal_conv's out: ConvGrads(dx, dweight, dbias,
+    dinitial), the last two where there is a bias and an initial."""
     a = _conv_input(x, weight, bias, offsets, initial)
     g = _packed("dout", dout, x, x.shape, x.dtype)
     new = _Results(x.device, stream)
@@ -356,8 +356,8 @@ def ps_selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, offsets=N
 
 def ps_selective_scan_bwd(x, dt, A, B, C, dout, checkpoints, *, D=None, z=None, dt_bias=None, offsets=None, initial=None,
                           workspace=None, stream=None):
-    """Gradients of ps_selective_scan, from the checkpoints that it wrote for
-    these inputs: ScanGrads, with None for the inputs that are not given."""
+    """Gradients of ps_selective_scan's out, from the checkpoints that it wrote
+    for these inputs: ScanGrads, with None for the inputs that are not given."""
     a = _scan_input(x, dt, A, B, C, D, z, dt_bias, offsets, initial)
     f32 = torch.float32
     g = _packed("dout", dout, x, x.shape, x.dtype)

@@ -90,7 +90,7 @@ __device__ __forceinline__ const T *at_row(const void *p, int64_t t, int64_t str
 __device__ __forceinline__ const float *at_col(const float *p, uint32_t c) { return p ? p + c : nullptr; }
 
 // One row: blockDim.x threads with K times 8 neighbouring channels each.
-// 16384 x 4096, bf16: 128 us (5.2 TB/s); 256 threads with two vectors 151 us.
+// 16384 x 4096, bf16: 129 to 133 us (5 TB/s); 256 threads with two vectors 151 us.
 template <class T, class R, int K>
 __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a, R *__restrict__ res_out, T *__restrict__ out) {
     constexpr int V = kVec;
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a, R *__
 // registers; part[workgroup][dscale, dpost, dpre][channel].  The next row's
 // loads are on their way while one is worked on (WHOLE: rows of whole
 // vectors, one a thread; others load their own).  8192 x 5120, bf16 with an
-// fp32 residual: 175 us and 6 us for the sums (5 TB/s); without the next row
-// on its way and with 20 channels a thread 535 us.
+// fp32 residual: 177 to 191 us and 5 us for the sums (4.7 TB/s or more); without
+// the next row on its way and with 20 channels a thread 535 us.
 
 // Eight activations as they were loaded: 16-bit types stay packed until they
 // are used, so that nothing waits for them before.

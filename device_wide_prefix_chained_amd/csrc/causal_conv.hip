@@ -8,8 +8,8 @@
 // owns 16 bytes of neighbouring channels and walks down a piece of one
 // sequence, the last W rows in registers and the next four on their way, so
 // every row is read once but for the W - 1 rows before each piece.
-// 16384 x 4096 in 13 sequences, bf16, W = 4: 51 us (5.3 TB/s), 60 us a call
-// among others; pieces of 16 to 64 rows and 2 to 8 rows ahead are within 10%.
+// 16384 x 4096 in 13 sequences, bf16, W = 4: 53 us (5.0 TB/s), 55 to 61 us a
+// call among others; pieces of 16 to 64 rows and 2 to 8 rows ahead are within 10%.
 #include <hip/hip_runtime.h>
 
 #include "block_device.hpp"
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_kernel(ConvArgs a, T *__res
 // and the rows before the sequence's first (dinitial) as dx.  A piece walks
 // W - 1 rows past its end for the g its last rows need, and sums dweight and
 // dbias over its own rows into part[piece][k][channel] (k = W: dbias).
-// 6001 x 1537, fp32, W = 3: 26 us and 4 us for the sums over pieces.
+// 6001 x 1537, fp32, W = 3: 28 us and 4 us for the sums over pieces.
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a, const T *__restrict__ dout,
                                                                 T *__restrict__ dx, T *__restrict__ dinit,
@@ -313,7 +313,8 @@ __global__ __launch_bounds__(256) void conv_params_kernel(const float *__restric
 // takes `each` rows, so that the weights, which are as large as the states of
 // a row in fp32, are read once for them.  The state may be updated in place,
 // so every channel has one thread that stores it, and what a thread reads of
-// the others' does not matter.  384 rows x 8192, bf16, W = 4: 10 us (5 TB/s).
+// the others' does not matter.  384 rows x 8192, bf16, W = 4: 15 us (3.4 TB/s),
+// 11 us (4.5 TB/s) with a part of it in the cache.
 template <class T, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, const T *state, T *new_state,
                                                                  const int32_t *__restrict__ slots, uint32_t pool,

@@ -22,8 +22,8 @@ namespace {
 // barrier a block.  The walk is bound by arithmetic: for every state exp2
 // (two issue slots) and 4 more operations (the broadcasts of step and step x
 // are part of the products), and 33 for 16 sums over states.  8191 x 4096 x 16
-// states, bf16, one sequence (a walking wave for each SIMD): 191 us, 77% of the
-// vector issue slots taken; without waves that feed 289 us, without the
+// states, bf16, one sequence (a walking wave for each SIMD): 191 to 207 us, 77%
+// of the vector issue slots taken; without waves that feed 289 us, without the
 // walking waves' priority 215 us.
 template <class T, int S, bool OUT, bool FULL>
 __global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a, T *__restrict__ out,
@@ -246,8 +246,8 @@ __global__ __launch_bounds__(2 * kScanThreads) void scan_walk_kernel(ScanArgs a,
 }
 
 // One (channel, state) per lane, from cell to cell; 256 cells of 2048 x 16 take
-// 28 us (2.4 TB/s, each load 256 bytes of a row of its own).  The loads of 32
-// cells are on their way at once (64 take 26 us, and all registers).
+// 23 us (2.9 TB/s, each load 256 bytes of a row of its own).  The loads of 32
+// cells are on their way at once (64 take all registers, for 7% less).
 __global__ __launch_bounds__(64) void scan_link_kernel(ScanArgs a, float *__restrict__ carry,
                                                         const float *__restrict__ steps,
                                                         const uint32_t *__restrict__ links, uint32_t cells,
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(64) void scan_link_kernel(ScanArgs a, float *__rest
 // `lanes` of them a channel, and a workgroup takes `each` rows: A, as large as
 // a row's states, is read once for them.  Bound by memory, the states once in
 // and once out; the next row's are on their way while one is worked on.
-// 384 rows x 4096 x 16 states: 38 us (5.6 TB/s); one row of 1536 channels: 3 us.
+// 384 rows x 4096 x 16 states: 46 us (4.7 TB/s); one row of 1536 channels: 3 us.
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float *state, float *new_state,
                                                         const int32_t *__restrict__ slots, uint32_t pool,
@@ -373,6 +373,9 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float 
 // sequence (random cuts: (1 + ln seqs) / seqs of the rows) and an even share;
 // cells 1.75 shares and about 30 turns for two more launches, and the link of
 // 32 cells about 4.  Cells are as long as leaves four workgroups for a CU.
+// The lengths are on the device and not looked at: one long sequence among many
+// short ones is walked whole (16384 rows of 512 channels in 41 sequences, one
+// of 16000 rows: 367 us).
 // Both sides in us, bf16, 16 states, one sequence, whole / cells: 16384 rows
 // of 64 channels 358 / 46, 512: 359 / 88, 1024: 361 / 151, 2048: 364 / 273
 // (4096: 387 whole); 256 channels of 4096 rows 91 / 33, 2048: 48 / 29 (1024:

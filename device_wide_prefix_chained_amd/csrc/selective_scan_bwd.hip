@@ -40,7 +40,7 @@ __device__ __forceinline__ f4 four(const float *p) { return *reinterpret_cast<co
 // range of channel blocks; four waves feed the four that walk.  A walk needs
 // exp2 and 3 operations for every state, about as much as the steps and gated
 // gradients that feed it, so the feeding waves are the other half of the work.
-// 8192 x 2048 x 16 states, bf16: 70 us; walking whole sequences took 307 us.
+// 8192 x 2048 x 16 states, bf16: 69 us; walking whole sequences took 307 us.
 template <class T, int S, bool FULL>
 __global__ __launch_bounds__(2 * kScanThreads) void scan_back_kernel(ScanArgs a, const T *__restrict__ dout,
                                                                      float *__restrict__ carry, float *__restrict__ steps,
@@ -220,7 +220,7 @@ __device__ __forceinline__ void fold_rows(float (&o)[8], float (&v)[32]) {
 // 256 registers that two waves per SIMD leave it; what it starts from and
 // leaves goes through shared memory too, since with those loads of its own it
 // spilled and waited for memory in every block (350 to 510 us).
-// 8192 x 2048 x 16 states, bf16: 295 us, 70% of the vector issue slots taken.
+// 8192 x 2048 x 16 states, bf16: 292 us, 70% of the vector issue slots taken.
 template <class T, bool FULL, bool MANY>
 __global__ __launch_bounds__(2 * kScanThreads, 2) void scan_grad_kernel(ScanArgs a, const T *__restrict__ dout,
                                                                         const float *__restrict__ marks,
@@ -625,9 +625,10 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(SumJobs jobs, ScanArgs a
 // Channel blocks that one workgroup goes through: as many as leave about 4
 // rounds of the 256 workgroups that the GPU holds, 16 at most (the sums of dB
 // and dC then leave a workgroup once in 256 channels).  Two rounds, and 4
-// blocks at most, with more than 16 states, whose sums wait in shared memory.  Several ranges are cut so that the last is
-// about half as long: run last, it fills the gaps that whole rounds leave
-// (8192 x 2048, 16 states: 308 us with 8 equal ranges, 293 with 8 and a half).
+// blocks at most, with more than 16 states, whose sums wait in shared memory.
+// Several ranges are cut so that the last is about half as long: run last, it
+// fills the gaps that whole rounds leave (8192 x 2048, 16 states: 308 us with 8
+// equal ranges, 293 with 8 and a half).
 uint32_t grad_range(const ScanArgs &a, uint64_t pieces) {
     const uint64_t fit = pieces * a.groups * a.group_blocks / (a.states > 16u ? 512u : 1024u);
     const uint64_t most = a.states > 16u ? 4u : 16u;

@@ -631,7 +631,7 @@ typedef struct ps_conv_input {
 /* final (optional): [num_seqs, width - 1, channels], the last width - 1 rows
  * of each sequence and its initial rows, the initial of what follows. */
 ps_status ps_causal_conv(const ps_conv_input *in, void *out, void *final, void *stream);
-/* Gradients of out given dout (packed): dx [tokens, channels] and dinitial
+/* Gradients of out (final has none) given dout (packed): dx [tokens, channels] and dinitial
  * [num_seqs, width - 1, channels] in the activations' type, dweight
  * [channels, width] and dbias [channels] in fp32.  dinitial and dbias may be
  * NULL. */
@@ -673,7 +673,7 @@ uint64_t ps_selective_scan_checkpoint_rows(uint64_t tokens, uint32_t states);
  * sequence.  checkpoints (optional): [checkpoint rows, channels, states]. */
 ps_status ps_selective_scan(void *ws, size_t *ws_bytes, const ps_scan_input *in, void *out, float *final,
                             float *checkpoints, void *stream);
-/* Gradients of out given dout (packed), from the checkpoints that
+/* Gradients of out (final has none) given dout (packed), from the checkpoints that
  * ps_selective_scan wrote for the same input: dx, ddt, dz [tokens,
  * channels], dB, dC [tokens, groups, states] in the activations' type; dA
  * [channels, states], dD, ddt_bias [channels], dinitial [num_seqs, channels,
