@@ -41,7 +41,6 @@ thread, timed on the same input, and its output is compared with the GPU's.
 from __future__ import annotations
 
 import argparse
-import glob
 import hashlib
 import json
 import os
@@ -66,19 +65,24 @@ TIMING_EVERY = 5
 
 
 # The source file that holds each workload's main kernel (scan.hip for the
-# rest); its hash, with every shared header, marks the counter summaries under
-# profiles/ taken on it, so that a change to one kernel leaves the others'
-# summaries valid.
+# rest); its hash, with the headers that it includes, marks the counter
+# summaries under profiles/ taken on it, so that a change to one kernel leaves
+# the others' summaries valid.
 KERNEL_FILE = {"segmented": "segscan.hip", "compact": "compact.hip",
                "copy": "common.hip", "read": "common.hip", "write": "common.hip"}
 
 
 def kernel_sources(workload: str):
     csrc = os.path.join(ROOT, "device_wide_prefix_chained_amd", "csrc")
-    files = [os.path.join(csrc, KERNEL_FILE.get(workload, "scan.hip"))]
-    files += sorted(glob.glob(os.path.join(csrc, "*.hpp")))
-    files.append(os.path.join(ROOT, "include", "dwps.h"))
-    return files
+    files, at = [os.path.join(csrc, KERNEL_FILE.get(workload, "scan.hip"))], 0
+    while at < len(files):
+        with open(files[at], encoding="utf-8") as f:
+            names = re.findall(r'^\s*#\s*include\s*"([^"]+)"', f.read(), re.M)
+        for name in names:
+            found = [p for p in (os.path.join(csrc, name), os.path.join(ROOT, "include", name)) if os.path.exists(p)]
+            files += [p for p in found[:1] if p not in files]
+        at += 1
+    return files[:1] + sorted(files[1:])
 
 
 def _code_text(text: str) -> str:

@@ -43,6 +43,19 @@ def test_every_workload_has_its_sources(workload):
     assert any(f.endswith("dwps.h") for f in files) and any(f.endswith("dwps_device.hpp") for f in files)
 
 
+@pytest.mark.parametrize("workload", WORKLOADS)
+def test_sources_are_those_that_are_included(workload):
+    """Headers of the kernels in other files do not count, so a change there
+    leaves a workload's counter summary valid; every header on the way does."""
+    names = [os.path.basename(f) for f in bench.kernel_sources(workload)]
+    assert len(names) == len(set(names))
+    assert not {"scan_block.hpp", "scan_shape.hpp", "block_device.hpp", "pieces.hpp", "launch_parts.hpp"} & set(names)
+    assert {"dwps.h", "host_common.hpp", "dwps_device.hpp", "ws_state.hpp"} <= set(names)
+    if workload not in ("copy", "read", "write"):
+        assert {"pipeline.hpp", "tile_io.hpp", "ws_device.hpp"} <= set(names)
+    assert ("twolevel.hpp" in names) == (names[0] == "scan.hip")
+
+
 def test_kernels_in_different_files_hash_apart():
     h = {w: bench.kernel_source_hash(w) for w in ("u32x", "f32", "segmented", "compact", "copy")}
     assert h["u32x"] == h["f32"]  # one source file
