@@ -42,6 +42,14 @@ class _ScanGrads(ctypes.Structure):
     _fields_ = [(n, _VP) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dinitial")]
 
 
+class _DeltaInput(ctypes.Structure):
+    _fields_ = [("q", _VP), ("k", _VP), ("v", _VP), ("q_stride", _I64), ("k_stride", _I64), ("v_stride", _I64),
+                ("g", _VP), ("beta", _VP), ("g_stride", _I64), ("beta_stride", _I64), ("offsets", _VP),
+                ("initial", _VP), ("tokens", _U64), ("kheads", _U32), ("heads", _U32), ("key_dim", _U32),
+                ("value_dim", _U32), ("num_seqs", _U32), ("dtype", _I32), ("normalize", _I32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class _NormInput(ctypes.Structure):
     _fields_ = [("y", _VP), ("gate", _VP), ("residual", _VP),
                 ("y_stride", _I64), ("gate_stride", _I64), ("residual_stride", _I64),
@@ -96,6 +104,8 @@ def _lib():
             "ps_selective_scan": [_VP, sz, P(_ScanInput), _VP, _VP, _VP, _VP],
             "ps_selective_scan_bwd": [_VP, sz, P(_ScanInput), _VP, _VP, P(_ScanGrads), _VP],
             "ps_selective_scan_step": [P(_ScanInput), _VP, _VP, _VP, _U32, _VP, _VP],
+            "ps_gated_delta": [_VP, sz, P(_DeltaInput), _VP, _VP, _VP, _VP],
+            "ps_gated_delta_step": [P(_DeltaInput), _VP, _VP, _VP, _U32, _VP, _VP],
             "ps_block_norm": [P(_NormInput), _VP, _VP, _VP],
             "ps_block_norm_bwd": [_VP, sz, P(_NormInput), _VP, _VP, P(_NormGrads), _VP],
         }
@@ -104,6 +114,8 @@ def _lib():
             getattr(L, name).restype = _I32
         L.ps_selective_scan_checkpoint_rows.argtypes = [_U64, _U32]
         L.ps_selective_scan_checkpoint_rows.restype = _U64
+        L.ps_gated_delta_checkpoint_floats.argtypes = [_U64, _U32, _U32, _U32, _U32]
+        L.ps_gated_delta_checkpoint_floats.restype = _U64
         _lib_ready = L
     return _lib_ready
 
@@ -386,6 +398,75 @@ def ps_selective_scan_step(x, state, dt, A, B, C, *, D=None, z=None, dt_bias=Non
     o = _Results(x.device, stream).like(x) if out is None else out
     _check("ps_selective_scan_step", _lib().ps_selective_scan_step(
         a, old, new, _slots(slots, x, a.tokens, pool), pool, _packed("out", o, x, x.shape, x.dtype), _stream(x, stream)))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+# ---------------------------------------------------------------------------
+def _delta_input(q, k, v, g, beta, scale, normalize, eps, offsets, initial):
+    f32 = torch.float32
+    tokens, kheads, key_dim = _shape("q", q, 3, "[tokens, kheads, key_dim]")
+    _, heads, value_dim = _shape("v", v, 3, "[tokens, heads, value_dim]")
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    code = _type_of("q", q)
+    qs, ks = _row_stride("q", q), _same("k", k, q, q.shape)
+    vs = _same("v", v, q, (tokens, heads, value_dim))
+    gs, bs = (_same(n, t, q, (tokens, heads), f32) for n, t in (("g", g), ("beta", beta)))
+    off, seqs = _sequences(offsets, q)
+    init = _packed("initial", initial, q, (seqs, heads, key_dim, value_dim), f32)
+    if scale is None:
+        scale = key_dim ** -0.5 if key_dim else 1.0
+    return _DeltaInput(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, g.data_ptr(), beta.data_ptr(), gs, bs,
+                       off, init, tokens, kheads, heads, key_dim, value_dim, seqs, code, bool(normalize), scale, eps)
+
+
+def ps_gated_delta_checkpoint_floats(tokens: int, num_seqs: int, heads: int, key_dim: int, value_dim: int) -> int:
+    """Floats of the ``checkpoints`` of a forward call that a backward call
+    follows."""
+    return int(_lib().ps_gated_delta_checkpoint_floats(int(tokens), int(num_seqs), int(heads), int(key_dim),
+                                                       int(value_dim)))
+
+
+def _delta_checkpoints(t, like, a):
+    n = ps_gated_delta_checkpoint_floats(a.tokens, a.num_seqs, a.heads, a.key_dim, a.value_dim)
+    return _packed("checkpoints", t, like, (n,), torch.float32)
+
+
+def ps_gated_delta(q, k, v, g, beta, *, scale=None, normalize=False, eps=1e-6, offsets=None, initial=None, out=None,
+                   final=None, checkpoints=None, workspace=None, stream=None):
+    """The gated delta rule of q and k [tokens, kheads, key_dim], v [tokens,
+    heads, value_dim], log decays g and strengths beta [tokens, heads]
+    (float32): out (and ``final`` [num_seqs, heads, key_dim, value_dim], the
+    states after each sequence; ``checkpoints``, what ps_gated_delta_bwd
+    starts from).  ``scale`` defaults to key_dim ** -0.5; ``normalize``
+    divides q and k by their lengths first."""
+    a = _delta_input(q, k, v, g, beta, scale, normalize, eps, offsets, initial)
+    o = _Results(q.device, stream)(v.shape, v.dtype) if out is None else out
+    to = _packed("out", o, q, v.shape, v.dtype)
+    fin = _packed("final", final, q, (a.num_seqs, a.heads, a.key_dim, a.value_dim), torch.float32)
+    kept = None if checkpoints is None else _delta_checkpoints(checkpoints, q, a)
+    s, f = _stream(q, stream), _lib().ps_gated_delta
+    _with_workspace("ps_gated_delta", lambda ws, wsb: f(ws, wsb, a, to, fin, kept, s), q, workspace, stream)
+    return o
+
+
+def ps_gated_delta_step(q, k, v, state, g, beta, *, scale=None, normalize=False, eps=1e-6, slots=None, new_state=None,
+                        out=None, stream=None):
+    """One token for each row of q, k [batch, kheads, key_dim] and v [batch,
+    heads, value_dim]; ``state`` [pool, heads, key_dim, value_dim] in float32,
+    row i's in slot slots[i].  The states after the token go to ``new_state``
+    (default: state itself)."""
+    a = _delta_input(q, k, v, g, beta, scale, normalize, eps, None, None)
+    f32 = torch.float32
+    pool = _shape("state", state, 4, "[pool, heads, key_dim, value_dim]")[0]
+    shape = (pool, a.heads, a.key_dim, a.value_dim)
+    old = _packed("state", state, q, shape, f32)
+    new = old if new_state is None else _packed("new_state", new_state, q, shape, f32)
+    o = _Results(q.device, stream)(v.shape, v.dtype) if out is None else out
+    _check("ps_gated_delta_step", _lib().ps_gated_delta_step(
+        a, old, new, _slots(slots, q, a.tokens, pool), pool, _packed("out", o, q, v.shape, v.dtype), _stream(q, stream)))
     return o
 
 

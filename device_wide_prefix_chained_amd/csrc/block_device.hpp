@@ -145,6 +145,17 @@ __device__ __forceinline__ void swap_rows(float &a, float &b) {
     asm("s_nop 4\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b));
 }
 
+// The sum over a wave, in every lane.
+__device__ __forceinline__ float wave_total(float v) {
+    v = row_total(v);
+    float w = v;
+    swap_rows(v, w);
+    v += w;
+    w = v;
+    swap_halves(v, w);
+    return v + w;
+}
+
 // f(0), f(1), ... with the index as a constant.
 template <class F, int... i>
 __device__ __forceinline__ void for_each_index(F f, std::integer_sequence<int, i...>) {

@@ -27,16 +27,6 @@ struct NormArgs {
 constexpr int kVec = 8;  // neighbouring channels of a thread
 constexpr int kMostWaves = 16;
 
-__device__ __forceinline__ float wave_total(float v) {
-    v = row_total(v);
-    float w = v;
-    swap_rows(v, w);
-    v += w;
-    w = v;
-    swap_halves(v, w);
-    return v + w;
-}
-
 // The workgroup's sums of n values, in every thread: wave sums meet in
 // shared memory, and every row of lanes adds the up to 16 of them.
 template <int n>

@@ -1,0 +1,535 @@
+// delta_block.hpp -- parts shared by the gated delta rule's kernels: operands
+// of the matrix instructions, the tile of a chunk's keys or queries in shared
+// memory, and the kernel that prepares a chunk.
+//
+// A chunk is 64 rows of one sequence, S the state that enters it, G the running
+// sum of g in it, e = exp(G), k and q with their factors nu and mu of length 1
+// (or 1), and
+//   a_ij = exp(G_i - G_j) k_i k_j (j < i),  P_ij = scale exp(G_i - G_j) q_i k_j (j <= i)
+//   rho  = (1 + a diag(beta))^-1 (V - e K S),  U = beta rho
+//   out  = scale e Q S + P U,  S' = e_C S + K^T diag(exp(G_C - G)) U
+// which is the rule S' = exp(g) S, u = beta (v - S'^T k), S = S' + k u^T of one
+// row after another, with 64 of the rows' corrections solved for at once.
+//
+// Operands.  A product's result has a column in a lane (l & 15) and four
+// neighbouring rows in its registers (4 (l >> 4) + r); the next product takes
+// its right operand with a column in a lane and eight places of the summed
+// index, 8 (l >> 4) + j.  So results pass on as operands in the same lane if
+// the rows of a pair of tiles are laid over the 32 places as place() says, and
+// states, corrections and values never leave the registers.
+//
+// Precision.  The matrix instructions take bf16.  Inputs are whole: one bf16
+// plane for bf16, two for fp16 (11 bits).  fp32 numbers that a chunk computes
+// (states, corrections, inverses) are two planes, a rounding to bf16 and the
+// rounding of what is left: off by at most 2^-18, against 2^-9 of one plane,
+// for which a product takes 2 or 3 instructions (the planes' largest products).
+// All sums are fp32, and so is everything kept from chunk to chunk.  fp32
+// activations use the fp32 matrix instruction throughout (a sixteenth of the
+// rate).
+#pragma once
+
+#include "block_device.hpp"
+#include "chunks.hpp"
+
+namespace dwps {
+
+constexpr uint32_t kChunk = 64u, kChunkShift = 6u;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct DeltaArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta;
+    int64_t g_stride, beta_stride;
+    const uint32_t *offsets;
+    const float *initial;
+    uint32_t tokens, kheads, heads, key_dim, value_dim, num_seqs;
+    uint32_t slots;  // numbers of chunks
+    uint32_t unit;   // q and k by their lengths
+    float scale, eps;
+};
+
+// Eight places of an operand: N bf16 planes, or the numbers themselves.
+template <int N>
+struct Planes {
+    bf16x8 p[N];
+};
+struct Wide {
+    float p[8];
+};
+
+// N planes of eight numbers: each the rounding of what the ones before leave.
+template <int N>
+__device__ __forceinline__ Planes<N> planes_of(const float (&v)[8]) {
+    Planes<N> r;
+    float left[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) left[j] = v[j];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r.p[i][j] = (__bf16)left[j];
+            if (i + 1 < N) left[j] -= (float)r.p[i][j];
+        }
+    }
+    return r;
+}
+
+// acc += A B over 32 places: the products of planes i and j with i + j below
+// the larger number of planes, smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 &acc, const Planes<NA> &a, const Planes<NB> &b) {
+    constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+    for (int sum = most - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (sum - i >= 0 && sum - i < NB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[sum - i], acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4 &acc, const Wide &a, const Wide &b) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.p[j], b.p[j], acc, 0, 0, 0);
+}
+
+// How activations of type T are held in shared memory (planes of words) and
+// become operands; Mid: operands made of computed numbers.
+template <class T>
+struct Form;
+template <>
+struct Form<bf16_t> {
+    typedef uint16_t Word;
+    static constexpr int planes = 1, pad = 8;
+    typedef Planes<1> In;
+    typedef Planes<2> Mid;
+};
+template <>
+struct Form<f16_t> {
+    typedef uint16_t Word;
+    static constexpr int planes = 2, pad = 8;
+    typedef Planes<2> In;
+    typedef Planes<2> Mid;
+};
+template <>
+struct Form<float> {
+    typedef float Word;
+    static constexpr int planes = 1, pad = 4;
+    typedef Wide In;
+    typedef Wide Mid;
+};
+
+__device__ __forceinline__ void operand_of(Planes<2> &o, const float (&v)[8]) { o = planes_of<2>(v); }
+__device__ __forceinline__ void operand_of(Planes<1> &o, const float (&v)[8]) { o = planes_of<1>(v); }
+__device__ __forceinline__ void operand_of(Wide &o, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.p[j] = v[j];
+}
+// The operand of two tiles of a result: rows 4 q + r of the first and of the second.
+template <class M>
+__device__ __forceinline__ M operand_of(const f32x4 &a, const f32x4 &b) {
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    M o;
+    operand_of(o, v);
+    return o;
+}
+
+// The place of row m of tile `tile` along a summed index: the pair's 32
+// places, eight to each quarter of the lanes, four of them in each tile.
+__device__ __forceinline__ uint32_t place(uint32_t tile, uint32_t m) {
+    return 32u * (tile >> 1) + 8u * (m >> 2) + 4u * (tile & 1u) + (m & 3u);
+}
+
+// kChunk rows of `W` columns of activations in shared memory.
+template <class T, int W>
+struct RowTile {
+    typedef Form<T> F;
+    typedef typename F::Word Word;
+    static constexpr int kStride = W + F::pad;
+    Word w[F::planes][kChunk][kStride];
+
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8]) {
+        typename F::In o;
+        operand_of(o, v);
+        put(row, col, o);
+    }
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Wide &o) {
+        *reinterpret_cast<float4 *>(&w[0][row][col]) = make_float4(o.p[0], o.p[1], o.p[2], o.p[3]);
+        *reinterpret_cast<float4 *>(&w[0][row][col + 4]) = make_float4(o.p[4], o.p[5], o.p[6], o.p[7]);
+    }
+    template <int N>
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Planes<N> &o) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8 *>(&w[i][row][col]) = o.p[i];
+    }
+    // Eight columns of a row.
+    __device__ __forceinline__ typename F::In along(uint32_t row, uint32_t col) const {
+        typename F::In o;
+        get(o, row, col);
+        return o;
+    }
+    __device__ __forceinline__ void get(Wide &o, uint32_t row, uint32_t col) const {
+        const float4 a = *reinterpret_cast<const float4 *>(&w[0][row][col]);
+        const float4 b = *reinterpret_cast<const float4 *>(&w[0][row][col + 4]);
+        o.p[0] = a.x, o.p[1] = a.y, o.p[2] = a.z, o.p[3] = a.w;
+        o.p[4] = b.x, o.p[5] = b.y, o.p[6] = b.z, o.p[7] = b.w;
+    }
+    template <int N>
+    __device__ __forceinline__ void get(Planes<N> &o, uint32_t row, uint32_t col) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const bf16x8 *>(&w[i][row][col]);
+    }
+    // Eight rows of a column.
+    __device__ __forceinline__ typename F::In across(uint32_t row, uint32_t col) const {
+        typename F::In o;
+        get_across(o, row, col);
+        return o;
+    }
+    __device__ __forceinline__ void get_across(Wide &o, uint32_t row, uint32_t col) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.p[j] = w[0][row + j][col];
+    }
+    template <int N>
+    __device__ __forceinline__ void get_across(Planes<N> &o, uint32_t row, uint32_t col) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o.p[i][j] = __builtin_bit_cast(__bf16, w[i][row + j][col]);
+    }
+    __device__ __forceinline__ float value(uint32_t row, uint32_t col) const {
+        if constexpr (sizeof(Word) == 4) {
+            return w[0][row][col];
+        } else {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = F::planes - 1; i >= 0; --i) v += (float)__builtin_bit_cast(__bf16, w[i][row][col]);
+            return v;
+        }
+    }
+};
+
+// Eight activations of a row from column c of `width`, zeros past its end.
+template <class T>
+__device__ __forceinline__ void load8(float (&v)[8], const T *row, uint32_t c, uint32_t width) {
+    if (c + 8u <= width) {
+        const Pack<T, 8> r = *reinterpret_cast<const Pack<T, 8> *>(row + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)r.v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < width ? (float)row[c + j] : 0.0f;
+    }
+}
+
+// Rows lo .. lo + rows of a head's keys or queries into a tile, zeros after
+// them; 256 threads, four a row.  Returns the thread's part of its row's sum
+// of squares (row threadIdx.x >> 2).
+template <class T, int W>
+__device__ __forceinline__ float fill_rows(RowTile<T, W> &tile, const void *from, int64_t stride, uint32_t head,
+                                           uint32_t width, uint32_t lo, uint32_t rows) {
+    const uint32_t row = threadIdx.x >> 2, part = threadIdx.x & 3u;
+    const T *p = static_cast<const T *>(from) + (int64_t)(lo + row) * stride + (int64_t)head * width;
+    float sum = 0.0f;
+#pragma unroll
+    for (uint32_t c = part * 8u; c < (uint32_t)W; c += 32u) {
+        float v[8] = {};
+        if (row < rows) load8<T>(v, p, c, width);
+        tile.put(row, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[j], v[j], sum);
+    }
+    return sum;
+}
+
+// A wave's columns of a head's state [key_dim, value_dim]: tile t's register i
+// is row place(t, 4 q + i) of column col0 + 16 ct + (lane & 15).
+template <int CT, int TILES>
+__device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *from, const DeltaArgs &a, uint32_t col0,
+                                            uint32_t lane) {
+#pragma unroll
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i) {
+                const uint32_t row = place(t, 4u * (lane >> 4) + i), col = col0 + 16u * ct + (lane & 15u);
+                S[ct][t][i] = from && row < a.key_dim && col < a.value_dim ? from[row * a.value_dim + col] : 0.0f;
+            }
+}
+template <int CT, int TILES>
+__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], const DeltaArgs &a, uint32_t col0,
+                                             uint32_t lane) {
+#pragma unroll
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i) {
+                const uint32_t row = place(t, 4u * (lane >> 4) + i), col = col0 + 16u * ct + (lane & 15u);
+                if (row < a.key_dim && col < a.value_dim) to[row * a.value_dim + col] = S[ct][t][i];
+            }
+}
+
+// ---------------------------------------------------------------------------
+// what a chunk's preparation leaves in the workspace for each head
+// ---------------------------------------------------------------------------
+// Numbers for each row: e nu, scale e mu, beta, exp(G_C - G) nu; then exp(G_C).
+constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowFloats = 320u;
+// Two triangles as operands in the order that the lanes read them: row tile t
+// (16 rows of place()) and 32 places s; six of the eight hold something.
+constexpr uint32_t kTriangle = 6u;
+__host__ __device__ constexpr uint32_t lower_at(uint32_t t, uint32_t s) { return t < 2u ? t : 2u * t - 2u + s; }
+__host__ __device__ constexpr uint32_t upper_at(uint32_t t, uint32_t s) { return t < 2u ? 2u * t + s : 2u + t; }
+
+template <class T>
+struct Prepared {
+    typedef typename Form<T>::Mid Mid;
+    float row[kRowFloats];
+    Mid inverse[kTriangle][64];
+    Mid scores[kTriangle][64];
+};
+
+__device__ __forceinline__ double shuffle_up(double v, uint32_t by, uint32_t lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const int from = (int)(lane - by) * 4;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Running sums of a chunk's log decays, in 64 bits: what passes between two
+// rows is the difference of two sums, which may be much smaller than they are.
+// A log decay below -512 counts as that, so that minus infinity, a state that
+// starts again, stays a number; exp of any sum with it is zero.
+__device__ __forceinline__ double running_decay(const DeltaArgs &a, uint32_t head, uint32_t lo, uint32_t rows,
+                                                uint32_t lane) {
+    float g = lane < rows ? a.g[(int64_t)(lo + lane) * a.g_stride + head] : 0.0f;
+    g = g < -512.0f ? -512.0f : g;
+    double G = g;
+#pragma unroll
+    for (uint32_t by = 1u; by < 64u; by *= 2u) {
+        const double below = shuffle_up(G, by, lane);
+        if (lane >= by) G += below;
+    }
+    return G;
+}
+__device__ __forceinline__ float exp_hw(float v) { return exp2_hw(v * kLog2e); }
+
+// Two products of a chunk with itself, rows of tile `wave` against all: D
+// tiles of K K^T and Q K^T, column 16 t + (lane & 15).
+template <class T, int W>
+__device__ __forceinline__ void chunk_products(const RowTile<T, W> &K, const RowTile<T, W> &Q, uint32_t wave,
+                                               uint32_t lane, f32x4 (&kk)[4], f32x4 (&qk)[4]) {
+    const uint32_t m = lane & 15u, c0 = (lane >> 4) * 8u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t c = 0; c < (uint32_t)W; c += 32u) {
+        const auto ka = K.along(16u * wave + m, c + c0), qa = Q.along(16u * wave + m, c + c0);
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            if (t > wave) continue;
+            const auto kb = K.along(16u * t + m, c + c0);
+            mma(kk[t], ka, kb);
+            mma(qk[t], qa, kb);
+        }
+    }
+}
+
+constexpr int kSquare = 68;  // words from row to row of a 64 x 64 array in shared memory
+typedef float Square[kChunk][kSquare];
+
+// One 16 x 16 x 16 product in fp32: rows of `a` from (row, col), lane's column
+// of the right operand in its registers (rows 4 q + r).
+__device__ __forceinline__ f32x4 block_product(const Square &a, uint32_t row, uint32_t col, const float (&b)[4],
+                                               uint32_t lane, f32x4 acc) {
+    const float4 v = *reinterpret_cast<const float4 *>(&a[row + (lane & 15u)][col + 4u * (lane >> 4)]);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.x, b[0], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.y, b[1], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.z, b[2], acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(v.w, b[3], acc, 0, 0, 0);
+}
+
+// inv = (1 + a)^-1 of a strictly lower triangle, 256 threads; `a` is complete
+// before the call, `inv` after it.  Forward substitution in blocks of 16: each
+// wave inverts a block of the diagonal (a column in a lane), then the blocks
+// below it follow, inv_ij = -inv_ii sum_l a_il inv_lj, a diagonal of blocks at
+// a time.  Nothing is squared or summed over powers, so a triangle of large
+// entries loses no more than the substitution itself.
+__device__ __forceinline__ void unit_inverse(const Square &a, Square &inv, uint32_t wave, uint32_t lane) {
+    const uint32_t n = lane & 15u, q = lane >> 4, at = 16u * wave;
+    {
+        float x[16];
+#pragma unroll
+        for (uint32_t i = 0; i < 16u; ++i) {
+            float s = i == n ? 1.0f : 0.0f;
+#pragma unroll
+            for (uint32_t l = 0; l < i; ++l) s = __builtin_fmaf(-a[at + i][at + l], x[l], s);
+            x[i] = s;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 16u; ++i)
+            if ((i >> 2) == q) inv[at + i][at + n] = x[i];
+        for (uint32_t t = wave + 1u; t < 4u; ++t)  // the blocks above the diagonal
+#pragma unroll
+            for (uint32_t r = 0; r < 4u; ++r) inv[at + 4u * q + r][16u * t + n] = 0.0f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t d = 1; d < 4u; ++d) {
+        if (wave + d < 4u) {
+            const uint32_t i = wave + d, j = wave;
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (uint32_t l = j; l < i; ++l) {
+                float b[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4u; ++r) b[r] = inv[16u * l + 4u * q + r][16u * j + n];
+                sum = block_product(a, 16u * i, 16u * l, b, lane, sum);
+            }
+            const float b[4] = {-sum[0], -sum[1], -sum[2], -sum[3]};
+            const f32x4 x = block_product(inv, 16u * i, 16u * i, b, lane, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+            for (uint32_t r = 0; r < 4u; ++r) inv[16u * i + 4u * q + r][16u * j + n] = x[r];
+        }
+        __syncthreads();
+    }
+}
+
+// A chunk's numbers for the kernels that walk over chunks.  One workgroup a
+// chunk and head of keys: the two products are shared by the heads of values.
+// Forwards the inverse of 1 + a diag(beta) and the scores P, backwards the
+// transposes of (1 + diag(beta) a)^-1 and P.
+template <class T, int W, bool BACK>
+__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, uint32_t first, Prepared<T> *__restrict__ to,
+                                                            uint32_t *hdr, uint32_t words) {
+    typedef typename Form<T>::Mid Mid;
+    union Shared {
+        struct {
+            RowTile<T, W> k, q;
+        } in;
+        struct {
+            Square a, inv, p;
+        } m;
+    };
+    __shared__ Shared sh;
+    __shared__ double G[kChunk];
+    __shared__ float nu[kChunk], mu[kChunk], beta[kChunk];
+    const uint32_t b = first + blockIdx.x;
+    if (b == 0u && threadIdx.x == 0u) mark_plain(hdr, words);
+    const uint32_t slot = b / a.kheads, khead = b % a.kheads;
+    const Chunk c = find_chunk(a.offsets, a.num_seqs, a.tokens, kChunkShift, slot);
+    const uint32_t rows = c.hi - c.lo;
+    if (rows == 0u) return;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
+    float ks = fill_rows<T, W>(sh.in.k, a.k, a.k_stride, khead, a.key_dim, c.lo, rows);
+    float qs = fill_rows<T, W>(sh.in.q, a.q, a.q_stride, khead, a.key_dim, c.lo, rows);
+    ks += dpp<kQuadSwap2>(ks);
+    ks += dpp<kQuadSwap1>(ks);
+    qs += dpp<kQuadSwap2>(qs);
+    qs += dpp<kQuadSwap1>(qs);
+    if ((threadIdx.x & 3u) == 0u) {
+        nu[threadIdx.x >> 2] = a.unit ? 1.0f / __builtin_sqrtf(ks + a.eps) : 1.0f;
+        mu[threadIdx.x >> 2] = a.unit ? 1.0f / __builtin_sqrtf(qs + a.eps) : 1.0f;
+    }
+    __syncthreads();
+    f32x4 kk[4], qk[4];
+    chunk_products(sh.in.k, sh.in.q, wave, lane, kk, qk);
+    const uint32_t per = a.heads / a.kheads;
+    for (uint32_t j = 0; j < per; ++j) {
+        const uint32_t head = khead * per + j;
+        Prepared<T> &out = to[(uint64_t)slot * a.heads + head];
+        __syncthreads();  // the products, or the triangles of the head before, are read
+        if (wave == 0u) {
+            const double sum = running_decay(a, head, c.lo, rows, lane);
+            const float be = lane < rows ? a.beta[(int64_t)(c.lo + lane) * a.beta_stride + head] : 0.0f;
+            G[lane] = sum;
+            beta[lane] = be;
+            const double all = __builtin_bit_cast(
+                double, (uint64_t)__builtin_amdgcn_readlane((int)(uint32_t)(__builtin_bit_cast(uint64_t, sum) >> 32), 63) << 32 |
+                            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)__builtin_bit_cast(uint64_t, sum), 63));
+            const float e = exp_hw((float)sum);
+            out.row[kRowE + lane] = e * nu[lane];
+            out.row[kRowQ + lane] = a.scale * e * mu[lane];
+            out.row[kRowBeta + lane] = be;
+            out.row[kRowTail + lane] = exp_hw((float)(all - sum)) * nu[lane];
+            if (lane == 0u) out.row[kRowWhole] = exp_hw((float)all);
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            const uint32_t col = 16u * t + n;
+#pragma unroll
+            for (uint32_t r = 0; r < 4u; ++r) {
+                const uint32_t row = 16u * wave + 4u * q + r;
+                float between = 0.0f, along = 0.0f;
+                if (col <= row) {
+                    const float pass = exp_hw((float)(G[row] - G[col])) * nu[col];
+                    along = a.scale * pass * mu[row] * qk[t][r];
+                    if (col < row) between = pass * nu[row] * kk[t][r] * (BACK ? beta[row] : beta[col]);
+                }
+                sh.m.a[row][col] = between;
+                sh.m.p[row][col] = along;
+            }
+        }
+        __syncthreads();
+        unit_inverse(sh.m.a, sh.m.inv, wave, lane);
+        for (uint32_t i = threadIdx.x; i < 2u * kTriangle * 64u; i += 256u) {
+            const uint32_t l = i & 63u, f = (i >> 6) % kTriangle;
+            const bool scores = i >= kTriangle * 64u;
+            const Square &from = scores ? sh.m.p : sh.m.inv;
+            uint32_t t, s;
+            if (BACK) {
+                t = f < 4u ? f >> 1 : f - 2u;
+                s = f < 4u ? f & 1u : 1u;
+            } else {
+                t = f < 2u ? f : (f + 2u) >> 1;
+                s = f < 2u ? 0u : f & 1u;
+            }
+            const uint32_t row = place(t, l & 15u), col = 32u * s + 8u * (l >> 4);
+            float v[8];
+#pragma unroll
+            for (uint32_t u = 0; u < 8u; ++u) v[u] = BACK ? from[col + u][row] : from[row][col + u];
+            Mid o;
+            operand_of(o, v);
+            (scores ? out.scores : out.inverse)[f][l] = o;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+ps_status delta_sizes(const ps_delta_input *in);
+ps_status delta_pointers(const ps_delta_input *in);
+DeltaArgs delta_args(const ps_delta_input *in);
+
+// Bytes of a call's arrays; keys and values: packed rows of activations.
+struct DeltaBytes {
+    size_t q, k, v, g, beta, offsets, states, keys, values, gates;
+    explicit DeltaBytes(const ps_delta_input *in) {
+        const size_t e = dtype_bytes(in->dtype), kd = (size_t)in->kheads * in->key_dim, vd = (size_t)in->heads * in->value_dim;
+        q = rows_bytes(in->tokens, in->q_stride, kd, e);
+        k = rows_bytes(in->tokens, in->k_stride, kd, e);
+        v = rows_bytes(in->tokens, in->v_stride, vd, e);
+        g = rows_bytes(in->tokens, in->g_stride, in->heads, 4u);
+        beta = rows_bytes(in->tokens, in->beta_stride, in->heads, 4u);
+        offsets = in->offsets ? ((size_t)in->num_seqs + 1u) * 4u : 0u;
+        states = (size_t)in->num_seqs * in->heads * in->key_dim * in->value_dim * 4u;
+        keys = in->tokens * kd * e;
+        values = in->tokens * vd * e;
+        gates = in->tokens * in->heads * 4u;
+    }
+};
+
+// Calls f with the padded number of keys as a constant.
+template <class F>
+inline ps_status with_key_width(uint32_t key_dim, F f) {
+    if (key_dim <= 32u) return f(std::integral_constant<int, 32>());
+    if (key_dim <= 64u) return f(std::integral_constant<int, 64>());
+    if (key_dim <= 128u) return f(std::integral_constant<int, 128>());
+    return f(std::integral_constant<int, 256>());
+}
+
+}  // namespace dwps

@@ -1,0 +1,411 @@
+// gated_delta.hip -- the gated delta rule over packed sequences, and for
+// single tokens.
+//
+//   S' = exp(g) S,  u = beta (v - S'^T k),  S = S' + k u^T,  out = scale S^T q
+//
+// Prompts run in two launches: every chunk of 64 rows is prepared by itself
+// (delta_block.hpp), then a workgroup walks over a sequence's chunks with 64 or
+// 128 columns of a head's state in its registers.
+#include <hip/hip_runtime.h>
+
+#include "delta_block.hpp"
+
+namespace dwps {
+
+ps_status delta_sizes(const ps_delta_input *in) {
+    if (!in) return PS_ERR_NULL;
+    if (!dtype_bytes(in->dtype)) return PS_ERR_UNSUPPORTED;
+    const int64_t kd = in->key_dim, vd = in->value_dim, kh = in->kheads, h = in->heads;
+    if (in->tokens > kBlockMaxTokens || in->num_seqs > kBlockMaxSeqs || (!in->offsets && in->num_seqs > 1u) || kd == 0 ||
+        kd > PS_DELTA_MAX_DIM || vd == 0 || vd > PS_DELTA_MAX_DIM || kh == 0 || h == 0 || h > PS_DELTA_MAX_HEADS ||
+        h % kh != 0)
+        return PS_ERR_SIZE;
+    auto bad = [](int64_t stride, int64_t row) { return stride < row || stride > kBlockMaxStride; };
+    if (bad(in->q_stride, kh * kd) || bad(in->k_stride, kh * kd) || bad(in->v_stride, h * vd) || bad(in->g_stride, h) ||
+        bad(in->beta_stride, h))
+        return PS_ERR_SIZE;
+    return PS_OK;
+}
+
+ps_status delta_pointers(const ps_delta_input *in) {
+    const size_t e = dtype_bytes(in->dtype);
+    if (in->tokens && (!in->q || !in->k || !in->v || !in->g || !in->beta)) return PS_ERR_NULL;
+    if (!aligned(in->q, e) || !aligned(in->k, e) || !aligned(in->v, e) || !aligned(in->g, 4) || !aligned(in->beta, 4) ||
+        !aligned(in->offsets, 4) || !aligned(in->initial, 4))
+        return PS_ERR_ALIGNMENT;
+    return PS_OK;
+}
+
+DeltaArgs delta_args(const ps_delta_input *in) {
+    DeltaArgs a{};
+    a.q = in->q, a.k = in->k, a.v = in->v;
+    a.q_stride = in->q_stride, a.k_stride = in->k_stride, a.v_stride = in->v_stride;
+    a.g = in->g, a.beta = in->beta;
+    a.g_stride = in->g_stride, a.beta_stride = in->beta_stride;
+    a.offsets = in->offsets;
+    a.initial = in->initial;
+    a.tokens = (uint32_t)in->tokens;
+    a.kheads = in->kheads, a.heads = in->heads, a.key_dim = in->key_dim, a.value_dim = in->value_dim;
+    a.num_seqs = in->offsets ? in->num_seqs : 1u;
+    a.slots = (uint32_t)chunk_slots(in->tokens, a.num_seqs, kChunkShift);
+    a.unit = in->normalize ? 1u : 0u;
+    a.scale = in->scale, a.eps = in->eps;
+    return a;
+}
+
+namespace {
+
+// A workgroup walks over a sequence's chunks; a wave has 16 CT columns of a
+// head's state: rows place(t, 4 q + r) of column lane & 15.
+template <class T, int W, int CT>
+__global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+                                                         T *__restrict__ out, float *__restrict__ final,
+                                                         float *__restrict__ states, float *__restrict__ rhos) {
+    typedef typename Form<T>::Mid Mid;
+    constexpr uint32_t kTiles = W / 16, kCols = 64u * CT;
+    __shared__ RowTile<T, W> K, Q;
+    const uint32_t blocks = (a.value_dim + kCols - 1u) / kCols, b = first + blockIdx.x;
+    const uint32_t head = b / blocks % a.heads, seq = b / blocks / a.heads, khead = head / (a.heads / a.kheads);
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const uint32_t col0 = (b % blocks) * kCols + wave * 16u * CT;
+    const bool works = col0 < a.value_dim;
+    const Rows r = sequence_rows(a.offsets, a.tokens, seq, kChunkShift);
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
+    const T *v = static_cast<const T *>(a.v);
+    f32x4 S[CT][kTiles];
+    const float *from = a.initial ? a.initial + ((uint64_t)seq * a.heads + head) * cells : nullptr;
+    load_states(S, from, a, col0, lane);
+    uint32_t slot = r.base;
+    for (uint32_t lo = r.lo; lo < r.hi; lo += kChunk, ++slot) {
+        const uint32_t rows = r.hi - lo < kChunk ? r.hi - lo : kChunk;
+        const Prepared<T> &p = prepared[(uint64_t)slot * a.heads + head];
+        __syncthreads();
+        fill_rows<T, W>(K, a.k, a.k_stride, khead, a.key_dim, lo, rows);
+        fill_rows<T, W>(Q, a.q, a.q_stride, khead, a.key_dim, lo, rows);
+        __syncthreads();
+        if (works) {
+            if (states) store_states(states + ((uint64_t)slot * a.heads + head) * cells, S, a, col0, lane);
+            f32x4 x[CT][4], o[CT][4], y[CT][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[ct][t] = o[ct][t] = y[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (uint32_t s = 0; s < kTiles / 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(S[ct][2u * s], S[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    const auto ka = K.along(place(t, m), 32u * s + 8u * q), qa = Q.along(place(t, m), 32u * s + 8u * q);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        mma(x[ct][t], ka, h[ct]);
+                        mma(o[ct][t], qa, h[ct]);
+                    }
+                }
+            }
+            f32x4 number[4];
+            auto numbers = [&](uint32_t which) {
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+                    number[t] = *reinterpret_cast<const f32x4 *>(&p.row[which + place(t, 4u * q)]);
+            };
+            numbers(kRowE);
+#pragma unroll
+            for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                const uint32_t col = col0 + 16u * ct + m;
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4u; ++i) {
+                        const uint32_t row = place(t, 4u * q + i);
+                        float have = 0.0f;
+                        if (row < rows && col < a.value_dim)
+                            have = (float)v[(int64_t)(lo + row) * a.v_stride + (uint64_t)head * a.value_dim + col];
+                        x[ct][t][i] = __builtin_fmaf(-number[t][i], x[ct][t][i], have);
+                    }
+            }
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const Mid h = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u]);
+#pragma unroll
+                    for (uint32_t t = 2u * s; t < 4u; ++t) mma(y[ct][t], p.inverse[lower_at(t, s)][lane], h);
+                }
+            if (rhos) {
+#pragma unroll
+                for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                    const uint32_t col = col0 + 16u * ct + m;
+#pragma unroll
+                    for (uint32_t t = 0; t < 4u; ++t)
+#pragma unroll
+                        for (uint32_t i = 0; i < 4u; ++i) {
+                            const uint32_t row = place(t, 4u * q + i);
+                            if (row < rows && col < a.value_dim)
+                                rhos[((uint64_t)(lo + row) * a.heads + head) * a.value_dim + col] = y[ct][t][i];
+                        }
+                }
+            }
+            numbers(kRowBeta);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[ct][t] *= number[t];
+            numbers(kRowQ);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) o[ct][t] *= number[t];
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const Mid h = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+#pragma unroll
+                    for (uint32_t t = 2u * s; t < 4u; ++t) mma(o[ct][t], p.scores[lower_at(t, s)][lane], h);
+                }
+#pragma unroll
+            for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                const uint32_t col = col0 + 16u * ct + m;
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4u; ++i) {
+                        const uint32_t row = place(t, 4u * q + i);
+                        if (row < rows && col < a.value_dim)
+                            out[((uint64_t)(lo + row) * a.heads + head) * a.value_dim + col] = (T)o[ct][t][i];
+                    }
+            }
+            numbers(kRowTail);
+            const float whole = p.row[kRowWhole];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[ct][t] *= number[t];
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) S[ct][t] *= whole;
+            }
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) {
+                    const auto ka = K.across(32u * s + 8u * q, place(t, m));
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(S[ct][t], ka, h[ct]);
+                }
+            }
+        }
+    }
+    if (final && works) store_states(final + ((uint64_t)seq * a.heads + head) * cells, S, a, col0, lane);
+}
+
+// ---------------------------------------------------------------------------
+// single tokens
+// ---------------------------------------------------------------------------
+// A workgroup has `cols` columns of one head's state, four a thread and up to
+// kStepRows rows of them: the state is read once, held in registers, and
+// written once.  out = scale (e S^T q + (k q) u) needs no second sum over the
+// new state.
+constexpr uint32_t kStepRows = 16u;
+
+template <class T>
+__global__ __launch_bounds__(1024) void delta_step_kernel(DeltaArgs a, uint32_t first, uint32_t groups, const float *state,
+                                                          float *new_state, const int32_t *__restrict__ slots,
+                                                          uint32_t pool, T *__restrict__ out) {
+    __shared__ float key[PS_DELTA_MAX_DIM], query[PS_DELTA_MAX_DIM];
+    __shared__ float part[2][4096];
+    const uint32_t cols = groups * 4u, blocks = (a.value_dim + cols - 1u) / cols;
+    const uint32_t b = first + blockIdx.x, head = b / blocks % a.heads, row = b / blocks / a.heads;
+    const uint32_t khead = head / (a.heads / a.kheads), lane = threadIdx.x & 63u;
+    const uint32_t mine = threadIdx.x % groups, band = threadIdx.x / groups, bands = blockDim.x / groups;
+    const uint32_t col = (b % blocks) * cols + mine * 4u, have = col < a.value_dim ? a.value_dim - col : 0u;
+    const int32_t slot = slots ? slots[row] : (int32_t)row;
+    const bool held = slot >= 0 && (uint32_t)slot < pool;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
+    const uint64_t at = held ? ((uint64_t)slot * a.heads + head) * cells + col : 0u;
+    float S[kStepRows][4];
+#pragma unroll
+    for (uint32_t i = 0; i < kStepRows; ++i) {
+        const uint32_t d = band + i * bands;
+        const float *p = state + at + (uint64_t)d * a.value_dim;
+        if (held && d < a.key_dim && have >= 4u) {
+            const Pack<float, 4> w = *reinterpret_cast<const Pack<float, 4> *>(p);
+#pragma unroll
+            for (uint32_t j = 0; j < 4u; ++j) S[i][j] = w.v[j];
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 4u; ++j) S[i][j] = held && d < a.key_dim && j < have ? p[j] : 0.0f;
+        }
+    }
+    const T *k = static_cast<const T *>(a.k) + (int64_t)row * a.k_stride + (uint64_t)khead * a.key_dim;
+    const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.q_stride + (uint64_t)khead * a.key_dim;
+    float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+    for (uint32_t d = lane; d < PS_DELTA_MAX_DIM; d += 64u) {
+        const float kd = d < a.key_dim ? (float)k[d] : 0.0f, qd = d < a.key_dim ? (float)q[d] : 0.0f;
+        kk = __builtin_fmaf(kd, kd, kk);
+        qq = __builtin_fmaf(qd, qd, qq);
+        kq = __builtin_fmaf(kd, qd, kq);
+        if (threadIdx.x < 64u) key[d] = kd, query[d] = qd;
+    }
+    kk = wave_total(kk), qq = wave_total(qq), kq = wave_total(kq);
+    const float nu = a.unit ? 1.0f / __builtin_sqrtf(kk + a.eps) : 1.0f, mu = a.unit ? 1.0f / __builtin_sqrtf(qq + a.eps) : 1.0f;
+    float g = a.g[(int64_t)row * a.g_stride + head];
+    const float beta = a.beta[(int64_t)row * a.beta_stride + head];
+    const float e = exp_hw(g);
+    __syncthreads();
+    float ks[4] = {}, qs[4] = {};
+#pragma unroll
+    for (uint32_t i = 0; i < kStepRows; ++i) {
+        const uint32_t d = band + i * bands;
+        const float kd = d < a.key_dim ? key[d] : 0.0f, qd = d < a.key_dim ? query[d] : 0.0f;
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) {
+            ks[j] = __builtin_fmaf(kd, S[i][j], ks[j]);
+            qs[j] = __builtin_fmaf(qd, S[i][j], qs[j]);
+        }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) {
+        part[0][band * cols + mine * 4u + j] = ks[j];
+        part[1][band * cols + mine * 4u + j] = qs[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) ks[j] = qs[j] = 0.0f;
+    for (uint32_t i = 0; i < bands; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) {
+            ks[j] += part[0][i * cols + mine * 4u + j];
+            qs[j] += part[1][i * cols + mine * 4u + j];
+        }
+    const T *v = static_cast<const T *>(a.v) + (int64_t)row * a.v_stride + (uint64_t)head * a.value_dim + col;
+    float u[4], o[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) {
+        const float value = j < have ? (float)v[j] : 0.0f;
+        u[j] = beta * __builtin_fmaf(-e * nu, ks[j], value);
+        o[j] = a.scale * mu * __builtin_fmaf(e, qs[j], kq * nu * u[j]);
+    }
+    if (band == 0u) {
+        T *to = out + ((uint64_t)row * a.heads + head) * a.value_dim + col;
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j)
+            if (j < have) to[j] = (T)o[j];
+    }
+    if (!held) return;
+#pragma unroll
+    for (uint32_t i = 0; i < kStepRows; ++i) {
+        const uint32_t d = band + i * bands;
+        if (d >= a.key_dim) continue;
+        const float kd = key[d] * nu;
+        float *p = new_state + at + (uint64_t)d * a.value_dim;
+        Pack<float, 4> w;
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) w.v[j] = __builtin_fmaf(kd, u[j], e * S[i][j]);
+        if (have >= 4u) *reinterpret_cast<Pack<float, 4> *>(p) = w;
+        else
+#pragma unroll
+            for (uint32_t j = 0; j < 4u; ++j)
+                if (j < have) p[j] = w.v[j];
+    }
+}
+
+}  // namespace
+}  // namespace dwps
+
+using namespace dwps;
+
+extern "C" uint64_t ps_gated_delta_checkpoint_floats(uint64_t tokens, uint32_t num_seqs, uint32_t heads, uint32_t key_dim,
+                                                     uint32_t value_dim) {
+    return chunk_slots(tokens, num_seqs, kChunkShift) * heads * key_dim * value_dim + tokens * heads * value_dim;
+}
+
+extern "C" ps_status ps_gated_delta(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final,
+                                    float *checkpoints, void *stream) {
+    ps_status st = delta_sizes(in);
+    if (st != PS_OK) return st;
+    const DeltaArgs a = delta_args(in);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        PlainWs plan;
+        const size_t prepared_at = plan.take((size_t)a.slots * a.heads * sizeof(Prepared<T>));
+        bool query = false;
+        ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+        if (st != PS_OK || query) return st;
+        if ((st = delta_pointers(in)) != PS_OK) return st;
+        if (in->tokens && !out) return PS_ERR_NULL;
+        if (!aligned(ws, 16) || !aligned(out, sizeof(T)) || !aligned(final, 4) || !aligned(checkpoints, 4))
+            return PS_ERR_ALIGNMENT;
+        const DeltaBytes n(in);
+        const size_t kept = ps_gated_delta_checkpoint_floats(in->tokens, a.num_seqs, a.heads, a.key_dim, a.value_dim) * 4u;
+        if (outputs_overlap({{out, n.values}, {final, n.states}, {checkpoints, kept}},
+                            {{in->q, n.q}, {in->k, n.k}, {in->v, n.v}, {in->g, n.g}, {in->beta, n.beta},
+                             {in->offsets, n.offsets}, {in->initial, n.states}}))
+            return PS_ERR_ALIAS;
+        if (!a.num_seqs) return PS_OK;
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
+        float *rhos = checkpoints ? checkpoints + (uint64_t)a.slots * a.heads * a.key_dim * a.value_dim : nullptr;
+        return with_key_width(a.key_dim, [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            timing_begin(s);
+            launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_prepare_kernel<T, W, false>), dim3(grid), dim3(256), 0, s, a, first, prepared,
+                                   ws_counter(ws), plan.words());
+            });
+            const uint64_t groups = (uint64_t)a.num_seqs * a.heads * ceil_div(a.value_dim, 64u);
+            launch_in_parts(groups, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_kernel<T, W, 1>), dim3(grid), dim3(256), 0, s, a, first, prepared,
+                                   static_cast<T *>(out), final, checkpoints, rhos);
+            });
+            timing_end(s);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" ps_status ps_gated_delta_step(const ps_delta_input *in, const float *state, float *new_state,
+                                         const int32_t *slots, uint32_t pool, void *out, void *stream) {
+    ps_delta_input one;
+    if (!in) return PS_ERR_NULL;
+    one = *in;
+    one.offsets = nullptr, one.initial = nullptr, one.num_seqs = 1u;
+    in = &one;
+    ps_status st = delta_sizes(in);
+    if (st != PS_OK) return st;
+    if (!slots && in->tokens > pool) return PS_ERR_SIZE;
+    if ((st = delta_pointers(in)) != PS_OK) return st;
+    if (!in->tokens) return PS_OK;
+    if (!out || (pool && (!state || !new_state))) return PS_ERR_NULL;
+    if (!aligned(out, dtype_bytes(in->dtype)) || !aligned(state, 4) || !aligned(new_state, 4) || !aligned(slots, 4))
+        return PS_ERR_ALIGNMENT;
+    const DeltaBytes n(in);
+    const size_t states = (size_t)pool * in->heads * in->key_dim * in->value_dim * 4u;
+    const Bytes before = {new_state == state ? nullptr : state, states};
+    if (outputs_overlap({{out, n.values}, {new_state, states}},
+                        {{in->q, n.q}, {in->k, n.k}, {in->v, n.v}, {in->g, n.g}, {in->beta, n.beta},
+                         {slots, slots ? in->tokens * 4u : 0u}, before}))
+        return PS_ERR_ALIAS;
+    const DeltaArgs a = delta_args(in);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(in->dtype, [&](auto zero) {
+        using T = decltype(zero);
+        uint32_t groups = 4u;
+        while (groups * 4u < a.value_dim) groups *= 2u;
+        uint32_t bands = 1u;
+        while (bands * kStepRows < a.key_dim || bands * groups < 64u) bands *= 2u;
+        const uint64_t work = (uint64_t)a.tokens * a.heads * ceil_div(a.value_dim, groups * 4u);
+        timing_begin(s);
+        launch_in_parts(work, 1u, groups * bands, [&](uint32_t first, uint32_t grid) {
+            hipLaunchKernelGGL((delta_step_kernel<T>), dim3(grid), dim3(groups * bands), 0, s, a, first, groups, state,
+                               new_state, slots, pool, static_cast<T *>(out));
+        });
+        timing_end(s);
+        return launch_status();
+    });
+}

@@ -690,6 +690,54 @@ ps_status ps_selective_scan_bwd(void *ws, size_t *ws_bytes, const ps_scan_input 
 ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, float *new_state,
                                  const int32_t *slots, uint32_t pool, void *out, void *stream);
 
+/* The gated delta rule: every head has a matrix of states S [key_dim,
+ * value_dim], which forgets, is corrected towards v at k, and is read at q:
+ *   S' = exp(g) S,  u = beta (v - S'^T k),  S = S' + k u^T,  out = scale S^T q
+ * for every token and head h of v, with head h / (heads / kheads) of q and k.
+ * normalize != 0: q and k are divided by sqrt(|q|^2 + eps), sqrt(|k|^2 + eps)
+ * first.  S before a sequence's first row is initial[s], or zero without it.
+ * g and beta are fp32; g is a log decay: a value below -512 counts as -512,
+ * after which nothing of the state before is left.
+ *
+ * Sequences are worked on in chunks of 64 rows from their first row on, so a
+ * sequence's results do not depend on what is packed beside it.  With bf16 and
+ * fp16 activations the products of numbers that the call computes (states,
+ * corrections) are off by at most 2^-17 of a term's size; sums, and states from
+ * chunk to chunk, are fp32.  A NaN or an infinity in a row reaches its
+ * sequence's rows after it and those of its chunk before it.
+ * PS_ERR_SIZE also: dimensions outside 1..PS_DELTA_MAX_DIM, heads outside
+ * 1..PS_DELTA_MAX_HEADS or no multiple of kheads. */
+#define PS_DELTA_MAX_DIM 256
+#define PS_DELTA_MAX_HEADS 65536
+typedef struct ps_delta_input {
+    const void *q, *k;       /* [tokens, kheads, key_dim] */
+    const void *v;           /* [tokens, heads, value_dim] */
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta;   /* [tokens, heads] */
+    int64_t g_stride, beta_stride;
+    const uint32_t *offsets; /* [num_seqs + 1] or NULL */
+    const float *initial;    /* [num_seqs, heads, key_dim, value_dim] or NULL */
+    uint64_t tokens;
+    uint32_t kheads, heads, key_dim, value_dim, num_seqs;
+    ps_dtype dtype;
+    int normalize;
+    float scale, eps;
+} ps_delta_input;
+/* Floats of a call's checkpoints, what the backward pass starts from: the
+ * states that enter every chunk, and what is corrected at every row. */
+uint64_t ps_gated_delta_checkpoint_floats(uint64_t tokens, uint32_t num_seqs, uint32_t heads, uint32_t key_dim,
+                                          uint32_t value_dim);
+/* out: [tokens, heads, value_dim].  final (optional): [num_seqs, heads,
+ * key_dim, value_dim], the states after each sequence.  checkpoints (optional):
+ * that many floats. */
+ps_status ps_gated_delta(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final,
+                         float *checkpoints, void *stream);
+/* One token for each of in->tokens rows, with state and new_state [pool,
+ * heads, key_dim, value_dim] in fp32; slots as in ps_causal_conv_step.
+ * in->offsets, in->initial and in->num_seqs are not used. */
+ps_status ps_gated_delta_step(const ps_delta_input *in, const float *state, float *new_state, const int32_t *slots,
+                              uint32_t pool, void *out, void *stream);
+
 /* The norms around a block, with its gate and residual sum.  With
  * norm(v) = v / sqrt(mean(v^2) + eps) over a row:
  *   residual_out = residual + scale * sigmoid(gate) * norm(y) * post_weight
