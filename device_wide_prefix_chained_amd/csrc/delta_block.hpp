@@ -14,9 +14,12 @@
 // Operands.  A product's result has a column in a lane (l & 15) and four
 // neighbouring rows in its registers (4 (l >> 4) + r); the next product takes
 // its right operand with a column in a lane and eight places of the summed
-// index, 8 (l >> 4) + j.  So results pass on as operands in the same lane if
-// the rows of a pair of tiles are laid over the 32 places as place() says, and
-// states, corrections and values never leave the registers.
+// index, 8 (l >> 4) + j.  The order of the summed index is free as long as both
+// operands have the same, so the eight places of a lane are its four rows of
+// each of two result tiles, and states, corrections and values never leave the
+// registers.  For rows of a chunk that means places in the order of token_at();
+// keys are laid over a pair of tiles by place() instead, so that a lane's eight
+// keys are neighbours.
 //
 // Precision.  The matrix instructions take bf16.  Inputs are whole: one bf16
 // plane for bf16, two for fp16 (11 bits).  fp32 numbers that a chunk computes
@@ -34,9 +37,18 @@
 namespace dwps {
 
 constexpr uint32_t kChunk = 64u, kChunkShift = 6u;
+constexpr size_t kMostShared = 160u * 1024u;  // of a workgroup
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint64_t uint64x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ i16x4 read_transposed(const uint16_t *shared) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) i16x4 *)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)shared);
+}
 
 struct DeltaArgs {
     const void *q, *k, *v;
@@ -136,10 +148,16 @@ __device__ __forceinline__ M operand_of(const f32x4 &a, const f32x4 &b) {
     return o;
 }
 
-// The place of row m of tile `tile` along a summed index: the pair's 32
-// places, eight to each quarter of the lanes, four of them in each tile.
+// The key in row m of a state's tile: the 32 keys of a pair of tiles, eight to
+// each quarter of the lanes, four of them in each tile.
 __device__ __forceinline__ uint32_t place(uint32_t tile, uint32_t m) {
     return 32u * (tile >> 1) + 8u * (m >> 2) + 4u * (tile & 1u) + (m & 3u);
+}
+
+// The row of a chunk at place j of lanes 16 q .. of the s-th 32 places: rows
+// 4 q + i of tiles 2 s and 2 s + 1.
+__device__ __forceinline__ uint32_t token_at(uint32_t s, uint32_t q, uint32_t j) {
+    return 32u * s + 16u * (j >> 2) + 4u * q + (j & 3u);
 }
 
 // kChunk rows of `W` columns of activations in shared memory.
@@ -181,22 +199,28 @@ struct RowTile {
 #pragma unroll
         for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const bf16x8 *>(&w[i][row][col]);
     }
-    // Eight rows of a column.
-    __device__ __forceinline__ typename F::In across(uint32_t row, uint32_t col) const {
+    // A column of tile `tile` of keys, key place(tile, lane & 15), at the places
+    // token_at(s, lane >> 4, 0..7): the transposing read gives lane m of 16 the
+    // m & 3'rd of the four words that lanes (m >> 2) + 4 j point at.
+    __device__ __forceinline__ typename F::In across(uint32_t s, uint32_t tile, uint32_t lane) const {
         typename F::In o;
-        get_across(o, row, col);
+        get_across(o, s, tile, lane);
         return o;
     }
-    __device__ __forceinline__ void get_across(Wide &o, uint32_t row, uint32_t col) const {
+    __device__ __forceinline__ void get_across(Wide &o, uint32_t s, uint32_t tile, uint32_t lane) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.p[j] = w[0][row + j][col];
+        for (uint32_t j = 0; j < 8u; ++j) o.p[j] = w[0][token_at(s, lane >> 4, j)][place(tile, lane & 15u)];
     }
     template <int N>
-    __device__ __forceinline__ void get_across(Planes<N> &o, uint32_t row, uint32_t col) const {
+    __device__ __forceinline__ void get_across(Planes<N> &o, uint32_t s, uint32_t tile, uint32_t lane) const {
+        const uint32_t i = lane & 15u, row = 32u * s + 4u * (lane >> 4) + (i >> 2);
+        const uint32_t col = 32u * (tile >> 1) + 8u * (i & 3u) + 4u * (tile & 1u);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o.p[i][j] = __builtin_bit_cast(__bf16, w[i][row + j][col]);
+        for (int n = 0; n < N; ++n) {
+            const uint64_t a = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row][col]));
+            const uint64_t b = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row + 16u][col]));
+            o.p[n] = __builtin_bit_cast(bf16x8, uint64x2{a, b});
+        }
     }
     __device__ __forceinline__ float value(uint32_t row, uint32_t col) const {
         if constexpr (sizeof(Word) == 4) {
@@ -223,6 +247,30 @@ __device__ __forceinline__ void load8(float (&v)[8], const T *row, uint32_t c, u
     }
 }
 
+// Eight activations as they are in memory, held until they are written on:
+// columns c .. c + 8 of a row of `width`, zeros past it or where !is.  E: the
+// width is a multiple of 8.  `any` is a row that exists.
+template <bool E, class T>
+__device__ __forceinline__ Pack<T, 8> raw8(const T *row, const T *any, bool is, uint32_t c, uint32_t width) {
+    Pack<T, 8> r;
+    if (E) {
+        const bool there = is && c < width;
+        r = *reinterpret_cast<const Pack<T, 8> *>(there ? row + c : any);
+        if (!there)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r.v[j] = (T)0.0f;
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8u; ++j) r.v[j] = is && c + j < width ? row[c + j] : (T)0.0f;
+    }
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void values_of(float (&v)[8], const Pack<T, 8> &r) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)r.v[j];
+}
+
 // Rows lo .. lo + rows of a head's keys or queries into a tile, zeros after
 // them; 256 threads, four a row.  Returns the thread's part of its row's sum
 // of squares (row threadIdx.x >> 2).
@@ -243,33 +291,71 @@ __device__ __forceinline__ float fill_rows(RowTile<T, W> &tile, const void *from
     return sum;
 }
 
+// The column in lane m of tile ct of a wave's 16 CT columns.
+template <int CT>
+__device__ __forceinline__ uint32_t column(uint32_t ct, uint32_t m) {
+    return CT == 1 ? m : place(ct, m);
+}
+
 // A wave's columns of a head's state [key_dim, value_dim]: tile t's register i
-// is row place(t, 4 q + i) of column col0 + 16 ct + (lane & 15).
-template <int CT, int TILES>
+// is row place(t, 4 q + i) of column col0 + column(ct, lane & 15).  E: both
+// dimensions are multiples of 8, so a lane's four rows are all there or none.
+template <bool E, int CT, int TILES>
 __device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *from, const DeltaArgs &a, uint32_t col0,
                                             uint32_t lane) {
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
 #pragma unroll
-        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+        for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
+            const uint32_t row = place(t, 4u * (lane >> 4));
+            S[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (!from || row >= a.key_dim || col >= a.value_dim) continue;
 #pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i) {
-                const uint32_t row = place(t, 4u * (lane >> 4) + i), col = col0 + 16u * ct + (lane & 15u);
-                S[ct][t][i] = from && row < a.key_dim && col < a.value_dim ? from[row * a.value_dim + col] : 0.0f;
-            }
+            for (uint32_t i = 0; i < 4u; ++i)
+                if (E || row + i < a.key_dim) S[ct][t][i] = from[(row + i) * a.value_dim + col];
+        }
+    }
 }
-template <int CT, int TILES>
+// The width is hidden from the compiler where it stores: it would keep the
+// addresses of every row over a whole walk, in registers that the walk needs.
+template <bool E, int CT, int TILES>
 __device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], const DeltaArgs &a, uint32_t col0,
                                              uint32_t lane) {
+    uint32_t width = a.value_dim;
+    asm volatile("" : "+s"(width));
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
 #pragma unroll
-        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+        for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
+            const uint32_t row = place(t, 4u * (lane >> 4));
+            if (row >= a.key_dim || col >= width) continue;
+            float *p = to + (row * width + col);
 #pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i) {
-                const uint32_t row = place(t, 4u * (lane >> 4) + i), col = col0 + 16u * ct + (lane & 15u);
-                if (row < a.key_dim && col < a.value_dim) to[row * a.value_dim + col] = S[ct][t][i];
-            }
+            for (uint32_t i = 0; i < 4u; ++i)
+                if (E || row + i < a.key_dim) p[i * width] = S[ct][t][i];
+        }
+    }
+}
+// A result's tiles over a chunk's rows into rows of `stride`, rows below `rows`.
+template <bool E, int CT>
+__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[CT][4], uint32_t rows,
+                                           uint32_t col0, uint32_t width, uint32_t lane) {
+    asm volatile("" : "+s"(stride));
+#pragma unroll
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
+        if (col >= width) continue;
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            const uint32_t row = 16u * t + 4u * (lane >> 4);
+            float *p = to + (row * stride + col);
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i)
+                if (row + i < rows) p[i * stride] = y[ct][t][i];
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -277,8 +363,8 @@ __device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TIL
 // ---------------------------------------------------------------------------
 // Numbers for each row: e nu, scale e mu, beta, exp(G_C - G) nu; then exp(G_C).
 constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowFloats = 320u;
-// Two triangles as operands in the order that the lanes read them: row tile t
-// (16 rows of place()) and 32 places s; six of the eight hold something.
+// Two triangles as operands in the order that the lanes read them: rows of tile
+// t and the places of token_at(s, ..); six of the eight hold something.
 constexpr uint32_t kTriangle = 6u;
 __host__ __device__ constexpr uint32_t lower_at(uint32_t t, uint32_t s) { return t < 2u ? t : 2u * t - 2u + s; }
 __host__ __device__ constexpr uint32_t upper_at(uint32_t t, uint32_t s) { return t < 2u ? 2u * t + s : 2u + t; }
@@ -317,105 +403,90 @@ __device__ __forceinline__ double running_decay(const DeltaArgs &a, uint32_t hea
 }
 __device__ __forceinline__ float exp_hw(float v) { return exp2_hw(v * kLog2e); }
 
-// Two products of a chunk with itself, rows of tile `wave` against all: D
-// tiles of K K^T and Q K^T, column 16 t + (lane & 15).
-template <class T, int W>
-__device__ __forceinline__ void chunk_products(const RowTile<T, W> &K, const RowTile<T, W> &Q, uint32_t wave,
-                                               uint32_t lane, f32x4 (&kk)[4], f32x4 (&qk)[4]) {
-    const uint32_t m = lane & 15u, c0 = (lane >> 4) * 8u;
+// A chunk's sums of g and its beta, held by every wave for itself.
+struct ChunkGates {
+    double sum[kChunk];
+    float beta[kChunk];
+};
+
+// One 16 x 16 x 16 product in fp32: rows of `a`, columns from `col`; the right
+// operand's tile as a result leaves it.
+__device__ __forceinline__ f32x4 block_product(const float *a, uint32_t stride, const f32x4 &b, uint32_t lane, f32x4 acc) {
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(a + (lane & 15u) * stride + 4u * (lane >> 4));
 #pragma unroll
-    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v[i], b[i], acc, 0, 0, 0);
+    return acc;
+}
+
+// The inverse of one plus a strict triangle, 256 threads.  Backwards a lower
+// triangle A is inverted by columns: wave w has block column w in x, tiles of
+// rows, by forward substitution in blocks of 16,
+//   x_w = (1 + A_ww)^-1,  x_i = -(1 + A_ii)^-1 sum_{w <= l < i} A_il x_l.
+// Forwards the rows of the inverse are wanted in the lanes, which is the same
+// of the transpose, an upper triangle, from the last block up.  `tri` is the
+// triangle, row after row, complete before the call.  Every wave inverts a
+// block of the diagonal (a column in a lane) for all; the rest of its blocks
+// it has in its own registers.  Nothing is squared or summed over powers, so a
+// triangle of large entries loses no more than the substitution itself.
+constexpr uint32_t kTriStride = 68u, kDiagonal = 20u;  // words from row to row
+template <bool BACK>
+__device__ __forceinline__ void unit_inverse(const float *tri, float (*diagonal)[16 * kDiagonal], uint32_t wave, uint32_t lane,
+                                             f32x4 (&x)[4]) {
+    const uint32_t n = lane & 15u, q = lane >> 4;
+    const float *block = tri + 16u * wave * (kTriStride + 1u);
+    float c[16];
 #pragma unroll
-    for (uint32_t c = 0; c < (uint32_t)W; c += 32u) {
-        const auto ka = K.along(16u * wave + m, c + c0), qa = Q.along(16u * wave + m, c + c0);
+    for (uint32_t k = 0; k < 16u; ++k) {
+        const uint32_t i = BACK ? k : 15u - k;
+        float s = i == n ? 1.0f : 0.0f;
 #pragma unroll
-        for (uint32_t t = 0; t < 4u; ++t) {
-            if (t > wave) continue;
-            const auto kb = K.along(16u * t + m, c + c0);
-            mma(kk[t], ka, kb);
-            mma(qk[t], qa, kb);
-        }
+        for (uint32_t l = 0; l < 16u; ++l)
+            if (BACK ? l < i : l > i) s = __builtin_fmaf(-block[i * kTriStride + l], c[l], s);
+        c[i] = s;
     }
-}
-
-constexpr int kSquare = 68;  // words from row to row of a 64 x 64 array in shared memory
-typedef float Square[kChunk][kSquare];
-
-// One 16 x 16 x 16 product in fp32: rows of `a` from (row, col), lane's column
-// of the right operand in its registers (rows 4 q + r).
-__device__ __forceinline__ f32x4 block_product(const Square &a, uint32_t row, uint32_t col, const float (&b)[4],
-                                               uint32_t lane, f32x4 acc) {
-    const float4 v = *reinterpret_cast<const float4 *>(&a[row + (lane & 15u)][col + 4u * (lane >> 4)]);
-    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.x, b[0], acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.y, b[1], acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.z, b[2], acc, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(v.w, b[3], acc, 0, 0, 0);
-}
-
-// inv = (1 + a)^-1 of a strictly lower triangle, 256 threads; `a` is complete
-// before the call, `inv` after it.  Forward substitution in blocks of 16: each
-// wave inverts a block of the diagonal (a column in a lane), then the blocks
-// below it follow, inv_ij = -inv_ii sum_l a_il inv_lj, a diagonal of blocks at
-// a time.  Nothing is squared or summed over powers, so a triangle of large
-// entries loses no more than the substitution itself.
-__device__ __forceinline__ void unit_inverse(const Square &a, Square &inv, uint32_t wave, uint32_t lane) {
-    const uint32_t n = lane & 15u, q = lane >> 4, at = 16u * wave;
-    {
-        float x[16];
+    f32x4 own;
 #pragma unroll
-        for (uint32_t i = 0; i < 16u; ++i) {
-            float s = i == n ? 1.0f : 0.0f;
-#pragma unroll
-            for (uint32_t l = 0; l < i; ++l) s = __builtin_fmaf(-a[at + i][at + l], x[l], s);
-            x[i] = s;
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < 16u; ++i)
-            if ((i >> 2) == q) inv[at + i][at + n] = x[i];
-        for (uint32_t t = wave + 1u; t < 4u; ++t)  // the blocks above the diagonal
-#pragma unroll
-            for (uint32_t r = 0; r < 4u; ++r) inv[at + 4u * q + r][16u * t + n] = 0.0f;
+    for (uint32_t i = 0; i < 4u; ++i) {
+        own[i] = q == 0u ? c[i] : q == 1u ? c[4u + i] : q == 2u ? c[8u + i] : c[12u + i];
+        diagonal[wave][(4u * q + i) * kDiagonal + n] = own[i];
     }
     __syncthreads();
+    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (uint32_t d = 1; d < 4u; ++d) {
-        if (wave + d < 4u) {
-            const uint32_t i = wave + d, j = wave;
-            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (uint32_t l = j; l < i; ++l) {
-                float b[4];
+    for (uint32_t k = 0; k < 4u; ++k) x[k] = k == wave ? own : none;
 #pragma unroll
-                for (uint32_t r = 0; r < 4u; ++r) b[r] = inv[16u * l + 4u * q + r][16u * j + n];
-                sum = block_product(a, 16u * i, 16u * l, b, lane, sum);
-            }
-            const float b[4] = {-sum[0], -sum[1], -sum[2], -sum[3]};
-            const f32x4 x = block_product(inv, 16u * i, 16u * i, b, lane, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    for (uint32_t k = 1; k < 4u; ++k) {
+        const uint32_t i = BACK ? k : 3u - k;
+        if (BACK ? i > wave : i < wave) {
+            f32x4 sum = none;
 #pragma unroll
-            for (uint32_t r = 0; r < 4u; ++r) inv[16u * i + 4u * q + r][16u * j + n] = x[r];
+            for (uint32_t l = 0; l < 4u; ++l)  // tiles not yet there are zero
+                if (BACK ? l < i : l > i) sum = block_product(tri + 16u * (i * kTriStride + l), kTriStride, x[l], lane, sum);
+            x[i] = block_product(diagonal[i], kDiagonal, -sum, lane, none);
         }
-        __syncthreads();
     }
 }
 
 // A chunk's numbers for the kernels that walk over chunks.  One workgroup a
 // chunk and head of keys: the two products are shared by the heads of values.
 // Forwards the inverse of 1 + a diag(beta) and the scores P, backwards the
-// transposes of (1 + diag(beta) a)^-1 and P.
+// transposes of (1 + diag(beta) a)^-1 and P.  Wave w has what operands of row
+// tile w hold: all tiles are computed with their summed index in the registers
+// and are operands as they come.
 template <class T, int W, bool BACK>
-__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, uint32_t first, Prepared<T> *__restrict__ to,
-                                                            uint32_t *hdr, uint32_t words) {
+__global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint32_t first, Prepared<T> *__restrict__ to,
+                                                               uint32_t *hdr, uint32_t words) {
     typedef typename Form<T>::Mid Mid;
     union Shared {
         struct {
             RowTile<T, W> k, q;
         } in;
-        struct {
-            Square a, inv, p;
-        } m;
+        float tri[kChunk * kTriStride];
     };
     __shared__ Shared sh;
-    __shared__ double G[kChunk];
-    __shared__ float nu[kChunk], mu[kChunk], beta[kChunk];
+    __shared__ float diagonal[4][16 * kDiagonal];
+    __shared__ ChunkGates gates[4];
+    __shared__ float nu[kChunk], mu[kChunk];
     const uint32_t b = first + blockIdx.x;
     if (b == 0u && threadIdx.x == 0u) mark_plain(hdr, words);
     const uint32_t slot = b / a.kheads, khead = b % a.kheads;
@@ -434,66 +505,73 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, uint32_
         mu[threadIdx.x >> 2] = a.unit ? 1.0f / __builtin_sqrtf(qs + a.eps) : 1.0f;
     }
     __syncthreads();
+    // kk: rows k_l, columns k of tile `wave`; qk: forwards rows k_j, columns q of
+    // the tile, backwards rows q_i, columns k.  l > column or l < column.
     f32x4 kk[4], qk[4];
-    chunk_products(sh.in.k, sh.in.q, wave, lane, kk, qk);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
+        const auto kb = sh.in.k.along(16u * wave + n, col + 8u * q);
+        const auto qb = sh.in.q.along(16u * wave + n, col + 8u * q);
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            const bool below = t <= wave, above = t >= wave;
+            if (BACK ? below : above) mma(kk[t], sh.in.k.along(16u * t + n, col + 8u * q), kb);
+            if (BACK && above) mma(qk[t], sh.in.q.along(16u * t + n, col + 8u * q), kb);
+            if (!BACK && below) mma(qk[t], sh.in.k.along(16u * t + n, col + 8u * q), qb);
+        }
+    }
     const uint32_t per = a.heads / a.kheads;
+    ChunkGates &gate = gates[wave];
     for (uint32_t j = 0; j < per; ++j) {
         const uint32_t head = khead * per + j;
         Prepared<T> &out = to[(uint64_t)slot * a.heads + head];
-        __syncthreads();  // the products, or the triangles of the head before, are read
+        const double sum = running_decay(a, head, c.lo, rows, lane);
+        const float beta = lane < rows ? a.beta[(int64_t)(c.lo + lane) * a.beta_stride + head] : 0.0f;
+        gate.sum[lane] = sum;
+        gate.beta[lane] = beta;
         if (wave == 0u) {
-            const double sum = running_decay(a, head, c.lo, rows, lane);
-            const float be = lane < rows ? a.beta[(int64_t)(c.lo + lane) * a.beta_stride + head] : 0.0f;
-            G[lane] = sum;
-            beta[lane] = be;
+            const uint64_t bits = __builtin_bit_cast(uint64_t, sum);
             const double all = __builtin_bit_cast(
-                double, (uint64_t)__builtin_amdgcn_readlane((int)(uint32_t)(__builtin_bit_cast(uint64_t, sum) >> 32), 63) << 32 |
-                            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)__builtin_bit_cast(uint64_t, sum), 63));
+                double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(bits >> 32), 63) << 32 |
+                            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, 63));
             const float e = exp_hw((float)sum);
             out.row[kRowE + lane] = e * nu[lane];
             out.row[kRowQ + lane] = a.scale * e * mu[lane];
-            out.row[kRowBeta + lane] = be;
+            out.row[kRowBeta + lane] = beta;
             out.row[kRowTail + lane] = exp_hw((float)(all - sum)) * nu[lane];
             if (lane == 0u) out.row[kRowWhole] = exp_hw((float)all);
         }
-        __syncthreads();
+        const uint32_t col = 16u * wave + n;
+        const double here = gate.sum[col];
+        const float beta_here = gate.beta[col], nu_here = nu[col], mu_here = mu[col];
+        f32x4 p[4], x[4];
+        __syncthreads();  // the products, or the triangle of the head before, are read
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
-            const uint32_t col = 16u * t + n;
+            f32x4 tri;
 #pragma unroll
-            for (uint32_t r = 0; r < 4u; ++r) {
-                const uint32_t row = 16u * wave + 4u * q + r;
-                float between = 0.0f, along = 0.0f;
-                if (col <= row) {
-                    const float pass = exp_hw((float)(G[row] - G[col])) * nu[col];
-                    along = a.scale * pass * mu[row] * qk[t][r];
-                    if (col < row) between = pass * nu[row] * kk[t][r] * (BACK ? beta[row] : beta[col]);
-                }
-                sh.m.a[row][col] = between;
-                sh.m.p[row][col] = along;
+            for (uint32_t i = 0; i < 4u; ++i) {
+                const uint32_t row = 16u * t + 4u * q + i;
+                const float apart = (float)(gate.sum[row] - here);  // from the column's row to this one
+                const float forth = exp_hw(row >= col ? apart : -apart);
+                const float both = forth * nu[row];
+                // forwards a_lj beta_j for l > j, the transpose's row j; backwards beta_i a_il
+                tri[i] = (BACK ? row < col : row > col) ? both * nu_here * beta_here * kk[t][i] : 0.0f;
+                const float along = BACK ? forth * mu[row] * nu_here : both * mu_here;
+                p[t][i] = (BACK ? row >= col : row <= col) ? a.scale * along * qk[t][i] : 0.0f;
             }
+            *reinterpret_cast<f32x4 *>(&sh.tri[col * kTriStride + 16u * t + 4u * q]) = tri;
         }
         __syncthreads();
-        unit_inverse(sh.m.a, sh.m.inv, wave, lane);
-        for (uint32_t i = threadIdx.x; i < 2u * kTriangle * 64u; i += 256u) {
-            const uint32_t l = i & 63u, f = (i >> 6) % kTriangle;
-            const bool scores = i >= kTriangle * 64u;
-            const Square &from = scores ? sh.m.p : sh.m.inv;
-            uint32_t t, s;
-            if (BACK) {
-                t = f < 4u ? f >> 1 : f - 2u;
-                s = f < 4u ? f & 1u : 1u;
-            } else {
-                t = f < 2u ? f : (f + 2u) >> 1;
-                s = f < 2u ? 0u : f & 1u;
-            }
-            const uint32_t row = place(t, l & 15u), col = 32u * s + 8u * (l >> 4);
-            float v[8];
+        unit_inverse<BACK>(sh.tri, diagonal, wave, lane, x);
 #pragma unroll
-            for (uint32_t u = 0; u < 8u; ++u) v[u] = BACK ? from[col + u][row] : from[row][col + u];
-            Mid o;
-            operand_of(o, v);
-            (scores ? out.scores : out.inverse)[f][l] = o;
+        for (uint32_t s = 0; s < 2u; ++s) {
+            if (BACK ? s < (wave >> 1) : s > (wave >> 1)) continue;
+            const uint32_t at = BACK ? upper_at(wave, s) : lower_at(wave, s);
+            out.inverse[at][lane] = operand_of<Mid>(x[2u * s], x[2u * s + 1u]);
+            out.scores[at][lane] = operand_of<Mid>(p[2u * s], p[2u * s + 1u]);
         }
     }
 }
