@@ -41,7 +41,10 @@ DWPS_HD inline Rows sequence_rows(const uint32_t *offsets, uint32_t tokens, uint
 }
 
 // The chunk with number p: rows [lo, hi), which are none where no chunk has
-// the number; `index` counts the sequence's chunks.
+// the number; `index` counts the sequence's chunks.  Each sequence's first
+// number is found with index 0, also that of an empty one; a number before the
+// first sequence's has the index kNoChunk.
+constexpr uint32_t kNoChunk = 0xFFFFFFFFu;
 struct Chunk {
     uint32_t seq, index;
     uint32_t lo, hi;
@@ -61,9 +64,9 @@ DWPS_HD inline Chunk find_chunk(const uint32_t *offsets, uint32_t num_seqs, uint
     const Rows r = sequence_rows(offsets, tokens, s, shift);
     Chunk c;
     c.seq = s;
-    c.index = p < r.base ? 0u : p - r.base;
+    c.index = p < r.base ? kNoChunk : p - r.base;
     const uint64_t at = r.lo + ((uint64_t)c.index << shift);
-    c.lo = p >= r.base && at < r.hi ? (uint32_t)at : r.hi;
+    c.lo = at < r.hi ? (uint32_t)at : r.hi;
     c.hi = r.hi - c.lo > (1u << shift) ? c.lo + (1u << shift) : r.hi;
     return c;
 }

@@ -297,12 +297,12 @@ __device__ __forceinline__ uint32_t column(uint32_t ct, uint32_t m) {
     return CT == 1 ? m : place(ct, m);
 }
 
-// A wave's columns of a head's state [key_dim, value_dim]: tile t's register i
+// A wave's columns of a matrix [rows, width], a head's state as a rule: tile t's register i
 // is row place(t, 4 q + i) of column col0 + column(ct, lane & 15).  E: both
 // dimensions are multiples of 8, so a lane's four rows are all there or none.
 template <bool E, int CT, int TILES>
-__device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *from, const DeltaArgs &a, uint32_t col0,
-                                            uint32_t lane) {
+__device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *from, uint32_t rows, uint32_t width,
+                                            uint32_t col0, uint32_t lane) {
 #pragma unroll
     for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
         const uint32_t col = col0 + column<CT>(ct, lane & 15u);
@@ -310,19 +310,18 @@ __device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *
         for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
             const uint32_t row = place(t, 4u * (lane >> 4));
             S[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (!from || row >= a.key_dim || col >= a.value_dim) continue;
+            if (!from || row >= rows || col >= width) continue;
 #pragma unroll
             for (uint32_t i = 0; i < 4u; ++i)
-                if (E || row + i < a.key_dim) S[ct][t][i] = from[(row + i) * a.value_dim + col];
+                if (E || row + i < rows) S[ct][t][i] = from[(row + i) * width + col];
         }
     }
 }
 // The width is hidden from the compiler where it stores: it would keep the
 // addresses of every row over a whole walk, in registers that the walk needs.
 template <bool E, int CT, int TILES>
-__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], const DeltaArgs &a, uint32_t col0,
-                                             uint32_t lane) {
-    uint32_t width = a.value_dim;
+__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], uint32_t rows, uint32_t width,
+                                             uint32_t col0, uint32_t lane) {
     asm volatile("" : "+s"(width));
 #pragma unroll
     for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
@@ -330,11 +329,11 @@ __device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TIL
 #pragma unroll
         for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
             const uint32_t row = place(t, 4u * (lane >> 4));
-            if (row >= a.key_dim || col >= width) continue;
+            if (row >= rows || col >= width) continue;
             float *p = to + (row * width + col);
 #pragma unroll
             for (uint32_t i = 0; i < 4u; ++i)
-                if (E || row + i < a.key_dim) p[i * width] = S[ct][t][i];
+                if (E || row + i < rows) p[i * width] = S[ct][t][i];
         }
     }
 }
@@ -582,6 +581,11 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
 ps_status delta_sizes(const ps_delta_input *in);
 ps_status delta_pointers(const ps_delta_input *in);
 DeltaArgs delta_args(const ps_delta_input *in);
+
+// ps_gated_delta of one type, after delta_sizes.
+template <class T>
+ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final, float *checkpoints,
+                        hipStream_t stream);
 
 // Bytes of a call's arrays; keys and values: packed rows of activations.
 struct DeltaBytes {

@@ -1,0 +1,449 @@
+// delta_walk.hpp -- the gated delta rule over packed sequences: kernels that walk
+// over chunks, and their launches.  One type of activations a source file.
+//
+// Every chunk of 64 rows is prepared by itself (delta_block.hpp).  Then a
+// workgroup walks over a sequence's chunks with 64 or 128 columns of a head's
+// state in its registers; long sequences in segments side by side, for which
+// two walks and a link first find the states that enter them.
+#pragma once
+
+#include "delta_block.hpp"
+
+namespace dwps {
+namespace {
+
+// What a step of a walk reads: a chunk's keys, queries and values, and what was
+// prepared of it.
+template <class T, int W, int CT>
+struct WalkTile {
+    static constexpr uint32_t kCols = 64u * CT;
+    RowTile<T, W> k, q;
+    Prepared<T> p;
+    T v[kChunk][kCols + 8u];
+};
+template <class T, int W, int CT>
+constexpr bool kValuesFit = sizeof(WalkTile<T, W, CT>) <= kMostShared;
+template <class T, int W, int CT>
+constexpr size_t walk_tile_bytes() {
+    return kValuesFit<T, W, CT> ? sizeof(WalkTile<T, W, CT>) : sizeof(WalkTile<T, W, CT>) - sizeof(WalkTile<T, W, CT>::v);
+}
+
+// Where a sequence is walked over in segments of 2^shift rows side by side: a
+// state that enters a segment leaves it as M S + N, whose columns are walks of
+// their own, M's from the unit matrix without values and N's from zero.
+// `shift` 31: whole sequences, one segment each.
+struct Segments {
+    uint32_t shift;
+    float *m;  // [segment numbers, heads, key_dim, key_dim]
+    float *n;  // [segment numbers, heads, key_dim, value_dim]: N, then the states that enter
+};
+struct WalkResults {
+    void *out;
+    float *final, *states, *rhos;
+};
+
+// Four waves walk over a segment's chunks, each with 16 CT columns of a head's
+// state; four feed them, loading a chunk while the one before is worked on and
+// leaving it in the tile of the two that is not in use (or, where shared memory
+// has room for one, after a barrier in that one).  LEAD: the walks for M and N,
+// of segments that another follows.
+template <class T, int W, int CT, bool E, bool LEAD>
+__global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+                                                         Segments seg, WalkResults to) {
+    typedef typename Form<T>::Mid Mid;
+    typedef WalkTile<T, W, CT> Tile;
+    constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, CT>()];
+    const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = LEAD ? (a.key_dim + kCols - 1u) / kCols : 0u;
+    const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
+    const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const bool unit = block < key_blocks;  // columns of M
+    const uint32_t block0 = (block - (unit ? 0u : key_blocks)) * kCols, width = unit ? a.key_dim : a.value_dim;
+    const Chunk r = find_chunk(a.offsets, a.num_seqs, a.tokens, seg.shift, number);
+    const Rows seq = sequence_rows(a.offsets, a.tokens, r.seq, kChunkShift);
+    if (r.index == kNoChunk || (r.lo == r.hi && r.index != 0u) || (LEAD && r.hi == seq.hi)) return;
+    const uint32_t chunks = (r.hi - r.lo + kChunk - 1u) / kChunk;
+    const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);  // its first chunk's number
+    const T *values = static_cast<const T *>(a.v) + (uint64_t)head * a.value_dim;
+    auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
+    if (wave >= 4u) {
+        // the feeding waves
+        constexpr uint32_t kKeys = (W + 31) / 32, kVals = kCols / 32u;
+        constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
+        const uint32_t thread = threadIdx.x - 256u, row = thread >> 2, part = (thread & 3u) * 8u;
+        Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
+        u32x4 ps[kWords];
+        auto fetch = [&](uint32_t i) {
+            const int64_t lo = r.lo + i * kChunk;
+            const bool is = lo + row < r.hi;
+            const T *k0 = static_cast<const T *>(a.k) + lo * a.k_stride + (uint64_t)khead * a.key_dim;
+            const T *q0 = static_cast<const T *>(a.q) + lo * a.q_stride + (uint64_t)khead * a.key_dim;
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) {
+                ks[c] = raw8<E, T>(k0 + row * a.k_stride, k0, is, part + 32u * c, a.key_dim);
+                if (!LEAD) qs[c] = raw8<E, T>(q0 + row * a.q_stride, q0, is, part + 32u * c, a.key_dim);
+            }
+            if constexpr (kV) {
+                const T *v0 = values + lo * a.v_stride;
+#pragma unroll
+                for (uint32_t c = 0; c < kVals; ++c)
+                    vs[c] = raw8<E, T>(v0 + row * a.v_stride, v0, is && !unit, block0 + part + 32u * c, a.value_dim);
+            }
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(&prepared[(uint64_t)(base + i) * a.heads + head]);
+#pragma unroll
+            for (uint32_t c = 0; c < kWords; ++c) {
+                const uint32_t at = thread + 256u * c;
+                if (at < kBytes / 16u) ps[c] = p[at];
+            }
+        };
+        auto leave = [&](uint32_t i) {
+            Tile *to = tile(i);
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) {
+                float v[8];
+                values_of<T>(v, ks[c]);
+                to->k.put(row, part + 32u * c, v);
+                if (!LEAD) {
+                    values_of<T>(v, qs[c]);
+                    to->q.put(row, part + 32u * c, v);
+                }
+            }
+            if constexpr (kV) {
+#pragma unroll
+                for (uint32_t c = 0; c < kVals; ++c) *reinterpret_cast<Pack<T, 8> *>(&to->v[row][part + 32u * c]) = vs[c];
+            }
+#pragma unroll
+            for (uint32_t c = 0; c < kWords; ++c) {
+                const uint32_t at = thread + 256u * c;
+                if (at < kBytes / 16u) reinterpret_cast<u32x4 *>(&to->p)[at] = ps[c];
+            }
+        };
+        if (chunks) fetch(0u), leave(0u);
+        __syncthreads();
+        for (uint32_t i = 0; i < chunks; ++i) {
+            const bool more = i + 1u < chunks;
+            if (more) fetch(i + 1u);
+            if (!kTwo) __syncthreads();
+            if (more) leave(i + 1u);
+            __syncthreads();
+        }
+        return;
+    }
+    const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
+    f32x4 S[CT][kTiles];
+    {
+        const float *from = nullptr;
+        if (!LEAD && r.index) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
+        else if (!LEAD && a.initial) from = a.initial + ((uint64_t)r.seq * a.heads + head) * cells;
+        load_states<E>(S, from, a.key_dim, a.value_dim, col0, lane);
+        if (unit) {
+#pragma unroll
+            for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4u; ++i)
+                        S[ct][t][i] = place(t, 4u * q + i) == col0 + column<CT>(ct, m) ? 1.0f : 0.0f;
+        }
+    }
+    __syncthreads();
+    for (uint32_t c = 0; c < chunks; ++c) {
+        const uint32_t lo = r.lo + c * kChunk, rows = r.hi - lo < kChunk ? r.hi - lo : kChunk;
+        const Tile &in = *tile(c);
+        if (col0 < width) {
+            if (!LEAD && to.states)
+                store_states<E>(to.states + ((uint64_t)(base + c) * a.heads + head) * cells, S, a.key_dim, a.value_dim, col0, lane);
+            f32x4 x[CT][4], o[CT][4], y[CT][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[ct][t] = o[ct][t] = y[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // K S, and (Q S)^T: the operands' sides are the other way round, which
+            // leaves a row of out in a lane and neighbouring columns in its registers
+#pragma unroll
+            for (uint32_t s = 0; s < kTiles / 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(S[ct][2u * s], S[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], ka, h[ct]);
+                    if (LEAD) continue;
+                    const auto qa = in.q.along(16u * t + m, 32u * s + 8u * q);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], qa);
+                }
+            }
+            auto numbers = [&](uint32_t which, uint32_t t) {
+                return *reinterpret_cast<const f32x4 *>(&in.p.row[which + 16u * t + 4u * q]);
+            };
+            __builtin_amdgcn_sched_barrier(0);
+            // R = V - e K S
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 e = numbers(kRowE, t);
+#pragma unroll
+                for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                    f32x4 v;
+                    if constexpr (kV && sizeof(T) == 2) {
+                        const uint32_t at = here + (CT == 1 ? 4u * (m & 3u) : 8u * (m & 3u) + 4u * ct);
+                        const i16x4 raw = read_transposed(
+                            reinterpret_cast<const uint16_t *>(&in.v[16u * t + 4u * q + (m >> 2)][at]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
+                    } else if constexpr (kV) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)in.v[16u * t + 4u * q + i][here + column<CT>(ct, m)];
+                    } else {
+                        const uint32_t col = col0 + column<CT>(ct, m);
+#pragma unroll
+                        for (uint32_t i = 0; i < 4u; ++i) {
+                            const uint32_t row = 16u * t + 4u * q + i;
+                            v[i] = row < rows && col < a.value_dim && !unit ? (float)values[(int64_t)(lo + row) * a.v_stride + col] : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[ct][t][i] = __builtin_fmaf(-e[i], x[ct][t][i], v[i]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // rho
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 2u * s; t < 4u; ++t) {
+                    const Mid inverse = in.p.inverse[lower_at(t, s)][lane];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
+                }
+            }
+            if (!LEAD && to.rhos)
+                store_rows<E>(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, rows,
+                              col0, a.value_dim, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            // out^T = scale e (Q S)^T + U^T P^T
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 beta = numbers(kRowBeta, t);
+                const float e = LEAD ? 0.0f : in.p.row[kRowQ + 16u * t + m];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= beta, o[ct][t] *= e;
+            }
+#pragma unroll
+            for (uint32_t s = 0; s < (LEAD ? 0u : 2u); ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 2u * s; t < 4u; ++t) {
+                    const Mid scores = in.p.scores[lower_at(t, s)][lane];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], scores);
+                }
+            }
+#pragma unroll
+            for (uint32_t t = 0; t < (LEAD ? 0u : 4u); ++t) {
+                const uint32_t row = 16u * t + m, col = col0 + 4u * CT * q;
+                if (row < rows && col < a.value_dim) {
+                    T *at = static_cast<T *>(to.out) + ((uint64_t)(lo + row) * a.heads + head) * a.value_dim + col;
+                    Pack<T, 4 * CT> w;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w.v[4 * ct + i] = (T)o[ct][t][i];
+                    if (E || col + 4u * CT <= a.value_dim) {
+                        *reinterpret_cast<Pack<T, 4 * CT> *>(at) = w;
+                    } else {
+#pragma unroll
+                        for (uint32_t i = 0; i < 4u * CT; ++i)
+                            if (col + i < a.value_dim) at[i] = w.v[i];
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // S = e_C S + K^T diag(exp(G_C - G)) U
+            const float whole = in.p.row[kRowWhole];
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 tail = numbers(kRowTail, t);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= tail;
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) S[ct][t] *= whole;
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) {
+                    const auto ka = in.k.across(s, t, lane);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(S[ct][t], ka, h[ct]);
+                }
+            }
+        }
+        if (!kTwo) __syncthreads();
+        __syncthreads();
+    }
+    if (col0 >= width) return;
+    const uint64_t place_of = (uint64_t)number * a.heads + head;
+    if (LEAD && unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, S, a.key_dim, a.key_dim, col0, lane);
+    else if (LEAD) store_states<E>(seg.n + place_of * cells, S, a.key_dim, a.value_dim, col0, lane);
+    else if (to.final && r.hi == seq.hi)
+        store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, a.key_dim, a.value_dim, col0, lane);
+}
+
+// The states that enter a sequence's segments after the first, S <- M S + N,
+// in the places of N.  A wave has 16 columns.
+template <class T, int W, bool E>
+__global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg) {
+    typedef typename Form<T>::Mid Mid;
+    constexpr uint32_t kTiles = W / 16;
+    const uint32_t blocks = (a.value_dim + 63u) / 64u, item = first + blockIdx.x / blocks, head = item % a.heads;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const uint32_t col0 = blockIdx.x % blocks * 64u + wave * 16u, s = item / a.heads;
+    const Rows r = sequence_rows(a.offsets, a.tokens, s, seg.shift);
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim, key_cells = (uint64_t)a.key_dim * a.key_dim;
+    const uint32_t segments = (uint32_t)(((uint64_t)(r.hi - r.lo) + (1ull << seg.shift) - 1u) >> seg.shift);
+    if (col0 >= a.value_dim || segments < 2u) return;
+    f32x4 S[1][kTiles], next[1][kTiles];
+    load_states<E>(S, a.initial ? a.initial + ((uint64_t)s * a.heads + head) * cells : nullptr, a.key_dim, a.value_dim, col0, lane);
+    float *n = seg.n + ((uint64_t)r.base * a.heads + head) * cells;
+    const float *mat = seg.m + ((uint64_t)r.base * a.heads + head) * key_cells;
+    load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
+    for (uint32_t i = 0; i + 1u < segments; ++i) {
+        Mid h[kTiles / 2];
+#pragma unroll
+        for (uint32_t c = 0; c < kTiles / 2u; ++c) h[c] = operand_of<Mid>(S[0][2u * c], S[0][2u * c + 1u]);
+#pragma unroll
+        for (uint32_t t = 0; t < kTiles; ++t) {
+            const uint32_t row = place(t, m);
+            S[0][t] = next[0][t];
+#pragma unroll
+            for (uint32_t c = 0; c < kTiles / 2u; ++c) {
+                float v[8] = {};
+                if (row < a.key_dim) load8<float>(v, mat + row * a.key_dim, 32u * c + 8u * q, a.key_dim);
+                Mid o;
+                operand_of(o, v);
+                mma(S[0][t], o, h[c]);
+            }
+        }
+        n += a.heads * cells;
+        mat += a.heads * key_cells;
+        if (i + 2u < segments) load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(n, S, a.key_dim, a.value_dim, col0, lane);
+    }
+}
+
+// Rows of a segment, as a shift: as many as make a call's steps fewest, by what
+// a step was measured to take next to a walk's over 32 columns a wave, where
+// 256 workgroups run at once and sequences are cut at random (the longest of n
+// is then the mean times 1 + 1/2 + ... + 1/n).  Walks for M and N 0.6 each, a
+// link 0.6.
+uint32_t segment_shift(const DeltaArgs &a, uint32_t cols) {
+    const double chunks = (double)(a.tokens >> kChunkShift) + 0.5 * a.num_seqs, heads = a.heads;
+    const double value_blocks = (double)ceil_div(a.value_dim, cols), key_blocks = (double)ceil_div(a.key_dim, cols);
+    double longest = 0.0;
+    for (uint32_t i = 1; i <= a.num_seqs && i <= 64u; ++i) longest += 1.0 / i;
+    longest *= chunks / a.num_seqs;
+    longest = longest > chunks ? chunks : longest;
+    const double work = chunks * heads * value_blocks / 256.0;
+    double best = longest > work ? longest : work;
+    uint32_t shift = 31u;
+    for (uint32_t by = 2u; by <= 7u; ++by) {
+        const double rows = (double)(1u << by), segments = chunks / rows + 0.5 * a.num_seqs;
+        if (longest < 2.0 * rows) break;
+        const double main = __builtin_ceil(segments * heads * value_blocks / 256.0) * rows;
+        const double led = segments - a.num_seqs > 0.0 ? segments - a.num_seqs : 0.0;
+        const double lead = 0.6 * __builtin_ceil(led * heads * (value_blocks + key_blocks) / 256.0) * rows;
+        const double cost = main + lead + 0.6 * longest / rows + 4.0;
+        if (cost < best) best = cost, shift = kChunkShift + by;
+    }
+    return shift;
+}
+
+}  // namespace
+
+template <class T>
+ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final, float *checkpoints,
+                        hipStream_t s) {
+    const DeltaArgs a = delta_args(in);
+    PlainWs plan;
+    const size_t prepared_at = plan.take((size_t)a.slots * a.heads * sizeof(Prepared<T>));
+    Segments seg{};
+    // 32 columns a wave where there are more than 64, and registers for their states
+    const bool wide = a.key_dim <= 128u && a.value_dim > 64u;
+    seg.shift = segment_shift(a, wide ? 128u : 64u);
+    const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
+    const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u;
+    const size_t m_at = plan.take(linked * a.key_dim * a.key_dim * 4u), n_at = plan.take(linked * cells * 4u);
+    bool query = false;
+    ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+    if (st != PS_OK || query) return st;
+    if ((st = delta_pointers(in)) != PS_OK) return st;
+    if (in->tokens && !out) return PS_ERR_NULL;
+    if (!aligned(ws, 16) || !aligned(out, sizeof(T)) || !aligned(final, 4) || !aligned(checkpoints, 4))
+        return PS_ERR_ALIGNMENT;
+    const DeltaBytes n(in);
+    const size_t kept = ps_gated_delta_checkpoint_floats(in->tokens, a.num_seqs, a.heads, a.key_dim, a.value_dim) * 4u;
+    if (outputs_overlap({{out, n.values}, {final, n.states}, {checkpoints, kept}},
+                        {{in->q, n.q}, {in->k, n.k}, {in->v, n.v}, {in->g, n.g}, {in->beta, n.beta},
+                         {in->offsets, n.offsets}, {in->initial, n.states}}))
+        return PS_ERR_ALIAS;
+    if (!a.num_seqs) return PS_OK;
+    Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
+    float *rhos = checkpoints ? checkpoints + (uint64_t)a.slots * a.heads * a.key_dim * a.value_dim : nullptr;
+    return with_key_width(a.key_dim, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        timing_begin(s);
+        launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+            hipLaunchKernelGGL((delta_prepare_kernel<T, W, false>), dim3(grid), dim3(256), 0, s, a, first, prepared,
+                               ws_counter(ws), plan.words());
+        });
+        seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
+        const WalkResults to = {out, final, checkpoints, rhos};
+        auto walk = [&](auto ct, auto eights) {
+            constexpr int CT = decltype(ct)::value;
+            constexpr bool E = decltype(eights)::value;
+            const uint64_t blocks = ceil_div(a.value_dim, 64u * CT), all = blocks + ceil_div(a.key_dim, 64u * CT);
+            if (linked) {
+                launch_in_parts(segments * a.heads, all, 512u, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_kernel<T, W, CT, E, true>), dim3(grid), dim3(512), 0, s, a,
+                                       first, prepared, seg, to);
+                });
+                const uint64_t columns = ceil_div(a.value_dim, 64u);
+                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, E>), dim3(grid), dim3(256), 0, s, a,
+                                       first, seg);
+                });
+            }
+            launch_in_parts(segments * a.heads, blocks, 512u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_kernel<T, W, CT, E, false>), dim3(grid), dim3(512), 0, s, a,
+                                   first, prepared, seg, to);
+            });
+        };
+        const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
+        auto shape = [&](auto e) {
+            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 2 : 1>(), e);
+            else walk(std::integral_constant<int, 1>(), e);
+        };
+        if (eights) shape(std::true_type());
+        else shape(std::false_type());
+        timing_end(s);
+        return launch_status();
+    });
+}
+
+}  // namespace dwps

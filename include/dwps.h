@@ -706,7 +706,8 @@ ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, fl
  * chunk to chunk, are fp32.  A NaN or an infinity in a row reaches its
  * sequence's rows after it and those of its chunk before it.
  * PS_ERR_SIZE also: dimensions outside 1..PS_DELTA_MAX_DIM, heads outside
- * 1..PS_DELTA_MAX_HEADS or no multiple of kheads. */
+ * 1..PS_DELTA_MAX_HEADS or no multiple of kheads, (tokens / 64 + num_seqs) *
+ * heads (single tokens: tokens * heads) of 2^31 or more. */
 #define PS_DELTA_MAX_DIM 256
 #define PS_DELTA_MAX_HEADS 65536
 typedef struct ps_delta_input {

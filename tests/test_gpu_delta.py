@@ -39,6 +39,13 @@ DELTA = [  # tokens, cuts, kheads, heads, key_dim, value_dim, type, normalize, i
     (130, [0, 129, 130], 1, 1, 130, 256, F32, True, True, True),
     (90, list(range(91)), 1, 2, 16, 24, BF16, True, True, False),
     (500, None, 1, 1, 24, 8, BF16, True, True, False),
+    # long sequences: segments of them side by side
+    (1500, None, 1, 2, 64, 72, BF16, True, True, False),
+    (1600, [0, 1300, 1310, 1310, 1600], 1, 1, 128, 128, BF16, True, True, True),
+    (1500, [0, 700, 1500], 1, 1, 40, 33, F16, True, False, False),
+    (1024, None, 1, 1, 256, 20, F16, True, True, False),
+    (1290, [3, 1290], 1, 1, 128, 96, F32, True, True, False),
+    (1100, None, 1, 1, 200, 24, BF16, False, True, False),
 ]
 
 
