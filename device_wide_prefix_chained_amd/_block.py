@@ -61,6 +61,11 @@ class _NormGrads(ctypes.Structure):
     _fields_ = [(n, _VP) for n in ("dy", "dgate", "dresidual", "dscale", "dpost_weight", "dpre_weight")]
 
 
+class _LayerInput(ctypes.Structure):
+    _fields_ = [("x", _VP), ("x_stride", _I64), ("weight", _VP), ("bias", _VP), ("tokens", _U64), ("channels", _U32),
+                ("dtype", _I32), ("eps", ctypes.c_float)]
+
+
 class ConvGrads(NamedTuple):
     dx: torch.Tensor
     dweight: torch.Tensor
@@ -89,6 +94,12 @@ class NormGrads(NamedTuple):
     dpre_weight: Optional[torch.Tensor]
 
 
+class LayerNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
 _lib_ready = None
 
 
@@ -108,6 +119,8 @@ def _lib():
             "ps_gated_delta_step": [P(_DeltaInput), _VP, _VP, _VP, _U32, _VP, _VP],
             "ps_block_norm": [P(_NormInput), _VP, _VP, _VP],
             "ps_block_norm_bwd": [_VP, sz, P(_NormInput), _VP, _VP, P(_NormGrads), _VP],
+            "ps_layer_norm": [P(_LayerInput), _VP, _VP],
+            "ps_layer_norm_bwd": [_VP, sz, P(_LayerInput), _VP, _VP, _VP, _VP, _VP],
         }
         for name, args in sigs.items():
             getattr(L, name).argtypes = args
@@ -517,4 +530,37 @@ def ps_block_norm_bwd(y, residual_out, dout, dresidual_out=None, *, gate=None, s
                        _addr(r.dpre_weight))
     s, f = _stream(y, stream), _lib().ps_block_norm_bwd
     _with_workspace("ps_block_norm_bwd", lambda ws, wsb: f(ws, wsb, a, g, dr, grads, s), y, workspace, stream)
+    return r
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+def _layer_input(x, weight, bias, eps):
+    stride = _first("x", x)
+    code = _type_of("x", x)
+    w = (x.shape[1],)
+    return _LayerInput(x.data_ptr(), stride, _packed("weight", weight, x, w, torch.float32),
+                       _packed("bias", bias, x, w, torch.float32), x.shape[0], x.shape[1], code, eps)
+
+
+def ps_layer_norm(x, weight=None, bias=None, *, eps=1e-5, out=None, stream=None):
+    """(x - mean) / sqrt(var + eps) * weight + bias over the channels of each
+    row of x [tokens, channels]."""
+    a = _layer_input(x, weight, bias, eps)
+    o = _Results(x.device, stream).like(x) if out is None else out
+    _check("ps_layer_norm", _lib().ps_layer_norm(a, _packed("out", o, x, x.shape, x.dtype), _stream(x, stream)))
+    return o
+
+
+def ps_layer_norm_bwd(x, dout, weight=None, bias=None, *, eps=1e-5, workspace=None, stream=None):
+    """Gradients of ps_layer_norm: LayerNormGrads(dx, dweight, dbias), the last
+    two where there is a weight and a bias."""
+    a = _layer_input(x, weight, bias, eps)
+    g = _packed("dout", dout, x, x.shape, x.dtype)
+    new = _Results(x.device, stream)
+    r = LayerNormGrads(*(new.like(t) for t in (x, weight, bias)))
+    s, f = _stream(x, stream), _lib().ps_layer_norm_bwd
+    call = lambda ws, wsb: f(ws, wsb, a, g, _addr(r.dx), _addr(r.dweight), _addr(r.dbias), s)  # noqa: E731
+    _with_workspace("ps_layer_norm_bwd", call, x, workspace, stream)
     return r

@@ -768,6 +768,25 @@ typedef struct ps_norm_grads {
 ps_status ps_block_norm_bwd(void *ws, size_t *ws_bytes, const ps_norm_input *in, const void *dout,
                             const void *dresidual_out, const ps_norm_grads *grads, void *stream);
 
+/* Layer norm over the channels of a row:
+ *   out = (x - mean) / sqrt(var + eps) * weight + bias
+ * with the row's mean and the mean of the squared differences from it; weight
+ * and bias are optional (1 and 0). */
+typedef struct ps_layer_input {
+    const void *x;           /* [tokens, channels] */
+    int64_t x_stride;
+    const float *weight, *bias; /* [channels] */
+    uint64_t tokens;
+    uint32_t channels;
+    ps_dtype dtype;
+    float eps;
+} ps_layer_input;
+ps_status ps_layer_norm(const ps_layer_input *in, void *out, void *stream);
+/* Gradients given dout (packed): dx [tokens, channels] (of dtype), dweight and
+ * dbias [channels] (fp32), of which the last two may be NULL. */
+ps_status ps_layer_norm_bwd(void *ws, size_t *ws_bytes, const ps_layer_input *in, const void *dout, void *dx,
+                            float *dweight, float *dbias, void *stream);
+
 /* Elements per tile of the flat scan kernel for `dtype` (PS_U64: the
  * widening scan), of the segmented
  * scan kernel, and the library version string. */
