@@ -50,6 +50,10 @@ class _DeltaInput(ctypes.Structure):
                 ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class _DeltaGrads(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("dq", "dk", "dv", "dg", "dbeta", "dinitial")]
+
+
 class _NormInput(ctypes.Structure):
     _fields_ = [("y", _VP), ("gate", _VP), ("residual", _VP),
                 ("y_stride", _I64), ("gate_stride", _I64), ("residual_stride", _I64),
@@ -94,6 +98,15 @@ class NormGrads(NamedTuple):
     dpre_weight: Optional[torch.Tensor]
 
 
+class DeltaGrads(NamedTuple):
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    dg: torch.Tensor
+    dbeta: torch.Tensor
+    dinitial: Optional[torch.Tensor]
+
+
 class LayerNormGrads(NamedTuple):
     dx: torch.Tensor
     dweight: Optional[torch.Tensor]
@@ -116,6 +129,7 @@ def _lib():
             "ps_selective_scan_bwd": [_VP, sz, P(_ScanInput), _VP, _VP, P(_ScanGrads), _VP],
             "ps_selective_scan_step": [P(_ScanInput), _VP, _VP, _VP, _U32, _VP, _VP],
             "ps_gated_delta": [_VP, sz, P(_DeltaInput), _VP, _VP, _VP, _VP],
+            "ps_gated_delta_bwd": [_VP, sz, P(_DeltaInput), _VP, _VP, _VP, P(_DeltaGrads), _VP],
             "ps_gated_delta_step": [P(_DeltaInput), _VP, _VP, _VP, _U32, _VP, _VP],
             "ps_block_norm": [P(_NormInput), _VP, _VP, _VP],
             "ps_block_norm_bwd": [_VP, sz, P(_NormInput), _VP, _VP, P(_NormGrads), _VP],
@@ -463,6 +477,23 @@ def ps_gated_delta(q, k, v, g, beta, *, scale=None, normalize=False, eps=1e-6, o
     s, f = _stream(q, stream), _lib().ps_gated_delta
     _with_workspace("ps_gated_delta", lambda ws, wsb: f(ws, wsb, a, to, fin, kept, s), q, workspace, stream)
     return o
+
+
+def ps_gated_delta_bwd(q, k, v, g, beta, dout, checkpoints, *, scale=None, normalize=False, eps=1e-6, offsets=None,
+                       initial=None, dfinal=None, workspace=None, stream=None):
+    """Gradients of ps_gated_delta's out and final, given ``dout`` and
+    ``dfinal`` (None: zero), from the checkpoints that it wrote for these
+    inputs: DeltaGrads, with dinitial None where no initial is given."""
+    a = _delta_input(q, k, v, g, beta, scale, normalize, eps, offsets, initial)
+    go = _packed("dout", dout, q, v.shape, v.dtype)
+    gf = _packed("dfinal", dfinal, q, (a.num_seqs, a.heads, a.key_dim, a.value_dim), torch.float32)
+    kept = _delta_checkpoints(checkpoints, q, a)
+    new = _Results(q.device, stream)
+    r = DeltaGrads(*(None if t is None else new(t.shape, t.dtype) for t in (q, k, v, g, beta, initial)))
+    grads = _DeltaGrads(*(_addr(t) for t in r))
+    s, f = _stream(q, stream), _lib().ps_gated_delta_bwd
+    _with_workspace("ps_gated_delta_bwd", lambda ws, wsb: f(ws, wsb, a, go, gf, kept, grads, s), q, workspace, stream)
+    return r
 
 
 def ps_gated_delta_step(q, k, v, state, g, beta, *, scale=None, normalize=False, eps=1e-6, slots=None, new_state=None,

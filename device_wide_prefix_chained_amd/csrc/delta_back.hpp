@@ -1,0 +1,727 @@
+// delta_back.hpp -- gradients of the gated delta rule over packed sequences.  One
+// type of activations a source file.
+//
+// With D the gradient of the state that leaves a chunk (delta_block.hpp names
+// the rest), backwards over the chunks
+//   dU = P^T dO + diag(exp(G_C - G)) K D,  omega = (1 + diag(beta) a)^-T dU
+//   dR = beta omega = dV
+//   D <- e_C D + Q^T diag(scale e) dO - K^T diag(e) dR
+// is a walk like the forward one, with the same segments.  It leaves D and
+// omega, from which every chunk finds its own gradients:
+//   dbeta = rho omega (summed over columns)
+//   dqk_ij = scale exp(G_i - G_j) dO_i U_j (j <= i),  dkk_ij = -exp(G_i - G_j) dR_i U_j (j < i)
+//   dQ = scale e dO S^T + dqk K
+//   dK = -e dR S^T + exp(G_C - G) U D^T + dkk K + dqk^T Q + dkk^T K
+// Every exp(G_i - G_j) holds the g of the rows t with j < t <= i, e_i those up to
+// i, exp(G_C - G_j) those after j, so with z_ij = dqk_ij q_i k_j + dkk_ij k_i k_j
+//   dg_t = sum_{j < t <= i} z_ij + sum_{i >= t} e_i (scale q_i S dO_i - k_i S dR_i)
+//        + sum_{j < t} exp(G_C - G_j) k_j D u_j + e_C <S, D>
+// as they stand: no term is added that another takes away.
+#pragma once
+
+#include "delta_walk.hpp"
+
+namespace dwps {
+namespace {
+
+struct BackResults {
+    const float *dfinal;  // [num_seqs, heads, key_dim, value_dim] or NULL
+    float *dinitial;      // the same, or NULL
+    float *dstates;       // [chunk numbers, heads, key_dim, value_dim]: D
+    float *omega;         // [tokens, heads, value_dim]
+};
+
+// Eight rows token_at(s, q, ..) of a column of a value tile.
+template <class T, uint32_t STRIDE>
+__device__ __forceinline__ void value_rows(float (&v)[8], const T (*tile)[STRIDE], uint32_t s, uint32_t q, uint32_t m,
+                                           uint32_t here, uint32_t ct, bool pairs) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t at = here + (pairs ? 8u * (m & 3u) + 4u * ct : 4u * (m & 3u));
+#pragma unroll
+        for (uint32_t h = 0; h < 2u; ++h) {
+            const i16x4 raw = read_transposed(
+                reinterpret_cast<const uint16_t *>(&tile[32u * s + 16u * h + 4u * q + (m >> 2)][at]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * h + i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
+        }
+    } else {
+        const uint32_t col = here + (pairs ? place(ct, m) : m);
+#pragma unroll
+        for (uint32_t j = 0; j < 8u; ++j) v[j] = tile[token_at(s, q, j)][col];
+    }
+}
+
+// The walk backwards.  lead: the walks for M and N of segments that are not a
+// sequence's first, which keep nothing but their end.
+template <class T, int W, int CT, bool E>
+__global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+                                                              Segments seg, const T *__restrict__ dout, bool lead, BackResults to) {
+    typedef typename Form<T>::Mid Mid;
+    typedef typename Form<T>::In In;
+    typedef WalkTile<T, W, CT> Tile;
+    constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, CT>()];
+    const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = lead ? (a.key_dim + kCols - 1u) / kCols : 0u;
+    const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
+    const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const bool unit = block < key_blocks;  // columns of M
+    const uint32_t block0 = (block - (unit ? 0u : key_blocks)) * kCols, width = unit ? a.key_dim : a.value_dim;
+    const Chunk r = find_chunk(a.offsets, a.num_seqs, a.tokens, seg.shift, number);
+    const Rows seq = sequence_rows(a.offsets, a.tokens, r.seq, kChunkShift);
+    if (r.index == kNoChunk || (r.lo == r.hi && r.index != 0u) || (lead && r.lo == seq.lo)) return;
+    const uint32_t chunks = (r.hi - r.lo + kChunk - 1u) / kChunk;
+    const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);
+    const T *grads = dout + (uint64_t)head * a.value_dim;
+    const int64_t grads_stride = (int64_t)a.heads * a.value_dim;
+    const DeltaFeed<T, W, CT, E> feed = {a, prepared, r, base, head, khead, block0, grads, grads_stride};
+    auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
+    if (wave >= 4u) {
+        feed.template run<false>(chunks, !unit, tile, [&](uint32_t i) { return chunks - 1u - i; });
+        return;
+    }
+    const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
+    f32x4 D[CT][kTiles];
+    {
+        const float *from = nullptr;
+        if (!lead && r.hi != seq.hi) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
+        else if (!lead && to.dfinal) from = to.dfinal + ((uint64_t)r.seq * a.heads + head) * cells;
+        load_states<E>(D, from, a.key_dim, a.value_dim, col0, lane);
+        if (unit) unit_states(D, col0, lane);
+    }
+    __syncthreads();
+    for (uint32_t i = 0; i < chunks; ++i) {
+        const uint32_t c = chunks - 1u - i, lo = r.lo + c * kChunk, rows = r.hi - lo < kChunk ? r.hi - lo : kChunk;
+        const Tile &in = *tile(i);
+        if (col0 < width) {
+            if (!lead)
+                store_states<E>(to.dstates + ((uint64_t)(base + c) * a.heads + head) * cells, D, a.key_dim, a.value_dim, col0, lane);
+            auto numbers = [&](uint32_t which, uint32_t t) {
+                return *reinterpret_cast<const f32x4 *>(&in.p.row[which + 16u * t + 4u * q]);
+            };
+            f32x4 x[CT][4], y[CT][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[ct][t] = y[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // dU = exp(G_C - G) K D + P^T dO
+#pragma unroll
+            for (uint32_t s = 0; s < kTiles / 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(D[ct][2u * s], D[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], ka, h[ct]);
+                }
+            }
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 tail = numbers(kRowTail, t);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) x[ct][t] *= tail;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            auto columns_of = [&](float (&v)[8], uint32_t s, uint32_t ct) {
+                if constexpr (kV) {
+                    value_rows<T, kCols + 8u>(v, in.v, s, q, m, here, ct, CT == 2);
+                } else {
+                    const uint32_t col = col0 + column<CT>(ct, m);
+#pragma unroll
+                    for (uint32_t j = 0; j < 8u; ++j) {
+                        const uint32_t row = token_at(s, q, j);
+                        v[j] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
+                    }
+                }
+            };
+            if (!unit) {
+#pragma unroll
+                for (uint32_t s = 0; s < 2u; ++s) {
+                    In h[CT];
+#pragma unroll
+                    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                        float v[8];
+                        columns_of(v, s, ct);
+                        operand_of(h[ct], v);
+                    }
+#pragma unroll
+                    for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
+                        const Mid scores = in.p.scores[upper_at(t, s)][lane];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], scores, h[ct]);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // omega
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
+                    const Mid inverse = in.p.inverse[upper_at(t, s)][lane];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
+                }
+            }
+            if (!lead)
+                store_rows<E>(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, rows, col0,
+                              a.value_dim, lane);
+            // D = e_C D + Q^T diag(scale e) dO - K^T diag(e) beta omega
+            __builtin_amdgcn_sched_barrier(0);
+            const float whole = in.p.row[kRowWhole];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) D[ct][t] *= whole;
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 e = numbers(kRowE, t) * numbers(kRowBeta, t);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= -e;
+            }
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                Mid h[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+#pragma unroll
+                for (uint32_t t = 0; t < kTiles; ++t) {
+                    const auto ka = in.k.across(s, t, lane);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(D[ct][t], ka, h[ct]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (!unit) {
+#pragma unroll
+                for (uint32_t s = 0; s < 2u; ++s) {
+                    const f32x4 e0 = numbers(kRowQ, 2u * s), e1 = numbers(kRowQ, 2u * s + 1u);
+                    Mid h[CT];
+#pragma unroll
+                    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
+                        float v[8];
+                        columns_of(v, s, ct);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] *= e0[j], v[4 + j] *= e1[j];
+                        operand_of(h[ct], v);
+                    }
+#pragma unroll
+                    for (uint32_t t = 0; t < kTiles; ++t) {
+                        const auto qa = in.q.across(s, t, lane);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma(D[ct][t], qa, h[ct]);
+                    }
+                }
+            }
+        }
+        if (!kTwo) __syncthreads();
+        __syncthreads();
+    }
+    if (col0 >= width) return;
+    const uint64_t place_of = (uint64_t)number * a.heads + head;
+    if (unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, D, a.key_dim, a.key_dim, col0, lane);
+    else if (lead) store_states<E>(seg.n + place_of * cells, D, a.key_dim, a.value_dim, col0, lane);
+    else if (to.dinitial && r.lo == seq.lo)
+        store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, a.key_dim, a.value_dim, col0, lane);
+}
+
+// ---------------------------------------------------------------------------
+// a chunk's own gradients
+// ---------------------------------------------------------------------------
+struct DeltaGradPtrs {
+    void *dq, *dk, *dv;
+    float *dg, *dbeta;
+};
+
+__device__ __forceinline__ double shuffle(double v, uint32_t from) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(from * 4u), (int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(from * 4u), (int)(uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float shuffle(float v, uint32_t from) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((int)(from * 4u), __builtin_bit_cast(int, v)));
+}
+// The sum over the four lanes of a column, in every one of them.
+__device__ __forceinline__ float column_total(float v) {
+    float w = v;
+    swap_rows(v, w);
+    v += w;
+    w = v;
+    swap_halves(v, w);
+    return v + w;
+}
+
+// Eight or four keys of a row held by a lane: four of each of its wave's tiles.
+template <class T, int W>
+__device__ __forceinline__ f32x4 four_keys(const RowTile<T, W> &tile, uint32_t row, uint32_t col) {
+    f32x4 v;
+    if constexpr (sizeof(typename RowTile<T, W>::Word) == 4) {
+        v = *reinterpret_cast<const f32x4 *>(&tile.w[0][row][col]);
+    } else {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int p = Form<T>::planes - 1; p >= 0; --p) {
+            const u16x4 r = *reinterpret_cast<const u16x4 *>(&tile.w[p][row][col]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += (float)__builtin_bit_cast(__bf16, (uint16_t)r[i]);
+        }
+    }
+    return v;
+}
+
+template <class T, int W>
+struct GradShared {
+    typedef typename Form<T>::Mid Mid;
+    // 32 columns of computed numbers: two planes, or themselves.  256 keys in two
+    // planes leave no room for the padding that spreads rows over the banks.
+    static constexpr int kPad = W == 256 && sizeof(RowTile<T, W>) > 66560u ? 0 : Form<T>::pad;
+    typedef RowTile<typename std::conditional<sizeof(T) == 2, f16_t, float>::type, 32, kPad> MidTile;
+    RowTile<T, W> k, q;
+    union {
+        struct {
+            RowTile<T, 32, kPad> dout;
+            MidTile u, dr;
+        } in;
+        Mid triangle[kTriangle][64];
+        struct {
+            float query[4][kChunk], key[4][kChunk], end[4][kChunk], pair[4][kChunk];
+        } part;
+    };
+    double sum[kChunk];
+    float beta[kChunk], nu[kChunk], mu[kChunk], dot[4];
+};
+
+// One workgroup a chunk and head of keys; it takes the heads of values that
+// share them in turn and adds their gradients in registers.  Wave w has the
+// keys of tiles DT w .. DT w + DT - 1 of all rows (a row in a lane, its keys in
+// the registers), and of the 64 x 64 products the columns 16 w .. 16 w + 15 of
+// both triangles.
+template <class T, int W, bool E>
+__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
+                                                          const float *__restrict__ states, const float *__restrict__ rhos,
+                                                          const float *__restrict__ dstates, const float *__restrict__ omega,
+                                                          DeltaGradPtrs to) {
+    typedef typename Form<T>::Mid Mid;
+    typedef typename Form<T>::In In;
+    constexpr uint32_t DT = W >= 64 ? W / 64 : 1, kTiles = W / 16;
+    __shared__ GradShared<T, W> sh;
+    const uint32_t item = first + blockIdx.x, slot = item / a.kheads, khead = item % a.kheads;
+    const Chunk c = find_chunk(a.offsets, a.num_seqs, a.tokens, kChunkShift, slot);
+    const uint32_t rows = c.hi - c.lo;
+    if (rows == 0u) return;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
+    const uint32_t row = threadIdx.x >> 2, part = (threadIdx.x & 3u) * 8u;
+    const bool works = wave * DT < kTiles;
+    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    {
+        float ks = fill_rows<T, W>(sh.k, a.k, a.k_stride, khead, a.key_dim, c.lo, rows);
+        float qs = fill_rows<T, W>(sh.q, a.q, a.q_stride, khead, a.key_dim, c.lo, rows);
+        ks += dpp<kQuadSwap2>(ks);
+        ks += dpp<kQuadSwap1>(ks);
+        qs += dpp<kQuadSwap2>(qs);
+        qs += dpp<kQuadSwap1>(qs);
+        if ((threadIdx.x & 3u) == 0u) {
+            sh.nu[row] = a.unit ? 1.0f / __builtin_sqrtf(ks + a.eps) : 1.0f;
+            sh.mu[row] = a.unit ? 1.0f / __builtin_sqrtf(qs + a.eps) : 1.0f;
+        }
+    }
+    __syncthreads();
+    // k_j k_i and k_j q_i, rows j in the registers, i = 16 wave + n in the lane
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = none;
+#pragma unroll
+    for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
+        const auto kb = sh.k.along(16u * wave + n, col + 8u * q), qb = sh.q.along(16u * wave + n, col + 8u * q);
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            if (t > wave) continue;
+            const auto ka = sh.k.along(16u * t + n, col + 8u * q);
+            mma(kk[t], ka, kb);
+            mma(qk[t], ka, qb);
+        }
+    }
+    f32x4 dq[DT][4], dk[DT][4];  // with respect to the keys and queries of length 1
+#pragma unroll
+    for (uint32_t d = 0; d < DT; ++d)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dq[d][t] = dk[d][t] = none;
+    const uint32_t per = a.heads / a.kheads;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim, rows_of = (uint64_t)a.heads * a.value_dim;
+    for (uint32_t j = 0; j < per; ++j) {
+        const uint32_t head = khead * per + j;
+        const double sums = running_decay(a, head, c.lo, rows, lane);
+        const float own_beta = row < rows ? a.beta[(int64_t)(c.lo + row) * a.beta_stride + head] : 0.0f;
+        __syncthreads();  // the head before is done with
+        if (wave == 0u) sh.sum[lane] = sums;
+        if ((threadIdx.x & 3u) == 0u) sh.beta[row] = own_beta;
+        const float *state = states + ((uint64_t)slot * a.heads + head) * cells;
+        const float *dstate = dstates + ((uint64_t)slot * a.heads + head) * cells;
+        f32x4 qs[DT][4], rs[DT][4], ends[DT][4], e1[5], e2[5];
+#pragma unroll
+        for (uint32_t d = 0; d < DT; ++d)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) qs[d][t] = rs[d][t] = ends[d][t] = none;
+#pragma unroll
+        for (int t = 0; t < 5; ++t) e1[t] = e2[t] = none;
+        float dot = 0.0f, dbeta = 0.0f;
+        for (uint32_t v0 = 0; v0 < a.value_dim; v0 += 32u) {
+            {
+                float u[8] = {}, w[8] = {}, o[8] = {};
+                const uint64_t at = ((uint64_t)(c.lo + row) * a.heads + head) * a.value_dim;
+                if (row < rows) {
+                    load8<float>(u, rhos + at, v0 + part, a.value_dim);
+                    load8<float>(w, omega + at, v0 + part, a.value_dim);
+                    load8<T>(o, dout + at, v0 + part, a.value_dim);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dbeta = __builtin_fmaf(u[i], w[i], dbeta);
+                    u[i] *= own_beta;
+                    w[i] *= own_beta;
+                }
+                if (row < rows) {
+                    T *p = static_cast<T *>(to.dv) + at + v0 + part;
+                    if (E || v0 + part + 8u <= a.value_dim) {
+                        Pack<T, 8> r;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r.v[i] = (T)w[i];
+                        if (v0 + part < a.value_dim) *reinterpret_cast<Pack<T, 8> *>(p) = r;
+                    } else {
+#pragma unroll
+                        for (uint32_t i = 0; i < 8u; ++i)
+                            if (v0 + part + i < a.value_dim) p[i] = (T)w[i];
+                    }
+                }
+                if (v0) __syncthreads();  // the columns before are read
+                sh.in.dout.put(row, part, o);
+                sh.in.u.put(row, part, u);
+                sh.in.dr.put(row, part, w);
+            }
+            __syncthreads();
+            Mid S[DT], D[DT];
+#pragma unroll
+            for (uint32_t d = 0; d < DT; ++d) {
+                float s[8] = {}, g[8] = {};
+                const uint32_t key = place(wave * DT + d, n);
+                if (works && key < a.key_dim) {
+                    load8<float>(s, state + key * a.value_dim, v0 + 8u * q, a.value_dim);
+                    load8<float>(g, dstate + key * a.value_dim, v0 + 8u * q, a.value_dim);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(s[i], g[i], dot);
+                operand_of(S[d], s);
+                operand_of(D[d], g);
+            }
+            const auto own_o = sh.in.dout.along(16u * wave + n, 8u * q);
+            const auto own_u = sh.in.u.along(16u * wave + n, 8u * q), own_r = sh.in.dr.along(16u * wave + n, 8u * q);
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const auto o = sh.in.dout.along(16u * t + n, 8u * q);
+                const auto u = sh.in.u.along(16u * t + n, 8u * q), r = sh.in.dr.along(16u * t + n, 8u * q);
+                if (works) {
+#pragma unroll
+                    for (uint32_t d = 0; d < DT; ++d) {
+                        mma(qs[d][t], S[d], o);
+                        mma(rs[d][t], S[d], r);
+                        mma(ends[d][t], D[d], u);
+                    }
+                }
+                if (t <= wave) {
+                    mma(e1[t], u, own_o);
+                    mma(e2[t], u, own_r);
+                }
+                if (t >= wave) {
+                    mma(e1[t + 1], o, own_u);
+                    mma(e2[t + 1], r, own_u);
+                }
+            }
+        }
+        dbeta += dpp<kQuadSwap2>(dbeta);
+        dbeta += dpp<kQuadSwap1>(dbeta);
+        if (row < rows && (threadIdx.x & 3u) == 0u) to.dbeta[(uint64_t)(c.lo + row) * a.heads + head] = dbeta;
+        dot = wave_total(dot);
+        __syncthreads();  // the last columns are read
+        if (lane == 0u) sh.dot[wave] = dot;
+        const double all = sh.sum[kChunk - 1u];
+        // the parts that a state has, their factors, and their sums with q and k
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            const uint32_t at = 16u * t + n;
+            const double G = sh.sum[at];
+            const float e = exp_hw((float)G), tail = exp_hw((float)(all - G)), nu = sh.nu[at], mu = sh.mu[at];
+            float query = 0.0f, key = 0.0f, end = 0.0f;
+            if (works) {
+#pragma unroll
+                for (uint32_t d = 0; d < DT; ++d) {
+                    const uint32_t col = place(wave * DT + d, 4u * q);
+                    const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+                    qs[d][t] *= a.scale * e;
+                    rs[d][t] *= e;
+                    ends[d][t] *= tail;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        query = __builtin_fmaf(qv[i], qs[d][t][i], query);
+                        key = __builtin_fmaf(kv[i], rs[d][t][i], key);
+                        end = __builtin_fmaf(kv[i], ends[d][t][i], end);
+                    }
+                    dq[d][t] += qs[d][t];
+                    dk[d][t] += ends[d][t] - rs[d][t];
+                }
+            }
+            query = column_total(query), key = column_total(key), end = column_total(end);
+            if (q == 0u) {
+                sh.part.query[wave][at] = query * mu;
+                sh.part.key[wave][at] = key * nu;
+                sh.part.end[wave][at] = end * nu;
+            }
+        }
+        // the triangles: e1, e2 become dqk and dkk, and the pairs' sums of z
+        const uint32_t own = 16u * wave + n;
+        const double G_own = sh.sum[own];
+        const float nu_own = sh.nu[own], mu_own = sh.mu[own];
+        float pairs[16], before = 0.0f;
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            float z[4] = {};
+            if (t <= wave) {
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i) {
+                    const uint32_t at = 16u * t + 4u * q + i;  // j
+                    const float f = at <= own ? exp_hw((float)(G_own - sh.sum[at])) * sh.nu[at] : 0.0f;
+                    e1[t][i] *= a.scale * f;
+                    e2[t][i] = at < own ? -f * e2[t][i] : 0.0f;
+                    z[i] = e1[t][i] * qk[t][i] * mu_own + e2[t][i] * kk[t][i] * nu_own;
+                }
+            }
+            // sums over the rows before each, this tile's and those of the tiles before
+            float upto = 0.0f;
+            const float four = (z[0] + z[1]) + (z[2] + z[3]);
+#pragma unroll
+            for (uint32_t p = 0; p < 3u; ++p) {
+                const float v = shuffle(four, n + 16u * p);
+                if (q > p) upto += v;
+            }
+            upto += before;
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i) {
+                pairs[4 * t + i] = 16u * t + 4u * q + i <= own ? upto : 0.0f;
+                upto += z[i];
+            }
+            before += column_total(four);
+        }
+        const float pair = row_sums(pairs, lane);  // lane n of quarter q: tile n >> 2, row 4 q + (n & 3)
+        sh.part.pair[wave][16u * (n >> 2) + 4u * q + (n & 3u)] = pair;
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            if (t < wave) continue;
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i) {
+                const uint32_t at = 16u * t + 4u * q + i;  // i; the lane has j
+                const float f = at >= own ? exp_hw((float)(sh.sum[at] - G_own)) : 0.0f;
+                e1[t + 1][i] *= a.scale * f * sh.mu[at];
+                e2[t + 1][i] = at > own ? -f * sh.nu[at] * e2[t + 1][i] : 0.0f;
+            }
+        }
+        __syncthreads();
+        if (wave == 0u) {
+            auto four = [&](const float(&p)[4][kChunk]) { return (p[0][lane] + p[1][lane]) + (p[2][lane] + p[3][lane]); };
+            double after = (double)four(sh.part.query) - (double)four(sh.part.key), ends_before = four(sh.part.end);
+#pragma unroll
+            for (uint32_t by = 1u; by < 64u; by *= 2u) {
+                const double up = shuffle(after, lane + by), down = shuffle(ends_before, lane - by);
+                if (lane + by < 64u) after += up;
+                if (lane >= by) ends_before += down;
+            }
+            const double whole = exp_hw((float)all) * ((sh.dot[0] + sh.dot[1]) + (sh.dot[2] + sh.dot[3]));
+            double prior = shuffle(ends_before, lane - 1u);  // up to the row before
+            if (lane == 0u) prior = 0.0;
+            if (lane < rows)
+                to.dg[(uint64_t)(c.lo + lane) * a.heads + head] = (float)(four(sh.part.pair) + after + prior + whole);
+        }
+        // dqk K, dkk K, dqk^T Q, dkk^T K, one triangle in shared memory at a time
+#pragma unroll
+        for (uint32_t which = 0; which < 4u; ++which) {
+            const bool upper = which >= 2u;
+            __syncthreads();
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s) {
+                if (upper ? s < (wave >> 1) : s > (wave >> 1)) continue;
+                f32x4 pair_of[2];
+#pragma unroll
+                for (uint32_t h = 0; h < 2u; ++h) {
+                    const uint32_t t = 2u * s + h;
+                    const bool there = upper ? t >= wave : t <= wave;
+                    const f32x4 v = which == 0u ? e1[t] : which == 1u ? e2[t] : which == 2u ? e1[t + 1] : e2[t + 1];
+                    pair_of[h] = there ? v : none;
+                }
+                sh.triangle[upper ? upper_at(wave, s) : lower_at(wave, s)][lane] = operand_of<Mid>(pair_of[0], pair_of[1]);
+            }
+            __syncthreads();
+            if (!works) continue;
+#pragma unroll
+            for (uint32_t s = 0; s < 2u; ++s)
+#pragma unroll
+                for (uint32_t d = 0; d < DT; ++d) {
+                    const In keys = which == 2u ? sh.q.across(s, wave * DT + d, lane) : sh.k.across(s, wave * DT + d, lane);
+#pragma unroll
+                    for (uint32_t t = 0; t < 4u; ++t) {
+                        if (upper ? s < (t >> 1) : s > (t >> 1)) continue;
+                        const Mid m = sh.triangle[upper ? upper_at(t, s) : lower_at(t, s)][lane];
+                        mma(which == 0u ? dq[d][t] : dk[d][t], keys, m);
+                    }
+                }
+        }
+    }
+    if (a.unit) {
+        // dq = mu (dq - q (q dq)) of q by its length
+        __syncthreads();
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) {
+            const uint32_t at = 16u * t + n;
+            float query = 0.0f, key = 0.0f;
+            if (works) {
+#pragma unroll
+                for (uint32_t d = 0; d < DT; ++d) {
+                    const uint32_t col = place(wave * DT + d, 4u * q);
+                    const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        query = __builtin_fmaf(qv[i], dq[d][t][i], query);
+                        key = __builtin_fmaf(kv[i], dk[d][t][i], key);
+                    }
+                }
+            }
+            query = column_total(query), key = column_total(key);
+            if (q == 0u) sh.part.query[wave][at] = query, sh.part.key[wave][at] = key;
+        }
+        __syncthreads();
+    }
+    if (!works) return;
+#pragma unroll
+    for (uint32_t t = 0; t < 4u; ++t) {
+        const uint32_t at = 16u * t + n;
+        float nu = 1.0f, mu = 1.0f, query = 0.0f, key = 0.0f;
+        if (a.unit) {
+            auto four = [&](const float(&p)[4][kChunk]) { return (p[0][at] + p[1][at]) + (p[2][at] + p[3][at]); };
+            nu = sh.nu[at], mu = sh.mu[at];
+            query = four(sh.part.query) * mu * mu, key = four(sh.part.key) * nu * nu;
+        }
+        if (at >= rows) continue;
+#pragma unroll
+        for (uint32_t d = 0; d < DT; ++d) {
+            const uint32_t col = place(wave * DT + d, 4u * q);
+            if (col >= a.key_dim) continue;
+            const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+            const uint64_t to_row = ((uint64_t)(c.lo + at) * a.kheads + khead) * a.key_dim + col;
+            Pack<T, 4> wq, wk;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wq.v[i] = (T)(mu * __builtin_fmaf(-qv[i], query, dq[d][t][i]));
+                wk.v[i] = (T)(nu * __builtin_fmaf(-kv[i], key, dk[d][t][i]));
+            }
+            T *pq = static_cast<T *>(to.dq) + to_row, *pk = static_cast<T *>(to.dk) + to_row;
+            if (E || col + 4u <= a.key_dim) {
+                *reinterpret_cast<Pack<T, 4> *>(pq) = wq;
+                *reinterpret_cast<Pack<T, 4> *>(pk) = wk;
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i)
+                    if (col + i < a.key_dim) pq[i] = wq.v[i], pk[i] = wk.v[i];
+            }
+        }
+    }
+}
+
+}  // namespace
+
+template <class T>
+ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, const void *dout, const float *dfinal,
+                         const float *checkpoints, const ps_delta_grads *grads, hipStream_t s) {
+    const DeltaArgs a = delta_args(in);
+    PlainWs plan;
+    const size_t prepared_at = plan.take((size_t)a.slots * a.heads * sizeof(Prepared<T>));
+    Segments seg{};
+    const bool wide = a.key_dim <= 128u && a.value_dim > 64u;
+    seg.shift = segment_shift(a, wide ? 128u : 64u);
+    const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
+    const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u, state_floats = (uint64_t)a.slots * a.heads * cells;
+    const size_t m_at = plan.take(linked * a.key_dim * a.key_dim * 4u), n_at = plan.take(linked * cells * 4u);
+    const size_t d_at = plan.take(state_floats * 4u), omega_at = plan.take((size_t)a.tokens * a.heads * a.value_dim * 4u);
+    bool query = false;
+    ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
+    if (st != PS_OK || query) return st;
+    if ((st = delta_pointers(in)) != PS_OK) return st;
+    if (!grads) return PS_ERR_NULL;
+    if (in->tokens && (!dout || !checkpoints || !grads->dq || !grads->dk || !grads->dv || !grads->dg || !grads->dbeta))
+        return PS_ERR_NULL;
+    if (!aligned(ws, 16) || !aligned(dout, sizeof(T)) || !aligned(dfinal, 4) || !aligned(checkpoints, 4) ||
+        !aligned(grads->dq, sizeof(T)) || !aligned(grads->dk, sizeof(T)) || !aligned(grads->dv, sizeof(T)) ||
+        !aligned(grads->dg, 4) || !aligned(grads->dbeta, 4) || !aligned(grads->dinitial, 4))
+        return PS_ERR_ALIGNMENT;
+    const DeltaBytes n(in);
+    const size_t kept = ps_gated_delta_checkpoint_floats(in->tokens, a.num_seqs, a.heads, a.key_dim, a.value_dim) * 4u;
+    if (outputs_overlap({{grads->dq, n.keys}, {grads->dk, n.keys}, {grads->dv, n.values}, {grads->dg, n.gates},
+                         {grads->dbeta, n.gates}, {grads->dinitial, n.states}},
+                        {{in->q, n.q}, {in->k, n.k}, {in->v, n.v}, {in->g, n.g}, {in->beta, n.beta}, {in->offsets, n.offsets},
+                         {in->initial, n.states}, {dout, n.values}, {dfinal, n.states}, {checkpoints, kept}}))
+        return PS_ERR_ALIAS;
+    if (!a.num_seqs) return PS_OK;
+    Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
+    seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
+    float *dstates = ws_at<float>(ws, d_at), *omega = ws_at<float>(ws, omega_at);
+    const T *g = static_cast<const T *>(dout);
+    const BackResults to = {dfinal, grads->dinitial, dstates, omega};
+    const DeltaGradPtrs out = {grads->dq, grads->dk, grads->dv, grads->dg, grads->dbeta};
+    return with_key_width(a.key_dim, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        timing_begin(s);
+        launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+            hipLaunchKernelGGL((delta_prepare_kernel<T, W, true>), dim3(grid), dim3(256), 0, s, a, first, prepared,
+                               ws_counter(ws), plan.words());
+        });
+        auto walk = [&](auto ct, auto eights) {
+            constexpr int CT = decltype(ct)::value;
+            constexpr bool E = decltype(eights)::value;
+            const uint64_t blocks = ceil_div(a.value_dim, 64u * CT), all = blocks + ceil_div(a.key_dim, 64u * CT);
+            if (linked) {
+                launch_in_parts(segments * a.heads, all, 512u, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared,
+                                       seg, g, true, to);
+                });
+                const uint64_t columns = ceil_div(a.value_dim, 64u);
+                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(256), 0, s, a, first, seg, dfinal);
+                });
+            }
+            launch_in_parts(segments * a.heads, blocks, 512u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared, seg,
+                                   g, false, to);
+            });
+            launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 256u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_grads_kernel<T, W, E>), dim3(grid), dim3(256), 0, s, a, first, g, checkpoints,
+                                   checkpoints + state_floats, dstates, omega, out);
+            });
+        };
+        const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
+        auto shape = [&](auto e) {
+            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 2 : 1>(), e);
+            else walk(std::integral_constant<int, 1>(), e);
+        };
+        if (eights) shape(std::true_type());
+        else shape(std::false_type());
+        timing_end(s);
+        return launch_status();
+    });
+}
+
+}  // namespace dwps

@@ -161,11 +161,11 @@ __device__ __forceinline__ uint32_t token_at(uint32_t s, uint32_t q, uint32_t j)
 }
 
 // kChunk rows of `W` columns of activations in shared memory.
-template <class T, int W>
+template <class T, int W, int PAD = Form<T>::pad>
 struct RowTile {
     typedef Form<T> F;
     typedef typename F::Word Word;
-    static constexpr int kStride = W + F::pad;
+    static constexpr int kStride = W + PAD;
     Word w[F::planes][kChunk][kStride];
 
     __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8]) {
@@ -604,6 +604,11 @@ struct DeltaBytes {
         gates = in->tokens * in->heads * 4u;
     }
 };
+
+// ps_gated_delta_bwd of one type, after delta_sizes.
+template <class T>
+ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, const void *dout, const float *dfinal,
+                         const float *checkpoints, const ps_delta_grads *grads, hipStream_t stream);
 
 // Calls f with the padded number of keys as a constant.
 template <class F>

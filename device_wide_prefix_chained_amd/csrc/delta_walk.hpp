@@ -42,6 +42,96 @@ struct WalkResults {
     float *final, *states, *rhos;
 };
 
+// The feeding waves of a walk: keys, queries, values and what was prepared of
+// each chunk, from memory into registers while the chunk before is worked on,
+// then into the tile.
+template <class T, int W, int CT, bool E>
+struct DeltaFeed {
+    typedef WalkTile<T, W, CT> Tile;
+    const DeltaArgs &a;
+    const Prepared<T> *prepared;
+    Chunk r;
+    uint32_t base, head, khead, block0;  // of the first chunk; the head and its keys'; the block's first column
+    const T *values;                     // of the head
+    int64_t values_stride;
+
+    // LEAD: no queries and no scores.  order(i): the i-th chunk to come.
+    template <bool LEAD, class F, class O>
+    __device__ __forceinline__ void run(uint32_t chunks, bool with_values, F tile, O order) const {
+        constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
+        constexpr uint32_t kKeys = (W + 31) / 32, kVals = Tile::kCols / 32u;
+        constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
+        const uint32_t thread = threadIdx.x - 256u, row = thread >> 2, part = (thread & 3u) * 8u;
+        Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
+        u32x4 ps[kWords];
+        auto fetch = [&](uint32_t i) {
+            const int64_t lo = r.lo + i * kChunk;
+            const bool is = lo + row < r.hi;
+            const T *k0 = static_cast<const T *>(a.k) + lo * a.k_stride + (uint64_t)khead * a.key_dim;
+            const T *q0 = static_cast<const T *>(a.q) + lo * a.q_stride + (uint64_t)khead * a.key_dim;
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) {
+                ks[c] = raw8<E, T>(k0 + row * a.k_stride, k0, is, part + 32u * c, a.key_dim);
+                if (!LEAD) qs[c] = raw8<E, T>(q0 + row * a.q_stride, q0, is, part + 32u * c, a.key_dim);
+            }
+            if constexpr (kV) {
+                const T *v0 = values + lo * values_stride;
+#pragma unroll
+                for (uint32_t c = 0; c < kVals; ++c)
+                    vs[c] = raw8<E, T>(v0 + row * values_stride, v0, is && with_values, block0 + part + 32u * c, a.value_dim);
+            }
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(&prepared[(uint64_t)(base + i) * a.heads + head]);
+#pragma unroll
+            for (uint32_t c = 0; c < kWords; ++c) {
+                const uint32_t at = thread + 256u * c;
+                if (at < kBytes / 16u) ps[c] = p[at];
+            }
+        };
+        auto leave = [&](Tile *to) {
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) {
+                float v[8];
+                values_of<T>(v, ks[c]);
+                to->k.put(row, part + 32u * c, v);
+                if (!LEAD) {
+                    values_of<T>(v, qs[c]);
+                    to->q.put(row, part + 32u * c, v);
+                }
+            }
+            if constexpr (kV) {
+#pragma unroll
+                for (uint32_t c = 0; c < kVals; ++c) *reinterpret_cast<Pack<T, 8> *>(&to->v[row][part + 32u * c]) = vs[c];
+            }
+#pragma unroll
+            for (uint32_t c = 0; c < kWords; ++c) {
+                const uint32_t at = thread + 256u * c;
+                if (at < kBytes / 16u) reinterpret_cast<u32x4 *>(&to->p)[at] = ps[c];
+            }
+        };
+        if (chunks) fetch(order(0u)), leave(tile(0u));
+        __syncthreads();
+        for (uint32_t i = 0; i < chunks; ++i) {
+            const bool more = i + 1u < chunks;
+            if (more) fetch(order(i + 1u));
+            if (!kTwo) __syncthreads();
+            if (more) leave(tile(i + 1u));
+            __syncthreads();
+        }
+    }
+};
+
+// The unit matrix's columns.
+template <int CT, int TILES>
+__device__ __forceinline__ void unit_states(f32x4 (&S)[CT][TILES], uint32_t col0, uint32_t lane) {
+#pragma unroll
+    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+#pragma unroll
+            for (uint32_t i = 0; i < 4u; ++i)
+                S[ct][t][i] = place(t, 4u * (lane >> 4) + i) == col0 + column<CT>(ct, lane & 15u) ? 1.0f : 0.0f;
+}
+
 // Four waves walk over a segment's chunks, each with 16 CT columns of a head's
 // state; four feed them, loading a chunk while the one before is worked on and
 // leaving it in the tile of the two that is not in use (or, where shared memory
@@ -68,67 +158,9 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);  // its first chunk's number
     const T *values = static_cast<const T *>(a.v) + (uint64_t)head * a.value_dim;
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
+    const DeltaFeed<T, W, CT, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
     if (wave >= 4u) {
-        // the feeding waves
-        constexpr uint32_t kKeys = (W + 31) / 32, kVals = kCols / 32u;
-        constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
-        const uint32_t thread = threadIdx.x - 256u, row = thread >> 2, part = (thread & 3u) * 8u;
-        Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
-        u32x4 ps[kWords];
-        auto fetch = [&](uint32_t i) {
-            const int64_t lo = r.lo + i * kChunk;
-            const bool is = lo + row < r.hi;
-            const T *k0 = static_cast<const T *>(a.k) + lo * a.k_stride + (uint64_t)khead * a.key_dim;
-            const T *q0 = static_cast<const T *>(a.q) + lo * a.q_stride + (uint64_t)khead * a.key_dim;
-#pragma unroll
-            for (uint32_t c = 0; c < kKeys; ++c) {
-                ks[c] = raw8<E, T>(k0 + row * a.k_stride, k0, is, part + 32u * c, a.key_dim);
-                if (!LEAD) qs[c] = raw8<E, T>(q0 + row * a.q_stride, q0, is, part + 32u * c, a.key_dim);
-            }
-            if constexpr (kV) {
-                const T *v0 = values + lo * a.v_stride;
-#pragma unroll
-                for (uint32_t c = 0; c < kVals; ++c)
-                    vs[c] = raw8<E, T>(v0 + row * a.v_stride, v0, is && !unit, block0 + part + 32u * c, a.value_dim);
-            }
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(&prepared[(uint64_t)(base + i) * a.heads + head]);
-#pragma unroll
-            for (uint32_t c = 0; c < kWords; ++c) {
-                const uint32_t at = thread + 256u * c;
-                if (at < kBytes / 16u) ps[c] = p[at];
-            }
-        };
-        auto leave = [&](uint32_t i) {
-            Tile *to = tile(i);
-#pragma unroll
-            for (uint32_t c = 0; c < kKeys; ++c) {
-                float v[8];
-                values_of<T>(v, ks[c]);
-                to->k.put(row, part + 32u * c, v);
-                if (!LEAD) {
-                    values_of<T>(v, qs[c]);
-                    to->q.put(row, part + 32u * c, v);
-                }
-            }
-            if constexpr (kV) {
-#pragma unroll
-                for (uint32_t c = 0; c < kVals; ++c) *reinterpret_cast<Pack<T, 8> *>(&to->v[row][part + 32u * c]) = vs[c];
-            }
-#pragma unroll
-            for (uint32_t c = 0; c < kWords; ++c) {
-                const uint32_t at = thread + 256u * c;
-                if (at < kBytes / 16u) reinterpret_cast<u32x4 *>(&to->p)[at] = ps[c];
-            }
-        };
-        if (chunks) fetch(0u), leave(0u);
-        __syncthreads();
-        for (uint32_t i = 0; i < chunks; ++i) {
-            const bool more = i + 1u < chunks;
-            if (more) fetch(i + 1u);
-            if (!kTwo) __syncthreads();
-            if (more) leave(i + 1u);
-            __syncthreads();
-        }
+        feed.template run<LEAD>(chunks, !unit, tile, [](uint32_t i) { return i; });
         return;
     }
     const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
@@ -139,15 +171,7 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
         if (!LEAD && r.index) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
         else if (!LEAD && a.initial) from = a.initial + ((uint64_t)r.seq * a.heads + head) * cells;
         load_states<E>(S, from, a.key_dim, a.value_dim, col0, lane);
-        if (unit) {
-#pragma unroll
-            for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
-#pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t)
-#pragma unroll
-                    for (uint32_t i = 0; i < 4u; ++i)
-                        S[ct][t][i] = place(t, 4u * q + i) == col0 + column<CT>(ct, m) ? 1.0f : 0.0f;
-        }
+        if (unit) unit_states(S, col0, lane);
     }
     __syncthreads();
     for (uint32_t c = 0; c < chunks; ++c) {
@@ -306,9 +330,11 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
 }
 
 // The states that enter a sequence's segments after the first, S <- M S + N,
-// in the places of N.  A wave has 16 columns.
-template <class T, int W, bool E>
-__global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg) {
+// in the places of N.  BACK: the gradients that enter from the segment after,
+// from the last to the first.  A wave has 16 columns; `start` holds what enters
+// the sequence, or is NULL.
+template <class T, int W, bool E, bool BACK>
+__global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
     constexpr uint32_t kTiles = W / 16;
     const uint32_t blocks = (a.value_dim + 63u) / 64u, item = first + blockIdx.x / blocks, head = item % a.heads;
@@ -319,11 +345,11 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
     const uint32_t segments = (uint32_t)(((uint64_t)(r.hi - r.lo) + (1ull << seg.shift) - 1u) >> seg.shift);
     if (col0 >= a.value_dim || segments < 2u) return;
     f32x4 S[1][kTiles], next[1][kTiles];
-    load_states<E>(S, a.initial ? a.initial + ((uint64_t)s * a.heads + head) * cells : nullptr, a.key_dim, a.value_dim, col0, lane);
-    float *n = seg.n + ((uint64_t)r.base * a.heads + head) * cells;
-    const float *mat = seg.m + ((uint64_t)r.base * a.heads + head) * key_cells;
-    load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
+    load_states<E>(S, start ? start + ((uint64_t)s * a.heads + head) * cells : nullptr, a.key_dim, a.value_dim, col0, lane);
+    auto number = [&](uint32_t i) { return (uint64_t)(r.base + (BACK ? segments - 1u - i : i)) * a.heads + head; };
+    load_states<E>(next, seg.n + number(0u) * cells, a.key_dim, a.value_dim, col0, lane);
     for (uint32_t i = 0; i + 1u < segments; ++i) {
+        const float *mat = seg.m + number(i) * key_cells;
         Mid h[kTiles / 2];
 #pragma unroll
         for (uint32_t c = 0; c < kTiles / 2u; ++c) h[c] = operand_of<Mid>(S[0][2u * c], S[0][2u * c + 1u]);
@@ -340,8 +366,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
                 mma(S[0][t], o, h[c]);
             }
         }
-        n += a.heads * cells;
-        mat += a.heads * key_cells;
+        float *n = seg.n + number(i + 1u) * cells;
         if (i + 2u < segments) load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
         store_states<E>(n, S, a.key_dim, a.value_dim, col0, lane);
     }
@@ -425,8 +450,8 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                 });
                 const uint64_t columns = ceil_div(a.value_dim, 64u);
                 launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_link_kernel<T, W, E>), dim3(grid), dim3(256), 0, s, a,
-                                       first, seg);
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, false>), dim3(grid), dim3(256), 0, s, a, first, seg,
+                                       a.initial);
                 });
             }
             launch_in_parts(segments * a.heads, blocks, 512u, [&](uint32_t first, uint32_t grid) {

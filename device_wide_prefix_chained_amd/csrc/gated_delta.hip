@@ -185,6 +185,16 @@ extern "C" ps_status ps_gated_delta(void *ws, size_t *ws_bytes, const ps_delta_i
     });
 }
 
+extern "C" ps_status ps_gated_delta_bwd(void *ws, size_t *ws_bytes, const ps_delta_input *in, const void *dout,
+                                        const float *dfinal, const float *checkpoints, const ps_delta_grads *grads,
+                                        void *stream) {
+    ps_status st = delta_sizes(in);
+    if (st != PS_OK) return st;
+    return with_type(in->dtype, [&](auto zero) {
+        return delta_backward<decltype(zero)>(ws, ws_bytes, in, dout, dfinal, checkpoints, grads, static_cast<hipStream_t>(stream));
+    });
+}
+
 extern "C" ps_status ps_gated_delta_step(const ps_delta_input *in, const float *state, float *new_state,
                                          const int32_t *slots, uint32_t pool, void *out, void *stream) {
     ps_delta_input one;

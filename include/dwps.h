@@ -733,6 +733,18 @@ uint64_t ps_gated_delta_checkpoint_floats(uint64_t tokens, uint32_t num_seqs, ui
  * that many floats. */
 ps_status ps_gated_delta(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final,
                          float *checkpoints, void *stream);
+/* Gradients of out and final given dout (packed) and dfinal ([num_seqs, heads,
+ * key_dim, value_dim], NULL = zero), from the checkpoints that ps_gated_delta
+ * wrote for the same input: dq, dk [tokens, kheads, key_dim] and dv [tokens,
+ * heads, value_dim] in the activations' type; dg, dbeta [tokens, heads] and
+ * dinitial [num_seqs, heads, key_dim, value_dim] in fp32.  dinitial may be
+ * NULL. */
+typedef struct ps_delta_grads {
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dinitial;
+} ps_delta_grads;
+ps_status ps_gated_delta_bwd(void *ws, size_t *ws_bytes, const ps_delta_input *in, const void *dout, const float *dfinal,
+                             const float *checkpoints, const ps_delta_grads *grads, void *stream);
 /* One token for each of in->tokens rows, with state and new_state [pool,
  * heads, key_dim, value_dim] in fp32; slots as in ps_causal_conv_step.
  * in->offsets, in->initial and in->num_seqs are not used. */

@@ -98,6 +98,36 @@ def test_delta(dw, case):
     assert (out.cpu()[_outside(cuts, T)] == 7.0).all()
 
 
+@pytest.mark.parametrize("case", DELTA, ids=str)
+def test_delta_gradients(dw, case):
+    """From dout alone and, where there are initial states, from dfinal too."""
+    T, cuts, KH, H, K, V, dtype, normalize, initial, wide = case
+    say("gated delta, gradients", case)
+    m = DeltaMaker(T + K + V, dtype, wide)
+    off = _offsets(cuts)
+    seqs = 1 if cuts is None else len(cuts) - 1
+    a, more = delta_inputs(m, T, KH, H, K, V, normalize, initial, seqs)
+    dout = m.act(T, H, V, packed=True)
+    dfinal = m.par(seqs, H, K, V, scale=0.3) if initial else None
+    kept = torch.full((dw.ps_gated_delta_checkpoint_floats(T, seqs, H, K, V),), float("nan"), device="cuda")
+    out = torch.zeros(T, H, V, dtype=dtype, device="cuda")
+    dw.ps_gated_delta(**a, **more, offsets=off, out=out, checkpoints=kept)
+    again = torch.zeros_like(out)
+    dw.ps_gated_delta(**a, **more, offsets=off, out=again)
+    assert torch.equal(out, again)
+    g = dw.ps_gated_delta_bwd(**a, **more, offsets=off, dout=dout, checkpoints=kept, dfinal=dfinal)
+    torch.cuda.synchronize()
+    want, bound = ref.delta(**a, **more, offsets=off, dout=dout, dfinal=dfinal, dtype=dtype)
+    rows = _finite_rows(cuts, T)
+    assert (g.dinitial is not None) == initial
+    for name in g._fields:
+        if name == "dinitial":
+            if initial:
+                ref.close(name, g.dinitial, want[name], bound[name])
+        else:
+            ref.close(name, getattr(g, name)[rows], want[name][rows], bound[name][rows])
+
+
 STEP = [  # batch, pool, kheads, heads, key_dim, value_dim, type, normalize, slots, strided
     (1, 1, 1, 1, 1, 1, F32, False, False, False),
     (7, 9, 2, 4, 40, 36, BF16, True, True, True),
