@@ -31,26 +31,6 @@ struct BackResults {
     float *omega;         // [tokens, heads, value_dim]
 };
 
-// Eight rows token_at(s, q, ..) of a column of a value tile.
-template <class T, uint32_t STRIDE>
-__device__ __forceinline__ void value_rows(float (&v)[8], const T (*tile)[STRIDE], uint32_t s, uint32_t q, uint32_t m,
-                                           uint32_t here, uint32_t ct, bool pairs) {
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t at = here + (pairs ? 8u * (m & 3u) + 4u * ct : 4u * (m & 3u));
-#pragma unroll
-        for (uint32_t h = 0; h < 2u; ++h) {
-            const i16x4 raw = read_transposed(
-                reinterpret_cast<const uint16_t *>(&tile[32u * s + 16u * h + 4u * q + (m >> 2)][at]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * h + i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
-        }
-    } else {
-        const uint32_t col = here + (pairs ? place(ct, m) : m);
-#pragma unroll
-        for (uint32_t j = 0; j < 8u; ++j) v[j] = tile[token_at(s, q, j)][col];
-    }
-}
-
 // The walk backwards.  lead: the walks for M and N of segments that are not a
 // sequence's first, which keep nothing but their end.
 template <class T, int W, int CT, bool E>
@@ -83,7 +63,9 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     }
     const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
-    f32x4 D[CT][kTiles];
+    constexpr bool kScaled = Form<T>::scaled;
+    f32x4 D[CT][kTiles];  // times `unit_of`, the gradients of the states
+    float unit_of = 1.0f;
     {
         const float *from = nullptr;
         if (!lead && r.hi != seq.hi) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
@@ -97,7 +79,10 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
         const Tile &in = *tile(i);
         if (col0 < width) {
             if (!lead)
-                store_states<E>(to.dstates + ((uint64_t)(base + c) * a.heads + head) * cells, D, a.key_dim, a.value_dim, col0, lane);
+                store_states<E>(to.dstates + ((uint64_t)(base + c) * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim,
+                                col0, lane);
+            const float most = kScaled ? wave_largest(largest(D)) : 0.0f;
+            const Scale of_d = scale_of<kScaled>(most);
             auto numbers = [&](uint32_t which, uint32_t t) {
                 return *reinterpret_cast<const f32x4 *>(&in.p.row[which + 16u * t + 4u * q]);
             };
@@ -111,7 +96,7 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
             for (uint32_t s = 0; s < kTiles / 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(D[ct][2u * s], D[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(D[ct][2u * s], D[ct][2u * s + 1u], of_d.by);
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
                     const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
@@ -119,35 +104,45 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
                     for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], ka, h[ct]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 o[CT][4];  // dO, tile by tile
+            if (!unit) {
+#pragma unroll
+                for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+                    for (uint32_t t = 0; t < 4u; ++t) {
+                        if constexpr (kV) {
+                            o[ct][t] = value_rows<T, CT>(in.v, t, q, m, here, ct);
+                        } else {
+                            const uint32_t col = col0 + column<CT>(ct, m);
+#pragma unroll
+                            for (uint32_t i = 0; i < 4u; ++i) {
+                                const uint32_t row = 16u * t + 4u * q + i;
+                                o[ct][t][i] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
+                            }
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) o[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            const Scale of_o = scale_of<kScaled>(kScaled ? wave_largest(largest(o)) : 0.0f);
+            const float to_x = kScaled ? of_o.by * in.p.row[kRowScores] : 1.0f;
+            const float from_x = kScaled ? of_o.back * in.p.row[kRowScoresBack] : 1.0f;
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 tail = numbers(kRowTail, t);
+                const f32x4 tail = numbers(kRowTail, t) * (of_d.back * unit_of) * to_x;
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) x[ct][t] *= tail;
             }
-            __builtin_amdgcn_sched_barrier(0);
-            auto columns_of = [&](float (&v)[8], uint32_t s, uint32_t ct) {
-                if constexpr (kV) {
-                    value_rows<T, kCols + 8u>(v, in.v, s, q, m, here, ct, CT == 2);
-                } else {
-                    const uint32_t col = col0 + column<CT>(ct, m);
-#pragma unroll
-                    for (uint32_t j = 0; j < 8u; ++j) {
-                        const uint32_t row = token_at(s, q, j);
-                        v[j] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
-                    }
-                }
-            };
             if (!unit) {
 #pragma unroll
                 for (uint32_t s = 0; s < 2u; ++s) {
                     In h[CT];
 #pragma unroll
-                    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-                        float v[8];
-                        columns_of(v, s, ct);
-                        operand_of(h[ct], v);
-                    }
+                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<In>(o[ct][2u * s], o[ct][2u * s + 1u], of_o.by);
 #pragma unroll
                     for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
                         const Mid scores = in.p.scores[upper_at(t, s)][lane];
@@ -158,11 +153,13 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
             }
             __builtin_amdgcn_sched_barrier(0);
             // omega
+            const Scale of_x = scale_of<kScaled>(kScaled ? wave_largest(largest(x)) : 0.0f);
+            const float from_y = kScaled ? of_x.back * from_x * in.p.row[kRowInverse] : 1.0f;
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u], of_x.by);
 #pragma unroll
                 for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
                     const Mid inverse = in.p.inverse[upper_at(t, s)][lane];
@@ -171,26 +168,29 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
                 }
             }
             if (!lead)
-                store_rows<E>(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, rows, col0,
-                              a.value_dim, lane);
+                store_rows<E>(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, from_y, rows,
+                              col0, a.value_dim, lane);
             // D = e_C D + Q^T diag(scale e) dO - K^T diag(e) beta omega
             __builtin_amdgcn_sched_barrier(0);
-            const float whole = in.p.row[kRowWhole];
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) {
+                const f32x4 e = numbers(kRowE, t) * numbers(kRowBeta, t) * -from_y, eq = numbers(kRowQ, t);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= e, o[ct][t] *= eq;
+            }
+            const float kept = unit_of * in.p.row[kRowWhole];
+            const Scale of_y = scale_of_sum<kScaled>(
+                kScaled ? wave_largest(__builtin_fmaxf(largest(y), largest(o))) : 0.0f, most * kept);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) D[ct][t] *= whole;
-#pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 e = numbers(kRowE, t) * numbers(kRowBeta, t);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= -e;
-            }
+                for (uint32_t t = 0; t < kTiles; ++t) D[ct][t] *= kept * of_y.by;
+            unit_of = of_y.back;
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_y.by);
 #pragma unroll
                 for (uint32_t t = 0; t < kTiles; ++t) {
                     const auto ka = in.k.across(s, t, lane);
@@ -202,16 +202,9 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
             if (!unit) {
 #pragma unroll
                 for (uint32_t s = 0; s < 2u; ++s) {
-                    const f32x4 e0 = numbers(kRowQ, 2u * s), e1 = numbers(kRowQ, 2u * s + 1u);
                     Mid h[CT];
 #pragma unroll
-                    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-                        float v[8];
-                        columns_of(v, s, ct);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] *= e0[j], v[4 + j] *= e1[j];
-                        operand_of(h[ct], v);
-                    }
+                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(o[ct][2u * s], o[ct][2u * s + 1u], of_y.by);
 #pragma unroll
                     for (uint32_t t = 0; t < kTiles; ++t) {
                         const auto qa = in.q.across(s, t, lane);
@@ -226,10 +219,10 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     }
     if (col0 >= width) return;
     const uint64_t place_of = (uint64_t)number * a.heads + head;
-    if (unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, D, a.key_dim, a.key_dim, col0, lane);
-    else if (lead) store_states<E>(seg.n + place_of * cells, D, a.key_dim, a.value_dim, col0, lane);
+    if (unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, D, unit_of, a.key_dim, a.key_dim, col0, lane);
+    else if (lead) store_states<E>(seg.n + place_of * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
     else if (to.dinitial && r.lo == seq.lo)
-        store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -260,16 +253,16 @@ __device__ __forceinline__ float column_total(float v) {
 }
 
 // Eight or four keys of a row held by a lane: four of each of its wave's tiles.
-template <class T, int W>
-__device__ __forceinline__ f32x4 four_keys(const RowTile<T, W> &tile, uint32_t row, uint32_t col) {
+template <class F, int W>
+__device__ __forceinline__ f32x4 four_keys(const RowTile<F, W> &tile, uint32_t row, uint32_t col) {
     f32x4 v;
-    if constexpr (sizeof(typename RowTile<T, W>::Word) == 4) {
+    if constexpr (sizeof(typename F::Word) == 4) {
         v = *reinterpret_cast<const f32x4 *>(&tile.w[0][row][col]);
     } else {
         typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
         v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int p = Form<T>::planes - 1; p >= 0; --p) {
+        for (int p = F::planes - 1; p >= 0; --p) {
             const u16x4 r = *reinterpret_cast<const u16x4 *>(&tile.w[p][row][col]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += (float)__builtin_bit_cast(__bf16, (uint16_t)r[i]);
@@ -280,15 +273,15 @@ __device__ __forceinline__ f32x4 four_keys(const RowTile<T, W> &tile, uint32_t r
 
 template <class T, int W>
 struct GradShared {
-    typedef typename Form<T>::Mid Mid;
+    typedef typename Plain<T>::Mid Mid;
     // 32 columns of computed numbers: two planes, or themselves.  256 keys in two
     // planes leave no room for the padding that spreads rows over the banks.
-    static constexpr int kPad = W == 256 && sizeof(RowTile<T, W>) > 66560u ? 0 : Form<T>::pad;
-    typedef RowTile<typename std::conditional<sizeof(T) == 2, f16_t, float>::type, 32, kPad> MidTile;
-    RowTile<T, W> k, q;
+    static constexpr int kPad = W == 256 && sizeof(RowTile<Plain<T>, W>) > 66560u ? 0 : Plain<T>::pad;
+    typedef RowTile<Plain<typename std::conditional<sizeof(T) == 2, f16_t, float>::type>, 32, kPad> MidTile;
+    RowTile<Plain<T>, W> k, q;
     union {
         struct {
-            RowTile<T, 32, kPad> dout;
+            RowTile<Plain<T>, 32, kPad> dout;
             MidTile u, dr;
         } in;
         Mid triangle[kTriangle][64];
@@ -310,8 +303,8 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
                                                           const float *__restrict__ states, const float *__restrict__ rhos,
                                                           const float *__restrict__ dstates, const float *__restrict__ omega,
                                                           DeltaGradPtrs to) {
-    typedef typename Form<T>::Mid Mid;
-    typedef typename Form<T>::In In;
+    typedef typename Plain<T>::Mid Mid;
+    typedef typename Plain<T>::In In;
     constexpr uint32_t DT = W >= 64 ? W / 64 : 1, kTiles = W / 16;
     __shared__ GradShared<T, W> sh;
     const uint32_t item = first + blockIdx.x, slot = item / a.kheads, khead = item % a.kheads;
@@ -323,16 +316,9 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
     const bool works = wave * DT < kTiles;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
     {
-        float ks = fill_rows<T, W>(sh.k, a.k, a.k_stride, khead, a.key_dim, c.lo, rows);
-        float qs = fill_rows<T, W>(sh.q, a.q, a.q_stride, khead, a.key_dim, c.lo, rows);
-        ks += dpp<kQuadSwap2>(ks);
-        ks += dpp<kQuadSwap1>(ks);
-        qs += dpp<kQuadSwap2>(qs);
-        qs += dpp<kQuadSwap1>(qs);
-        if ((threadIdx.x & 3u) == 0u) {
-            sh.nu[row] = a.unit ? 1.0f / __builtin_sqrtf(ks + a.eps) : 1.0f;
-            sh.mu[row] = a.unit ? 1.0f / __builtin_sqrtf(qs + a.eps) : 1.0f;
-        }
+        const float own_nu = fill_rows<T>(sh.k, a.k, a.k_stride, khead, c.lo, rows, a);
+        const float own_mu = fill_rows<T>(sh.q, a.q, a.q_stride, khead, c.lo, rows, a);
+        if ((threadIdx.x & 3u) == 0u) sh.nu[row] = own_nu, sh.mu[row] = own_mu;
     }
     __syncthreads();
     // k_j k_i and k_j q_i, rows j in the registers, i = 16 wave + n in the lane
@@ -464,7 +450,7 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
                 for (uint32_t d = 0; d < DT; ++d) {
                     const uint32_t col = place(wave * DT + d, 4u * q);
-                    const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+                    const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
                     qs[d][t] *= a.scale * e;
                     rs[d][t] *= e;
                     ends[d][t] *= tail;
@@ -593,7 +579,7 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
                 for (uint32_t d = 0; d < DT; ++d) {
                     const uint32_t col = place(wave * DT + d, 4u * q);
-                    const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+                    const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         query = __builtin_fmaf(qv[i], dq[d][t][i], query);
@@ -621,7 +607,7 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
         for (uint32_t d = 0; d < DT; ++d) {
             const uint32_t col = place(wave * DT + d, 4u * q);
             if (col >= a.key_dim) continue;
-            const f32x4 kv = four_keys<T, W>(sh.k, at, col), qv = four_keys<T, W>(sh.q, at, col);
+            const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
             const uint64_t to_row = ((uint64_t)(c.lo + at) * a.kheads + khead) * a.key_dim + col;
             Pack<T, 4> wq, wk;
 #pragma unroll

@@ -21,14 +21,17 @@
 // keys are laid over a pair of tiles by place() instead, so that a lane's eight
 // keys are neighbours.
 //
-// Precision.  The matrix instructions take bf16.  Inputs are whole: one bf16
-// plane for bf16, two for fp16 (11 bits).  fp32 numbers that a chunk computes
-// (states, corrections, inverses) are two planes, a rounding to bf16 and the
-// rounding of what is left: off by at most 2^-18, against 2^-9 of one plane,
-// for which a product takes 2 or 3 instructions (the planes' largest products).
-// All sums are fp32, and so is everything kept from chunk to chunk.  fp32
-// activations use the fp32 matrix instruction throughout (a sixteenth of the
-// rate).
+// Precision.  16-bit activations use the fp16 matrix instruction.  A row of
+// keys or queries is one fp16 plane times a power of two that brings its largest
+// near 2^15 (whole for fp16 and, down to 2^-21 of the row's largest, for bf16).
+// fp32 numbers that a chunk computes (states, corrections, inverses) are two
+// fp16 planes of a common power of two for a wave's tiles, a rounding and the
+// rounding of what is left: off by 2^-22 of the number or 2^-39 of the largest,
+// against 2^-11 of one plane, for which a product takes 2 or 3 instructions (the
+// planes' largest products).  Two planes of bf16 would need no powers of two but
+// hold 16 bits: states came out 2 to 3e-6 off (norms; now 2e-7).  All sums are
+// fp32, and so is everything kept from chunk to chunk.  fp32 activations use the
+// fp32 matrix instruction throughout (a sixteenth of the rate).
 #pragma once
 
 #include "block_device.hpp"
@@ -39,7 +42,6 @@ namespace dwps {
 constexpr uint32_t kChunk = 64u, kChunkShift = 6u;
 constexpr size_t kMostShared = 160u * 1024u;  // of a workgroup
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -63,44 +65,55 @@ struct DeltaArgs {
     float scale, eps;
 };
 
-// Eight places of an operand: N bf16 planes, or the numbers themselves.
-template <int N>
+// Eight places of an operand: N planes of a 16-bit type, or the numbers themselves.
+template <class E, int N>
 struct Planes {
-    bf16x8 p[N];
+    typedef E Eight __attribute__((ext_vector_type(8)));
+    Eight p[N];
 };
 struct Wide {
     float p[8];
 };
 
-// N planes of eight numbers: each the rounding of what the ones before leave.
-template <int N>
-__device__ __forceinline__ Planes<N> planes_of(const float (&v)[8]) {
-    Planes<N> r;
-    float left[8];
+// The operand of eight numbers times `by`: each plane is the rounding of what
+// the ones before leave.
+template <class E, int N>
+__device__ __forceinline__ void operand_of(Planes<E, N> &o, const float (&v)[8], float by = 1.0f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) left[j] = v[j];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r.p[i][j] = (__bf16)left[j];
-            if (i + 1 < N) left[j] -= (float)r.p[i][j];
-        }
+    for (int j = 0; j < 8; ++j) {
+        o.p[0][j] = (E)(v[j] * by);
+        if (N > 1) o.p[N - 1][j] = (E)__builtin_fmaf(v[j], by, -(float)o.p[0][j]);
     }
-    return r;
+}
+__device__ __forceinline__ void operand_of(Wide &o, const float (&v)[8], float = 1.0f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.p[j] = v[j];
+}
+// The operand of two tiles of a result: rows 4 q + r of the first and of the second.
+template <class M>
+__device__ __forceinline__ M operand_of(const f32x4 &a, const f32x4 &b, float by = 1.0f) {
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    M o;
+    operand_of(o, v, by);
+    return o;
 }
 
 // acc += A B over 32 places: the products of planes i and j with i + j below
 // the larger number of planes, smallest first.
-template <int NA, int NB>
-__device__ __forceinline__ void mma(f32x4 &acc, const Planes<NA> &a, const Planes<NB> &b) {
+__device__ __forceinline__ void mma_one(f32x4 &acc, const Planes<bf16_t, 1>::Eight &a, const Planes<bf16_t, 1>::Eight &b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma_one(f32x4 &acc, const Planes<f16_t, 1>::Eight &a, const Planes<f16_t, 1>::Eight &b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
+}
+template <class E, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 &acc, const Planes<E, NA> &a, const Planes<E, NB> &b) {
     constexpr int most = NA > NB ? NA : NB;
 #pragma unroll
     for (int sum = most - 1; sum >= 0; --sum)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (sum - i >= 0 && sum - i < NB)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[sum - i], acc, 0, 0, 0);
+            if (sum - i >= 0 && sum - i < NB) mma_one(acc, a.p[i], b.p[sum - i]);
 }
 __device__ __forceinline__ void mma(f32x4 &acc, const Wide &a, const Wide &b) {
 #pragma unroll
@@ -108,44 +121,84 @@ __device__ __forceinline__ void mma(f32x4 &acc, const Wide &a, const Wide &b) {
 }
 
 // How activations of type T are held in shared memory (planes of words) and
-// become operands; Mid: operands made of computed numbers.
+// become operands; Mid: operands made of computed numbers.  Form is that of the
+// walks, scaled to fp16's range; Plain that of the pass over the chunks'
+// gradients, which sums over columns that it does not have at once, so that no
+// power of two is theirs: bf16 planes, two for fp16 and computed numbers.
 template <class T>
-struct Form;
-template <>
-struct Form<bf16_t> {
+struct Form {
     typedef uint16_t Word;
+    typedef f16_t Part;
+    static constexpr bool scaled = true;
     static constexpr int planes = 1, pad = 8;
-    typedef Planes<1> In;
-    typedef Planes<2> Mid;
+    typedef Planes<f16_t, 1> In;
+    typedef Planes<f16_t, 2> Mid;
 };
-template <>
-struct Form<f16_t> {
+template <class T>
+struct Plain {
     typedef uint16_t Word;
-    static constexpr int planes = 2, pad = 8;
-    typedef Planes<2> In;
-    typedef Planes<2> Mid;
+    typedef bf16_t Part;
+    static constexpr bool scaled = false;
+    static constexpr int planes = std::is_same<T, bf16_t>::value ? 1 : 2, pad = 8;
+    typedef Planes<bf16_t, planes> In;
+    typedef Planes<bf16_t, 2> Mid;
 };
-template <>
-struct Form<float> {
+struct WideForm {
     typedef float Word;
+    typedef float Part;
+    static constexpr bool scaled = false;
     static constexpr int planes = 1, pad = 4;
     typedef Wide In;
     typedef Wide Mid;
 };
+template <>
+struct Form<float> : WideForm {};
+template <>
+struct Plain<float> : WideForm {};
 
-__device__ __forceinline__ void operand_of(Planes<2> &o, const float (&v)[8]) { o = planes_of<2>(v); }
-__device__ __forceinline__ void operand_of(Planes<1> &o, const float (&v)[8]) { o = planes_of<1>(v); }
-__device__ __forceinline__ void operand_of(Wide &o, const float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o.p[j] = v[j];
+// A power of two that brings numbers up to `most` to 2^14 .. 2^15, and its
+// reciprocal.  Numbers below 2^least are left small: a product's scale is that
+// of both operands, and what is added to it has to stay in fp32's range (least
+// -60 for one and -20 for the other leave it 2^17).
+struct Scale {
+    float by, back;
+};
+template <bool scaled, int least = -60>
+__device__ __forceinline__ Scale scale_of(float most) {
+    if (!scaled) return {1.0f, 1.0f};
+    int e = __builtin_amdgcn_frexp_expf(most);
+    e = e < least ? least : e;
+    return {__builtin_amdgcn_ldexpf(1.0f, 15 - e), __builtin_amdgcn_ldexpf(1.0f, e - 15)};
 }
-// The operand of two tiles of a result: rows 4 q + r of the first and of the second.
-template <class M>
-__device__ __forceinline__ M operand_of(const f32x4 &a, const f32x4 &b) {
-    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    M o;
-    operand_of(o, v);
-    return o;
+// The same for terms that are added to numbers up to `held`, which take the
+// scale with them and must not leave fp32's range for small terms.
+template <bool scaled>
+__device__ __forceinline__ Scale scale_of_sum(float most, float held) {
+    return scale_of<scaled>(__builtin_fmaxf(most, held * 0x1p-24f));
+}
+// The largest of a lane's tiles.
+template <int CT, int N>
+__device__ __forceinline__ float largest(const f32x4 (&v)[CT][N]) {
+    float m[4] = {};
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = __builtin_fmaxf(m[i], __builtin_fabsf(v[ct][t][i]));
+    return __builtin_fmaxf(__builtin_fmaxf(m[0], m[1]), __builtin_fmaxf(m[2], m[3]));
+}
+__device__ __forceinline__ float wave_largest(float v) {
+    v = __builtin_fmaxf(v, dpp<kRowMirror>(v));
+    v = __builtin_fmaxf(v, dpp<kRowHalfMirror>(v));
+    v = __builtin_fmaxf(v, dpp<kQuadSwap2>(v));
+    v = __builtin_fmaxf(v, dpp<kQuadSwap1>(v));
+    float w = v;
+    swap_rows(v, w);
+    v = __builtin_fmaxf(v, w);
+    w = v;
+    swap_halves(v, w);
+    return __builtin_fmaxf(v, w);
 }
 
 // The key in row m of a state's tile: the 32 keys of a pair of tiles, eight to
@@ -160,27 +213,26 @@ __device__ __forceinline__ uint32_t token_at(uint32_t s, uint32_t q, uint32_t j)
     return 32u * s + 16u * (j >> 2) + 4u * q + (j & 3u);
 }
 
-// kChunk rows of `W` columns of activations in shared memory.
-template <class T, int W, int PAD = Form<T>::pad>
+// kChunk rows of `W` columns of activations in shared memory, in form F.
+template <class F, int W, int PAD = F::pad>
 struct RowTile {
-    typedef Form<T> F;
     typedef typename F::Word Word;
     static constexpr int kStride = W + PAD;
     Word w[F::planes][kChunk][kStride];
 
-    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8]) {
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8], float by = 1.0f) {
         typename F::In o;
-        operand_of(o, v);
+        operand_of(o, v, by);
         put(row, col, o);
     }
     __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Wide &o) {
-        *reinterpret_cast<float4 *>(&w[0][row][col]) = make_float4(o.p[0], o.p[1], o.p[2], o.p[3]);
-        *reinterpret_cast<float4 *>(&w[0][row][col + 4]) = make_float4(o.p[4], o.p[5], o.p[6], o.p[7]);
+        *reinterpret_cast<f32x4 *>(&w[0][row][col]) = f32x4{o.p[0], o.p[1], o.p[2], o.p[3]};
+        *reinterpret_cast<f32x4 *>(&w[0][row][col + 4]) = f32x4{o.p[4], o.p[5], o.p[6], o.p[7]};
     }
-    template <int N>
-    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Planes<N> &o) {
+    template <class E, int N>
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Planes<E, N> &o) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8 *>(&w[i][row][col]) = o.p[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<typename Planes<E, N>::Eight *>(&w[i][row][col]) = o.p[i];
     }
     // Eight columns of a row.
     __device__ __forceinline__ typename F::In along(uint32_t row, uint32_t col) const {
@@ -189,15 +241,15 @@ struct RowTile {
         return o;
     }
     __device__ __forceinline__ void get(Wide &o, uint32_t row, uint32_t col) const {
-        const float4 a = *reinterpret_cast<const float4 *>(&w[0][row][col]);
-        const float4 b = *reinterpret_cast<const float4 *>(&w[0][row][col + 4]);
-        o.p[0] = a.x, o.p[1] = a.y, o.p[2] = a.z, o.p[3] = a.w;
-        o.p[4] = b.x, o.p[5] = b.y, o.p[6] = b.z, o.p[7] = b.w;
-    }
-    template <int N>
-    __device__ __forceinline__ void get(Planes<N> &o, uint32_t row, uint32_t col) const {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(&w[0][row][col]);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(&w[0][row][col + 4]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const bf16x8 *>(&w[i][row][col]);
+        for (int i = 0; i < 4; ++i) o.p[i] = a[i], o.p[4 + i] = b[i];
+    }
+    template <class E, int N>
+    __device__ __forceinline__ void get(Planes<E, N> &o, uint32_t row, uint32_t col) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const typename Planes<E, N>::Eight *>(&w[i][row][col]);
     }
     // A column of tile `tile` of keys, key place(tile, lane & 15), at the places
     // token_at(s, lane >> 4, 0..7): the transposing read gives lane m of 16 the
@@ -211,25 +263,15 @@ struct RowTile {
 #pragma unroll
         for (uint32_t j = 0; j < 8u; ++j) o.p[j] = w[0][token_at(s, lane >> 4, j)][place(tile, lane & 15u)];
     }
-    template <int N>
-    __device__ __forceinline__ void get_across(Planes<N> &o, uint32_t s, uint32_t tile, uint32_t lane) const {
+    template <class E, int N>
+    __device__ __forceinline__ void get_across(Planes<E, N> &o, uint32_t s, uint32_t tile, uint32_t lane) const {
         const uint32_t i = lane & 15u, row = 32u * s + 4u * (lane >> 4) + (i >> 2);
         const uint32_t col = 32u * (tile >> 1) + 8u * (i & 3u) + 4u * (tile & 1u);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const uint64_t a = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row][col]));
             const uint64_t b = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row + 16u][col]));
-            o.p[n] = __builtin_bit_cast(bf16x8, uint64x2{a, b});
-        }
-    }
-    __device__ __forceinline__ float value(uint32_t row, uint32_t col) const {
-        if constexpr (sizeof(Word) == 4) {
-            return w[0][row][col];
-        } else {
-            float v = 0.0f;
-#pragma unroll
-            for (int i = F::planes - 1; i >= 0; --i) v += (float)__builtin_bit_cast(__bf16, w[i][row][col]);
-            return v;
+            o.p[n] = __builtin_bit_cast(typename Planes<E, N>::Eight, uint64x2{a, b});
         }
     }
 };
@@ -271,24 +313,40 @@ __device__ __forceinline__ void values_of(float (&v)[8], const Pack<T, 8> &r) {
     for (int j = 0; j < 8; ++j) v[j] = (float)r.v[j];
 }
 
+// The largest of a row's numbers that four neighbouring threads hold.
+template <int N>
+__device__ __forceinline__ float row_largest(const float (&v)[N][8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[c][j]));
+    m = __builtin_fmaxf(m, dpp<kQuadSwap2>(m));
+    return __builtin_fmaxf(m, dpp<kQuadSwap1>(m));
+}
+
 // Rows lo .. lo + rows of a head's keys or queries into a tile, zeros after
-// them; 256 threads, four a row.  Returns the thread's part of its row's sum
-// of squares (row threadIdx.x >> 2).
-template <class T, int W>
-__device__ __forceinline__ float fill_rows(RowTile<T, W> &tile, const void *from, int64_t stride, uint32_t head,
-                                           uint32_t width, uint32_t lo, uint32_t rows) {
-    const uint32_t row = threadIdx.x >> 2, part = threadIdx.x & 3u;
-    const T *p = static_cast<const T *>(from) + (int64_t)(lo + row) * stride + (int64_t)head * width;
-    float sum = 0.0f;
+// them; 256 threads, four a row.  Returns the factor of the thread's row
+// (threadIdx.x >> 2) in a product with the tile: 1 by its length or 1, and what
+// takes the tile's power of two back.
+template <class T, class F, int W>
+__device__ __forceinline__ float fill_rows(RowTile<F, W> &tile, const void *from, int64_t stride, uint32_t head,
+                                           uint32_t lo, uint32_t rows, const DeltaArgs &a) {
+    const uint32_t row = threadIdx.x >> 2, part = (threadIdx.x & 3u) * 8u;
+    const T *p = static_cast<const T *>(from) + (int64_t)(lo + row) * stride + (int64_t)head * a.key_dim;
+    float v[W / 32][8] = {}, sum = 0.0f;
 #pragma unroll
-    for (uint32_t c = part * 8u; c < (uint32_t)W; c += 32u) {
-        float v[8] = {};
-        if (row < rows) load8<T>(v, p, c, width);
-        tile.put(row, c, v);
+    for (uint32_t c = 0; c < W / 32u; ++c) {
+        if (row < rows) load8<T>(v[c], p, part + 32u * c, a.key_dim);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[j], v[j], sum);
+        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[c][j], v[c][j], sum);
     }
-    return sum;
+    const Scale s = scale_of<F::scaled>(F::scaled ? row_largest(v) : 0.0f);
+#pragma unroll
+    for (uint32_t c = 0; c < W / 32u; ++c) tile.put(row, part + 32u * c, v[c], s.by);
+    sum += dpp<kQuadSwap2>(sum);
+    sum += dpp<kQuadSwap1>(sum);
+    return a.unit ? s.back / __builtin_sqrtf(sum + a.eps) : s.back;
 }
 
 // The column in lane m of tile ct of a wave's 16 CT columns.
@@ -320,7 +378,7 @@ __device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *
 // The width is hidden from the compiler where it stores: it would keep the
 // addresses of every row over a whole walk, in registers that the walk needs.
 template <bool E, int CT, int TILES>
-__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], uint32_t rows, uint32_t width,
+__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], float by, uint32_t rows, uint32_t width,
                                              uint32_t col0, uint32_t lane) {
     asm volatile("" : "+s"(width));
 #pragma unroll
@@ -333,13 +391,13 @@ __device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TIL
             float *p = to + (row * width + col);
 #pragma unroll
             for (uint32_t i = 0; i < 4u; ++i)
-                if (E || row + i < rows) p[i * width] = S[ct][t][i];
+                if (E || row + i < rows) p[i * width] = S[ct][t][i] * by;
         }
     }
 }
 // A result's tiles over a chunk's rows into rows of `stride`, rows below `rows`.
 template <bool E, int CT>
-__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[CT][4], uint32_t rows,
+__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[CT][4], float by, uint32_t rows,
                                            uint32_t col0, uint32_t width, uint32_t lane) {
     asm volatile("" : "+s"(stride));
 #pragma unroll
@@ -352,7 +410,7 @@ __device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32
             float *p = to + (row * stride + col);
 #pragma unroll
             for (uint32_t i = 0; i < 4u; ++i)
-                if (row + i < rows) p[i * stride] = y[ct][t][i];
+                if (row + i < rows) p[i * stride] = y[ct][t][i] * by;
         }
     }
 }
@@ -360,8 +418,11 @@ __device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32
 // ---------------------------------------------------------------------------
 // what a chunk's preparation leaves in the workspace for each head
 // ---------------------------------------------------------------------------
-// Numbers for each row: e nu, scale e mu, beta, exp(G_C - G) nu; then exp(G_C).
-constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowFloats = 320u;
+// Numbers for each row: e nu, scale e mu, beta, exp(G_C - G) nu (nu and mu with
+// what takes the keys' and queries' powers of two back); then exp(G_C) and the
+// scales of the triangles: the inverse's back, the scores' and its back.
+constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowInverse = 257u,
+                   kRowScores = 258u, kRowScoresBack = 259u, kRowFloats = 320u;
 // Two triangles as operands in the order that the lanes read them: rows of tile
 // t and the places of token_at(s, ..); six of the eight hold something.
 constexpr uint32_t kTriangle = 6u;
@@ -478,14 +539,14 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
     typedef typename Form<T>::Mid Mid;
     union Shared {
         struct {
-            RowTile<T, W> k, q;
+            RowTile<Form<T>, W> k, q;
         } in;
         float tri[kChunk * kTriStride];
     };
     __shared__ Shared sh;
     __shared__ float diagonal[4][16 * kDiagonal];
     __shared__ ChunkGates gates[4];
-    __shared__ float nu[kChunk], mu[kChunk];
+    __shared__ float nu[kChunk], mu[kChunk], most[2][4];
     const uint32_t b = first + blockIdx.x;
     if (b == 0u && threadIdx.x == 0u) mark_plain(hdr, words);
     const uint32_t slot = b / a.kheads, khead = b % a.kheads;
@@ -493,16 +554,9 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
     const uint32_t rows = c.hi - c.lo;
     if (rows == 0u) return;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
-    float ks = fill_rows<T, W>(sh.in.k, a.k, a.k_stride, khead, a.key_dim, c.lo, rows);
-    float qs = fill_rows<T, W>(sh.in.q, a.q, a.q_stride, khead, a.key_dim, c.lo, rows);
-    ks += dpp<kQuadSwap2>(ks);
-    ks += dpp<kQuadSwap1>(ks);
-    qs += dpp<kQuadSwap2>(qs);
-    qs += dpp<kQuadSwap1>(qs);
-    if ((threadIdx.x & 3u) == 0u) {
-        nu[threadIdx.x >> 2] = a.unit ? 1.0f / __builtin_sqrtf(ks + a.eps) : 1.0f;
-        mu[threadIdx.x >> 2] = a.unit ? 1.0f / __builtin_sqrtf(qs + a.eps) : 1.0f;
-    }
+    const float own_nu = fill_rows<T>(sh.in.k, a.k, a.k_stride, khead, c.lo, rows, a);
+    const float own_mu = fill_rows<T>(sh.in.q, a.q, a.q_stride, khead, c.lo, rows, a);
+    if ((threadIdx.x & 3u) == 0u) nu[threadIdx.x >> 2] = own_nu, mu[threadIdx.x >> 2] = own_mu;
     __syncthreads();
     // kk: rows k_l, columns k of tile `wave`; qk: forwards rows k_j, columns q of
     // the tile, backwards rows q_i, columns k.  l > column or l < column.
@@ -545,7 +599,7 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
         const uint32_t col = 16u * wave + n;
         const double here = gate.sum[col];
         const float beta_here = gate.beta[col], nu_here = nu[col], mu_here = mu[col];
-        f32x4 p[4], x[4];
+        f32x4 p[1][4], x[1][4];
         __syncthreads();  // the products, or the triangle of the head before, are read
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
@@ -559,18 +613,32 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
                 // forwards a_lj beta_j for l > j, the transpose's row j; backwards beta_i a_il
                 tri[i] = (BACK ? row < col : row > col) ? both * nu_here * beta_here * kk[t][i] : 0.0f;
                 const float along = BACK ? forth * mu[row] * nu_here : both * mu_here;
-                p[t][i] = (BACK ? row >= col : row <= col) ? a.scale * along * qk[t][i] : 0.0f;
+                p[0][t][i] = (BACK ? row >= col : row <= col) ? a.scale * along * qk[t][i] : 0.0f;
             }
             *reinterpret_cast<f32x4 *>(&sh.tri[col * kTriStride + 16u * t + 4u * q]) = tri;
         }
         __syncthreads();
-        unit_inverse<BACK>(sh.tri, diagonal, wave, lane, x);
+        unit_inverse<BACK>(sh.tri, diagonal, wave, lane, x[0]);
+        Scale inverse = {1.0f, 1.0f}, scores = {1.0f, 1.0f};
+        if constexpr (Form<T>::scaled) {
+            const float mx = wave_largest(largest(x)), mp = wave_largest(largest(p));
+            if (lane == 0u) most[0][wave] = mx, most[1][wave] = mp;
+            __syncthreads();
+            auto all = [&](const float(&m)[4]) { return __builtin_fmaxf(__builtin_fmaxf(m[0], m[1]), __builtin_fmaxf(m[2], m[3])); };
+            inverse = scale_of<true, -20>(all(most[0]));
+            scores = scale_of<true, -20>(all(most[1]));
+        }
+        if (threadIdx.x == 0u) {
+            out.row[kRowInverse] = inverse.back;
+            out.row[kRowScores] = scores.by;
+            out.row[kRowScoresBack] = scores.back;
+        }
 #pragma unroll
         for (uint32_t s = 0; s < 2u; ++s) {
             if (BACK ? s < (wave >> 1) : s > (wave >> 1)) continue;
             const uint32_t at = BACK ? upper_at(wave, s) : lower_at(wave, s);
-            out.inverse[at][lane] = operand_of<Mid>(x[2u * s], x[2u * s + 1u]);
-            out.scores[at][lane] = operand_of<Mid>(p[2u * s], p[2u * s + 1u]);
+            out.inverse[at][lane] = operand_of<Mid>(x[0][2u * s], x[0][2u * s + 1u], inverse.by);
+            out.scores[at][lane] = operand_of<Mid>(p[0][2u * s], p[0][2u * s + 1u], scores.by);
         }
     }
 }

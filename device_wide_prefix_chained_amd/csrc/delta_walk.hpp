@@ -17,7 +17,7 @@ namespace {
 template <class T, int W, int CT>
 struct WalkTile {
     static constexpr uint32_t kCols = 64u * CT;
-    RowTile<T, W> k, q;
+    RowTile<Form<T>, W> k, q;
     Prepared<T> p;
     T v[kChunk][kCols + 8u];
 };
@@ -26,6 +26,23 @@ constexpr bool kValuesFit = sizeof(WalkTile<T, W, CT>) <= kMostShared;
 template <class T, int W, int CT>
 constexpr size_t walk_tile_bytes() {
     return kValuesFit<T, W, CT> ? sizeof(WalkTile<T, W, CT>) : sizeof(WalkTile<T, W, CT>) - sizeof(WalkTile<T, W, CT>::v);
+}
+
+// Rows 16 t + 4 q + i of column `here` + column(ct, m) of a tile of values.
+template <class T, int CT, uint32_t STRIDE>
+__device__ __forceinline__ f32x4 value_rows(const T (&tile)[kChunk][STRIDE], uint32_t t, uint32_t q, uint32_t m, uint32_t here,
+                                            uint32_t ct) {
+    f32x4 v;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t at = here + (CT == 1 ? 4u * (m & 3u) : 8u * (m & 3u) + 4u * ct);
+        const i16x4 raw = read_transposed(reinterpret_cast<const uint16_t *>(&tile[16u * t + 4u * q + (m >> 2)][at]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)tile[16u * t + 4u * q + i][here + column<CT>(ct, m)];
+    }
+    return v;
 }
 
 // Where a sequence is walked over in segments of 2^shift rows side by side: a
@@ -59,7 +76,7 @@ struct DeltaFeed {
     template <bool LEAD, class F, class O>
     __device__ __forceinline__ void run(uint32_t chunks, bool with_values, F tile, O order) const {
         constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
-        constexpr uint32_t kKeys = (W + 31) / 32, kVals = Tile::kCols / 32u;
+        constexpr uint32_t kKeys = W / 32, kVals = Tile::kCols / 32u;
         constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
         const uint32_t thread = threadIdx.x - 256u, row = thread >> 2, part = (thread & 3u) * 8u;
         Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
@@ -88,16 +105,16 @@ struct DeltaFeed {
             }
         };
         auto leave = [&](Tile *to) {
+            auto put = [&](RowTile<Form<T>, W> &tile, const Pack<T, 8>(&from)[kKeys]) {
+                float v[kKeys][8];
 #pragma unroll
-            for (uint32_t c = 0; c < kKeys; ++c) {
-                float v[8];
-                values_of<T>(v, ks[c]);
-                to->k.put(row, part + 32u * c, v);
-                if (!LEAD) {
-                    values_of<T>(v, qs[c]);
-                    to->q.put(row, part + 32u * c, v);
-                }
-            }
+                for (uint32_t c = 0; c < kKeys; ++c) values_of<T>(v[c], from[c]);
+                const Scale by = scale_of<Form<T>::scaled>(Form<T>::scaled ? row_largest(v) : 0.0f);
+#pragma unroll
+                for (uint32_t c = 0; c < kKeys; ++c) tile.put(row, part + 32u * c, v[c], by.by);
+            };
+            put(to->k, ks);
+            if (!LEAD) put(to->q, qs);
             if constexpr (kV) {
 #pragma unroll
                 for (uint32_t c = 0; c < kVals; ++c) *reinterpret_cast<Pack<T, 8> *>(&to->v[row][part + 32u * c]) = vs[c];
@@ -165,7 +182,9 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     }
     const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
-    f32x4 S[CT][kTiles];
+    constexpr bool kScaled = Form<T>::scaled;
+    f32x4 S[CT][kTiles];  // times `unit_of`, the states
+    float unit_of = 1.0f;
     {
         const float *from = nullptr;
         if (!LEAD && r.index) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
@@ -179,7 +198,10 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
         const Tile &in = *tile(c);
         if (col0 < width) {
             if (!LEAD && to.states)
-                store_states<E>(to.states + ((uint64_t)(base + c) * a.heads + head) * cells, S, a.key_dim, a.value_dim, col0, lane);
+                store_states<E>(to.states + ((uint64_t)(base + c) * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim,
+                                col0, lane);
+            const float most = kScaled ? wave_largest(largest(S)) : 0.0f;
+            const Scale of_s = scale_of<kScaled>(most);
             f32x4 x[CT][4], o[CT][4], y[CT][4];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
@@ -191,7 +213,7 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
             for (uint32_t s = 0; s < kTiles / 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(S[ct][2u * s], S[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(S[ct][2u * s], S[ct][2u * s + 1u], of_s.by);
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
                     const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
@@ -208,21 +230,15 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
             };
             __builtin_amdgcn_sched_barrier(0);
             // R = V - e K S
+            const float from_s = of_s.back * unit_of;
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 e = numbers(kRowE, t);
+                const f32x4 e = numbers(kRowE, t) * from_s;
 #pragma unroll
                 for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
                     f32x4 v;
-                    if constexpr (kV && sizeof(T) == 2) {
-                        const uint32_t at = here + (CT == 1 ? 4u * (m & 3u) : 8u * (m & 3u) + 4u * ct);
-                        const i16x4 raw = read_transposed(
-                            reinterpret_cast<const uint16_t *>(&in.v[16u * t + 4u * q + (m >> 2)][at]));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
-                    } else if constexpr (kV) {
-#pragma unroll
-                        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)in.v[16u * t + 4u * q + i][here + column<CT>(ct, m)];
+                    if constexpr (kV) {
+                        v = value_rows<T, CT>(in.v, t, q, m, here, ct);
                     } else {
                         const uint32_t col = col0 + column<CT>(ct, m);
 #pragma unroll
@@ -237,11 +253,13 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
             }
             __builtin_amdgcn_sched_barrier(0);
             // rho
+            const Scale of_x = scale_of<kScaled>(kScaled ? wave_largest(largest(x)) : 0.0f);
+            const float from_x = kScaled ? of_x.back * in.p.row[kRowInverse] : 1.0f;
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u], of_x.by);
 #pragma unroll
                 for (uint32_t t = 2u * s; t < 4u; ++t) {
                     const Mid inverse = in.p.inverse[lower_at(t, s)][lane];
@@ -250,27 +268,38 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
                 }
             }
             if (!LEAD && to.rhos)
-                store_rows<E>(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, rows,
-                              col0, a.value_dim, lane);
+                store_rows<E>(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, from_x,
+                              rows, col0, a.value_dim, lane);
             __builtin_amdgcn_sched_barrier(0);
-            // out^T = scale e (Q S)^T + U^T P^T
+            // U, and out^T = scale e (Q S)^T + U^T P^T
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 beta = numbers(kRowBeta, t);
-                const float e = LEAD ? 0.0f : in.p.row[kRowQ + 16u * t + m];
+                const f32x4 beta = numbers(kRowBeta, t) * from_x;
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= beta, o[ct][t] *= e;
+                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= beta;
             }
+            float from_o = 1.0f;
+            if constexpr (!LEAD) {
+                const Scale of_u = scale_of<kScaled>(kScaled ? wave_largest(largest(y)) : 0.0f);
+                const float to_o = kScaled ? from_s * of_u.by * in.p.row[kRowScores] : 1.0f;
+                from_o = kScaled ? of_u.back * in.p.row[kRowScoresBack] : 1.0f;
 #pragma unroll
-            for (uint32_t s = 0; s < (LEAD ? 0u : 2u); ++s) {
-                Mid h[CT];
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    const float e = in.p.row[kRowQ + 16u * t + m] * to_o;
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+                    for (int ct = 0; ct < CT; ++ct) o[ct][t] *= e;
+                }
 #pragma unroll
-                for (uint32_t t = 2u * s; t < 4u; ++t) {
-                    const Mid scores = in.p.scores[lower_at(t, s)][lane];
+                for (uint32_t s = 0; s < 2u; ++s) {
+                    Mid h[CT];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], scores);
+                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_u.by);
+#pragma unroll
+                    for (uint32_t t = 2u * s; t < 4u; ++t) {
+                        const Mid scores = in.p.scores[lower_at(t, s)][lane];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], scores);
+                    }
                 }
             }
 #pragma unroll
@@ -282,7 +311,7 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w.v[4 * ct + i] = (T)o[ct][t][i];
+                        for (int i = 0; i < 4; ++i) w.v[4 * ct + i] = (T)(o[ct][t][i] * from_o);
                     if (E || col + 4u * CT <= a.value_dim) {
                         *reinterpret_cast<Pack<T, 4 * CT> *>(at) = w;
                     } else {
@@ -294,22 +323,24 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
             }
             __builtin_amdgcn_sched_barrier(0);
             // S = e_C S + K^T diag(exp(G_C - G)) U
-            const float whole = in.p.row[kRowWhole];
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) {
                 const f32x4 tail = numbers(kRowTail, t);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[ct][t] *= tail;
             }
+            const float kept = unit_of * in.p.row[kRowWhole];
+            const Scale of_u = scale_of_sum<kScaled>(kScaled ? wave_largest(largest(y)) : 0.0f, most * kept);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) S[ct][t] *= whole;
+                for (uint32_t t = 0; t < kTiles; ++t) S[ct][t] *= kept * of_u.by;
+            unit_of = of_u.back;
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s) {
                 Mid h[CT];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u]);
+                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_u.by);
 #pragma unroll
                 for (uint32_t t = 0; t < kTiles; ++t) {
                     const auto ka = in.k.across(s, t, lane);
@@ -323,10 +354,10 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     }
     if (col0 >= width) return;
     const uint64_t place_of = (uint64_t)number * a.heads + head;
-    if (LEAD && unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, S, a.key_dim, a.key_dim, col0, lane);
-    else if (LEAD) store_states<E>(seg.n + place_of * cells, S, a.key_dim, a.value_dim, col0, lane);
+    if (LEAD && unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, S, unit_of, a.key_dim, a.key_dim, col0, lane);
+    else if (LEAD) store_states<E>(seg.n + place_of * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
     else if (to.final && r.hi == seq.hi)
-        store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
 }
 
 // The states that enter a sequence's segments after the first, S <- M S + N,
@@ -337,6 +368,7 @@ template <class T, int W, bool E, bool BACK>
 __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
     constexpr uint32_t kTiles = W / 16;
+    constexpr bool kScaled = Form<T>::scaled;
     const uint32_t blocks = (a.value_dim + 63u) / 64u, item = first + blockIdx.x / blocks, head = item % a.heads;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
     const uint32_t col0 = blockIdx.x % blocks * 64u + wave * 16u, s = item / a.heads;
@@ -350,9 +382,10 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
     load_states<E>(next, seg.n + number(0u) * cells, a.key_dim, a.value_dim, col0, lane);
     for (uint32_t i = 0; i + 1u < segments; ++i) {
         const float *mat = seg.m + number(i) * key_cells;
+        const Scale of_s = scale_of<kScaled>(kScaled ? wave_largest(largest(S)) : 0.0f);
         Mid h[kTiles / 2];
 #pragma unroll
-        for (uint32_t c = 0; c < kTiles / 2u; ++c) h[c] = operand_of<Mid>(S[0][2u * c], S[0][2u * c + 1u]);
+        for (uint32_t c = 0; c < kTiles / 2u; ++c) h[c] = operand_of<Mid>(S[0][2u * c], S[0][2u * c + 1u], of_s.by);
 #pragma unroll
         for (uint32_t t = 0; t < kTiles; ++t) {
             const uint32_t row = place(t, m);
@@ -362,13 +395,19 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
                 float v[8] = {};
                 if (row < a.key_dim) load8<float>(v, mat + row * a.key_dim, 32u * c + 8u * q, a.key_dim);
                 Mid o;
-                operand_of(o, v);
-                mma(S[0][t], o, h[c]);
+                float most = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) most = __builtin_fmaxf(most, __builtin_fabsf(v[j]));
+                const Scale of_m = scale_of<kScaled>(kScaled ? wave_largest(most) : 0.0f);
+                operand_of(o, v, of_m.by);
+                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma(sum, o, h[c]);
+                S[0][t] += sum * (of_m.back * of_s.back);
             }
         }
         float *n = seg.n + number(i + 1u) * cells;
         if (i + 2u < segments) load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
-        store_states<E>(n, S, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(n, S, 1.0f, a.key_dim, a.value_dim, col0, lane);
     }
 }
 
