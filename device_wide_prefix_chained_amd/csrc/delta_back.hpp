@@ -29,7 +29,9 @@ struct BackResults {
     float *dinitial;      // the same, or NULL
     float *dstates;       // [chunk numbers, heads, key_dim, value_dim]: D
     float *omega;         // [tokens, heads, value_dim]
+    float *sizes;         // [chunk numbers, heads, kBackSizes]: the largest of `dstates`, `omega` and dout
 };
+constexpr uint32_t kBackSizes = 3u * kSizeWaves;
 
 // The walk backwards.  lead: the walks for M and N of segments that are not a
 // sequence's first, which keep nothing but their end.
@@ -45,7 +47,7 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = lead ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
     const bool unit = block < key_blocks;  // columns of M
     const uint32_t block0 = (block - (unit ? 0u : key_blocks)) * kCols, width = unit ? a.key_dim : a.value_dim;
     const Chunk r = find_chunk(a.offsets, a.num_seqs, a.tokens, seg.shift, number);
@@ -128,7 +130,8 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
 #pragma unroll
                     for (int t = 0; t < 4; ++t) o[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
-            const Scale of_o = scale_of<kScaled>(kScaled ? wave_largest(largest(o)) : 0.0f);
+            const float most_o = kScaled ? wave_largest(largest(o)) : 0.0f;
+            const Scale of_o = scale_of<kScaled>(most_o);
             const float to_x = kScaled ? of_o.by * in.p.row[kRowScores] : 1.0f;
             const float from_x = kScaled ? of_o.back * in.p.row[kRowScoresBack] : 1.0f;
 #pragma unroll
@@ -166,6 +169,12 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
                 }
+            }
+            if (!lead && kScaled) {
+                const float of_y = wave_largest(largest(y)) * from_y;
+                float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kBackSizes + col0 / (16u * CT);
+                if (lane == 0u)
+                    sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y, sizes[2u * kSizeWaves] = most_o;
             }
             if (!lead)
                 store_rows<E>(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, from_y, rows,
@@ -252,189 +261,213 @@ __device__ __forceinline__ float column_total(float v) {
     return v + w;
 }
 
-// Eight or four keys of a row held by a lane: four of each of its wave's tiles.
-template <class F, int W>
-__device__ __forceinline__ f32x4 four_keys(const RowTile<F, W> &tile, uint32_t row, uint32_t col) {
-    f32x4 v;
-    if constexpr (sizeof(typename F::Word) == 4) {
-        v = *reinterpret_cast<const f32x4 *>(&tile.w[0][row][col]);
-    } else {
-        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-        v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int p = F::planes - 1; p >= 0; --p) {
-            const u16x4 r = *reinterpret_cast<const u16x4 *>(&tile.w[p][row][col]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += (float)__builtin_bit_cast(__bf16, (uint16_t)r[i]);
-        }
-    }
-    return v;
-}
-
 template <class T, int W>
 struct GradShared {
-    typedef typename Plain<T>::Mid Mid;
-    // 32 columns of computed numbers: two planes, or themselves.  256 keys in two
-    // planes leave no room for the padding that spreads rows over the banks.
-    static constexpr int kPad = W == 256 && sizeof(RowTile<Plain<T>, W>) > 66560u ? 0 : Plain<T>::pad;
-    typedef RowTile<Plain<typename std::conditional<sizeof(T) == 2, f16_t, float>::type>, 32, kPad> MidTile;
-    RowTile<Plain<T>, W> k, q;
+    typedef typename Form<T>::Mid Mid;
+    KeyTile<T, W> k, q;
     union {
         struct {
-            RowTile<Plain<T>, 32, kPad> dout;
-            MidTile u, dr;
+            RowTile<typename Form<T>::In, 32> dout;
+            RowTile<Mid, 32> rho, omega;
         } in;
-        Mid triangle[kTriangle][64];
+        Mid triangle[2][kTriangle][64];
         struct {
-            float query[4][kChunk], key[4][kChunk], end[4][kChunk], pair[4][kChunk];
+            float query[8][kChunk], key[8][kChunk], end[8][kChunk], pair[8][kChunk];
         } part;
     };
     double sum[kChunk];
-    float beta[kChunk], nu[kChunk], mu[kChunk], dot[4];
+    float beta[kChunk], nu[kChunk], mu[kChunk], dot[8], most[8];
 };
 
 // One workgroup a chunk and head of keys; it takes the heads of values that
-// share them in turn and adds their gradients in registers.  Wave w has the
-// keys of tiles DT w .. DT w + DT - 1 of all rows (a row in a lane, its keys in
-// the registers), and of the 64 x 64 products the columns 16 w .. 16 w + 15 of
-// both triangles.
+// share them in turn and adds their gradients in registers.  A wave has DT tiles
+// of 16 keys for TT tiles of 16 rows, a row in a lane and its keys in the
+// registers.  Of the 64 x 64 products waves 0 to 3 have dO rho^T, waves 4 to 7
+// omega rho^T: wave w the columns of tile w & 3 of the lower triangle as it is
+// (five, slots up to w: rows j, columns i) and transposed (slots above: rows
+// i, columns j), so that both are operands as they come.
 template <class T, int W, bool E>
-__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
+__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
                                                           const float *__restrict__ states, const float *__restrict__ rhos,
-                                                          const float *__restrict__ dstates, const float *__restrict__ omega,
-                                                          DeltaGradPtrs to) {
-    typedef typename Plain<T>::Mid Mid;
-    typedef typename Plain<T>::In In;
-    constexpr uint32_t DT = W >= 64 ? W / 64 : 1, kTiles = W / 16;
+                                                          const float *__restrict__ sizes, const float *__restrict__ dstates,
+                                                          const float *__restrict__ omega, const float *__restrict__ back_sizes,
+                                                          uint32_t size_waves, DeltaGradPtrs to) {
+    typedef typename Form<T>::Mid Mid;
+    constexpr bool kScaled = Form<T>::scaled;
+    constexpr uint32_t DT = W > 128 ? W / 128 : 1, TT = W >= 128 ? 4 : W / 32, kTiles = W / 16;
     __shared__ GradShared<T, W> sh;
     const uint32_t item = first + blockIdx.x, slot = item / a.kheads, khead = item % a.kheads;
     const Chunk c = find_chunk(a.offsets, a.num_seqs, a.tokens, kChunkShift, slot);
     const uint32_t rows = c.hi - c.lo;
     if (rows == 0u) return;
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
-    const uint32_t row = threadIdx.x >> 2, part = (threadIdx.x & 3u) * 8u;
-    const bool works = wave * DT < kTiles;
+    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
+    const uint32_t tile0 = W >= 128 ? wave * DT : wave % kTiles, t0 = W >= 128 ? 0u : wave / kTiles * TT;
+    const uint32_t own_tile = wave & 3u, own = 16u * own_tile + n;
+    const bool keys_side = wave >= 4u;  // omega rho^T and k k^T, not dO rho^T and q k^T
+    const uint32_t row = threadIdx.x >> 3, part = (threadIdx.x & 7u) * 4u;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    float raw_nu, raw_mu;
     {
-        const float own_nu = fill_rows<T>(sh.k, a.k, a.k_stride, khead, c.lo, rows, a);
-        const float own_mu = fill_rows<T>(sh.q, a.q, a.q_stride, khead, c.lo, rows, a);
-        if ((threadIdx.x & 3u) == 0u) sh.nu[row] = own_nu, sh.mu[row] = own_mu;
+        const float own_nu = fill_rows<T, 8, W>(sh.k, a.k, a.k_stride, khead, c.lo, rows, a, &raw_nu);
+        const float own_mu = fill_rows<T, 8, W>(sh.q, a.q, a.q_stride, khead, c.lo, rows, a, &raw_mu);
+        if ((threadIdx.x & 7u) == 0u) sh.nu[row] = own_nu, sh.mu[row] = own_mu;
     }
     __syncthreads();
-    // k_j k_i and k_j q_i, rows j in the registers, i = 16 wave + n in the lane
-    f32x4 kk[4], qk[4];
+    // k_j k_i or k_j q_i, rows j in the registers, i = own in the lane
+    f32x4 kk[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = none;
+    for (int t = 0; t < 4; ++t) kk[t] = none;
 #pragma unroll
     for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
-        const auto kb = sh.k.along(16u * wave + n, col + 8u * q), qb = sh.q.along(16u * wave + n, col + 8u * q);
+        const auto b = keys_side ? sh.k.along(own, col + 8u * q) : sh.q.along(own, col + 8u * q);
 #pragma unroll
-        for (uint32_t t = 0; t < 4u; ++t) {
-            if (t > wave) continue;
-            const auto ka = sh.k.along(16u * t + n, col + 8u * q);
-            mma(kk[t], ka, kb);
-            mma(qk[t], ka, qb);
-        }
+        for (uint32_t t = 0; t < 4u; ++t)
+            if (t <= own_tile) mma(kk[t], sh.k.along(16u * t + n, col + 8u * q), b);
     }
-    f32x4 dq[DT][4], dk[DT][4];  // with respect to the keys and queries of length 1
+    f32x4 dq[DT][TT], dk[DT][TT];  // with respect to the keys and queries of length 1
 #pragma unroll
     for (uint32_t d = 0; d < DT; ++d)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) dq[d][t] = dk[d][t] = none;
+        for (uint32_t t = 0; t < TT; ++t) dq[d][t] = dk[d][t] = none;
     const uint32_t per = a.heads / a.kheads;
-    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim, rows_of = (uint64_t)a.heads * a.value_dim;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     for (uint32_t j = 0; j < per; ++j) {
         const uint32_t head = khead * per + j;
+        const uint64_t of_head = (uint64_t)slot * a.heads + head, at_row = ((uint64_t)(c.lo + row) * a.heads + head) * a.value_dim;
+        const float *state = states + of_head * cells, *dstate = dstates + of_head * cells;
+        // the next 32 columns, on their way while some are worked on
+        struct {
+            float s[DT][8], d[DT][8];
+            f32x4 rho, omega, dout;
+        } next;
+        auto fetch = [&](uint32_t v0) {
+#pragma unroll
+            for (uint32_t d = 0; d < DT; ++d) {
+                const uint32_t key = 16u * (tile0 + d) + n, col = v0 + 8u * q;
+                const bool there = key < a.key_dim && col < a.value_dim;
+                const uint32_t at = there ? key * a.value_dim + col : 0u;
+                if (E) {
+                    const Pack<float, 8> s = *reinterpret_cast<const Pack<float, 8> *>(state + at);
+                    const Pack<float, 8> g = *reinterpret_cast<const Pack<float, 8> *>(dstate + at);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) next.s[d][i] = there ? s.v[i] : 0.0f, next.d[d][i] = there ? g.v[i] : 0.0f;
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < 8u; ++i) {
+                        const bool is = there && col + i < a.value_dim;
+                        next.s[d][i] = is ? state[at + i] : 0.0f;
+                        next.d[d][i] = is ? dstate[at + i] : 0.0f;
+                    }
+                }
+            }
+            const bool there = row < rows && v0 + part < a.value_dim;
+            const uint64_t at = there ? at_row + v0 + part : ((uint64_t)c.lo * a.heads + head) * a.value_dim;
+            if (E) {
+                next.rho = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(rhos + at));
+                next.omega = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(omega + at));
+                const Pack<T, 4> o = *reinterpret_cast<const Pack<T, 4> *>(dout + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) next.dout[i] = (float)o.v[i];
+                if (!there) next.rho = next.omega = next.dout = none;
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i) {
+                    const bool is = there && v0 + part + i < a.value_dim;
+                    next.rho[i] = is ? rhos[at + i] : 0.0f;
+                    next.omega[i] = is ? omega[at + i] : 0.0f;
+                    next.dout[i] = is ? (float)dout[at + i] : 0.0f;
+                }
+            }
+        };
+        fetch(0u);
         const double sums = running_decay(a, head, c.lo, rows, lane);
         const float own_beta = row < rows ? a.beta[(int64_t)(c.lo + row) * a.beta_stride + head] : 0.0f;
+        Scale of_s = {1.0f, 1.0f}, of_d = of_s, of_rho = of_s, of_omega = of_s, of_o = of_s;
+        if constexpr (kScaled) {
+            const bool has = lane < size_waves;
+            const float *f = sizes + of_head * kSizes + lane, *b = back_sizes + of_head * kBackSizes + lane;
+            of_s = scale_of<true>(wave_largest(has ? f[0] : 0.0f));
+            of_rho = scale_of<true>(wave_largest(has ? f[kSizeWaves] : 0.0f));
+            of_d = scale_of<true>(wave_largest(has ? b[0] : 0.0f));
+            of_omega = scale_of<true>(wave_largest(has ? b[kSizeWaves] : 0.0f));
+            of_o = scale_of<true>(wave_largest(has ? b[2u * kSizeWaves] : 0.0f));
+        }
         __syncthreads();  // the head before is done with
         if (wave == 0u) sh.sum[lane] = sums;
-        if ((threadIdx.x & 3u) == 0u) sh.beta[row] = own_beta;
-        const float *state = states + ((uint64_t)slot * a.heads + head) * cells;
-        const float *dstate = dstates + ((uint64_t)slot * a.heads + head) * cells;
-        f32x4 qs[DT][4], rs[DT][4], ends[DT][4], e1[5], e2[5];
+        if ((threadIdx.x & 7u) == 0u) sh.beta[row] = own_beta;
+        f32x4 qs[DT][TT], rs[DT][TT], ends[DT][TT], e[5];
 #pragma unroll
         for (uint32_t d = 0; d < DT; ++d)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) qs[d][t] = rs[d][t] = ends[d][t] = none;
+            for (uint32_t t = 0; t < TT; ++t) qs[d][t] = rs[d][t] = ends[d][t] = none;
 #pragma unroll
-        for (int t = 0; t < 5; ++t) e1[t] = e2[t] = none;
+        for (int t = 0; t < 5; ++t) e[t] = none;
         float dot = 0.0f, dbeta = 0.0f;
         for (uint32_t v0 = 0; v0 < a.value_dim; v0 += 32u) {
-            {
-                float u[8] = {}, w[8] = {}, o[8] = {};
-                const uint64_t at = ((uint64_t)(c.lo + row) * a.heads + head) * a.value_dim;
-                if (row < rows) {
-                    load8<float>(u, rhos + at, v0 + part, a.value_dim);
-                    load8<float>(w, omega + at, v0 + part, a.value_dim);
-                    load8<T>(o, dout + at, v0 + part, a.value_dim);
-                }
+            if (v0) __syncthreads();  // the columns before are read
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dbeta = __builtin_fmaf(u[i], w[i], dbeta);
-                    u[i] *= own_beta;
-                    w[i] *= own_beta;
-                }
-                if (row < rows) {
-                    T *p = static_cast<T *>(to.dv) + at + v0 + part;
-                    if (E || v0 + part + 8u <= a.value_dim) {
-                        Pack<T, 8> r;
+            for (int i = 0; i < 4; ++i) dbeta = __builtin_fmaf(next.rho[i], next.omega[i], dbeta);
+            if (row < rows) {
+                T *p = static_cast<T *>(to.dv) + at_row + v0 + part;
+                Pack<T, 4> w;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) r.v[i] = (T)w[i];
-                        if (v0 + part < a.value_dim) *reinterpret_cast<Pack<T, 8> *>(p) = r;
-                    } else {
+                for (int i = 0; i < 4; ++i) w.v[i] = (T)(own_beta * next.omega[i]);
+                if (E) {
+                    if (v0 + part < a.value_dim) *reinterpret_cast<Pack<T, 4> *>(p) = w;
+                } else {
 #pragma unroll
-                        for (uint32_t i = 0; i < 8u; ++i)
-                            if (v0 + part + i < a.value_dim) p[i] = (T)w[i];
-                    }
+                    for (uint32_t i = 0; i < 4u; ++i)
+                        if (v0 + part + i < a.value_dim) p[i] = w.v[i];
                 }
-                if (v0) __syncthreads();  // the columns before are read
-                sh.in.dout.put(row, part, o);
-                sh.in.u.put(row, part, u);
-                sh.in.dr.put(row, part, w);
             }
-            __syncthreads();
+            sh.in.dout.put(row, part, next.dout, of_o.by);
+            sh.in.rho.put(row, part, next.rho, of_rho.by);
+            sh.in.omega.put(row, part, next.omega, of_omega.by);
             Mid S[DT], D[DT];
 #pragma unroll
             for (uint32_t d = 0; d < DT; ++d) {
-                float s[8] = {}, g[8] = {};
-                const uint32_t key = place(wave * DT + d, n);
-                if (works && key < a.key_dim) {
-                    load8<float>(s, state + key * a.value_dim, v0 + 8u * q, a.value_dim);
-                    load8<float>(g, dstate + key * a.value_dim, v0 + 8u * q, a.value_dim);
-                }
+                if (t0 == 0u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(s[i], g[i], dot);
-                operand_of(S[d], s);
-                operand_of(D[d], g);
+                    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(next.s[d][i], next.d[d][i], dot);
+                operand_of(S[d], next.s[d], of_s.by);
+                operand_of(D[d], next.d[d], of_d.by);
             }
-            const auto own_o = sh.in.dout.along(16u * wave + n, 8u * q);
-            const auto own_u = sh.in.u.along(16u * wave + n, 8u * q), own_r = sh.in.dr.along(16u * wave + n, 8u * q);
+            if (v0 + 32u < a.value_dim) fetch(v0 + 32u);
+            __syncthreads();
 #pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const auto o = sh.in.dout.along(16u * t + n, 8u * q);
-                const auto u = sh.in.u.along(16u * t + n, 8u * q), r = sh.in.dr.along(16u * t + n, 8u * q);
-                if (works) {
+            for (uint32_t t = 0; t < TT; ++t) {
+                const uint32_t at = 16u * (t0 + t) + n;
+                const auto o = sh.in.dout.along(at, 8u * q);
+                const auto w = sh.in.omega.along(at, 8u * q), r = sh.in.rho.along(at, 8u * q);
 #pragma unroll
-                    for (uint32_t d = 0; d < DT; ++d) {
-                        mma(qs[d][t], S[d], o);
-                        mma(rs[d][t], S[d], r);
-                        mma(ends[d][t], D[d], u);
-                    }
+                for (uint32_t d = 0; d < DT; ++d) {
+                    mma(qs[d][t], S[d], o);
+                    mma(rs[d][t], S[d], w);
+                    mma(ends[d][t], D[d], r);
                 }
-                if (t <= wave) {
-                    mma(e1[t], u, own_o);
-                    mma(e2[t], u, own_r);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const auto own_r = sh.in.rho.along(own, 8u * q);
+            if (keys_side) {
+                const auto own_w = sh.in.omega.along(own, 8u * q);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    if (t <= own_tile) mma(e[t], sh.in.rho.along(16u * t + n, 8u * q), own_w);
+                    if (t >= own_tile) mma(e[t + 1], sh.in.omega.along(16u * t + n, 8u * q), own_r);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (t >= wave) {
-                    mma(e1[t + 1], o, own_u);
-                    mma(e2[t + 1], r, own_u);
+            } else {
+                const auto own_o = sh.in.dout.along(own, 8u * q);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) {
+                    if (t <= own_tile) mma(e[t], sh.in.rho.along(16u * t + n, 8u * q), own_o);
+                    if (t >= own_tile) mma(e[t + 1], sh.in.dout.along(16u * t + n, 8u * q), own_r);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        dbeta += dpp<kQuadSwap2>(dbeta);
-        dbeta += dpp<kQuadSwap1>(dbeta);
-        if (row < rows && (threadIdx.x & 3u) == 0u) to.dbeta[(uint64_t)(c.lo + row) * a.heads + head] = dbeta;
+        dbeta = neighbours_sum<8>(dbeta);
+        if (row < rows && (threadIdx.x & 7u) == 0u) to.dbeta[(uint64_t)(c.lo + row) * a.heads + head] = dbeta;
         dot = wave_total(dot);
         __syncthreads();  // the last columns are read
         if (lane == 0u) sh.dot[wave] = dot;
@@ -443,50 +476,56 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
             const uint32_t at = 16u * t + n;
-            const double G = sh.sum[at];
-            const float e = exp_hw((float)G), tail = exp_hw((float)(all - G)), nu = sh.nu[at], mu = sh.mu[at];
             float query = 0.0f, key = 0.0f, end = 0.0f;
-            if (works) {
+            if (t >= t0 && t < t0 + TT) {
+                const double G = sh.sum[at];
+                const float grow = exp_hw((float)G), tail = exp_hw((float)(all - G)), be = sh.beta[at];
+                const float by_q = a.scale * grow * (of_s.back * of_o.back), by_r = grow * be * (of_s.back * of_omega.back);
+                const float by_e = tail * be * (of_d.back * of_rho.back);
 #pragma unroll
-                for (uint32_t d = 0; d < DT; ++d) {
-                    const uint32_t col = place(wave * DT + d, 4u * q);
-                    const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
-                    qs[d][t] *= a.scale * e;
-                    rs[d][t] *= e;
-                    ends[d][t] *= tail;
+                for (uint32_t tt = 0; tt < TT; ++tt) {
+                    if (t0 + tt != t) continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        query = __builtin_fmaf(qv[i], qs[d][t][i], query);
-                        key = __builtin_fmaf(kv[i], rs[d][t][i], key);
-                        end = __builtin_fmaf(kv[i], ends[d][t][i], end);
+                    for (uint32_t d = 0; d < DT; ++d) {
+                        const uint32_t col = 16u * (tile0 + d) + 4u * q;
+                        const f32x4 kv = sh.k.four(at, col), qv = sh.q.four(at, col);
+                        const f32x4 x = qs[d][tt] * by_q, y = rs[d][tt] * by_r, z = ends[d][tt] * by_e;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            query = __builtin_fmaf(qv[i], x[i], query);
+                            key = __builtin_fmaf(kv[i], y[i], key);
+                            end = __builtin_fmaf(kv[i], z[i], end);
+                        }
+                        dq[d][tt] += x;
+                        dk[d][tt] += z - y;
                     }
-                    dq[d][t] += qs[d][t];
-                    dk[d][t] += ends[d][t] - rs[d][t];
                 }
             }
             query = column_total(query), key = column_total(key), end = column_total(end);
             if (q == 0u) {
-                sh.part.query[wave][at] = query * mu;
-                sh.part.key[wave][at] = key * nu;
-                sh.part.end[wave][at] = end * nu;
+                sh.part.query[wave][at] = query * sh.mu[at];
+                sh.part.key[wave][at] = key * sh.nu[at];
+                sh.part.end[wave][at] = end * sh.nu[at];
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // the triangles: e1, e2 become dqk and dkk, and the pairs' sums of z
-        const uint32_t own = 16u * wave + n;
+        // the triangles become dqk or dkk with the factors of what they meet, and
+        // the pairs' sums of z
         const double G_own = sh.sum[own];
-        const float nu_own = sh.nu[own], mu_own = sh.mu[own];
+        const float beta_own = sh.beta[own], with_own = keys_side ? -beta_own * sh.nu[own] : a.scale * sh.mu[own];
+        const float back = of_rho.back * (keys_side ? of_omega.back : of_o.back), by_own = back * (keys_side ? -beta_own : a.scale);
         float pairs[16], before = 0.0f;
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
             float z[4] = {};
-            if (t <= wave) {
+            if (t <= own_tile) {
 #pragma unroll
                 for (uint32_t i = 0; i < 4u; ++i) {
-                    const uint32_t at = 16u * t + 4u * q + i;  // j
-                    const float f = at <= own ? exp_hw((float)(G_own - sh.sum[at])) * sh.nu[at] : 0.0f;
-                    e1[t][i] *= a.scale * f;
-                    e2[t][i] = at < own ? -f * e2[t][i] : 0.0f;
-                    z[i] = e1[t][i] * qk[t][i] * mu_own + e2[t][i] * kk[t][i] * nu_own;
+                    const uint32_t at = 16u * t + 4u * q + i;  // j; the lane has i
+                    const bool is = keys_side ? at < own : at <= own;
+                    const float f = is ? exp_hw((float)(G_own - sh.sum[at])) * sh.beta[at] * sh.nu[at] : 0.0f;
+                    z[i] = f * e[t][i] * back * kk[t][i] * with_own;
+                    e[t][i] *= f * by_own;
                 }
             }
             // sums over the rows before each, this tile's and those of the tiles before
@@ -504,116 +543,158 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, uint32_t 
                 upto += z[i];
             }
             before += column_total(four);
+            __builtin_amdgcn_sched_barrier(0);
         }
         const float pair = row_sums(pairs, lane);  // lane n of quarter q: tile n >> 2, row 4 q + (n & 3)
         sh.part.pair[wave][16u * (n >> 2) + 4u * q + (n & 3u)] = pair;
+        const float into_own = back * beta_own * (keys_side ? -1.0f : a.scale);
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
-            if (t < wave) continue;
+            if (t < own_tile) continue;
 #pragma unroll
             for (uint32_t i = 0; i < 4u; ++i) {
                 const uint32_t at = 16u * t + 4u * q + i;  // i; the lane has j
-                const float f = at >= own ? exp_hw((float)(sh.sum[at] - G_own)) : 0.0f;
-                e1[t + 1][i] *= a.scale * f * sh.mu[at];
-                e2[t + 1][i] = at > own ? -f * sh.nu[at] * e2[t + 1][i] : 0.0f;
+                const bool is = keys_side ? at > own : at >= own;
+                const float f = is ? exp_hw((float)(sh.sum[at] - G_own)) : 0.0f;
+                e[t + 1][i] *= f * into_own * (keys_side ? sh.beta[at] * sh.nu[at] : sh.mu[at]);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kScaled) {
+            float m = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 5; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(e[t][i]));
+            m = wave_largest(m);
+            if (lane == 0u) sh.most[wave] = m;
         }
         __syncthreads();
+        Scale of_e = {1.0f, 1.0f};
+        if constexpr (kScaled) {
+            float m = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) m = __builtin_fmaxf(m, sh.most[w]);
+            of_e = scale_of<true, -30>(m);
+        }
         if (wave == 0u) {
-            auto four = [&](const float(&p)[4][kChunk]) { return (p[0][lane] + p[1][lane]) + (p[2][lane] + p[3][lane]); };
-            double after = (double)four(sh.part.query) - (double)four(sh.part.key), ends_before = four(sh.part.end);
+            auto sum_of = [&](const float(&p)[8][kChunk]) {
+                return ((p[0][lane] + p[1][lane]) + (p[2][lane] + p[3][lane])) + ((p[4][lane] + p[5][lane]) + (p[6][lane] + p[7][lane]));
+            };
+            double after = (double)sum_of(sh.part.query) - (double)sum_of(sh.part.key), ends_before = sum_of(sh.part.end);
 #pragma unroll
             for (uint32_t by = 1u; by < 64u; by *= 2u) {
                 const double up = shuffle(after, lane + by), down = shuffle(ends_before, lane - by);
                 if (lane + by < 64u) after += up;
                 if (lane >= by) ends_before += down;
             }
-            const double whole = exp_hw((float)all) * ((sh.dot[0] + sh.dot[1]) + (sh.dot[2] + sh.dot[3]));
+            float whole = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) whole += sh.dot[w];
             double prior = shuffle(ends_before, lane - 1u);  // up to the row before
             if (lane == 0u) prior = 0.0;
             if (lane < rows)
-                to.dg[(uint64_t)(c.lo + lane) * a.heads + head] = (float)(four(sh.part.pair) + after + prior + whole);
+                to.dg[(uint64_t)(c.lo + lane) * a.heads + head] =
+                    (float)(sum_of(sh.part.pair) + after + prior + (double)(exp_hw((float)all) * whole));
         }
-        // dqk K, dkk K, dqk^T Q, dkk^T K, one triangle in shared memory at a time
+        // dqk K and dkk K, then dqk^T Q and dkk^T K, two triangles in shared memory at a time
+        if (kScaled) {
 #pragma unroll
-        for (uint32_t which = 0; which < 4u; ++which) {
-            const bool upper = which >= 2u;
+            for (uint32_t d = 0; d < DT; ++d)
+#pragma unroll
+                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_e.by, dk[d][t] *= of_e.by;
+        }
+#pragma unroll
+        for (uint32_t upper = 0; upper < 2u; ++upper) {
             __syncthreads();
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s) {
-                if (upper ? s < (wave >> 1) : s > (wave >> 1)) continue;
-                f32x4 pair_of[2];
+                if (upper ? s < (own_tile >> 1) : s > (own_tile >> 1)) continue;
+                f32x4 two[2];
 #pragma unroll
                 for (uint32_t h = 0; h < 2u; ++h) {
                     const uint32_t t = 2u * s + h;
-                    const bool there = upper ? t >= wave : t <= wave;
-                    const f32x4 v = which == 0u ? e1[t] : which == 1u ? e2[t] : which == 2u ? e1[t + 1] : e2[t + 1];
-                    pair_of[h] = there ? v : none;
+                    const bool there = upper ? t >= own_tile : t <= own_tile;
+                    two[h] = there ? e[t + upper] : none;
                 }
-                sh.triangle[upper ? upper_at(wave, s) : lower_at(wave, s)][lane] = operand_of<Mid>(pair_of[0], pair_of[1]);
+                sh.triangle[keys_side ? 1 : 0][upper ? upper_at(own_tile, s) : lower_at(own_tile, s)][lane] =
+                    operand_of<Mid>(two[0], two[1], of_e.by);
             }
             __syncthreads();
-            if (!works) continue;
 #pragma unroll
             for (uint32_t s = 0; s < 2u; ++s)
 #pragma unroll
                 for (uint32_t d = 0; d < DT; ++d) {
-                    const In keys = which == 2u ? sh.q.across(s, wave * DT + d, lane) : sh.k.across(s, wave * DT + d, lane);
+                    const auto keys = sh.k.columns(s, 16u * (tile0 + d), 4u, lane);
+                    const auto queries = upper ? sh.q.columns(s, 16u * (tile0 + d), 4u, lane) : keys;
 #pragma unroll
-                    for (uint32_t t = 0; t < 4u; ++t) {
-                        if (upper ? s < (t >> 1) : s > (t >> 1)) continue;
-                        const Mid m = sh.triangle[upper ? upper_at(t, s) : lower_at(t, s)][lane];
-                        mma(which == 0u ? dq[d][t] : dk[d][t], keys, m);
+                    for (uint32_t t = 0; t < TT; ++t) {
+                        const uint32_t tile = t0 + t;
+                        if (upper ? s < (tile >> 1) : s > (tile >> 1)) continue;
+                        const uint32_t at = upper ? upper_at(tile, s) : lower_at(tile, s);
+                        mma(upper ? dk[d][t] : dq[d][t], queries, sh.triangle[0][at][lane]);
+                        mma(dk[d][t], keys, sh.triangle[1][at][lane]);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
         }
+        if (kScaled) {
+#pragma unroll
+            for (uint32_t d = 0; d < DT; ++d)
+#pragma unroll
+                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_e.back, dk[d][t] *= of_e.back;
+        }
     }
+    __syncthreads();
+    if ((threadIdx.x & 7u) == 0u) sh.beta[row] = raw_mu, sh.sum[row] = raw_nu;
     if (a.unit) {
         // dq = mu (dq - q (q dq)) of q by its length
-        __syncthreads();
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
             const uint32_t at = 16u * t + n;
             float query = 0.0f, key = 0.0f;
-            if (works) {
+#pragma unroll
+            for (uint32_t tt = 0; tt < TT; ++tt) {
+                if (t0 + tt != t) continue;
 #pragma unroll
                 for (uint32_t d = 0; d < DT; ++d) {
-                    const uint32_t col = place(wave * DT + d, 4u * q);
-                    const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
+                    const uint32_t col = 16u * (tile0 + d) + 4u * q;
+                    const f32x4 kv = sh.k.four(at, col), qv = sh.q.four(at, col);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        query = __builtin_fmaf(qv[i], dq[d][t][i], query);
-                        key = __builtin_fmaf(kv[i], dk[d][t][i], key);
+                        query = __builtin_fmaf(qv[i], dq[d][tt][i], query);
+                        key = __builtin_fmaf(kv[i], dk[d][tt][i], key);
                     }
                 }
             }
             query = column_total(query), key = column_total(key);
             if (q == 0u) sh.part.query[wave][at] = query, sh.part.key[wave][at] = key;
         }
-        __syncthreads();
     }
-    if (!works) return;
+    __syncthreads();
 #pragma unroll
-    for (uint32_t t = 0; t < 4u; ++t) {
-        const uint32_t at = 16u * t + n;
-        float nu = 1.0f, mu = 1.0f, query = 0.0f, key = 0.0f;
+    for (uint32_t t = 0; t < TT; ++t) {
+        const uint32_t at = 16u * (t0 + t) + n;
+        float query = 0.0f, key = 0.0f;
+        const float nu = sh.nu[at], mu = sh.mu[at], by_q = sh.beta[at], by_k = (float)sh.sum[at];
         if (a.unit) {
-            auto four = [&](const float(&p)[4][kChunk]) { return (p[0][at] + p[1][at]) + (p[2][at] + p[3][at]); };
-            nu = sh.nu[at], mu = sh.mu[at];
-            query = four(sh.part.query) * mu * mu, key = four(sh.part.key) * nu * nu;
+            auto sum_of = [&](const float(&p)[8][kChunk]) {
+                return ((p[0][at] + p[1][at]) + (p[2][at] + p[3][at])) + ((p[4][at] + p[5][at]) + (p[6][at] + p[7][at]));
+            };
+            query = sum_of(sh.part.query) * mu * mu, key = sum_of(sh.part.key) * nu * nu;
         }
         if (at >= rows) continue;
 #pragma unroll
         for (uint32_t d = 0; d < DT; ++d) {
-            const uint32_t col = place(wave * DT + d, 4u * q);
+            const uint32_t col = 16u * (tile0 + d) + 4u * q;
             if (col >= a.key_dim) continue;
-            const f32x4 kv = four_keys(sh.k, at, col), qv = four_keys(sh.q, at, col);
+            const f32x4 kv = sh.k.four(at, col), qv = sh.q.four(at, col);
             const uint64_t to_row = ((uint64_t)(c.lo + at) * a.kheads + khead) * a.key_dim + col;
             Pack<T, 4> wq, wk;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                wq.v[i] = (T)(mu * __builtin_fmaf(-qv[i], query, dq[d][t][i]));
-                wk.v[i] = (T)(nu * __builtin_fmaf(-kv[i], key, dk[d][t][i]));
+                wq.v[i] = (T)(by_q * __builtin_fmaf(-qv[i], query, dq[d][t][i]));
+                wk.v[i] = (T)(by_k * __builtin_fmaf(-kv[i], key, dk[d][t][i]));
             }
             T *pq = static_cast<T *>(to.dq) + to_row, *pk = static_cast<T *>(to.dk) + to_row;
             if (E || col + 4u <= a.key_dim) {
@@ -642,6 +723,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u, state_floats = (uint64_t)a.slots * a.heads * cells;
     const size_t m_at = plan.take(linked * a.key_dim * a.key_dim * 4u), n_at = plan.take(linked * cells * 4u);
+    const size_t sizes_at = plan.take((size_t)a.slots * a.heads * kBackSizes * 4u);
     const size_t d_at = plan.take(state_floats * 4u), omega_at = plan.take((size_t)a.tokens * a.heads * a.value_dim * 4u);
     bool query = false;
     ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
@@ -666,7 +748,9 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
     float *dstates = ws_at<float>(ws, d_at), *omega = ws_at<float>(ws, omega_at);
     const T *g = static_cast<const T *>(dout);
-    const BackResults to = {dfinal, grads->dinitial, dstates, omega};
+    float *back_sizes = ws_at<float>(ws, sizes_at);
+    const float *rhos = checkpoints + state_floats, *sizes = rhos + (uint64_t)a.tokens * a.heads * a.value_dim;
+    const BackResults to = {dfinal, grads->dinitial, dstates, omega, back_sizes};
     const DeltaGradPtrs out = {grads->dq, grads->dk, grads->dv, grads->dg, grads->dbeta};
     return with_key_width(a.key_dim, [&](auto w) {
         constexpr int W = decltype(w)::value;
@@ -693,9 +777,9 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                 hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared, seg,
                                    g, false, to);
             });
-            launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 256u, [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_grads_kernel<T, W, E>), dim3(grid), dim3(256), 0, s, a, first, g, checkpoints,
-                                   checkpoints + state_floats, dstates, omega, out);
+            launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 512u, [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_grads_kernel<T, W, E>), dim3(grid), dim3(512), 0, s, a, first, g, checkpoints, rhos, sizes,
+                                   dstates, omega, back_sizes, (uint32_t)ceil_div(a.value_dim, 16u * CT), out);
             });
         };
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;

@@ -42,6 +42,8 @@ namespace dwps {
 constexpr uint32_t kChunk = 64u, kChunkShift = 6u;
 constexpr size_t kMostShared = 160u * 1024u;  // of a workgroup
 
+typedef f16_t f16x8 __attribute__((ext_vector_type(8)));
+typedef f16_t f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -65,11 +67,16 @@ struct DeltaArgs {
     float scale, eps;
 };
 
-// Eight places of an operand: N planes of a 16-bit type, or the numbers themselves.
-template <class E, int N>
+// The wave's number in its workgroup, in a scalar register: what depends on it
+// is a branch of the wave, not a mask of its lanes.
+__device__ __forceinline__ uint32_t wave_number() {
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
+// Eight places of an operand: N fp16 planes, or the numbers themselves.
+template <int N>
 struct Planes {
-    typedef E Eight __attribute__((ext_vector_type(8)));
-    Eight p[N];
+    f16x8 p[N];
 };
 struct Wide {
     float p[8];
@@ -77,12 +84,12 @@ struct Wide {
 
 // The operand of eight numbers times `by`: each plane is the rounding of what
 // the ones before leave.
-template <class E, int N>
-__device__ __forceinline__ void operand_of(Planes<E, N> &o, const float (&v)[8], float by = 1.0f) {
+template <int N>
+__device__ __forceinline__ void operand_of(Planes<N> &o, const float (&v)[8], float by = 1.0f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        o.p[0][j] = (E)(v[j] * by);
-        if (N > 1) o.p[N - 1][j] = (E)__builtin_fmaf(v[j], by, -(float)o.p[0][j]);
+        o.p[0][j] = (f16_t)(v[j] * by);
+        if (N > 1) o.p[N - 1][j] = (f16_t)__builtin_fmaf(v[j], by, -(float)o.p[0][j]);
     }
 }
 __device__ __forceinline__ void operand_of(Wide &o, const float (&v)[8], float = 1.0f) {
@@ -100,61 +107,39 @@ __device__ __forceinline__ M operand_of(const f32x4 &a, const f32x4 &b, float by
 
 // acc += A B over 32 places: the products of planes i and j with i + j below
 // the larger number of planes, smallest first.
-__device__ __forceinline__ void mma_one(f32x4 &acc, const Planes<bf16_t, 1>::Eight &a, const Planes<bf16_t, 1>::Eight &b) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
-}
-__device__ __forceinline__ void mma_one(f32x4 &acc, const Planes<f16_t, 1>::Eight &a, const Planes<f16_t, 1>::Eight &b) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
-}
-template <class E, int NA, int NB>
-__device__ __forceinline__ void mma(f32x4 &acc, const Planes<E, NA> &a, const Planes<E, NB> &b) {
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 &acc, const Planes<NA> &a, const Planes<NB> &b) {
     constexpr int most = NA > NB ? NA : NB;
 #pragma unroll
     for (int sum = most - 1; sum >= 0; --sum)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (sum - i >= 0 && sum - i < NB) mma_one(acc, a.p[i], b.p[sum - i]);
+            if (sum - i >= 0 && sum - i < NB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.p[i], b.p[sum - i], acc, 0, 0, 0);
 }
 __device__ __forceinline__ void mma(f32x4 &acc, const Wide &a, const Wide &b) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.p[j], b.p[j], acc, 0, 0, 0);
 }
 
-// How activations of type T are held in shared memory (planes of words) and
-// become operands; Mid: operands made of computed numbers.  Form is that of the
-// walks, scaled to fp16's range; Plain that of the pass over the chunks'
-// gradients, which sums over columns that it does not have at once, so that no
-// power of two is theirs: bf16 planes, two for fp16 and computed numbers.
+// How activations of type T are held in shared memory and become operands; Mid:
+// operands made of computed numbers.
 template <class T>
 struct Form {
     typedef uint16_t Word;
-    typedef f16_t Part;
     static constexpr bool scaled = true;
-    static constexpr int planes = 1, pad = 8;
-    typedef Planes<f16_t, 1> In;
-    typedef Planes<f16_t, 2> Mid;
+    static constexpr int pad = 8;
+    typedef Planes<1> In;
+    typedef Planes<2> Mid;
 };
-template <class T>
-struct Plain {
-    typedef uint16_t Word;
-    typedef bf16_t Part;
-    static constexpr bool scaled = false;
-    static constexpr int planes = std::is_same<T, bf16_t>::value ? 1 : 2, pad = 8;
-    typedef Planes<bf16_t, planes> In;
-    typedef Planes<bf16_t, 2> Mid;
-};
-struct WideForm {
+template <>
+struct Form<float> {
     typedef float Word;
-    typedef float Part;
     static constexpr bool scaled = false;
-    static constexpr int planes = 1, pad = 4;
+    static constexpr int pad = 4;
     typedef Wide In;
     typedef Wide Mid;
 };
-template <>
-struct Form<float> : WideForm {};
-template <>
-struct Plain<float> : WideForm {};
 
 // A power of two that brings numbers up to `most` to 2^14 .. 2^15, and its
 // reciprocal.  Numbers below 2^least are left small: a product's scale is that
@@ -213,68 +198,93 @@ __device__ __forceinline__ uint32_t token_at(uint32_t s, uint32_t q, uint32_t j)
     return 32u * s + 16u * (j >> 2) + 4u * q + (j & 3u);
 }
 
-// kChunk rows of `W` columns of activations in shared memory, in form F.
-template <class F, int W, int PAD = F::pad>
-struct RowTile {
-    typedef typename F::Word Word;
-    static constexpr int kStride = W + PAD;
-    Word w[F::planes][kChunk][kStride];
-
-    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8], float by = 1.0f) {
-        typename F::In o;
+// kChunk rows of `W` columns in shared memory, as operands O (one or two planes
+// of words, or numbers).  A column of a tile of keys is read across the rows
+// with the transposing read, which gives lane m of 16 the m & 3'rd of the four
+// words that lanes (m >> 2) + 4 j point at.
+template <class O, int W>
+struct RowTile;
+template <int N, int W>
+struct RowTile<Planes<N>, W> {
+    static constexpr int kStride = W + 8;
+    uint16_t w[N][kChunk][kStride];
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8], float by) {
+        Planes<N> o;
         operand_of(o, v, by);
-        put(row, col, o);
-    }
-    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Wide &o) {
-        *reinterpret_cast<f32x4 *>(&w[0][row][col]) = f32x4{o.p[0], o.p[1], o.p[2], o.p[3]};
-        *reinterpret_cast<f32x4 *>(&w[0][row][col + 4]) = f32x4{o.p[4], o.p[5], o.p[6], o.p[7]};
-    }
-    template <class E, int N>
-    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const Planes<E, N> &o) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<typename Planes<E, N>::Eight *>(&w[i][row][col]) = o.p[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<f16x8 *>(&w[i][row][col]) = o.p[i];
     }
-    // Eight columns of a row.
-    __device__ __forceinline__ typename F::In along(uint32_t row, uint32_t col) const {
-        typename F::In o;
-        get(o, row, col);
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const f32x4 &v, float by) {
+        f16x4 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = (f16_t)(v[i] * by);
+            lo[i] = (f16_t)__builtin_fmaf(v[i], by, -(float)hi[i]);
+        }
+        *reinterpret_cast<f16x4 *>(&w[0][row][col]) = hi;
+        if (N > 1) *reinterpret_cast<f16x4 *>(&w[N - 1][row][col]) = lo;
+    }
+    // Eight columns of a row; four of them as numbers (of the first plane).
+    __device__ __forceinline__ Planes<N> along(uint32_t row, uint32_t col) const {
+        Planes<N> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const f16x8 *>(&w[i][row][col]);
         return o;
     }
-    __device__ __forceinline__ void get(Wide &o, uint32_t row, uint32_t col) const {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(&w[0][row][col]);
-        const f32x4 b = *reinterpret_cast<const f32x4 *>(&w[0][row][col + 4]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o.p[i] = a[i], o.p[4 + i] = b[i];
+    __device__ __forceinline__ f32x4 four(uint32_t row, uint32_t col) const {
+        const f16x4 r = *reinterpret_cast<const f16x4 *>(&w[0][row][col]);
+        return f32x4{(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
     }
-    template <class E, int N>
-    __device__ __forceinline__ void get(Planes<E, N> &o, uint32_t row, uint32_t col) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) o.p[i] = *reinterpret_cast<const typename Planes<E, N>::Eight *>(&w[i][row][col]);
-    }
-    // A column of tile `tile` of keys, key place(tile, lane & 15), at the places
-    // token_at(s, lane >> 4, 0..7): the transposing read gives lane m of 16 the
-    // m & 3'rd of the four words that lanes (m >> 2) + 4 j point at.
-    __device__ __forceinline__ typename F::In across(uint32_t s, uint32_t tile, uint32_t lane) const {
-        typename F::In o;
-        get_across(o, s, tile, lane);
-        return o;
-    }
-    __device__ __forceinline__ void get_across(Wide &o, uint32_t s, uint32_t tile, uint32_t lane) const {
-#pragma unroll
-        for (uint32_t j = 0; j < 8u; ++j) o.p[j] = w[0][token_at(s, lane >> 4, j)][place(tile, lane & 15u)];
-    }
-    template <class E, int N>
-    __device__ __forceinline__ void get_across(Planes<E, N> &o, uint32_t s, uint32_t tile, uint32_t lane) const {
-        const uint32_t i = lane & 15u, row = 32u * s + 4u * (lane >> 4) + (i >> 2);
-        const uint32_t col = 32u * (tile >> 1) + 8u * (i & 3u) + 4u * (tile & 1u);
+    // Columns col0 + step (m >> 2) + (m & 3) at the places token_at(s, q, 0..7).
+    __device__ __forceinline__ Planes<N> columns(uint32_t s, uint32_t col0, uint32_t step, uint32_t lane) const {
+        const uint32_t i = lane & 15u, row = 32u * s + 4u * (lane >> 4) + (i >> 2), col = col0 + step * (i & 3u);
+        Planes<N> o;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const uint64_t a = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row][col]));
             const uint64_t b = __builtin_bit_cast(uint64_t, read_transposed(&w[n][row + 16u][col]));
-            o.p[n] = __builtin_bit_cast(typename Planes<E, N>::Eight, uint64x2{a, b});
+            o.p[n] = __builtin_bit_cast(f16x8, uint64x2{a, b});
         }
+        return o;
+    }
+    __device__ __forceinline__ Planes<N> across(uint32_t s, uint32_t tile, uint32_t lane) const {
+        return columns(s, place(tile, 0u), 8u, lane);
     }
 };
+template <int W>
+struct RowTile<Wide, W> {
+    static constexpr int kStride = W + 4;
+    float w[1][kChunk][kStride];
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8], float) {
+        *reinterpret_cast<f32x4 *>(&w[0][row][col]) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4 *>(&w[0][row][col + 4]) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+    __device__ __forceinline__ void put(uint32_t row, uint32_t col, const f32x4 &v, float) {
+        *reinterpret_cast<f32x4 *>(&w[0][row][col]) = v;
+    }
+    __device__ __forceinline__ Wide along(uint32_t row, uint32_t col) const {
+        const f32x4 a = four(row, col), b = four(row, col + 4u);
+        Wide o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.p[i] = a[i], o.p[4 + i] = b[i];
+        return o;
+    }
+    __device__ __forceinline__ f32x4 four(uint32_t row, uint32_t col) const {
+        return *reinterpret_cast<const f32x4 *>(&w[0][row][col]);
+    }
+    __device__ __forceinline__ Wide columns(uint32_t s, uint32_t col0, uint32_t step, uint32_t lane) const {
+        const uint32_t m = lane & 15u;
+        Wide o;
+#pragma unroll
+        for (uint32_t j = 0; j < 8u; ++j) o.p[j] = w[0][token_at(s, lane >> 4, j)][col0 + step * (m >> 2) + (m & 3u)];
+        return o;
+    }
+    __device__ __forceinline__ Wide across(uint32_t s, uint32_t tile, uint32_t lane) const {
+        return columns(s, place(tile, 0u), 8u, lane);
+    }
+};
+template <class T, int W>
+using KeyTile = RowTile<typename Form<T>::In, W>;
 
 // Eight activations of a row from column c of `width`, zeros past its end.
 template <class T>
@@ -313,40 +323,55 @@ __device__ __forceinline__ void values_of(float (&v)[8], const Pack<T, 8> &r) {
     for (int j = 0; j < 8; ++j) v[j] = (float)r.v[j];
 }
 
-// The largest of a row's numbers that four neighbouring threads hold.
-template <int N>
-__device__ __forceinline__ float row_largest(const float (&v)[N][8]) {
+// Sum or largest of a row's numbers over its PER = 4 or 8 neighbouring threads.
+template <int PER>
+__device__ __forceinline__ float neighbours_sum(float v) {
+    v += dpp<kQuadSwap2>(v);
+    v += dpp<kQuadSwap1>(v);
+    return PER == 8 ? v + dpp<kRowHalfMirror>(v) : v;
+}
+template <int PER>
+__device__ __forceinline__ float neighbours_largest(float m) {
+    m = __builtin_fmaxf(m, dpp<kQuadSwap2>(m));
+    m = __builtin_fmaxf(m, dpp<kQuadSwap1>(m));
+    return PER == 8 ? __builtin_fmaxf(m, dpp<kRowHalfMirror>(m)) : m;
+}
+// The scale of a row of keys or queries that PER neighbouring threads hold.
+template <class T, int PER, int N>
+__device__ __forceinline__ Scale row_scale(const float (&v)[N][8]) {
+    if (!Form<T>::scaled) return {1.0f, 1.0f};
     float m = 0.0f;
 #pragma unroll
     for (int c = 0; c < N; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[c][j]));
-    m = __builtin_fmaxf(m, dpp<kQuadSwap2>(m));
-    return __builtin_fmaxf(m, dpp<kQuadSwap1>(m));
+    return scale_of<true>(neighbours_largest<PER>(m));
 }
 
 // Rows lo .. lo + rows of a head's keys or queries into a tile, zeros after
-// them; 256 threads, four a row.  Returns the factor of the thread's row
-// (threadIdx.x >> 2) in a product with the tile: 1 by its length or 1, and what
-// takes the tile's power of two back.
-template <class T, class F, int W>
-__device__ __forceinline__ float fill_rows(RowTile<F, W> &tile, const void *from, int64_t stride, uint32_t head,
-                                           uint32_t lo, uint32_t rows, const DeltaArgs &a) {
-    const uint32_t row = threadIdx.x >> 2, part = (threadIdx.x & 3u) * 8u;
+// them, PER threads a row.  Returns the factor of the thread's row (threadIdx.x
+// / PER) in a product with the tile: 1 by its length or 1, and what takes the
+// tile's power of two back; `raw`: without the latter.
+template <class T, int PER, int W>
+__device__ __forceinline__ float fill_rows(KeyTile<T, W> &tile, const void *from, int64_t stride, uint32_t head,
+                                           uint32_t lo, uint32_t rows, const DeltaArgs &a, float *raw = nullptr) {
+    constexpr uint32_t kStep = 8u * PER, kVecs = (W + kStep - 1u) / kStep;
+    const uint32_t row = threadIdx.x / PER, part = (threadIdx.x % PER) * 8u;
     const T *p = static_cast<const T *>(from) + (int64_t)(lo + row) * stride + (int64_t)head * a.key_dim;
-    float v[W / 32][8] = {}, sum = 0.0f;
+    float v[kVecs][8] = {}, sum = 0.0f;
 #pragma unroll
-    for (uint32_t c = 0; c < W / 32u; ++c) {
-        if (row < rows) load8<T>(v[c], p, part + 32u * c, a.key_dim);
+    for (uint32_t c = 0; c < kVecs; ++c) {
+        if (row < rows) load8<T>(v[c], p, part + kStep * c, a.key_dim);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[c][j], v[c][j], sum);
     }
-    const Scale s = scale_of<F::scaled>(F::scaled ? row_largest(v) : 0.0f);
+    const Scale s = row_scale<T, PER>(v);
 #pragma unroll
-    for (uint32_t c = 0; c < W / 32u; ++c) tile.put(row, part + 32u * c, v[c], s.by);
-    sum += dpp<kQuadSwap2>(sum);
-    sum += dpp<kQuadSwap1>(sum);
-    return a.unit ? s.back / __builtin_sqrtf(sum + a.eps) : s.back;
+    for (uint32_t c = 0; c < kVecs; ++c)
+        if (part + kStep * c < (uint32_t)W) tile.put(row, part + kStep * c, v[c], s.by);
+    const float by = a.unit ? 1.0f / __builtin_sqrtf(neighbours_sum<PER>(sum) + a.eps) : 1.0f;
+    if (raw) *raw = by;
+    return by * s.back;
 }
 
 // The column in lane m of tile ct of a wave's 16 CT columns.
@@ -539,7 +564,7 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
     typedef typename Form<T>::Mid Mid;
     union Shared {
         struct {
-            RowTile<Form<T>, W> k, q;
+            KeyTile<T, W> k, q;
         } in;
         float tri[kChunk * kTriStride];
     };
@@ -553,9 +578,9 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
     const Chunk c = find_chunk(a.offsets, a.num_seqs, a.tokens, kChunkShift, slot);
     const uint32_t rows = c.hi - c.lo;
     if (rows == 0u) return;
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
-    const float own_nu = fill_rows<T>(sh.in.k, a.k, a.k_stride, khead, c.lo, rows, a);
-    const float own_mu = fill_rows<T>(sh.in.q, a.q, a.q_stride, khead, c.lo, rows, a);
+    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
+    const float own_nu = fill_rows<T, 4, W>(sh.in.k, a.k, a.k_stride, khead, c.lo, rows, a);
+    const float own_mu = fill_rows<T, 4, W>(sh.in.q, a.q, a.q_stride, khead, c.lo, rows, a);
     if ((threadIdx.x & 3u) == 0u) nu[threadIdx.x >> 2] = own_nu, mu[threadIdx.x >> 2] = own_mu;
     __syncthreads();
     // kk: rows k_l, columns k of tile `wave`; qk: forwards rows k_j, columns q of
@@ -642,6 +667,10 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
         }
     }
 }
+
+// Sizes of a chunk's states and corrections that a walk leaves for the gradients:
+// the largest of each, by wave of columns.
+constexpr uint32_t kSizeWaves = 16u, kSizes = 2u * kSizeWaves;
 
 // ---------------------------------------------------------------------------
 // host side

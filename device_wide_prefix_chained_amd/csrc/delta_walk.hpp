@@ -17,7 +17,7 @@ namespace {
 template <class T, int W, int CT>
 struct WalkTile {
     static constexpr uint32_t kCols = 64u * CT;
-    RowTile<Form<T>, W> k, q;
+    KeyTile<T, W> k, q;
     Prepared<T> p;
     T v[kChunk][kCols + 8u];
 };
@@ -57,6 +57,7 @@ struct Segments {
 struct WalkResults {
     void *out;
     float *final, *states, *rhos;
+    float *sizes;  // [chunk numbers, heads, kSizes]: the largest of `states` and of `rhos`, by wave of columns
 };
 
 // The feeding waves of a walk: keys, queries, values and what was prepared of
@@ -105,11 +106,11 @@ struct DeltaFeed {
             }
         };
         auto leave = [&](Tile *to) {
-            auto put = [&](RowTile<Form<T>, W> &tile, const Pack<T, 8>(&from)[kKeys]) {
+            auto put = [&](KeyTile<T, W> &tile, const Pack<T, 8>(&from)[kKeys]) {
                 float v[kKeys][8];
 #pragma unroll
                 for (uint32_t c = 0; c < kKeys; ++c) values_of<T>(v[c], from[c]);
-                const Scale by = scale_of<Form<T>::scaled>(Form<T>::scaled ? row_largest(v) : 0.0f);
+                const Scale by = row_scale<T, 4>(v);
 #pragma unroll
                 for (uint32_t c = 0; c < kKeys; ++c) tile.put(row, part + 32u * c, v[c], by.by);
             };
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = LEAD ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
     const bool unit = block < key_blocks;  // columns of M
     const uint32_t block0 = (block - (unit ? 0u : key_blocks)) * kCols, width = unit ? a.key_dim : a.value_dim;
     const Chunk r = find_chunk(a.offsets, a.num_seqs, a.tokens, seg.shift, number);
@@ -267,9 +268,15 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
                     for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
                 }
             }
-            if (!LEAD && to.rhos)
+            if (!LEAD && to.rhos) {
+                if (kScaled) {
+                    const float of_y = wave_largest(largest(y)) * from_x;
+                    float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kSizes + col0 / (16u * CT);
+                    if (lane == 0u) sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y;
+                }
                 store_rows<E>(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, from_x,
                               rows, col0, a.value_dim, lane);
+            }
             __builtin_amdgcn_sched_barrier(0);
             // U, and out^T = scale e (Q S)^T + U^T P^T
 #pragma unroll
@@ -370,7 +377,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
     constexpr uint32_t kTiles = W / 16;
     constexpr bool kScaled = Form<T>::scaled;
     const uint32_t blocks = (a.value_dim + 63u) / 64u, item = first + blockIdx.x / blocks, head = item % a.heads;
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
+    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
     const uint32_t col0 = blockIdx.x % blocks * 64u + wave * 16u, s = item / a.heads;
     const Rows r = sequence_rows(a.offsets, a.tokens, s, seg.shift);
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim, key_cells = (uint64_t)a.key_dim * a.key_dim;
@@ -468,7 +475,8 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
         return PS_ERR_ALIAS;
     if (!a.num_seqs) return PS_OK;
     Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
-    float *rhos = checkpoints ? checkpoints + (uint64_t)a.slots * a.heads * a.key_dim * a.value_dim : nullptr;
+    float *rhos = checkpoints ? checkpoints + (uint64_t)a.slots * a.heads * cells : nullptr;
+    float *sizes = checkpoints ? rhos + (uint64_t)a.tokens * a.heads * a.value_dim : nullptr;
     return with_key_width(a.key_dim, [&](auto w) {
         constexpr int W = decltype(w)::value;
         timing_begin(s);
@@ -477,7 +485,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                                ws_counter(ws), plan.words());
         });
         seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
-        const WalkResults to = {out, final, checkpoints, rhos};
+        const WalkResults to = {out, final, checkpoints, rhos, sizes};
         auto walk = [&](auto ct, auto eights) {
             constexpr int CT = decltype(ct)::value;
             constexpr bool E = decltype(eights)::value;
