@@ -300,11 +300,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
     const Chunk c = find_chunk(a.offsets, a.num_seqs, a.tokens, kChunkShift, slot);
     const uint32_t rows = c.hi - c.lo;
     if (rows == 0u) return;
-    const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
+    const uint32_t wave = wave_number();
+    uint32_t lane = threadIdx.x & 63u, n = lane & 15u, q = lane >> 4;
     const uint32_t tile0 = W >= 128 ? wave * DT : wave % kTiles, t0 = W >= 128 ? 0u : wave / kTiles * TT;
-    const uint32_t own_tile = wave & 3u, own = 16u * own_tile + n;
+    const uint32_t own_tile = wave & 3u;
+    uint32_t own = 16u * own_tile + n;
     const bool keys_side = wave >= 4u;  // omega rho^T and k k^T, not dO rho^T and q k^T
-    const uint32_t row = threadIdx.x >> 3, part = (threadIdx.x & 7u) * 4u;
+    uint32_t row = threadIdx.x >> 3, part = (threadIdx.x & 7u) * 4u;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
     float raw_nu, raw_mu;
     {
@@ -313,17 +315,6 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
         if ((threadIdx.x & 7u) == 0u) sh.nu[row] = own_nu, sh.mu[row] = own_mu;
     }
     __syncthreads();
-    // k_j k_i or k_j q_i, rows j in the registers, i = own in the lane
-    f32x4 kk[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) kk[t] = none;
-#pragma unroll
-    for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
-        const auto b = keys_side ? sh.k.along(own, col + 8u * q) : sh.q.along(own, col + 8u * q);
-#pragma unroll
-        for (uint32_t t = 0; t < 4u; ++t)
-            if (t <= own_tile) mma(kk[t], sh.k.along(16u * t + n, col + 8u * q), b);
-    }
     f32x4 dq[DT][TT], dk[DT][TT];  // with respect to the keys and queries of length 1
 #pragma unroll
     for (uint32_t d = 0; d < DT; ++d)
@@ -333,6 +324,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     for (uint32_t j = 0; j < per; ++j) {
         const uint32_t head = khead * per + j;
+        // what follows from a lane's number is found anew for each head: kept over
+        // the heads it takes the registers that the sums need
+        asm volatile("" : "+v"(n), "+v"(q), "+v"(own), "+v"(lane), "+v"(row), "+v"(part));
         const uint64_t of_head = (uint64_t)slot * a.heads + head, at_row = ((uint64_t)(c.lo + row) * a.heads + head) * a.value_dim;
         const float *state = states + of_head * cells, *dstate = dstates + of_head * cells;
         // the next 32 columns, on their way while some are worked on
@@ -509,6 +503,17 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+            // k_j k_i or k_j q_i, rows j in the registers, i = own in the lane
+            f32x4 kk[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kk[t] = none;
+#pragma unroll
+            for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
+                const auto b = keys_side ? sh.k.along(own, col + 8u * q) : sh.q.along(own, col + 8u * q);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+                    if (t <= own_tile) mma(kk[t], sh.k.along(16u * t + n, col + 8u * q), b);
+            }
         // the triangles become dqk or dkk with the factors of what they meet, and
         // the pairs' sums of z
         const double G_own = sh.sum[own];
