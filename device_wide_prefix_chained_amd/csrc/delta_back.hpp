@@ -61,6 +61,9 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
     if (wave >= 4u) {
         feed.template run<false>(chunks, !unit, tile, [&](uint32_t i) { return chunks - 1u - i; });
+        if (unit)
+            store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
     const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
@@ -226,10 +229,14 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
         if (!kTwo) __syncthreads();
         __syncthreads();
     }
-    if (col0 >= width) return;
     const uint64_t place_of = (uint64_t)number * a.heads + head;
-    if (unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, D, unit_of, a.key_dim, a.key_dim, col0, lane);
-    else if (lead) store_states<E>(seg.n + place_of * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
+    if (unit) {
+        store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), D, unit_of,
+                               block0, wave, lane, true);
+        return;
+    }
+    if (col0 >= width) return;
+    if (lead) store_states<E>(seg.n + place_of * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
     else if (to.dinitial && r.lo == seq.lo)
         store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
 }
@@ -727,7 +734,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     seg.shift = segment_shift(a, wide ? 128u : 64u);
     const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u, state_floats = (uint64_t)a.slots * a.heads * cells;
-    const size_t m_at = plan.take(linked * a.key_dim * a.key_dim * 4u), n_at = plan.take(linked * cells * 4u);
+    const size_t m_at = plan.take(linked * matrix_bytes<T>(a.key_dim)), n_at = plan.take(linked * cells * 4u);
     const size_t sizes_at = plan.take((size_t)a.slots * a.heads * kBackSizes * 4u);
     const size_t d_at = plan.take(state_floats * 4u), omega_at = plan.take((size_t)a.tokens * a.heads * a.value_dim * 4u);
     bool query = false;
@@ -750,7 +757,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
         return PS_ERR_ALIAS;
     if (!a.num_seqs) return PS_OK;
     Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
-    seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
+    seg.m = ws_at<void *>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
     float *dstates = ws_at<float>(ws, d_at), *omega = ws_at<float>(ws, omega_at);
     const T *g = static_cast<const T *>(dout);
     float *back_sizes = ws_at<float>(ws, sizes_at);
@@ -773,7 +780,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                     hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared,
                                        seg, g, true, to);
                 });
-                const uint64_t columns = ceil_div(a.value_dim, 64u);
+                const uint64_t columns = ceil_div(a.value_dim, 32u);
                 launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
                     hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(256), 0, s, a, first, seg, dfinal);
                 });

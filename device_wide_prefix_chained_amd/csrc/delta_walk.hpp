@@ -51,9 +51,46 @@ __device__ __forceinline__ f32x4 value_rows(const T (&tile)[kChunk][STRIDE], uin
 // `shift` 31: whole sequences, one segment each.
 struct Segments {
     uint32_t shift;
-    float *m;  // [segment numbers, heads, key_dim, key_dim]
+    void *m;   // [segment numbers, heads] of SegmentMatrix
     float *n;  // [segment numbers, heads, key_dim, value_dim]: N, then the states that enter
 };
+// M as operands: rows place(t, lane & 15), columns 32 c + 8 (lane >> 4) .., each
+// operand with what takes its scale back.
+template <class T, int W>
+struct SegmentMatrix {
+    typename Form<T>::Mid m[W / 16][W / 32][64];
+    float back[W / 16][W / 32];
+};
+// Columns of M that four waves hold, into operands, by way of shared memory;
+// all eight waves, `walks`: those that hold them.
+template <class T, int W, int CT>
+__device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *shared, const f32x4 (*S)[W / 16], float by,
+                                             uint32_t block0, uint32_t wave, uint32_t lane, bool walks) {
+    constexpr uint32_t kCols = 64u * CT, kRow = kCols + 4u;
+    static_assert(W * kRow * 4u <= kMostShared, "a block of M fits shared memory");
+    const uint32_t m = lane & 15u, q = lane >> 4;
+    if (walks) {
+#pragma unroll
+        for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+#pragma unroll
+            for (uint32_t t = 0; t < W / 16u; ++t)
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i)
+                    shared[place(t, 4u * q + i) * kRow + wave * 16u * CT + column<CT>(ct, m)] = S[ct][t][i] * by;
+    }
+    __syncthreads();
+    for (uint32_t i = wave; i < W / 16u * (kCols / 32u); i += 8u) {
+        const uint32_t t = i / (kCols / 32u), c = i % (kCols / 32u);
+        if (block0 + 32u * c >= (uint32_t)W) continue;
+        const float *p = shared + place(t, m) * kRow + 32u * c + 8u * q;
+        float v[8], most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p[j], most = __builtin_fmaxf(most, __builtin_fabsf(v[j]));
+        const Scale of = scale_of<Form<T>::scaled>(Form<T>::scaled ? wave_largest(most) : 0.0f);
+        operand_of(to.m[t][block0 / 32u + c][lane], v, of.by);
+        if (lane == 0u) to.back[t][block0 / 32u + c] = of.back;
+    }
+}
 struct WalkResults {
     void *out;
     float *final, *states, *rhos;
@@ -179,6 +216,9 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     const DeltaFeed<T, W, CT, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
     if (wave >= 4u) {
         feed.template run<LEAD>(chunks, !unit, tile, [](uint32_t i) { return i; });
+        if (LEAD && unit)
+            store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
     const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
@@ -359,63 +399,132 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
         if (!kTwo) __syncthreads();
         __syncthreads();
     }
-    if (col0 >= width) return;
     const uint64_t place_of = (uint64_t)number * a.heads + head;
-    if (LEAD && unit) store_states<E>(seg.m + place_of * a.key_dim * a.key_dim, S, unit_of, a.key_dim, a.key_dim, col0, lane);
-    else if (LEAD) store_states<E>(seg.n + place_of * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
+    if (LEAD && unit) {
+        store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), S, unit_of,
+                               block0, wave, lane, true);
+        return;
+    }
+    if (col0 >= width) return;
+    if (LEAD) store_states<E>(seg.n + place_of * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
     else if (to.final && r.hi == seq.hi)
         store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
 }
 
 // The states that enter a sequence's segments after the first, S <- M S + N,
 // in the places of N.  BACK: the gradients that enter from the segment after,
-// from the last to the first.  A wave has 16 columns; `start` holds what enters
-// the sequence, or is NULL.
+// from the last to the first; `start` holds what enters the sequence, or is
+// NULL.  A workgroup has 32 columns, a wave 32 keys of them (W 256: 64), so that
+// a step is short: every wave leaves its keys as operands in shared memory, and
+// multiplies its rows of M, which arrived while the step before was worked on.
+// 15 steps of 16 heads, 128 x 128: LINK_US us; a wave with all keys of 16 columns
+// 85 us, with M as rows of numbers 138 us.
 template <class T, int W, bool E, bool BACK>
 __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
-    constexpr uint32_t kTiles = W / 16;
+    constexpr uint32_t kKeys = W / 32, NC = W == 256 ? 2 : 1, CT = 2;
     constexpr bool kScaled = Form<T>::scaled;
-    const uint32_t blocks = (a.value_dim + 63u) / 64u, item = first + blockIdx.x / blocks, head = item % a.heads;
+    __shared__ Mid operands[2][kKeys][CT][64];
+    __shared__ float backs[2][kKeys];
+    const uint32_t blocks = (a.value_dim + 31u) / 32u, item = first + blockIdx.x / blocks, head = item % a.heads;
     const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
-    const uint32_t col0 = blockIdx.x % blocks * 64u + wave * 16u, s = item / a.heads;
+    const uint32_t col0 = blockIdx.x % blocks * 32u, s = item / a.heads;
     const Rows r = sequence_rows(a.offsets, a.tokens, s, seg.shift);
-    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim, key_cells = (uint64_t)a.key_dim * a.key_dim;
+    const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     const uint32_t segments = (uint32_t)(((uint64_t)(r.hi - r.lo) + (1ull << seg.shift) - 1u) >> seg.shift);
-    if (col0 >= a.value_dim || segments < 2u) return;
-    f32x4 S[1][kTiles], next[1][kTiles];
-    load_states<E>(S, start ? start + ((uint64_t)s * a.heads + head) * cells : nullptr, a.key_dim, a.value_dim, col0, lane);
+    if (segments < 2u) return;
+    const bool works = wave * NC < kKeys;
     auto number = [&](uint32_t i) { return (uint64_t)(r.base + (BACK ? segments - 1u - i : i)) * a.heads + head; };
-    load_states<E>(next, seg.n + number(0u) * cells, a.key_dim, a.value_dim, col0, lane);
+    auto each = [&](auto f) {  // f(keys, columns, half, row of the four, offset or none)
+#pragma unroll
+        for (uint32_t k = 0; k < NC; ++k)
+#pragma unroll
+            for (uint32_t ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (uint32_t h = 0; h < 2u; ++h)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4u; ++i) {
+                        const uint32_t row = place(2u * (wave * NC + k) + h, 4u * q + i), col = col0 + 16u * ct + m;
+                        const bool is = works && row < a.key_dim && col < a.value_dim;
+                        f(k, ct, h, i, is, row * a.value_dim + col);
+                    }
+    };
+    f32x4 S[NC][CT][2], N[NC][CT][2];
+    auto load = [&](f32x4 (&to)[NC][CT][2], const float *from) {
+        each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool is, uint32_t at) {
+            to[k][ct][h][i] = from && is ? from[at] : 0.0f;
+        });
+    };
+    Mid mat[NC][2][kKeys];
+    float back[NC][2][kKeys];
+    auto fetch = [&](uint32_t i, uint32_t k, uint32_t h, uint32_t c) {
+        const SegmentMatrix<T, W> &from = static_cast<const SegmentMatrix<T, W> *>(seg.m)[number(i)];
+        const uint32_t t = 2u * (wave * NC + k) + h;
+        mat[k][h][c] = from.m[t][c][lane];
+        back[k][h][c] = kScaled ? from.back[t][c] : 1.0f;
+    };
+    load(S, start ? start + ((uint64_t)s * a.heads + head) * cells : nullptr);
+    load(N, seg.n + number(0u) * cells);
+    if (works)
+#pragma unroll
+        for (uint32_t k = 0; k < NC; ++k)
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) fetch(0u, k, 0u, c), fetch(0u, k, 1u, c);
     for (uint32_t i = 0; i + 1u < segments; ++i) {
-        const float *mat = seg.m + number(i) * key_cells;
-        const Scale of_s = scale_of<kScaled>(kScaled ? wave_largest(largest(S)) : 0.0f);
-        Mid h[kTiles / 2];
+        const uint32_t b = i & 1u;
+        if (works) {
 #pragma unroll
-        for (uint32_t c = 0; c < kTiles / 2u; ++c) h[c] = operand_of<Mid>(S[0][2u * c], S[0][2u * c + 1u], of_s.by);
+            for (uint32_t k = 0; k < NC; ++k) {
+                const Scale of = scale_of<kScaled>(kScaled ? wave_largest(largest(S[k])) : 0.0f);
 #pragma unroll
-        for (uint32_t t = 0; t < kTiles; ++t) {
-            const uint32_t row = place(t, m);
-            S[0][t] = next[0][t];
-#pragma unroll
-            for (uint32_t c = 0; c < kTiles / 2u; ++c) {
-                float v[8] = {};
-                if (row < a.key_dim) load8<float>(v, mat + row * a.key_dim, 32u * c + 8u * q, a.key_dim);
-                Mid o;
-                float most = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) most = __builtin_fmaxf(most, __builtin_fabsf(v[j]));
-                const Scale of_m = scale_of<kScaled>(kScaled ? wave_largest(most) : 0.0f);
-                operand_of(o, v, of_m.by);
-                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma(sum, o, h[c]);
-                S[0][t] += sum * (of_m.back * of_s.back);
+                for (uint32_t ct = 0; ct < CT; ++ct)
+                    operands[b][wave * NC + k][ct][lane] = operand_of<Mid>(S[k][ct][0], S[k][ct][1], of.by);
+                if (lane == 0u) backs[b][wave * NC + k] = of.back;
             }
         }
-        float *n = seg.n + number(i + 1u) * cells;
-        if (i + 2u < segments) load_states<E>(next, n, a.key_dim, a.value_dim, col0, lane);
-        store_states<E>(n, S, 1.0f, a.key_dim, a.value_dim, col0, lane);
+        __syncthreads();  // two sets of operands: those of the step before may still be read
+        if (works) {
+#pragma unroll
+            for (uint32_t k = 0; k < NC; ++k)
+#pragma unroll
+                for (uint32_t ct = 0; ct < CT; ++ct) S[k][ct][0] = N[k][ct][0], S[k][ct][1] = N[k][ct][1];
+#pragma unroll
+            for (uint32_t c = 0; c < kKeys; ++c) {
+                const float from = backs[b][c];
+#pragma unroll
+                for (uint32_t ct = 0; ct < CT; ++ct) {
+                    const Mid h = operands[b][c][ct][lane];
+#pragma unroll
+                    for (uint32_t k = 0; k < NC; ++k)
+#pragma unroll
+                        for (uint32_t t = 0; t < 2u; ++t) {
+                            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma(sum, mat[k][t][c], h);
+                            S[k][ct][t] += sum * (back[k][t][c] * from);
+                        }
+                }
+                if (i + 2u < segments)
+#pragma unroll
+                    for (uint32_t k = 0; k < NC; ++k) fetch(i + 1u, k, 0u, c), fetch(i + 1u, k, 1u, c);
+            }
+            float *n = seg.n + number(i + 1u) * cells;
+            if (i + 2u < segments) load(N, n);
+            each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t j, bool is, uint32_t at) {
+                if (is) n[at] = S[k][ct][h][j];
+            });
+        }
     }
+}
+
+// Bytes of a segment's M.
+template <class T>
+inline size_t matrix_bytes(uint32_t key_dim) {
+    size_t n = 0;
+    with_key_width(key_dim, [&](auto w) {
+        n = sizeof(SegmentMatrix<T, decltype(w)::value>);
+        return PS_OK;
+    });
+    return n;
 }
 
 // Rows of a segment, as a shift: as many as make a call's steps fewest, by what
@@ -459,7 +568,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
     seg.shift = segment_shift(a, wide ? 128u : 64u);
     const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u;
-    const size_t m_at = plan.take(linked * a.key_dim * a.key_dim * 4u), n_at = plan.take(linked * cells * 4u);
+    const size_t m_at = plan.take(linked * matrix_bytes<T>(a.key_dim)), n_at = plan.take(linked * cells * 4u);
     bool query = false;
     ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
     if (st != PS_OK || query) return st;
@@ -484,7 +593,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
             hipLaunchKernelGGL((delta_prepare_kernel<T, W, false>), dim3(grid), dim3(256), 0, s, a, first, prepared,
                                ws_counter(ws), plan.words());
         });
-        seg.m = ws_at<float>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
+        seg.m = ws_at<void *>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
         const WalkResults to = {out, final, checkpoints, rhos, sizes};
         auto walk = [&](auto ct, auto eights) {
             constexpr int CT = decltype(ct)::value;
@@ -495,7 +604,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                     hipLaunchKernelGGL((delta_walk_kernel<T, W, CT, E, true>), dim3(grid), dim3(512), 0, s, a,
                                        first, prepared, seg, to);
                 });
-                const uint64_t columns = ceil_div(a.value_dim, 64u);
+                const uint64_t columns = ceil_div(a.value_dim, 32u);
                 launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
                     hipLaunchKernelGGL((delta_link_kernel<T, W, E, false>), dim3(grid), dim3(256), 0, s, a, first, seg,
                                        a.initial);
