@@ -35,15 +35,15 @@ constexpr uint32_t kBackSizes = 3u * kSizeWaves;
 
 // The walk backwards.  lead: the walks for M and N of segments that are not a
 // sequence's first, which keep nothing but their end.
-template <class T, int W, int CT, bool E>
-__global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+template <class T, int W, int NW, bool E>
+__global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
                                                               Segments seg, const T *__restrict__ dout, bool lead, BackResults to) {
     typedef typename Form<T>::Mid Mid;
     typedef typename Form<T>::In In;
-    typedef WalkTile<T, W, CT> Tile;
+    typedef WalkTile<T, W, NW> Tile;
     constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
-    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
-    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, CT>()];
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, NW>()];
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = lead ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
@@ -57,26 +57,26 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);
     const T *grads = dout + (uint64_t)head * a.value_dim;
     const int64_t grads_stride = (int64_t)a.heads * a.value_dim;
-    const DeltaFeed<T, W, CT, E> feed = {a, prepared, r, base, head, khead, block0, grads, grads_stride};
+    const DeltaFeed<T, W, NW, E> feed = {a, prepared, r, base, head, khead, block0, grads, grads_stride};
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
-    if (wave >= 4u) {
+    if (wave >= (uint32_t)NW) {
         feed.template run<false>(chunks, !unit, tile, [&](uint32_t i) { return chunks - 1u - i; });
         if (unit)
-            store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+            store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
                                    reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
-    const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
+    const uint32_t here = wave * 16u, col0 = block0 + here, col = col0 + m;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     constexpr bool kScaled = Form<T>::scaled;
-    f32x4 D[CT][kTiles];  // times `unit_of`, the gradients of the states
+    f32x4 D[kTiles];  // times `unit_of`, the gradients of the states
     float unit_of = 1.0f;
     {
         const float *from = nullptr;
         if (!lead && r.hi != seq.hi) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
         else if (!lead && to.dfinal) from = to.dfinal + ((uint64_t)r.seq * a.heads + head) * cells;
-        load_states<E>(D, from, a.key_dim, a.value_dim, col0, lane);
-        if (unit) unit_states(D, col0, lane);
+        load_states<E>(D, from, a.key_dim, a.value_dim, col, q);
+        if (unit) unit_states(D, col, q);
     }
     __syncthreads();
     for (uint32_t i = 0; i < chunks; ++i) {
@@ -85,145 +85,93 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
         if (col0 < width) {
             if (!lead)
                 store_states<E>(to.dstates + ((uint64_t)(base + c) * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim,
-                                col0, lane);
+                                col, q);
             const float most = kScaled ? wave_largest(largest(D)) : 0.0f;
             const Scale of_d = scale_of<kScaled>(most);
-            auto numbers = [&](uint32_t which, uint32_t t) {
-                return *reinterpret_cast<const f32x4 *>(&in.p.row[which + 16u * t + 4u * q]);
-            };
-            f32x4 x[CT][4], y[CT][4];
+            f32x4 x[4], y[4], o[4];  // o: dO
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) x[ct][t] = y[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < 4; ++t) x[t] = y[t] = o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             // dU = exp(G_C - G) K D + P^T dO
+            In ka[4];
+            auto keys = [&](uint32_t s) {
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) ka[t] = in.k.along(16u * t + m, 32u * s + 8u * q);
+            };
+            keys(0u);
 #pragma unroll
             for (uint32_t s = 0; s < kTiles / 2u; ++s) {
-                Mid h[CT];
+                mma_rows(x, ka, operand_of<Mid>(D[2u * s], D[2u * s + 1u], of_d.by));
+                if (s + 1u < kTiles / 2u) keys(s + 1u);
+            }
+            RowNumbers tail;
+            tail.load(in.p.row + kRowTail, q);
+            Triangle<Mid> tri;
+            if (!unit) {
+                if constexpr (kV) {
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(D[ct][2u * s], D[ct][2u * s + 1u], of_d.by);
+                    for (uint32_t t = 0; t < 4u; ++t) o[t] = value_rows<T>(in.v, t, q, m, here);
+                } else {
 #pragma unroll
-                for (uint32_t t = 0; t < 4u; ++t) {
-                    const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
+                    for (uint32_t t = 0; t < 4u; ++t)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], ka, h[ct]);
+                        for (uint32_t j = 0; j < 4u; ++j) {
+                            const uint32_t row = 16u * t + 4u * q + j;
+                            o[t][j] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
+                        }
                 }
+                tri.load(in.p.scores, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
-            f32x4 o[CT][4];  // dO, tile by tile
-            if (!unit) {
-#pragma unroll
-                for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
-#pragma unroll
-                    for (uint32_t t = 0; t < 4u; ++t) {
-                        if constexpr (kV) {
-                            o[ct][t] = value_rows<T, CT>(in.v, t, q, m, here, ct);
-                        } else {
-                            const uint32_t col = col0 + column<CT>(ct, m);
-#pragma unroll
-                            for (uint32_t i = 0; i < 4u; ++i) {
-                                const uint32_t row = 16u * t + 4u * q + i;
-                                o[ct][t][i] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
-                            }
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) o[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
             const float most_o = kScaled ? wave_largest(largest(o)) : 0.0f;
             const Scale of_o = scale_of<kScaled>(most_o);
             const float to_x = kScaled ? of_o.by * in.p.row[kRowScores] : 1.0f;
             const float from_x = kScaled ? of_o.back * in.p.row[kRowScoresBack] : 1.0f;
+            const float from_d = of_d.back * unit_of * to_x;
 #pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 tail = numbers(kRowTail, t) * (of_d.back * unit_of) * to_x;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) x[ct][t] *= tail;
-            }
+            for (uint32_t t = 0; t < 4u; ++t) x[t] *= tail.of[t] * from_d;
             if (!unit) {
-#pragma unroll
-                for (uint32_t s = 0; s < 2u; ++s) {
-                    In h[CT];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<In>(o[ct][2u * s], o[ct][2u * s + 1u], of_o.by);
-#pragma unroll
-                    for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
-                        const Mid scores = in.p.scores[upper_at(t, s)][lane];
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], scores, h[ct]);
-                    }
-                }
+                const In h[2] = {operand_of<In>(o[0], o[1], of_o.by), operand_of<In>(o[2], o[3], of_o.by)};
+                mma_upper(x, tri, h);
             }
+            tri.load(in.p.inverse, lane);
+            const float inverse_back = in.p.row[kRowInverse], kept = unit_of * in.p.row[kRowWhole];
             __builtin_amdgcn_sched_barrier(0);
             // omega
             const Scale of_x = scale_of<kScaled>(kScaled ? wave_largest(largest(x)) : 0.0f);
-            const float from_y = kScaled ? of_x.back * from_x * in.p.row[kRowInverse] : 1.0f;
-#pragma unroll
-            for (uint32_t s = 0; s < 2u; ++s) {
-                Mid h[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u], of_x.by);
-#pragma unroll
-                for (uint32_t t = 0; t < 2u * s + 2u; ++t) {
-                    const Mid inverse = in.p.inverse[upper_at(t, s)][lane];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
+            const float from_y = kScaled ? of_x.back * from_x * inverse_back : 1.0f;
+            {
+                const Mid h[2] = {operand_of<Mid>(x[0], x[1], of_x.by), operand_of<Mid>(x[2], x[3], of_x.by)};
+                mma_upper(y, tri, h);
+            }
+            if (!lead) {
+                if (kScaled) {
+                    const float of_y = wave_largest(largest(y)) * from_y;
+                    float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kBackSizes + col0 / 16u;
+                    if (lane == 0u) sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y, sizes[2u * kSizeWaves] = most_o;
                 }
+                if (col < a.value_dim)
+                    store_rows(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, from_y, rows, col, q);
             }
-            if (!lead && kScaled) {
-                const float of_y = wave_largest(largest(y)) * from_y;
-                float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kBackSizes + col0 / (16u * CT);
-                if (lane == 0u)
-                    sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y, sizes[2u * kSizeWaves] = most_o;
-            }
-            if (!lead)
-                store_rows<E>(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, from_y, rows,
-                              col0, a.value_dim, lane);
             // D = e_C D + Q^T diag(scale e) dO - K^T diag(e) beta omega
             __builtin_amdgcn_sched_barrier(0);
+            RowNumbers e, eq;
+            e.load(in.p.row + kRowE, q);
+            eq.load(in.p.row + kRowQ, q);
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 e = numbers(kRowE, t) * numbers(kRowBeta, t) * -from_y, eq = numbers(kRowQ, t);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= e, o[ct][t] *= eq;
+                y[t] *= e.of[t] * -from_y;
+                o[t] *= eq.of[t];
             }
-            const float kept = unit_of * in.p.row[kRowWhole];
             const Scale of_y = scale_of_sum<kScaled>(
                 kScaled ? wave_largest(__builtin_fmaxf(largest(y), largest(o))) : 0.0f, most * kept);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) D[ct][t] *= kept * of_y.by;
+            for (uint32_t t = 0; t < kTiles; ++t) D[t] *= kept * of_y.by;
             unit_of = of_y.back;
-#pragma unroll
-            for (uint32_t s = 0; s < 2u; ++s) {
-                Mid h[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_y.by);
-#pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) {
-                    const auto ka = in.k.across(s, t, lane);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(D[ct][t], ka, h[ct]);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            mma_keys(D, in.k, 0u, operand_of<Mid>(y[0], y[1], of_y.by), lane);
+            mma_keys(D, in.k, 1u, operand_of<Mid>(y[2], y[3], of_y.by), lane);
             if (!unit) {
-#pragma unroll
-                for (uint32_t s = 0; s < 2u; ++s) {
-                    Mid h[CT];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(o[ct][2u * s], o[ct][2u * s + 1u], of_y.by);
-#pragma unroll
-                    for (uint32_t t = 0; t < kTiles; ++t) {
-                        const auto qa = in.q.across(s, t, lane);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mma(D[ct][t], qa, h[ct]);
-                    }
-                }
+                mma_keys(D, in.q, 0u, operand_of<Mid>(o[0], o[1], of_y.by), lane);
+                mma_keys(D, in.q, 1u, operand_of<Mid>(o[2], o[3], of_y.by), lane);
             }
         }
         if (!kTwo) __syncthreads();
@@ -231,14 +179,14 @@ __global__ __launch_bounds__(512) void delta_walk_back_kernel(DeltaArgs a, uint3
     }
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (unit) {
-        store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), D, unit_of,
+        store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &D, unit_of,
                                block0, wave, lane, true);
         return;
     }
     if (col0 >= width) return;
-    if (lead) store_states<E>(seg.n + place_of * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
+    if (lead) store_states<E>(seg.n + place_of * cells, D, unit_of, a.key_dim, a.value_dim, col, q);
     else if (to.dinitial && r.lo == seq.lo)
-        store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(to.dinitial + ((uint64_t)r.seq * a.heads + head) * cells, D, unit_of, a.key_dim, a.value_dim, col, q);
 }
 
 // ---------------------------------------------------------------------------
@@ -771,13 +719,13 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
             hipLaunchKernelGGL((delta_prepare_kernel<T, W, true>), dim3(grid), dim3(256), 0, s, a, first, prepared,
                                ws_counter(ws), plan.words());
         });
-        auto walk = [&](auto ct, auto eights) {
-            constexpr int CT = decltype(ct)::value;
+        auto walk = [&](auto waves, auto eights) {
+            constexpr int NW = decltype(waves)::value;
             constexpr bool E = decltype(eights)::value;
-            const uint64_t blocks = ceil_div(a.value_dim, 64u * CT), all = blocks + ceil_div(a.key_dim, 64u * CT);
+            const uint64_t blocks = ceil_div(a.value_dim, 16u * NW), all = blocks + ceil_div(a.key_dim, 16u * NW);
             if (linked) {
-                launch_in_parts(segments * a.heads, all, 512u, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared,
+                launch_in_parts(segments * a.heads, all, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_back_kernel<T, W, NW, E>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a, first, prepared,
                                        seg, g, true, to);
                 });
                 const uint64_t columns = ceil_div(a.value_dim, 32u);
@@ -785,19 +733,19 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                     hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(256), 0, s, a, first, seg, dfinal);
                 });
             }
-            launch_in_parts(segments * a.heads, blocks, 512u, [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_walk_back_kernel<T, W, CT, E>), dim3(grid), dim3(512), 0, s, a, first, prepared, seg,
+            launch_in_parts(segments * a.heads, blocks, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_back_kernel<T, W, NW, E>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a, first, prepared, seg,
                                    g, false, to);
             });
             launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 512u, [&](uint32_t first, uint32_t grid) {
                 hipLaunchKernelGGL((delta_grads_kernel<T, W, E>), dim3(grid), dim3(512), 0, s, a, first, g, checkpoints, rhos, sizes,
-                                   dstates, omega, back_sizes, (uint32_t)ceil_div(a.value_dim, 16u * CT), out);
+                                   dstates, omega, back_sizes, (uint32_t)ceil_div(a.value_dim, 16u), out);
             });
         };
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
         auto shape = [&](auto e) {
-            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 2 : 1>(), e);
-            else walk(std::integral_constant<int, 1>(), e);
+            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 8 : 4>(), e);
+            else walk(std::integral_constant<int, 4>(), e);
         };
         if (eights) shape(std::true_type());
         else shape(std::false_type());

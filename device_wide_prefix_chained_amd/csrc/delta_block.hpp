@@ -117,6 +117,46 @@ __device__ __forceinline__ void mma(f32x4 &acc, const Planes<NA> &a, const Plane
             if (sum - i >= 0 && sum - i < NB)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.p[i], b.p[sum - i], acc, 0, 0, 0);
 }
+// The same for N sums with one left operand or one right operand each: product
+// by product over all sums, so that no instruction waits for the one before.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const Planes<NA> (&a)[N], const Planes<NB> &b) {
+    constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+    for (int sum = most - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (sum - i >= 0 && sum - i < NB)
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t].p[i], b.p[sum - i], acc[t], 0, 0, 0);
+}
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_columns(f32x4 (&acc)[N], const Planes<NA> &a, const Planes<NB> (&b)[N]) {
+    constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+    for (int sum = most - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (sum - i >= 0 && sum - i < NB)
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.p[i], b[t].p[sum - i], acc[t], 0, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const Wide (&a)[N], const Wide &b) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int t = 0; t < N; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[t].p[j], b.p[j], acc[t], 0, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void mma_columns(f32x4 (&acc)[N], const Wide &a, const Wide (&b)[N]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int t = 0; t < N; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a.p[j], b[t].p[j], acc[t], 0, 0, 0);
+}
 __device__ __forceinline__ void mma(f32x4 &acc, const Wide &a, const Wide &b) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.p[j], b.p[j], acc, 0, 0, 0);
@@ -151,9 +191,9 @@ struct Scale {
 template <bool scaled, int least = -60>
 __device__ __forceinline__ Scale scale_of(float most) {
     if (!scaled) return {1.0f, 1.0f};
-    int e = __builtin_amdgcn_frexp_expf(most);
-    e = e < least ? least : e;
-    return {__builtin_amdgcn_ldexpf(1.0f, 15 - e), __builtin_amdgcn_ldexpf(1.0f, e - 15)};
+    // exponents as they stand in the words: 2^14 over the largest's
+    const uint32_t e = __builtin_bit_cast(uint32_t, __builtin_fmaxf(most, __builtin_ldexpf(1.0f, least))) & 0x7F800000u;
+    return {__builtin_bit_cast(float, (268u << 23) - e), __builtin_bit_cast(float, e - (14u << 23))};
 }
 // The same for terms that are added to numbers up to `held`, which take the
 // scale with them and must not leave fp32's range for small terms.
@@ -162,15 +202,13 @@ __device__ __forceinline__ Scale scale_of_sum(float most, float held) {
     return scale_of<scaled>(__builtin_fmaxf(most, held * 0x1p-24f));
 }
 // The largest of a lane's tiles.
-template <int CT, int N>
-__device__ __forceinline__ float largest(const f32x4 (&v)[CT][N]) {
+template <int N>
+__device__ __forceinline__ float largest(const f32x4 (&v)[N]) {
     float m[4] = {};
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+    for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int t = 0; t < N; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = __builtin_fmaxf(m[i], __builtin_fabsf(v[ct][t][i]));
+        for (int i = 0; i < 4; ++i) m[i] = __builtin_fmaxf(m[i], __builtin_fabsf(v[t][i]));
     return __builtin_fmaxf(__builtin_fmaxf(m[0], m[1]), __builtin_fmaxf(m[2], m[3]));
 }
 __device__ __forceinline__ float wave_largest(float v) {
@@ -374,76 +412,57 @@ __device__ __forceinline__ float fill_rows(KeyTile<T, W> &tile, const void *from
     return by * s.back;
 }
 
-// The column in lane m of tile ct of a wave's 16 CT columns.
-template <int CT>
-__device__ __forceinline__ uint32_t column(uint32_t ct, uint32_t m) {
-    return CT == 1 ? m : place(ct, m);
-}
-
-// A wave's columns of a matrix [rows, width], a head's state as a rule: tile t's register i
-// is row place(t, 4 q + i) of column col0 + column(ct, lane & 15).  E: both
-// dimensions are multiples of 8, so a lane's four rows are all there or none.
-template <bool E, int CT, int TILES>
-__device__ __forceinline__ void load_states(f32x4 (&S)[CT][TILES], const float *from, uint32_t rows, uint32_t width,
-                                            uint32_t col0, uint32_t lane) {
+// A wave's 16 columns of a matrix [rows, width], a head's state as a rule: tile
+// t's register i is row place(t, 4 q + i) of column col.  E: both dimensions are
+// multiples of 8, so a lane's four rows are all there or none.
+template <bool E, int TILES>
+__device__ __forceinline__ void load_states(f32x4 (&S)[TILES], const float *from, uint32_t rows, uint32_t width, uint32_t col,
+                                            uint32_t q) {
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
+    for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
+        const uint32_t row = place(t, 4u * q);
+        S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!from || row >= rows || col >= width) continue;
 #pragma unroll
-        for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
-            const uint32_t row = place(t, 4u * (lane >> 4));
-            S[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (!from || row >= rows || col >= width) continue;
-#pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i)
-                if (E || row + i < rows) S[ct][t][i] = from[(row + i) * width + col];
-        }
+        for (uint32_t i = 0; i < 4u; ++i)
+            if (E || row + i < rows) S[t][i] = from[(row + i) * width + col];
     }
 }
 // The width is hidden from the compiler where it stores: it would keep the
 // addresses of every row over a whole walk, in registers that the walk needs.
-template <bool E, int CT, int TILES>
-__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[CT][TILES], float by, uint32_t rows, uint32_t width,
-                                             uint32_t col0, uint32_t lane) {
+template <bool E, int TILES>
+__device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[TILES], float by, uint32_t rows, uint32_t width,
+                                             uint32_t col, uint32_t q) {
     asm volatile("" : "+s"(width));
+    if (col >= width) return;
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
+    for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
+        const uint32_t row = place(t, 4u * q);
+        if (row >= rows) continue;
+        float *p = to + (row * width + col);
 #pragma unroll
-        for (uint32_t t = 0; t < (uint32_t)TILES; ++t) {
-            const uint32_t row = place(t, 4u * (lane >> 4));
-            if (row >= rows || col >= width) continue;
-            float *p = to + (row * width + col);
-#pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i)
-                if (E || row + i < rows) p[i * width] = S[ct][t][i] * by;
-        }
+        for (uint32_t i = 0; i < 4u; ++i)
+            if (E || row + i < rows) p[i * width] = S[t][i] * by;
     }
 }
 // A result's tiles over a chunk's rows into rows of `stride`, rows below `rows`.
-template <bool E, int CT>
-__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[CT][4], float by, uint32_t rows,
-                                           uint32_t col0, uint32_t width, uint32_t lane) {
+__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[4], float by, uint32_t rows,
+                                           uint32_t col, uint32_t q) {
     asm volatile("" : "+s"(stride));
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-        const uint32_t col = col0 + column<CT>(ct, lane & 15u);
-        if (col >= width) continue;
+    for (uint32_t t = 0; t < 4u; ++t) {
+        const uint32_t row = 16u * t + 4u * q;
+        float *p = to + (row * stride + col);
 #pragma unroll
-        for (uint32_t t = 0; t < 4u; ++t) {
-            const uint32_t row = 16u * t + 4u * (lane >> 4);
-            float *p = to + (row * stride + col);
-#pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i)
-                if (row + i < rows) p[i * stride] = y[ct][t][i] * by;
-        }
+        for (uint32_t i = 0; i < 4u; ++i)
+            if (row + i < rows) p[i * stride] = y[t][i] * by;
     }
 }
 
 // ---------------------------------------------------------------------------
 // what a chunk's preparation leaves in the workspace for each head
 // ---------------------------------------------------------------------------
-// Numbers for each row: e nu, scale e mu, beta, exp(G_C - G) nu (nu and mu with
+// Numbers for each row: e nu (backwards times beta), scale e mu, beta, exp(G_C - G) nu (nu and mu with
 // what takes the keys' and queries' powers of two back); then exp(G_C) and the
 // scales of the triangles: the inverse's back, the scores' and its back.
 constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowInverse = 257u,
@@ -615,7 +634,7 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
                 double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(bits >> 32), 63) << 32 |
                             (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, 63));
             const float e = exp_hw((float)sum);
-            out.row[kRowE + lane] = e * nu[lane];
+            out.row[kRowE + lane] = e * nu[lane] * (BACK ? beta : 1.0f);
             out.row[kRowQ + lane] = a.scale * e * mu[lane];
             out.row[kRowBeta + lane] = beta;
             out.row[kRowTail + lane] = exp_hw((float)(all - sum)) * nu[lane];
@@ -624,7 +643,7 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
         const uint32_t col = 16u * wave + n;
         const double here = gate.sum[col];
         const float beta_here = gate.beta[col], nu_here = nu[col], mu_here = mu[col];
-        f32x4 p[1][4], x[1][4];
+        f32x4 p[4], x[4];
         __syncthreads();  // the products, or the triangle of the head before, are read
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
@@ -638,12 +657,12 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
                 // forwards a_lj beta_j for l > j, the transpose's row j; backwards beta_i a_il
                 tri[i] = (BACK ? row < col : row > col) ? both * nu_here * beta_here * kk[t][i] : 0.0f;
                 const float along = BACK ? forth * mu[row] * nu_here : both * mu_here;
-                p[0][t][i] = (BACK ? row >= col : row <= col) ? a.scale * along * qk[t][i] : 0.0f;
+                p[t][i] = (BACK ? row >= col : row <= col) ? a.scale * along * qk[t][i] : 0.0f;
             }
             *reinterpret_cast<f32x4 *>(&sh.tri[col * kTriStride + 16u * t + 4u * q]) = tri;
         }
         __syncthreads();
-        unit_inverse<BACK>(sh.tri, diagonal, wave, lane, x[0]);
+        unit_inverse<BACK>(sh.tri, diagonal, wave, lane, x);
         Scale inverse = {1.0f, 1.0f}, scores = {1.0f, 1.0f};
         if constexpr (Form<T>::scaled) {
             const float mx = wave_largest(largest(x)), mp = wave_largest(largest(p));
@@ -662,8 +681,8 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
         for (uint32_t s = 0; s < 2u; ++s) {
             if (BACK ? s < (wave >> 1) : s > (wave >> 1)) continue;
             const uint32_t at = BACK ? upper_at(wave, s) : lower_at(wave, s);
-            out.inverse[at][lane] = operand_of<Mid>(x[0][2u * s], x[0][2u * s + 1u], inverse.by);
-            out.scores[at][lane] = operand_of<Mid>(p[0][2u * s], p[0][2u * s + 1u], scores.by);
+            out.inverse[at][lane] = operand_of<Mid>(x[2u * s], x[2u * s + 1u], inverse.by);
+            out.scores[at][lane] = operand_of<Mid>(p[2u * s], p[2u * s + 1u], scores.by);
         }
     }
 }

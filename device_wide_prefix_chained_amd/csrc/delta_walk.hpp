@@ -14,33 +14,32 @@ namespace {
 
 // What a step of a walk reads: a chunk's keys, queries and values, and what was
 // prepared of it.
-template <class T, int W, int CT>
+template <class T, int W, int NW>
 struct WalkTile {
-    static constexpr uint32_t kCols = 64u * CT;
+    static constexpr uint32_t kCols = 16u * NW;
     KeyTile<T, W> k, q;
     Prepared<T> p;
     T v[kChunk][kCols + 8u];
 };
-template <class T, int W, int CT>
-constexpr bool kValuesFit = sizeof(WalkTile<T, W, CT>) <= kMostShared;
-template <class T, int W, int CT>
+template <class T, int W, int NW>
+constexpr bool kValuesFit = sizeof(WalkTile<T, W, NW>) <= kMostShared;
+template <class T, int W, int NW>
 constexpr size_t walk_tile_bytes() {
-    return kValuesFit<T, W, CT> ? sizeof(WalkTile<T, W, CT>) : sizeof(WalkTile<T, W, CT>) - sizeof(WalkTile<T, W, CT>::v);
+    return kValuesFit<T, W, NW> ? sizeof(WalkTile<T, W, NW>) : sizeof(WalkTile<T, W, NW>) - sizeof(WalkTile<T, W, NW>::v);
 }
 
-// Rows 16 t + 4 q + i of column `here` + column(ct, m) of a tile of values.
-template <class T, int CT, uint32_t STRIDE>
-__device__ __forceinline__ f32x4 value_rows(const T (&tile)[kChunk][STRIDE], uint32_t t, uint32_t q, uint32_t m, uint32_t here,
-                                            uint32_t ct) {
+// Rows 16 t + 4 q + i of column `here` + m of a tile of values.
+template <class T, uint32_t STRIDE>
+__device__ __forceinline__ f32x4 value_rows(const T (&tile)[kChunk][STRIDE], uint32_t t, uint32_t q, uint32_t m, uint32_t here) {
     f32x4 v;
     if constexpr (sizeof(T) == 2) {
-        const uint32_t at = here + (CT == 1 ? 4u * (m & 3u) : 8u * (m & 3u) + 4u * ct);
-        const i16x4 raw = read_transposed(reinterpret_cast<const uint16_t *>(&tile[16u * t + 4u * q + (m >> 2)][at]));
+        const i16x4 raw = read_transposed(
+            reinterpret_cast<const uint16_t *>(&tile[16u * t + 4u * q + (m >> 2)][here + 4u * (m & 3u)]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
     } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)tile[16u * t + 4u * q + i][here + column<CT>(ct, m)];
+        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)tile[16u * t + 4u * q + i][here + m];
     }
     return v;
 }
@@ -63,23 +62,20 @@ struct SegmentMatrix {
 };
 // Columns of M that four waves hold, into operands, by way of shared memory;
 // all eight waves, `walks`: those that hold them.
-template <class T, int W, int CT>
+template <class T, int W, int NW>
 __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *shared, const f32x4 (*S)[W / 16], float by,
                                              uint32_t block0, uint32_t wave, uint32_t lane, bool walks) {
-    constexpr uint32_t kCols = 64u * CT, kRow = kCols + 4u;
+    constexpr uint32_t kCols = 16u * NW, kRow = kCols + 4u;
     static_assert(W * kRow * 4u <= kMostShared, "a block of M fits shared memory");
     const uint32_t m = lane & 15u, q = lane >> 4;
     if (walks) {
 #pragma unroll
-        for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+        for (uint32_t t = 0; t < W / 16u; ++t)
 #pragma unroll
-            for (uint32_t t = 0; t < W / 16u; ++t)
-#pragma unroll
-                for (uint32_t i = 0; i < 4u; ++i)
-                    shared[place(t, 4u * q + i) * kRow + wave * 16u * CT + column<CT>(ct, m)] = S[ct][t][i] * by;
+            for (uint32_t i = 0; i < 4u; ++i) shared[place(t, 4u * q + i) * kRow + wave * 16u + m] = (*S)[t][i] * by;
     }
     __syncthreads();
-    for (uint32_t i = wave; i < W / 16u * (kCols / 32u); i += 8u) {
+    for (uint32_t i = wave; i < W / 16u * (kCols / 32u); i += NW + 4u) {
         const uint32_t t = i / (kCols / 32u), c = i % (kCols / 32u);
         if (block0 + 32u * c >= (uint32_t)W) continue;
         const float *p = shared + place(t, m) * kRow + 32u * c + 8u * q;
@@ -98,11 +94,11 @@ struct WalkResults {
 };
 
 // The feeding waves of a walk: keys, queries, values and what was prepared of
-// each chunk, from memory into registers while the chunk before is worked on,
-// then into the tile.
-template <class T, int W, int CT, bool E>
+// each chunk, from memory into registers, a whole chunk's work before they are
+// waited for, then into the tile.
+template <class T, int W, int NW, bool E>
 struct DeltaFeed {
-    typedef WalkTile<T, W, CT> Tile;
+    typedef WalkTile<T, W, NW> Tile;
     const DeltaArgs &a;
     const Prepared<T> *prepared;
     Chunk r;
@@ -113,10 +109,10 @@ struct DeltaFeed {
     // LEAD: no queries and no scores.  order(i): the i-th chunk to come.
     template <bool LEAD, class F, class O>
     __device__ __forceinline__ void run(uint32_t chunks, bool with_values, F tile, O order) const {
-        constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
+        constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
         constexpr uint32_t kKeys = W / 32, kVals = Tile::kCols / 32u;
         constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
-        const uint32_t thread = threadIdx.x - 256u, row = thread >> 2, part = (thread & 3u) * 8u;
+        const uint32_t thread = threadIdx.x - 64u * NW, row = thread >> 2, part = (thread & 3u) * 8u;
         Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
         u32x4 ps[kWords];
         auto fetch = [&](uint32_t i) {
@@ -164,42 +160,87 @@ struct DeltaFeed {
             }
         };
         if (chunks) fetch(order(0u)), leave(tile(0u));
+        if (chunks > 1u) fetch(order(1u));
         __syncthreads();
         for (uint32_t i = 0; i < chunks; ++i) {
-            const bool more = i + 1u < chunks;
-            if (more) fetch(order(i + 1u));
             if (!kTwo) __syncthreads();
-            if (more) leave(tile(i + 1u));
+            if (i + 1u < chunks) leave(tile(i + 1u));
+            if (i + 2u < chunks) fetch(order(i + 2u));
             __syncthreads();
         }
     }
 };
 
-// The unit matrix's columns.
-template <int CT, int TILES>
-__device__ __forceinline__ void unit_states(f32x4 (&S)[CT][TILES], uint32_t col0, uint32_t lane) {
+// A column of the unit matrix.
+template <int TILES>
+__device__ __forceinline__ void unit_states(f32x4 (&S)[TILES], uint32_t col, uint32_t q) {
 #pragma unroll
-    for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct)
+    for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
 #pragma unroll
-        for (uint32_t t = 0; t < (uint32_t)TILES; ++t)
+        for (uint32_t i = 0; i < 4u; ++i) S[t][i] = place(t, 4u * q + i) == col ? 1.0f : 0.0f;
+}
+// The operands of one triangle, and four numbers of each of a chunk's rows.
+template <class M>
+struct Triangle {
+    M of[kTriangle];
+    __device__ __forceinline__ void load(const M (&from)[kTriangle][64], uint32_t lane) {
 #pragma unroll
-            for (uint32_t i = 0; i < 4u; ++i)
-                S[ct][t][i] = place(t, 4u * (lane >> 4) + i) == col0 + column<CT>(ct, lane & 15u) ? 1.0f : 0.0f;
+        for (uint32_t i = 0; i < kTriangle; ++i) of[i] = from[i][lane];
+    }
+};
+struct RowNumbers {
+    f32x4 of[4];
+    __device__ __forceinline__ void load(const float *row, uint32_t q) {
+#pragma unroll
+        for (uint32_t t = 0; t < 4u; ++t) of[t] = *reinterpret_cast<const f32x4 *>(row + 16u * t + 4u * q);
+    }
+};
+// y += T h for the lower triangle's tiles (upper: the upper one's) of 32 places s.
+template <class M, class H>
+__device__ __forceinline__ void mma_lower(f32x4 (&y)[4], const Triangle<M> &t, const H (&h)[2]) {
+    f32x4 low[2] = {y[2], y[3]};
+    mma_rows(y, {t.of[lower_at(0, 0)], t.of[lower_at(1, 0)], t.of[lower_at(2, 0)], t.of[lower_at(3, 0)]}, h[0]);
+    low[0] = y[2], low[1] = y[3];
+    mma_rows(low, {t.of[lower_at(2, 1)], t.of[lower_at(3, 1)]}, h[1]);
+    y[2] = low[0], y[3] = low[1];
+}
+template <class M, class H>
+__device__ __forceinline__ void mma_upper(f32x4 (&y)[4], const Triangle<M> &t, const H (&h)[2]) {
+    mma_rows(y, {t.of[upper_at(0, 1)], t.of[upper_at(1, 1)], t.of[upper_at(2, 1)], t.of[upper_at(3, 1)]}, h[1]);
+    f32x4 high[2] = {y[0], y[1]};
+    mma_rows(high, {t.of[upper_at(0, 0)], t.of[upper_at(1, 0)]}, h[0]);
+    y[0] = high[0], y[1] = high[1];
+}
+// S += K^T h, four tiles of keys at a time.
+template <int TILES, class Tile, class M>
+__device__ __forceinline__ void mma_keys(f32x4 (&S)[TILES], const Tile &k, uint32_t s, const M &h, uint32_t lane) {
+    constexpr int G = TILES < 4 ? TILES : 4;
+#pragma unroll
+    for (int g = 0; g < TILES; g += G) {
+        decltype(k.across(0u, 0u, 0u)) a[G];
+        f32x4 acc[G];
+#pragma unroll
+        for (int t = 0; t < G; ++t) a[t] = k.across(s, g + t, lane), acc[t] = S[g + t];
+        mma_rows(acc, a, h);
+#pragma unroll
+        for (int t = 0; t < G; ++t) S[g + t] = acc[t];
+    }
 }
 
-// Four waves walk over a segment's chunks, each with 16 CT columns of a head's
-// state; four feed them, loading a chunk while the one before is worked on and
-// leaving it in the tile of the two that is not in use (or, where shared memory
-// has room for one, after a barrier in that one).  LEAD: the walks for M and N,
-// of segments that another follows.
-template <class T, int W, int CT, bool E, bool LEAD>
-__global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+// NW waves walk over a segment's chunks, each with 16 columns of a head's state;
+// four feed them, leaving a chunk in the tile of the two that is not in use while
+// the one before is worked on (or, where shared memory has room for one, after a
+// barrier in that one).  LEAD: the walks for M and N, of segments that another
+// follows.
+template <class T, int W, int NW, bool E, bool LEAD>
+__global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
                                                          Segments seg, WalkResults to) {
     typedef typename Form<T>::Mid Mid;
-    typedef WalkTile<T, W, CT> Tile;
+    typedef typename Form<T>::In In;
+    typedef WalkTile<T, W, NW> Tile;
     constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
-    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, CT>;
-    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, CT>()];
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, NW>()];
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = LEAD ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
@@ -213,25 +254,25 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
     const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);  // its first chunk's number
     const T *values = static_cast<const T *>(a.v) + (uint64_t)head * a.value_dim;
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
-    const DeltaFeed<T, W, CT, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
-    if (wave >= 4u) {
+    const DeltaFeed<T, W, NW, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
+    if (wave >= (uint32_t)NW) {
         feed.template run<LEAD>(chunks, !unit, tile, [](uint32_t i) { return i; });
         if (LEAD && unit)
-            store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+            store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
                                    reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
-    const uint32_t col0 = block0 + wave * 16u * CT, here = wave * 16u * CT;
+    const uint32_t here = wave * 16u, col0 = block0 + here, col = col0 + m;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     constexpr bool kScaled = Form<T>::scaled;
-    f32x4 S[CT][kTiles];  // times `unit_of`, the states
+    f32x4 S[kTiles];  // times `unit_of`, the states
     float unit_of = 1.0f;
     {
         const float *from = nullptr;
         if (!LEAD && r.index) from = seg.n + ((uint64_t)number * a.heads + head) * cells;
         else if (!LEAD && a.initial) from = a.initial + ((uint64_t)r.seq * a.heads + head) * cells;
-        load_states<E>(S, from, a.key_dim, a.value_dim, col0, lane);
-        if (unit) unit_states(S, col0, lane);
+        load_states<E>(S, from, a.key_dim, a.value_dim, col, q);
+        if (unit) unit_states(S, col, q);
     }
     __syncthreads();
     for (uint32_t c = 0; c < chunks; ++c) {
@@ -240,175 +281,138 @@ __global__ __launch_bounds__(512) void delta_walk_kernel(DeltaArgs a, uint32_t f
         if (col0 < width) {
             if (!LEAD && to.states)
                 store_states<E>(to.states + ((uint64_t)(base + c) * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim,
-                                col0, lane);
+                                col, q);
             const float most = kScaled ? wave_largest(largest(S)) : 0.0f;
             const Scale of_s = scale_of<kScaled>(most);
-            f32x4 x[CT][4], o[CT][4], y[CT][4];
+            f32x4 x[4], o[4], y[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) x[ct][t] = o[ct][t] = y[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < 4; ++t) x[t] = o[t] = y[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             // K S, and (Q S)^T: the operands' sides are the other way round, which
             // leaves a row of out in a lane and neighbouring columns in its registers
-#pragma unroll
-            for (uint32_t s = 0; s < kTiles / 2u; ++s) {
-                Mid h[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(S[ct][2u * s], S[ct][2u * s + 1u], of_s.by);
+            In ka[4], qa[4];
+            auto keys = [&](uint32_t s) {
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
-                    const auto ka = in.k.along(16u * t + m, 32u * s + 8u * q);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(x[ct][t], ka, h[ct]);
-                    if (LEAD) continue;
-                    const auto qa = in.q.along(16u * t + m, 32u * s + 8u * q);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], qa);
+                    ka[t] = in.k.along(16u * t + m, 32u * s + 8u * q);
+                    if (!LEAD) qa[t] = in.q.along(16u * t + m, 32u * s + 8u * q);
                 }
-            }
-            auto numbers = [&](uint32_t which, uint32_t t) {
-                return *reinterpret_cast<const f32x4 *>(&in.p.row[which + 16u * t + 4u * q]);
             };
-            __builtin_amdgcn_sched_barrier(0);
+            keys(0u);
+#pragma unroll
+            for (uint32_t s = 0; s < kTiles / 2u; ++s) {
+                const Mid h = operand_of<Mid>(S[2u * s], S[2u * s + 1u], of_s.by);
+                mma_rows(x, ka, h);
+                if (!LEAD) mma_columns(o, h, qa);
+                if (s + 1u < kTiles / 2u) keys(s + 1u);
+            }
             // R = V - e K S
+            RowNumbers e;
+            e.load(in.p.row + kRowE, q);
+            f32x4 v[4];
+            if constexpr (kV) {
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) v[t] = value_rows<T>(in.v, t, q, m, here);
+            } else {
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4u; ++i) {
+                        const uint32_t row = 16u * t + 4u * q + i;
+                        v[t][i] = row < rows && col < a.value_dim && !unit ? (float)values[(int64_t)(lo + row) * a.v_stride + col] : 0.0f;
+                    }
+            }
+            Triangle<Mid> tri;
+            tri.load(in.p.inverse, lane);
+            const float inverse_back = in.p.row[kRowInverse];
+            __builtin_amdgcn_sched_barrier(0);
             const float from_s = of_s.back * unit_of;
 #pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 e = numbers(kRowE, t) * from_s;
+            for (uint32_t t = 0; t < 4u; ++t)
 #pragma unroll
-                for (uint32_t ct = 0; ct < (uint32_t)CT; ++ct) {
-                    f32x4 v;
-                    if constexpr (kV) {
-                        v = value_rows<T, CT>(in.v, t, q, m, here, ct);
-                    } else {
-                        const uint32_t col = col0 + column<CT>(ct, m);
-#pragma unroll
-                        for (uint32_t i = 0; i < 4u; ++i) {
-                            const uint32_t row = 16u * t + 4u * q + i;
-                            v[i] = row < rows && col < a.value_dim && !unit ? (float)values[(int64_t)(lo + row) * a.v_stride + col] : 0.0f;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[ct][t][i] = __builtin_fmaf(-e[i], x[ct][t][i], v[i]);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 4; ++i) x[t][i] = __builtin_fmaf(-from_s * e.of[t][i], x[t][i], v[t][i]);
             // rho
             const Scale of_x = scale_of<kScaled>(kScaled ? wave_largest(largest(x)) : 0.0f);
-            const float from_x = kScaled ? of_x.back * in.p.row[kRowInverse] : 1.0f;
-#pragma unroll
-            for (uint32_t s = 0; s < 2u; ++s) {
-                Mid h[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(x[ct][2u * s], x[ct][2u * s + 1u], of_x.by);
-#pragma unroll
-                for (uint32_t t = 2u * s; t < 4u; ++t) {
-                    const Mid inverse = in.p.inverse[lower_at(t, s)][lane];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(y[ct][t], inverse, h[ct]);
-                }
+            const float from_x = kScaled ? of_x.back * inverse_back : 1.0f;
+            {
+                const Mid h[2] = {operand_of<Mid>(x[0], x[1], of_x.by), operand_of<Mid>(x[2], x[3], of_x.by)};
+                mma_lower(y, tri, h);
             }
             if (!LEAD && to.rhos) {
                 if (kScaled) {
                     const float of_y = wave_largest(largest(y)) * from_x;
-                    float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kSizes + col0 / (16u * CT);
+                    float *sizes = to.sizes + ((uint64_t)(base + c) * a.heads + head) * kSizes + col0 / 16u;
                     if (lane == 0u) sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y;
                 }
-                store_rows<E>(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, from_x,
-                              rows, col0, a.value_dim, lane);
+                if (col < a.value_dim)
+                    store_rows(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, from_x,
+                               rows, col, q);
             }
             __builtin_amdgcn_sched_barrier(0);
             // U, and out^T = scale e (Q S)^T + U^T P^T
+            RowNumbers beta, tail;
+            float eq[4];
+            beta.load(in.p.row + kRowBeta, q);
+            if (!LEAD) {
+                tri.load(in.p.scores, lane);
 #pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 beta = numbers(kRowBeta, t) * from_x;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= beta;
+                for (uint32_t t = 0; t < 4u; ++t) eq[t] = in.p.row[kRowQ + 16u * t + m];
             }
-            float from_o = 1.0f;
+            const float kept = unit_of * in.p.row[kRowWhole], scores_by = in.p.row[kRowScores], scores_back = in.p.row[kRowScoresBack];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t t = 0; t < 4u; ++t) y[t] *= beta.of[t] * from_x;
+            tail.load(in.p.row + kRowTail, q);
             if constexpr (!LEAD) {
                 const Scale of_u = scale_of<kScaled>(kScaled ? wave_largest(largest(y)) : 0.0f);
-                const float to_o = kScaled ? from_s * of_u.by * in.p.row[kRowScores] : 1.0f;
-                from_o = kScaled ? of_u.back * in.p.row[kRowScoresBack] : 1.0f;
+                const float to_o = kScaled ? from_s * of_u.by * scores_by : 1.0f, from_o = kScaled ? of_u.back * scores_back : 1.0f;
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) o[t] *= eq[t] * to_o;
+                const Mid h[2] = {operand_of<Mid>(y[0], y[1], of_u.by), operand_of<Mid>(y[2], y[3], of_u.by)};
+                mma_columns(o, h[0], {tri.of[lower_at(0, 0)], tri.of[lower_at(1, 0)], tri.of[lower_at(2, 0)], tri.of[lower_at(3, 0)]});
+                f32x4 low[2] = {o[2], o[3]};
+                mma_columns(low, h[1], {tri.of[lower_at(2, 1)], tri.of[lower_at(3, 1)]});
+                o[2] = low[0], o[3] = low[1];
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
-                    const float e = in.p.row[kRowQ + 16u * t + m] * to_o;
+                    const uint32_t row = 16u * t + m, at = col0 + 4u * q;
+                    if (row < rows && at < a.value_dim) {
+                        T *p = static_cast<T *>(to.out) + ((uint64_t)(lo + row) * a.heads + head) * a.value_dim + at;
+                        Pack<T, 4> w;
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) o[ct][t] *= e;
-                }
+                        for (int i = 0; i < 4; ++i) w.v[i] = (T)(o[t][i] * from_o);
+                        if (E || at + 4u <= a.value_dim) {
+                            *reinterpret_cast<Pack<T, 4> *>(p) = w;
+                        } else {
 #pragma unroll
-                for (uint32_t s = 0; s < 2u; ++s) {
-                    Mid h[CT];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_u.by);
-#pragma unroll
-                    for (uint32_t t = 2u * s; t < 4u; ++t) {
-                        const Mid scores = in.p.scores[lower_at(t, s)][lane];
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mma(o[ct][t], h[ct], scores);
+                            for (uint32_t i = 0; i < 4u; ++i)
+                                if (at + i < a.value_dim) p[i] = w.v[i];
+                        }
                     }
                 }
             }
-#pragma unroll
-            for (uint32_t t = 0; t < (LEAD ? 0u : 4u); ++t) {
-                const uint32_t row = 16u * t + m, col = col0 + 4u * CT * q;
-                if (row < rows && col < a.value_dim) {
-                    T *at = static_cast<T *>(to.out) + ((uint64_t)(lo + row) * a.heads + head) * a.value_dim + col;
-                    Pack<T, 4 * CT> w;
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w.v[4 * ct + i] = (T)(o[ct][t][i] * from_o);
-                    if (E || col + 4u * CT <= a.value_dim) {
-                        *reinterpret_cast<Pack<T, 4 * CT> *>(at) = w;
-                    } else {
-#pragma unroll
-                        for (uint32_t i = 0; i < 4u * CT; ++i)
-                            if (col + i < a.value_dim) at[i] = w.v[i];
-                    }
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
             // S = e_C S + K^T diag(exp(G_C - G)) U
 #pragma unroll
-            for (uint32_t t = 0; t < 4u; ++t) {
-                const f32x4 tail = numbers(kRowTail, t);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][t] *= tail;
-            }
-            const float kept = unit_of * in.p.row[kRowWhole];
+            for (uint32_t t = 0; t < 4u; ++t) y[t] *= tail.of[t];
             const Scale of_u = scale_of_sum<kScaled>(kScaled ? wave_largest(largest(y)) : 0.0f, most * kept);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) S[ct][t] *= kept * of_u.by;
+            for (uint32_t t = 0; t < kTiles; ++t) S[t] *= kept * of_u.by;
             unit_of = of_u.back;
-#pragma unroll
-            for (uint32_t s = 0; s < 2u; ++s) {
-                Mid h[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) h[ct] = operand_of<Mid>(y[ct][2u * s], y[ct][2u * s + 1u], of_u.by);
-#pragma unroll
-                for (uint32_t t = 0; t < kTiles; ++t) {
-                    const auto ka = in.k.across(s, t, lane);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(S[ct][t], ka, h[ct]);
-                }
-            }
+            mma_keys(S, in.k, 0u, operand_of<Mid>(y[0], y[1], of_u.by), lane);
+            mma_keys(S, in.k, 1u, operand_of<Mid>(y[2], y[3], of_u.by), lane);
         }
         if (!kTwo) __syncthreads();
         __syncthreads();
     }
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (LEAD && unit) {
-        store_matrix<T, W, CT>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), S, unit_of,
+        store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &S, unit_of,
                                block0, wave, lane, true);
         return;
     }
     if (col0 >= width) return;
-    if (LEAD) store_states<E>(seg.n + place_of * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
+    if (LEAD) store_states<E>(seg.n + place_of * cells, S, unit_of, a.key_dim, a.value_dim, col, q);
     else if (to.final && r.hi == seq.hi)
-        store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim, col0, lane);
+        store_states<E>(to.final + ((uint64_t)r.seq * a.heads + head) * cells, S, unit_of, a.key_dim, a.value_dim, col, q);
 }
 
 // The states that enter a sequence's segments after the first, S <- M S + N,
@@ -475,7 +479,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
         if (works) {
 #pragma unroll
             for (uint32_t k = 0; k < NC; ++k) {
-                const Scale of = scale_of<kScaled>(kScaled ? wave_largest(largest(S[k])) : 0.0f);
+                const Scale of = scale_of<kScaled>(kScaled ? wave_largest(__builtin_fmaxf(largest(S[k][0]), largest(S[k][1]))) : 0.0f);
 #pragma unroll
                 for (uint32_t ct = 0; ct < CT; ++ct)
                     operands[b][wave * NC + k][ct][lane] = operand_of<Mid>(S[k][ct][0], S[k][ct][1], of.by);
@@ -595,13 +599,13 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
         });
         seg.m = ws_at<void *>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
         const WalkResults to = {out, final, checkpoints, rhos, sizes};
-        auto walk = [&](auto ct, auto eights) {
-            constexpr int CT = decltype(ct)::value;
+        auto walk = [&](auto waves, auto eights) {
+            constexpr int NW = decltype(waves)::value;
             constexpr bool E = decltype(eights)::value;
-            const uint64_t blocks = ceil_div(a.value_dim, 64u * CT), all = blocks + ceil_div(a.key_dim, 64u * CT);
+            const uint64_t blocks = ceil_div(a.value_dim, 16u * NW), all = blocks + ceil_div(a.key_dim, 16u * NW);
             if (linked) {
-                launch_in_parts(segments * a.heads, all, 512u, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_walk_kernel<T, W, CT, E, true>), dim3(grid), dim3(512), 0, s, a,
+                launch_in_parts(segments * a.heads, all, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_kernel<T, W, NW, E, true>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a,
                                        first, prepared, seg, to);
                 });
                 const uint64_t columns = ceil_div(a.value_dim, 32u);
@@ -610,15 +614,15 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                                        a.initial);
                 });
             }
-            launch_in_parts(segments * a.heads, blocks, 512u, [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_walk_kernel<T, W, CT, E, false>), dim3(grid), dim3(512), 0, s, a,
+            launch_in_parts(segments * a.heads, blocks, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_kernel<T, W, NW, E, false>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a,
                                    first, prepared, seg, to);
             });
         };
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
         auto shape = [&](auto e) {
-            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 2 : 1>(), e);
-            else walk(std::integral_constant<int, 1>(), e);
+            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 8 : 4>(), e);
+            else walk(std::integral_constant<int, 4>(), e);
         };
         if (eights) shape(std::true_type());
         else shape(std::false_type());
