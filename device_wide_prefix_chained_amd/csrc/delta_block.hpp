@@ -244,7 +244,7 @@ template <class O, int W>
 struct RowTile;
 template <int N, int W>
 struct RowTile<Planes<N>, W> {
-    static constexpr int kStride = W + 8;
+    static constexpr int kStride = W + 16;  // 32 bytes: the transposing reads of 16 rows meet no bank twice
     uint16_t w[N][kChunk][kStride];
     __device__ __forceinline__ void put(uint32_t row, uint32_t col, const float (&v)[8], float by) {
         Planes<N> o;

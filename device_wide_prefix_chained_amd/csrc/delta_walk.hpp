@@ -531,28 +531,28 @@ inline size_t matrix_bytes(uint32_t key_dim) {
     return n;
 }
 
-// Rows of a segment, as a shift: as many as make a call's steps fewest, by what
-// a step was measured to take next to a walk's over 32 columns a wave, where
-// 256 workgroups run at once and sequences are cut at random (the longest of n
-// is then the mean times 1 + 1/2 + ... + 1/n).  Walks for M and N 0.6 each, a
-// link 0.6.
+// Rows of a segment, as a shift: as many as take the least time by what the
+// parts of a call were measured to take (us; 128 keys and columns, where 256
+// workgroups run at once): a step of a walk 5.5, of the walks for M and N 3.9,
+// the start of either 7, a link 2.2.  Sequences are reckoned to be cut at random:
+// the longest of n is then the mean times 1 + 1/2 + ... + 1/n.
 uint32_t segment_shift(const DeltaArgs &a, uint32_t cols) {
-    const double chunks = (double)(a.tokens >> kChunkShift) + 0.5 * a.num_seqs, heads = a.heads;
+    const double chunks = (double)ceil_div(a.tokens, kChunk), heads = a.heads, n = a.num_seqs;
     const double value_blocks = (double)ceil_div(a.value_dim, cols), key_blocks = (double)ceil_div(a.key_dim, cols);
     double longest = 0.0;
     for (uint32_t i = 1; i <= a.num_seqs && i <= 64u; ++i) longest += 1.0 / i;
-    longest *= chunks / a.num_seqs;
+    longest *= chunks / n;
     longest = longest > chunks ? chunks : longest;
-    const double work = chunks * heads * value_blocks / 256.0;
-    double best = longest > work ? longest : work;
+    auto rounds = [](double groups) { return groups > 256.0 ? groups / 256.0 : 1.0; };
+    const double work = (chunks + 0.5 * (n - 1.0)) * heads * value_blocks / 256.0;
+    double best = 7.0 + 5.5 * (longest > work ? longest : work);
     uint32_t shift = 31u;
     for (uint32_t by = 2u; by <= 7u; ++by) {
-        const double rows = (double)(1u << by), segments = chunks / rows + 0.5 * a.num_seqs;
+        const double rows = (double)(1u << by), segments = __builtin_ceil(chunks / rows) + 0.5 * (n - 1.0);
         if (longest < 2.0 * rows) break;
-        const double main = __builtin_ceil(segments * heads * value_blocks / 256.0) * rows;
-        const double led = segments - a.num_seqs > 0.0 ? segments - a.num_seqs : 0.0;
-        const double lead = 0.6 * __builtin_ceil(led * heads * (value_blocks + key_blocks) / 256.0) * rows;
-        const double cost = main + lead + 0.6 * longest / rows + 4.0;
+        const double led = segments > n ? segments - n : 1.0;
+        const double cost = rounds(segments * heads * value_blocks) * (7.0 + 5.5 * rows) +
+                            rounds(led * heads * (value_blocks + key_blocks)) * (7.0 + 3.9 * rows) + 2.2 * longest / rows + 6.0;
         if (cost < best) best = cost, shift = kChunkShift + by;
     }
     return shift;

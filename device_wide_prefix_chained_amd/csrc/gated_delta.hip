@@ -61,15 +61,15 @@ namespace {
 // A workgroup has `cols` columns of one head's state, four a thread and up to
 // kStepRows rows of them: the state is read once, held in registers, and
 // written once.  out = scale (e S^T q + (k q) u) needs no second sum over the
-// new state.
-constexpr uint32_t kStepRows = 16u;
+// new state.  Bound by memory: the state's 8 bytes an element.
+constexpr uint32_t kStepRows = 16u, kStepThreads = 512u;
 
 template <class T>
-__global__ __launch_bounds__(1024) void delta_step_kernel(DeltaArgs a, uint32_t first, uint32_t groups, const float *state,
+__global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, uint32_t first, uint32_t groups, const float *state,
                                                           float *new_state, const int32_t *__restrict__ slots,
                                                           uint32_t pool, T *__restrict__ out) {
     __shared__ float key[PS_DELTA_MAX_DIM], query[PS_DELTA_MAX_DIM];
-    __shared__ float part[2][4096];
+    __shared__ float part[2][2048];
     const uint32_t cols = groups * 4u, blocks = (a.value_dim + cols - 1u) / cols;
     const uint32_t item = first + blockIdx.x / blocks, head = item % a.heads, row = item / a.heads;
     const uint32_t khead = head / (a.heads / a.kheads), lane = threadIdx.x & 63u;
@@ -221,8 +221,10 @@ extern "C" ps_status ps_gated_delta_step(const ps_delta_input *in, const float *
     hipStream_t s = static_cast<hipStream_t>(stream);
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
+        // up to 128 columns a workgroup; fewer while they leave CUs without one
         uint32_t groups = 4u;
-        while (groups * 4u < a.value_dim) groups *= 2u;
+        while (groups < 32u && groups * 4u < a.value_dim) groups *= 2u;
+        while (groups > 4u && (uint64_t)a.tokens * a.heads * ceil_div(a.value_dim, groups * 4u) < 256u) groups /= 2u;
         uint32_t bands = 1u;
         while (bands * kStepRows < a.key_dim || bands * groups < 64u) bands *= 2u;
         const uint64_t blocks = ceil_div(a.value_dim, groups * 4u);
