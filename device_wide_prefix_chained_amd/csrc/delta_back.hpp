@@ -28,7 +28,7 @@ struct BackResults {
     const float *dfinal;  // [num_seqs, heads, key_dim, value_dim] or NULL
     float *dinitial;      // the same, or NULL
     float *dstates;       // [chunk numbers, heads, key_dim, value_dim]: D
-    float *omega;         // [tokens, heads, value_dim]
+    float *omega;         // [chunk numbers, heads, kChunk, value_dim]
     float *sizes;         // [chunk numbers, heads, kBackSizes]: the largest of `dstates`, `omega` and dout
 };
 constexpr uint32_t kBackSizes = 3u * kSizeWaves;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArg
                     if (lane == 0u) sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y, sizes[2u * kSizeWaves] = most_o;
                 }
                 if (col < a.value_dim)
-                    store_rows(to.omega + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)grads_stride, y, from_y, rows, col, q);
+                    store_rows(to.omega + ((uint64_t)(base + c) * a.heads + head) * kChunk * a.value_dim, a.value_dim, y, from_y, col, q);
             }
             // D = e_C D + Q^T diag(scale e) dO - K^T diag(e) beta omega
             __builtin_amdgcn_sched_barrier(0);
@@ -216,22 +216,35 @@ __device__ __forceinline__ float column_total(float v) {
     return v + w;
 }
 
+// 32 columns of a chunk's rows.
+template <class T>
+struct GradColumns {
+    RowTile<typename Form<T>::In, 32> dout;
+    RowTile<typename Form<T>::Mid, 32> rho, omega;
+};
+// Sums over keys of a chunk's rows, by wave.
+struct GradSums {
+    float query[8][kChunk], key[8][kChunk], end[8][kChunk], pair[8][kChunk];
+};
 template <class T, int W>
 struct GradShared {
-    typedef typename Form<T>::Mid Mid;
+    static constexpr size_t kFixed = 2u * sizeof(KeyTile<T, W>) + 2048u;
+    // two sets of columns, and the sums in memory of their own, where there is room
+    static constexpr bool kTwo = kFixed + 2u * sizeof(GradColumns<T>) + sizeof(GradSums) <= kMostShared;
+    static constexpr bool kApart = kTwo;
     KeyTile<T, W> k, q;
     union {
-        struct {
-            RowTile<typename Form<T>::In, 32> dout;
-            RowTile<Mid, 32> rho, omega;
-        } in;
-        Mid triangle[2][kTriangle][64];
-        struct {
-            float query[8][kChunk], key[8][kChunk], end[8][kChunk], pair[8][kChunk];
-        } part;
+        GradColumns<T> in[kTwo ? 2 : 1];
+        typename Form<T>::Mid triangle[2][kTriangle][64];
+        GradSums within;
     };
+    GradSums apart[kApart ? 1 : 0];
     double sum[kChunk];
     float beta[kChunk], nu[kChunk], mu[kChunk], dot[8], most[8];
+    __device__ __forceinline__ GradSums &part() {
+        if constexpr (kApart) return apart[0];
+        else return within;
+    }
 };
 
 // One workgroup a chunk and head of keys; it takes the heads of values that
@@ -241,7 +254,7 @@ struct GradShared {
 // omega rho^T: wave w the columns of tile w & 3 of the lower triangle as it is
 // (five, slots up to w: rows j, columns i) and transposed (slots above: rows
 // i, columns j), so that both are operands as they come.
-template <class T, int W, bool E>
+template <class T, int W, bool E, bool SOLO>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
                                                           const float *__restrict__ states, const float *__restrict__ rhos,
                                                           const float *__restrict__ sizes, const float *__restrict__ dstates,
@@ -271,11 +284,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
     }
     __syncthreads();
     f32x4 dq[DT][TT], dk[DT][TT];  // with respect to the keys and queries of length 1
+    if (!SOLO)
 #pragma unroll
-    for (uint32_t d = 0; d < DT; ++d)
+        for (uint32_t d = 0; d < DT; ++d)
 #pragma unroll
-        for (uint32_t t = 0; t < TT; ++t) dq[d][t] = dk[d][t] = none;
-    const uint32_t per = a.heads / a.kheads;
+            for (uint32_t t = 0; t < TT; ++t) dq[d][t] = dk[d][t] = none;
+    const uint32_t per = SOLO ? 1u : a.heads / a.kheads;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     for (uint32_t j = 0; j < per; ++j) {
         const uint32_t head = khead * per + j;
@@ -284,11 +298,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
         asm volatile("" : "+v"(n), "+v"(q), "+v"(own), "+v"(lane), "+v"(row), "+v"(part));
         const uint64_t of_head = (uint64_t)slot * a.heads + head, at_row = ((uint64_t)(c.lo + row) * a.heads + head) * a.value_dim;
         const float *state = states + of_head * cells, *dstate = dstates + of_head * cells;
-        // the next 32 columns, on their way while some are worked on
-        struct {
-            float s[DT][8], d[DT][8];
-            f32x4 rho, omega, dout;
-        } next;
+        // the next 32 columns of the rows, on their way while some are worked on
+        f32x4 next_rho, next_omega, next_dout;
+        float next_s[DT][8], next_d[DT][8];
         auto fetch = [&](uint32_t v0) {
 #pragma unroll
             for (uint32_t d = 0; d < DT; ++d) {
@@ -296,35 +308,36 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                 const bool there = key < a.key_dim && col < a.value_dim;
                 const uint32_t at = there ? key * a.value_dim + col : 0u;
                 if (E) {
-                    const Pack<float, 8> s = *reinterpret_cast<const Pack<float, 8> *>(state + at);
-                    const Pack<float, 8> g = *reinterpret_cast<const Pack<float, 8> *>(dstate + at);
+                    const Pack<float, 8> ps = *reinterpret_cast<const Pack<float, 8> *>(state + at);
+                    const Pack<float, 8> pg = *reinterpret_cast<const Pack<float, 8> *>(dstate + at);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) next.s[d][i] = there ? s.v[i] : 0.0f, next.d[d][i] = there ? g.v[i] : 0.0f;
+                    for (int i = 0; i < 8; ++i) next_s[d][i] = there ? ps.v[i] : 0.0f, next_d[d][i] = there ? pg.v[i] : 0.0f;
                 } else {
 #pragma unroll
                     for (uint32_t i = 0; i < 8u; ++i) {
                         const bool is = there && col + i < a.value_dim;
-                        next.s[d][i] = is ? state[at + i] : 0.0f;
-                        next.d[d][i] = is ? dstate[at + i] : 0.0f;
+                        next_s[d][i] = is ? state[at + i] : 0.0f;
+                        next_d[d][i] = is ? dstate[at + i] : 0.0f;
                     }
                 }
             }
             const bool there = row < rows && v0 + part < a.value_dim;
             const uint64_t at = there ? at_row + v0 + part : ((uint64_t)c.lo * a.heads + head) * a.value_dim;
+            const uint64_t kept = of_head * kChunk * a.value_dim + (there ? row * a.value_dim + v0 + part : 0u);
             if (E) {
-                next.rho = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(rhos + at));
-                next.omega = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(omega + at));
+                next_rho = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(rhos + kept));
+                next_omega = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(omega + kept));
                 const Pack<T, 4> o = *reinterpret_cast<const Pack<T, 4> *>(dout + at);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) next.dout[i] = (float)o.v[i];
-                if (!there) next.rho = next.omega = next.dout = none;
+                for (int i = 0; i < 4; ++i) next_dout[i] = (float)o.v[i];
+                if (!there) next_rho = next_omega = next_dout = none;
             } else {
 #pragma unroll
                 for (uint32_t i = 0; i < 4u; ++i) {
                     const bool is = there && v0 + part + i < a.value_dim;
-                    next.rho[i] = is ? rhos[at + i] : 0.0f;
-                    next.omega[i] = is ? omega[at + i] : 0.0f;
-                    next.dout[i] = is ? (float)dout[at + i] : 0.0f;
+                    next_rho[i] = is ? rhos[kept + i] : 0.0f;
+                    next_omega[i] = is ? omega[kept + i] : 0.0f;
+                    next_dout[i] = is ? (float)dout[at + i] : 0.0f;
                 }
             }
         };
@@ -353,14 +366,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
         for (int t = 0; t < 5; ++t) e[t] = none;
         float dot = 0.0f, dbeta = 0.0f;
         for (uint32_t v0 = 0; v0 < a.value_dim; v0 += 32u) {
-            if (v0) __syncthreads();  // the columns before are read
+            if (!GradShared<T, W>::kTwo && v0) __syncthreads();  // the columns before are read
+            GradColumns<T> &in = sh.in[GradShared<T, W>::kTwo ? v0 >> 5 & 1u : 0u];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dbeta = __builtin_fmaf(next.rho[i], next.omega[i], dbeta);
+            for (int i = 0; i < 4; ++i) dbeta = __builtin_fmaf(next_rho[i], next_omega[i], dbeta);
             if (row < rows) {
                 T *p = static_cast<T *>(to.dv) + at_row + v0 + part;
                 Pack<T, 4> w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w.v[i] = (T)(own_beta * next.omega[i]);
+                for (int i = 0; i < 4; ++i) w.v[i] = (T)(own_beta * next_omega[i]);
                 if (E) {
                     if (v0 + part < a.value_dim) *reinterpret_cast<Pack<T, 4> *>(p) = w;
                 } else {
@@ -369,48 +383,48 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                         if (v0 + part + i < a.value_dim) p[i] = w.v[i];
                 }
             }
-            sh.in.dout.put(row, part, next.dout, of_o.by);
-            sh.in.rho.put(row, part, next.rho, of_rho.by);
-            sh.in.omega.put(row, part, next.omega, of_omega.by);
+            in.dout.put(row, part, next_dout, of_o.by);
+            in.rho.put(row, part, next_rho, of_rho.by);
+            in.omega.put(row, part, next_omega, of_omega.by);
             Mid S[DT], D[DT];
 #pragma unroll
             for (uint32_t d = 0; d < DT; ++d) {
                 if (t0 == 0u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(next.s[d][i], next.d[d][i], dot);
-                operand_of(S[d], next.s[d], of_s.by);
-                operand_of(D[d], next.d[d], of_d.by);
+                    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(next_s[d][i], next_d[d][i], dot);
+                operand_of(S[d], next_s[d], of_s.by);
+                operand_of(D[d], next_d[d], of_d.by);
             }
             if (v0 + 32u < a.value_dim) fetch(v0 + 32u);
             __syncthreads();
 #pragma unroll
             for (uint32_t t = 0; t < TT; ++t) {
                 const uint32_t at = 16u * (t0 + t) + n;
-                const auto o = sh.in.dout.along(at, 8u * q);
-                const auto w = sh.in.omega.along(at, 8u * q), r = sh.in.rho.along(at, 8u * q);
+                const auto o = in.dout.along(at, 8u * q);
+                const auto w = in.omega.along(at, 8u * q), r = in.rho.along(at, 8u * q);
 #pragma unroll
                 for (uint32_t d = 0; d < DT; ++d) {
-                    mma(qs[d][t], S[d], o);
                     mma(rs[d][t], S[d], w);
                     mma(ends[d][t], D[d], r);
+                    mma(qs[d][t], S[d], o);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const auto own_r = sh.in.rho.along(own, 8u * q);
+            const auto own_r = in.rho.along(own, 8u * q);
             if (keys_side) {
-                const auto own_w = sh.in.omega.along(own, 8u * q);
+                const auto own_w = in.omega.along(own, 8u * q);
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
-                    if (t <= own_tile) mma(e[t], sh.in.rho.along(16u * t + n, 8u * q), own_w);
-                    if (t >= own_tile) mma(e[t + 1], sh.in.omega.along(16u * t + n, 8u * q), own_r);
+                    if (t <= own_tile) mma(e[t], in.rho.along(16u * t + n, 8u * q), own_w);
+                    if (t >= own_tile) mma(e[t + 1], in.omega.along(16u * t + n, 8u * q), own_r);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-                const auto own_o = sh.in.dout.along(own, 8u * q);
+                const auto own_o = in.dout.along(own, 8u * q);
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
-                    if (t <= own_tile) mma(e[t], sh.in.rho.along(16u * t + n, 8u * q), own_o);
-                    if (t >= own_tile) mma(e[t + 1], sh.in.dout.along(16u * t + n, 8u * q), own_r);
+                    if (t <= own_tile) mma(e[t], in.rho.along(16u * t + n, 8u * q), own_o);
+                    if (t >= own_tile) mma(e[t + 1], in.dout.along(16u * t + n, 8u * q), own_r);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -445,16 +459,16 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                             key = __builtin_fmaf(kv[i], y[i], key);
                             end = __builtin_fmaf(kv[i], z[i], end);
                         }
-                        dq[d][tt] += x;
-                        dk[d][tt] += z - y;
+                        dq[d][tt] = SOLO ? x : dq[d][tt] + x;
+                        dk[d][tt] = SOLO ? z - y : dk[d][tt] + (z - y);
                     }
                 }
             }
             query = column_total(query), key = column_total(key), end = column_total(end);
             if (q == 0u) {
-                sh.part.query[wave][at] = query * sh.mu[at];
-                sh.part.key[wave][at] = key * sh.nu[at];
-                sh.part.end[wave][at] = end * sh.nu[at];
+                sh.part().query[wave][at] = query * sh.mu[at];
+                sh.part().key[wave][at] = key * sh.nu[at];
+                sh.part().end[wave][at] = end * sh.nu[at];
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -506,7 +520,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             __builtin_amdgcn_sched_barrier(0);
         }
         const float pair = row_sums(pairs, lane);  // lane n of quarter q: tile n >> 2, row 4 q + (n & 3)
-        sh.part.pair[wave][16u * (n >> 2) + 4u * q + (n & 3u)] = pair;
+        sh.part().pair[wave][16u * (n >> 2) + 4u * q + (n & 3u)] = pair;
         const float into_own = back * beta_own * (keys_side ? -1.0f : a.scale);
 #pragma unroll
         for (uint32_t t = 0; t < 4u; ++t) {
@@ -537,11 +551,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             for (int w = 0; w < 8; ++w) m = __builtin_fmaxf(m, sh.most[w]);
             of_e = scale_of<true, -30>(m);
         }
-        if (wave == 0u) {
+        // the log decays' gradients, from the sums that all waves have left
+        auto decays = [&]() {
+            if (wave != 0u) return;
             auto sum_of = [&](const float(&p)[8][kChunk]) {
                 return ((p[0][lane] + p[1][lane]) + (p[2][lane] + p[3][lane])) + ((p[4][lane] + p[5][lane]) + (p[6][lane] + p[7][lane]));
             };
-            double after = (double)sum_of(sh.part.query) - (double)sum_of(sh.part.key), ends_before = sum_of(sh.part.end);
+            double after = (double)sum_of(sh.part().query) - (double)sum_of(sh.part().key), ends_before = sum_of(sh.part().end);
 #pragma unroll
             for (uint32_t by = 1u; by < 64u; by *= 2u) {
                 const double up = shuffle(after, lane + by), down = shuffle(ends_before, lane - by);
@@ -555,8 +571,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             if (lane == 0u) prior = 0.0;
             if (lane < rows)
                 to.dg[(uint64_t)(c.lo + lane) * a.heads + head] =
-                    (float)(sum_of(sh.part.pair) + after + prior + (double)(exp_hw((float)all) * whole));
-        }
+                    (float)(sum_of(sh.part().pair) + after + prior + (double)(exp_hw((float)all) * whole));
+        };
+        if (!GradShared<T, W>::kApart) decays();
         // dqk K and dkk K, then dqk^T Q and dkk^T K, two triangles in shared memory at a time
         if (kScaled) {
 #pragma unroll
@@ -604,6 +621,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
                 for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_e.back, dk[d][t] *= of_e.back;
         }
+        if (GradShared<T, W>::kApart) decays();
     }
     __syncthreads();
     if ((threadIdx.x & 7u) == 0u) sh.beta[row] = raw_mu, sh.sum[row] = raw_nu;
@@ -628,7 +646,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                 }
             }
             query = column_total(query), key = column_total(key);
-            if (q == 0u) sh.part.query[wave][at] = query, sh.part.key[wave][at] = key;
+            if (q == 0u) sh.part().query[wave][at] = query, sh.part().key[wave][at] = key;
         }
     }
     __syncthreads();
@@ -641,7 +659,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             auto sum_of = [&](const float(&p)[8][kChunk]) {
                 return ((p[0][at] + p[1][at]) + (p[2][at] + p[3][at])) + ((p[4][at] + p[5][at]) + (p[6][at] + p[7][at]));
             };
-            query = sum_of(sh.part.query) * mu * mu, key = sum_of(sh.part.key) * nu * nu;
+            query = sum_of(sh.part().query) * mu * mu, key = sum_of(sh.part().key) * nu * nu;
         }
         if (at >= rows) continue;
 #pragma unroll
@@ -684,7 +702,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u, state_floats = (uint64_t)a.slots * a.heads * cells;
     const size_t m_at = plan.take(linked * matrix_bytes<T>(a.key_dim)), n_at = plan.take(linked * cells * 4u);
     const size_t sizes_at = plan.take((size_t)a.slots * a.heads * kBackSizes * 4u);
-    const size_t d_at = plan.take(state_floats * 4u), omega_at = plan.take((size_t)a.tokens * a.heads * a.value_dim * 4u);
+    const size_t d_at = plan.take(state_floats * 4u), omega_at = plan.take((size_t)a.slots * a.heads * kChunk * a.value_dim * 4u);
     bool query = false;
     ps_status st = workspace_protocol(ws, ws_bytes, plan.at, &query);
     if (st != PS_OK || query) return st;
@@ -709,7 +727,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     float *dstates = ws_at<float>(ws, d_at), *omega = ws_at<float>(ws, omega_at);
     const T *g = static_cast<const T *>(dout);
     float *back_sizes = ws_at<float>(ws, sizes_at);
-    const float *rhos = checkpoints + state_floats, *sizes = rhos + (uint64_t)a.tokens * a.heads * a.value_dim;
+    const float *rhos = checkpoints + state_floats, *sizes = rhos + (uint64_t)a.slots * a.heads * kChunk * a.value_dim;
     const BackResults to = {dfinal, grads->dinitial, dstates, omega, back_sizes};
     const DeltaGradPtrs out = {grads->dq, grads->dk, grads->dv, grads->dg, grads->dbeta};
     return with_key_width(a.key_dim, [&](auto w) {
@@ -738,8 +756,13 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                                    g, false, to);
             });
             launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 512u, [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_grads_kernel<T, W, E>), dim3(grid), dim3(512), 0, s, a, first, g, checkpoints, rhos, sizes,
-                                   dstates, omega, back_sizes, (uint32_t)ceil_div(a.value_dim, 16u), out);
+                auto launch = [&](auto solo) {
+                    hipLaunchKernelGGL((delta_grads_kernel<T, W, E, decltype(solo)::value>), dim3(grid), dim3(512), 0, s, a, first, g,
+                                       checkpoints, rhos, sizes, dstates, omega, back_sizes,
+                                       (uint32_t)ceil_div(a.value_dim, 16u), out);
+                };
+                if (a.heads == a.kheads) launch(std::true_type());
+                else launch(std::false_type());
             });
         };
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;

@@ -445,17 +445,14 @@ __device__ __forceinline__ void store_states(float *to, const f32x4 (&S)[TILES],
             if (E || row + i < rows) p[i * width] = S[t][i] * by;
     }
 }
-// A result's tiles over a chunk's rows into rows of `stride`, rows below `rows`.
-__device__ __forceinline__ void store_rows(float *to, uint64_t stride, const f32x4 (&y)[4], float by, uint32_t rows,
-                                           uint32_t col, uint32_t q) {
-    asm volatile("" : "+s"(stride));
+// A result's tiles over all of a chunk's rows into packed rows of `width`.
+__device__ __forceinline__ void store_rows(float *to, uint32_t width, const f32x4 (&y)[4], float by, uint32_t col, uint32_t q) {
+    asm volatile("" : "+s"(width));
 #pragma unroll
     for (uint32_t t = 0; t < 4u; ++t) {
-        const uint32_t row = 16u * t + 4u * q;
-        float *p = to + (row * stride + col);
+        float *p = to + ((16u * t + 4u * q) * width + col);
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; ++i)
-            if (row + i < rows) p[i * stride] = y[t][i] * by;
+        for (uint32_t i = 0; i < 4u; ++i) p[i * width] = y[t][i] * by;
     }
 }
 

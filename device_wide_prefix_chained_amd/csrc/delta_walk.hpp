@@ -89,7 +89,8 @@ __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *sha
 }
 struct WalkResults {
     void *out;
-    float *final, *states, *rhos;
+    float *final;
+    float *states, *rhos;  // [chunk numbers, heads, key_dim | kChunk, value_dim]
     float *sizes;  // [chunk numbers, heads, kSizes]: the largest of `states` and of `rhos`, by wave of columns
 };
 
@@ -344,8 +345,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, 
                     if (lane == 0u) sizes[0] = most * unit_of, sizes[kSizeWaves] = of_y;
                 }
                 if (col < a.value_dim)
-                    store_rows(to.rhos + ((uint64_t)lo * a.heads + head) * a.value_dim, (uint64_t)a.heads * a.value_dim, y, from_x,
-                               rows, col, q);
+                    store_rows(to.rhos + ((uint64_t)(base + c) * a.heads + head) * kChunk * a.value_dim, a.value_dim, y, from_x, col, q);
             }
             __builtin_amdgcn_sched_barrier(0);
             // U, and out^T = scale e (Q S)^T + U^T P^T
@@ -589,7 +589,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
     if (!a.num_seqs) return PS_OK;
     Prepared<T> *prepared = ws_at<Prepared<T>>(ws, prepared_at);
     float *rhos = checkpoints ? checkpoints + (uint64_t)a.slots * a.heads * cells : nullptr;
-    float *sizes = checkpoints ? rhos + (uint64_t)a.tokens * a.heads * a.value_dim : nullptr;
+    float *sizes = checkpoints ? rhos + (uint64_t)a.slots * a.heads * kChunk * a.value_dim : nullptr;
     return with_key_width(a.key_dim, [&](auto w) {
         constexpr int W = decltype(w)::value;
         timing_begin(s);
