@@ -116,7 +116,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArg
 #pragma unroll
                         for (uint32_t j = 0; j < 4u; ++j) {
                             const uint32_t row = 16u * t + 4u * q + j;
-                            o[t][j] = row < rows && col < a.value_dim ? (float)grads[(int64_t)(lo + row) * grads_stride + col] : 0.0f;
+                            o[t][j] = row < rows && col < a.value_dim ? finite_or_nan((float)grads[(int64_t)(lo + row) * grads_stride + col]) : 0.0f;
                         }
                 }
                 tri.load(in.p.scores, lane);
@@ -472,17 +472,17 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-            // k_j k_i or k_j q_i, rows j in the registers, i = own in the lane
-            f32x4 kk[4];
+        // k_j k_i or k_j q_i, rows j in the registers, i = own in the lane
+        f32x4 kk[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) kk[t] = none;
+        for (int t = 0; t < 4; ++t) kk[t] = none;
 #pragma unroll
-            for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
-                const auto b = keys_side ? sh.k.along(own, col + 8u * q) : sh.q.along(own, col + 8u * q);
+        for (uint32_t col = 0; col < (uint32_t)W; col += 32u) {
+            const auto b = keys_side ? sh.k.along(own, col + 8u * q) : sh.q.along(own, col + 8u * q);
 #pragma unroll
-                for (uint32_t t = 0; t < 4u; ++t)
-                    if (t <= own_tile) mma(kk[t], sh.k.along(16u * t + n, col + 8u * q), b);
-            }
+            for (uint32_t t = 0; t < 4u; ++t)
+                if (t <= own_tile) mma(kk[t], sh.k.along(16u * t + n, col + 8u * q), b);
+        }
         // the triangles become dqk or dkk with the factors of what they meet, and
         // the pairs' sums of z
         const double G_own = sh.sum[own];

@@ -168,7 +168,6 @@ template <class T>
 struct Form {
     typedef uint16_t Word;
     static constexpr bool scaled = true;
-    static constexpr int pad = 8;
     typedef Planes<1> In;
     typedef Planes<2> Mid;
 };
@@ -176,7 +175,6 @@ template <>
 struct Form<float> {
     typedef float Word;
     static constexpr bool scaled = false;
-    static constexpr int pad = 4;
     typedef Wide In;
     typedef Wide Mid;
 };
@@ -184,7 +182,8 @@ struct Form<float> {
 // A power of two that brings numbers up to `most` to 2^14 .. 2^15, and its
 // reciprocal.  Numbers below 2^least are left small: a product's scale is that
 // of both operands, and what is added to it has to stay in fp32's range (least
-// -60 for one and -20 for the other leave it 2^17).
+// -60 for one and -20 for the other leave it 2^17).  Of numbers with an infinity
+// among them no power of two keeps the others: the scale is NaN, and so are they.
 struct Scale {
     float by, back;
 };
@@ -193,8 +192,12 @@ __device__ __forceinline__ Scale scale_of(float most) {
     if (!scaled) return {1.0f, 1.0f};
     // exponents as they stand in the words: 2^14 over the largest's
     const uint32_t e = __builtin_bit_cast(uint32_t, __builtin_fmaxf(most, __builtin_ldexpf(1.0f, least))) & 0x7F800000u;
-    return {__builtin_bit_cast(float, (268u << 23) - e), __builtin_bit_cast(float, e - (14u << 23))};
+    const uint32_t by = e == 0x7F800000u ? 0x7FC00000u : (268u << 23) - e;
+    return {__builtin_bit_cast(float, by), __builtin_bit_cast(float, e - (14u << 23))};
 }
+// NaN for an infinity: a column that holds one has no finite result, and its
+// neighbours, which share its scale, keep theirs.
+__device__ __forceinline__ float finite_or_nan(float v) { return __builtin_fmaf(v, 0.0f, v); }
 // The same for terms that are added to numbers up to `held`, which take the
 // scale with them and must not leave fp32's range for small terms.
 template <bool scaled>
@@ -425,7 +428,7 @@ __device__ __forceinline__ void load_states(f32x4 (&S)[TILES], const float *from
         if (!from || row >= rows || col >= width) continue;
 #pragma unroll
         for (uint32_t i = 0; i < 4u; ++i)
-            if (E || row + i < rows) S[t][i] = from[(row + i) * width + col];
+            if (E || row + i < rows) S[t][i] = finite_or_nan(from[(row + i) * width + col]);
     }
 }
 // The width is hidden from the compiler where it stores: it would keep the

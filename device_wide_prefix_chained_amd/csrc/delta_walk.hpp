@@ -36,10 +36,10 @@ __device__ __forceinline__ f32x4 value_rows(const T (&tile)[kChunk][STRIDE], uin
         const i16x4 raw = read_transposed(
             reinterpret_cast<const uint16_t *>(&tile[16u * t + 4u * q + (m >> 2)][here + 4u * (m & 3u)]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)__builtin_bit_cast(T, (uint16_t)raw[i]);
+        for (int i = 0; i < 4; ++i) v[i] = finite_or_nan((float)__builtin_bit_cast(T, (uint16_t)raw[i]));
     } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; ++i) v[i] = (float)tile[16u * t + 4u * q + i][here + m];
+        for (uint32_t i = 0; i < 4u; ++i) v[i] = finite_or_nan((float)tile[16u * t + 4u * q + i][here + m]);
     }
     return v;
 }
@@ -319,7 +319,9 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, 
 #pragma unroll
                     for (uint32_t i = 0; i < 4u; ++i) {
                         const uint32_t row = 16u * t + 4u * q + i;
-                        v[t][i] = row < rows && col < a.value_dim && !unit ? (float)values[(int64_t)(lo + row) * a.v_stride + col] : 0.0f;
+                        v[t][i] = row < rows && col < a.value_dim && !unit
+                                      ? finite_or_nan((float)values[(int64_t)(lo + row) * a.v_stride + col])
+                                      : 0.0f;
                     }
             }
             Triangle<Mid> tri;
@@ -456,7 +458,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
     f32x4 S[NC][CT][2], N[NC][CT][2];
     auto load = [&](f32x4 (&to)[NC][CT][2], const float *from) {
         each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool is, uint32_t at) {
-            to[k][ct][h][i] = from && is ? from[at] : 0.0f;
+            to[k][ct][h][i] = from && is ? finite_or_nan(from[at]) : 0.0f;
         });
     };
     Mid mat[NC][2][kKeys];

@@ -702,9 +702,13 @@ ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, fl
  * Sequences are worked on in chunks of 64 rows from their first row on, so a
  * sequence's results do not depend on what is packed beside it.  With bf16 and
  * fp16 activations the products of numbers that the call computes (states,
- * corrections) are off by at most 2^-17 of a term's size; sums, and states from
- * chunk to chunk, are fp32.  A NaN or an infinity in a row reaches its
- * sequence's rows after it and those of its chunk before it.
+ * corrections) are off by at most 2^-22 of a term's size where that is not below
+ * 2^-17 of the largest beside it (2^-39 of that largest below), and bf16 keys and
+ * queries below 2^-21 of their row's largest lose bits; sums, and states from
+ * chunk to chunk, are fp32.  A NaN or an infinity in a row (they are not told
+ * apart) reaches its sequence's rows after it and may reach those of its chunk
+ * before it, in its head, and from v or initial in its column; which of that
+ * sequence's gradients are numbers then is not said.
  * PS_ERR_SIZE also: dimensions outside 1..PS_DELTA_MAX_DIM, heads outside
  * 1..PS_DELTA_MAX_HEADS or no multiple of kheads, (tokens / 64 + num_seqs) *
  * heads (single tokens: tokens * heads) of 2^31 or more. */
@@ -746,7 +750,8 @@ typedef struct ps_delta_grads {
 ps_status ps_gated_delta_bwd(void *ws, size_t *ws_bytes, const ps_delta_input *in, const void *dout, const float *dfinal,
                              const float *checkpoints, const ps_delta_grads *grads, void *stream);
 /* One token for each of in->tokens rows, with state and new_state [pool,
- * heads, key_dim, value_dim] in fp32; slots as in ps_causal_conv_step.
+ * heads, key_dim, value_dim] in fp32; slots as in ps_causal_conv_step (of rows
+ * with the same slot each reads and writes it at a time of its own).
  * in->offsets, in->initial and in->num_seqs are not used. */
 ps_status ps_gated_delta_step(const ps_delta_input *in, const float *state, float *new_state, const int32_t *slots,
                               uint32_t pool, void *out, void *stream);

@@ -13,9 +13,11 @@ and N_c in the columns' place.
 Roundings of a chunk: eight products on the way of a value (k S, the inverse
 and its blocks, its product with what is left, beta, the scores' two products,
 k^T u), each off by `eps` of its terms' lengths, times up to 4 for the length of
-the inverse (1 + a diag(beta))^-1.  eps is 2^-17 where products take two bf16
-planes of a number (2^-18 for the number, 2^-18 for the product of the last
-planes); in fp32 products sum up to key_dim + 64 terms, each off by 2^-24."""
+the inverse (1 + a diag(beta))^-1.  eps is 2^-17 where products take two fp16
+planes of a number, which hold it to 2^-22 if it is 2^-17 or more of the largest
+of its tiles and to 2^-39 of that largest otherwise: 64 and more such terms of a
+column are off by less than 2^-17 of its length.  In fp32 products sum up to
+key_dim + 64 terms, each off by 2^-24."""
 from __future__ import annotations
 
 import torch
