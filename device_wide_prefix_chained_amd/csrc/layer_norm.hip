@@ -42,14 +42,17 @@ __device__ __forceinline__ void row_sums_of(float (&v)[n], float (*shared)[kMost
     }
 }
 
-// R rows at once: their loads are on their way together.  A workgroup has 256 / G
-// rows R times (G 0: one row, blockDim.x threads with K times 8 channels each).
+// R rows at once: their loads are on their way together, and G 0 has a barrier
+// for all their sums.  A workgroup has 256 / G rows R times (G 0: R rows,
+// blockDim.x threads with K times 8 channels each).  16384 rows of 4096 channels
+// in bf16: 48 us, 5.6 TB/s, with 2 rows (1 row 52, 4 rows 50; 3 rows in all: 2.9
+// us, 2.4 with 1); 131072 rows of 128: 11 to 14 us.
 template <class T, int G, int K, int R>
 __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_kernel(LayerArgs a, uint32_t first,
                                                                               T *__restrict__ out) {
     constexpr int V = kVec;
     constexpr uint32_t kRows = G ? 256u / (G ? G : 1) : 1u;
-    __shared__ float sh[2][1][kMostWaves];
+    __shared__ float sh[2][R][kMostWaves];
     const uint32_t lane = G ? threadIdx.x % (G ? G : 1) : threadIdx.x, lanes = G ? G : blockDim.x;
     const int64_t C = a.channels, t0 = (int64_t)(first + blockIdx.x) * (kRows * R) + (G ? threadIdx.x / (G ? G : 1) : 0u);
     float x[R][K][V], w[K][V], b[K][V];
@@ -66,25 +69,32 @@ __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_kernel(L
         load_n<float, V>(w[k], at_col(a.weight, c), have[k], 1.0f);
         load_n<float, V>(b[k], at_col(a.bias, c), have[k], 0.0f);
     }
+    float sum[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float sum[1] = {0.0f};
+        sum[i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum[0] += x[i][k][j];
-        row_sums_of<G, 1>(sum, sh[0]);
-        const float mean = sum[0] / a.count;
-        sum[0] = 0.0f;
+            for (int j = 0; j < V; ++j) sum[i] += x[i][k][j];
+    }
+    row_sums_of<G, R>(sum, sh[0]);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float mean = sum[i] / a.count;
+        sum[i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 x[i][k][j] = (uint32_t)j < have[k] ? x[i][k][j] - mean : 0.0f;
-                sum[0] = __builtin_fmaf(x[i][k][j], x[i][k][j], sum[0]);
+                sum[i] = __builtin_fmaf(x[i][k][j], x[i][k][j], sum[i]);
             }
-        row_sums_of<G, 1>(sum, sh[1]);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps));
+    }
+    row_sums_of<G, R>(sum, sh[1]);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[i], a.inv, a.eps));
         const int64_t t = t0 + i * kRows;
         if (t >= (int64_t)a.tokens) break;
 #pragma unroll
@@ -98,7 +108,8 @@ __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_kernel(L
 
 // A workgroup takes every gridDim.x-th set of rows, the next one's loads on
 // their way (WHOLE: rows of whole vectors), and keeps its sums over rows in
-// registers; part[workgroup][dweight, dbias][channel].
+// registers; part[workgroup][dweight, dbias][channel].  8192 rows of 5120
+// channels in bf16: 57 us, 4.4 TB/s: the next row's loads wait for two barriers.
 template <class T, int G, int K, bool WHOLE>
 __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_bwd_kernel(LayerArgs a, const T *__restrict__ dout,
                                                                                   T *__restrict__ dx, float *__restrict__ part,
@@ -204,19 +215,22 @@ __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_bwd_kern
     }
 }
 
-__global__ __launch_bounds__(256) void layer_params_kernel(const float *__restrict__ part, uint32_t rows, uint32_t channels,
-                                                           float *__restrict__ dweight, float *__restrict__ dbias) {
-    __shared__ float s[4][64];
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t cols = 2u * channels, col = blockIdx.x * 64u + lane;
-    float v = col < cols ? column_sum(part + col, wave, 4u, rows, cols) : 0.0f;
-    s[wave][lane] = v;
+// 16 columns a workgroup, so that few channels too are summed by many: 128
+// channels of 1024 workgroups 3.9 us, with 64 columns a workgroup of 4 waves 12.6.
+__global__ __launch_bounds__(1024) void layer_params_kernel(const float *__restrict__ part, uint32_t rows, uint32_t channels,
+                                                            float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ float s[64][17];
+    const uint32_t lane = threadIdx.x & 15u, set = threadIdx.x >> 4;
+    const uint32_t cols = 2u * channels, col = blockIdx.x * 16u + lane;
+    s[set][lane] = col < cols ? column_sum(part + col, set, 64u, rows, cols) : 0.0f;
     __syncthreads();
-    if (wave == 0u && col < cols) {
-        v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
-        float *to = col < channels ? dweight : dbias;
-        if (to) to[col < channels ? col : col - channels] = v;
-    }
+    if (threadIdx.x >= 256u) return;
+    // 16 lanes a column, four sets each
+    const uint32_t c = threadIdx.x >> 4, to_col = blockIdx.x * 16u + c;
+    const float v = row_total((s[lane][c] + s[lane + 16u][c]) + (s[lane + 32u][c] + s[lane + 48u][c]));
+    if (lane || to_col >= cols) return;
+    float *to = to_col < channels ? dweight : dbias;
+    if (to) to[to_col < channels ? to_col : to_col - channels] = v;
 }
 
 // Calls f(lanes a row, or 0 for a workgroup, vectors a thread, threads).
@@ -233,14 +247,21 @@ ps_status with_rows(uint32_t channels, F f) {
     return f(std::integral_constant<int, 0>(), std::integral_constant<int, 2>(), (uint32_t)ceil_div(channels, 2u * wave) * 64u);
 }
 
-// Workgroups that share the rows backwards.
+// Workgroups that share the rows backwards: 16 waves or more a CU where the
+// registers hold them (8192 rows of 5120 channels, 10 waves a workgroup: 72 us
+// with one a CU, 57 with two, 70 with four), and four sets of rows each, down to
+// one a CU: what a workgroup leaves has to be read again (2047 rows of 1537: the
+// sums over workgroups 4.2 us, 6.3 with two sets each, 3.8 with eight, which
+// takes 3 us longer before).
 uint32_t layer_bwd_groups(const ps_layer_input *in) {
     uint32_t groups = 0;
-    with_rows(in->channels, [&](auto lanes, auto, uint32_t threads) {
+    with_rows(in->channels, [&](auto lanes, auto k, uint32_t threads) {
         constexpr uint32_t G = decltype(lanes)::value;
-        const uint32_t each = 1024u / threads, rows = G ? 256u / (G ? G : 1u) : 1u;
-        const uint64_t sets = ceil_div(in->tokens, rows), most = 256u * (each ? each : 1u);
-        groups = (uint32_t)(sets < most ? sets : most);
+        const uint32_t held = (decltype(k)::value == 1 ? 28u : 16u) * 64u / threads, wanted = (uint32_t)ceil_div(1024u, threads);
+        const uint64_t sets = ceil_div(in->tokens, G ? 256u / (G ? G : 1u) : 1u), most = 256u * (wanted < held ? wanted : held);
+        uint64_t n = ceil_div(sets, 4u);
+        if (n < 256u) n = sets < 256u ? sets : 256u;
+        groups = (uint32_t)(n < most ? n : most);
         return PS_OK;
     });
     return groups;
@@ -291,8 +312,8 @@ extern "C" ps_status ps_layer_norm(const ps_layer_input *in, void *out, void *st
     return with_type(in->dtype, [&](auto zero) {
         using T = decltype(zero);
         return with_rows(in->channels, [&](auto lanes, auto k, uint32_t threads) {
-            constexpr int G = decltype(lanes)::value, R = G ? 4 : 1;
-            constexpr uint32_t rows = G ? 256u / (G ? G : 1) * R : 1u;
+            constexpr int G = decltype(lanes)::value, R = G ? 4 : 2;
+            constexpr uint32_t rows = G ? 256u / (G ? G : 1) * R : R;
             timing_begin(s);
             launch_in_parts(ceil_div(in->tokens, rows), 1u, threads, [&](uint32_t first, uint32_t grid) {
                 hipLaunchKernelGGL((layer_norm_kernel<T, G, decltype(k)::value, R>), dim3(grid), dim3(threads), 0, s, a, first,
@@ -338,7 +359,7 @@ extern "C" ps_status ps_layer_norm_bwd(void *ws, size_t *ws_bytes, const ps_laye
             if (groups && in->channels % kVec == 0u) launch(std::true_type());
             else if (groups) launch(std::false_type());
             if (dweight || dbias)
-                hipLaunchKernelGGL(layer_params_kernel, dim3((uint32_t)ceil_div(2u * in->channels, 64)), dim3(256), 0, s, part,
+                hipLaunchKernelGGL(layer_params_kernel, dim3((uint32_t)ceil_div(2u * in->channels, 16)), dim3(1024), 0, s, part,
                                    groups, in->channels, dweight, dbias);
             timing_end(s);
             return launch_status();
