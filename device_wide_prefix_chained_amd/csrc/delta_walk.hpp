@@ -423,8 +423,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, 
 // NULL.  A workgroup has 32 columns, a wave 32 keys of them (W 256: 64), so that
 // a step is short: every wave leaves its keys as operands in shared memory, and
 // multiplies its rows of M, which arrived while the step before was worked on.
-// 15 steps of 16 heads, 128 x 128: LINK_US us; a wave with all keys of 16 columns
-// 85 us, with M as rows of numbers 138 us.
+// Bound by a step's chain of loads, products and a barrier, 2.4 us: 15 steps of
+// 16 heads, 128 x 128, 36 to 44 us; with a wave for all keys of 16 columns 85 us,
+// and M as rows of numbers 138 us.  Nothing is done to N as it arrives, or the
+// step before would wait for it (80 us).
 template <class T, int W, bool E, bool BACK>
 __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
     f32x4 S[NC][CT][2], N[NC][CT][2];
     auto load = [&](f32x4 (&to)[NC][CT][2], const float *from) {
         each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool is, uint32_t at) {
-            to[k][ct][h][i] = from && is ? finite_or_nan(from[at]) : 0.0f;
+            to[k][ct][h][i] = from && is ? from[at] : 0.0f;
         });
     };
     Mid mat[NC][2][kKeys];
@@ -470,6 +472,7 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
         back[k][h][c] = kScaled ? from.back[t][c] : 1.0f;
     };
     load(S, start ? start + ((uint64_t)s * a.heads + head) * cells : nullptr);
+    each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool, uint32_t) { S[k][ct][h][i] = finite_or_nan(S[k][ct][h][i]); });
     load(N, seg.n + number(0u) * cells);
     if (works)
 #pragma unroll
