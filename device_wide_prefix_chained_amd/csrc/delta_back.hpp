@@ -34,16 +34,17 @@ struct BackResults {
 constexpr uint32_t kBackSizes = 3u * kSizeWaves;
 
 // The walk backwards.  lead: the walks for M and N of segments that are not a
-// sequence's first, which keep nothing but their end.
-template <class T, int W, int NW, bool E>
-__global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+// sequence's first, which keep nothing but their end.  Bound like the walk
+// forwards: 8192 rows of 16 heads, 128 x 128, bf16, 104 us, and 104 for M and N.
+template <class T, int W, bool E>
+__global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_back_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
                                                               Segments seg, const T *__restrict__ dout, bool lead, BackResults to) {
     typedef typename Form<T>::Mid Mid;
     typedef typename Form<T>::In In;
-    typedef WalkTile<T, W, NW> Tile;
+    typedef WalkTile<T, W> Tile;
     constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
-    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
-    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, NW>()];
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W>()];
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = lead ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
@@ -57,12 +58,12 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArg
     const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);
     const T *grads = dout + (uint64_t)head * a.value_dim;
     const int64_t grads_stride = (int64_t)a.heads * a.value_dim;
-    const DeltaFeed<T, W, NW, E> feed = {a, prepared, r, base, head, khead, block0, grads, grads_stride};
+    const DeltaFeed<T, W, E> feed = {a, prepared, r, base, head, khead, block0, grads, grads_stride};
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
-    if (wave >= (uint32_t)NW) {
+    if (wave >= (uint32_t)kWalkWaves) {
         feed.template run<false>(chunks, !unit, tile, [&](uint32_t i) { return chunks - 1u - i; });
         if (unit)
-            store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+            store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
                                    reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_back_kernel(DeltaArg
     }
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (unit) {
-        store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &D, unit_of,
+        store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &D, unit_of,
                                block0, wave, lane, true);
         return;
     }
@@ -254,6 +255,12 @@ struct GradShared {
 // omega rho^T: wave w the columns of tile w & 3 of the lower triangle as it is
 // (five, slots up to w: rows j, columns i) and transposed (slots above: rows
 // i, columns j), so that both are operands as they come.
+// Bound by latency: 108 KB of shared memory and 240 registers leave a CU one
+// workgroup, whose parts wait for one another.  8192 rows of 16 heads, 128 x 128,
+// bf16: 300 us for 364 MB, of which start and end 80, the sums over columns 136,
+// the triangles 83; in half the registers it spills (596 us).  SOLO, heads that
+// share no keys, adds up nothing over heads (27 us
+// more with the sums).
 template <class T, int W, bool E, bool SOLO>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
                                                           const float *__restrict__ states, const float *__restrict__ rhos,
@@ -696,8 +703,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
     PlainWs plan;
     const size_t prepared_at = plan.take((size_t)a.slots * a.heads * sizeof(Prepared<T>));
     Segments seg{};
-    const bool wide = a.key_dim <= 128u && a.value_dim > 64u;
-    seg.shift = segment_shift(a, wide ? 128u : 64u);
+    seg.shift = segment_shift(a);
     const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u, state_floats = (uint64_t)a.slots * a.heads * cells;
     const size_t m_at = plan.take(linked * matrix_bytes<T>(a.key_dim)), n_at = plan.take(linked * cells * 4u);
@@ -737,13 +743,12 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
             hipLaunchKernelGGL((delta_prepare_kernel<T, W, true>), dim3(grid), dim3(256), 0, s, a, first, prepared,
                                ws_counter(ws), plan.words());
         });
-        auto walk = [&](auto waves, auto eights) {
-            constexpr int NW = decltype(waves)::value;
+        auto walk = [&](auto eights) {
             constexpr bool E = decltype(eights)::value;
-            const uint64_t blocks = ceil_div(a.value_dim, 16u * NW), all = blocks + ceil_div(a.key_dim, 16u * NW);
+            const uint64_t blocks = ceil_div(a.value_dim, 16u * kWalkWaves), all = blocks + ceil_div(a.key_dim, 16u * kWalkWaves);
             if (linked) {
-                launch_in_parts(segments * a.heads, all, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_walk_back_kernel<T, W, NW, E>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a, first, prepared,
+                launch_in_parts(segments * a.heads, all, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_back_kernel<T, W, E>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a, first, prepared,
                                        seg, g, true, to);
                 });
                 const uint64_t columns = ceil_div(a.value_dim, 32u);
@@ -751,8 +756,8 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                     hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(256), 0, s, a, first, seg, dfinal);
                 });
             }
-            launch_in_parts(segments * a.heads, blocks, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_walk_back_kernel<T, W, NW, E>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a, first, prepared, seg,
+            launch_in_parts(segments * a.heads, blocks, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_back_kernel<T, W, E>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a, first, prepared, seg,
                                    g, false, to);
             });
             launch_in_parts((uint64_t)a.slots * a.kheads, 1u, 512u, [&](uint32_t first, uint32_t grid) {
@@ -766,12 +771,8 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
             });
         };
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
-        auto shape = [&](auto e) {
-            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 8 : 4>(), e);
-            else walk(std::integral_constant<int, 4>(), e);
-        };
-        if (eights) shape(std::true_type());
-        else shape(std::false_type());
+        if (eights) walk(std::true_type());
+        else walk(std::false_type());
         timing_end(s);
         return launch_status();
     });

@@ -2,8 +2,8 @@
 // over chunks, and their launches.  One type of activations a source file.
 //
 // Every chunk of 64 rows is prepared by itself (delta_block.hpp).  Then a
-// workgroup walks over a sequence's chunks with 64 or 128 columns of a head's
-// state in its registers; long sequences in segments side by side, for which
+// workgroup walks over a sequence's chunks with 64 columns of a head's state in its
+// registers; long sequences in segments side by side, for which
 // two walks and a link first find the states that enter them.
 #pragma once
 
@@ -12,20 +12,26 @@
 namespace dwps {
 namespace {
 
+// Waves of a workgroup that walk, with 16 columns each; four more feed them.  With
+// eight, a chunk's keys are read once for 128 columns, but the eight wait for one
+// another at more barriers: 453 us in place of 422 for 16384 rows of 16 heads, 128
+// x 128, bf16, 869 in place of 849 for a training step of 8192.
+constexpr int kWalkWaves = 4;
+
 // What a step of a walk reads: a chunk's keys, queries and values, and what was
 // prepared of it.
-template <class T, int W, int NW>
+template <class T, int W>
 struct WalkTile {
-    static constexpr uint32_t kCols = 16u * NW;
+    static constexpr uint32_t kCols = 16u * kWalkWaves;
     KeyTile<T, W> k, q;
     Prepared<T> p;
     T v[kChunk][kCols + 8u];
 };
-template <class T, int W, int NW>
-constexpr bool kValuesFit = sizeof(WalkTile<T, W, NW>) <= kMostShared;
-template <class T, int W, int NW>
+template <class T, int W>
+constexpr bool kValuesFit = sizeof(WalkTile<T, W>) <= kMostShared;
+template <class T, int W>
 constexpr size_t walk_tile_bytes() {
-    return kValuesFit<T, W, NW> ? sizeof(WalkTile<T, W, NW>) : sizeof(WalkTile<T, W, NW>) - sizeof(WalkTile<T, W, NW>::v);
+    return kValuesFit<T, W> ? sizeof(WalkTile<T, W>) : sizeof(WalkTile<T, W>) - sizeof(WalkTile<T, W>::v);
 }
 
 // Rows 16 t + 4 q + i of column `here` + m of a tile of values.
@@ -62,10 +68,10 @@ struct SegmentMatrix {
 };
 // Columns of M that four waves hold, into operands, by way of shared memory;
 // all eight waves, `walks`: those that hold them.
-template <class T, int W, int NW>
+template <class T, int W>
 __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *shared, const f32x4 (*S)[W / 16], float by,
                                              uint32_t block0, uint32_t wave, uint32_t lane, bool walks) {
-    constexpr uint32_t kCols = 16u * NW, kRow = kCols + 4u;
+    constexpr uint32_t kCols = 16u * kWalkWaves, kRow = kCols + 4u;
     static_assert(W * kRow * 4u <= kMostShared, "a block of M fits shared memory");
     const uint32_t m = lane & 15u, q = lane >> 4;
     if (walks) {
@@ -75,7 +81,7 @@ __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *sha
             for (uint32_t i = 0; i < 4u; ++i) shared[place(t, 4u * q + i) * kRow + wave * 16u + m] = (*S)[t][i] * by;
     }
     __syncthreads();
-    for (uint32_t i = wave; i < W / 16u * (kCols / 32u); i += NW + 4u) {
+    for (uint32_t i = wave; i < W / 16u * (kCols / 32u); i += kWalkWaves + 4u) {
         const uint32_t t = i / (kCols / 32u), c = i % (kCols / 32u);
         if (block0 + 32u * c >= (uint32_t)W) continue;
         const float *p = shared + place(t, m) * kRow + 32u * c + 8u * q;
@@ -97,9 +103,9 @@ struct WalkResults {
 // The feeding waves of a walk: keys, queries, values and what was prepared of
 // each chunk, from memory into registers, a whole chunk's work before they are
 // waited for, then into the tile.
-template <class T, int W, int NW, bool E>
+template <class T, int W, bool E>
 struct DeltaFeed {
-    typedef WalkTile<T, W, NW> Tile;
+    typedef WalkTile<T, W> Tile;
     const DeltaArgs &a;
     const Prepared<T> *prepared;
     Chunk r;
@@ -110,10 +116,10 @@ struct DeltaFeed {
     // LEAD: no queries and no scores.  order(i): the i-th chunk to come.
     template <bool LEAD, class F, class O>
     __device__ __forceinline__ void run(uint32_t chunks, bool with_values, F tile, O order) const {
-        constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
+        constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W>;
         constexpr uint32_t kKeys = W / 32, kVals = Tile::kCols / 32u;
         constexpr uint32_t kBytes = LEAD ? offsetof(Prepared<T>, scores) : sizeof(Prepared<T>), kWords = (kBytes + 4095u) / 4096u;
-        const uint32_t thread = threadIdx.x - 64u * NW, row = thread >> 2, part = (thread & 3u) * 8u;
+        const uint32_t thread = threadIdx.x - 64u * kWalkWaves, row = thread >> 2, part = (thread & 3u) * 8u;
         Pack<T, 8> ks[kKeys], qs[kKeys], vs[kVals];
         u32x4 ps[kWords];
         auto fetch = [&](uint32_t i) {
@@ -228,20 +234,25 @@ __device__ __forceinline__ void mma_keys(f32x4 (&S)[TILES], const Tile &k, uint3
     }
 }
 
-// NW waves walk over a segment's chunks, each with 16 columns of a head's state;
+// kWalkWaves waves walk over a segment's chunks, each with 16 columns of a head's state;
 // four feed them, leaving a chunk in the tile of the two that is not in use while
 // the one before is worked on (or, where shared memory has room for one, after a
 // barrier in that one).  LEAD: the walks for M and N, of segments that another
 // follows.
-template <class T, int W, int NW, bool E, bool LEAD>
-__global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
+// Bound by the chain of a step, K S, the inverse, U and the state, each of which
+// waits for the one before: 3.1 us with one wave, 5.5 with the eight that share
+// the CU's matrix units and shared memory (16384 rows of 16 heads, 128 x 128,
+// bf16: 179 us, and 133 for M and N).  16 columns a wave: with 32 the states took
+// the registers that the operands of the next product wait in.
+template <class T, int W, bool E, bool LEAD>
+__global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
                                                          Segments seg, WalkResults to) {
     typedef typename Form<T>::Mid Mid;
     typedef typename Form<T>::In In;
-    typedef WalkTile<T, W, NW> Tile;
+    typedef WalkTile<T, W> Tile;
     constexpr uint32_t kTiles = W / 16, kCols = Tile::kCols;
-    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W, NW>;
-    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W, NW>()];
+    constexpr bool kTwo = 2u * sizeof(Tile) <= kMostShared, kV = kValuesFit<T, W>;
+    __shared__ __attribute__((aligned(16))) char memory[kTwo ? 2u * sizeof(Tile) : walk_tile_bytes<T, W>()];
     const uint32_t value_blocks = (a.value_dim + kCols - 1u) / kCols, key_blocks = LEAD ? (a.key_dim + kCols - 1u) / kCols : 0u;
     const uint32_t blocks = value_blocks + key_blocks, block = blockIdx.x % blocks, item = first + blockIdx.x / blocks;
     const uint32_t head = item % a.heads, number = item / a.heads, khead = head / (a.heads / a.kheads);
@@ -255,11 +266,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, 
     const uint32_t base = seq.base + ((r.lo - seq.lo) >> kChunkShift);  // its first chunk's number
     const T *values = static_cast<const T *>(a.v) + (uint64_t)head * a.value_dim;
     auto tile = [&](uint32_t i) { return reinterpret_cast<Tile *>(memory + (kTwo && (i & 1u) ? sizeof(Tile) : 0u)); };
-    const DeltaFeed<T, W, NW, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
-    if (wave >= (uint32_t)NW) {
+    const DeltaFeed<T, W, E> feed = {a, prepared, r, base, head, khead, block0, values, a.v_stride};
+    if (wave >= (uint32_t)kWalkWaves) {
         feed.template run<LEAD>(chunks, !unit, tile, [](uint32_t i) { return i; });
         if (LEAD && unit)
-            store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
+            store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
                                    reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
         return;
     }
@@ -407,7 +418,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void delta_walk_kernel(DeltaArgs a, 
     }
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (LEAD && unit) {
-        store_matrix<T, W, NW>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &S, unit_of,
+        store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &S, unit_of,
                                block0, wave, lane, true);
         return;
     }
@@ -541,7 +552,8 @@ inline size_t matrix_bytes(uint32_t key_dim) {
 // workgroups run at once): a step of a walk 5.5, of the walks for M and N 3.9,
 // the start of either 7, a link 2.2.  Sequences are reckoned to be cut at random:
 // the longest of n is then the mean times 1 + 1/2 + ... + 1/n.
-uint32_t segment_shift(const DeltaArgs &a, uint32_t cols) {
+uint32_t segment_shift(const DeltaArgs &a) {
+    constexpr uint32_t cols = 16u * kWalkWaves;
     const double chunks = (double)ceil_div(a.tokens, kChunk), heads = a.heads, n = a.num_seqs;
     const double value_blocks = (double)ceil_div(a.value_dim, cols), key_blocks = (double)ceil_div(a.key_dim, cols);
     double longest = 0.0;
@@ -572,9 +584,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
     PlainWs plan;
     const size_t prepared_at = plan.take((size_t)a.slots * a.heads * sizeof(Prepared<T>));
     Segments seg{};
-    // 32 columns a wave where there are more than 64, and registers for their states
-    const bool wide = a.key_dim <= 128u && a.value_dim > 64u;
-    seg.shift = segment_shift(a, wide ? 128u : 64u);
+    seg.shift = segment_shift(a);
     const uint64_t segments = chunk_slots(a.tokens, a.num_seqs, seg.shift), cells = (uint64_t)a.key_dim * a.value_dim;
     const uint64_t linked = seg.shift < 31u ? segments * a.heads : 0u;
     const size_t m_at = plan.take(linked * matrix_bytes<T>(a.key_dim)), n_at = plan.take(linked * cells * 4u);
@@ -604,13 +614,12 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
         });
         seg.m = ws_at<void *>(ws, m_at), seg.n = ws_at<float>(ws, n_at);
         const WalkResults to = {out, final, checkpoints, rhos, sizes};
-        auto walk = [&](auto waves, auto eights) {
-            constexpr int NW = decltype(waves)::value;
+        auto walk = [&](auto eights) {
             constexpr bool E = decltype(eights)::value;
-            const uint64_t blocks = ceil_div(a.value_dim, 16u * NW), all = blocks + ceil_div(a.key_dim, 16u * NW);
+            const uint64_t blocks = ceil_div(a.value_dim, 16u * kWalkWaves), all = blocks + ceil_div(a.key_dim, 16u * kWalkWaves);
             if (linked) {
-                launch_in_parts(segments * a.heads, all, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_walk_kernel<T, W, NW, E, true>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a,
+                launch_in_parts(segments * a.heads, all, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_walk_kernel<T, W, E, true>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a,
                                        first, prepared, seg, to);
                 });
                 const uint64_t columns = ceil_div(a.value_dim, 32u);
@@ -619,18 +628,16 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                                        a.initial);
                 });
             }
-            launch_in_parts(segments * a.heads, blocks, 64u * (NW + 4), [&](uint32_t first, uint32_t grid) {
-                hipLaunchKernelGGL((delta_walk_kernel<T, W, NW, E, false>), dim3(grid), dim3(64 * (NW + 4)), 0, s, a,
+            launch_in_parts(segments * a.heads, blocks, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {
+                hipLaunchKernelGGL((delta_walk_kernel<T, W, E, false>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a,
                                    first, prepared, seg, to);
             });
         };
+        // rows of whole vectors of 8 have no bounds within one: 453 us, and 965 for
+        // the same rows with bounds for every number
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
-        auto shape = [&](auto e) {
-            if (W <= 128 && wide) walk(std::integral_constant<int, W <= 128 ? 8 : 4>(), e);
-            else walk(std::integral_constant<int, 4>(), e);
-        };
-        if (eights) shape(std::true_type());
-        else shape(std::false_type());
+        if (eights) walk(std::true_type());
+        else walk(std::false_type());
         timing_end(s);
         return launch_status();
     });

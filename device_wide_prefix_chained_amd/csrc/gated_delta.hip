@@ -61,7 +61,8 @@ namespace {
 // A workgroup has `cols` columns of one head's state, four a thread and up to
 // kStepRows rows of them: the state is read once, held in registers, and
 // written once.  out = scale (e S^T q + (k q) u) needs no second sum over the
-// new state.  Bound by memory: the state's 8 bytes an element.
+// new state.  Bound by memory, the state's 8 bytes an element: 256 rows of 16
+// heads, 128 x 128, 130 us, 4.2 TB/s (with 64 columns a workgroup 154 us).
 constexpr uint32_t kStepRows = 16u, kStepThreads = 512u;
 
 template <class T>
