@@ -549,7 +549,7 @@ inline size_t matrix_bytes(uint32_t key_dim) {
 
 // Rows of a segment, as a shift: as many as take the least time by what the
 // parts of a call were measured to take (us; 128 keys and columns, where 256
-// workgroups run at once): a step of a walk 5.5, of the walks for M and N 3.9,
+// workgroups run at once): a step of a walk 4.3, of the walks for M and N 2.7,
 // the start of either 7, a link 2.2.  Sequences are reckoned to be cut at random:
 // the longest of n is then the mean times 1 + 1/2 + ... + 1/n.
 uint32_t segment_shift(const DeltaArgs &a) {
@@ -562,14 +562,14 @@ uint32_t segment_shift(const DeltaArgs &a) {
     longest = longest > chunks ? chunks : longest;
     auto rounds = [](double groups) { return groups > 256.0 ? groups / 256.0 : 1.0; };
     const double work = (chunks + 0.5 * (n - 1.0)) * heads * value_blocks / 256.0;
-    double best = 7.0 + 5.5 * (longest > work ? longest : work);
+    double best = 7.0 + 4.3 * (longest > work ? longest : work);
     uint32_t shift = 31u;
     for (uint32_t by = 2u; by <= 7u; ++by) {
         const double rows = (double)(1u << by), segments = __builtin_ceil(chunks / rows) + 0.5 * (n - 1.0);
         if (longest < 2.0 * rows) break;
         const double led = segments > n ? segments - n : 1.0;
-        const double cost = rounds(segments * heads * value_blocks) * (7.0 + 5.5 * rows) +
-                            rounds(led * heads * (value_blocks + key_blocks)) * (7.0 + 3.9 * rows) + 2.2 * longest / rows + 6.0;
+        const double cost = rounds(segments * heads * value_blocks) * (7.0 + 4.3 * rows) +
+                            rounds(led * heads * (value_blocks + key_blocks)) * (7.0 + 2.7 * rows) + 2.2 * longest / rows + 6.0;
         if (cost < best) best = cost, shift = kChunkShift + by;
     }
     return shift;
