@@ -240,10 +240,10 @@ __device__ __forceinline__ void mma_keys(f32x4 (&S)[TILES], const Tile &k, uint3
 // barrier in that one).  LEAD: the walks for M and N, of segments that another
 // follows.
 // Bound by the chain of a step, K S, the inverse, U and the state, each of which
-// waits for the one before: 3.1 us with one wave, 5.5 with the eight that share
-// the CU's matrix units and shared memory (16384 rows of 16 heads, 128 x 128,
-// bf16: 179 us, and 133 for M and N).  16 columns a wave: with 32 the states took
-// the registers that the operands of the next product wait in.
+// waits for the one before: 3.1 us with one wave, 4.3 with the four that share the
+// CU's matrix units and shared memory.  8192 rows of 16 heads, 128 x 128, bf16, in
+// one sequence: 75 us, and 90 for M and N.  16 columns a wave: with 32 the states
+// took the registers that the operands of the next product wait in.
 template <class T, int W, bool E, bool LEAD>
 __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(DeltaArgs a, uint32_t first, const Prepared<T> *__restrict__ prepared,
                                                          Segments seg, WalkResults to) {
@@ -434,8 +434,8 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
 // NULL.  A workgroup has 32 columns, a wave 32 keys of them (W 256: 64), so that
 // a step is short: every wave leaves its keys as operands in shared memory, and
 // multiplies its rows of M, which arrived while the step before was worked on.
-// Bound by a step's chain of loads, products and a barrier, 2.4 us: 15 steps of
-// 16 heads, 128 x 128, 36 to 44 us; with a wave for all keys of 16 columns 85 us,
+// Bound by a step's chain of loads, products and a barrier, 2.4 to 2.9 us: 15 steps
+// of 16 heads, 128 x 128, 36 to 44 us; with a wave for all keys of 16 columns 85 us,
 // and M as rows of numbers 138 us.  Nothing is done to N as it arrives, or the
 // step before would wait for it (80 us).
 template <class T, int W, bool E, bool BACK>
