@@ -315,7 +315,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                 const uint32_t key = 16u * (tile0 + d) + n, col = v0 + 8u * q;
                 const bool there = key < a.key_dim && col < a.value_dim;
                 const uint32_t at = there ? key * a.value_dim + col : 0u;
-                if (E) {
+                if (E || (there && col + 8u <= a.value_dim)) {
                     const Pack<float, 8> ps = *reinterpret_cast<const Pack<float, 8> *>(state + at);
                     const Pack<float, 8> pg = *reinterpret_cast<const Pack<float, 8> *>(dstate + at);
 #pragma unroll
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             const bool there = row < rows && v0 + part < a.value_dim;
             const uint64_t at = there ? at_row + v0 + part : ((uint64_t)c.lo * a.heads + head) * a.value_dim;
             const uint64_t kept = of_head * kChunk * a.value_dim + (there ? row * a.value_dim + v0 + part : 0u);
-            if (E) {
+            if (E || (there && v0 + part + 4u <= a.value_dim)) {
                 next_rho = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(rhos + kept));
                 next_omega = __builtin_bit_cast(f32x4, *reinterpret_cast<const Pack<float, 4> *>(omega + kept));
                 const Pack<T, 4> o = *reinterpret_cast<const Pack<T, 4> *>(dout + at);
@@ -383,9 +383,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                 Pack<T, 4> w;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w.v[i] = (T)(own_beta * next_omega[i]);
-                if (E) {
-                    if (v0 + part < a.value_dim) *reinterpret_cast<Pack<T, 4> *>(p) = w;
-                } else {
+                if (E ? v0 + part < a.value_dim : v0 + part + 4u <= a.value_dim) {
+                    *reinterpret_cast<Pack<T, 4> *>(p) = w;
+                } else if (!E) {
 #pragma unroll
                     for (uint32_t i = 0; i < 4u; ++i)
                         if (v0 + part + i < a.value_dim) p[i] = w.v[i];

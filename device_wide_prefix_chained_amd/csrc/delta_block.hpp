@@ -352,6 +352,8 @@ __device__ __forceinline__ Pack<T, 8> raw8(const T *row, const T *any, bool is, 
         if (!there)
 #pragma unroll
             for (int j = 0; j < 8; ++j) r.v[j] = (T)0.0f;
+    } else if (is && c + 8u <= width) {
+        r = *reinterpret_cast<const Pack<T, 8> *>(row + c);
     } else {
 #pragma unroll
         for (uint32_t j = 0; j < 8u; ++j) r.v[j] = is && c + j < width ? row[c + j] : (T)0.0f;

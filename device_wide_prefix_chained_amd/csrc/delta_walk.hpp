@@ -633,8 +633,8 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                                    first, prepared, seg, to);
             });
         };
-        // rows of whole vectors of 8 have no bounds within one: 453 us, and 965 for
-        // the same rows with bounds for every number
+        // rows of whole vectors of 8 have no bounds within one: 8192 rows of 16 heads,
+        // 128 keys, bf16, with checkpoints 271 us for 128 columns, 358 for 124
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
         if (eights) walk(std::true_type());
         else walk(std::false_type());
