@@ -461,3 +461,52 @@ def test_rows_past_32_bits(dw):
     assert torch.equal(out[-100:], want)
     x = out.view(T * 16, -1)
     assert torch.equal(dw.ps_layer_norm(x)[-1600:], dw.ps_layer_norm(x[-1600:].contiguous()))
+
+
+@pytest.mark.parametrize("heads", [80, 160])
+def test_many_workgroups_of_sequences_that_differ(dw, heads):
+    """More walks than run at once, of lengths that differ: every sequence gives
+    the same bits as by itself, empty and equally long ones too."""
+    m = DeltaMaker(37 + heads, BF16)
+    cuts = [3, 3, 20, 60, 60, 190, 207, 247, 247]
+    T = 260
+    a, more = delta_inputs(m, T, heads // 4, heads, 16, 8, True, True, len(cuts) - 1)
+    dout = m.act(T, heads, 8, packed=True)
+    kept = lambda n, s: torch.empty(dw.ps_gated_delta_checkpoint_floats(n, s, heads, 16, 8), device="cuda")  # noqa: E731
+    say("sequences that differ", heads)
+    c, final = kept(T, len(cuts) - 1), torch.empty_like(more["initial"])
+    out = dw.ps_gated_delta(**a, **more, offsets=_offsets(cuts), checkpoints=c, final=final)
+    g = dw.ps_gated_delta_bwd(**a, **more, offsets=_offsets(cuts), dout=dout, checkpoints=c, dfinal=final)
+    for s, (lo, hi) in enumerate(zip(cuts, cuts[1:])):
+        if lo == hi:
+            assert torch.equal(final[s], more["initial"][s]) and torch.equal(g.dinitial[s], final[s])
+            continue
+        one = {k: v[lo:hi] for k, v in a.items()}
+        how = dict(normalize=True, initial=more["initial"][s:s + 1].contiguous())
+        c1, f1 = kept(hi - lo, 1), torch.empty(1, heads, 16, 8, device="cuda")
+        assert torch.equal(dw.ps_gated_delta(**one, **how, checkpoints=c1, final=f1), out[lo:hi])
+        g1 = dw.ps_gated_delta_bwd(**one, **how, dout=dout[lo:hi], checkpoints=c1, dfinal=f1)
+        assert torch.equal(f1[0], final[s]) and torch.equal(g1.dinitial[0], g.dinitial[s])
+        for name in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(getattr(g1, name), getattr(g, name)[lo:hi]), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+def test_nan_outside_all_sequences_is_not_read(dw, dtype):
+    """Rows before the first sequence and behind the last hold NaN, gates and
+    gradients too; the sequences' results have none."""
+    m = DeltaMaker(38, dtype)
+    T, lo, hi = 150, 5, 140
+    a, more = delta_inputs(m, T, 1, 2, 24, 12, True, True, 2)
+    dout = m.act(T, 2, 12, packed=True)
+    for t in (*a.values(), dout):
+        t[:lo], t[hi:] = float("nan"), float("nan")
+    off = _offsets([lo, 75, hi])
+    say("NaN outside all sequences", dtype)
+    kept = torch.empty(dw.ps_gated_delta_checkpoint_floats(T, 2, 2, 24, 12), device="cuda")
+    out, final = torch.full((T, 2, 12), 7.0, dtype=dtype, device="cuda"), torch.empty_like(more["initial"])
+    dw.ps_gated_delta(**a, **more, offsets=off, checkpoints=kept, out=out, final=final)
+    g = dw.ps_gated_delta_bwd(**a, **more, offsets=off, dout=dout, checkpoints=kept, dfinal=final)
+    assert (out[:lo] == 7.0).all() and (out[hi:] == 7.0).all()
+    for t in (out[lo:hi], final, g.dinitial, *(t[lo:hi] for t in g[:5])):
+        assert torch.isfinite(t).all()
