@@ -412,7 +412,9 @@ __device__ __forceinline__ float fill_rows(KeyTile<T, W> &tile, const void *from
 #pragma unroll
     for (uint32_t c = 0; c < kVecs; ++c)
         if (part + kStep * c < (uint32_t)W) tile.put(row, part + kStep * c, v[c], s.by);
-    const float by = a.unit ? 1.0f / __builtin_sqrtf(neighbours_sum<PER>(sum) + a.eps) : 1.0f;
+    const float squares = neighbours_sum<PER>(sum);
+    // 1 for a row that is not there, also where eps is 0
+    const float by = a.unit && row < rows ? 1.0f / __builtin_sqrtf(squares + a.eps) : 1.0f;
     if (raw) *raw = by;
     return by * s.back;
 }

@@ -179,7 +179,8 @@ __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_bwd_kern
                 sum[1] = __builtin_fmaf(weight[k][j] * g[k][j], x[k][j], sum[1]);
             }
         row_sums_of<G, 2>(sum, sh[1]);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps)), tilt = sum[1] * a.inv * r * r;
+        // 0 for a row that is not there, also where eps is 0
+        const float r = there ? __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], a.inv, a.eps)) : 0.0f, tilt = sum[1] * a.inv * r * r;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll

@@ -9,6 +9,7 @@ import torch
 
 import block_ref
 import delta_ref as ref
+import layer_ref
 from gpu_util import require_gpu, say
 from test_gpu_block import Maker, _offsets
 from test_gpu_delta import BF16, F16, F32, DeltaMaker, delta_inputs
@@ -510,3 +511,31 @@ def test_nan_outside_all_sequences_is_not_read(dw, dtype):
     assert (out[:lo] == 7.0).all() and (out[hi:] == 7.0).all()
     for t in (out[lo:hi], final, g.dinitial, *(t[lo:hi] for t in g[:5])):
         assert torch.isfinite(t).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+def test_eps_zero(dw, dtype):
+    """eps 0 with rows that are no zeros: chunks and sets of rows that are partly
+    filled divide nothing by the lengths of rows that are not there."""
+    m = DeltaMaker(39, dtype)
+    T, cuts = 90, [0, 3, 90]
+    a, more = delta_inputs(m, T, 1, 2, 24, 12, True, True, 2)
+    dout = m.act(T, 2, 12, packed=True)
+    say("eps zero", dtype)
+    off = _offsets(cuts)
+    kept = torch.empty(dw.ps_gated_delta_checkpoint_floats(T, 2, 2, 24, 12), device="cuda")
+    out, final = torch.empty_like(dout), torch.empty_like(more["initial"])
+    dw.ps_gated_delta(**a, **more, eps=0.0, offsets=off, checkpoints=kept, out=out, final=final)
+    g = dw.ps_gated_delta_bwd(**a, **more, eps=0.0, offsets=off, dout=dout, checkpoints=kept)
+    want, bound = ref.delta(**a, **more, eps=0.0, offsets=off, dout=dout, dtype=dtype)
+    ref.close("out", out, want["out"], bound["out"])
+    ref.close("final", final, want["final"], bound["final"])
+    for name in g._fields:
+        ref.close(name, getattr(g, name), want[name], bound[name])
+    for ch in (100, 300, 600):
+        x, d, w = m.act(21, ch), m.act(21, ch), m.par(ch)
+        got = dw.ps_layer_norm_bwd(x, d, w, w, eps=0.0)
+        want, mag = (layer_ref.layer_norm(x, w, w, eps=0.0, dout=d, bound=v) for v in (False, True))
+        for name, t in (("out", dw.ps_layer_norm(x, w, w, eps=0.0)), ("dx", got.dx), ("dweight", got.dweight),
+                        ("dbias", got.dbias)):
+            block_ref.close(name, t, want[name], mag[name], 2 * (ch + 64) + 21)
