@@ -62,8 +62,9 @@ namespace {
 // kStepRows rows of them: the state is read once, held in registers, and
 // written once.  out = scale (e S^T q + (k q) u) needs no second sum over the
 // new state.  Bound by memory, the state's 8 bytes an element: 256 rows of 16
-// heads, 128 x 128, 130 us, 4.2 TB/s (with 64 columns a workgroup 154 us).
-constexpr uint32_t kStepRows = 16u, kStepThreads = 512u;
+// heads, 128 x 128, 115 us, 4.7 TB/s (129 with the gates, keys and values asked
+// for after the state, 154 also with 64 columns a workgroup); a row of 16 heads 7.
+constexpr uint32_t kStepRows = 16u, kStepThreads = 512u, kStepKeys = PS_DELTA_MAX_DIM / 64u;
 
 template <class T>
 __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, uint32_t first, uint32_t groups, const float *state,
@@ -77,14 +78,29 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, u
     const uint32_t mine = threadIdx.x % groups, band = threadIdx.x / groups, bands = blockDim.x / groups;
     const uint32_t col = (blockIdx.x % blocks) * cols + mine * 4u, have = col < a.value_dim ? a.value_dim - col : 0u;
     const int32_t slot = slots ? slots[row] : (int32_t)row;
+    // what does not hang on the slot is on its way before the state
+    const T *k = static_cast<const T *>(a.k) + (int64_t)row * a.k_stride + (uint64_t)khead * a.key_dim;
+    const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.q_stride + (uint64_t)khead * a.key_dim;
+    const T *v = static_cast<const T *>(a.v) + (int64_t)row * a.v_stride + (uint64_t)head * a.value_dim + col;
+    const float g = a.g[(int64_t)row * a.g_stride + head], beta = a.beta[(int64_t)row * a.beta_stride + head];
+    T ks_in[kStepKeys], qs_in[kStepKeys], value[4];
+#pragma unroll
+    for (uint32_t i = 0; i < kStepKeys; ++i) {
+        const uint32_t d = lane + 64u * i;
+        ks_in[i] = d < a.key_dim ? k[d] : (T)0.0f, qs_in[i] = d < a.key_dim ? q[d] : (T)0.0f;
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) value[j] = j < have ? v[j] : (T)0.0f;
     const bool held = slot >= 0 && (uint32_t)slot < pool;
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
-    const uint64_t at = held ? ((uint64_t)slot * a.heads + head) * cells + col : 0u;
+    const uint64_t at = held ? ((uint64_t)slot * a.heads + head) * cells : 0u;
+    const float *from = state + at;
+    float *into = new_state + at;
     float S[kStepRows][4];
 #pragma unroll
     for (uint32_t i = 0; i < kStepRows; ++i) {
         const uint32_t d = band + i * bands;
-        const float *p = state + at + (uint64_t)d * a.value_dim;
+        const float *p = from + (d * a.value_dim + col);
         if (held && d < a.key_dim && have >= 4u) {
             const Pack<float, 4> w = *reinterpret_cast<const Pack<float, 4> *>(p);
 #pragma unroll
@@ -94,20 +110,17 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, u
             for (uint32_t j = 0; j < 4u; ++j) S[i][j] = held && d < a.key_dim && j < have ? p[j] : 0.0f;
         }
     }
-    const T *k = static_cast<const T *>(a.k) + (int64_t)row * a.k_stride + (uint64_t)khead * a.key_dim;
-    const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.q_stride + (uint64_t)khead * a.key_dim;
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
-    for (uint32_t d = lane; d < PS_DELTA_MAX_DIM; d += 64u) {
-        const float kd = d < a.key_dim ? (float)k[d] : 0.0f, qd = d < a.key_dim ? (float)q[d] : 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < kStepKeys; ++i) {
+        const float kd = (float)ks_in[i], qd = (float)qs_in[i];
         kk = __builtin_fmaf(kd, kd, kk);
         qq = __builtin_fmaf(qd, qd, qq);
         kq = __builtin_fmaf(kd, qd, kq);
-        if (threadIdx.x < 64u) key[d] = kd, query[d] = qd;
+        if (threadIdx.x < 64u) key[lane + 64u * i] = kd, query[lane + 64u * i] = qd;
     }
     kk = wave_total(kk), qq = wave_total(qq), kq = wave_total(kq);
     const float nu = a.unit ? 1.0f / __builtin_sqrtf(kk + a.eps) : 1.0f, mu = a.unit ? 1.0f / __builtin_sqrtf(qq + a.eps) : 1.0f;
-    float g = a.g[(int64_t)row * a.g_stride + head];
-    const float beta = a.beta[(int64_t)row * a.beta_stride + head];
     const float e = exp_hw(g);
     __syncthreads();
     float ks[4] = {}, qs[4] = {};
@@ -135,12 +148,10 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, u
             ks[j] += part[0][i * cols + mine * 4u + j];
             qs[j] += part[1][i * cols + mine * 4u + j];
         }
-    const T *v = static_cast<const T *>(a.v) + (int64_t)row * a.v_stride + (uint64_t)head * a.value_dim + col;
     float u[4], o[4];
 #pragma unroll
     for (uint32_t j = 0; j < 4u; ++j) {
-        const float value = j < have ? (float)v[j] : 0.0f;
-        u[j] = beta * __builtin_fmaf(-e * nu, ks[j], value);
+        u[j] = beta * __builtin_fmaf(-e * nu, ks[j], (float)value[j]);
         o[j] = a.scale * mu * __builtin_fmaf(e, qs[j], kq * nu * u[j]);
     }
     if (band == 0u) {
@@ -155,7 +166,7 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a, u
         const uint32_t d = band + i * bands;
         if (d >= a.key_dim) continue;
         const float kd = key[d] * nu;
-        float *p = new_state + at + (uint64_t)d * a.value_dim;
+        float *p = into + (d * a.value_dim + col);
         Pack<float, 4> w;
 #pragma unroll
         for (uint32_t j = 0; j < 4u; ++j) w.v[j] = __builtin_fmaf(kd, u[j], e * S[i][j]);
