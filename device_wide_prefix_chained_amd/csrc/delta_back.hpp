@@ -752,9 +752,9 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                     hipLaunchKernelGGL((delta_walk_back_kernel<T, W, E>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a, first, prepared,
                                        seg, g, true, to);
                 });
-                const uint64_t columns = ceil_div(a.value_dim, 32u);
-                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(256), 0, s, a, first, seg, dfinal);
+                const uint64_t columns = ceil_div(a.value_dim, Link<W>::kColumns);
+                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, Link<W>::kThreads, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg, dfinal);
                 });
             }
             launch_in_parts(segments * a.heads, blocks, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {

@@ -431,83 +431,85 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
 // The states that enter a sequence's segments after the first, S <- M S + N,
 // in the places of N.  BACK: the gradients that enter from the segment after,
 // from the last to the first; `start` holds what enters the sequence, or is
-// NULL.  A workgroup has 32 columns, a wave 32 keys of them (W 256: 64), so that
-// a step is short: every wave leaves its keys as operands in shared memory, and
-// multiplies its rows of M, which arrived while the step before was worked on.
+// NULL.  A wave has 32 keys of a workgroup's columns, so that a step is short: every
+// wave leaves its keys as operands in shared memory, and multiplies its rows of M,
+// which are on their way kAhead groups of 32 columns before they are used.
 // Bound by a step's chain of loads, products and a barrier, 2.4 to 2.9 us: 15 steps
 // of 16 heads, 128 x 128, 36 to 44 us; with a wave for all keys of 16 columns 85 us,
 // and M as rows of numbers 138 us.  Nothing is done to N as it arrives, or the
 // step before would wait for it (80 us).
+// More than 128 keys: eight waves, 16 columns a workgroup and half of M ahead, which
+// 200 registers hold; 7 steps of 16 heads, 256 x 256, 25 us (fp32 31).  Four waves
+// with twice the keys and all of M ahead spilled 580 registers, took 126 us, and in
+// fp32 came out wrong: the compiler (ROCm 7.2) lost one of the four registers of a
+// tile of N that it had moved to accumulation registers and to scratch in part.
+template <int W>
+struct Link {
+    static constexpr uint32_t kKeys = W / 32, kAhead = kKeys < 4 ? kKeys : 4, kColumns = W > 128 ? 16 : 32;
+    static constexpr int kThreads = kKeys < 4 ? 256 : 64 * kKeys;
+};
 template <class T, int W, bool E, bool BACK>
-__global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
+__global__ __launch_bounds__(Link<W>::kThreads) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
-    constexpr uint32_t kKeys = W / 32, NC = W == 256 ? 2 : 1, CT = 2;
+    constexpr uint32_t kKeys = Link<W>::kKeys, kAhead = Link<W>::kAhead, CT = Link<W>::kColumns / 16;
     constexpr bool kScaled = Form<T>::scaled;
     __shared__ Mid operands[2][kKeys][CT][64];
     __shared__ float backs[2][kKeys];
-    const uint32_t blocks = (a.value_dim + 31u) / 32u, item = first + blockIdx.x / blocks, head = item % a.heads;
+    const uint32_t blocks = (a.value_dim + 16u * CT - 1u) / (16u * CT), item = first + blockIdx.x / blocks, head = item % a.heads;
     const uint32_t wave = wave_number(), lane = threadIdx.x & 63u, m = lane & 15u, q = lane >> 4;
-    const uint32_t col0 = blockIdx.x % blocks * 32u, s = item / a.heads;
+    const uint32_t col0 = blockIdx.x % blocks * 16u * CT, s = item / a.heads;
     const Rows r = sequence_rows(a.offsets, a.tokens, s, seg.shift);
     const uint64_t cells = (uint64_t)a.key_dim * a.value_dim;
     const uint32_t segments = (uint32_t)(((uint64_t)(r.hi - r.lo) + (1ull << seg.shift) - 1u) >> seg.shift);
     if (segments < 2u) return;
-    const bool works = wave * NC < kKeys;
+    const bool works = wave < kKeys;
     auto number = [&](uint32_t i) { return (uint64_t)(r.base + (BACK ? segments - 1u - i : i)) * a.heads + head; };
-    auto each = [&](auto f) {  // f(keys, columns, half, row of the four, offset or none)
+    auto each = [&](auto f) {  // f(columns, half, row of the four, whether it is there, offset)
 #pragma unroll
-        for (uint32_t k = 0; k < NC; ++k)
+        for (uint32_t ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (uint32_t ct = 0; ct < CT; ++ct)
+            for (uint32_t h = 0; h < 2u; ++h)
 #pragma unroll
-                for (uint32_t h = 0; h < 2u; ++h)
-#pragma unroll
-                    for (uint32_t i = 0; i < 4u; ++i) {
-                        const uint32_t row = place(2u * (wave * NC + k) + h, 4u * q + i), col = col0 + 16u * ct + m;
-                        const bool is = works && row < a.key_dim && col < a.value_dim;
-                        f(k, ct, h, i, is, row * a.value_dim + col);
-                    }
+                for (uint32_t i = 0; i < 4u; ++i) {
+                    const uint32_t row = place(2u * wave + h, 4u * q + i), col = col0 + 16u * ct + m;
+                    const bool is = works && row < a.key_dim && col < a.value_dim;
+                    f(ct, h, i, is, row * a.value_dim + col);
+                }
     };
-    f32x4 S[NC][CT][2], N[NC][CT][2];
-    auto load = [&](f32x4 (&to)[NC][CT][2], const float *from) {
-        each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool is, uint32_t at) {
-            to[k][ct][h][i] = from && is ? from[at] : 0.0f;
-        });
+    f32x4 S[CT][2], N[CT][2];
+    auto load = [&](f32x4 (&to)[CT][2], const float *from) {
+        each([&](uint32_t ct, uint32_t h, uint32_t i, bool is, uint32_t at) { to[ct][h][i] = from && is ? from[at] : 0.0f; });
     };
-    Mid mat[NC][2][kKeys];
-    float back[NC][2][kKeys];
-    auto fetch = [&](uint32_t i, uint32_t k, uint32_t h, uint32_t c) {
+    Mid mat[2][kAhead];
+    float back[2][kAhead];
+    auto fetch = [&](uint32_t i, uint32_t h, uint32_t c) {
         const SegmentMatrix<T, W> &from = static_cast<const SegmentMatrix<T, W> *>(seg.m)[number(i)];
-        const uint32_t t = 2u * (wave * NC + k) + h;
-        mat[k][h][c] = from.m[t][c][lane];
-        back[k][h][c] = kScaled ? from.back[t][c] : 1.0f;
+        const uint32_t t = 2u * wave + h;
+        mat[h][c % kAhead] = from.m[t][c][lane];
+        back[h][c % kAhead] = kScaled ? from.back[t][c] : 1.0f;
     };
     load(S, start ? start + ((uint64_t)s * a.heads + head) * cells : nullptr);
-    each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t i, bool, uint32_t) { S[k][ct][h][i] = finite_or_nan(S[k][ct][h][i]); });
+    each([&](uint32_t ct, uint32_t h, uint32_t i, bool, uint32_t) { S[ct][h][i] = finite_or_nan(S[ct][h][i]); });
     load(N, seg.n + number(0u) * cells);
     if (works)
 #pragma unroll
-        for (uint32_t k = 0; k < NC; ++k)
-#pragma unroll
-            for (uint32_t c = 0; c < kKeys; ++c) fetch(0u, k, 0u, c), fetch(0u, k, 1u, c);
+        for (uint32_t c = 0; c < kAhead; ++c) fetch(0u, 0u, c), fetch(0u, 1u, c);
     for (uint32_t i = 0; i + 1u < segments; ++i) {
         const uint32_t b = i & 1u;
         if (works) {
+            float most = 0.0f;
+            if (kScaled)
 #pragma unroll
-            for (uint32_t k = 0; k < NC; ++k) {
-                const Scale of = scale_of<kScaled>(kScaled ? wave_largest(__builtin_fmaxf(largest(S[k][0]), largest(S[k][1]))) : 0.0f);
+                for (uint32_t ct = 0; ct < CT; ++ct) most = __builtin_fmaxf(most, largest(S[ct]));
+            const Scale of = scale_of<kScaled>(kScaled ? wave_largest(most) : 0.0f);
 #pragma unroll
-                for (uint32_t ct = 0; ct < CT; ++ct)
-                    operands[b][wave * NC + k][ct][lane] = operand_of<Mid>(S[k][ct][0], S[k][ct][1], of.by);
-                if (lane == 0u) backs[b][wave * NC + k] = of.back;
-            }
+            for (uint32_t ct = 0; ct < CT; ++ct) operands[b][wave][ct][lane] = operand_of<Mid>(S[ct][0], S[ct][1], of.by);
+            if (lane == 0u) backs[b][wave] = of.back;
         }
         __syncthreads();  // two sets of operands: those of the step before may still be read
         if (works) {
 #pragma unroll
-            for (uint32_t k = 0; k < NC; ++k)
-#pragma unroll
-                for (uint32_t ct = 0; ct < CT; ++ct) S[k][ct][0] = N[k][ct][0], S[k][ct][1] = N[k][ct][1];
+            for (uint32_t ct = 0; ct < CT; ++ct) S[ct][0] = N[ct][0], S[ct][1] = N[ct][1];
 #pragma unroll
             for (uint32_t c = 0; c < kKeys; ++c) {
                 const float from = backs[b][c];
@@ -515,22 +517,19 @@ __global__ __launch_bounds__(256) void delta_link_kernel(DeltaArgs a, uint32_t f
                 for (uint32_t ct = 0; ct < CT; ++ct) {
                     const Mid h = operands[b][c][ct][lane];
 #pragma unroll
-                    for (uint32_t k = 0; k < NC; ++k)
-#pragma unroll
-                        for (uint32_t t = 0; t < 2u; ++t) {
-                            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma(sum, mat[k][t][c], h);
-                            S[k][ct][t] += sum * (back[k][t][c] * from);
-                        }
+                    for (uint32_t t = 0; t < 2u; ++t) {
+                        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma(sum, mat[t][c % kAhead], h);
+                        S[ct][t] += sum * (back[t][c % kAhead] * from);
+                    }
                 }
-                if (i + 2u < segments)
-#pragma unroll
-                    for (uint32_t k = 0; k < NC; ++k) fetch(i + 1u, k, 0u, c), fetch(i + 1u, k, 1u, c);
+                if (c + kAhead < kKeys) fetch(i, 0u, c + kAhead), fetch(i, 1u, c + kAhead);
+                else if (i + 2u < segments) fetch(i + 1u, 0u, c + kAhead - kKeys), fetch(i + 1u, 1u, c + kAhead - kKeys);
             }
             float *n = seg.n + number(i + 1u) * cells;
             if (i + 2u < segments) load(N, n);
-            each([&](uint32_t k, uint32_t ct, uint32_t h, uint32_t j, bool is, uint32_t at) {
-                if (is) n[at] = S[k][ct][h][j];
+            each([&](uint32_t ct, uint32_t h, uint32_t j, bool is, uint32_t at) {
+                if (is) n[at] = S[ct][h][j];
             });
         }
     }
@@ -622,9 +621,9 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                     hipLaunchKernelGGL((delta_walk_kernel<T, W, E, true>), dim3(grid), dim3(64 * (kWalkWaves + 4)), 0, s, a,
                                        first, prepared, seg, to);
                 });
-                const uint64_t columns = ceil_div(a.value_dim, 32u);
-                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, 256u, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, false>), dim3(grid), dim3(256), 0, s, a, first, seg,
+                const uint64_t columns = ceil_div(a.value_dim, Link<W>::kColumns);
+                launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, Link<W>::kThreads, [&](uint32_t first, uint32_t grid) {
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, false>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg,
                                        a.initial);
                 });
             }

@@ -1,0 +1,39 @@
+"""The gated delta rule over sequences long enough for segments side by side."""
+import pytest
+import torch
+
+import delta_norm
+import delta_ref as ref
+from gpu_util import require_gpu, say
+from test_gpu_block import _offsets
+from test_gpu_delta import BF16, F16, F32, DeltaMaker, delta_inputs
+
+pytestmark = pytest.mark.gpu
+
+T, CUTS = 1500, [0, 1490, 1500]  # six segments of the first sequence
+
+
+@pytest.fixture(scope="module")
+def dw():
+    return require_gpu()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("keys,values", [(256, 40), (200, 24), (193, 17), (128, 40), (100, 33), (64, 72), (24, 16)])
+def test_segments(dw, keys, values, dtype):
+    """By norms, so that a single wrong column of the states that enter the segments
+    is seen."""
+    H, seqs = 2, len(CUTS) - 1
+    m = DeltaMaker(50 + keys, dtype)
+    a, more = delta_inputs(m, T, 1, H, keys, values, True, True, seqs)
+    dout, dfinal = m.act(T, H, values), m.par(seqs, H, keys, values, scale=0.3)
+    how = dict(more, offsets=_offsets(CUTS))
+    say("segments", keys, values, dtype)
+    kept = torch.empty(dw.ps_gated_delta_checkpoint_floats(T, seqs, H, keys, values), device="cuda")
+    final = torch.empty(seqs, H, keys, values, device="cuda")
+    out = dw.ps_gated_delta(**a, **how, final=final, checkpoints=kept)
+    g = dw.ps_gated_delta_bwd(**a, **how, dout=dout, dfinal=dfinal, checkpoints=kept)
+    torch.cuda.synchronize()
+    want = ref.delta(**a, **how, dout=dout, dfinal=dfinal, dtype=dtype)[0]
+    for name, t in dict(out=out, final=final, **g._asdict()).items():
+        delta_norm.close(name, t, want[name])
