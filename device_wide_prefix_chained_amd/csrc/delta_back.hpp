@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_back_kernel(
         feed.template run<false>(chunks, !unit, tile, [&](uint32_t i) { return chunks - 1u - i; });
         if (unit)
             store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
-                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
+                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, a.key_dim, wave, lane, false);
         return;
     }
     const uint32_t here = wave * 16u, col0 = block0 + here, col = col0 + m;
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_back_kernel(
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (unit) {
         store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &D, unit_of,
-                               block0, wave, lane, true);
+                               block0, a.key_dim, wave, lane, true);
         return;
     }
     if (col0 >= width) return;

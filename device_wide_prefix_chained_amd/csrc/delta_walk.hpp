@@ -67,10 +67,12 @@ struct SegmentMatrix {
     float back[W / 16][W / 32];
 };
 // Columns of M that four waves hold, into operands, by way of shared memory;
-// all eight waves, `walks`: those that hold them.
+// all eight waves, `walks`: those that hold them.  The block with the last of the
+// `keys` columns leaves zeros for the blocks after it, which have no walk (129 to
+// 192 keys of W 256): the link reads all W columns.
 template <class T, int W>
 __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *shared, const f32x4 (*S)[W / 16], float by,
-                                             uint32_t block0, uint32_t wave, uint32_t lane, bool walks) {
+                                             uint32_t block0, uint32_t keys, uint32_t wave, uint32_t lane, bool walks) {
     constexpr uint32_t kCols = 16u * kWalkWaves, kRow = kCols + 4u;
     static_assert(W * kRow * 4u <= kMostShared, "a block of M fits shared memory");
     const uint32_t m = lane & 15u, q = lane >> 4;
@@ -91,6 +93,15 @@ __device__ __forceinline__ void store_matrix(SegmentMatrix<T, W> &to, float *sha
         const Scale of = scale_of<Form<T>::scaled>(Form<T>::scaled ? wave_largest(most) : 0.0f);
         operand_of(to.m[t][block0 / 32u + c][lane], v, of.by);
         if (lane == 0u) to.back[t][block0 / 32u + c] = of.back;
+    }
+    const uint32_t next = block0 + kCols;
+    if (next < keys || next >= (uint32_t)W) return;
+    const uint32_t rest = ((uint32_t)W - next) / 32u;
+    for (uint32_t i = wave; i < W / 16u * rest; i += kWalkWaves + 4u) {
+        const uint32_t t = i / rest, c = next / 32u + i % rest;
+        const float zeros[8] = {};
+        operand_of(to.m[t][c][lane], zeros);
+        if (lane == 0u) to.back[t][c] = 0.0f;
     }
 }
 struct WalkResults {
@@ -271,7 +282,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
         feed.template run<LEAD>(chunks, !unit, tile, [](uint32_t i) { return i; });
         if (LEAD && unit)
             store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[(uint64_t)number * a.heads + head],
-                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, wave, lane, false);
+                                   reinterpret_cast<float *>(memory), nullptr, 1.0f, block0, a.key_dim, wave, lane, false);
         return;
     }
     const uint32_t here = wave * 16u, col0 = block0 + here, col = col0 + m;
@@ -419,7 +430,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
     const uint64_t place_of = (uint64_t)number * a.heads + head;
     if (LEAD && unit) {
         store_matrix<T, W>(static_cast<SegmentMatrix<T, W> *>(seg.m)[place_of], reinterpret_cast<float *>(memory), &S, unit_of,
-                               block0, wave, lane, true);
+                               block0, a.key_dim, wave, lane, true);
         return;
     }
     if (col0 >= width) return;

@@ -37,3 +37,32 @@ def test_segments(dw, keys, values, dtype):
     want = ref.delta(**a, **how, dout=dout, dfinal=dfinal, dtype=dtype)[0]
     for name, t in dict(out=out, final=final, **g._asdict()).items():
         delta_norm.close(name, t, want[name])
+
+
+# a multiple of 32 keys and not, in each padded width; 129 to 192 keys leave the
+# last 64 columns of what a segment does to a state without a walk
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=str)
+@pytest.mark.parametrize("keys", [129, 160, 192, 193, 256, 128, 72, 40, 64, 20])
+def test_what_the_workspace_held_is_not_read(dw, keys, dtype):
+    """On a workspace and checkpoints that hold NaN in every type, and again on zeros."""
+    H, V, seqs = 2, 24, len(CUTS) - 1
+    m = DeltaMaker(40 + keys, dtype)
+    a, more = delta_inputs(m, T, 1, H, keys, V, True, True, seqs)
+    dout, dfinal = m.act(T, H, V), m.par(seqs, H, keys, V, scale=0.3)
+    how = dict(more, offsets=_offsets(CUTS))
+
+    def run(byte):
+        filled = lambda n: torch.full((n,), byte, dtype=torch.uint8, device="cuda")  # noqa: E731
+        kept = filled(4 * dw.ps_gated_delta_checkpoint_floats(T, seqs, H, keys, V)).view(torch.float32)
+        final = torch.empty(seqs, H, keys, V, device="cuda")
+        out = dw.ps_gated_delta(**a, **how, final=final, checkpoints=kept, workspace=filled(1 << 26))
+        g = dw.ps_gated_delta_bwd(**a, **how, dout=dout, dfinal=dfinal, checkpoints=kept, workspace=filled(1 << 26))
+        torch.cuda.synchronize()
+        return dict(out=out, final=final, **g._asdict())
+    say("segments on a workspace of NaN", keys, dtype)
+    got = run(0xFF)
+    want = ref.delta(**a, **how, dout=dout, dfinal=dfinal, dtype=dtype)[0]
+    for name, t in got.items():
+        delta_norm.close(name, t, want[name])
+    for name, t in run(0).items():
+        assert torch.equal(t, got[name]), name
