@@ -2,14 +2,14 @@
 norm over each head's rows: what the bounds of single elements in delta_ref, which
 allow every rounding the worst direction, are too wide to see.
 
-Errors of many elements have signs of their own, so in a norm the chunks' errors do
-not add up and the lengths that a bound multiplies by do not meet.  What is left are
-the products on the way of a value through a chunk (delta_ref counts eight), each off
-by 2^-22 of its terms: two fp16 planes hold a number to that, and a sum of up to 320
-fp32 terms is off by less (sqrt(320) 2^-24 / 2 = 2^-20.8 if all terms were as long as
-the sum).  Eight of them with one sign: 2^-19 of the result's own norm.  Gradients
-go through the forward chain and the one back, and join both in one more product of
-each: four times as much.
+Errors of many elements have signs of their own, so in a norm errors add up by their
+squares, and the lengths that a bound multiplies by do not meet.  What a value passes
+in a chunk are the products that delta_ref counts, eight, each off by 2^-22 of its
+terms: two fp16 planes hold a number to that, and a sum of up to 320 fp32 terms is off
+by less (sqrt(320) 2^-24 / 2 = 2^-20.8 if all terms were as long as the sum).  Over up
+to 32 chunks, through which a state may keep all that was added to it, that is
+sqrt(8 * 32) 2^-22 = 2^-18 of the result's own norm.  Gradients go through the forward
+chain and the one back, and join both in one more product of each: four times as much.
 
 The last rounding is taken off each element by itself: a number w + d that is rounded
 to its type is off from w by at most half a step and |d|, so what is left of |got - w|
@@ -20,7 +20,7 @@ import torch
 
 from block_ref import f64
 
-FORWARD, GRADIENT = 2.0 ** -19, 2.0 ** -17
+FORWARD, GRADIENT = 2.0 ** -18, 2.0 ** -16
 
 
 def tolerance(name):
@@ -49,3 +49,10 @@ def close(name, got, want):
     off, tol = off_by(got, want), tolerance(name)
     assert bool((off <= tol).all()), "%s: heads are off by %s of their norms, tolerance %.2e" % (
         name, " ".join("%.2e" % float(v) for v in off[:8]), tol)
+
+
+def decays(tokens, heads, generator):
+    """Log decays by head: what is left after a chunk is 0.6 of a state for the first,
+    the next three forget four times as fast as the one before."""
+    rate = torch.tensor([2.0 ** -6 * 4.0 ** (h % 4) for h in range(heads)])
+    return -rate * torch.rand(tokens, heads, generator=generator)

@@ -22,10 +22,11 @@ def dw():
 @pytest.mark.parametrize("keys,values", [(256, 40), (200, 24), (193, 17), (128, 40), (100, 33), (64, 72), (24, 16)])
 def test_segments(dw, keys, values, dtype):
     """By norms, so that a single wrong column of the states that enter the segments
-    is seen."""
+    is seen, with decays that leave much of a state after a segment."""
     H, seqs = 2, len(CUTS) - 1
     m = DeltaMaker(50 + keys, dtype)
     a, more = delta_inputs(m, T, 1, H, keys, values, True, True, seqs)
+    a["g"] = m.of(delta_norm.decays(T, H, m.g), F32)
     dout, dfinal = m.act(T, H, values), m.par(seqs, H, keys, values, scale=0.3)
     how = dict(more, offsets=_offsets(CUTS))
     say("segments", keys, values, dtype)
@@ -48,6 +49,7 @@ def test_what_the_workspace_held_is_not_read(dw, keys, dtype):
     H, V, seqs = 2, 24, len(CUTS) - 1
     m = DeltaMaker(40 + keys, dtype)
     a, more = delta_inputs(m, T, 1, H, keys, V, True, True, seqs)
+    a["g"] = m.of(delta_norm.decays(T, H, m.g), F32)
     dout, dfinal = m.act(T, H, V), m.par(seqs, H, keys, V, scale=0.3)
     how = dict(more, offsets=_offsets(CUTS))
 
