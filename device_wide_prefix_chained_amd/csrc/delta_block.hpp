@@ -722,7 +722,7 @@ struct DeltaBytes {
         g = rows_bytes(in->tokens, in->g_stride, in->heads, 4u);
         beta = rows_bytes(in->tokens, in->beta_stride, in->heads, 4u);
         offsets = in->offsets ? ((size_t)in->num_seqs + 1u) * 4u : 0u;
-        states = (size_t)in->num_seqs * in->heads * in->key_dim * in->value_dim * 4u;
+        states = (size_t)(in->offsets ? in->num_seqs : 1u) * in->heads * in->key_dim * in->value_dim * 4u;
         keys = in->tokens * kd * e;
         values = in->tokens * vd * e;
         gates = in->tokens * in->heads * 4u;

@@ -185,7 +185,8 @@ using namespace dwps;
 
 extern "C" uint64_t ps_gated_delta_checkpoint_floats(uint64_t tokens, uint32_t num_seqs, uint32_t heads, uint32_t key_dim,
                                                      uint32_t value_dim) {
-    return chunk_slots(tokens, num_seqs, kChunkShift) * heads * ((uint64_t)(key_dim + kChunk) * value_dim + kSizes);
+    // no offsets may come with no number of sequences: all rows are one
+    return chunk_slots(tokens, num_seqs ? num_seqs : 1u, kChunkShift) * heads * ((uint64_t)(key_dim + kChunk) * value_dim + kSizes);
 }
 
 extern "C" ps_status ps_gated_delta(void *ws, size_t *ws_bytes, const ps_delta_input *in, void *out, float *final,

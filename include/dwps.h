@@ -729,7 +729,8 @@ typedef struct ps_delta_input {
     float scale, eps;
 } ps_delta_input;
 /* Floats of a call's checkpoints, what the backward pass starts from: the
- * states that enter every chunk, and what is corrected at every row. */
+ * states that enter every chunk, and what is corrected at every row.  num_seqs
+ * as in the call's input: 0 counts as 1. */
 uint64_t ps_gated_delta_checkpoint_floats(uint64_t tokens, uint32_t num_seqs, uint32_t heads, uint32_t key_dim,
                                           uint32_t value_dim);
 /* out: [tokens, heads, value_dim].  final (optional): [num_seqs, heads,
