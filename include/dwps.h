@@ -699,8 +699,11 @@ ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, fl
  * g and beta are fp32; g is a log decay: a value below -512 counts as -512,
  * after which nothing of the state before is left.
  *
- * Sequences are worked on in chunks of 64 rows from their first row on, so a
- * sequence's results do not depend on what is packed beside it.  With bf16 and
+ * Sequences are worked on in chunks of 64 rows from their first row on, long ones
+ * where it pays in segments of some chunks side by side.  How they are cut follows
+ * from the call's tokens, num_seqs, heads and dimensions alone: in calls that have
+ * these in common a sequence gives the same bits whatever else is packed, in others
+ * it agrees to the errors that follow.  With bf16 and
  * fp16 activations the products of numbers that the call computes (states,
  * corrections) are off by at most 2^-22 of a term's size where that is not below
  * 2^-17 of the largest beside it (2^-39 of that largest below), and bf16 keys and

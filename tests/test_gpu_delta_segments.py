@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import block_ref
 import delta_norm
 import delta_ref as ref
 from gpu_util import require_gpu, say
@@ -68,3 +69,44 @@ def test_what_the_workspace_held_is_not_read(dw, keys, dtype):
         delta_norm.close(name, t, want[name])
     for name, t in run(0).items():
         assert torch.equal(t, got[name]), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+def test_a_long_sequence_alone_and_among_others(dw, dtype):
+    """Alone 1500 rows are cut into segments, among 29 short sequences they are walked
+    whole: each is off from the formula by what delta_norm allows, so one is from the
+    other by twice that (a rounding to 16 bits counts for both).  Calls alike in
+    tokens and sequences give the same bits, whatever else they hold."""
+    H, K, V, seqs, more_rows = 4, 48, 40, 30, 400
+    m = DeltaMaker(60, dtype)
+    a, more = delta_inputs(m, T + more_rows, 2, H, K, V, True, True, seqs)
+    a["g"] = m.of(delta_norm.decays(T + more_rows, H, m.g), F32)
+    dout = m.act(T + more_rows, H, V, packed=True)
+
+    def run(rows, cuts, initial):
+        at = {k: v[rows] for k, v in a.items()}
+        n, s = at["q"].shape[0], len(cuts) - 1
+        how = dict(offsets=_offsets(cuts), initial=initial, normalize=True)
+        kept = torch.empty(dw.ps_gated_delta_checkpoint_floats(n, s, H, K, V), device="cuda")
+        final = torch.empty_like(initial)
+        out = dw.ps_gated_delta(**at, **how, checkpoints=kept, final=final)
+        return out, final, dw.ps_gated_delta_bwd(**at, **how, dout=dout[rows], checkpoints=kept)
+    say("a long sequence alone and among others", dtype)
+    short = torch.arange(1, seqs) * more_rows // (seqs - 1)
+    one, f1, g1 = run(slice(0, T), [0, T], more["initial"][:1].contiguous())
+    two, f2, g2 = run(slice(0, T + more_rows), [0, T] + (T + short).tolist(), more["initial"])
+    pairs = [("out", one, two), ("final", f1, f2), ("dinitial", g1.dinitial, g2.dinitial)]
+    pairs += [(n, getattr(g1, n), getattr(g2, n)) for n in ("dq", "dk", "dv", "dg", "dbeta")]
+    for name, x, y in pairs:
+        y = y[:x.shape[0]]
+        rounding = delta_norm.half_step(x.dtype, block_ref.f64(y)) * (x.dtype != F32)
+        over = ((block_ref.f64(x) - block_ref.f64(y)).abs() - 2 * rounding).clamp(min=0.0)
+        off = (over.norm() / block_ref.f64(y).norm()).item()
+        assert off <= 2 * delta_norm.tolerance(name), (name, off)
+    # the rows behind the first sequence changed and cut elsewhere
+    for t in a.values():
+        t[T:] = t[T:].flip(0)
+    three, f3, g3 = run(slice(0, T + more_rows), [0, T] + (T + (short ** 2 // more_rows)).tolist(), more["initial"])
+    assert torch.equal(two[:T], three[:T]) and torch.equal(f2[0], f3[0]) and torch.equal(g2.dinitial[0], g3.dinitial[0])
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(getattr(g2, n)[:T], getattr(g3, n)[:T]), n
