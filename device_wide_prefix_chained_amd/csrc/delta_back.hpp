@@ -126,21 +126,28 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_back_kernel(
             __builtin_amdgcn_sched_barrier(0);
             const float most_o = kScaled ? wave_largest(largest(o)) : 0.0f;
             const Scale of_o = scale_of<kScaled>(most_o);
-            const float to_x = kScaled ? of_o.by * in.p.row[kRowScores] : 1.0f;
-            const float from_x = kScaled ? of_o.back * in.p.row[kRowScoresBack] : 1.0f;
-            const float from_d = of_d.back * unit_of * to_x;
+            // K D and P^T dO are summed with their scales taken back: where dO and the
+            // scores are zero or small, theirs would take K D past fp32's range
+            const float from_p = kScaled ? of_o.back * in.p.row[kRowScores] : 1.0f, from_d = of_d.back * unit_of;
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) x[t] *= tail.of[t] * from_d;
             if (!unit) {
+                f32x4 p[4];
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t) p[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 const In h[2] = {operand_of<In>(o[0], o[1], of_o.by), operand_of<In>(o[2], o[3], of_o.by)};
-                mma_upper(x, tri, h);
+                mma_upper(p, tri, h);
+#pragma unroll
+                for (uint32_t t = 0; t < 4u; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[t][j] = __builtin_fmaf(p[t][j], from_p, x[t][j]);
             }
             tri.load(in.p.inverse, lane);
             const float inverse_back = in.p.row[kRowInverse], kept = unit_of * in.p.row[kRowWhole];
             __builtin_amdgcn_sched_barrier(0);
             // omega
             const Scale of_x = scale_of<kScaled>(kScaled ? wave_largest(largest(x)) : 0.0f);
-            const float from_y = kScaled ? of_x.back * from_x * inverse_back : 1.0f;
+            const float from_y = kScaled ? of_x.back * inverse_back : 1.0f;
             {
                 const Mid h[2] = {operand_of<Mid>(x[0], x[1], of_x.by), operand_of<Mid>(x[2], x[3], of_x.by)};
                 mma_upper(y, tri, h);

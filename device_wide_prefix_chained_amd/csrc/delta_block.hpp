@@ -468,10 +468,10 @@ __device__ __forceinline__ void store_rows(float *to, uint32_t width, const f32x
 // ---------------------------------------------------------------------------
 // Numbers for each row: e nu (backwards times beta), scale e mu, beta, exp(G_C -
 // G) nu (nu and mu with what takes the keys' and queries' powers of two back);
-// then exp(G_C) and the scales of the triangles: the inverse's back, the scores'
-// and its back.
+// then exp(G_C) and what takes the triangles' scales back, the inverse's and the
+// scores'.
 constexpr uint32_t kRowE = 0u, kRowQ = 64u, kRowBeta = 128u, kRowTail = 192u, kRowWhole = 256u, kRowInverse = 257u,
-                   kRowScores = 258u, kRowScoresBack = 259u, kRowFloats = 320u;
+                   kRowScores = 258u, kRowFloats = 320u;
 // Two triangles as operands in the order that the lanes read them: rows of tile
 // t and the places of token_at(s, ..); six of the eight hold something.
 constexpr uint32_t kTriangle = 6u;
@@ -682,8 +682,7 @@ __global__ __launch_bounds__(256, 3) void delta_prepare_kernel(DeltaArgs a, uint
         }
         if (threadIdx.x == 0u) {
             out.row[kRowInverse] = inverse.back;
-            out.row[kRowScores] = scores.by;
-            out.row[kRowScoresBack] = scores.back;
+            out.row[kRowScores] = scores.back;
         }
 #pragma unroll
         for (uint32_t s = 0; s < 2u; ++s) {

@@ -381,21 +381,25 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) eq[t] = in.p.row[kRowQ + 16u * t + m];
             }
-            const float kept = unit_of * in.p.row[kRowWhole], scores_by = in.p.row[kRowScores], scores_back = in.p.row[kRowScoresBack];
+            const float kept = unit_of * in.p.row[kRowWhole], scores_back = in.p.row[kRowScores];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (uint32_t t = 0; t < 4u; ++t) y[t] *= beta.of[t] * from_x;
             tail.load(in.p.row + kRowTail, q);
             if constexpr (!LEAD) {
                 const Scale of_u = scale_of<kScaled>(kScaled ? wave_largest(largest(y)) : 0.0f);
-                const float to_o = kScaled ? from_s * of_u.by * scores_by : 1.0f, from_o = kScaled ? of_u.back * scores_back : 1.0f;
+                const float from_o = kScaled ? of_u.back * scores_back : 1.0f;
+                // the two parts of out are summed at the end, each by its own scale: where U
+                // and the scores are zero or small, theirs would take the states' part past
+                // fp32's range
+                f32x4 pu[4];
 #pragma unroll
-                for (uint32_t t = 0; t < 4u; ++t) o[t] *= eq[t] * to_o;
+                for (uint32_t t = 0; t < 4u; ++t) pu[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, o[t] *= eq[t] * from_s;
                 const Mid h[2] = {operand_of<Mid>(y[0], y[1], of_u.by), operand_of<Mid>(y[2], y[3], of_u.by)};
-                mma_columns(o, h[0], {tri.of[lower_at(0, 0)], tri.of[lower_at(1, 0)], tri.of[lower_at(2, 0)], tri.of[lower_at(3, 0)]});
-                f32x4 low[2] = {o[2], o[3]};
+                mma_columns(pu, h[0], {tri.of[lower_at(0, 0)], tri.of[lower_at(1, 0)], tri.of[lower_at(2, 0)], tri.of[lower_at(3, 0)]});
+                f32x4 low[2] = {pu[2], pu[3]};
                 mma_columns(low, h[1], {tri.of[lower_at(2, 1)], tri.of[lower_at(3, 1)]});
-                o[2] = low[0], o[3] = low[1];
+                pu[2] = low[0], pu[3] = low[1];
 #pragma unroll
                 for (uint32_t t = 0; t < 4u; ++t) {
                     const uint32_t row = 16u * t + m, at = col0 + 4u * q;
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
                         T *p = static_cast<T *>(to.out) + ((uint64_t)(lo + row) * a.heads + head) * a.value_dim + at;
                         Pack<T, 4> w;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w.v[i] = (T)(o[t][i] * from_o);
+                        for (int i = 0; i < 4; ++i) w.v[i] = (T)__builtin_fmaf(pu[t][i], from_o, o[t][i]);
                         if (E || at + 4u <= a.value_dim) {
                             *reinterpret_cast<Pack<T, 4> *>(p) = w;
                         } else {
