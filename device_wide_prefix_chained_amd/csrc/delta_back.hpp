@@ -559,12 +559,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
             if (lane == 0u) sh.most[wave] = m;
         }
         __syncthreads();
-        Scale of_e = {1.0f, 1.0f};
+        // dqk has a scale of its own for dq, and dkk's too where they meet in dk
+        Scale of_e = {1.0f, 1.0f}, of_q = of_e;
         if constexpr (kScaled) {
-            float m = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) m = __builtin_fmaxf(m, sh.most[w]);
-            of_e = scale_of<true, -30>(m);
+            auto four = [&](int w) {
+                return __builtin_fmaxf(__builtin_fmaxf(sh.most[w], sh.most[w + 1]), __builtin_fmaxf(sh.most[w + 2], sh.most[w + 3]));
+            };
+            const float m = four(0);
+            of_q = scale_of<true, -30>(m);
+            of_e = scale_of<true, -30>(__builtin_fmaxf(m, four(4)));
         }
         // the log decays' gradients, from the sums that all waves have left
         auto decays = [&]() {
@@ -594,7 +597,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
             for (uint32_t d = 0; d < DT; ++d)
 #pragma unroll
-                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_e.by, dk[d][t] *= of_e.by;
+                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_q.by, dk[d][t] *= of_e.by;
         }
 #pragma unroll
         for (uint32_t upper = 0; upper < 2u; ++upper) {
@@ -610,7 +613,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
                     two[h] = there ? e[t + upper] : none;
                 }
                 sh.triangle[keys_side ? 1 : 0][upper ? upper_at(own_tile, s) : lower_at(own_tile, s)][lane] =
-                    operand_of<Mid>(two[0], two[1], of_e.by);
+                    operand_of<Mid>(two[0], two[1], upper || keys_side ? of_e.by : of_q.by);
             }
             __syncthreads();
 #pragma unroll
@@ -634,7 +637,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
             for (uint32_t d = 0; d < DT; ++d)
 #pragma unroll
-                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_e.back, dk[d][t] *= of_e.back;
+                for (uint32_t t = 0; t < TT; ++t) dq[d][t] *= of_q.back, dk[d][t] *= of_e.back;
         }
         if (GradShared<T, W>::kApart) decays();
     }
