@@ -23,7 +23,8 @@
 //
 // Precision.  16-bit activations use the fp16 matrix instruction.  A row of
 // keys or queries is one fp16 plane times a power of two that brings its largest
-// near 2^15 (whole for fp16 and, down to 2^-21 of the row's largest, for bf16).
+// near 2^15 (whole for fp16 and, down to 2^-21 of the row's largest, for bf16); dout
+// is one plane too, by the largest of a wave's columns or of a chunk.
 // fp32 numbers that a chunk computes (states, corrections, inverses) are two
 // fp16 planes of a common power of two for a wave's tiles, a rounding and the
 // rounding of what is left: off by 2^-22 of the number or 2^-39 of the largest,

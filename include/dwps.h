@@ -581,8 +581,9 @@ ps_status ps_kernel_timing_read(double *total_ms, uint64_t *launches);
  *    another; strides are in elements, at least the row's length, and
  *    outputs of the call are packed (stride = row length).  Parameters
  *    (weight, bias, A, D, dt_bias, norm weights), scan states and the
- *    gradients of all of these are fp32.  All arithmetic is fp32; a value is
- *    rounded once, when it is stored.
+ *    gradients of all of these are fp32.  All arithmetic is fp32 and a value is
+ *    rounded once, when it is stored, but for the gated delta rule's products of
+ *    16-bit activations (there).
  *  - Tokens of several sequences are packed one after another: rows
  *    offsets[s] .. offsets[s + 1] are sequence s (num_seqs + 1 entries, not
  *    decreasing, as in the segmented scan).  Sequences may be empty.
@@ -703,15 +704,21 @@ ps_status ps_selective_scan_step(const ps_scan_input *in, const float *state, fl
  * where it pays in segments of some chunks side by side.  How they are cut follows
  * from the call's tokens, num_seqs, heads and dimensions alone: in calls that have
  * these in common a sequence gives the same bits whatever else is packed, in others
- * it agrees to the errors that follow.  With bf16 and
- * fp16 activations the products of numbers that the call computes (states,
- * corrections) are off by at most 2^-22 of a term's size where that is not below
- * 2^-17 of the largest beside it (2^-39 of that largest below), and bf16 keys and
- * queries below 2^-21 of their row's largest lose bits; sums, and states from
- * chunk to chunk, are fp32.  A NaN or an infinity in a row (they are not told
- * apart) reaches its sequence's rows after it and may reach those of its chunk
- * before it, in its head, and from v or initial in its column; which of that
- * sequence's gradients are numbers then is not said.
+ * it agrees to the errors that follow.
+ * With PS_F32 all arithmetic is fp32.  With PS_BF16 and PS_F16 (single tokens:
+ * fp32 too) products run on fp16 matrix instructions, sums are fp32, and so are
+ * states from chunk to chunk.  Operands are fp16 numbers times a power of two:
+ *  - one for a key, a query or an element of dout: bf16 ones below 2^-21 of the
+ *    largest of their row (dout: of 64 rows of a head) lose bits;
+ *  - two, about 22 bits, for what the call computes (states and their gradients,
+ *    corrections, inverses, scores and what the gradients make of them): a number
+ *    is held to 2^-22 of its size where it is not below 2^-17 of the largest of its
+ *    kind in a chunk of a head, to 2^-39 of that largest below.  Of two such
+ *    numbers' product that of the low halves, 2^-22 of it, is left out.
+ * A NaN or an infinity in a row (they are not told apart) reaches its sequence's
+ * rows after it and may reach those of its chunk before it, in its head, and from v
+ * or initial in its column; which of that sequence's gradients are numbers then is
+ * not said.
  * PS_ERR_SIZE also: dimensions outside 1..PS_DELTA_MAX_DIM, heads outside
  * 1..PS_DELTA_MAX_HEADS or no multiple of kheads, (tokens / 64 + num_seqs) *
  * heads (single tokens: tokens * heads) of 2^31 or more. */
