@@ -65,9 +65,9 @@ TIMING_EVERY = 5
 
 
 # The source file that holds each workload's main kernel (scan.hip for the
-# rest); its hash, with the headers that it includes, marks the counter
-# summaries under profiles/ taken on it, so that a change to one kernel leaves
-# the others' summaries valid.
+# rest); its hash, with the headers that it includes (of the public one what
+# they use), marks the counter summaries under profiles/ taken on it, so that a
+# change to one kernel leaves the others' summaries valid.
 KERNEL_FILE = {"segmented": "segscan.hip", "compact": "compact.hip",
                "copy": "common.hip", "read": "common.hip", "write": "common.hip"}
 
@@ -85,22 +85,62 @@ def kernel_sources(workload: str):
     return files[:1] + sorted(files[1:])
 
 
+def _without_comments(text: str) -> str:
+    """A string literal is kept whole, so that a comment marker inside one is
+    not taken for a comment."""
+    token = re.compile(r'"(?:\\.|[^"\\])*"|//[^\n]*|/\*.*?\*/', re.S)
+    return token.sub(lambda m: m.group(0) if m.group(0).startswith('"') else " ", text)
+
+
 def _code_text(text: str) -> str:
     """The source with its comments removed and its whitespace collapsed,
-    so that a change to comments alone keeps the hash.  A string literal is
-    kept whole, so that a comment marker inside one is not taken for a
-    comment."""
-    token = re.compile(r'"(?:\\.|[^"\\])*"|//[^\n]*|/\*.*?\*/', re.S)
-    text = token.sub(lambda m: m.group(0) if m.group(0).startswith('"') else " ", text)
-    return " ".join(text.split())
+    so that a change to comments alone keeps the hash."""
+    return " ".join(_without_comments(text).split())
+
+
+def _declarations(text: str):
+    """(name, text) of what a C header of ours declares: macros, enumerators one
+    by one, structs and functions."""
+    text = re.sub(r"^\s*#\s*ifdef\s+__cplusplus.*?#\s*endif", "", text, flags=re.M | re.S)
+    for name, rest in re.findall(r"^\s*#\s*define\s+(\w+)(.*)$", text, re.M):
+        yield name, _code_text("#define %s %s" % (name, rest))
+    code = _code_text(re.sub(r"^\s*#.*$", "", text, flags=re.M))
+    for one in re.findall(r"[^;{}]+(?:\{[^{}]*\}[^;{}]*)?;", code):
+        enum = re.match(r"\s*(?:typedef )?enum\b[^{]*\{(.*)\}", one)
+        if enum:
+            for item in enum.group(1).split(","):
+                yield item.split("=")[0].strip(), item.strip()
+        elif "{" in one:
+            yield re.search(r"(\w+)\s*;$", one).group(1), one.strip()
+        else:
+            yield re.search(r"(\w+)\s*\(", one).group(1), one.strip()
+
+
+def used_declarations(header: str, names) -> str:
+    """What of a header the code with these names uses, with what that uses: a
+    declaration for other kernels leaves a workload's counter summary valid."""
+    found, used = list(_declarations(header)), set(names)
+    taken = [False] * len(found)
+    while True:
+        new = [i for i, (name, _) in enumerate(found) if not taken[i] and name in used]
+        if not new:
+            return " ".join(t for (_, t), is_used in zip(found, taken) if is_used)
+        for i in new:
+            taken[i] = True
+            used |= set(re.findall(r"\w+", found[i][1]))
 
 
 def kernel_source_hash(workload: str) -> str:
     h = hashlib.sha256()
+    texts = []
     for p in kernel_sources(workload):
         with open(p, encoding="utf-8") as f:
-            h.update(os.path.basename(p).encode())
-            h.update(_code_text(f.read()).encode())
+            texts.append((p, f.read()))
+    public = os.path.join(ROOT, "include")
+    names = {w for p, t in texts if os.path.dirname(p) != public for w in re.findall(r"\w+", _code_text(t))}
+    for p, t in texts:
+        h.update(os.path.basename(p).encode())
+        h.update((used_declarations(_without_comments(t), names) if os.path.dirname(p) == public else _code_text(t)).encode())
     return h.hexdigest()[:16]
 
 
