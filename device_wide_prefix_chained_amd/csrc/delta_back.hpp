@@ -764,7 +764,7 @@ ps_status delta_backward(void *ws, size_t *ws_bytes, const ps_delta_input *in, c
                 });
                 const uint64_t columns = ceil_div(a.value_dim, Link<W>::kColumns);
                 launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, Link<W>::kThreads, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, true>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg, dfinal);
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, true>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg, dfinal);
                 });
             }
             launch_in_parts(segments * a.heads, blocks, 64u * (kWalkWaves + 4), [&](uint32_t first, uint32_t grid) {

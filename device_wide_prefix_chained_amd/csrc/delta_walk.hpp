@@ -454,7 +454,7 @@ __global__ __launch_bounds__(64 * (kWalkWaves + 4)) void delta_walk_kernel(Delta
 // and M as rows of numbers 138 us.  Nothing is done to N as it arrives, or the
 // step before would wait for it (80 us).
 // More than 128 keys: eight waves, 16 columns a workgroup and half of M ahead, which
-// 200 registers hold; 7 steps of 16 heads, 256 x 256, 25 us (fp32 31).  Four waves
+// 200 registers hold; 3 steps of 16 heads, 256 x 256, 25 us (fp32 31).  Four waves
 // with twice the keys and all of M ahead spilled 580 registers, took 126 us, and in
 // fp32 came out wrong: the compiler (ROCm 7.2) lost one of the four registers of a
 // tile of N that it had moved to accumulation registers and to scratch in part.
@@ -463,7 +463,7 @@ struct Link {
     static constexpr uint32_t kKeys = W / 32, kAhead = kKeys < 4 ? kKeys : 4, kColumns = W > 128 ? 16 : 32;
     static constexpr int kThreads = kKeys < 4 ? 256 : 64 * kKeys;
 };
-template <class T, int W, bool E, bool BACK>
+template <class T, int W, bool BACK>
 __global__ __launch_bounds__(Link<W>::kThreads) void delta_link_kernel(DeltaArgs a, uint32_t first, Segments seg, const float *start) {
     typedef typename Form<T>::Mid Mid;
     constexpr uint32_t kKeys = Link<W>::kKeys, kAhead = Link<W>::kAhead, CT = Link<W>::kColumns / 16;
@@ -638,7 +638,7 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
                 });
                 const uint64_t columns = ceil_div(a.value_dim, Link<W>::kColumns);
                 launch_in_parts((uint64_t)a.num_seqs * a.heads, columns, Link<W>::kThreads, [&](uint32_t first, uint32_t grid) {
-                    hipLaunchKernelGGL((delta_link_kernel<T, W, E, false>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg,
+                    hipLaunchKernelGGL((delta_link_kernel<T, W, false>), dim3(grid), dim3(Link<W>::kThreads), 0, s, a, first, seg,
                                        a.initial);
                 });
             }
