@@ -216,9 +216,8 @@ struct RowNumbers {
 // y += T h for the lower triangle's tiles (upper: the upper one's) of 32 places s.
 template <class M, class H>
 __device__ __forceinline__ void mma_lower(f32x4 (&y)[4], const Triangle<M> &t, const H (&h)[2]) {
-    f32x4 low[2] = {y[2], y[3]};
     mma_rows(y, {t.of[lower_at(0, 0)], t.of[lower_at(1, 0)], t.of[lower_at(2, 0)], t.of[lower_at(3, 0)]}, h[0]);
-    low[0] = y[2], low[1] = y[3];
+    f32x4 low[2] = {y[2], y[3]};
     mma_rows(low, {t.of[lower_at(2, 1)], t.of[lower_at(3, 1)]}, h[1]);
     y[2] = low[0], y[3] = low[1];
 }
