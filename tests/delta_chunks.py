@@ -61,7 +61,7 @@ def delta(q, k, v, g, beta, scale=None, normalize=False, eps=1e-6, offsets=None,
             Q, Kc, Vc = (t[rows].transpose(0, 1) for t in (q, k, v))
             b, G = beta[rows].t()[..., None], g[rows].t().cumsum(-1)
             e, tail, whole = torch.exp(G)[..., None], torch.exp(G[..., -1:] - G)[..., None], torch.exp(G[..., -1:])[..., None]
-            between = torch.tril(torch.exp((G[..., :, None] - G[..., None, :]).clamp(max=0.0)))
+            between = torch.tril(torch.exp(torch.tril(G[..., :, None] - G[..., None, :])))
             a = torch.tril(between * (Kc @ mT(Kc)), -1)
             P = scale * between * (Q @ mT(Kc))
             one = torch.eye(Q.shape[1], dtype=F64)

@@ -90,3 +90,12 @@ def test_half_a_step():
         above = torch.nextafter(v.to(kind).abs(), torch.tensor(float("inf"), dtype=kind)).double()
         assert torch.equal(2 * delta_norm.half_step(kind, v.to(kind).double())[:-1], (above - v.to(kind).double().abs())[:-1])
         assert float(delta_norm.half_step(kind, v)[-1]) == torch.finfo(kind).tiny * torch.finfo(kind).eps / 2
+
+
+def test_chunks_of_states_that_grow():
+    """Positive log decays among the others: the model by chunks is the rule there too."""
+    a, rows = inputs((150, [0, 40, 150], 1, 2, 24, 16, F32, True, True))
+    a["g"] = 0.3 * torch.randn(150, 2, generator=torch.Generator().manual_seed(1))
+    want, got = ref.delta(**a)[0], delta_chunks.delta(**a)
+    for name, w in want.items():
+        assert float((got[name] - w).norm()) <= 1e-10 * float(w.norm()), name
