@@ -267,8 +267,8 @@ struct GradShared {
 // workgroup, whose parts wait for one another.  8192 rows of 16 heads, 128 x 128,
 // bf16: 300 us for 364 MB, of which start and end 80, the sums over columns 136,
 // the triangles 83; in half the registers it spills (596 us).  SOLO, heads that
-// share no keys, adds up nothing over heads (27 us
-// more with the sums).
+// share no keys, adds up nothing over heads (27 us more with the sums, which spill 13
+// to 29 registers at 128 keys).  More than 128 keys spill 76 to 285.
 template <class T, int W, bool E, bool SOLO>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, uint32_t first, const T *__restrict__ dout,
                                                           const float *__restrict__ states, const float *__restrict__ rhos,

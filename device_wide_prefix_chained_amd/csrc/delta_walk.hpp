@@ -561,10 +561,19 @@ inline size_t matrix_bytes(uint32_t key_dim) {
 }
 
 // Rows of a segment, as a shift: as many as take the least time by what the
-// parts of a call were measured to take (us; 128 keys and columns, where 256
+// parts of a call were measured to take (us; bf16, 128 keys and columns, where 256
 // workgroups run at once): a step of a walk 4.3, of the walks for M and N 2.7,
-// the start of either 7, a link 2.2.  Sequences are reckoned to be cut at random:
-// the longest of n is then the mean times 1 + 1/2 + ... + 1/n.
+// the start of either 7, a link 2.2.  Other types and widths take other times in
+// about the same proportions: with each shift tried, the chosen one was within 4% of
+// the best, in us for 8191 rows of 16 heads in one sequence (in brackets walked
+// whole): 128 x 128 219 (460), fp32 476 (1275); 64 x 64 137 (352), fp32 202 (709);
+// 256 x 256 616 (871), fp32 2030 (3113); 16384 rows in four sequences, 128 x 128,
+// fp32 737 (809).
+// A call knows how many rows and sequences it has, not where they are cut, which is on
+// the device: they are reckoned to be cut at random, and the longest of n is then
+// the mean times 1 + 1/2 + ... + 1/n.  One long sequence among many short ones may be
+// walked whole for that: 12000 of 16384 rows, 19 others, 16 heads, 128 x 128, bf16,
+// 768 us, where segments of 1024 rows would take 415.
 uint32_t segment_shift(const DeltaArgs &a) {
     constexpr uint32_t cols = 16u * kWalkWaves;
     const double chunks = (double)ceil_div(a.tokens, kChunk), heads = a.heads, n = a.num_seqs;
@@ -647,7 +656,8 @@ ps_status delta_forward(void *ws, size_t *ws_bytes, const ps_delta_input *in, vo
             });
         };
         // rows of whole vectors of 8 have no bounds within one: 8192 rows of 16 heads,
-        // 128 keys, bf16, with checkpoints 271 us for 128 columns, 358 for 124
+        // 128 keys, bf16, with checkpoints 285 us for 128 columns, 396 for 124 (more
+        // than 128 keys in 16 bits, not whole vectors: 62 spilled registers, 65 backwards)
         const bool eights = a.key_dim % 8u == 0u && a.value_dim % 8u == 0u;
         if (eights) walk(std::true_type());
         else walk(std::false_type());

@@ -63,7 +63,9 @@ namespace {
 // written once.  out = scale (e S^T q + (k q) u) needs no second sum over the
 // new state.  Bound by memory, the state's 8 bytes an element: 256 rows of 16
 // heads, 128 x 128, 115 us, 4.7 TB/s (129 with the gates, keys and values asked
-// for after the state, 154 also with 64 columns a workgroup); a row of 16 heads 7.
+// for after the state, 154 also with 64 columns a workgroup).  A row of 16 heads 7.2,
+// and 6.8 with 16 x 16 states: the launch and one wave's chain of loads, sums and
+// barriers, not the state's bytes (8.2 where they come from HBM).
 constexpr uint32_t kStepRows = 16u, kStepThreads = 512u, kStepKeys = PS_DELTA_MAX_DIM / 64u;
 
 template <class T>

@@ -46,7 +46,9 @@ __device__ __forceinline__ void row_sums_of(float (&v)[n], float (*shared)[kMost
 // for all their sums.  A workgroup has 256 / G rows R times (G 0: R rows,
 // blockDim.x threads with K times 8 channels each).  16384 rows of 4096 channels
 // in bf16: 48 us, 5.6 TB/s, with 2 rows (1 row 52, 4 rows 50; 3 rows in all: 2.9
-// us, 2.4 with 1); 131072 rows of 128: 11 to 14 us.
+// us, 2.4 with 1); 131072 rows of 128: 11 to 14 us.  8192 rows of 5120: 41 us, 4.1
+// TB/s: of workgroups of 10 waves a CU holds two, 20 of its 32 waves (wave cycles over
+// busy cycles: 5.0 a SIMD, 7.2 with workgroups of 8 or 16).
 template <class T, int G, int K, int R>
 __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_kernel(LayerArgs a, uint32_t first,
                                                                               T *__restrict__ out) {
@@ -110,6 +112,7 @@ __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_kernel(L
 // their way (WHOLE: rows of whole vectors), and keeps its sums over rows in
 // registers; part[workgroup][dweight, dbias][channel].  8192 rows of 5120
 // channels in bf16: 57 us, 4.4 TB/s: the next row's loads wait for two barriers.
+// fp32 rows of more than 8192 channels in whole vectors spill 19 of 128 registers.
 template <class T, int G, int K, bool WHOLE>
 __global__ __launch_bounds__(G ? 256 : 64 * kMostWaves) void layer_norm_bwd_kernel(LayerArgs a, const T *__restrict__ dout,
                                                                                   T *__restrict__ dx, float *__restrict__ part,
