@@ -110,3 +110,57 @@ def test_a_long_sequence_alone_and_among_others(dw, dtype):
     assert torch.equal(two[:T], three[:T]) and torch.equal(f2[0], f3[0]) and torch.equal(g2.dinitial[0], g3.dinitial[0])
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert torch.equal(getattr(g2, n)[:T], getattr(g3, n)[:T]), n
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "initial", "dout", "dfinal"])
+def test_nan_and_infinities_among_segments(dw, where, dtype):
+    """In the third of six segments, of three sequences the second: other heads and
+    rows before its chunk are what they are without it, from v and initial other
+    columns too; other sequences keep every gradient, forwards and back."""
+    H, K, V, cuts = 2, 48, 40, [0, 70, 1570, 1650]
+    m = DeltaMaker(80, dtype)
+    a, more = delta_inputs(m, cuts[-1], H, H, K, V, True, True, 3)
+    a["g"] = m.of(delta_norm.decays(cuts[-1], H, m.g), F32)
+    more.update(offsets=_offsets(cuts))
+    back = dict(dout=m.act(cuts[-1], H, V, packed=True), dfinal=m.par(3, H, K, V))
+
+    def run(a, more, back):
+        kept = torch.empty(dw.ps_gated_delta_checkpoint_floats(cuts[-1], 3, H, K, V), device="cuda")
+        final = torch.empty(3, H, K, V, device="cuda")
+        out = dw.ps_gated_delta(**a, **more, final=final, checkpoints=kept)
+        return dict(out=out, final=final, **dw.ps_gated_delta_bwd(**a, **more, **back, checkpoints=kept)._asdict())
+    want = run(a, more, back)
+    at = 70 + 512 + 64 + 7  # in the second chunk of that segment
+    for bad in (float("nan"), float("inf")):
+        say("nan and infinities among segments", where, bad, dtype)
+        new = [{k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()} for d in (a, more, back)]
+        for d in new:
+            if where in d:
+                if where in ("initial", "dfinal"):
+                    d[where][1, 1, 3, 5] = bad
+                elif where == "g":
+                    d[where][at, 1] = bad
+                else:
+                    d[where][at, 1, 5] = bad
+        got = run(*new)
+        for name, w in want.items():
+            if name in ("final", "dinitial"):
+                assert torch.equal(got[name][[0, 2]], w[[0, 2]]), name
+            else:
+                assert torch.equal(got[name][:70], w[:70]) and torch.equal(got[name][1570:], w[1570:]), name
+            assert torch.equal(got[name][:, 0], w[:, 0]), name  # no heads share keys here
+        if where in ("dout", "dfinal"):
+            assert torch.equal(got["out"], want["out"]) and torch.equal(got["final"], want["final"])
+            continue
+        same = torch.ones(cuts[-1], H, V, dtype=torch.bool, device="cuda")
+        first = 70 if where == "initial" else 70 + 512 + 64
+        same[first:1570, 1, 5 if where in ("v", "initial") else slice(None)] = False
+        assert torch.equal(got["out"][same], want["out"][same])
+        after = slice(at, at + 1) if where == "q" else slice(at if where != "initial" else 70, 1570)
+        cols = slice(5, 6) if where in ("v", "initial") else slice(None)
+        assert not torch.isfinite(got["out"][after, 1, cols]).any()
+        if where in ("v", "initial"):
+            keep = [c for c in range(V) if c != 5]
+            assert torch.equal(got["final"][1, 1][:, keep], want["final"][1, 1][:, keep])
+            assert not torch.isfinite(got["final"][1, 1][:, 5]).any()
